@@ -31,10 +31,13 @@
  *   device error word, which moe_read_device_status() reads.
  * - Pointers must be 16-byte aligned and every row pitch a multiple of 16
  *   bytes, which makes D, I and I_shared multiples of 8 (16 for fp8 weights).
+ * - The control block has to be zero when a workspace is first used (zero-fill
+ *   it once); the calls leave it ready for the next.  A workspace serves one
+ *   call at a time: calls that may overlap on the GPU need one each.
  * - Dtypes: act_dtype applies to x, W_g, the permuted rows and out.  w_dtype
  *   applies to W13, W2 and the shared expert's weights.  Supported pairs:
  *   (F32, F32), (BF16, BF16), (BF16, FP8_E4M3), (BF16, FP8_E4M3_NK),
- *   (BF16, FP8_E4M3_NK_A8).
+ *   (BF16, FP8_E4M3_NK_A8), and for moe_layer_few (BF16, W4_*).
  *   Router logits and gate weights are always fp32; the expert outputs
  *   y_perm and the shared-expert output are fp32, or bf16 for fp8-weight
  *   layers (one rounding each, inside the 6e-2 RMS bar of those layers).
@@ -72,6 +75,15 @@
  *   router still projects the bf16 x.  This changes the result (e4m3 keeps
  *   4 significant bits of each activation); the bf16-activation layouts
  *   above are the configured arithmetic.
+ * - W4_G32 / W4_G64 / W4_G128: 4-bit weights with group scales, taken by
+ *   moe_layer_few (moe_layer and moe_grouped_ffn return
+ *   MOE_ERR_UNSUPPORTED; moe_dequantize_w4 gives them bf16 weights).  A matrix
+ *   with N outputs and K inputs is [N, K/2] bytes: byte j of a row holds the
+ *   codes 0..15 of inputs 2j (low nibble) and 2j + 1 (high nibble); with a
+ *   bf16 scale per row and group, [N, K/group], the weight is
+ *   (code - 8) * scale.  W13 [E, 2I, D/2] (rows [0, I) gate, [I, 2I) up), s13
+ *   [E, 2I, D/group], W2 [E, D, I/2], s2 [E, D, I/group], the shared expert's
+ *   likewise without E.  D, I and I_shared are multiples of the group.
  */
 #ifndef MOE_GB300_H
 #define MOE_GB300_H
@@ -88,7 +100,10 @@ typedef enum {
   MOE_BF16 = 1,
   MOE_FP8_E4M3 = 2,   /* weights [.., K, N] as the pages write them */
   MOE_FP8_E4M3_NK = 3, /* the same weights transposed per matrix (moe_pack_weights_nk) */
-  MOE_FP8_E4M3_NK_A8 = 4 /* FP8_E4M3_NK weights, activations quantised per row (W8A8) */
+  MOE_FP8_E4M3_NK_A8 = 4, /* FP8_E4M3_NK weights, activations quantised per row (W8A8) */
+  MOE_W4_G32 = 5,  /* 4-bit weights, a scale per row and group of 32 inputs (moe_layer_few) */
+  MOE_W4_G64 = 6,  /* groups of 64 */
+  MOE_W4_G128 = 7  /* groups of 128 */
 } moe_dtype_t;
 
 /* SwiGLU: SiLU(gate) * up.  GEGLU: tanh-approximated GELU(gate) * up. */
@@ -245,6 +260,71 @@ int moe_layer(const moe_config_t* cfg, const void* x, const void* Wg, const floa
               const void* W13, const float* s13, const void* W2, const float* s2,
               const void* W13s, const float* s13s, const void* W2s, const float* s2s, void* out,
               void* ws, size_t ws_bytes, void* stream);
+
+/* The whole layer for a few tokens (1 <= T <= 32) as one kernel launch: the
+ * decode step of a small batch, where moe_layer's launches cost more than the
+ * weights take to read.  Pages: "用SGLang-JAX在TPU上优化Ling-2.6-1T" §4 (decode
+ * near the weight-read bound); "CANN/cann-recipes-infer：Qwen3-MoE优化" (the
+ * single-batch decode it is measured on, and its 4-bit weights).
+ *   Arguments, layouts and results as moe_layer, with any E in 1..512 (W_g's
+ *   rows need no padding here) and with the weight types BF16, FP8_E4M3,
+ *   FP8_E4M3_NK and W4_*.  s13 / s2 / s13s / s2s: fp32 per column for e4m3
+ *   weights, bf16 per row and group for 4-bit weights, NULL for bf16.
+ *   Other types and T > 32 return MOE_ERR_UNSUPPORTED.
+ *   Arithmetic: weights and x enter the products exactly, in bf16 (4-bit codes
+ *   minus 8 and e4m3 values are exact there), with fp32 sums; e4m3 scales
+ *   multiply the finished sums, group scales the fp32 sums of their group.  h is
+ *   carried as two bf16 terms (16 significant bits); the weighted sum over a
+ *   token's experts (j ascending, the shared expert last) is fp32, rounded once
+ *   to bf16.  The same inputs give the same bits on every call.
+ *   Logits, ids and weights are left in the workspace (MOE_WS_LOGITS,
+ *   MOE_WS_TOPK_IDS, MOE_WS_TOPK_W), no other intermediate is.
+ *   The kernel is launched cooperatively, one CTA on every SM: it starts when
+ *   every SM has room for it.  Waits inside it are bounded; one that gives up
+ *   sets MOE_DEV_WAIT_TIMEOUT (zero-fill the control block before the next
+ *   call then).  Capturable into a CUDA graph after a first call per shape
+ *   class outside of one. */
+int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const float* logit_bias,
+                  const void* W13, const void* s13, const void* W2, const void* s2, const void* W13s,
+                  const void* s13s, const void* W2s, const void* s2s, void* out, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/* y = x W^T for a few rows of x and 4-bit weights with group scales:
+ *   y[m, n] = sum_k x[m, k] * (code[n, k] - zero[n, k / group]) * scale[n, k / group]
+ * for the projections around the layer (a dense or shared projection, the
+ * logits of a decode step).  No page has this operator by itself; the Qwen3-MoE
+ * page's 4-bit weights are its source.
+ *   M       rows of x, 0..32 (more: MOE_ERR_UNSUPPORTED).
+ *   K, N    inputs, a multiple of `group`; outputs, any N >= 1.
+ *   group   32, 64 or 128.
+ *   x       [M, K] bf16.
+ *   Wq      [N, K/2] bytes as MOE_W4_* describes.
+ *   scales  [N, K/group] bf16.
+ *   zeros   [N, K/group] bytes, zero points in their low four bits, or NULL: 8.
+ *   y       [M, N] bf16 or fp32 (y_dtype MOE_BF16 / MOE_F32), one rounding.
+ *   ws      moe_linear_w4_workspace_size(M, K, N) bytes, 256-byte aligned,
+ *           zero-filled once (all of it); its control block takes the device
+ *           error word.  A larger workspace serves too.  After
+ *           MOE_DEV_WAIT_TIMEOUT, zero-fill it before the next call.
+ *   x, Wq, scales and y 16-byte aligned.  Sums are fp32; the same inputs give
+ *   the same bits on every call. */
+size_t moe_linear_w4_workspace_size(int32_t M, int32_t K, int32_t N);
+int moe_linear_w4(int32_t M, int32_t K, int32_t N, int32_t group, const void* x, const void* Wq,
+                  const void* scales, const void* zeros, void* y, int32_t y_dtype, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/* Weights [G, K, N] (the pages' layout, bf16 or fp32: w_dtype) to the 4-bit form:
+ * Wq [G, N, K/2] and scales [G, N, K/group].  Per row and group: scale =
+ * bf16(max |w| / 7), code = round(w / scale) (nearest, ties to even, clamped to
+ * -8..7) + 8; an all-zero group gets scale 1; a group with an infinity or NaN
+ * gets a NaN scale, so that its products are NaN.  1 <= G <= 65535.
+ * Run once when weights are loaded. */
+int moe_quantize_w4(const void* W, int32_t w_dtype, int64_t G, int32_t K, int32_t N, int32_t group,
+                    void* Wq, void* scales, void* stream);
+/* The way back: W [G, K, N] bf16 = bf16((code - zero) * scale), for moe_layer
+ * (prefill) on weights kept in 4 bits.  zeros [G, N, K/group] or NULL: 8. */
+int moe_dequantize_w4(const void* Wq, const void* scales, const void* zeros, int64_t G, int32_t K,
+                      int32_t N, int32_t group, void* W, void* stream);
 
 /* Device byte offsets inside `ws` where moe_layer keeps its intermediates,
  * for inspection (logits, ids, weights, counts, offsets, sorted_rows, dest,

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "libmoe_gb300.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "moe.h")
 
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_NK, MOE_FP8_E4M3_NK_A8 = 0, 1, 2, 3, 4
+MOE_W4_G32, MOE_W4_G64, MOE_W4_G128 = 5, 6, 7
 MOE_ACT_SWIGLU, MOE_ACT_GEGLU_TANH = 0, 1
 MOE_OK = 0
 MOE_DEV_BAD_EXPERT_ID = 0x1
@@ -29,7 +30,9 @@ WS_SLOTS = ["logits", "topk_ids", "topk_w", "counts", "offsets", "sorted_rows", 
             "x_perm", "h", "y_perm", "h_shared", "s", "x16", "tok_inv", "row_inv"]
 
 _DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3,
-           "fp8_e4m3_nk": MOE_FP8_E4M3_NK, "fp8_e4m3_nk_a8": MOE_FP8_E4M3_NK_A8}
+           "fp8_e4m3_nk": MOE_FP8_E4M3_NK, "fp8_e4m3_nk_a8": MOE_FP8_E4M3_NK_A8,
+           "w4_g32": MOE_W4_G32, "w4_g64": MOE_W4_G64, "w4_g128": MOE_W4_G128}
+MOE_FEW_MAX_TOKENS = 32  # most tokens of moe_layer_few, most rows of moe_linear_w4
 _ACTS = {"swiglu": MOE_ACT_SWIGLU, "geglu_tanh": MOE_ACT_GEGLU_TANH}
 
 
@@ -64,6 +67,14 @@ _SIGS = {
     "moe_permute_noalloc": (ctypes.c_int, [ctypes.POINTER(MoEConfig)] + [_P] * 7 + [_P]),
     "moe_set_option": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "moe_pack_weights_nk": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P]),
+    "moe_layer_few": (ctypes.c_int, [ctypes.POINTER(MoEConfig)] + [_P] * 12 + [_P, ctypes.c_size_t, _P]),
+    "moe_linear_w4_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 3),
+    "moe_linear_w4": (ctypes.c_int, [ctypes.c_int32] * 4 + [_P] * 5 +
+                      [ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "moe_quantize_w4": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.c_int32, _P, _P, _P]),
+    "moe_dequantize_w4": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.c_int32, _P, _P]),
 }
 MOE_OPT_PAIR_TILES = 1
 MOE_OPT_GATHER_A = 2
@@ -241,6 +252,72 @@ def moe_layer(cfg, x, Wg, logit_bias, W13, s13, W2, s2, W13s, s13s, W2s, s2s, ou
         ctypes.byref(cfg), _ptr(x), _ptr(Wg), _ptr(logit_bias), _ptr(W13), _ptr(s13), _ptr(W2),
         _ptr(s2), _ptr(W13s), _ptr(s13s), _ptr(W2s), _ptr(s2s), _ptr(out), wp, wb,
         _stream(stream)))
+
+
+def moe_layer_few(cfg, x, Wg, logit_bias, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, stream=None):
+    """moe_layer for 1 to 32 tokens as one kernel launch; also takes 4-bit
+    weights (w_dtype "w4_g32", "w4_g64" or "w4_g128", see quantize_w4)."""
+    wp, wb = _ws(ws)
+    _check("moe_layer_few", load_library().moe_layer_few(
+        ctypes.byref(cfg), _ptr(x), _ptr(Wg), _ptr(logit_bias), _ptr(W13), _ptr(s13), _ptr(W2),
+        _ptr(s2), _ptr(W13s), _ptr(s13s), _ptr(W2s), _ptr(s2s), _ptr(out), wp, wb,
+        _stream(stream)))
+
+
+def moe_linear_w4_workspace_size(M: int, K: int, N: int) -> int:
+    return int(load_library().moe_linear_w4_workspace_size(M, K, N))
+
+
+def _float_dtype(t) -> int:
+    """moe_dtype_t of a tensor's dtype (-1: none, which the library refuses)."""
+    return {"torch.float32": MOE_F32, "torch.bfloat16": MOE_BF16}.get(str(t.dtype), -1)
+
+
+def moe_linear_w4(M: int, K: int, N: int, group: int, x, Wq, scales, zeros, y, ws, stream=None) -> None:
+    """y [M, N] (bf16 or fp32) = x [M, K] times 4-bit weights [N, K/2] with
+    scales (and zero points, or None) [N, K/group]."""
+    wp, wb = _ws(ws)
+    _check("moe_linear_w4", load_library().moe_linear_w4(
+        M, K, N, group, _ptr(x), _ptr(Wq), _ptr(scales), _ptr(zeros), _ptr(y), _float_dtype(y), wp, wb,
+        _stream(stream)))
+
+
+def moe_quantize_w4(W, G: int, K: int, N: int, group: int, Wq, scales, stream=None) -> None:
+    _check("moe_quantize_w4", load_library().moe_quantize_w4(
+        _ptr(W), _float_dtype(W), G, K, N, group, _ptr(Wq), _ptr(scales), _stream(stream)))
+
+
+def moe_dequantize_w4(Wq, scales, zeros, G: int, K: int, N: int, group: int, W, stream=None) -> None:
+    _check("moe_dequantize_w4", load_library().moe_dequantize_w4(
+        _ptr(Wq), _ptr(scales), _ptr(zeros), G, K, N, group, _ptr(W), _stream(stream)))
+
+
+def quantize_w4(W, group: int = 128, stream=None):
+    """(codes [.., N, K/2] uint8, scales [.., N, K/group] bf16) of the bf16 or
+    fp32 weights W [K, N] or [G, K, N], written by moe_quantize_w4."""
+    import torch
+
+    if W.dim() not in (2, 3):
+        raise ValueError("quantize_w4 takes [K, N] or [G, K, N] weights")
+    if group not in (32, 64, 128) or W.shape[-2] % group:
+        raise ValueError("quantize_w4: groups of 32, 64 or 128, K a multiple of the group")
+    lead, (K, N) = tuple(W.shape[:-2]), W.shape[-2:]
+    q = torch.empty((*lead, N, K // 2), dtype=torch.uint8, device=W.device)
+    s = torch.empty((*lead, N, K // group), dtype=torch.bfloat16, device=W.device)
+    moe_quantize_w4(W, lead[0] if lead else 1, K, N, group, q, s, stream)
+    return q, s
+
+
+def dequantize_w4(Wq, scales, zeros=None, stream=None):
+    """bf16 weights [.., K, N] of the 4-bit ones, written by moe_dequantize_w4."""
+    import torch
+
+    if Wq.dim() not in (2, 3) or Wq.dim() != scales.dim():
+        raise ValueError("dequantize_w4 takes [N, K/2] or [G, N, K/2] codes and scales like them")
+    lead, N, K = tuple(Wq.shape[:-2]), Wq.shape[-2], 2 * Wq.shape[-1]
+    W = torch.empty((*lead, K, N), dtype=torch.bfloat16, device=Wq.device)
+    moe_dequantize_w4(Wq, scales, zeros, lead[0] if lead else 1, K, N, K // scales.shape[-1], W, stream)
+    return W
 
 
 def moe_pack_weights_nk(W, G: int, K: int, N: int, W_nk, stream=None) -> None:

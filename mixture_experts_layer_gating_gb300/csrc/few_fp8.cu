@@ -1,0 +1,6 @@
+// The few-token layer for e4m3 expert weights stored [.., K, N].
+#include "few_layer.cuh"
+
+namespace moe {
+cudaError_t launch_few_fp8(const FewArgs& a, cudaStream_t s) { return launch_few_kind<kStreamFp8, 0>(a, s); }
+}  // namespace moe

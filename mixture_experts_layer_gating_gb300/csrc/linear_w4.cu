@@ -1,0 +1,433 @@
+// y = x W^T for at most 32 rows of x and 4-bit weights with group scales
+// (moe_linear_w4), and the weights' way into and out of the 4-bit form.
+#include "stream_sm103.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kLinStrip = 128;  // output features of a strip (one stage's rows)
+
+struct LinParams {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* sc;
+  const uint8_t* zp;
+  void* y;
+  int32_t* err;
+  int32_t* cnt;   // [strips] arrivals, zero between launches
+  float* part;    // [ctas][2][M][128]: a CTA's part of a strip begun earlier, of one it leaves unfinished
+  int M, K, N;
+};
+
+template <int GRP, int NT>
+struct LinSmem {
+  using Tr = StreamTraits<kStreamW4, GRP>;
+  static constexpr int kBBuf = 8 * NT * Tr::PITCH;
+  struct Ctrl {
+    uint64_t full[12], empty[12];
+    int abort;
+    int last;
+  };
+  static constexpr int kOther = 2 * kBBuf + static_cast<int>(sizeof(Ctrl)) + 16;
+  static constexpr int NST = stream_stages(kOther);
+  static constexpr int kBytes = 1024 + NST * kStageBytes + kOther;
+};
+
+__device__ __forceinline__ void store_y(float* y, size_t at, float v) { y[at] = v; }
+__device__ __forceinline__ void store_y(__nv_bfloat16* y, size_t at, float v) {
+  y[at] = __float2bfloat16_rn(v);
+}
+
+// Strips of 128 output features x stages of 256 k, divided into equal runs
+// over the CTAs.  A strip inside one CTA's run is written at once; one that
+// several CTAs share gets its parts added, in the order of k, by the CTA that
+// finishes last (an arrival count per strip).
+template <int GRP, int NT, bool ZERO, typename TY>
+__global__ void __launch_bounds__(kStreamBlock, 1)
+    linear_w4_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ LinParams p) {
+  using Tr = StreamTraits<kStreamW4, GRP>;
+  using Sm = LinSmem<GRP, NT>;
+  using Ctrl = typename Sm::Ctrl;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* ring_ptr = smem_raw + pad;
+  uint8_t* bptr = ring_ptr + Sm::NST * kStageBytes;
+  Ctrl* ctl = reinterpret_cast<Ctrl*>(bptr + 2 * Sm::kBBuf);
+  const int tid = threadIdx.x, b = blockIdx.x, G = gridDim.x;
+  const int C = (p.K + 255) / 256, S = (p.N + kLinStrip - 1) / kLinStrip;
+  const Split sp = make_split(static_cast<long long>(S) * C, G);
+  const long long lo = split_lo(sp, b), hi = split_lo(sp, b + 1);
+
+  if (tid == 0) {
+    for (int i = 0; i < Sm::NST; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], kStreamWarps);
+    }
+    ctl->abort = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (tid >= kStreamThreads) {  // producer
+    if ((tid & 31) == 0) {
+      const uint64_t policy = l2_policy_evict_first();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      long long q = lo;
+      for (; q < hi; ++q) {
+        if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort)) {
+          ok = false;
+          break;
+        }
+        const int s = static_cast<int>(q / C), kc = static_cast<int>(q % C);
+        uint8_t* d = ring_ptr + stage * kStageBytes;
+        mbar_arrive_expect_tx(&ctl->full[stage], kStageBytes);
+        tma_load_2d(d, &mw, &ctl->full[stage], kc * 128, s * kLinStrip, policy);
+        if (++stage == Sm::NST) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok || *reinterpret_cast<volatile int*>(&ctl->abort)) {
+        if (!*reinterpret_cast<volatile int*>(&ctl->abort)) {
+          *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+          atomicOr(p.err, MOE_DEV_WAIT_TIMEOUT);
+        }
+        for (int i = 0; i < Sm::NST; ++i) {
+          stage = stage == 0 ? Sm::NST - 1 : stage - 1;
+          if (stage == Sm::NST - 1) phase ^= 1u;
+          mbar_wait_drain(&ctl->full[stage], phase);
+        }
+        drain_grace();
+      }
+    }
+    return;
+  }
+
+  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_u32(ring_ptr), bbase = smem_u32(bptr);
+  TY* y = static_cast<TY*>(p.y);
+  // x rows of a stage: 32 pieces of 8 inputs a row, NT pieces a thread (row
+  // tid / 32 + 8 i, piece tid % 32), put in the k order of the weights on the way
+  constexpr int J = GRP / 32;
+  const int pc = tid & 31, prow = tid >> 5;
+  const int pq = pc / (4 * J), pr = pc % (4 * J);
+  const uint32_t pdst = ((pq * J + pr % J) * 4 + pr / J) * 16;
+  uint4 xr[NT];
+  auto load_x = [&](int kc) {
+    const int k0 = kc * 256 + pc * 8;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int row = prow + 8 * i;
+      xr[i] = make_uint4(0, 0, 0, 0);
+      if (row < p.M && k0 < p.K)
+        xr[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row) * p.K + k0));
+    }
+  };
+  auto put_x = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      uint4 v;
+      v.x = __byte_perm(xr[i].x, xr[i].z, 0x5410);
+      v.y = __byte_perm(xr[i].x, xr[i].z, 0x7632);
+      v.z = __byte_perm(xr[i].y, xr[i].w, 0x5410);
+      v.w = __byte_perm(xr[i].y, xr[i].w, 0x7632);
+      *reinterpret_cast<uint4*>(bptr + buf * Sm::kBBuf + (prow + 8 * i) * Tr::PITCH + pdst) = v;
+    }
+  };
+  W4Scales<GRP> sc_now, sc_next;
+  const int r = nk_row<kStreamW4, GRP>(g);
+  auto scales = [&](W4Scales<GRP>& dst, int s, int kc) {
+    const int n0 = s * kLinStrip + warp * 16 + r;
+    w4_load_scales<GRP>(dst, p.sc, p.zp, n0 < p.N ? n0 : -1, n0 + 8 < p.N ? n0 + 8 : -1, p.K / GRP,
+                        kc * (256 / GRP), lane);
+  };
+
+  float acc[NT][1][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][0][t] = 0.0f;
+  const int ntu = (p.M + 7) >> 3;
+  int s = 0, kc = 0;
+  if (lo < hi) {
+    s = static_cast<int>(lo / C);
+    kc = static_cast<int>(lo % C);
+    load_x(kc);
+    scales(sc_next, s, kc);
+  }
+  bool begun_earlier = kc != 0;
+  int stage = 0, buf = 0;
+  uint32_t phase = 0;
+  for (long long q = lo; q < hi; ++q) {
+    put_x(buf);
+    sc_now = sc_next;
+    const bool strip_end = kc + 1 == C;
+    if (q + 1 < hi) {
+      load_x(strip_end ? 0 : kc + 1);
+      scales(sc_next, strip_end ? s + 1 : s, strip_end ? 0 : kc + 1);
+    }
+    bar_consumers();
+    if (!mbar_wait(&ctl->full[stage], phase, &ctl->abort)) {
+      if (lane == 0 && !*reinterpret_cast<volatile int*>(&ctl->abort)) {
+        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+        atomicOr(p.err, MOE_DEV_WAIT_TIMEOUT);
+      }
+    }
+    __syncwarp();
+    stage_mma_w4<GRP, NT, false, ZERO>(ring + stage * kStageBytes, bbase + buf * Sm::kBBuf, 0, warp, lane,
+                                       ntu, sc_now, min(256, p.K - kc * 256) / GRP, acc);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->empty[stage]);
+    if (++stage == Sm::NST) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    buf ^= 1;
+
+    if (strip_end || q + 1 == hi) {
+      const int col = warp * 16 + r, n0 = s * kLinStrip;
+      if (strip_end && !begun_earlier) {  // the whole strip is this CTA's
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int row = nt * 8 + 2 * c + (t & 1), n = n0 + col + (t >> 1) * 8;
+            if (row < p.M && n < p.N) store_y(y, static_cast<size_t>(row) * p.N + n, acc[nt][0][t]);
+          }
+      } else {
+        float* mine = p.part + (static_cast<size_t>(b) * 2 + (begun_earlier ? 0 : 1)) * p.M * kLinStrip;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int row = nt * 8 + 2 * c + (t & 1);
+            if (row < p.M) mine[row * kLinStrip + col + (t >> 1) * 8] = acc[nt][0][t];
+          }
+        __threadfence();
+        bar_consumers();
+        const long long q0 = static_cast<long long>(s) * C;
+        const int c0 = split_cta(sp, q0), c1 = split_cta(sp, q0 + C - 1);
+        if (tid == 0) ctl->last = atomicAdd(p.cnt + s, 1) == c1 - c0;
+        bar_consumers();
+        if (ctl->last) {
+          __threadfence();
+          for (int i = tid; i < p.M * kLinStrip; i += kStreamThreads) {
+            const int row = i / kLinStrip, n = n0 + i % kLinStrip;
+            if (n >= p.N) continue;
+            float v = __ldcg(p.part + (static_cast<size_t>(c0) * 2 + 1) * p.M * kLinStrip + i);
+            for (int cta = c0 + 1; cta <= c1; ++cta)
+              v += __ldcg(p.part + static_cast<size_t>(cta) * 2 * p.M * kLinStrip + i);
+            store_y(y, static_cast<size_t>(row) * p.N + n, v);
+          }
+          if (tid == 0) p.cnt[s] = 0;
+        }
+      }
+      begun_earlier = false;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][0][t] = 0.0f;
+    }
+    if (strip_end) {
+      kc = 0;
+      ++s;
+    } else {
+      ++kc;
+    }
+  }
+}
+
+template <int GRP, int NT, bool ZERO, typename TY>
+cudaError_t launch_lin(const CUtensorMap& m, const LinParams& p, int grid, cudaStream_t s) {
+  using Sm = LinSmem<GRP, NT>;
+  auto kern = linear_w4_kernel<GRP, NT, ZERO, TY>;
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+  }
+  return launch_kernel(kern, dim3(grid), dim3(kStreamBlock), Sm::kBytes, s, m, p);
+}
+
+template <int GRP, int NT>
+cudaError_t launch_lin_types(const CUtensorMap& m, const LinParams& p, bool f32, int grid, cudaStream_t s) {
+  if (p.zp)
+    return f32 ? launch_lin<GRP, NT, true, float>(m, p, grid, s)
+               : launch_lin<GRP, NT, true, __nv_bfloat16>(m, p, grid, s);
+  return f32 ? launch_lin<GRP, NT, false, float>(m, p, grid, s)
+             : launch_lin<GRP, NT, false, __nv_bfloat16>(m, p, grid, s);
+}
+
+template <int GRP>
+cudaError_t launch_lin_rows(const CUtensorMap& m, const LinParams& p, bool f32, int grid, cudaStream_t s) {
+  if (p.M <= 8) return launch_lin_types<GRP, 1>(m, p, f32, grid, s);
+  if (p.M <= 16) return launch_lin_types<GRP, 2>(m, p, f32, grid, s);
+  return launch_lin_types<GRP, 4>(m, p, f32, grid, s);
+}
+
+// ------------------------------------------------------------ 4-bit weights
+constexpr int kQCols = 64;
+
+// One group of 64 columns per block: column amax, scale = bf16(amax / 7), codes
+// round(w / scale) + 8 in [0, 15].  Bound by the reads of W.
+template <int GRP, typename T>
+__global__ void __launch_bounds__(256) quantize_w4_kernel(const T* __restrict__ W, int K, int N,
+                                                          uint8_t* __restrict__ q,
+                                                          __nv_bfloat16* __restrict__ sc) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ float tile[GRP][kQCols + 1];
+  __shared__ float scale[kQCols];
+  const int tid = threadIdx.x, n0 = blockIdx.x * kQCols, kg = blockIdx.y;
+  const size_t mat = blockIdx.z;
+  const T* src = W + mat * K * N + static_cast<size_t>(kg) * GRP * N;
+  for (int i = tid; i < GRP * kQCols; i += 256) {
+    const int k = i / kQCols, n = i % kQCols;
+    tile[k][n] = n0 + n < N ? static_cast<float>(src[static_cast<size_t>(k) * N + n0 + n]) : 0.0f;
+  }
+  __syncthreads();
+  if (tid < kQCols) {
+    float m = 0.0f;
+    bool bad = false;
+    for (int k = 0; k < GRP; ++k) {
+      const float v = fabsf(tile[k][tid]);
+      bad |= !isfinite(v);
+      m = fmaxf(m, v);
+    }
+    float s = __bfloat162float(__float2bfloat16_rn(m / 7.0f));
+    if (bad) s = __int_as_float(0x7fc00000);  // a group with an Inf or NaN: its products are NaN
+    else if (s == 0.0f) s = 1.0f;             // all zeros (or below the scale's range)
+    scale[tid] = s;
+    if (n0 + tid < N) sc[(mat * N + n0 + tid) * (K / GRP) + kg] = __float2bfloat16_rn(s);
+  }
+  __syncthreads();
+  constexpr int WORDS = GRP / 8;
+  for (int i = tid; i < kQCols * WORDS; i += 256) {
+    const int n = i / WORDS, w = i % WORDS;
+    if (n0 + n >= N) continue;
+    const float s = scale[n];
+    uint32_t v = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = rintf(tile[8 * w + j][n] / s);
+      const int u = isnan(t) ? 8 : static_cast<int>(fminf(fmaxf(t, -8.0f), 7.0f)) + 8;
+      v |= static_cast<uint32_t>(u) << (4 * j);
+    }
+    *reinterpret_cast<uint32_t*>(q + (mat * N + n0 + n) * (K / 2) + static_cast<size_t>(kg) * (GRP / 2) + 4 * w) = v;
+  }
+}
+
+// W[k][n] = bf16((code - zero) * scale), back in the [.., K, N] layout.
+template <int GRP>
+__global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint8_t* __restrict__ q,
+                                                            const __nv_bfloat16* __restrict__ sc,
+                                                            const uint8_t* __restrict__ zp, int K, int N,
+                                                            __nv_bfloat16* __restrict__ W) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ __nv_bfloat16 tile[GRP][kQCols + 2];
+  const int tid = threadIdx.x, n0 = blockIdx.x * kQCols, kg = blockIdx.y;
+  const size_t mat = blockIdx.z;
+  constexpr int WORDS = GRP / 8;
+  for (int i = tid; i < kQCols * WORDS; i += 256) {
+    const int n = i / WORDS, w = i % WORDS;
+    if (n0 + n >= N) continue;
+    const size_t row = mat * N + n0 + n;
+    const uint32_t v =
+        *reinterpret_cast<const uint32_t*>(q + row * (K / 2) + static_cast<size_t>(kg) * (GRP / 2) + 4 * w);
+    const size_t at = row * (K / GRP) + kg;
+    const float s = __bfloat162float(sc[at]);
+    const int z = zp ? zp[at] & 15 : 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      tile[8 * w + j][n] = __float2bfloat16_rn(static_cast<float>(static_cast<int>((v >> (4 * j)) & 15u) - z) * s);
+  }
+  __syncthreads();
+  __nv_bfloat16* dst = W + mat * K * N + static_cast<size_t>(kg) * GRP * N;
+  for (int i = tid; i < GRP * kQCols; i += 256) {
+    const int k = i / kQCols, n = i % kQCols;
+    if (n0 + n < N) dst[static_cast<size_t>(k) * N + n0 + n] = tile[k][n];
+  }
+}
+
+template <int GRP>
+cudaError_t launch_quantize(const void* W, bool f32, long long G, int K, int N, uint8_t* q,
+                            __nv_bfloat16* sc, cudaStream_t s) {
+  const dim3 grid((N + kQCols - 1) / kQCols, K / GRP, static_cast<unsigned>(G));
+  if (f32)
+    return launch_kernel(quantize_w4_kernel<GRP, float>, grid, dim3(256), 0, s, static_cast<const float*>(W),
+                         K, N, q, sc);
+  return launch_kernel(quantize_w4_kernel<GRP, __nv_bfloat16>, grid, dim3(256), 0, s,
+                       static_cast<const __nv_bfloat16*>(W), K, N, q, sc);
+}
+
+template <int GRP>
+cudaError_t launch_dequantize(const uint8_t* q, const __nv_bfloat16* sc, const uint8_t* zp, long long G,
+                              int K, int N, __nv_bfloat16* W, cudaStream_t s) {
+  const dim3 grid((N + kQCols - 1) / kQCols, K / GRP, static_cast<unsigned>(G));
+  return launch_kernel(dequantize_w4_kernel<GRP>, grid, dim3(256), 0, s, q, sc, zp, K, N, W);
+}
+
+}  // namespace
+
+size_t linear_w4_strips(int N) { return (static_cast<size_t>(N) + kLinStrip - 1) / kLinStrip; }
+size_t linear_w4_part_bytes(int M) {
+  return static_cast<size_t>(kStreamMaxCtas) * 2 * M * kLinStrip * 4;
+}
+
+cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, const void* wq, const void* sc,
+                             const uint8_t* zp, void* y, bool y_f32, int32_t* err, int32_t* cnt, float* part,
+                             cudaStream_t s) {
+  CUtensorMap m;
+  const uint64_t dims[2] = {static_cast<uint64_t>(K) / 2, static_cast<uint64_t>(N)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(K) / 2};
+  const uint32_t box[2] = {128, kLinStrip};
+  if (!encode_tmap(&m, wq, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8)) return cudaErrorInvalidValue;
+  LinParams p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.sc = static_cast<const __nv_bfloat16*>(sc);
+  p.zp = zp;
+  p.y = y;
+  p.err = err;
+  p.cnt = cnt;
+  p.part = part;
+  p.M = M;
+  p.K = K;
+  p.N = N;
+  const long long chunks = static_cast<long long>(linear_w4_strips(N)) * ((K + 255) / 256);
+  int grid = device_sm_count();
+  if (grid > kStreamMaxCtas) grid = kStreamMaxCtas;
+  if (grid > chunks) grid = static_cast<int>(chunks);
+  if (group == 32) return launch_lin_rows<32>(m, p, y_f32, grid, s);
+  if (group == 64) return launch_lin_rows<64>(m, p, y_f32, grid, s);
+  return launch_lin_rows<128>(m, p, y_f32, grid, s);
+}
+
+cudaError_t launch_quantize_w4(const void* W, bool f32, long long G, int K, int N, int group, void* q,
+                               void* sc, cudaStream_t s) {
+  auto* qq = static_cast<uint8_t*>(q);
+  auto* ss = static_cast<__nv_bfloat16*>(sc);
+  if (group == 32) return launch_quantize<32>(W, f32, G, K, N, qq, ss, s);
+  if (group == 64) return launch_quantize<64>(W, f32, G, K, N, qq, ss, s);
+  return launch_quantize<128>(W, f32, G, K, N, qq, ss, s);
+}
+
+cudaError_t launch_dequantize_w4(const void* q, const void* sc, const uint8_t* zp, long long G, int K, int N,
+                                 int group, void* W, cudaStream_t s) {
+  auto* qq = static_cast<const uint8_t*>(q);
+  auto* ss = static_cast<const __nv_bfloat16*>(sc);
+  auto* ww = static_cast<__nv_bfloat16*>(W);
+  if (group == 32) return launch_dequantize<32>(qq, ss, zp, G, K, N, ww, s);
+  if (group == 64) return launch_dequantize<64>(qq, ss, zp, G, K, N, ww, s);
+  return launch_dequantize<128>(qq, ss, zp, G, K, N, ww, s);
+}
+
+}  // namespace moe

@@ -109,8 +109,11 @@ bool cfg_valid(const moe_config_t* c) {
   if (c->act != MOE_ACT_SWIGLU && c->act != MOE_ACT_GEGLU_TANH) return false;
   if (c->act_dtype != MOE_F32 && c->act_dtype != MOE_BF16) return false;
   if (c->w_dtype != MOE_F32 && c->w_dtype != MOE_BF16 && c->w_dtype != MOE_FP8_E4M3 &&
-      c->w_dtype != MOE_FP8_E4M3_NK && c->w_dtype != MOE_FP8_E4M3_NK_A8)
+      c->w_dtype != MOE_FP8_E4M3_NK && c->w_dtype != MOE_FP8_E4M3_NK_A8 && !w4_group(c->w_dtype))
     return false;
+  // 4-bit weights: whole groups along both reductions
+  if (const int g = w4_group(c->w_dtype))
+    if (c->D % g || c->I % g || c->I_shared % g) return false;
   if ((c->w_dtype == MOE_FP8_E4M3 || c->w_dtype == MOE_FP8_E4M3_NK ||
        c->w_dtype == MOE_FP8_E4M3_NK_A8) &&
       (c->D % 16 || c->I % 16 || c->I_shared % 16))
@@ -123,7 +126,7 @@ bool cfg_valid(const moe_config_t* c) {
 bool combo_supported(const moe_config_t* c) {
   if (c->act_dtype == MOE_F32) return c->w_dtype == MOE_F32;
   return c->w_dtype == MOE_BF16 || c->w_dtype == MOE_FP8_E4M3 || c->w_dtype == MOE_FP8_E4M3_NK ||
-         c->w_dtype == MOE_FP8_E4M3_NK_A8;
+         c->w_dtype == MOE_FP8_E4M3_NK_A8 || w4_group(c->w_dtype);
 }
 
 }  // namespace moe
@@ -237,6 +240,8 @@ Layout make_layout(const moe_config_t* c) {
     L.hs16 = take(T * Is * 2);
     L.hs_inv = take(T * 4);
   }
+  // moe_layer_few's scratch is the last region
+  if (const size_t few = few_workspace_bytes(c)) take(few);
   L.total = cur;
   return L;
 }
@@ -634,6 +639,7 @@ int moe_grouped_ffn(const moe_config_t* cfg, const void* x_perm, const int32_t* 
                     size_t ws_bytes, void* stream) {
   int st = common_checks(cfg, ws, ws_bytes);
   if (st != MOE_OK) return st;
+  if (w4_group(cfg->w_dtype)) return MOE_ERR_UNSUPPORTED;  // moe_layer_few
   if (!x_perm || !offsets || !W13 || !W2 || !h || !y_perm) return MOE_ERR_INVALID_ARG;
   for (const void* p : {x_perm, W13, W2, static_cast<const void*>(h), static_cast<const void*>(y_perm)})
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
@@ -691,6 +697,7 @@ int moe_layer(const moe_config_t* cfg, const void* x, const void* Wg, const floa
               void* ws, size_t ws_bytes, void* stream) {
   int st = common_checks(cfg, ws, ws_bytes);
   if (st != MOE_OK) return st;
+  if (w4_group(cfg->w_dtype)) return MOE_ERR_UNSUPPORTED;  // moe_layer_few
   if (!x || !Wg || !W13 || !W2 || !out) return MOE_ERR_INVALID_ARG;
   for (const void* p : {x, Wg, W13, W2, static_cast<const void*>(out)})
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
@@ -940,7 +947,7 @@ int moe_set_trace_events(void* const* events, int n_events) {
 }
 
 int moe_layer_launch_count(const moe_config_t* cfg) {
-  if (!cfg_valid(cfg) || cfg->T == 0) return 0;
+  if (!cfg_valid(cfg) || cfg->T == 0 || w4_group(cfg->w_dtype)) return 0;
   int n = 0;
   // router projection and top-k softmax (one launch when fused)
   const int nsplit = router_k_split(cfg->T, cfg->E, cfg->D);

@@ -21,6 +21,9 @@ static_assert(sizeof(ControlBlock) == 256, "control block is 256 bytes");
 // and down GEMMs and of the shared expert's two GEMMs (dynamic tile order),
 // zeroed by the call that launches them before its first kernel
 constexpr int kTileCounterSlot = 7;
+// reserved[kGridBarrierSlot] and [kGridBarrierSlot + 16]: arrivals and
+// generation of moe_layer_few's grid barrier (arrivals are zero between launches)
+constexpr int kGridBarrierSlot = 31;
 
 // ------------------------------------------------- programmatic dependent launch
 // Every kernel of the library starts with pdl_wait() (griddepcontrol.wait:
@@ -71,6 +74,28 @@ bool encode_tmap(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims
 // w_dtype, act) combination is built.
 bool cfg_valid(const moe_config_t* c);
 bool combo_supported(const moe_config_t* c);
+
+// Inputs per group of a 4-bit weight type, 0 for the other types.
+inline int w4_group(int dt) {
+  return dt == MOE_W4_G32 ? 32 : dt == MOE_W4_G64 ? 64 : dt == MOE_W4_G128 ? 128 : 0;
+}
+
+// ---------------------------------------------------------------- few_api.cu
+// Whether moe_layer_few takes the configuration, and the scratch it needs at
+// the end of the workspace (0: not taken).
+bool few_supported(const moe_config_t* c);
+size_t few_workspace_bytes(const moe_config_t* c);
+
+// ---------------------------------------------------------------- linear_w4.cu
+size_t linear_w4_strips(int N);     // arrival counters of a product
+size_t linear_w4_part_bytes(int M); // room for the partial sums
+cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, const void* wq, const void* sc,
+                             const uint8_t* zp, void* y, bool y_f32, int32_t* err, int32_t* cnt, float* part,
+                             cudaStream_t s);
+cudaError_t launch_quantize_w4(const void* W, bool f32, long long G, int K, int N, int group, void* q,
+                               void* sc, cudaStream_t s);
+cudaError_t launch_dequantize_w4(const void* q, const void* sc, const uint8_t* zp, long long G, int K, int N,
+                                 int group, void* W, cudaStream_t s);
 
 inline size_t act_bytes(int dt) { return dt == MOE_F32 ? 4 : 2; }
 inline size_t w_bytes(int dt) { return dt == MOE_F32 ? 4 : (dt == MOE_BF16 ? 2 : 1); }
