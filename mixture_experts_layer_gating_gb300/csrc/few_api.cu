@@ -41,7 +41,7 @@ int few_planes(const moe_config_t* c) {
 }
 
 struct FewLayout {
-  size_t planes, xp, hp, prim, extra, total;
+  size_t cnt, planes, xp, xinv, hp, hmax, part, prim, extra, total;
   int Dp, Ip, W;
 };
 FewLayout few_layout(const moe_config_t* c) {
@@ -49,7 +49,7 @@ FewLayout few_layout(const moe_config_t* c) {
   FewLayout L{};
   L.Dp = ceil_div(c->D, g.kch) * g.kch;
   L.Ip = ceil_div(std::max(c->I, c->I_shared), g.kch) * g.kch;
-  L.W = 2 * g.hc * std::max({ceil_div(c->I, g.hc), ceil_div(c->I_shared, g.hc), ceil_div(c->D, 2 * g.hc)});
+  L.W = 2 * g.hc * ceil_div(c->D, 2 * g.hc);
   const size_t T = c->T, rows = T * c->k + T;
   size_t cur = 0;
   auto take = [&](size_t bytes) {
@@ -57,9 +57,13 @@ FewLayout few_layout(const moe_config_t* c) {
     cur = up256(cur + bytes);
     return o;
   };
+  L.cnt = take(2 * kStreamMaxCtas * 4);
   L.planes = take(static_cast<size_t>(few_planes(c)) * T * c->E * 4);
   L.xp = take(T * L.Dp * 2);
-  L.hp = take(2 * rows * L.Ip * 2);
+  L.xinv = take(T * 4);
+  L.hp = take(rows * L.Ip * 4);
+  L.hmax = take(rows * 4);
+  L.part = take(static_cast<size_t>(4) * kStreamMaxCtas * T * 2 * g.hc * 4);
   L.prim = take(rows * L.W * 4);
   L.extra = take(static_cast<size_t>(2) * kStreamMaxCtas * T * 2 * g.hc * 4);
   L.total = cur;
@@ -96,6 +100,8 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
     if (!q || !al16(q)) return MOE_ERR_INVALID_ARG;
   const bool scaled = cfg->w_dtype != MOE_BF16, shared = cfg->I_shared > 0;
   if (scaled != (s13 != nullptr) || scaled != (s2 != nullptr)) return MOE_ERR_INVALID_ARG;
+  for (const void* q : {s13, s2, shared ? s13s : nullptr, shared ? s2s : nullptr})
+    if (!al16(q)) return MOE_ERR_INVALID_ARG;
   if (shared) {
     if (!W13s || !W2s || !al16(W13s) || !al16(W2s)) return MOE_ERR_INVALID_ARG;
     if (scaled != (s13s != nullptr) || scaled != (s2s != nullptr)) return MOE_ERR_INVALID_ARG;
@@ -117,12 +123,16 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
   ControlBlock* cb = reinterpret_cast<ControlBlock*>(ws);
   p.err = &cb->err;
   p.bar = reinterpret_cast<uint32_t*>(cb->reserved + kGridBarrierSlot);
+  p.cnt = reinterpret_cast<int32_t*>(few + L.cnt);
   p.logits = reinterpret_cast<float*>(base + moe_workspace_offset(cfg, MOE_WS_LOGITS));
   p.ids = reinterpret_cast<int32_t*>(base + moe_workspace_offset(cfg, MOE_WS_TOPK_IDS));
   p.topw = reinterpret_cast<float*>(base + moe_workspace_offset(cfg, MOE_WS_TOPK_W));
   p.planes = reinterpret_cast<float*>(few + L.planes);
-  p.xp = reinterpret_cast<__nv_bfloat16*>(few + L.xp);
-  p.hp = reinterpret_cast<__nv_bfloat16*>(few + L.hp);
+  p.xp = reinterpret_cast<uint16_t*>(few + L.xp);
+  p.xinv = reinterpret_cast<float*>(few + L.xinv);
+  p.hp = few + L.hp;
+  p.hmax = reinterpret_cast<uint32_t*>(few + L.hmax);
+  p.part = reinterpret_cast<float*>(few + L.part);
   p.prim = reinterpret_cast<float*>(few + L.prim);
   p.extra = reinterpret_cast<float*>(few + L.extra);
   p.T = cfg->T;
@@ -154,7 +164,7 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
 
 size_t moe_linear_w4_workspace_size(int32_t M, int32_t K, int32_t N) {
   if (M < 0 || M > kStreamMaxRows || K < 32 || K % 32 || N < 1) return 0;
-  return sizeof(ControlBlock) + up256(linear_w4_strips(N) * 4) + linear_w4_part_bytes(std::max(M, 1));
+  return sizeof(ControlBlock) + up256(kStreamMaxCtas * 4) + linear_w4_part_bytes(std::max(M, 1));
 }
 
 int moe_linear_w4(int32_t M, int32_t K, int32_t N, int32_t group, const void* x, const void* Wq,
@@ -169,7 +179,7 @@ int moe_linear_w4(int32_t M, int32_t K, int32_t N, int32_t group, const void* x,
   if (M == 0) return MOE_OK;
   uint8_t* base = static_cast<uint8_t*>(ws);
   int32_t* cnt = reinterpret_cast<int32_t*>(base + sizeof(ControlBlock));
-  float* part = reinterpret_cast<float*>(base + sizeof(ControlBlock) + up256(linear_w4_strips(N) * 4));
+  float* part = reinterpret_cast<float*>(base + sizeof(ControlBlock) + up256(kStreamMaxCtas * 4));
   const cudaError_t e =
       launch_linear_w4(M, K, N, group, x, Wq, scales, static_cast<const uint8_t*>(zeros), y,
                        y_dtype == MOE_F32, &reinterpret_cast<ControlBlock*>(ws)->err, cnt, part,

@@ -1,18 +1,25 @@
 // The whole MoE layer for at most 32 tokens as one cooperative launch of one
-// CTA per SM (moe_layer_few).  Phases, a grid barrier between each two:
+// CTA per SM (moe_layer_few).  Phases, with a grid barrier where one needs
+// another CTA's results:
 //   0  router projection into fp32 planes (slices of D); x in the k order of the
 //      weight layout (perm_k), zero-padded to whole stages
-//   1  CTA t: token t's planes summed, top-k softmax
-//   2  every CTA lists the chosen experts and their rows; gate/up products:
-//      the chosen experts' (and the shared expert's) weight stages, one equal
-//      run of them per CTA, so every SM streams the same number of bytes
-//      whatever the routing; a 64-column strip that two CTAs share gets one
-//      partial sum from each
-//   3  h = act(gate) * up of the summed strips, as a bf16 pair (hi, lo)
-//   4  down products, divided up the same way
-//   5  out = sum_j w_j y_j + shared, from the partial sums, one rounding
-// The producer thread runs ahead of the barriers: the weights of the next
-// phase are on their way while the barrier is waited for (up to 192 KB per SM).
+//   -- barrier 0
+//   1  top-k softmax: every CTA for every token where the planes are small (one
+//      warp per token), else CTA t for token t and barrier 1; every CTA then
+//      lists the chosen experts and their rows
+//   2  gate/up products: the chosen experts' (and the shared expert's) weight
+//      stages, one equal run of them per CTA, so that every SM streams the same
+//      number of bytes whatever the routing.  At the end of a strip of columns
+//      h = act(gate) * up, as a bf16 pair (hi, lo) in the k order of the down
+//      weights; of a strip that several CTAs share, the one that finishes last
+//      adds the partial sums (in the order of k) and does that
+//   -- barrier 2
+//   3  down products, divided up the same way, into fp32 rows and the partial
+//      sums of shared strips
+//   -- barrier 3
+//   4  out = sum_j w_j y_j + shared, one rounding
+// The producer runs ahead of the barriers: the weights of the next phase are on
+// their way while a barrier is waited for (up to 192 KB per SM).
 #pragma once
 
 #include "stream_sm103.cuh"
@@ -22,6 +29,9 @@ namespace moe {
 
 constexpr int kFewMaxPlanes = 16;
 constexpr int kFewMaxR = 512;  // expanded rows: 32 tokens, 16 experts each
+// Up to this many bytes of router planes every CTA reads them all (152 x 64 KB
+// from L2 take about as long as one more barrier).
+constexpr int kFewPlaneBytes = 65536;
 
 struct FewParams {
   const __nv_bfloat16* x;
@@ -30,15 +40,21 @@ struct FewParams {
   const void *s13, *s2, *s13s, *s2s;  // fp32 per column (e4m3) or bf16 per group (4-bit)
   __nv_bfloat16* out;
   int32_t* err;
-  uint32_t* bar;  // grid barrier: arrivals at [0], generation at [16]
+  uint32_t* bar;  // grid barriers: arrivals of barrier i at [8 i], all zero between launches but
+                  // barrier 3's, which the next launch clears
+  int32_t* cnt;   // [2][kStreamMaxCtas]: arrivals at the strip that CTA c begins and others share
   float* logits;
   int32_t* ids;
   float* topw;
   float* planes;       // [nplanes][T][E]
-  __nv_bfloat16* xp;   // [T][Dp]
-  __nv_bfloat16* hp;   // [2][R + T][Ip] (hi, lo); row R + t: token t of the shared expert
-  float* prim;         // [R + T][W]: the first partial sum of every strip of a row
-  float* extra;        // [2][ctas][T][2 HC]: a CTA's part of a strip begun by an earlier one
+  uint16_t* xp;        // [T][Dp]: x in the weights' k order, bf16 or scaled fp16
+  float* xinv;         // [T]: what undoes the scale
+  void* hp;            // [R + T][Ip] h, row R + t token t of the shared expert: fp32 in natural
+                       // order, or (bf16 weights) [2][R + T][Ip] bf16 hi and lo in the k order
+  uint32_t* hmax;      // [R + T]: the row's largest |h| (bits of an fp32)
+  float* part;         // [2][ctas][2][T][2 HC]: gate/up sums of shared strips
+  float* prim;         // [R + T][W]: the first partial sum of every down strip of a row
+  float* extra;        // [2][ctas][T][2 HC]: a CTA's part of a down strip begun by an earlier one
   int T, D, E, k, I, Is, act, renorm;
   int Dp, Ip;          // padded row lengths of xp, hp (elements)
   int W;               // floats per row of prim
@@ -54,27 +70,35 @@ __device__ __forceinline__ float few_act(float g, float u, int act) {
 template <int KIND, int GRP, int NT>
 struct FewSmem {
   using Tr = StreamTraits<KIND, GRP>;
-  static constexpr int kBBuf = 2 * 8 * NT * Tr::PITCH;  // hi and lo rows of one stage's k
-  static constexpr int kRed = Tr::KN ? 8 * NT * (2 * Tr::HC + 4) * 4 : 0;
-  static constexpr int kRedMin = 8 * NT * 68 * 4;       // the router's partial sums
-  static constexpr int kRedBytes = kRed > kRedMin ? kRed : kRedMin;
+  // Two consumer teams where the accumulators leave room (at most 96 registers a thread)
+  static constexpr int kTeams = KIND == kStreamFp8 ? (NT == 1 ? 2 : 1) : (NT <= 2 ? 2 : 1);
+  static constexpr int kCons = 32 * kStreamWarps * kTeams;  // consumer threads
+  static constexpr int kFeeders = 2;                        // feeder warps
+  static constexpr int kBlock = kCons + 32 + 32 * kFeeders;
+  // token rows of a stage: bf16 weights take h as two terms
+  static constexpr bool kHilo = KIND == kStreamBf16;
+  static constexpr int kRows = (kHilo ? 2 : 1) * 8 * NT * Tr::PITCH;
+  static constexpr int kSlot = stream_slot(kRows);
+  static constexpr int kRP = 2 * Tr::HC + 4;  // floats per row of red
+  // the router's partial sums take kPlanes planes of red
+  static constexpr int kPlanes = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+  static constexpr int kRedBytes = 8 * NT * 4 * (kRP > 68 * kPlanes ? kRP : 68 * kPlanes);
   struct Ctrl {
-    uint64_t full[12], empty[12];
-    int abort;
+    StreamRing ring;
     int na;
-    int cnt[512];           // rows of an expert; the token's summed logits in phase 1
+    int cnt[512];           // rows of an expert
+    int ids[kFewMaxR];      // expert of an expanded row
+    float w[kFewMaxR];      // its weight
     uint16_t aexp[512];     // active experts, ascending
     uint16_t aoff[513];     // first sorted position of an active expert
     uint16_t amap[512];     // expert -> its index among the active
-    uint16_t sid[kFewMaxR]; // expert of an expanded row
-    uint16_t srow[kFewMaxR];  // expanded row at a sorted position
+    uint16_t srow[kFewMaxR];  // token of a sorted position
     uint16_t pos[kFewMaxR];   // sorted position of an expanded row
-    uint16_t apos[kFewMaxR];  // active index of a sorted position
   };
-  static constexpr int kOther = 3 * kBBuf + kRedBytes + static_cast<int>(sizeof(Ctrl)) + 16;
-  static constexpr int NST = stream_stages(kOther);
-  static constexpr int kBytes = 1024 + NST * kStageBytes + kOther;
-  static_assert(NST >= 4, "too few stages");
+  static constexpr int kOther = kRedBytes + static_cast<int>(sizeof(Ctrl)) + 16;
+  static constexpr int NST = stream_stages(kSlot, kOther);
+  static constexpr int kBytes = 1024 + NST * kSlot + kOther;
+  static_assert(NST >= 4 && NST % kFeeders == 0, "ring sizes");
   static_assert(kBytes <= kStreamSmemMax, "shared memory");
 };
 
@@ -82,540 +106,530 @@ struct FewSmem {
 struct FewPass {
   Split sp;
   long long lo, hi;
-  int S, C;  // strips of a group, chunks (stages) of a strip
+  int S, C;      // strips of a group, chunks (stages) of a strip
+  int K, width;  // the reduction, the output columns (of gate and up each)
 };
 template <int KIND, int GRP>
 __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, bool routed, int na, int G,
                                             int b) {
   using Tr = StreamTraits<KIND, GRP>;
-  const int K = down ? (routed ? p.I : p.Is) : p.D;
-  const int width = down ? p.D : (routed ? p.I : p.Is);
-  const int per = down ? 2 * Tr::HC : Tr::HC;
+  const int I = routed ? p.I : p.Is;
   FewPass f;
-  f.S = (width + per - 1) / per;
-  f.C = (K + Tr::KCH - 1) / Tr::KCH;
+  f.K = down ? I : p.D;
+  f.width = down ? p.D : I;
+  const int per = down ? 2 * Tr::HC : Tr::HC;
+  f.S = (f.width + per - 1) / per;
+  f.C = (f.K + Tr::KCH - 1) / Tr::KCH;
   const int groups = routed ? na : (p.Is > 0 ? 1 : 0);
   f.sp = make_split(static_cast<long long>(groups) * f.S * f.C, G);
   f.lo = split_lo(f.sp, b);
   f.hi = split_lo(f.sp, b + 1);
   return f;
 }
-
-// Waits until all G CTAs have arrived.  Bounded: after the limit the CTA flags
-// an error and goes on without waiting (every later wait ends at once).
-__device__ __forceinline__ void few_grid_sync(uint32_t* bar, int G, int* abort, int32_t* err) {
-  bar_consumers();
-  if (threadIdx.x == 0 && !*reinterpret_cast<volatile int*>(abort)) {
-    uint32_t old;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(old) : "l"(bar + 16) : "memory");
-    __threadfence();
-    if (atomicAdd(bar, 1u) == static_cast<uint32_t>(G - 1)) {
-      *reinterpret_cast<volatile uint32_t*>(bar) = 0;
-      __threadfence();
-      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(bar + 16), "r"(old + 1) : "memory");
+// A chunk's place: active expert, strip, chunk of the strip.
+struct FewAt {
+  int a, s, kc;
+  __device__ __forceinline__ FewAt(const FewPass& f, long long q) {
+    // runs start anywhere: 32-bit divisions unless the pass is huge
+    if ((f.sp.N >> 31) == 0) {
+      const uint32_t strip = static_cast<uint32_t>(q) / static_cast<uint32_t>(f.C);
+      kc = static_cast<int>(static_cast<uint32_t>(q) - strip * f.C);
+      a = static_cast<int>(strip / static_cast<uint32_t>(f.S));
+      s = static_cast<int>(strip - static_cast<uint32_t>(a) * f.S);
     } else {
-      const uint64_t t0 = globaltimer_ns();
-      for (uint32_t i = 1;; ++i) {
-        uint32_t now;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(bar + 16) : "memory");
-        if (now != old) break;
-        if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
-          *reinterpret_cast<volatile int*>(abort) = 1;
-          atomicOr(err, MOE_DEV_WAIT_TIMEOUT);
-          break;
-        }
+      const long long strip = q / f.C;
+      kc = static_cast<int>(q - strip * f.C);
+      a = static_cast<int>(strip / f.S);
+      s = static_cast<int>(strip - static_cast<long long>(a) * f.S);
+    }
+  }
+  __device__ __forceinline__ void next(const FewPass& f) {
+    if (++kc == f.C) {
+      kc = 0;
+      if (++s == f.S) {
+        s = 0;
+        ++a;
       }
     }
-    __threadfence();
   }
-  bar_consumers();
-}
+};
 
 template <int KIND, int GRP, int NT>
 struct Few {
   using Tr = StreamTraits<KIND, GRP>;
   using Sm = FewSmem<KIND, GRP, NT>;
   using Ctrl = typename Sm::Ctrl;
+  static constexpr int CT = Sm::kCons;
+
+  static __device__ __forceinline__ void bar() { bar_consumers<CT>(); }
+
+  // Grid barrier i, by the consumers.  One CTA clears the arrivals of `clear`,
+  // a barrier that every CTA has left.
+  static __device__ __forceinline__ void grid_sync(const FewParams& p, StreamRing* ring, int i, int clear) {
+    bar();
+    if (threadIdx.x == 0 && !ring->aborted()) {
+      uint32_t* at = p.bar + 8 * i;
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(at) : "memory");
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t n = 1;; ++n) {
+        uint32_t now;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(at) : "memory");
+        if (now == gridDim.x) break;
+        if ((n & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
+          ring->give_up(p.err);
+          break;
+        }
+      }
+      if (blockIdx.x == 0 && clear >= 0) *reinterpret_cast<volatile uint32_t*>(p.bar + 8 * clear) = 0;
+      if (blockIdx.x == 0 && i == 2) *reinterpret_cast<volatile uint32_t*>(p.bar + 8) = 0;
+    }
+    bar();
+  }
 
   // ---------------------------------------------------------------- producer
-  // Fills the ring with the run [f.lo, f.hi) of one pass.
   static __device__ __forceinline__ bool produce(const CUtensorMap* m, const FewPass& f, bool down,
-                                                 const uint16_t* aexp, uint32_t ring, Ctrl* ctl,
-                                                 uint8_t* ring_ptr, int& stage, uint32_t& phase,
-                                                 uint64_t policy) {
+                                                 const uint16_t* aexp, StreamRing* r, uint8_t* ring,
+                                                 RingPos& pos, uint64_t policy) {
     if (f.lo >= f.hi) return true;
-    long long strip = f.lo / f.C;
-    int kc = static_cast<int>(f.lo - strip * f.C);
-    int a = static_cast<int>(strip / f.S), s = static_cast<int>(strip % f.S);
-    for (long long q = f.lo; q < f.hi; ++q) {
-      if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort)) return false;
-      uint64_t* bar = &ctl->full[stage];
-      uint8_t* dst = ring_ptr + stage * kStageBytes;
-      const int e = aexp ? aexp[a] : 0;
-      mbar_arrive_expect_tx(bar, kStageBytes);
+    FewAt at(f, f.lo);
+    for (int left = static_cast<int>(f.hi - f.lo); left > 0; --left) {
+      if (!mbar_wait(&r->empty[pos.at], pos.phase ^ 1u, &r->abort)) return false;
+      uint64_t* full = &r->full[pos.at];
+      uint8_t* dst = ring + pos.at * Sm::kSlot;
+      const int e = aexp ? aexp[at.a] : 0;
+      mbar_arrive_expect_tx(full, kStageBytes);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint8_t* d = dst + h * kHalfBytes;
         if (Tr::KN) {
-          if (down) tma_load_3d(d, m, bar, s * 2 * Tr::HC + h * Tr::HC, kc * Tr::KCH, e, policy);
-          else tma_load_4d(d, m, bar, s * Tr::HC, h, kc * Tr::KCH, e, policy);
+          if (down) tma_load_3d(d, m, full, at.s * 2 * Tr::HC + h * Tr::HC, at.kc * Tr::KCH, e, policy);
+          else tma_load_4d(d, m, full, at.s * Tr::HC, h, at.kc * Tr::KCH, e, policy);
         } else {
-          if (down) tma_load_3d(d, m, bar, kc * 128, s * 128 + h * 64, e, policy);
-          else tma_load_4d(d, m, bar, kc * 128, s * 64, h, e, policy);
+          if (down) tma_load_3d(d, m, full, at.kc * 128, at.s * 128 + h * 64, e, policy);
+          else tma_load_4d(d, m, full, at.kc * 128, at.s * 64, h, e, policy);
         }
       }
-      if (++stage == Sm::NST) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      if (++kc == f.C) {
-        kc = 0;
-        if (++s == f.S) {
-          s = 0;
-          ++a;
+      pos.next(Sm::NST);
+      at.next(f);
+    }
+    return true;
+  }
+
+  // ------------------------------------------------------------------ feeder
+  // e such that 2^e puts a row with largest element `bits` in [2^14, 2^15): 0 for
+  // rows of zeros, at most 100 (a row below 2^-86 keeps fewer bits).  A row with
+  // an infinity or NaN takes -113, which no finite element overflows at.
+  static __device__ __forceinline__ int row_exp(uint32_t bits) {
+    const int e = static_cast<int>(bits >> 23);
+    return bits == 0 ? 0 : max(-113, min(100, 141 - e));
+  }
+  static __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
+
+  // The token rows of the run's chunks that this feeder warp takes (every
+  // kFeeders-th, always the same slots: a wait cannot mistake a fill for the one
+  // before).  n rows x KCH inputs, 8 inputs a lane.
+  template <bool DOWN, bool ROUTED>
+  static __device__ __forceinline__ bool feed(const FewParams& p, const FewPass& f, Ctrl* ctl, uint8_t* ring,
+                                              RingPos& pos, int& turn, int lane) {
+    constexpr int P = Tr::KCH / 8;  // pieces of a row
+    if (f.lo >= f.hi) return true;
+    const int R = p.T * p.k;
+    FewAt at(f, f.lo);
+    for (int left = static_cast<int>(f.hi - f.lo); left > 0; --left) {
+      if (turn == 0) {
+        if (!mbar_wait(&ctl->ring.empty[pos.at], pos.phase ^ 1u, &ctl->ring.abort)) return false;
+        const int off = ROUTED ? ctl->aoff[at.a] : 0;
+        const int n = ROUTED ? ctl->aoff[at.a + 1] - off : p.T;
+        uint8_t* rows = ring + pos.at * Sm::kSlot + kStageBytes;
+        if (DOWN && !Sm::kHilo) {
+          // fp32 h to scaled fp16, in the weights' k order
+          const int k_end = f.K - at.kc * Tr::KCH;  // inputs of this chunk (zeros beyond)
+          constexpr int U = 4;                      // pieces in flight
+          for (int i0 = lane; i0 < n * P; i0 += 32 * U) {
+            float4 a[U], b[U];
+            uint32_t mx[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int i = i0 + 32 * u, pc = i % P, row = i / P;
+              a[u] = b[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              mx[u] = 0;
+              if (i < n * P && pc * 8 < k_end) {
+                const int r = (ROUTED ? off : R) + row;
+                const float4* src = reinterpret_cast<const float4*>(
+                    static_cast<const float*>(p.hp) + static_cast<size_t>(r) * p.Ip + at.kc * Tr::KCH + pc * 8);
+                a[u] = src[0];  // (through L1: every strip takes the same rows)
+                b[u] = src[1];
+                mx[u] = p.hmax[r];
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int i = i0 + 32 * u, pc = i % P, row = i / P;
+              if (i < n * P) {
+                const float sc = exp2_int(row_exp(mx[u]));
+                const float v[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
+                uint8_t* d = rows + row * Tr::PITCH;
+                auto pair = [&](int j0, int j1) {
+                  const __half2 h = __floats2half2_rn(v[j0] * sc, v[j1] * sc);
+                  return *reinterpret_cast<const uint32_t*>(&h);
+                };
+                const int at8 = perm_k<KIND, GRP>(pc * 8) * 2;
+                if constexpr (Tr::KN) {  // pairs go to every other word
+#pragma unroll
+                  for (int j = 0; j < 8; j += 2) *reinterpret_cast<uint32_t*>(d + at8 + j * 4) = pair(j, j + 1);
+                } else if constexpr (KIND == kStreamW4) {
+                  *reinterpret_cast<uint4*>(d + at8) = make_uint4(pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7));
+                } else {
+                  *reinterpret_cast<uint4*>(d + at8) = make_uint4(pair(0, 1), pair(2, 3), pair(4, 5), pair(6, 7));
+                }
+              }
+            }
+          }
+          mbar_arrive(&ctl->ring.full[pos.at]);
+        } else {
+          const uint32_t dst = smem_u32(rows);
+          const size_t plane = static_cast<size_t>(R + p.T) * p.Ip;
+          for (int i = lane; i < n * P; i += 32) {
+            const int pc = i % P, row = i / P;
+            const int src = DOWN ? (ROUTED ? off : R) + row : (ROUTED ? ctl->srow[off + row] : row);
+            const uint16_t* g = (DOWN ? static_cast<const uint16_t*>(p.hp) : p.xp) +
+                                static_cast<size_t>(src) * (DOWN ? p.Ip : p.Dp) + at.kc * Tr::KCH + pc * 8;
+            const uint32_t d = dst + row * Tr::PITCH + pc * 16;
+            cp_async_16(d, g, 16);
+            if (DOWN) cp_async_16(d + 8 * NT * Tr::PITCH, g + plane, 16);
+          }
+          cp_async_mbar_arrive_noinc(&ctl->ring.full[pos.at]);
         }
       }
+      turn = turn == 0 ? Sm::kFeeders - 1 : turn - 1;
+      pos.next(Sm::NST);
+      at.next(f);
     }
     return true;
   }
 
   // --------------------------------------------------------------- consumers
-  // Token rows of chunk (a, kc) into buffer `buf` (cp.async, 16 bytes a piece).
-  template <bool DOWN, bool ROUTED>
-  static __device__ __forceinline__ void load_rows(const FewParams& p, const Ctrl* ctl, uint32_t buf,
-                                                   int a, int kc, int tid) {
-    constexpr int P = Tr::KCH / 8;  // pieces of a row
-    constexpr int PL = DOWN ? 2 : 1;
-    const int off = ROUTED ? ctl->aoff[a] : 0;
-    const int n = ROUTED ? ctl->aoff[a + 1] - off : p.T;
-    const int Kp = DOWN ? p.Ip : p.Dp;
-    const size_t plane = static_cast<size_t>(p.T * p.k + p.T) * p.Ip;
-    for (int i = tid; i < n * P * PL; i += kStreamThreads) {
-      const int pc = i % P, row = (i / P) / PL, pl = (i / P) % PL;
-      int src;
-      if (DOWN) src = ROUTED ? off + row : p.T * p.k + row;
-      else src = ROUTED ? ctl->srow[off + row] / p.k : row;
-      const __nv_bfloat16* g = (DOWN ? p.hp + pl * plane : p.xp) + static_cast<size_t>(src) * Kp +
-                               kc * Tr::KCH + pc * 8;
-      cp_async_16(buf + pl * (8 * NT * Tr::PITCH) + row * Tr::PITCH + pc * 16, g, 16);
-    }
+  // Where the partial sums of shared strips of gate/up are: CTA `cta`'s part of
+  // a strip begun earlier (which 0) or of one it leaves unfinished (1).
+  static __device__ __forceinline__ float* part_at(const FewParams& p, bool routed, int cta, int which) {
+    return p.part + ((static_cast<size_t>(routed ? 1 : 0) * kStreamMaxCtas + cta) * 2 + which) * p.T * 2 * Tr::HC;
   }
 
-  template <bool DOWN, bool ROUTED>
-  static __device__ __forceinline__ void consume(const FewParams& p, const FewPass& f, Ctrl* ctl,
-                                                 uint32_t ring, uint32_t bbase, float* red, int& stage,
-                                                 uint32_t& phase, int b, int G) {
-    if (f.lo >= f.hi) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, c = lane & 3;
-    constexpr uint32_t kLo = 8 * NT * Tr::PITCH;
-    const int K = DOWN ? (ROUTED ? p.I : p.Is) : p.D;
-    const int width = DOWN ? p.D : (ROUTED ? p.I : p.Is);
-    long long strip = f.lo / f.C;
-    int kc = static_cast<int>(f.lo - strip * f.C);
-    int a = static_cast<int>(strip / f.S), s = static_cast<int>(strip % f.S);
-    bool first_is_extra = kc != 0;  // this CTA's first strip was begun by an earlier one
-
-    // lookahead of the token rows: two chunks
-    int la = a, ls = s, lk = kc;
-    long long lq = f.lo;
-    auto ahead = [&](int slot) {
-      if (lq < f.hi) {
-        load_rows<DOWN, ROUTED>(p, ctl, bbase + slot * Sm::kBBuf, la, lk, tid);
-        ++lq;
-        if (++lk == f.C) {
-          lk = 0;
-          if (++ls == f.S) {
-            ls = 0;
-            ++la;
+  // A finished gate/up strip (its sums by sum(row, column, v[8])) to h rows:
+  // eight columns a thread.  bf16 weights: the last strip also zeroes the row up
+  // to the end of the down pass's last stage.
+  template <bool ROUTED, typename SUM>
+  static __device__ __forceinline__ void finish_h(const FewParams& p, const FewPass& f, const Ctrl* ctl, int a,
+                                                  int s, int n, int tid, SUM sum) {
+    const int off = ROUTED ? ctl->aoff[a] : 0, row0 = ROUTED ? off : p.T * p.k;
+    const int c0 = s * Tr::HC;
+    constexpr int per = Tr::HC / 8;  // threads of a row, consecutive lanes
+    for (int i0 = tid; i0 - (tid & 31) < n * per; i0 += CT) {
+      const bool in = i0 < n * per;
+      const int i = in ? i0 : 0, row = i / per, col = (i % per) * 8;
+      float h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = 0.0f;
+      if (c0 + col < f.width) {
+        float u[8];
+        sum(row, col, h);
+        sum(row, col + Tr::HC, u);
+        if constexpr (Tr::F16) {
+          const float inv = __ldcg(p.xinv + (ROUTED ? ctl->srow[off + row] : row));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            h[j] *= inv;
+            u[j] *= inv;
+          }
+        }
+        if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
+          const float4* sc = reinterpret_cast<const float4*>(
+              static_cast<const float*>(ROUTED ? p.s13 : p.s13s) +
+              (ROUTED ? static_cast<size_t>(ctl->aexp[a]) * 2 * f.width : 0) + c0 + col);
+          const float4 g0 = __ldg(sc), g1 = __ldg(sc + 1), u0 = __ldg(sc + f.width / 4), u1 = __ldg(sc + f.width / 4 + 1);
+          h[0] *= g0.x; h[1] *= g0.y; h[2] *= g0.z; h[3] *= g0.w;
+          h[4] *= g1.x; h[5] *= g1.y; h[6] *= g1.z; h[7] *= g1.w;
+          u[0] *= u0.x; u[1] *= u0.y; u[2] *= u0.z; u[3] *= u0.w;
+          u[4] *= u1.x; u[5] *= u1.y; u[6] *= u1.z; u[7] *= u1.w;
+        }
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+          // rolled, so that there is one copy of the activation: the registers rotate
+          const float v = few_act(h[0], u[0], p.act);
+#pragma unroll
+          for (int t = 0; t < 7; ++t) {
+            h[t] = h[t + 1];
+            u[t] = u[t + 1];
+          }
+          h[7] = v;
+        }
+      }
+      const size_t at = static_cast<size_t>(row0 + row) * p.Ip + c0 + col;
+      if constexpr (Tr::F16) {
+        if (in && c0 + col < f.width) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.hp) + at);
+          dst[0] = make_float4(h[0], h[1], h[2], h[3]);
+          dst[1] = make_float4(h[4], h[5], h[6], h[7]);
+        }
+        // the bits of non-negative floats order as the floats do (NaN highest)
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(h[j]) & 0x7fffffffu);
+        if (!in) m = 0;
+#pragma unroll
+        for (int o = 1; o < per; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (in && col == 0) atomicMax(p.hmax + row0 + row, m);
+      } else if (in) {
+        // eight columns are whole pairs of the permuted row
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.hp);
+        const size_t plane = static_cast<size_t>(p.T * p.k + p.T) * p.Ip;
+        if (c0 + col < p.Ip) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            __nv_bfloat162 hi, lo;
+            split_bf16(h[j], hi.x, lo.x);
+            split_bf16(h[j + 1], hi.y, lo.y);
+            const size_t o = at - (c0 + col) + perm_k<KIND, GRP>(c0 + col + j);
+            *reinterpret_cast<__nv_bfloat162*>(dst + o) = hi;
+            *reinterpret_cast<__nv_bfloat162*>(dst + plane + o) = lo;
           }
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    // 4-bit weights: the group scales of the next chunk, one ahead
-    W4Scales<GRP == 0 ? 128 : GRP> sc_now, sc_next;
-    auto scales = [&](auto& dst, int a_, int s_, int kc_) {
-      if constexpr (KIND == kStreamW4) {
-        const void* base = DOWN ? (ROUTED ? p.s2 : p.s2s) : (ROUTED ? p.s13 : p.s13s);
-        const int r = nk_row<KIND, GRP>(g);
-        const int l0 = (DOWN ? s_ * 128 + warp * 16 : s_ * 64 + (warp & 3) * 16) + r;
-        const int half = DOWN ? 0 : warp >> 2;
-        const long long e = ROUTED ? ctl->aexp[a_] : 0;
-        const long long row = (e * (DOWN ? 1 : 2) + half) * width + l0;
-        w4_load_scales<GRP>(dst, static_cast<const __nv_bfloat16*>(base), nullptr,
-                            l0 < width ? row : -1, l0 + 8 < width ? row + 8 : -1, K / GRP,
-                            kc_ * (256 / GRP), lane);
-      }
+    }
+  }
+
+  // fp32 h rows r0 .. r0 + n - 1, as far as the first chunks of the run reach
+  // and one line a thread.
+  static __device__ __forceinline__ void prefetch_h(const FewParams& p, const FewPass& f, int r0, int n) {
+    if (f.lo >= f.hi) return;
+    const int lines = (f.K + 31) / 32, i = threadIdx.x;
+    if (i < n * lines)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const float*>(p.hp) +
+                                                    static_cast<size_t>(r0 + i / lines) * p.Ip + (i % lines) * 32));
+  }
+
+  template <bool DOWN, bool ROUTED>
+  static __device__ __forceinline__ void consume(const FewParams& p, const FewPass& f, Ctrl* ctl, uint32_t ring,
+                                                 float* red, RingPos& ring_pos, int b) {
+    if (f.lo >= f.hi) return;
+    const int tid = threadIdx.x, team = Sm::kTeams == 1 ? 0 : tid / (32 * kStreamWarps);
+    const int warp = (tid >> 5) % kStreamWarps, lane = tid & 31;
+    const int g = lane >> 2, c = lane & 3;
+    constexpr uint32_t kLo = 8 * NT * Tr::PITCH;
+    constexpr int RP = Sm::kRP;
+    FewAt at(f, f.lo);
+    int left = static_cast<int>(f.hi - f.lo);
+    bool begun_earlier = at.kc != 0;  // this CTA's first strip was begun by an earlier one
+
+    // 4-bit weights: the lane's row of group scales
+    [[maybe_unused]] W4Scales<GRP == 0 ? 128 : GRP> sc0, sc1, sc2;
+    [[maybe_unused]] long long srow = 0;
+    auto scales = [&](auto& dst, int kc) {
+      if constexpr (KIND == kStreamW4)
+        w4_load_scales<GRP>(dst, static_cast<const __nv_bfloat16*>(DOWN ? (ROUTED ? p.s2 : p.s2s) : (ROUTED ? p.s13 : p.s13s)),
+                            nullptr, srow, f.K / GRP, kc * (256 / GRP), lane);
     };
 
     float acc[NT][Tr::MT][4];
-    auto zero = [&]() {
+    while (left > 0) {  // a strip, or this CTA's part of it
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < Tr::MT; ++j)
 #pragma unroll
           for (int t = 0; t < 4; ++t) acc[i][j][t] = 0.0f;
-    };
-    zero();
-    ahead(0);
-    ahead(1);
-    scales(sc_next, a, s, kc);
-    int slot = 0, n = 0;
-    for (long long q = f.lo; q < f.hi; ++q) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      bar_consumers();  // this chunk's rows are visible; the previous chunk's buffer is free
-      ahead(slot == 0 ? 2 : slot - 1);
-      n = ROUTED ? ctl->aoff[a + 1] - ctl->aoff[a] : p.T;
+      const int n = ROUTED ? ctl->aoff[at.a + 1] - ctl->aoff[at.a] : p.T;
       const int ntu = (n + 7) >> 3;
-      const bool strip_end = kc + 1 == f.C;
+      const int chunks = min(f.C - at.kc, left), end = at.kc + chunks;
+      const bool strip_end = end == f.C;
+      RingPos pos = ring_pos;
+      if (team) pos.next(Sm::NST);
       if constexpr (KIND == kStreamW4) {
-        sc_now = sc_next;
-        if (q + 1 < f.hi) {
-          if (!strip_end) scales(sc_next, a, s, kc + 1);
-          else if (s + 1 < f.S) scales(sc_next, a, s + 1, 0);
-          else scales(sc_next, a + 1, 0, 0);
-        }
+        const int l = (DOWN ? at.s * 128 + warp * 16 : at.s * 64 + (warp & 3) * 16) + nk_row<KIND, GRP>(g) +
+                      (c & 1) * 8;
+        const int half = DOWN ? 0 : warp >> 2;
+        const long long e = ROUTED ? ctl->aexp[at.a] : 0;
+        srow = l < f.width ? ((e * (DOWN ? 1 : 2) + half) * f.width + l) * (f.K / GRP) : -1;
+        scales(sc0, at.kc + team);
+        scales(sc1, at.kc + team + Sm::kTeams);
       }
-      if (!mbar_wait(&ctl->full[stage], phase, &ctl->abort)) {
-        if (lane == 0 && !*reinterpret_cast<volatile int*>(&ctl->abort)) {
-          *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-          atomicOr(p.err, MOE_DEV_WAIT_TIMEOUT);
-        }
-      }
-      __syncwarp();
-      const uint32_t st = ring + stage * kStageBytes, bb = bbase + slot * Sm::kBBuf;
-      if constexpr (Tr::KN) stage_mma_kn<KIND, NT, DOWN>(st, bb, kLo, warp, lane, ntu, acc);
-      else if constexpr (KIND == kStreamFp8Nk)
-        stage_mma_fp8nk<NT, DOWN>(st, bb, kLo, warp, lane, ntu, acc);
-      else
-        stage_mma_w4<GRP, NT, DOWN, false>(st, bb, kLo, warp, lane, ntu, sc_now,
-                                           min(256, K - kc * 256) / GRP, acc);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->empty[stage]);
-      if (++stage == Sm::NST) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      slot = slot == 2 ? 0 : slot + 1;
-
-      if (strip_end || q + 1 == f.hi) {
-        // the strip's partial sum: row j, columns [0, 2 HC)
-        float* dst;
-        size_t pitch;
-        if (first_is_extra) {
-          dst = p.extra + (static_cast<size_t>(ROUTED ? 1 : 0) * kStreamMaxCtas + b) * p.T * 2 * Tr::HC;
-          pitch = 2 * Tr::HC;
-        } else {
-          const int row0 = ROUTED ? ctl->aoff[a] : p.T * p.k;
-          dst = p.prim + static_cast<size_t>(row0) * p.W + static_cast<size_t>(s) * 2 * Tr::HC;
-          pitch = p.W;
-        }
-        first_is_extra = false;
-        if constexpr (Tr::KN) {
-          // four warps hold partial sums of a half's columns: added in the
-          // order of k, one after another
-          constexpr int RP = 2 * Tr::HC + 4;
-          const int half = warp & 1, kw = warp >> 1;
 #pragma unroll 1
-          for (int r = 0; r < 4; ++r) {
-            if (kw == r) {
+      for (int kc = at.kc + team; kc < end; kc += Sm::kTeams) {
+        if constexpr (KIND == kStreamW4) scales(sc2, kc + 2 * Sm::kTeams);
+        if (!mbar_wait(&ctl->ring.full[pos.at], pos.phase, &ctl->ring.abort)) ctl->ring.give_up(p.err);
+        __syncwarp();
+        const uint32_t st = ring + pos.at * Sm::kSlot, rows = st + kStageBytes;
+        if constexpr (Tr::KN) stage_mma_kn<KIND, NT, DOWN && Sm::kHilo>(st, rows, kLo, warp, lane, ntu, acc);
+        else if constexpr (KIND == kStreamFp8Nk)
+          stage_mma_fp8nk<NT>(st, rows, warp, lane, ntu, acc);
+        else {
+          stage_mma_w4<GRP, NT, false, true>(st, rows, warp, lane, ntu, sc0, min(256, f.K - kc * 256) / GRP, acc);
+          sc0 = sc1;
+          sc1 = sc2;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->ring.empty[pos.at]);
+        pos.skip(Sm::kTeams, Sm::NST);
+      }
+      ring_pos.skip(chunks % Sm::NST, Sm::NST);
+      ring_pos.phase ^= (chunks / Sm::NST) & 1;
+      // a slot is one team's as long as the strips' lengths are even: an odd one
+      // swaps the teams, behind the barriers below
+      left -= chunks;
+      {
+        // the strip's sums over this CTA's chunks of it, in red[row][2 HC]: the
+        // warps that hold sums of the same columns add theirs one after another,
+        // in a fixed order
+        constexpr int KW = (Tr::KN ? 4 : 1) * Sm::kTeams;
+        const int mine = Tr::KN ? team * 4 + (warp >> 1) : team;  // (a team without a chunk adds zeros)
+#pragma unroll 1
+        for (int r = 0; r < KW; ++r) {
+          if (mine == r) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                if (nt < ntu) {
+            for (int nt = 0; nt < NT; ++nt)
+              if (nt < ntu) {
 #pragma unroll
-                  for (int mt = 0; mt < Tr::MT; ++mt) {
-                    float* at = red + (nt * 8 + 2 * c) * RP + half * Tr::HC + kn_col<KIND>(lane, mt);
-                    const float* v = acc[nt][mt];
-                    if (r == 0) {
-                      at[0] = v[0]; at[RP] = v[1]; at[1] = v[2]; at[RP + 1] = v[3];
-                    } else {
-                      at[0] += v[0]; at[RP] += v[1]; at[1] += v[2]; at[RP + 1] += v[3];
-                    }
+                for (int mt = 0; mt < Tr::MT; ++mt) {
+                  // columns of v[0..1] and v[2..3]
+                  const int col = Tr::KN ? (warp & 1) * Tr::HC + kn_col<KIND>(lane, mt)
+                                         : warp * 16 + nk_row<KIND, GRP>(g);
+                  constexpr int step = Tr::KN ? 1 : 8;
+                  float* at_ = red + (nt * 8 + 2 * c) * RP + col;
+                  const float* v = acc[nt][mt];
+                  if (r == 0) {
+                    at_[0] = v[0]; at_[RP] = v[1]; at_[step] = v[2]; at_[RP + step] = v[3];
+                  } else {
+                    at_[0] += v[0]; at_[RP] += v[1]; at_[step] += v[2]; at_[RP + step] += v[3];
                   }
                 }
-            }
-            bar_consumers();
+              }
           }
-          constexpr int Q = 2 * Tr::HC / 4;
-          for (int i = tid; i < n * Q; i += kStreamThreads) {
+          bar();
+        }
+        constexpr int Q = 2 * Tr::HC / 4;
+        auto copy_out = [&](float* dst, size_t pitch) {
+          for (int i = tid; i < n * Q; i += CT) {
             const int row = i / Q, col = (i % Q) * 4;
             *reinterpret_cast<float4*>(dst + row * pitch + col) =
                 *reinterpret_cast<const float4*>(red + row * RP + col);
           }
-          bar_consumers();  // before the next strip's sums overwrite red
+        };
+        if (DOWN) {
+          if (begun_earlier)
+            copy_out(p.extra + (static_cast<size_t>(ROUTED ? 1 : 0) * kStreamMaxCtas + b) * p.T * 2 * Tr::HC,
+                     2 * Tr::HC);
+          else
+            copy_out(p.prim + static_cast<size_t>(ROUTED ? ctl->aoff[at.a] : p.T * p.k) * p.W +
+                         static_cast<size_t>(at.s) * 2 * Tr::HC,
+                     p.W);
+        } else if (strip_end && !begun_earlier) {  // the whole strip is this CTA's
+          finish_h<ROUTED>(p, f, ctl, at.a, at.s, n, tid, [&](int row, int col, float (&v)[8]) {
+            const float4 x = *reinterpret_cast<const float4*>(red + row * RP + col);
+            const float4 y = *reinterpret_cast<const float4*>(red + row * RP + col + 4);
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+            v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+          });
         } else {
-          const int col = warp * 16 + nk_row<KIND, GRP>(g);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int r0 = nt * 8 + 2 * c;
-            if (r0 < n) {
-              dst[r0 * pitch + col] = acc[nt][0][0];
-              dst[r0 * pitch + col + 8] = acc[nt][0][2];
-            }
-            if (r0 + 1 < n) {
-              dst[(r0 + 1) * pitch + col] = acc[nt][0][1];
-              dst[(r0 + 1) * pitch + col + 8] = acc[nt][0][3];
-            }
+          copy_out(part_at(p, ROUTED, b, begun_earlier ? 0 : 1), 2 * Tr::HC);
+          __threadfence();
+          bar();
+          const long long q0 = f.hi - left - end;  // the strip's first chunk
+          const int c0 = split_cta(f.sp, q0), c1 = split_cta(f.sp, q0 + f.C - 1);
+          int32_t* cnt = p.cnt + (ROUTED ? kStreamMaxCtas : 0) + c0;
+          if (tid == 0) {
+            ctl->ring.last = atomicAdd(cnt, 1) == c1 - c0;
           }
-        }
-        zero();
-      }
-      if (strip_end) {
-        kc = 0;
-        if (++s == f.S) {
-          s = 0;
-          ++a;
-        }
-      } else {
-        ++kc;
-      }
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    bar_consumers();
-  }
-
-  // Eight consecutive columns of one row of a strip, summed over the CTAs that
-  // computed parts of it.  `at`: row r of prim, slot = the row's index inside
-  // its expert, gs = the strip's index in the pass, col inside the strip.
-  static __device__ __forceinline__ void gather8(const FewParams& p, const FewPass& f, bool routed,
-                                                 int r, int slot, long long gs, int s, int col,
-                                                 float (&v)[8]) {
-    const float4* a = reinterpret_cast<const float4*>(p.prim + static_cast<size_t>(r) * p.W +
-                                                      static_cast<size_t>(s) * 2 * Tr::HC + col);
-    const float4 x = __ldcg(a), y = __ldcg(a + 1);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    const int c0 = split_cta(f.sp, gs * f.C), c1 = split_cta(f.sp, gs * f.C + f.C - 1);
-    for (int cta = c0 + 1; cta <= c1; ++cta) {
-      const float4* e = reinterpret_cast<const float4*>(
-          p.extra + ((static_cast<size_t>(routed ? 1 : 0) * kStreamMaxCtas + cta) * p.T + slot) * 2 * Tr::HC +
-          col);
-      const float4 m = __ldcg(e), n = __ldcg(e + 1);
-      v[0] += m.x; v[1] += m.y; v[2] += m.z; v[3] += m.w;
-      v[4] += n.x; v[5] += n.y; v[6] += n.z; v[7] += n.w;
-    }
-  }
-};
-
-template <int KIND, int GRP, int NT>
-__global__ void __launch_bounds__(kStreamBlock, 1)
-    few_layer_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant__ CUtensorMap m2,
-                     const __grid_constant__ CUtensorMap m13s, const __grid_constant__ CUtensorMap m2s,
-                     const __grid_constant__ FewParams p) {
-  using F = Few<KIND, GRP, NT>;
-  using Tr = StreamTraits<KIND, GRP>;
-  using Sm = FewSmem<KIND, GRP, NT>;
-  using Ctrl = typename Sm::Ctrl;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  uint8_t* ring_ptr = smem_raw + pad;
-  uint8_t* bptr = ring_ptr + Sm::NST * kStageBytes;
-  float* red = reinterpret_cast<float*>(bptr + 3 * Sm::kBBuf);
-  Ctrl* ctl = reinterpret_cast<Ctrl*>(bptr + 3 * Sm::kBBuf + Sm::kRedBytes);
-  const uint32_t ring = smem_u32(ring_ptr);
-  const int tid = threadIdx.x, b = blockIdx.x, G = gridDim.x;
-  const int R = p.T * p.k;
-  const bool shared = p.Is > 0;
-
-  if (tid == 0) {
-    for (int i = 0; i < Sm::NST; ++i) {
-      mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], kStreamWarps);
-    }
-    ctl->abort = 0;
-    fence_mbarrier_init();
-  }
-  __syncthreads();
-
-  if (tid >= kStreamThreads) {  // ------------------------------------ producer
-    const int lane = tid & 31;
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    const uint64_t policy = l2_policy_evict_first();
-    if (lane == 0 && shared) {
-      const FewPass f = few_pass<KIND, GRP>(p, false, false, 0, G, b);
-      ok = F::produce(&m13s, f, false, nullptr, ring, ctl, ring_ptr, stage, phase, policy);
-    }
-    __syncwarp();
-    asm volatile("bar.sync 2, %0;" ::"n"(kStreamBlock) : "memory");  // the expert lists are built
-    if (lane == 0) {
-      const int na = ctl->na;
-      if (ok) ok = F::produce(&m13, few_pass<KIND, GRP>(p, false, true, na, G, b), false, ctl->aexp, ring,
-                              ctl, ring_ptr, stage, phase, policy);
-      if (ok && shared)
-        ok = F::produce(&m2s, few_pass<KIND, GRP>(p, true, false, na, G, b), true, nullptr, ring, ctl,
-                        ring_ptr, stage, phase, policy);
-      if (ok) ok = F::produce(&m2, few_pass<KIND, GRP>(p, true, true, na, G, b), true, ctl->aexp, ring, ctl,
-                              ring_ptr, stage, phase, policy);
-      if (!ok || *reinterpret_cast<volatile int*>(&ctl->abort)) {
-        // gave up: copies still in flight have to land before the CTA exits
-        if (!*reinterpret_cast<volatile int*>(&ctl->abort)) {
-          *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-          atomicOr(p.err, MOE_DEV_WAIT_TIMEOUT);
-        }
-        for (int i = 0; i < Sm::NST; ++i) {
-          stage = stage == 0 ? Sm::NST - 1 : stage - 1;
-          if (stage == Sm::NST - 1) phase ^= 1u;
-          mbar_wait_drain(&ctl->full[stage], phase);
-        }
-        drain_grace();
-      }
-    }
-    return;
-  }
-
-  // ------------------------------------------------------------------ consumers
-  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int gtid = b * kStreamThreads + tid, gthreads = G * kStreamThreads;
-
-  // phase 0: router planes.  A unit is 64 experts x one slice of D; its k16
-  // steps go round the CTA's warps.
-  {
-    const int SE = (p.E + 63) / 64, steps = (p.D + 15) / 16;
-    const bool vec = (p.E & 7) == 0;
-    for (int u = b; u < SE * p.nplanes; u += G) {
-      const int se = u % SE, pl = u / SE;
-      const int s0 = static_cast<int>(static_cast<long long>(steps) * pl / p.nplanes);
-      const int s1 = static_cast<int>(static_cast<long long>(steps) * (pl + 1) / p.nplanes);
-      float acc[NT][4][4];
+          bar();
+          if (ctl->ring.last) {
+            __threadfence();
+            finish_h<ROUTED>(p, f, ctl, at.a, at.s, n, tid, [&](int row, int col, float (&v)[8]) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[i][j][t] = 0.0f;
-      const int col = se * 64 + g * 8;
-      for (int st = s0 + warp; st < s1; st += kStreamWarps) {
-        uint32_t w[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = st * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
-          w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
-          if (k < p.D) {
-            const __nv_bfloat16* src = p.Wg + static_cast<size_t>(k) * p.E + col;
-            if (vec) {
-              if (col < p.E) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+              for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+              for (int cta = c0; cta <= c1; ++cta) {
+                const float4* m = reinterpret_cast<const float4*>(
+                    part_at(p, ROUTED, cta, cta == c0 ? 1 : 0) + row * 2 * Tr::HC + col);
+                const float4 x = __ldcg(m), y = __ldcg(m + 1);
+                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
               }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (col + j < p.E)
-                  w[i][j >> 1] |= static_cast<uint32_t>(
-                                      __ldg(reinterpret_cast<const unsigned short*>(src) + j))
-                                  << (16 * (j & 1));
-            }
+            });
           }
         }
-        uint32_t x0[NT], x1[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int t = nt * 8 + g, k = st * 16 + 2 * c;
-          x0[nt] = x1[nt] = 0u;
-          if (t < p.T) {
-            const __nv_bfloat16* src = p.x + static_cast<size_t>(t) * p.D + k;
-            if (k < p.D) x0[nt] = __ldg(reinterpret_cast<const uint32_t*>(src));
-            if (k + 8 < p.D) x1[nt] = __ldg(reinterpret_cast<const uint32_t*>(src + 8));
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          const uint32_t a0 = __byte_perm(w[0][mt], w[1][mt], 0x5410);
-          const uint32_t a1 = __byte_perm(w[0][mt], w[1][mt], 0x7632);
-          const uint32_t a2 = __byte_perm(w[2][mt], w[3][mt], 0x5410);
-          const uint32_t a3 = __byte_perm(w[2][mt], w[3][mt], 0x7632);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_bf16(acc[nt][mt], a0, a1, a2, a3, x0[nt], x1[nt]);
-        }
+        bar();  // before the next strip's sums overwrite red
+        begun_earlier = false;
       }
+      at.kc = f.C - 1;
+      at.next(f);
+    }
+  }
+
+  // Top-k softmax of tokens t0, t0 + step, ...: the planes summed by all consumers,
+  // as many tokens at a time as red holds, then a warp for each token.
+  static __device__ __forceinline__ void topk(const FewParams& p, int t0, int step, bool keep_logits,
+                                              int32_t* ids, float* w, float* red) {
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int batch = min(Sm::kRedBytes / 4 / p.E, CT / 32);
+    const size_t plane = static_cast<size_t>(p.T) * p.E;
 #pragma unroll 1
-      for (int r = 0; r < kStreamWarps; ++r) {
-        if (warp == r) {
+    for (; t0 < p.T; t0 += batch * step) {
+      const int here = min(batch, (p.T - t0 + step - 1) / step);
+#pragma unroll 1
+      for (int i = tid; i < here * p.E; i += CT) {
+        const int t = i / p.E, e = i - t * p.E;
+        const float* src = p.planes + static_cast<size_t>(t0 + t * step) * p.E + e;
+        float v[kFewMaxPlanes];  // all in flight
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int pl = 0; pl < kFewMaxPlanes; ++pl) v[pl] = pl < p.nplanes ? __ldcg(src + pl * plane) : 0.0f;
+        float sum = v[0];
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-              float* at = red + (nt * 8 + 2 * c) * 68 + g * 8 + 2 * mt;
-              const float* v = acc[nt][mt];
-              if (r == 0) {
-                at[0] = v[0]; at[68] = v[1]; at[1] = v[2]; at[69] = v[3];
-              } else {
-                at[0] += v[0]; at[68] += v[1]; at[1] += v[2]; at[69] += v[3];
-              }
-            }
-        }
-        bar_consumers();
+        for (int pl = 1; pl < kFewMaxPlanes; ++pl) sum += v[pl];
+        red[i] = sum;
       }
-      for (int i = tid; i < p.T * 64; i += kStreamThreads) {
-        const int t = i >> 6, e = se * 64 + (i & 63);
-        if (e < p.E) p.planes[(static_cast<size_t>(pl) * p.T + t) * p.E + e] = red[t * 68 + (i & 63)];
+      bar();
+      if (wid < here) {
+        const int t = t0 + wid * step;
+        const float* row = red + wid * p.E;
+        float* keep = keep_logits ? p.logits + static_cast<size_t>(t) * p.E : nullptr;
+        if (p.E <= 128) topk_row<4>(p, row, lane, keep, ids + t * p.k, w + t * p.k);
+        else if (p.E <= 256) topk_row<8>(p, row, lane, keep, ids + t * p.k, w + t * p.k);
+        else topk_row<16>(p, row, lane, keep, ids + t * p.k, w + t * p.k);
       }
-      bar_consumers();
+      bar();
     }
-    // x in the layout's k order, rows padded with zeros
-    for (int i = gtid; i < p.T * (p.Dp / 8); i += gthreads) {
-      const int t = i / (p.Dp / 8), k0 = (i % (p.Dp / 8)) * 8;
-      union {
-        uint4 v;
-        unsigned short h[8];
-      } in;
-      in.v = make_uint4(0, 0, 0, 0);
-      if (k0 < p.D) in.v = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.D + k0));
-      unsigned short* dst = reinterpret_cast<unsigned short*>(p.xp) + static_cast<size_t>(t) * p.Dp;
+  }
+  template <int EPL>
+  static __device__ __forceinline__ void topk_row(const FewParams& p, const float* row, int lane, float* keep,
+                                                  int32_t* ids, float* w) {
+    float v[EPL];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dst[perm_k<KIND, GRP>(k0 + j)] = in.h[j];
-    }
+    for (int i = 0; i < EPL; ++i) v[i] = lane + 32 * i < p.E ? row[lane + 32 * i] : 0.0f;
+    warp_topk_softmax<EPL>(v, lane, p.E, p.k, p.renorm, p.bias, keep, ids, w, p.err);
   }
-  few_grid_sync(p.bar, G, &ctl->abort, p.err);
 
-  // phase 1: top-k of one token per CTA
-  for (int t = b; t < p.T; t += G) {
-    float* sum = reinterpret_cast<float*>(ctl->cnt);
-    for (int e = tid; e < p.E; e += kStreamThreads) {
-      float v = 0.0f;
-      for (int pl = 0; pl < p.nplanes; ++pl)
-        v += __ldcg(p.planes + (static_cast<size_t>(pl) * p.T + t) * p.E + e);
-      sum[e] = v;
+  // The chosen experts in ascending order and their rows in ascending order, by
+  // one warp; ctl->cnt is zero on entry.
+  static __device__ __forceinline__ void build_lists(const FewParams& p, Ctrl* ctl, int lane) {
+    const int R = p.T * p.k;
+    // a row's rank among the rows of its expert, 32 rows at a time
+#pragma unroll 1
+    for (int r0 = 0; r0 < R; r0 += 32) {
+      const int r = r0 + lane, e = r < R ? ctl->ids[r] : -1 - lane;
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const int before = r < R ? ctl->cnt[e] : 0;
+      __syncwarp();
+      if (r < R) {
+        ctl->pos[r] = static_cast<uint16_t>(before + __popc(same & ((1u << lane) - 1u)));
+        if ((same >> lane) == 1u) ctl->cnt[e] = before + __popc(same);  // the last of them
+      }
+      __syncwarp();
     }
-    bar_consumers();
-    if (warp == 0) {
-      float v[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = lane + 32 * i < p.E ? sum[lane + 32 * i] : 0.0f;
-      warp_topk_softmax<16>(v, lane, p.E, p.k, p.renorm, p.bias, p.logits + static_cast<size_t>(t) * p.E,
-                            p.ids + t * p.k, p.topw + t * p.k, p.err);
-    }
-    bar_consumers();
-  }
-  few_grid_sync(p.bar, G, &ctl->abort, p.err);
-
-  // phase 2: the chosen experts and their rows
-  for (int e = tid; e < p.E; e += kStreamThreads) ctl->cnt[e] = 0;
-  for (int r = tid; r < R; r += kStreamThreads) {
-    int e = __ldcg(p.ids + r);
-    if (static_cast<unsigned>(e) >= static_cast<unsigned>(p.E)) {  // only after a wait that gave up
-      e = 0;
-      atomicOr(p.err, MOE_DEV_BAD_EXPERT_ID);
-    }
-    ctl->sid[r] = static_cast<uint16_t>(e);
-  }
-  bar_consumers();
-  for (int r = tid; r < R; r += kStreamThreads) atomicAdd(&ctl->cnt[ctl->sid[r]], 1);
-  bar_consumers();
-  if (warp == 0) {
-    // 16 consecutive experts per lane
+    const int per = (p.E + 31) / 32;  // consecutive experts of a lane
     int rows = 0, act = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int e = lane * 16 + i;
-      if (e < p.E && ctl->cnt[e] > 0) {
-        rows += ctl->cnt[e];
-        ++act;
-      }
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const int e = lane * per + i, n = e < p.E ? ctl->cnt[e] : 0;
+      rows += n;
+      act += n > 0;
     }
     int ir = rows, ia = act;
 #pragma unroll
@@ -631,135 +645,352 @@ __global__ void __launch_bounds__(kStreamBlock, 1)
       ctl->aoff[ia] = static_cast<uint16_t>(ir);
     }
     int ro = ir - rows, ao = ia - act;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int e = lane * 16 + i;
-      if (e < p.E && ctl->cnt[e] > 0) {
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const int e = lane * per + i, n = e < p.E ? ctl->cnt[e] : 0;
+      if (n > 0) {
         ctl->aexp[ao] = static_cast<uint16_t>(e);
         ctl->aoff[ao] = static_cast<uint16_t>(ro);
         ctl->amap[e] = static_cast<uint16_t>(ao);
-        ro += ctl->cnt[e];
+        ro += n;
         ++ao;
       }
     }
+    __syncwarp();
+#pragma unroll 1
+    for (int r = lane; r < R; r += 32) {
+      const int at = ctl->aoff[ctl->amap[ctl->ids[r]]] + ctl->pos[r];
+      ctl->srow[at] = static_cast<uint16_t>(r / p.k);
+      ctl->pos[r] = static_cast<uint16_t>(at);
+    }
   }
-  bar_consumers();
-  for (int r = tid; r < R; r += kStreamThreads) {
-    const int e = ctl->sid[r];
-    int rank = 0;
-    for (int q = 0; q < r; ++q) rank += ctl->sid[q] == e;
-    const int a = ctl->amap[e], at = ctl->aoff[a] + rank;
-    ctl->srow[at] = static_cast<uint16_t>(r);
-    ctl->apos[at] = static_cast<uint16_t>(a);
-    ctl->pos[r] = static_cast<uint16_t>(at);
-  }
-  __threadfence_block();
-  asm volatile("bar.arrive 2, %0;" ::"n"(kStreamBlock) : "memory");
-  bar_consumers();
-  const int na = ctl->na;
 
-  int stage = 0;
-  uint32_t phase = 0;
-  const uint32_t bbase = smem_u32(bptr);
-  const FewPass us = few_pass<KIND, GRP>(p, false, false, na, G, b);
-  const FewPass ur = few_pass<KIND, GRP>(p, false, true, na, G, b);
-  if (shared) F::template consume<false, false>(p, us, ctl, ring, bbase, red, stage, phase, b, G);
-  F::template consume<false, true>(p, ur, ctl, ring, bbase, red, stage, phase, b, G);
-  few_grid_sync(p.bar, G, &ctl->abort, p.err);
-
-  // phase 3: h = act(gate) * up, as a bf16 pair in the k order of the down pass
-  {
-    const int per = p.Ip / 8;
-    const int rows = R + (shared ? p.T : 0);
-    const size_t plane = static_cast<size_t>(R + p.T) * p.Ip;
-    for (int i = gtid; i < rows * per; i += gthreads) {
-      const int r = i / per, k0 = (i % per) * 8;
-      const bool rt = r < R;
-      const int width = rt ? p.I : p.Is;
-      float h[8];
+  // The router's planes.  A unit is 64 experts x one slice of D; its k16 steps
+  // go round the CTA's warps, two at a time.
+  static __device__ __forceinline__ void router(const FewParams& p, float* red, int b, int G) {
+    constexpr int NW = CT / 32, PL = Sm::kPlanes, PW = 8 * NT * 68;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int SE = (p.E + 63) / 64, steps = (p.D + 15) / 16;
+    const bool vec = (p.E & 7) == 0;
+#pragma unroll 1
+    for (int u = b; u < SE * p.nplanes; u += G) {
+      const int se = u % SE, pl = u / SE;
+      const int s0 = steps * pl / p.nplanes, s1 = steps * (pl + 1) / p.nplanes;
+      float acc[NT][4][4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = 0.0f;
-      if (k0 < width) {
-        const FewPass& f = rt ? ur : us;
-        const int a = rt ? ctl->apos[r] : 0;
-        const int sl = rt ? r - ctl->aoff[a] : r - R;
-        const int s = k0 / Tr::HC, col = k0 % Tr::HC;
-        const long long gs = static_cast<long long>(a) * f.S + s;
-        float u[8];
-        F::gather8(p, f, rt, r, sl, gs, s, col, h);
-        F::gather8(p, f, rt, r, sl, gs, s, col + Tr::HC, u);
-        if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
-          const float* sc = static_cast<const float*>(rt ? p.s13 : p.s13s) +
-                            (rt ? static_cast<size_t>(ctl->aexp[a]) * 2 * width : 0);
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            h[j] *= __ldg(sc + k0 + j);
-            u[j] *= __ldg(sc + width + k0 + j);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[i][j][t] = 0.0f;
+      const int col = se * 64 + g * 8;
+#pragma unroll 1
+      for (int st = s0 + wid; st < s1; st += 2 * NW) {
+        uint32_t w[2][4][4], x[2][NT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k0 = st + h * NW < s1 ? (st + h * NW) * 16 : p.D;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = k0 + 2 * c + (i & 1) + (i >> 1) * 8;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[h][i][j] = 0u;
+            if (k < p.D) {
+              const __nv_bfloat16* src = p.Wg + static_cast<size_t>(k) * p.E + col;
+              if (vec) {
+                if (col < p.E) {
+                  const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+                  w[h][i][0] = v.x; w[h][i][1] = v.y; w[h][i][2] = v.z; w[h][i][3] = v.w;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (col + j < p.E)
+                    w[h][i][j >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(src) + j))
+                                       << (16 * (j & 1));
+              }
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int t = nt * 8 + g, k = k0 + 2 * c;
+            x[h][nt][0] = x[h][nt][1] = 0u;
+            if (t < p.T) {
+              const __nv_bfloat16* src = p.x + static_cast<size_t>(t) * p.D + k;
+              if (k < p.D) x[h][nt][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+              if (k + 8 < p.D) x[h][nt][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 8));
+            }
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = few_act(h[j], u[j], p.act);
-      }
-      __nv_bfloat16* dst = p.hp + static_cast<size_t>(r) * p.Ip;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        __nv_bfloat16 hi, lo;
-        split_bf16(h[j], hi, lo);
-        const int at = perm_k<KIND, GRP>(k0 + j);
-        dst[at] = hi;
-        dst[plane + at] = lo;
+          for (int mt = 0; mt < 4; ++mt) {
+            const uint32_t a0 = __byte_perm(w[h][0][mt], w[h][1][mt], 0x5410);
+            const uint32_t a1 = __byte_perm(w[h][0][mt], w[h][1][mt], 0x7632);
+            const uint32_t a2 = __byte_perm(w[h][2][mt], w[h][3][mt], 0x5410);
+            const uint32_t a3 = __byte_perm(w[h][2][mt], w[h][3][mt], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816<false>(acc[nt][mt], a0, a1, a2, a3, x[h][nt][0], x[h][nt][1]);
+          }
+      }
+      // warp w adds to plane w % PL in round w / PL
+#pragma unroll 1
+      for (int r = 0; r < NW / PL; ++r) {
+        if (wid / PL == r) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              float* at = red + (wid % PL) * PW + (nt * 8 + 2 * c) * 68 + g * 8 + 2 * mt;
+              const float* v = acc[nt][mt];
+              if (r == 0) {
+                at[0] = v[0]; at[68] = v[1]; at[1] = v[2]; at[69] = v[3];
+              } else {
+                at[0] += v[0]; at[68] += v[1]; at[1] += v[2]; at[69] += v[3];
+              }
+            }
+        }
+        bar();
+      }
+#pragma unroll 1
+      for (int i = tid; i < p.T * 64; i += CT) {
+        const int t = i >> 6, e = se * 64 + (i & 63);
+        float v = red[t * 68 + (i & 63)];
+#pragma unroll
+        for (int q = 1; q < PL; ++q) v += red[q * PW + t * 68 + (i & 63)];
+        if (e < p.E) p.planes[(static_cast<size_t>(pl) * p.T + t) * p.E + e] = v;
+      }
+      bar();
+    }
+  }
+
+  // Token rows in the layout's k order, padded with zeros, a CTA for each (the
+  // highest first: they have no router unit); fp16 rows by their power of two.
+  static __device__ __forceinline__ void stage_x(const FewParams& p, float* red, int b, int G) {
+    const int tid = threadIdx.x;
+#pragma unroll 1
+    for (int t = G - 1 - b; t < p.T; t += G) {
+      const __nv_bfloat16* src = p.x + static_cast<size_t>(t) * p.D;
+      uint16_t* dst = p.xp + static_cast<size_t>(t) * p.Dp;
+      float sc = 1.0f;
+      if constexpr (Tr::F16) {
+        uint32_t m = 0;  // bf16 bits order as 16-bit whole numbers
+        for (int k0 = tid * 8; k0 < p.D; k0 += CT * 8) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + k0));
+          m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                   __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
+        m = max(m & 0xffffu, m >> 16) << 16;
+        m = __reduce_max_sync(0xffffffffu, m);
+        uint32_t* all = reinterpret_cast<uint32_t*>(red);
+        if ((tid & 31) == 0) all[tid >> 5] = m;
+        bar();
+        m = __reduce_max_sync(0xffffffffu, (tid & 31) < CT / 32 ? all[tid & 31] : 0u);
+        bar();
+        const int e = row_exp(m);
+        sc = exp2_int(e);
+        if (tid == 0) p.xinv[t] = exp2_int(-e);
+      }
+#pragma unroll 1
+      for (int k0 = tid * 8; k0 < p.Dp; k0 += CT * 8) {
+        union {
+          uint4 v;
+          __nv_bfloat16 h[8];
+        } in;
+        in.v = make_uint4(0, 0, 0, 0);
+        if (k0 < p.D) in.v = __ldg(reinterpret_cast<const uint4*>(src + k0));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint16_t o;
+          if constexpr (Tr::F16) o = __half_as_ushort(__float2half_rn(__bfloat162float(in.h[j]) * sc));
+          else o = __bfloat16_as_ushort(in.h[j]);
+          dst[perm_k<KIND, GRP>(k0 + j)] = o;
+        }
       }
     }
   }
-  few_grid_sync(p.bar, G, &ctl->abort, p.err);
+};
 
-  // phase 4: down products
+template <int KIND, int GRP, int NT>
+__global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
+    few_layer_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant__ CUtensorMap m2,
+                     const __grid_constant__ CUtensorMap m13s, const __grid_constant__ CUtensorMap m2s,
+                     const __grid_constant__ FewParams p) {
+  using F = Few<KIND, GRP, NT>;
+  using Tr = StreamTraits<KIND, GRP>;
+  using Sm = FewSmem<KIND, GRP, NT>;
+  using Ctrl = typename Sm::Ctrl;
+  constexpr int CT = Sm::kCons;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* red = reinterpret_cast<float*>(ring + Sm::NST * Sm::kSlot);
+  Ctrl* ctl = reinterpret_cast<Ctrl*>(ring + Sm::NST * Sm::kSlot + Sm::kRedBytes);
+  StreamRing* sr = &ctl->ring;
+  const int tid = threadIdx.x, b = blockIdx.x, G = gridDim.x, lane = tid & 31;
+  const int R = p.T * p.k;
+  const bool shared = p.Is > 0;
+
+  if (tid == 0) sr->init();
+  __syncthreads();
+
+  if (tid >= CT + 32) {  // -------------------------------------------- feeders
+    RingPos pos;
+    int turn = (tid - CT - 32) >> 5;
+    asm volatile("bar.sync 4, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");  // x rows and expert lists are there
+    const int na = ctl->na;
+    bool ok = true;
+    if (shared)
+      ok = F::template feed<false, false>(p, few_pass<KIND, GRP>(p, false, false, na, G, b), ctl, ring, pos, turn, lane);
+    if (ok)
+      ok = F::template feed<false, true>(p, few_pass<KIND, GRP>(p, false, true, na, G, b), ctl, ring, pos, turn, lane);
+    asm volatile("bar.sync 3, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");  // h rows are there
+    if (ok && shared)
+      ok = F::template feed<true, false>(p, few_pass<KIND, GRP>(p, true, false, na, G, b), ctl, ring, pos, turn, lane);
+    if (ok)
+      ok = F::template feed<true, true>(p, few_pass<KIND, GRP>(p, true, true, na, G, b), ctl, ring, pos, turn, lane);
+    if (!ok) sr->give_up(p.err);
+    cp_async_wait_all();
+    return;
+  }
+  if (tid >= CT) {  // ------------------------------------------------ producer
+    RingPos pos;
+    bool ok = true;
+    const uint64_t policy = l2_policy_evict_first();
+    if (lane == 0 && shared)
+      ok = F::produce(&m13s, few_pass<KIND, GRP>(p, false, false, 0, G, b), false, nullptr, sr, ring, pos, policy);
+    __syncwarp();
+    asm volatile("bar.sync 2, %0;" ::"n"(CT + 32) : "memory");  // the expert lists are built
+    if (lane == 0) {
+      const int na = ctl->na;
+      if (ok)
+        ok = F::produce(&m13, few_pass<KIND, GRP>(p, false, true, na, G, b), false, ctl->aexp, sr, ring, pos, policy);
+      if (ok && shared)
+        ok = F::produce(&m2s, few_pass<KIND, GRP>(p, true, false, na, G, b), true, nullptr, sr, ring, pos, policy);
+      if (ok) ok = F::produce(&m2, few_pass<KIND, GRP>(p, true, true, na, G, b), true, ctl->aexp, sr, ring, pos, policy);
+      if (!ok) sr->give_up(p.err);
+      if (sr->aborted()) drain_ring(sr, pos, Sm::NST);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  if (tid < 2) p.cnt[tid * kStreamMaxCtas + b] = 0;
+  if (Tr::F16)
+    for (int r = b * CT + tid; r < R + p.T; r += G * CT) p.hmax[r] = 0;
+  // phase 0
+  F::router(p, red, b, G);
+  F::stage_x(p, red, b, G);
+  F::grid_sync(p, sr, 0, 3);
+
+  // phase 1
+  for (int e = tid; e < p.E; e += CT) ctl->cnt[e] = 0;
+  if (p.nplanes * p.T * p.E * 4 <= kFewPlaneBytes) {
+    F::topk(p, 0, 1, b == 0, ctl->ids, ctl->w, red);
+    if (b == 0)
+      for (int r = tid; r < R; r += CT) {
+        p.ids[r] = ctl->ids[r];
+        p.topw[r] = ctl->w[r];
+      }
+  } else {
+    F::topk(p, b, G, true, p.ids, p.topw, red);
+    F::grid_sync(p, sr, 1, -1);
+    for (int r = tid; r < R; r += CT) {
+      const int e = __ldcg(p.ids + r);
+      const bool bad = static_cast<unsigned>(e) >= static_cast<unsigned>(p.E);  // only after a wait that gave up
+      ctl->ids[r] = bad ? 0 : e;
+      ctl->w[r] = __ldcg(p.topw + r);
+    }
+    F::bar();
+  }
+  if (tid < 32) F::build_lists(p, ctl, lane);
+  F::bar();
+  // each role has a barrier of its own: the producer may still be waiting for
+  // stages of the shared expert that the consumers free once the feeders run
+  asm volatile("bar.arrive 4, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");
+  asm volatile("bar.arrive 2, %0;" ::"n"(CT + 32) : "memory");
+  const int na = ctl->na;
+
+  RingPos pos;
+  const uint32_t ring_a = smem_u32(ring);
+  // phase 2: gate/up
+  if (shared)
+    F::template consume<false, false>(p, few_pass<KIND, GRP>(p, false, false, na, G, b), ctl, ring_a, red, pos, b);
+  F::template consume<false, true>(p, few_pass<KIND, GRP>(p, false, true, na, G, b), ctl, ring_a, red, pos, b);
+  F::grid_sync(p, sr, 2, 0);
+  asm volatile("bar.arrive 3, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");
+
+  // phase 3: down
   const FewPass ds = few_pass<KIND, GRP>(p, true, false, na, G, b);
   const FewPass dr = few_pass<KIND, GRP>(p, true, true, na, G, b);
-  if (shared) F::template consume<true, false>(p, ds, ctl, ring, bbase, red, stage, phase, b, G);
-  F::template consume<true, true>(p, dr, ctl, ring, bbase, red, stage, phase, b, G);
-  few_grid_sync(p.bar, G, &ctl->abort, p.err);
-
-  // phase 5: the weighted sum of a token's rows, j ascending, the shared row last
-  {
-    const int per = p.D / 8;
-    for (int i = gtid; i < p.T * per; i += gthreads) {
-      const int t = i / per, d0 = (i % per) * 8;
-      const int s = d0 / (2 * Tr::HC), col = d0 % (2 * Tr::HC);
-      float o[8], y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-      for (int j = 0; j < p.k; ++j) {
-        const int r = ctl->pos[t * p.k + j], a = ctl->apos[r];
-        F::gather8(p, dr, true, r, r - ctl->aoff[a], static_cast<long long>(a) * dr.S + s, s, col, y);
-        if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
-          const float* sc = static_cast<const float*>(p.s2) + static_cast<size_t>(ctl->aexp[a]) * p.D + d0;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] *= __ldg(sc + q);
-        }
-        const float w = __ldcg(p.topw + t * p.k + j);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) o[q] = fmaf(w, y[q], o[q]);
-      }
-      if (shared) {
-        F::gather8(p, ds, false, R + t, t, s, s, col, y);
-        if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
-          const float* sc = static_cast<const float*>(p.s2s) + d0;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] *= __ldg(sc + q);
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) o[q] += y[q];
-      }
-      union {
-        uint4 v;
-        __nv_bfloat16 h[8];
-      } w;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) w.h[q] = __float2bfloat16_rn(o[q]);
-      *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(t) * p.D + d0) = w.v;
+  if (Tr::F16) {
+    // the h rows of the run's first strips into L1 at once: the feeders, which
+    // load and convert them stage by stage, would wait for L2 at every stage
+    if (shared) F::prefetch_h(p, ds, R, p.T);
+    if (dr.lo < dr.hi) {
+      const int a = FewAt(dr, dr.lo).a;
+      F::prefetch_h(p, dr, ctl->aoff[a], ctl->aoff[a + 1] - ctl->aoff[a]);
     }
   }
+  if (shared) F::template consume<true, false>(p, ds, ctl, ring_a, red, pos, b);
+  F::template consume<true, true>(p, dr, ctl, ring_a, red, pos, b);
+  F::grid_sync(p, sr, 3, 2);
+
+  // phase 4: the weighted sum of a token's rows.  Four columns a group of eight
+  // lanes; lane l takes experts l, l + 8 and the shared expert as number k, and
+  // the lanes' sums are added in a fixed tree.
+  {
+    const int per = p.D / 4, l = lane & 7, items = p.T * per;
+    const int terms = p.k + (shared ? 1 : 0);
+    for (int i0 = (b * CT + tid) >> 3; i0 - (lane >> 3) < items; i0 += (G * CT) >> 3) {
+      const bool in = i0 < items;
+      const int i = in ? i0 : items - 1;
+      const int t = i / per, d0 = (i - t * per) * 4;
+      const int s = d0 / (2 * Tr::HC), col = d0 % (2 * Tr::HC);
+      float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = l; j < terms; j += 8) {
+        const bool rt = j < p.k;
+        const FewPass& f = rt ? dr : ds;
+        const int e = rt ? ctl->ids[t * p.k + j] : 0, a = rt ? ctl->amap[e] : 0;
+        const int r = rt ? ctl->pos[t * p.k + j] : R + t, sl = rt ? r - ctl->aoff[a] : t;
+        float w = rt ? ctl->w[t * p.k + j] : 1.0f;
+        if constexpr (Tr::F16) w *= F::exp2_int(-F::row_exp(__ldcg(p.hmax + r)));
+        const long long q0 = (static_cast<long long>(a) * f.S + s) * f.C;
+        float4 y = __ldcg(reinterpret_cast<const float4*>(p.prim + static_cast<size_t>(r) * p.W +
+                                                          static_cast<size_t>(s) * 2 * Tr::HC + col));
+        const int c0 = split_cta(f.sp, q0), c1 = split_cta(f.sp, q0 + f.C - 1);
+        for (int cta = c0 + 1; cta <= c1; ++cta) {
+          const float4 m = __ldcg(reinterpret_cast<const float4*>(
+              p.extra + ((static_cast<size_t>(rt ? 1 : 0) * kStreamMaxCtas + cta) * p.T + sl) * 2 * Tr::HC + col));
+          y.x += m.x; y.y += m.y; y.z += m.z; y.w += m.w;
+        }
+        if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
+          const float4 sc = __ldg(reinterpret_cast<const float4*>(
+              static_cast<const float*>(rt ? p.s2 : p.s2s) + (rt ? static_cast<size_t>(e) * p.D : 0) + d0));
+          y.x *= sc.x; y.y *= sc.y; y.z *= sc.z; y.w *= sc.w;
+        }
+        o[0] = fmaf(w, y.x, o[0]);
+        o[1] = fmaf(w, y.y, o[1]);
+        o[2] = fmaf(w, y.z, o[2]);
+        o[3] = fmaf(w, y.w, o[3]);
+      }
+#pragma unroll
+      for (int m = 1; m < 8; m <<= 1)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] += __shfl_xor_sync(0xffffffffu, o[q], m);
+      if (in && l == 0) {
+        union {
+          uint2 v;
+          __nv_bfloat16 h[4];
+        } w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w.h[q] = __float2bfloat16_rn(o[q]);
+        *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(t) * p.D + d0) = w.v;
+      }
+    }
+  }
+  if (sr->aborted()) drain_grace();  // copies that the producer could not wait for
 }
 
 // ------------------------------------------------------------------ launch
@@ -816,7 +1047,7 @@ cudaError_t launch_few_nt(const FewArgs& a, cudaStream_t s) {
   if (sms > kStreamMaxCtas) sms = kStreamMaxCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms);
-  cfg.blockDim = dim3(kStreamBlock);
+  cfg.blockDim = dim3(Sm::kBlock);
   cfg.dynamicSmemBytes = Sm::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

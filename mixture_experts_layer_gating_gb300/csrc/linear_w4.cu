@@ -14,7 +14,7 @@ struct LinParams {
   const uint8_t* zp;
   void* y;
   int32_t* err;
-  int32_t* cnt;   // [strips] arrivals, zero between launches
+  int32_t* cnt;   // [ctas] arrivals, zero between launches
   float* part;    // [ctas][2][M][128]: a CTA's part of a strip begun earlier, of one it leaves unfinished
   int M, K, N;
 };
@@ -22,15 +22,17 @@ struct LinParams {
 template <int GRP, int NT>
 struct LinSmem {
   using Tr = StreamTraits<kStreamW4, GRP>;
-  static constexpr int kBBuf = 8 * NT * Tr::PITCH;
-  struct Ctrl {
-    uint64_t full[12], empty[12];
-    int abort;
-    int last;
-  };
-  static constexpr int kOther = 2 * kBBuf + static_cast<int>(sizeof(Ctrl)) + 16;
-  static constexpr int NST = stream_stages(kOther);
-  static constexpr int kBytes = 1024 + NST * kStageBytes + kOther;
+  static constexpr int kTeams = NT <= 2 ? 2 : 1;
+  static constexpr int kCons = 32 * kStreamWarps * kTeams;
+  static constexpr int kFeeders = 2;  // feeder warps
+  static constexpr int kBlock = kCons + 32 + 32 * kFeeders;
+  static constexpr int kSlot = stream_slot(8 * NT * Tr::PITCH);
+  static constexpr int kRP = 128 + 4;
+  static constexpr int kRedBytes = 8 * NT * kRP * 4;
+  static constexpr int kOther = kRedBytes + static_cast<int>(sizeof(StreamRing)) + 16;
+  static constexpr int NST = stream_stages(kSlot, kOther);
+  static constexpr int kBytes = 1024 + NST * kSlot + kOther;
+  static_assert(NST >= 4 && NST % kFeeders == 0 && kBytes <= kStreamSmemMax, "shared memory");
 };
 
 __device__ __forceinline__ void store_y(float* y, size_t at, float v) { y[at] = v; }
@@ -41,181 +43,176 @@ __device__ __forceinline__ void store_y(__nv_bfloat16* y, size_t at, float v) {
 // Strips of 128 output features x stages of 256 k, divided into equal runs
 // over the CTAs.  A strip inside one CTA's run is written at once; one that
 // several CTAs share gets its parts added, in the order of k, by the CTA that
-// finishes last (an arrival count per strip).
+// finishes last (an arrival count per CTA that begins a shared strip).
 template <int GRP, int NT, bool ZERO, typename TY>
-__global__ void __launch_bounds__(kStreamBlock, 1)
+__global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     linear_w4_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ LinParams p) {
   using Tr = StreamTraits<kStreamW4, GRP>;
   using Sm = LinSmem<GRP, NT>;
-  using Ctrl = typename Sm::Ctrl;
+  constexpr int CT = Sm::kCons, RP = Sm::kRP;
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  uint8_t* ring_ptr = smem_raw + pad;
-  uint8_t* bptr = ring_ptr + Sm::NST * kStageBytes;
-  Ctrl* ctl = reinterpret_cast<Ctrl*>(bptr + 2 * Sm::kBBuf);
-  const int tid = threadIdx.x, b = blockIdx.x, G = gridDim.x;
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* red = reinterpret_cast<float*>(ring + Sm::NST * Sm::kSlot);
+  StreamRing* sr = reinterpret_cast<StreamRing*>(ring + Sm::NST * Sm::kSlot + Sm::kRedBytes);
+  const int tid = threadIdx.x, b = blockIdx.x, lane = tid & 31;
   const int C = (p.K + 255) / 256, S = (p.N + kLinStrip - 1) / kLinStrip;
-  const Split sp = make_split(static_cast<long long>(S) * C, G);
+  const Split sp = make_split(static_cast<long long>(S) * C, gridDim.x);
   const long long lo = split_lo(sp, b), hi = split_lo(sp, b + 1);
 
-  if (tid == 0) {
-    for (int i = 0; i < Sm::NST; ++i) {
-      mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], kStreamWarps);
-    }
-    ctl->abort = 0;
-    fence_mbarrier_init();
-  }
+  if (tid == 0) sr->init();
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
+  int s = static_cast<int>(lo / C), kc = static_cast<int>(lo % C);
 
-  if (tid >= kStreamThreads) {  // producer
-    if ((tid & 31) == 0) {
-      const uint64_t policy = l2_policy_evict_first();
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      long long q = lo;
-      for (; q < hi; ++q) {
-        if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort)) {
-          ok = false;
+  if (tid >= CT + 32) {  // feeders: x rows of every kFeeders-th stage, in the k order of the weights
+    // (always the same slots: a wait cannot mistake a fill for the one before); 32
+    // pieces of 8 inputs a row, one a lane
+    constexpr int J = GRP / 32;
+    const int pc = lane;
+    const uint32_t pdst = (((pc / (4 * J)) * J + pc % J) * 4 + (pc % (4 * J)) / J) * 16;
+    int turn = (tid - CT - 32) >> 5;
+    RingPos pos;
+    for (int left = static_cast<int>(hi - lo); left > 0; --left) {
+      if (turn == 0) {
+        if (!mbar_wait(&sr->empty[pos.at], pos.phase ^ 1u, &sr->abort)) {
+          sr->give_up(p.err);
           break;
         }
-        const int s = static_cast<int>(q / C), kc = static_cast<int>(q % C);
-        uint8_t* d = ring_ptr + stage * kStageBytes;
-        mbar_arrive_expect_tx(&ctl->full[stage], kStageBytes);
-        tma_load_2d(d, &mw, &ctl->full[stage], kc * 128, s * kLinStrip, policy);
-        if (++stage == Sm::NST) {
-          stage = 0;
-          phase ^= 1u;
+        uint8_t* dst = ring + pos.at * Sm::kSlot + kStageBytes + pdst;
+        const int k0 = kc * 256 + pc * 8;
+#pragma unroll 1
+        for (int r0 = 0; r0 < p.M; r0 += 8) {
+          uint4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r0 + i < p.M && k0 < p.K)
+              x[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(r0 + i) * p.K + k0));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint4 v;
+            v.x = __byte_perm(x[i].x, x[i].z, 0x5410);
+            v.y = __byte_perm(x[i].x, x[i].z, 0x7632);
+            v.z = __byte_perm(x[i].y, x[i].w, 0x5410);
+            v.w = __byte_perm(x[i].y, x[i].w, 0x7632);
+            *reinterpret_cast<uint4*>(dst + (r0 + i) * Tr::PITCH) = v;
+          }
+        }
+        mbar_arrive(&sr->full[pos.at]);
+      }
+      turn = turn == 0 ? Sm::kFeeders - 1 : turn - 1;
+      pos.next(Sm::NST);
+      kc = kc + 1 == C ? 0 : kc + 1;
+    }
+    return;
+  }
+  if (tid >= CT) {  // producer
+    if (lane == 0) {
+      const uint64_t policy = l2_policy_evict_first();
+      RingPos pos;
+      for (long long q = lo; q < hi; ++q) {
+        if (!mbar_wait(&sr->empty[pos.at], pos.phase ^ 1u, &sr->abort)) {
+          sr->give_up(p.err);
+          break;
+        }
+        mbar_arrive_expect_tx(&sr->full[pos.at], kStageBytes);
+        tma_load_2d(ring + pos.at * Sm::kSlot, &mw, &sr->full[pos.at], kc * 128, s * kLinStrip, policy);
+        pos.next(Sm::NST);
+        if (++kc == C) {
+          kc = 0;
+          ++s;
         }
       }
-      if (!ok || *reinterpret_cast<volatile int*>(&ctl->abort)) {
-        if (!*reinterpret_cast<volatile int*>(&ctl->abort)) {
-          *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-          atomicOr(p.err, MOE_DEV_WAIT_TIMEOUT);
-        }
-        for (int i = 0; i < Sm::NST; ++i) {
-          stage = stage == 0 ? Sm::NST - 1 : stage - 1;
-          if (stage == Sm::NST - 1) phase ^= 1u;
-          mbar_wait_drain(&ctl->full[stage], phase);
-        }
-        drain_grace();
-      }
+      if (sr->aborted()) drain_ring(sr, pos, Sm::NST);
     }
     return;
   }
 
-  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const uint32_t ring = smem_u32(ring_ptr), bbase = smem_u32(bptr);
+  // consumers
+  const int team = Sm::kTeams == 1 ? 0 : tid / (32 * kStreamWarps);
+  const int warp = (tid >> 5) % kStreamWarps, g = lane >> 2, c = lane & 3;
+  const uint32_t ring_a = smem_u32(ring);
   TY* y = static_cast<TY*>(p.y);
-  // x rows of a stage: 32 pieces of 8 inputs a row, NT pieces a thread (row
-  // tid / 32 + 8 i, piece tid % 32), put in the k order of the weights on the way
-  constexpr int J = GRP / 32;
-  const int pc = tid & 31, prow = tid >> 5;
-  const int pq = pc / (4 * J), pr = pc % (4 * J);
-  const uint32_t pdst = ((pq * J + pr % J) * 4 + pr / J) * 16;
-  uint4 xr[NT];
-  auto load_x = [&](int kc) {
-    const int k0 = kc * 256 + pc * 8;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int row = prow + 8 * i;
-      xr[i] = make_uint4(0, 0, 0, 0);
-      if (row < p.M && k0 < p.K)
-        xr[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row) * p.K + k0));
-    }
-  };
-  auto put_x = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      uint4 v;
-      v.x = __byte_perm(xr[i].x, xr[i].z, 0x5410);
-      v.y = __byte_perm(xr[i].x, xr[i].z, 0x7632);
-      v.z = __byte_perm(xr[i].y, xr[i].w, 0x5410);
-      v.w = __byte_perm(xr[i].y, xr[i].w, 0x7632);
-      *reinterpret_cast<uint4*>(bptr + buf * Sm::kBBuf + (prow + 8 * i) * Tr::PITCH + pdst) = v;
-    }
-  };
-  W4Scales<GRP> sc_now, sc_next;
-  const int r = nk_row<kStreamW4, GRP>(g);
-  auto scales = [&](W4Scales<GRP>& dst, int s, int kc) {
-    const int n0 = s * kLinStrip + warp * 16 + r;
-    w4_load_scales<GRP>(dst, p.sc, p.zp, n0 < p.N ? n0 : -1, n0 + 8 < p.N ? n0 + 8 : -1, p.K / GRP,
-                        kc * (256 / GRP), lane);
-  };
-
-  float acc[NT][1][4];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int t = 0; t < 4; ++t) acc[i][0][t] = 0.0f;
+  const int r = nk_row<kStreamW4, GRP>(g), groups = p.K / GRP;
   const int ntu = (p.M + 7) >> 3;
-  int s = 0, kc = 0;
-  if (lo < hi) {
-    s = static_cast<int>(lo / C);
-    kc = static_cast<int>(lo % C);
-    load_x(kc);
-    scales(sc_next, s, kc);
-  }
   bool begun_earlier = kc != 0;
-  int stage = 0, buf = 0;
-  uint32_t phase = 0;
-  for (long long q = lo; q < hi; ++q) {
-    put_x(buf);
-    sc_now = sc_next;
-    const bool strip_end = kc + 1 == C;
-    if (q + 1 < hi) {
-      load_x(strip_end ? 0 : kc + 1);
-      scales(sc_next, strip_end ? s + 1 : s, strip_end ? 0 : kc + 1);
+  RingPos ring_pos;
+  int left = static_cast<int>(hi - lo);
+  float acc[NT][1][4];
+  while (left > 0) {  // a strip, or this CTA's part of it
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[i][0][t] = 0.0f;
+    const int chunks = min(C - kc, left), end = kc + chunks;
+    const bool strip_end = end == C;
+    RingPos pos = ring_pos;
+    if (team) pos.next(Sm::NST);
+    // the lane's row of group scales, loaded two of the team's chunks ahead
+    const int n = s * kLinStrip + warp * 16 + r + (c & 1) * 8;
+    const long long srow = n < p.N ? static_cast<long long>(n) * groups : -1;
+    W4Scales<GRP> sc0, sc1, sc2;
+    w4_load_scales<GRP>(sc0, p.sc, p.zp, srow, groups, (kc + team) * (256 / GRP), lane);
+    w4_load_scales<GRP>(sc1, p.sc, p.zp, srow, groups, (kc + team + Sm::kTeams) * (256 / GRP), lane);
+#pragma unroll 1
+    for (int q = kc + team; q < end; q += Sm::kTeams) {
+      w4_load_scales<GRP>(sc2, p.sc, p.zp, srow, groups, (q + 2 * Sm::kTeams) * (256 / GRP), lane);
+      if (!mbar_wait(&sr->full[pos.at], pos.phase, &sr->abort)) sr->give_up(p.err);
+      __syncwarp();
+      const uint32_t st = ring_a + pos.at * Sm::kSlot;
+      stage_mma_w4<GRP, NT, ZERO, false>(st, st + kStageBytes, warp, lane, ntu, sc0, min(256, p.K - q * 256) / GRP,
+                                         acc);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sr->empty[pos.at]);
+      pos.skip(Sm::kTeams, Sm::NST);
+      sc0 = sc1;
+      sc1 = sc2;
     }
-    bar_consumers();
-    if (!mbar_wait(&ctl->full[stage], phase, &ctl->abort)) {
-      if (lane == 0 && !*reinterpret_cast<volatile int*>(&ctl->abort)) {
-        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-        atomicOr(p.err, MOE_DEV_WAIT_TIMEOUT);
+    ring_pos.skip(chunks % Sm::NST, Sm::NST);
+    ring_pos.phase ^= (chunks / Sm::NST) & 1;
+    left -= chunks;
+    {
+#pragma unroll 1
+      for (int t = 0; t < Sm::kTeams; ++t) {  // the teams' sums, in a fixed order
+        if (team == t) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            if (nt < ntu) {
+              float* at = red + (nt * 8 + 2 * c) * RP + warp * 16 + r;
+              const float* v = acc[nt][0];
+              if (t == 0) {
+                at[0] = v[0]; at[RP] = v[1]; at[8] = v[2]; at[RP + 8] = v[3];
+              } else {
+                at[0] += v[0]; at[RP] += v[1]; at[8] += v[2]; at[RP + 8] += v[3];
+              }
+            }
+        }
+        bar_consumers<CT>();
       }
-    }
-    __syncwarp();
-    stage_mma_w4<GRP, NT, false, ZERO>(ring + stage * kStageBytes, bbase + buf * Sm::kBBuf, 0, warp, lane,
-                                       ntu, sc_now, min(256, p.K - kc * 256) / GRP, acc);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->empty[stage]);
-    if (++stage == Sm::NST) {
-      stage = 0;
-      phase ^= 1u;
-    }
-    buf ^= 1;
-
-    if (strip_end || q + 1 == hi) {
-      const int col = warp * 16 + r, n0 = s * kLinStrip;
+      const int n0 = s * kLinStrip;
       if (strip_end && !begun_earlier) {  // the whole strip is this CTA's
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int row = nt * 8 + 2 * c + (t & 1), n = n0 + col + (t >> 1) * 8;
-            if (row < p.M && n < p.N) store_y(y, static_cast<size_t>(row) * p.N + n, acc[nt][0][t]);
-          }
+        for (int i = tid; i < p.M * kLinStrip; i += CT) {
+          const int row = i / kLinStrip, col = i % kLinStrip;
+          if (n0 + col < p.N) store_y(y, static_cast<size_t>(row) * p.N + n0 + col, red[row * RP + col]);
+        }
       } else {
         float* mine = p.part + (static_cast<size_t>(b) * 2 + (begun_earlier ? 0 : 1)) * p.M * kLinStrip;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int row = nt * 8 + 2 * c + (t & 1);
-            if (row < p.M) mine[row * kLinStrip + col + (t >> 1) * 8] = acc[nt][0][t];
-          }
+        for (int i = tid; i < p.M * kLinStrip; i += CT) mine[i] = red[i / kLinStrip * RP + i % kLinStrip];
         __threadfence();
-        bar_consumers();
+        bar_consumers<CT>();
         const long long q0 = static_cast<long long>(s) * C;
         const int c0 = split_cta(sp, q0), c1 = split_cta(sp, q0 + C - 1);
-        if (tid == 0) ctl->last = atomicAdd(p.cnt + s, 1) == c1 - c0;
-        bar_consumers();
-        if (ctl->last) {
+        if (tid == 0) {
+          const int last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+          if (last) p.cnt[c0] = 0;
+          sr->last = last;
+        }
+        bar_consumers<CT>();
+        if (sr->last) {
           __threadfence();
-          for (int i = tid; i < p.M * kLinStrip; i += kStreamThreads) {
+          for (int i = tid; i < p.M * kLinStrip; i += CT) {
             const int row = i / kLinStrip, n = n0 + i % kLinStrip;
             if (n >= p.N) continue;
             float v = __ldcg(p.part + (static_cast<size_t>(c0) * 2 + 1) * p.M * kLinStrip + i);
@@ -223,22 +220,15 @@ __global__ void __launch_bounds__(kStreamBlock, 1)
               v += __ldcg(p.part + static_cast<size_t>(cta) * 2 * p.M * kLinStrip + i);
             store_y(y, static_cast<size_t>(row) * p.N + n, v);
           }
-          if (tid == 0) p.cnt[s] = 0;
         }
       }
+      bar_consumers<CT>();  // before the next strip's sums overwrite red
       begun_earlier = false;
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[i][0][t] = 0.0f;
     }
-    if (strip_end) {
-      kc = 0;
-      ++s;
-    } else {
-      ++kc;
-    }
+    kc = 0;
+    ++s;
   }
+  if (sr->aborted()) drain_grace();
 }
 
 template <int GRP, int NT, bool ZERO, typename TY>
@@ -254,7 +244,7 @@ cudaError_t launch_lin(const CUtensorMap& m, const LinParams& p, int grid, cudaS
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
-  return launch_kernel(kern, dim3(grid), dim3(kStreamBlock), Sm::kBytes, s, m, p);
+  return launch_kernel(kern, dim3(grid), dim3(Sm::kBlock), Sm::kBytes, s, m, p);
 }
 
 template <int GRP, int NT>
@@ -378,7 +368,6 @@ cudaError_t launch_dequantize(const uint8_t* q, const __nv_bfloat16* sc, const u
 
 }  // namespace
 
-size_t linear_w4_strips(int N) { return (static_cast<size_t>(N) + kLinStrip - 1) / kLinStrip; }
 size_t linear_w4_part_bytes(int M) {
   return static_cast<size_t>(kStreamMaxCtas) * 2 * M * kLinStrip * 4;
 }
@@ -402,7 +391,7 @@ cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, cons
   p.M = M;
   p.K = K;
   p.N = N;
-  const long long chunks = static_cast<long long>(linear_w4_strips(N)) * ((K + 255) / 256);
+  const long long chunks = (static_cast<long long>(N) + kLinStrip - 1) / kLinStrip * ((K + 255) / 256);
   int grid = device_sm_count();
   if (grid > kStreamMaxCtas) grid = kStreamMaxCtas;
   if (grid > chunks) grid = static_cast<int>(chunks);

@@ -21,8 +21,8 @@ static_assert(sizeof(ControlBlock) == 256, "control block is 256 bytes");
 // and down GEMMs and of the shared expert's two GEMMs (dynamic tile order),
 // zeroed by the call that launches them before its first kernel
 constexpr int kTileCounterSlot = 7;
-// reserved[kGridBarrierSlot] and [kGridBarrierSlot + 16]: arrivals and
-// generation of moe_layer_few's grid barrier (arrivals are zero between launches)
+// reserved[kGridBarrierSlot + 8 i], i < 4: arrivals at moe_layer_few's grid
+// barriers
 constexpr int kGridBarrierSlot = 31;
 
 // ------------------------------------------------- programmatic dependent launch
@@ -87,7 +87,6 @@ bool few_supported(const moe_config_t* c);
 size_t few_workspace_bytes(const moe_config_t* c);
 
 // ---------------------------------------------------------------- linear_w4.cu
-size_t linear_w4_strips(int N);     // arrival counters of a product
 size_t linear_w4_part_bytes(int M); // room for the partial sums
 cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, const void* wq, const void* sc,
                              const uint8_t* zp, void* y, bool y_f32, int32_t* err, int32_t* cnt, float* part,

@@ -50,12 +50,13 @@ def _call(cfg, d, ws, out=None, stream=None):
     return out
 
 
-def _check(cfg, d, w, ws, out, act, renorm, rows=None):
+def _check(cfg, d, w, ws, out, act, renorm, rows=None, where="cpu"):
     """out (and the routing left in ws) against the reference; rows: only these."""
     T, E, k = cfg.T, cfg.E, cfg.k
     ids = moe.workspace_view(ws, cfg, "topk_ids", (T, k), torch.int32).long().cpu()
     logits = moe.workspace_view(ws, cfg, "logits", (T, E), torch.float32).double().cpu()
-    c = {n: (None if v is None else v.cpu()) for n, v in d.items()}
+    c = {n: (None if v is None else v.to(where)) for n, v in d.items()}
+    ids, logits, out = ids.to(where), logits.to(where), out.to(where)
     if rows is not None:
         c["x"], ids, logits, out = c["x"][rows], ids[rows], logits[rows], out[rows]
     want, tol, exact, el = ref.layer(c["x"], c["Wg"], c["bias"], c["W13"], c["s13"], c["W2"], c["s2"],
@@ -63,7 +64,7 @@ def _check(cfg, d, w, ws, out, act, renorm, rows=None):
     assert ((logits - exact).abs() <= el).all()
     order = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :k]
     assert torch.equal(ids, order)  # the kernel's own logits, ties to the lower index
-    worst = ((out.double().cpu() - want).abs() / tol).max().item()
+    worst = ((out.double() - want).abs() / tol).max().item()
     assert worst <= 1.0, f"{worst} times the allowed error"
 
 
@@ -107,6 +108,30 @@ def test_layer_ragged_widths(w, unit, T, D, I, Is):
     out = _call(cfg, d, ws)
     assert moe.moe_read_device_status(ws) == 0
     _check(cfg, d, w, ws, out, "swiglu", True)
+
+
+@pytest.mark.parametrize("w", KINDS)
+@pytest.mark.parametrize("T", [2, 12, 32])
+def test_layer_long_runs(w, T):
+    """Every CTA streams more stages than its ring holds, of the shared expert
+    (before the routing is known) and of the routed ones; router planes that are
+    read by one CTA per token (512 experts)."""
+    D, E, k, I, Is = (4096, 512, 2, 128, 2048) if w == "bf16" else (8192, 512, 2, 128, 4096)
+    cfg = moe.make_config(T, D, E, k, I, Is, w_dtype=w)
+    d = _inputs(w, T, D, E, k, I, Is, seed=T)
+    ws = moe.alloc_workspace(cfg)
+    out = _call(cfg, d, ws)
+    assert moe.moe_read_device_status(ws) == 0
+    _check(cfg, d, w, ws, out, "swiglu", True, where="cuda")
+    cfg = moe.make_config(T, 2048, 4, 4, 2048, 0, w_dtype=w)
+    d = _inputs(w, T, 2048, 4, 4, 2048, 0, seed=T)
+    ws = moe.alloc_workspace(cfg)
+    out = _call(cfg, d, ws)
+    for _ in range(30):  # back to back, nothing waits in between
+        again = _call(cfg, d, ws)
+    assert torch.equal(out, again)
+    assert moe.moe_read_device_status(ws) == 0
+    _check(cfg, d, w, ws, out, "swiglu", True, where="cuda")
 
 
 @pytest.mark.parametrize("w", KINDS)
