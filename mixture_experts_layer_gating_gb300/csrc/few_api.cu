@@ -57,15 +57,15 @@ FewLayout few_layout(const moe_config_t* c) {
     cur = up256(cur + bytes);
     return o;
   };
-  L.cnt = take(2 * kStreamMaxCtas * 4);
+  L.cnt = take(kStreamMaxCtas * 4);
   L.planes = take(static_cast<size_t>(few_planes(c)) * T * c->E * 4);
   L.xp = take(T * L.Dp * 2);
   L.xinv = take(T * 4);
   L.hp = take(rows * L.Ip * 4);
   L.hmax = take(rows * 4);
-  L.part = take(static_cast<size_t>(4) * kStreamMaxCtas * T * 2 * g.hc * 4);
+  L.part = take(static_cast<size_t>(2) * kStreamMaxCtas * T * 2 * g.hc * 4);
   L.prim = take(rows * L.W * 4);
-  L.extra = take(static_cast<size_t>(2) * kStreamMaxCtas * T * 2 * g.hc * 4);
+  L.extra = take(static_cast<size_t>(kStreamMaxCtas) * T * 2 * g.hc * 4);
   L.total = cur;
   return L;
 }

@@ -42,7 +42,7 @@ struct FewParams {
   int32_t* err;
   uint32_t* bar;  // grid barriers: arrivals of barrier i at [8 i], all zero between launches but
                   // barrier 3's, which the next launch clears
-  int32_t* cnt;   // [2][kStreamMaxCtas]: arrivals at the strip that CTA c begins and others share
+  int32_t* cnt;   // [kStreamMaxCtas]: arrivals at the strip that CTA c begins and others share
   float* logits;
   int32_t* ids;
   float* topw;
@@ -52,9 +52,9 @@ struct FewParams {
   void* hp;            // [R + T][Ip] h, row R + t token t of the shared expert: fp32 in natural
                        // order, or (bf16 weights) [2][R + T][Ip] bf16 hi and lo in the k order
   uint32_t* hmax;      // [R + T]: the row's largest |h| (bits of an fp32)
-  float* part;         // [2][ctas][2][T][2 HC]: gate/up sums of shared strips
+  float* part;         // [ctas][2][T][2 HC]: gate/up sums of shared strips
   float* prim;         // [R + T][W]: the first partial sum of every down strip of a row
-  float* extra;        // [2][ctas][T][2 HC]: a CTA's part of a down strip begun by an earlier one
+  float* extra;        // [ctas][T][2 HC]: a CTA's part of a down strip begun by an earlier one
   int T, D, E, k, I, Is, act, renorm;
   int Dp, Ip;          // padded row lengths of xp, hp (elements)
   int W;               // floats per row of prim
@@ -67,6 +67,15 @@ __device__ __forceinline__ float few_act(float g, float u, int act) {
   return 0.5f * g * (1.0f + tanhf(c * (g + 0.044715f * g * g * g))) * u;
 }
 
+// One pass over weights: the shared expert's strips, then the chosen experts',
+// every strip C chunks (stages) long; this CTA's run of the chunks.  Index 0 of
+// S, C, K, width: the shared expert, 1: the routed ones.
+struct FewPass {
+  Split sp;
+  long long lo, hi, shared;  // shared: chunks of the shared expert
+  int S[2], C[2];            // strips of an expert, chunks of a strip
+  int K[2], width[2];        // the reduction, the output columns (of gate and up each)
+};
 template <int KIND, int GRP, int NT>
 struct FewSmem {
   using Tr = StreamTraits<KIND, GRP>;
@@ -74,7 +83,7 @@ struct FewSmem {
   static constexpr int kTeams = KIND == kStreamFp8 ? (NT == 1 ? 2 : 1) : (NT <= 2 ? 2 : 1);
   static constexpr int kCons = 32 * kStreamWarps * kTeams;  // consumer threads
   static constexpr int kFeeders = 2;                        // feeder warps
-  static constexpr int kBlock = kCons + 32 + 32 * kFeeders;
+  static constexpr int kBlock = kCons + 32 + 32 * kFeeders + 32;  // + producer, feeders, finisher: 12 or 20 warps
   // token rows of a stage: bf16 weights take h as two terms
   static constexpr bool kHilo = KIND == kStreamBf16;
   static constexpr int kRows = (kHilo ? 2 : 1) * 8 * NT * Tr::PITCH;
@@ -86,71 +95,72 @@ struct FewSmem {
   struct Ctrl {
     StreamRing ring;
     int na;
+    int last;               // of an arrival count
+    FewPass pass[2];        // gate/up, down
     int cnt[512];           // rows of an expert
     int ids[kFewMaxR];      // expert of an expanded row
     float w[kFewMaxR];      // its weight
     uint16_t aexp[512];     // active experts, ascending
     uint16_t aoff[513];     // first sorted position of an active expert
     uint16_t amap[512];     // expert -> its index among the active
-    uint16_t srow[kFewMaxR];  // token of a sorted position
+    uint16_t srow[kFewMaxR + kStreamMaxRows];  // token of a row (routed in sorted order, then shared)
     uint16_t pos[kFewMaxR];   // sorted position of an expanded row
   };
-  static constexpr int kOther = kRedBytes + static_cast<int>(sizeof(Ctrl)) + 16;
+  static constexpr int kOther = 2 * kRedBytes + static_cast<int>(sizeof(Ctrl)) + 16;
   static constexpr int NST = stream_stages(kSlot, kOther);
   static constexpr int kBytes = 1024 + NST * kSlot + kOther;
   static_assert(NST >= 4 && NST % kFeeders == 0, "ring sizes");
   static_assert(kBytes <= kStreamSmemMax, "shared memory");
 };
 
-// One pass over weights: groups x strips x chunks, this CTA's run of them.
-struct FewPass {
-  Split sp;
-  long long lo, hi;
-  int S, C;      // strips of a group, chunks (stages) of a strip
-  int K, width;  // the reduction, the output columns (of gate and up each)
-};
 template <int KIND, int GRP>
-__device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, bool routed, int na, int G,
-                                            int b) {
+__device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int na, int G, int b) {
   using Tr = StreamTraits<KIND, GRP>;
-  const int I = routed ? p.I : p.Is;
   FewPass f;
-  f.K = down ? I : p.D;
-  f.width = down ? p.D : I;
-  const int per = down ? 2 * Tr::HC : Tr::HC;
-  f.S = (f.width + per - 1) / per;
-  f.C = (f.K + Tr::KCH - 1) / Tr::KCH;
-  const int groups = routed ? na : (p.Is > 0 ? 1 : 0);
-  f.sp = make_split(static_cast<long long>(groups) * f.S * f.C, G);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int I = r ? p.I : p.Is;
+    f.K[r] = down ? I : p.D;
+    f.width[r] = down ? p.D : I;
+    const int per = down ? 2 * Tr::HC : Tr::HC;
+    f.S[r] = (f.width[r] + per - 1) / per;
+    f.C[r] = (f.K[r] + Tr::KCH - 1) / Tr::KCH;
+  }
+  f.shared = p.Is > 0 ? static_cast<long long>(f.S[0]) * f.C[0] : 0;
+  f.sp = make_split(f.shared + static_cast<long long>(na) * f.S[1] * f.C[1], G);
   f.lo = split_lo(f.sp, b);
   f.hi = split_lo(f.sp, b + 1);
   return f;
 }
-// A chunk's place: active expert, strip, chunk of the strip.
+// A chunk's place: shared (r 0) or routed (r 1) expert, active expert, strip,
+// chunk of the strip.
 struct FewAt {
-  int a, s, kc;
+  int r, a, s, kc;
   __device__ __forceinline__ FewAt(const FewPass& f, long long q) {
-    // runs start anywhere: 32-bit divisions unless the pass is huge
-    if ((f.sp.N >> 31) == 0) {
-      const uint32_t strip = static_cast<uint32_t>(q) / static_cast<uint32_t>(f.C);
-      kc = static_cast<int>(static_cast<uint32_t>(q) - strip * f.C);
-      a = static_cast<int>(strip / static_cast<uint32_t>(f.S));
-      s = static_cast<int>(strip - static_cast<uint32_t>(a) * f.S);
+    r = q >= f.shared;
+    if (r) q -= f.shared;
+    if ((f.sp.N >> 31) == 0) {  // 32-bit divisions unless the pass is huge
+      const uint32_t strip = static_cast<uint32_t>(q) / static_cast<uint32_t>(f.C[r]);
+      kc = static_cast<int>(static_cast<uint32_t>(q) - strip * f.C[r]);
+      a = static_cast<int>(strip / static_cast<uint32_t>(f.S[r]));
+      s = static_cast<int>(strip - static_cast<uint32_t>(a) * f.S[r]);
     } else {
-      const long long strip = q / f.C;
-      kc = static_cast<int>(q - strip * f.C);
-      a = static_cast<int>(strip / f.S);
-      s = static_cast<int>(strip - static_cast<long long>(a) * f.S);
+      const long long strip = q / f.C[r];
+      kc = static_cast<int>(q - strip * f.C[r]);
+      a = static_cast<int>(strip / f.S[r]);
+      s = static_cast<int>(strip - static_cast<long long>(a) * f.S[r]);
+    }
+  }
+  __device__ __forceinline__ void next_strip(const FewPass& f) {
+    kc = 0;
+    if (++s == f.S[r]) {
+      s = 0;
+      if (r) ++a;
+      r = 1;
     }
   }
   __device__ __forceinline__ void next(const FewPass& f) {
-    if (++kc == f.C) {
-      kc = 0;
-      if (++s == f.S) {
-        s = 0;
-        ++a;
-      }
-    }
+    if (++kc == f.C[r]) next_strip(f);
   }
 };
 
@@ -162,6 +172,14 @@ struct Few {
   static constexpr int CT = Sm::kCons;
 
   static __device__ __forceinline__ void bar() { bar_consumers<CT>(); }
+  // An expert's rows: the first one's place in the row arrays (routed rows in
+  // sorted order, then the shared expert's), and how many.
+  static __device__ __forceinline__ int row_first(const FewParams& p, const Ctrl* ctl, const FewAt& at) {
+    return at.r ? ctl->aoff[at.a] : p.T * p.k;
+  }
+  static __device__ __forceinline__ int row_count(const FewParams& p, const Ctrl* ctl, const FewAt& at) {
+    return at.r ? ctl->aoff[at.a + 1] - ctl->aoff[at.a] : p.T;
+  }
 
   // Grid barrier i, by the consumers.  One CTA clears the arrivals of `clear`,
   // a barrier that every CTA has left.
@@ -187,25 +205,28 @@ struct Few {
   }
 
   // ---------------------------------------------------------------- producer
-  static __device__ __forceinline__ bool produce(const CUtensorMap* m, const FewPass& f, bool down,
-                                                 const uint16_t* aexp, StreamRing* r, uint8_t* ring,
+  template <bool DOWN>
+  static __device__ __forceinline__ bool produce(const CUtensorMap* routed, const CUtensorMap* shared,
+                                                 const FewPass& f, const Ctrl* ctl, StreamRing* r, uint8_t* ring,
                                                  RingPos& pos, uint64_t policy) {
     if (f.lo >= f.hi) return true;
     FewAt at(f, f.lo);
+#pragma unroll 1
     for (int left = static_cast<int>(f.hi - f.lo); left > 0; --left) {
       if (!mbar_wait(&r->empty[pos.at], pos.phase ^ 1u, &r->abort)) return false;
       uint64_t* full = &r->full[pos.at];
       uint8_t* dst = ring + pos.at * Sm::kSlot;
-      const int e = aexp ? aexp[at.a] : 0;
+      const CUtensorMap* m = at.r ? routed : shared;
+      const int e = at.r ? ctl->aexp[at.a] : 0;
       mbar_arrive_expect_tx(full, kStageBytes);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint8_t* d = dst + h * kHalfBytes;
         if (Tr::KN) {
-          if (down) tma_load_3d(d, m, full, at.s * 2 * Tr::HC + h * Tr::HC, at.kc * Tr::KCH, e, policy);
+          if (DOWN) tma_load_3d(d, m, full, at.s * 2 * Tr::HC + h * Tr::HC, at.kc * Tr::KCH, e, policy);
           else tma_load_4d(d, m, full, at.s * Tr::HC, h, at.kc * Tr::KCH, e, policy);
         } else {
-          if (down) tma_load_3d(d, m, full, at.kc * 128, at.s * 128 + h * 64, e, policy);
+          if (DOWN) tma_load_3d(d, m, full, at.kc * 128, at.s * 128 + h * 64, e, policy);
           else tma_load_4d(d, m, full, at.kc * 128, at.s * 64, h, e, policy);
         }
       }
@@ -213,6 +234,30 @@ struct Few {
       at.next(f);
     }
     return true;
+  }
+
+  // While the routing is found out: this CTA's share of the shared expert's
+  // weights into L2, as much as that holds.
+  template <bool DOWN>
+  static __device__ __forceinline__ void prefetch_shared(const FewParams& p, const CUtensorMap* m, int b, int G,
+                                                         int most) {
+    FewPass f = few_pass<KIND, GRP>(p, DOWN, 0, G, b);
+    if (f.lo >= f.hi) return;
+    FewAt at(f, f.lo);
+#pragma unroll 1
+    for (int left = min(most, static_cast<int>(f.hi - f.lo)); left > 0; --left) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (Tr::KN) {
+          if (DOWN) tma_prefetch_l2_3d(m, at.s * 2 * Tr::HC + h * Tr::HC, at.kc * Tr::KCH, 0);
+          else tma_prefetch_l2_4d(m, at.s * Tr::HC, h, at.kc * Tr::KCH, 0);
+        } else {
+          if (DOWN) tma_prefetch_l2_3d(m, at.kc * 128, at.s * 128 + h * 64, 0);
+          else tma_prefetch_l2_4d(m, at.kc * 128, at.s * 64, h, 0);
+        }
+      }
+      at.next(f);
+    }
   }
 
   // ------------------------------------------------------------------ feeder
@@ -228,22 +273,21 @@ struct Few {
   // The token rows of the run's chunks that this feeder warp takes (every
   // kFeeders-th, always the same slots: a wait cannot mistake a fill for the one
   // before).  n rows x KCH inputs, 8 inputs a lane.
-  template <bool DOWN, bool ROUTED>
+  template <bool DOWN>
   static __device__ __forceinline__ bool feed(const FewParams& p, const FewPass& f, Ctrl* ctl, uint8_t* ring,
                                               RingPos& pos, int& turn, int lane) {
     constexpr int P = Tr::KCH / 8;  // pieces of a row
     if (f.lo >= f.hi) return true;
-    const int R = p.T * p.k;
     FewAt at(f, f.lo);
+#pragma unroll 1
     for (int left = static_cast<int>(f.hi - f.lo); left > 0; --left) {
       if (turn == 0) {
         if (!mbar_wait(&ctl->ring.empty[pos.at], pos.phase ^ 1u, &ctl->ring.abort)) return false;
-        const int off = ROUTED ? ctl->aoff[at.a] : 0;
-        const int n = ROUTED ? ctl->aoff[at.a + 1] - off : p.T;
+        const int first = row_first(p, ctl, at), n = row_count(p, ctl, at);
         uint8_t* rows = ring + pos.at * Sm::kSlot + kStageBytes;
         if (DOWN && !Sm::kHilo) {
           // fp32 h to scaled fp16, in the weights' k order
-          const int k_end = f.K - at.kc * Tr::KCH;  // inputs of this chunk (zeros beyond)
+          const int k_end = f.K[at.r] - at.kc * Tr::KCH;  // inputs of this chunk (zeros beyond)
           constexpr int U = 4;                      // pieces in flight
           for (int i0 = lane; i0 < n * P; i0 += 32 * U) {
             float4 a[U], b[U];
@@ -254,7 +298,7 @@ struct Few {
               a[u] = b[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               mx[u] = 0;
               if (i < n * P && pc * 8 < k_end) {
-                const int r = (ROUTED ? off : R) + row;
+                const int r = first + row;
                 const float4* src = reinterpret_cast<const float4*>(
                     static_cast<const float*>(p.hp) + static_cast<size_t>(r) * p.Ip + at.kc * Tr::KCH + pc * 8);
                 a[u] = src[0];  // (through L1: every strip takes the same rows)
@@ -288,10 +332,10 @@ struct Few {
           mbar_arrive(&ctl->ring.full[pos.at]);
         } else {
           const uint32_t dst = smem_u32(rows);
-          const size_t plane = static_cast<size_t>(R + p.T) * p.Ip;
+          const size_t plane = static_cast<size_t>(p.T * p.k + p.T) * p.Ip;
           for (int i = lane; i < n * P; i += 32) {
             const int pc = i % P, row = i / P;
-            const int src = DOWN ? (ROUTED ? off : R) + row : (ROUTED ? ctl->srow[off + row] : row);
+            const int src = DOWN ? first + row : ctl->srow[first + row];
             const uint16_t* g = (DOWN ? static_cast<const uint16_t*>(p.hp) : p.xp) +
                                 static_cast<size_t>(src) * (DOWN ? p.Ip : p.Dp) + at.kc * Tr::KCH + pc * 8;
             const uint32_t d = dst + row * Tr::PITCH + pc * 16;
@@ -311,123 +355,187 @@ struct Few {
   // --------------------------------------------------------------- consumers
   // Where the partial sums of shared strips of gate/up are: CTA `cta`'s part of
   // a strip begun earlier (which 0) or of one it leaves unfinished (1).
-  static __device__ __forceinline__ float* part_at(const FewParams& p, bool routed, int cta, int which) {
-    return p.part + ((static_cast<size_t>(routed ? 1 : 0) * kStreamMaxCtas + cta) * 2 + which) * p.T * 2 * Tr::HC;
+  static __device__ __forceinline__ float* part_at(const FewParams& p, int cta, int which) {
+    return p.part + (static_cast<size_t>(cta) * 2 + which) * p.T * 2 * Tr::HC;
   }
 
-  // A finished gate/up strip (its sums by sum(row, column, v[8])) to h rows:
-  // eight columns a thread.  bf16 weights: the last strip also zeroes the row up
-  // to the end of the down pass's last stage.
-  template <bool ROUTED, typename SUM>
-  static __device__ __forceinline__ void finish_h(const FewParams& p, const FewPass& f, const Ctrl* ctl, int a,
-                                                  int s, int n, int tid, SUM sum) {
-    const int off = ROUTED ? ctl->aoff[a] : 0, row0 = ROUTED ? off : p.T * p.k;
-    const int c0 = s * Tr::HC;
-    constexpr int per = Tr::HC / 8;  // threads of a row, consecutive lanes
-    for (int i0 = tid; i0 - (tid & 31) < n * per; i0 += CT) {
-      const bool in = i0 < n * per;
-      const int i = in ? i0 : 0, row = i / per, col = (i % per) * 8;
-      float h[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = 0.0f;
-      if (c0 + col < f.width) {
-        float u[8];
-        sum(row, col, h);
-        sum(row, col + Tr::HC, u);
-        if constexpr (Tr::F16) {
-          const float inv = __ldcg(p.xinv + (ROUTED ? ctl->srow[off + row] : row));
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            h[j] *= inv;
-            u[j] *= inv;
-          }
-        }
-        if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
-          const float4* sc = reinterpret_cast<const float4*>(
-              static_cast<const float*>(ROUTED ? p.s13 : p.s13s) +
-              (ROUTED ? static_cast<size_t>(ctl->aexp[a]) * 2 * f.width : 0) + c0 + col);
-          const float4 g0 = __ldg(sc), g1 = __ldg(sc + 1), u0 = __ldg(sc + f.width / 4), u1 = __ldg(sc + f.width / 4 + 1);
-          h[0] *= g0.x; h[1] *= g0.y; h[2] *= g0.z; h[3] *= g0.w;
-          h[4] *= g1.x; h[5] *= g1.y; h[6] *= g1.z; h[7] *= g1.w;
-          u[0] *= u0.x; u[1] *= u0.y; u[2] *= u0.z; u[3] *= u0.w;
-          u[4] *= u1.x; u[5] *= u1.y; u[6] *= u1.z; u[7] *= u1.w;
-        }
+  // A finished gate/up strip (its sums by sum(row, column)) to h rows, two columns
+  // a thread, four times at once.  bf16 weights: the last strip also zeroes the
+  // row up to the end of the down pass's last stage.
+  template <int THREADS, typename SUM>
+  static __device__ __forceinline__ void finish_h(const FewParams& p, const FewPass& f, const Ctrl* ctl,
+                                                  const FewAt& at, int n, int i0, SUM sum) {
+    constexpr int U = 4, per = Tr::HC / 2;  // per: threads of a row, whole warps
+    const int first = row_first(p, ctl, at), c0 = at.s * Tr::HC, width = f.width[at.r];
+    const float* sc = static_cast<const float*>(at.r ? p.s13 : p.s13s) +
+                      (at.r ? static_cast<size_t>(ctl->aexp[at.a]) * 2 * width : 0);
 #pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
-          // rolled, so that there is one copy of the activation: the registers rotate
-          const float v = few_act(h[0], u[0], p.act);
+    for (; i0 < n * per; i0 += U * THREADS) {
+      float2 g[U], u[U], sg[U], su[U];
+      float inv[U];
 #pragma unroll
-          for (int t = 0; t < 7; ++t) {
-            h[t] = h[t + 1];
-            u[t] = u[t + 1];
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * THREADS, row = i / per, k = c0 + (i % per) * 2;
+        g[j] = u[j] = make_float2(0.0f, 0.0f);
+        sg[j] = su[j] = make_float2(1.0f, 1.0f);
+        inv[j] = 1.0f;
+        if (i < n * per && k < width) {
+          g[j] = sum(row, k - c0);
+          u[j] = sum(row, k - c0 + Tr::HC);
+          if constexpr (Tr::F16) inv[j] = __ldcg(p.xinv + ctl->srow[first + row]);
+          if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
+            sg[j] = __ldg(reinterpret_cast<const float2*>(sc + k));
+            su[j] = __ldg(reinterpret_cast<const float2*>(sc + width + k));
           }
-          h[7] = v;
         }
       }
-      const size_t at = static_cast<size_t>(row0 + row) * p.Ip + c0 + col;
-      if constexpr (Tr::F16) {
-        if (in && c0 + col < f.width) {
-          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.hp) + at);
-          dst[0] = make_float4(h[0], h[1], h[2], h[3]);
-          dst[1] = make_float4(h[4], h[5], h[6], h[7]);
-        }
-        // the bits of non-negative floats order as the floats do (NaN highest)
-        uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(h[j]) & 0x7fffffffu);
-        if (!in) m = 0;
-#pragma unroll
-        for (int o = 1; o < per; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (in && col == 0) atomicMax(p.hmax + row0 + row, m);
-      } else if (in) {
-        // eight columns are whole pairs of the permuted row
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.hp);
-        const size_t plane = static_cast<size_t>(p.T * p.k + p.T) * p.Ip;
-        if (c0 + col < p.Ip) {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            __nv_bfloat162 hi, lo;
-            split_bf16(h[j], hi.x, lo.x);
-            split_bf16(h[j + 1], hi.y, lo.y);
-            const size_t o = at - (c0 + col) + perm_k<KIND, GRP>(c0 + col + j);
-            *reinterpret_cast<__nv_bfloat162*>(dst + o) = hi;
-            *reinterpret_cast<__nv_bfloat162*>(dst + plane + o) = lo;
-          }
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * THREADS, row = i / per, k = c0 + (i % per) * 2;
+        if (i >= n * per) break;  // (whole warps)
+        float2 h;
+        h.x = few_act(g[j].x * inv[j] * sg[j].x, u[j].x * inv[j] * su[j].x, p.act);
+        h.y = few_act(g[j].y * inv[j] * sg[j].y, u[j].y * inv[j] * su[j].y, p.act);
+        const size_t o = static_cast<size_t>(first + row) * p.Ip;
+        if constexpr (Tr::F16) {
+          if (k < width) *reinterpret_cast<float2*>(static_cast<float*>(p.hp) + o + k) = h;
+          // the bits of non-negative floats order as the floats do (NaN highest);
+          // a warp's lanes are all of one row
+          const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(h.x) & 0x7fffffffu,
+                                                                __float_as_uint(h.y) & 0x7fffffffu));
+          if ((threadIdx.x & 31) == 0) atomicMax(p.hmax + first + row, m);
+        } else if (k < p.Ip) {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.hp) + o + perm_k<KIND, GRP>(k);
+          __nv_bfloat162 hi, lo;
+          split_bf16(h.x, hi.x, lo.x);
+          split_bf16(h.y, hi.y, lo.y);
+          *reinterpret_cast<__nv_bfloat162*>(dst) = hi;
+          *reinterpret_cast<__nv_bfloat162*>(dst + static_cast<size_t>(p.T * p.k + p.T) * p.Ip) = lo;
         }
       }
     }
   }
 
-  // fp32 h rows r0 .. r0 + n - 1, as far as the first chunks of the run reach
-  // and one line a thread.
-  static __device__ __forceinline__ void prefetch_h(const FewParams& p, const FewPass& f, int r0, int n) {
+  // One strip's sums (red), or this CTA's part of them, by THREADS threads (the
+  // finisher warp, or all consumers): down strips become fp32 rows; gate/up strips
+  // become h, those that several CTAs share by the one that arrives last.
+  template <bool DOWN, int THREADS>
+  static __device__ __noinline__ void finish_strip(const FewParams& p, const FewPass& f, Ctrl* ctl, const float* red,
+                                                   FewAt at, int end, long long q0, int b, int i0) {
+    constexpr int RP = Sm::kRP, Q = 2 * Tr::HC / 4;
+    const int n = row_count(p, ctl, at);
+    const bool begun_earlier = at.kc != 0;
+    if (!DOWN && end == f.C[at.r] && !begun_earlier) {  // the whole strip is this CTA's
+      finish_h<THREADS>(p, f, ctl, at, n, i0,
+                        [&](int row, int col) { return *reinterpret_cast<const float2*>(red + row * RP + col); });
+      return;
+    }
+    float* dst;
+    size_t pitch = 2 * Tr::HC;
+    if (!DOWN) {
+      dst = part_at(p, b, begun_earlier ? 0 : 1);
+    } else if (begun_earlier) {
+      dst = p.extra + static_cast<size_t>(b) * p.T * 2 * Tr::HC;
+    } else {
+      dst = p.prim + static_cast<size_t>(row_first(p, ctl, at)) * p.W + static_cast<size_t>(at.s) * 2 * Tr::HC;
+      pitch = p.W;
+    }
+#pragma unroll 2
+    for (int i = i0; i < n * Q; i += THREADS) {
+      const int row = i / Q, col = (i % Q) * 4;
+      *reinterpret_cast<float4*>(dst + row * pitch + col) = *reinterpret_cast<const float4*>(red + row * RP + col);
+    }
+    if (DOWN) return;
+    const int c0 = split_cta(f.sp, q0), c1 = split_cta(f.sp, q0 + f.C[at.r] - 1);
+    int last = 0;
+    __threadfence();
+    if (THREADS == 32) {
+      __syncwarp();
+      if (i0 == 0) last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+      last = __shfl_sync(0xffffffffu, last, 0);
+    } else {
+      bar();
+      if (i0 == 0) ctl->last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+      bar();
+      last = ctl->last;
+    }
+    if (!last) return;
+    __threadfence();
+    const size_t step = static_cast<size_t>(2) * p.T * 2 * Tr::HC;  // from a CTA's parts to the next one's
+    const float* head = part_at(p, c0, 1);
+    const float* rest = part_at(p, c0 + 1, 0);
+    finish_h<THREADS>(p, f, ctl, at, n, i0, [&](int row, int col) {
+      const size_t o = static_cast<size_t>(row) * 2 * Tr::HC + col;
+      // c1 > c0; three parts in flight
+      float2 v = __ldcg(reinterpret_cast<const float2*>(head + o));
+      const float2 w = __ldcg(reinterpret_cast<const float2*>(rest + o));
+      float2 x = make_float2(0.0f, 0.0f);
+      if (c1 > c0 + 1) x = __ldcg(reinterpret_cast<const float2*>(rest + step + o));
+      v.x = v.x + w.x + x.x;
+      v.y = v.y + w.y + x.y;
+#pragma unroll 1
+      for (int cta = c0 + 3; cta <= c1; ++cta) {
+        const float2 m = __ldcg(reinterpret_cast<const float2*>(rest + (cta - c0 - 1) * step + o));
+        v.x += m.x;
+        v.y += m.y;
+      }
+      return v;
+    });
+  }
+
+  // The finisher's part of a pass: every strip's sums as the consumers hand them
+  // over, but for the run's last, which the consumers finish themselves.
+  template <bool DOWN>
+  static __device__ __forceinline__ void finish(const FewParams& p, const FewPass& f, Ctrl* ctl, const float* red0,
+                                                RingPos& rpos, int b, int lane) {
     if (f.lo >= f.hi) return;
-    const int lines = (f.K + 31) / 32, i = threadIdx.x;
+    FewAt at(f, f.lo);
+    int left = static_cast<int>(f.hi - f.lo);
+#pragma unroll 1
+    for (;;) {
+      const int chunks = min(f.C[at.r] - at.kc, left), end = at.kc + chunks;
+      left -= chunks;
+      if (left == 0) break;
+      if (!mbar_wait(&ctl->ring.red_full[rpos.at], rpos.phase, &ctl->ring.abort)) ctl->ring.give_up(p.err);
+      __syncwarp();
+      finish_strip<DOWN, 32>(p, f, ctl, red0 + rpos.at * (Sm::kRedBytes / 4), at, end, f.hi - left - end, b, lane);
+      __syncwarp();
+      mbar_arrive(&ctl->ring.red_empty[rpos.at]);
+      rpos.next(2);
+      at.next_strip(f);
+    }
+  }
+
+  // fp32 h rows of the run's first strip, one line a thread.
+  static __device__ __forceinline__ void prefetch_h(const FewParams& p, const FewPass& f, const Ctrl* ctl) {
+    if (f.lo >= f.hi) return;
+    const FewAt at(f, f.lo);
+    const int r0 = row_first(p, ctl, at), n = row_count(p, ctl, at);
+    const int lines = (f.K[at.r] + 31) / 32, i = threadIdx.x;
     if (i < n * lines)
       asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const float*>(p.hp) +
                                                     static_cast<size_t>(r0 + i / lines) * p.Ip + (i % lines) * 32));
   }
 
-  template <bool DOWN, bool ROUTED>
+  template <bool DOWN>
   static __device__ __forceinline__ void consume(const FewParams& p, const FewPass& f, Ctrl* ctl, uint32_t ring,
-                                                 float* red, RingPos& ring_pos, int b) {
+                                                 float* red0, RingPos& ring_pos, RingPos& rpos, int b) {
     if (f.lo >= f.hi) return;
     const int tid = threadIdx.x, team = Sm::kTeams == 1 ? 0 : tid / (32 * kStreamWarps);
     const int warp = (tid >> 5) % kStreamWarps, lane = tid & 31;
-    const int g = lane >> 2, c = lane & 3;
+    [[maybe_unused]] const int g = lane >> 2, c = lane & 3;
     constexpr uint32_t kLo = 8 * NT * Tr::PITCH;
-    constexpr int RP = Sm::kRP;
     FewAt at(f, f.lo);
     int left = static_cast<int>(f.hi - f.lo);
-    bool begun_earlier = at.kc != 0;  // this CTA's first strip was begun by an earlier one
 
     // 4-bit weights: the lane's row of group scales
     [[maybe_unused]] W4Scales<GRP == 0 ? 128 : GRP> sc0, sc1, sc2;
+    [[maybe_unused]] const __nv_bfloat16* sbase = nullptr;
     [[maybe_unused]] long long srow = 0;
+    [[maybe_unused]] int groups = 0;
     auto scales = [&](auto& dst, int kc) {
       if constexpr (KIND == kStreamW4)
-        w4_load_scales<GRP>(dst, static_cast<const __nv_bfloat16*>(DOWN ? (ROUTED ? p.s2 : p.s2s) : (ROUTED ? p.s13 : p.s13s)),
-                            nullptr, srow, f.K / GRP, kc * (256 / GRP), lane);
+        w4_load_scales<GRP>(dst, sbase, nullptr, srow, groups, kc * (256 / GRP) + (warp & 1) * (128 / GRP));
     };
 
     float acc[NT][Tr::MT][4];
@@ -438,18 +546,19 @@ struct Few {
         for (int j = 0; j < Tr::MT; ++j)
 #pragma unroll
           for (int t = 0; t < 4; ++t) acc[i][j][t] = 0.0f;
-      const int n = ROUTED ? ctl->aoff[at.a + 1] - ctl->aoff[at.a] : p.T;
-      const int ntu = (n + 7) >> 3;
-      const int chunks = min(f.C - at.kc, left), end = at.kc + chunks;
-      const bool strip_end = end == f.C;
+      const int ntu = (row_count(p, ctl, at) + 7) >> 3;
+      const int chunks = min(f.C[at.r] - at.kc, left), end = at.kc + chunks;
       RingPos pos = ring_pos;
       if (team) pos.next(Sm::NST);
       if constexpr (KIND == kStreamW4) {
-        const int l = (DOWN ? at.s * 128 + warp * 16 : at.s * 64 + (warp & 3) * 16) + nk_row<KIND, GRP>(g) +
-                      (c & 1) * 8;
+        // the lane's row: tile c / 2, row g or g + 8; rows 64 on of a gate/up stage are up rows
         const int half = DOWN ? 0 : warp >> 2;
-        const long long e = ROUTED ? ctl->aexp[at.a] : 0;
-        srow = l < f.width ? ((e * (DOWN ? 1 : 2) + half) * f.width + l) * (f.K / GRP) : -1;
+        const int l = at.s * (DOWN ? 128 : 64) + ((warp >> 1) & (DOWN ? 3 : 1)) * 32 + (c >> 1) * 16 +
+                      nk_row<KIND, GRP>(g) + (c & 1) * 8;
+        const long long e = at.r ? ctl->aexp[at.a] : 0;
+        sbase = static_cast<const __nv_bfloat16*>(DOWN ? (at.r ? p.s2 : p.s2s) : (at.r ? p.s13 : p.s13s));
+        groups = f.K[at.r] / GRP;
+        srow = l < f.width[at.r] ? ((e * (DOWN ? 1 : 2) + half) * f.width[at.r] + l) * groups : -1;
         scales(sc0, at.kc + team);
         scales(sc1, at.kc + team + Sm::kTeams);
       }
@@ -463,7 +572,7 @@ struct Few {
         else if constexpr (KIND == kStreamFp8Nk)
           stage_mma_fp8nk<NT>(st, rows, warp, lane, ntu, acc);
         else {
-          stage_mma_w4<GRP, NT, false, true>(st, rows, warp, lane, ntu, sc0, min(256, f.K - kc * 256) / GRP, acc);
+          stage_mma_w4<GRP, NT, false, true>(st, rows, warp, lane, ntu, sc0, acc);
           sc0 = sc1;
           sc1 = sc2;
         }
@@ -473,93 +582,23 @@ struct Few {
       }
       ring_pos.skip(chunks % Sm::NST, Sm::NST);
       ring_pos.phase ^= (chunks / Sm::NST) & 1;
-      // a slot is one team's as long as the strips' lengths are even: an odd one
-      // swaps the teams, behind the barriers below
       left -= chunks;
-      {
-        // the strip's sums over this CTA's chunks of it, in red[row][2 HC]: the
-        // warps that hold sums of the same columns add theirs one after another,
-        // in a fixed order
-        constexpr int KW = (Tr::KN ? 4 : 1) * Sm::kTeams;
-        const int mine = Tr::KN ? team * 4 + (warp >> 1) : team;  // (a team without a chunk adds zeros)
-#pragma unroll 1
-        for (int r = 0; r < KW; ++r) {
-          if (mine == r) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              if (nt < ntu) {
-#pragma unroll
-                for (int mt = 0; mt < Tr::MT; ++mt) {
-                  // columns of v[0..1] and v[2..3]
-                  const int col = Tr::KN ? (warp & 1) * Tr::HC + kn_col<KIND>(lane, mt)
-                                         : warp * 16 + nk_row<KIND, GRP>(g);
-                  constexpr int step = Tr::KN ? 1 : 8;
-                  float* at_ = red + (nt * 8 + 2 * c) * RP + col;
-                  const float* v = acc[nt][mt];
-                  if (r == 0) {
-                    at_[0] = v[0]; at_[RP] = v[1]; at_[step] = v[2]; at_[RP + step] = v[3];
-                  } else {
-                    at_[0] += v[0]; at_[RP] += v[1]; at_[step] += v[2]; at_[RP + step] += v[3];
-                  }
-                }
-              }
-          }
-          bar();
-        }
-        constexpr int Q = 2 * Tr::HC / 4;
-        auto copy_out = [&](float* dst, size_t pitch) {
-          for (int i = tid; i < n * Q; i += CT) {
-            const int row = i / Q, col = (i % Q) * 4;
-            *reinterpret_cast<float4*>(dst + row * pitch + col) =
-                *reinterpret_cast<const float4*>(red + row * RP + col);
-          }
-        };
-        if (DOWN) {
-          if (begun_earlier)
-            copy_out(p.extra + (static_cast<size_t>(ROUTED ? 1 : 0) * kStreamMaxCtas + b) * p.T * 2 * Tr::HC,
-                     2 * Tr::HC);
-          else
-            copy_out(p.prim + static_cast<size_t>(ROUTED ? ctl->aoff[at.a] : p.T * p.k) * p.W +
-                         static_cast<size_t>(at.s) * 2 * Tr::HC,
-                     p.W);
-        } else if (strip_end && !begun_earlier) {  // the whole strip is this CTA's
-          finish_h<ROUTED>(p, f, ctl, at.a, at.s, n, tid, [&](int row, int col, float (&v)[8]) {
-            const float4 x = *reinterpret_cast<const float4*>(red + row * RP + col);
-            const float4 y = *reinterpret_cast<const float4*>(red + row * RP + col + 4);
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-            v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+      // the sums over this CTA's chunks of the strip, to the finisher
+      add_sums<KIND, GRP, NT, Sm::kTeams, Sm::kRP>(
+          red0 + rpos.at * (Sm::kRedBytes / 4), team, warp, lane, ntu, acc, [&]() {
+            if (!mbar_wait(&ctl->ring.red_empty[rpos.at], rpos.phase ^ 1u, &ctl->ring.abort)) ctl->ring.give_up(p.err);
+            __syncwarp();
           });
-        } else {
-          copy_out(part_at(p, ROUTED, b, begun_earlier ? 0 : 1), 2 * Tr::HC);
-          __threadfence();
-          bar();
-          const long long q0 = f.hi - left - end;  // the strip's first chunk
-          const int c0 = split_cta(f.sp, q0), c1 = split_cta(f.sp, q0 + f.C - 1);
-          int32_t* cnt = p.cnt + (ROUTED ? kStreamMaxCtas : 0) + c0;
-          if (tid == 0) {
-            ctl->ring.last = atomicAdd(cnt, 1) == c1 - c0;
-          }
-          bar();
-          if (ctl->ring.last) {
-            __threadfence();
-            finish_h<ROUTED>(p, f, ctl, at.a, at.s, n, tid, [&](int row, int col, float (&v)[8]) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-              for (int cta = c0; cta <= c1; ++cta) {
-                const float4* m = reinterpret_cast<const float4*>(
-                    part_at(p, ROUTED, cta, cta == c0 ? 1 : 0) + row * 2 * Tr::HC + col);
-                const float4 x = __ldcg(m), y = __ldcg(m + 1);
-                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-                v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-              }
-            });
-          }
-        }
-        bar();  // before the next strip's sums overwrite red
-        begun_earlier = false;
+      if (left > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->ring.red_full[rpos.at]);
+        rpos.next(2);
+        at.next_strip(f);
+      } else {  // the run's last strip: by all consumers, which have nothing else to do
+        bar();
+        finish_strip<DOWN, CT>(p, f, ctl, red0 + rpos.at * (Sm::kRedBytes / 4), at, end, f.hi - end, b, tid);
+        bar();
       }
-      at.kc = f.C - 1;
-      at.next(f);
     }
   }
 
@@ -580,10 +619,11 @@ struct Few {
         float v[kFewMaxPlanes];  // all in flight
 #pragma unroll
         for (int pl = 0; pl < kFewMaxPlanes; ++pl) v[pl] = pl < p.nplanes ? __ldcg(src + pl * plane) : 0.0f;
+        const float bias = p.bias ? __ldg(p.bias + e) : 0.0f;
         float sum = v[0];
 #pragma unroll
         for (int pl = 1; pl < kFewMaxPlanes; ++pl) sum += v[pl];
-        red[i] = sum;
+        red[i] = sum + bias;
       }
       bar();
       if (wid < here) {
@@ -603,7 +643,7 @@ struct Few {
     float v[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) v[i] = lane + 32 * i < p.E ? row[lane + 32 * i] : 0.0f;
-    warp_topk_softmax<EPL>(v, lane, p.E, p.k, p.renorm, p.bias, keep, ids, w, p.err);
+    warp_topk_softmax<EPL>(v, lane, p.E, p.k, p.renorm, nullptr, keep, ids, w, p.err);
   }
 
   // The chosen experts in ascending order and their rows in ascending order, by
@@ -663,6 +703,7 @@ struct Few {
       ctl->srow[at] = static_cast<uint16_t>(r / p.k);
       ctl->pos[r] = static_cast<uint16_t>(at);
     }
+    if (lane < p.T) ctl->srow[R + lane] = static_cast<uint16_t>(lane);
   }
 
   // The router's planes.  A unit is 64 experts x one slice of D; its k16 steps
@@ -826,49 +867,48 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* red = reinterpret_cast<float*>(ring + Sm::NST * Sm::kSlot);
-  Ctrl* ctl = reinterpret_cast<Ctrl*>(ring + Sm::NST * Sm::kSlot + Sm::kRedBytes);
+  Ctrl* ctl = reinterpret_cast<Ctrl*>(ring + Sm::NST * Sm::kSlot + 2 * Sm::kRedBytes);
   StreamRing* sr = &ctl->ring;
   const int tid = threadIdx.x, b = blockIdx.x, G = gridDim.x, lane = tid & 31;
   const int R = p.T * p.k;
   const bool shared = p.Is > 0;
 
-  if (tid == 0) sr->init();
+  if (tid == 0) sr->init(CT / 32);
   __syncthreads();
 
+  if (tid >= CT + 32 + 32 * Sm::kFeeders) {  // ------------------------ finisher
+    RingPos rpos;
+    asm volatile("bar.sync 4, %0;" ::"n"(CT + 32 * Sm::kFeeders + 32) : "memory");  // the expert lists are built
+    F::template finish<false>(p, ctl->pass[0], ctl, red, rpos, b, lane);
+    asm volatile("bar.arrive 5, %0;" ::"n"(CT + 32) : "memory");  // h is written
+    F::template finish<true>(p, ctl->pass[1], ctl, red, rpos, b, lane);
+    asm volatile("bar.arrive 6, %0;" ::"n"(CT + 32) : "memory");  // y is written
+    return;
+  }
   if (tid >= CT + 32) {  // -------------------------------------------- feeders
     RingPos pos;
     int turn = (tid - CT - 32) >> 5;
-    asm volatile("bar.sync 4, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");  // x rows and expert lists are there
-    const int na = ctl->na;
-    bool ok = true;
-    if (shared)
-      ok = F::template feed<false, false>(p, few_pass<KIND, GRP>(p, false, false, na, G, b), ctl, ring, pos, turn, lane);
-    if (ok)
-      ok = F::template feed<false, true>(p, few_pass<KIND, GRP>(p, false, true, na, G, b), ctl, ring, pos, turn, lane);
+    asm volatile("bar.sync 4, %0;" ::"n"(CT + 32 * Sm::kFeeders + 32) : "memory");  // x rows and expert lists are there
+    bool ok = F::template feed<false>(p, ctl->pass[0], ctl, ring, pos, turn, lane);
     asm volatile("bar.sync 3, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");  // h rows are there
-    if (ok && shared)
-      ok = F::template feed<true, false>(p, few_pass<KIND, GRP>(p, true, false, na, G, b), ctl, ring, pos, turn, lane);
-    if (ok)
-      ok = F::template feed<true, true>(p, few_pass<KIND, GRP>(p, true, true, na, G, b), ctl, ring, pos, turn, lane);
+    if (ok) ok = F::template feed<true>(p, ctl->pass[1], ctl, ring, pos, turn, lane);
     if (!ok) sr->give_up(p.err);
     cp_async_wait_all();
     return;
   }
   if (tid >= CT) {  // ------------------------------------------------ producer
-    RingPos pos;
-    bool ok = true;
-    const uint64_t policy = l2_policy_evict_first();
-    if (lane == 0 && shared)
-      ok = F::produce(&m13s, few_pass<KIND, GRP>(p, false, false, 0, G, b), false, nullptr, sr, ring, pos, policy);
+    if (lane == 0 && shared) {
+      // in L2 beside what streams by: 32 MB of each projection
+      F::template prefetch_shared<false>(p, &m13s, b, G, 2048 / G);
+      F::template prefetch_shared<true>(p, &m2s, b, G, 2048 / G);
+    }
     __syncwarp();
     asm volatile("bar.sync 2, %0;" ::"n"(CT + 32) : "memory");  // the expert lists are built
     if (lane == 0) {
-      const int na = ctl->na;
-      if (ok)
-        ok = F::produce(&m13, few_pass<KIND, GRP>(p, false, true, na, G, b), false, ctl->aexp, sr, ring, pos, policy);
-      if (ok && shared)
-        ok = F::produce(&m2s, few_pass<KIND, GRP>(p, true, false, na, G, b), true, nullptr, sr, ring, pos, policy);
-      if (ok) ok = F::produce(&m2, few_pass<KIND, GRP>(p, true, true, na, G, b), true, ctl->aexp, sr, ring, pos, policy);
+      RingPos pos;
+      const uint64_t policy = l2_policy_evict_first();
+      bool ok = F::template produce<false>(&m13, &m13s, ctl->pass[0], ctl, sr, ring, pos, policy);
+      if (ok) ok = F::template produce<true>(&m2, &m2s, ctl->pass[1], ctl, sr, ring, pos, policy);
       if (!ok) sr->give_up(p.err);
       if (sr->aborted()) drain_ring(sr, pos, Sm::NST);
     }
@@ -876,7 +916,9 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   }
 
   // ------------------------------------------------------------------ consumers
-  if (tid < 2) p.cnt[tid * kStreamMaxCtas + b] = 0;
+  // (every named barrier but the consumers' own is used once: a role without
+  // work of its own may be at its next one before the others reach the last)
+  if (tid == 0) p.cnt[b] = 0;
   if (Tr::F16)
     for (int r = b * CT + tid; r < R + p.T; r += G * CT) p.hmax[r] = 0;
   // phase 0
@@ -904,37 +946,30 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
     }
     F::bar();
   }
-  if (tid < 32) F::build_lists(p, ctl, lane);
+  if (tid < 32) {
+    F::build_lists(p, ctl, lane);
+    __syncwarp();
+    if (lane < 2) ctl->pass[lane] = few_pass<KIND, GRP>(p, lane == 1, ctl->na, G, b);
+  }
   F::bar();
-  // each role has a barrier of its own: the producer may still be waiting for
-  // stages of the shared expert that the consumers free once the feeders run
-  asm volatile("bar.arrive 4, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");
+  asm volatile("bar.arrive 4, %0;" ::"n"(CT + 32 * Sm::kFeeders + 32) : "memory");
   asm volatile("bar.arrive 2, %0;" ::"n"(CT + 32) : "memory");
-  const int na = ctl->na;
 
-  RingPos pos;
+  RingPos pos, rpos;
   const uint32_t ring_a = smem_u32(ring);
   // phase 2: gate/up
-  if (shared)
-    F::template consume<false, false>(p, few_pass<KIND, GRP>(p, false, false, na, G, b), ctl, ring_a, red, pos, b);
-  F::template consume<false, true>(p, few_pass<KIND, GRP>(p, false, true, na, G, b), ctl, ring_a, red, pos, b);
+  F::template consume<false>(p, ctl->pass[0], ctl, ring_a, red, pos, rpos, b);
+  asm volatile("bar.sync 5, %0;" ::"n"(CT + 32) : "memory");  // the finisher is through
   F::grid_sync(p, sr, 2, 0);
   asm volatile("bar.arrive 3, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");
 
   // phase 3: down
-  const FewPass ds = few_pass<KIND, GRP>(p, true, false, na, G, b);
-  const FewPass dr = few_pass<KIND, GRP>(p, true, true, na, G, b);
-  if (Tr::F16) {
-    // the h rows of the run's first strips into L1 at once: the feeders, which
-    // load and convert them stage by stage, would wait for L2 at every stage
-    if (shared) F::prefetch_h(p, ds, R, p.T);
-    if (dr.lo < dr.hi) {
-      const int a = FewAt(dr, dr.lo).a;
-      F::prefetch_h(p, dr, ctl->aoff[a], ctl->aoff[a + 1] - ctl->aoff[a]);
-    }
-  }
-  if (shared) F::template consume<true, false>(p, ds, ctl, ring_a, red, pos, b);
-  F::template consume<true, true>(p, dr, ctl, ring_a, red, pos, b);
+  const FewPass& dn = ctl->pass[1];
+  // the h rows of the run's first strip into L1 at once: the feeders, which load
+  // and convert them stage by stage, would wait for L2 at every stage
+  if (Tr::F16) F::prefetch_h(p, dn, ctl);
+  F::template consume<true>(p, dn, ctl, ring_a, red, pos, rpos, b);
+  asm volatile("bar.sync 6, %0;" ::"n"(CT + 32) : "memory");  // the finisher is through
   F::grid_sync(p, sr, 3, 2);
 
   // phase 4: the weighted sum of a token's rows.  Four columns a group of eight
@@ -951,18 +986,18 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
       float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int j = l; j < terms; j += 8) {
         const bool rt = j < p.k;
-        const FewPass& f = rt ? dr : ds;
         const int e = rt ? ctl->ids[t * p.k + j] : 0, a = rt ? ctl->amap[e] : 0;
         const int r = rt ? ctl->pos[t * p.k + j] : R + t, sl = rt ? r - ctl->aoff[a] : t;
         float w = rt ? ctl->w[t * p.k + j] : 1.0f;
         if constexpr (Tr::F16) w *= F::exp2_int(-F::row_exp(__ldcg(p.hmax + r)));
-        const long long q0 = (static_cast<long long>(a) * f.S + s) * f.C;
+        const int C = dn.C[rt];
+        const long long q0 = rt ? dn.shared + (static_cast<long long>(a) * dn.S[1] + s) * C : static_cast<long long>(s) * C;
         float4 y = __ldcg(reinterpret_cast<const float4*>(p.prim + static_cast<size_t>(r) * p.W +
                                                           static_cast<size_t>(s) * 2 * Tr::HC + col));
-        const int c0 = split_cta(f.sp, q0), c1 = split_cta(f.sp, q0 + f.C - 1);
+        const int c0 = split_cta(dn.sp, q0), c1 = split_cta(dn.sp, q0 + C - 1);
         for (int cta = c0 + 1; cta <= c1; ++cta) {
           const float4 m = __ldcg(reinterpret_cast<const float4*>(
-              p.extra + ((static_cast<size_t>(rt ? 1 : 0) * kStreamMaxCtas + cta) * p.T + sl) * 2 * Tr::HC + col));
+              p.extra + (static_cast<size_t>(cta) * p.T + sl) * 2 * Tr::HC + col));
           y.x += m.x; y.y += m.y; y.z += m.z; y.w += m.w;
         }
         if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {

@@ -25,11 +25,11 @@ struct LinSmem {
   static constexpr int kTeams = NT <= 2 ? 2 : 1;
   static constexpr int kCons = 32 * kStreamWarps * kTeams;
   static constexpr int kFeeders = 2;  // feeder warps
-  static constexpr int kBlock = kCons + 32 + 32 * kFeeders;
+  static constexpr int kBlock = kCons + 32 + 32 * kFeeders + 32;  // + producer, feeders, finisher
   static constexpr int kSlot = stream_slot(8 * NT * Tr::PITCH);
   static constexpr int kRP = 128 + 4;
   static constexpr int kRedBytes = 8 * NT * kRP * 4;
-  static constexpr int kOther = kRedBytes + static_cast<int>(sizeof(StreamRing)) + 16;
+  static constexpr int kOther = 2 * kRedBytes + static_cast<int>(sizeof(StreamRing)) + 16;
   static constexpr int NST = stream_stages(kSlot, kOther);
   static constexpr int kBytes = 1024 + NST * kSlot + kOther;
   static_assert(NST >= 4 && NST % kFeeders == 0 && kBytes <= kStreamSmemMax, "shared memory");
@@ -53,18 +53,68 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* red = reinterpret_cast<float*>(ring + Sm::NST * Sm::kSlot);
-  StreamRing* sr = reinterpret_cast<StreamRing*>(ring + Sm::NST * Sm::kSlot + Sm::kRedBytes);
+  StreamRing* sr = reinterpret_cast<StreamRing*>(ring + Sm::NST * Sm::kSlot + 2 * Sm::kRedBytes);
   const int tid = threadIdx.x, b = blockIdx.x, lane = tid & 31;
   const int C = (p.K + 255) / 256, S = (p.N + kLinStrip - 1) / kLinStrip;
   const Split sp = make_split(static_cast<long long>(S) * C, gridDim.x);
   const long long lo = split_lo(sp, b), hi = split_lo(sp, b + 1);
 
-  if (tid == 0) sr->init();
+  if (tid == 0) sr->init(CT / 32);
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
   int s = static_cast<int>(lo / C), kc = static_cast<int>(lo % C);
 
+  if (tid >= CT + 32 + 32 * Sm::kFeeders) {  // finisher: a strip's sums to y
+    TY* y = static_cast<TY*>(p.y);
+    RingPos rpos;
+    bool begun_earlier = kc != 0;
+#pragma unroll 1
+    for (int left = static_cast<int>(hi - lo); left > 0; kc = 0, ++s, begun_earlier = false) {
+      const int chunks = min(C - kc, left), end = kc + chunks, n0 = s * kLinStrip;
+      left -= chunks;
+      const float* sums = red + rpos.at * (Sm::kRedBytes / 4);
+      if (!mbar_wait(&sr->red_full[rpos.at], rpos.phase, &sr->abort)) sr->give_up(p.err);
+      __syncwarp();
+      if (end == C && !begun_earlier) {  // the whole strip is this CTA's
+#pragma unroll 4
+        for (int i = lane; i < p.M * kLinStrip; i += 32) {
+          const int row = i / kLinStrip, col = i % kLinStrip;
+          if (n0 + col < p.N) store_y(y, static_cast<size_t>(row) * p.N + n0 + col, sums[row * RP + col]);
+        }
+      } else {
+        float* mine = p.part + (static_cast<size_t>(b) * 2 + (begun_earlier ? 0 : 1)) * p.M * kLinStrip;
+#pragma unroll 4
+        for (int i = lane; i < p.M * kLinStrip; i += 32) mine[i] = sums[i / kLinStrip * RP + i % kLinStrip];
+        const long long q0 = static_cast<long long>(s) * C;
+        const int c0 = split_cta(sp, q0), c1 = split_cta(sp, q0 + C - 1);
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) {
+          last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+          if (last) p.cnt[c0] = 0;
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          __threadfence();
+#pragma unroll 4
+          for (int i = lane; i < p.M * kLinStrip; i += 32) {
+            const int row = i / kLinStrip, n = n0 + i % kLinStrip;
+            if (n >= p.N) continue;
+            float v = __ldcg(p.part + (static_cast<size_t>(c0) * 2 + 1) * p.M * kLinStrip + i);
+#pragma unroll 4
+            for (int cta = c0 + 1; cta <= c1; ++cta)
+              v += __ldcg(p.part + static_cast<size_t>(cta) * 2 * p.M * kLinStrip + i);
+            store_y(y, static_cast<size_t>(row) * p.N + n, v);
+          }
+        }
+      }
+      __syncwarp();
+      mbar_arrive(&sr->red_empty[rpos.at]);
+      rpos.next(2);
+    }
+    return;
+  }
   if (tid >= CT + 32) {  // feeders: x rows of every kFeeders-th stage, in the k order of the weights
     // (always the same slots: a wait cannot mistake a fill for the one before); 32
     // pieces of 8 inputs a row, one a lane
@@ -134,36 +184,35 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
   const int team = Sm::kTeams == 1 ? 0 : tid / (32 * kStreamWarps);
   const int warp = (tid >> 5) % kStreamWarps, g = lane >> 2, c = lane & 3;
   const uint32_t ring_a = smem_u32(ring);
-  TY* y = static_cast<TY*>(p.y);
   const int r = nk_row<kStreamW4, GRP>(g), groups = p.K / GRP;
   const int ntu = (p.M + 7) >> 3;
-  bool begun_earlier = kc != 0;
-  RingPos ring_pos;
-  int left = static_cast<int>(hi - lo);
-  float acc[NT][1][4];
-  while (left > 0) {  // a strip, or this CTA's part of it
+  RingPos ring_pos, rpos;
+  float acc[NT][2][4];
+#pragma unroll 1
+  for (int left = static_cast<int>(hi - lo); left > 0; kc = 0, ++s) {  // a strip, or this CTA's part of it
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[i][0][t] = 0.0f;
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][j][t] = 0.0f;
     const int chunks = min(C - kc, left), end = kc + chunks;
-    const bool strip_end = end == C;
     RingPos pos = ring_pos;
     if (team) pos.next(Sm::NST);
     // the lane's row of group scales, loaded two of the team's chunks ahead
-    const int n = s * kLinStrip + warp * 16 + r + (c & 1) * 8;
+    const int n = s * kLinStrip + (warp >> 1) * 32 + (c >> 1) * 16 + r + (c & 1) * 8;
     const long long srow = n < p.N ? static_cast<long long>(n) * groups : -1;
+    const int qh = (warp & 1) * (128 / GRP);
     W4Scales<GRP> sc0, sc1, sc2;
-    w4_load_scales<GRP>(sc0, p.sc, p.zp, srow, groups, (kc + team) * (256 / GRP), lane);
-    w4_load_scales<GRP>(sc1, p.sc, p.zp, srow, groups, (kc + team + Sm::kTeams) * (256 / GRP), lane);
+    w4_load_scales<GRP>(sc0, p.sc, p.zp, srow, groups, (kc + team) * (256 / GRP) + qh);
+    w4_load_scales<GRP>(sc1, p.sc, p.zp, srow, groups, (kc + team + Sm::kTeams) * (256 / GRP) + qh);
 #pragma unroll 1
     for (int q = kc + team; q < end; q += Sm::kTeams) {
-      w4_load_scales<GRP>(sc2, p.sc, p.zp, srow, groups, (q + 2 * Sm::kTeams) * (256 / GRP), lane);
+      w4_load_scales<GRP>(sc2, p.sc, p.zp, srow, groups, (q + 2 * Sm::kTeams) * (256 / GRP) + qh);
       if (!mbar_wait(&sr->full[pos.at], pos.phase, &sr->abort)) sr->give_up(p.err);
       __syncwarp();
       const uint32_t st = ring_a + pos.at * Sm::kSlot;
-      stage_mma_w4<GRP, NT, ZERO, false>(st, st + kStageBytes, warp, lane, ntu, sc0, min(256, p.K - q * 256) / GRP,
-                                         acc);
+      stage_mma_w4<GRP, NT, ZERO, false>(st, st + kStageBytes, warp, lane, ntu, sc0, acc);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sr->empty[pos.at]);
       pos.skip(Sm::kTeams, Sm::NST);
@@ -173,60 +222,13 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     ring_pos.skip(chunks % Sm::NST, Sm::NST);
     ring_pos.phase ^= (chunks / Sm::NST) & 1;
     left -= chunks;
-    {
-#pragma unroll 1
-      for (int t = 0; t < Sm::kTeams; ++t) {  // the teams' sums, in a fixed order
-        if (team == t) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (nt < ntu) {
-              float* at = red + (nt * 8 + 2 * c) * RP + warp * 16 + r;
-              const float* v = acc[nt][0];
-              if (t == 0) {
-                at[0] = v[0]; at[RP] = v[1]; at[8] = v[2]; at[RP + 8] = v[3];
-              } else {
-                at[0] += v[0]; at[RP] += v[1]; at[8] += v[2]; at[RP + 8] += v[3];
-              }
-            }
-        }
-        bar_consumers<CT>();
-      }
-      const int n0 = s * kLinStrip;
-      if (strip_end && !begun_earlier) {  // the whole strip is this CTA's
-        for (int i = tid; i < p.M * kLinStrip; i += CT) {
-          const int row = i / kLinStrip, col = i % kLinStrip;
-          if (n0 + col < p.N) store_y(y, static_cast<size_t>(row) * p.N + n0 + col, red[row * RP + col]);
-        }
-      } else {
-        float* mine = p.part + (static_cast<size_t>(b) * 2 + (begun_earlier ? 0 : 1)) * p.M * kLinStrip;
-        for (int i = tid; i < p.M * kLinStrip; i += CT) mine[i] = red[i / kLinStrip * RP + i % kLinStrip];
-        __threadfence();
-        bar_consumers<CT>();
-        const long long q0 = static_cast<long long>(s) * C;
-        const int c0 = split_cta(sp, q0), c1 = split_cta(sp, q0 + C - 1);
-        if (tid == 0) {
-          const int last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
-          if (last) p.cnt[c0] = 0;
-          sr->last = last;
-        }
-        bar_consumers<CT>();
-        if (sr->last) {
-          __threadfence();
-          for (int i = tid; i < p.M * kLinStrip; i += CT) {
-            const int row = i / kLinStrip, n = n0 + i % kLinStrip;
-            if (n >= p.N) continue;
-            float v = __ldcg(p.part + (static_cast<size_t>(c0) * 2 + 1) * p.M * kLinStrip + i);
-            for (int cta = c0 + 1; cta <= c1; ++cta)
-              v += __ldcg(p.part + static_cast<size_t>(cta) * 2 * p.M * kLinStrip + i);
-            store_y(y, static_cast<size_t>(row) * p.N + n, v);
-          }
-        }
-      }
-      bar_consumers<CT>();  // before the next strip's sums overwrite red
-      begun_earlier = false;
-    }
-    kc = 0;
-    ++s;
+    add_sums<kStreamW4, GRP, NT, Sm::kTeams, RP>(red + rpos.at * (Sm::kRedBytes / 4), team, warp, lane, ntu, acc, [&]() {
+      if (!mbar_wait(&sr->red_empty[rpos.at], rpos.phase ^ 1u, &sr->abort)) sr->give_up(p.err);
+      __syncwarp();
+    });
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sr->red_full[rpos.at]);
+    rpos.next(2);
   }
   if (sr->aborted()) drain_grace();
 }

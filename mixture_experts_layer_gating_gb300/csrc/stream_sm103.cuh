@@ -14,8 +14,9 @@
 // Roles of a CTA: consumer warps in one or two teams of eight (two teams take
 // the stages in turn and add their sums at the end of a strip: twice the time
 // per stage for the latencies of a stage's loads, conversions and multiplies),
-// a producer warp (weights) and feeder warps (the token rows of a stage, put
-// beside its weights; the feeders take the stages in turn).
+// a producer warp (weights), feeder warps (the token rows of a stage, put
+// beside its weights; the feeders take the stages in turn) and a finisher warp
+// (a strip's sums to memory, so that its round trips delay no consumer).
 //
 // Operand types: bf16 weights are multiplied as bf16; e4m3 weights and 4-bit
 // codes (exact there) as fp16, by token rows that are fp16 times a power of
@@ -27,7 +28,8 @@
 //     warp w multiplies k 16 (w / 2) .. + 15 of half w % 2, so the four warps of
 //     a half hold partial sums of the same columns;
 //   [.., N, K] weights (e4m3, 4-bit): 64 output rows a half, 128 or 256
-//     consecutive k; warp w owns rows 16 w .. + 15 of the 128 and all the k.
+//     consecutive k; warp w owns rows 32 (w / 2) .. + 31 of the 128 and one half
+//     of the k (two 16-row tiles share the token rows that it loads).
 // The k order inside an mma is free as long as both operands use the same:
 // each layout takes the order in which a thread's 16-byte shared loads hold its
 // operand registers, and the token rows are stored in that order (perm_k).
@@ -58,7 +60,8 @@ struct StreamTraits {
   static constexpr bool KN = KIND == kStreamBf16 || KIND == kStreamFp8;
   static constexpr int KCH = KN ? 64 : (KIND == kStreamFp8Nk ? 128 : 256);  // k of a stage
   static constexpr int HC = KIND == kStreamFp8 ? 128 : 64;  // output columns of a half
-  static constexpr int MT = KN ? HC / 16 : 1;               // 16-column mma tiles of a warp
+  static constexpr int MT = KN ? HC / 16 : 2;               // 16-column mma tiles of a warp
+  static constexpr int KW = KN ? 4 : 2;  // warps of a team that hold sums of the same columns
   // bytes between token rows in shared memory: the padding makes a quarter-
   // (KN: half-) warp's loads of several rows fall on different banks
   static constexpr int PITCH = KCH * 2 + (KN ? 32 : 64);
@@ -163,9 +166,14 @@ __device__ __forceinline__ void bar_consumers() {
 // the team that took it is through.
 struct StreamRing {
   uint64_t full[kMaxStages], empty[kMaxStages];
+  // the two buffers of finished sums that the consumers hand to the finisher
+  uint64_t red_full[2], red_empty[2];
   int abort;
-  int last;  // of an arrival count (finish a shared strip)
-  __device__ void init() {
+  __device__ void init(int consumer_warps) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&red_full[i], consumer_warps);
+      mbar_init(&red_empty[i], 32);
+    }
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&full[i], 1 + 32);
       mbar_init(&empty[i], kStreamWarps);
@@ -313,158 +321,207 @@ __device__ __forceinline__ int nk_row(int g) {
   return (g >> 1) | ((g & 1) << 2);
 }
 
-// For few rows the k steps are summed in chains of their own, so that a warp has
-// several multiplies in flight; the chains are added at the end of the stage.
+// For few rows the two words of eight k are summed in chains of their own, so
+// that a warp has four multiplies in flight; the chains are added at the end.
 template <int NT>
 __device__ __forceinline__ void stage_mma_fp8nk(uint32_t stage, uint32_t rows, int warp, int lane, int ntu,
-                                                float (&acc)[NT][1][4]) {
+                                                float (&acc)[NT][2][4]) {
   using Tr = StreamTraits<kStreamFp8Nk, 0>;
-  constexpr int CH = NT == 1 ? 4 : NT == 2 ? 2 : 1;
-  const int g = lane >> 2, c = lane & 3;
+  constexpr int CH = NT == 1 ? 2 : 1;
+  const int g = lane >> 2, c = lane & 3, kh = warp & 1;
   const int r = nk_row<kStreamFp8Nk, 0>(g);
-  const uint32_t base = stage + (warp * 16 + r) * 128;
-  const uint32_t ba = rows + g * Tr::PITCH + c * 16;
-  float t[NT][CH][4];
+  const uint32_t base = stage + ((warp >> 1) * 32 + r) * 128 + (static_cast<uint32_t>((4 * kh + c) ^ r) << 4);
+  const uint32_t ba = rows + g * Tr::PITCH + kh * 128 + c * 16;
+  uint32_t w[2][2][4];  // [tile][row g, g + 8][word]
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int h = 0; h < CH; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t[nt][h][i] = h == 0 ? acc[nt][0][i] : 0.0f;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t xo = static_cast<uint32_t>((4 * i + c) ^ r) << 4;
-    const uint4 u = lds128(base + xo), v = lds128(base + 1024 + xo);
-    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+  for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t a[8];
+      const uint4 v = lds128(base + mt * 2048 + h * 1024);
+      w[mt][h][0] = v.x; w[mt][h][1] = v.y; w[mt][h][2] = v.z; w[mt][h][3] = v.w;
+    }
+  float t[NT][2][4];
+  if (CH == 2)
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        a[4 * w] = e4m3x2_to_f16x2<false>(uu[2 * h + w]);
-        a[4 * w + 1] = e4m3x2_to_f16x2<false>(vv[2 * h + w]);
-        a[4 * w + 2] = e4m3x2_to_f16x2<true>(uu[2 * h + w]);
-        a[4 * w + 3] = e4m3x2_to_f16x2<true>(vv[2 * h + w]);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[nt][mt][i] = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t a[2][8];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        a[mt][4 * u] = e4m3x2_to_f16x2<false>(w[mt][0][2 * h + u]);
+        a[mt][4 * u + 1] = e4m3x2_to_f16x2<false>(w[mt][1][2 * h + u]);
+        a[mt][4 * u + 2] = e4m3x2_to_f16x2<true>(w[mt][0][2 * h + u]);
+        a[mt][4 * u + 3] = e4m3x2_to_f16x2<true>(w[mt][1][2 * h + u]);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (nt < ntu) {
-          const uint4 b = lds128(ba + nt * 8 * Tr::PITCH + (2 * i + h) * 64);
-          mma_16816<true>(t[nt][(2 * h) % CH], a[0], a[1], a[2], a[3], b.x, b.y);
-          mma_16816<true>(t[nt][(2 * h + 1) % CH], a[4], a[5], a[6], a[7], b.z, b.w);
+    for (int nt = 0; nt < NT; ++nt)
+      if (nt < ntu) {
+        const uint4 b = lds128(ba + nt * 8 * Tr::PITCH + h * 64);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          mma_16816<true>(acc[nt][mt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b.x, b.y);
+          if (CH == 2) mma_16816<true>(t[nt][mt], a[mt][4], a[mt][5], a[mt][6], a[mt][7], b.z, b.w);
+          else mma_16816<true>(acc[nt][mt], a[mt][4], a[mt][5], a[mt][6], a[mt][7], b.z, b.w);
         }
-    }
+      }
   }
+  if (CH == 2)
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v = t[nt][0][i];
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int h = 1; h < CH; ++h) v += t[nt][h][i];
-      acc[nt][0][i] = v;
-    }
+        for (int i = 0; i < 4; ++i) acc[nt][mt][i] += t[nt][mt][i];
 }
 
-// Group scales (bf16 bits, zero point in the upper half) of a warp's 16 rows
-// for one 256-k stage, spread over the four lanes of a row pair: lane c holds
-// groups 2 i + c / 2 (slot i) of mma row g (even c) or g + 8 (odd c).
+// Group scales (bf16 bits, zero point in the upper half) of a warp's 32 rows and
+// half of the k of one 256-k stage: lane c of a quad holds those of mma row g
+// (even c) or g + 8 (odd c) of tile c / 2, a slot for each group.
 template <int GRP>
 struct W4Scales {
-  static constexpr int kSlots = 256 / GRP / 2;
+  static constexpr int kSlots = 128 / GRP;
   uint32_t v[kSlots];
 };
 // `at`: index of the lane's row's first group (-1: a row outside the matrix),
-// groups = groups of a row; q0 = the stage's first group.
+// groups = groups of a row; q0 = the first group.
 template <int GRP>
 __device__ __forceinline__ void w4_load_scales(W4Scales<GRP>& s, const __nv_bfloat16* sc, const uint8_t* zp,
-                                               long long at, int groups, int q0, int lane) {
-  q0 += (lane & 3) >> 1;
+                                               long long at, int groups, int q0) {
 #pragma unroll
   for (int i = 0; i < W4Scales<GRP>::kSlots; ++i) {
     uint32_t w = 8u << 16;
-    if (at >= 0 && q0 + 2 * i < groups) {
-      const long long j = at + q0 + 2 * i;
-      w = __ldg(reinterpret_cast<const unsigned short*>(sc) + j) |
-          (zp ? static_cast<uint32_t>(__ldg(zp + j) & 15u) << 16 : 8u << 16);
+    if (at >= 0 && q0 + i < groups) {
+      w = __ldg(reinterpret_cast<const unsigned short*>(sc) + at + q0 + i) |
+          (zp ? static_cast<uint32_t>(__ldg(zp + at + q0 + i) & 15u) << 16 : 8u << 16);
     }
     s.v[i] = w;
   }
 }
 
+// (Groups beyond the end of a row have scale 0 and zero token rows.)
 template <int GRP, int NT, bool ZERO, bool F16>
 __device__ __forceinline__ void stage_mma_w4(uint32_t stage, uint32_t rows, int warp, int lane, int ntu,
-                                             const W4Scales<GRP>& sc, int groups_here,
-                                             float (&acc)[NT][1][4]) {
+                                             const W4Scales<GRP>& sc, float (&acc)[NT][2][4]) {
   static_assert(!(ZERO && F16), "zero points come with bf16 operands");
   using Tr = StreamTraits<kStreamW4, GRP>;
-  constexpr int J = GRP / 32, QB = 256 / GRP;
-  constexpr int CH = NT == 1 ? 2 : 1;
-  const int g = lane >> 2, c = lane & 3;
+  constexpr int J = GRP / 32, QB = 128 / GRP;
+  constexpr int CH = NT == 1 ? 2 : 1;  // for few rows: two chains of multiplies a tile
+  const int g = lane >> 2, c = lane & 3, kh = warp & 1;
   const int r = nk_row<kStreamW4, GRP>(g);
-  const uint32_t base = stage + (warp * 16 + r) * 128;
-  const uint32_t ba = rows + g * Tr::PITCH + c * 16;
+  const uint32_t base = stage + ((warp >> 1) * 32 + r) * 128;
+  const uint32_t ba = rows + g * Tr::PITCH + kh * 256 + c * 16;
+  const int from = lane & ~3;
 #pragma unroll
   for (int q = 0; q < QB; ++q) {
-    if (q >= groups_here) break;
-    uint32_t wa[J], wb[J];
-    if constexpr (GRP == 128) {
-      const uint32_t xo = static_cast<uint32_t>((4 * q + c) ^ (r & 7)) << 4;
-      const uint4 u = lds128(base + xo), v = lds128(base + 1024 + xo);
-      wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
-      wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
-    } else if constexpr (GRP == 64) {
-      const uint32_t xo = (static_cast<uint32_t>((2 * q + (c >> 1)) ^ (r & 7)) << 4) + (c & 1) * 8;
-      const uint2 u = lds64(base + xo), v = lds64(base + 1024 + xo);
-      wa[0] = u.x; wa[1] = u.y;
-      wb[0] = v.x; wb[1] = v.y;
-    } else {
-      const uint32_t xo = (static_cast<uint32_t>(q ^ (r & 7)) << 4) + c * 4;
-      wa[0] = lds32(base + xo);
-      wb[0] = lds32(base + 1024 + xo);
-    }
-    const int from = (lane & ~3);
-    const uint32_t s0 = __shfl_sync(0xffffffffu, sc.v[q >> 1], from | ((2 * q) & 3));
-    const uint32_t s1 = __shfl_sync(0xffffffffu, sc.v[q >> 1], from | ((2 * q + 1) & 3));
-    uint32_t z0 = 0x43084308u, z1 = 0x43084308u;  // 128 + 8
-    if (ZERO) {
-      z0 = s0 >> 16;
-      z1 = s1 >> 16;
-      z0 = 0x43004300u | z0 | (z0 << 16);
-      z1 = 0x43004300u | z1 | (z1 << 16);
-    }
-    // for few rows the two halves of a word are summed in chains of their own
-    float part[NT][CH][4];
+    uint32_t w[2][2][J];  // [tile][row g, g + 8][word]
+    const int qq = kh * QB + q;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = base + mt * 2048 + h * 1024;
+        if constexpr (GRP == 128) {
+          const uint4 u = lds128(at + (static_cast<uint32_t>((4 * qq + c) ^ (r & 7)) << 4));
+          w[mt][h][0] = u.x; w[mt][h][1] = u.y; w[mt][h][2] = u.z; w[mt][h][3] = u.w;
+        } else if constexpr (GRP == 64) {
+          const uint2 u = lds64(at + (static_cast<uint32_t>((2 * qq + (c >> 1)) ^ (r & 7)) << 4) + (c & 1) * 8);
+          w[mt][h][0] = u.x; w[mt][h][1] = u.y;
+        } else {
+          w[mt][h][0] = lds32(at + (static_cast<uint32_t>(qq ^ (r & 7)) << 4) + c * 4);
+        }
+      }
+    float f[2][2];
+    uint32_t z[2][2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t v = __shfl_sync(0xffffffffu, sc.v[q], from | (2 * mt + h));
+        f[mt][h] = __uint_as_float(v << 16);
+        z[mt][h] = ZERO ? 0x43004300u | (v >> 16) | (v & 0xffff0000u) : 0x43084308u;  // 128 + zero point
+      }
+    float part[NT][2][CH][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int h = 0; h < CH; ++h)
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[nt][h][i] = 0.0f;
+        for (int h = 0; h < CH; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[nt][mt][h][i] = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      uint32_t a[4], b[4];
-      w4_pairs<F16>(wa[j], z0, a);
-      w4_pairs<F16>(wb[j], z1, b);
+      uint32_t a[2][4], b[2][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        w4_pairs<F16>(w[mt][0][j], z[mt][0], a[mt]);
+        w4_pairs<F16>(w[mt][1][j], z[mt][1], b[mt]);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         if (nt < ntu) {
           const uint4 x = lds128(ba + nt * 8 * Tr::PITCH + (q * J + j) * 64);
-          mma_16816<F16>(part[nt][0], a[0], b[0], a[1], b[1], x.x, x.y);
-          mma_16816<F16>(part[nt][CH - 1], a[2], b[2], a[3], b[3], x.z, x.w);
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            mma_16816<F16>(part[nt][mt][0], a[mt][0], b[mt][0], a[mt][1], b[mt][1], x.x, x.y);
+            mma_16816<F16>(part[nt][mt][CH - 1], a[mt][2], b[mt][2], a[mt][3], b[mt][3], x.z, x.w);
+          }
         }
     }
-    const float f0 = __uint_as_float(s0 << 16), f1 = __uint_as_float(s1 << 16);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
       if (nt < ntu) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = part[nt][0][i];
-          if (CH == 2) v += part[nt][CH - 1][i];
-          acc[nt][0][i] = fmaf(i < 2 ? f0 : f1, v, acc[nt][0][i]);
-        }
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = part[nt][mt][0][i];
+            if (CH == 2) v += part[nt][mt][CH - 1][i];
+            acc[nt][mt][i] = fmaf(f[mt][i >> 1], v, acc[nt][mt][i]);
+          }
       }
+  }
+}
+
+// A team's sums into red[row][columns] (RP floats a row): the KW warps of a team
+// that hold sums of the same columns, and the teams, add theirs one after
+// another, in a fixed order.  `before_first` runs before anything is written.
+template <int KIND, int GRP, int NT, int TEAMS, int RP, typename WAIT>
+__device__ __forceinline__ void add_sums(float* red, int team, int warp, int lane, int ntu,
+                                         const float (&acc)[NT][StreamTraits<KIND, GRP>::MT][4], WAIT before_first) {
+  using Tr = StreamTraits<KIND, GRP>;
+  const int g = lane >> 2, c = lane & 3;
+  const int mine = team * Tr::KW + (Tr::KN ? warp >> 1 : warp & 1);
+  if (mine == 0) before_first();
+#pragma unroll 1
+  for (int r = 0; r < Tr::KW * TEAMS; ++r) {
+    if (r > 0) bar_consumers<32 * kStreamWarps * TEAMS>();
+    if (mine == r) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (nt < ntu) {
+#pragma unroll
+          for (int mt = 0; mt < Tr::MT; ++mt) {
+            const int col = Tr::KN ? (warp & 1) * Tr::HC + kn_col<KIND>(lane, mt)
+                                   : (warp >> 1) * 32 + mt * 16 + nk_row<KIND, GRP>(g);
+            constexpr int step = Tr::KN ? 1 : 8;  // column of v[2..3] after that of v[0..1]
+            float* at = red + (nt * 8 + 2 * c) * RP + col;
+            const float* v = acc[nt][mt];
+            if (r == 0) {
+              at[0] = v[0]; at[RP] = v[1]; at[step] = v[2]; at[RP + step] = v[3];
+            } else {
+              at[0] += v[0]; at[RP] += v[1]; at[step] += v[2]; at[RP + step] += v[3];
+            }
+          }
+        }
+    }
   }
 }
 
