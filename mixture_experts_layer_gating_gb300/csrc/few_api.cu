@@ -21,10 +21,10 @@ struct FewGeom {
 };
 FewGeom few_geom(int w_dtype) {
   switch (w_dtype) {
-    case MOE_BF16: return {64, 64};
-    case MOE_FP8_E4M3: return {64, 128};
-    case MOE_FP8_E4M3_NK: return {128, 64};
-    default: return {256, 64};
+    case MOE_BF16: return {StreamTraits<kStreamBf16, 0>::KCH, StreamTraits<kStreamBf16, 0>::HC};
+    case MOE_FP8_E4M3: return {StreamTraits<kStreamFp8, 0>::KCH, StreamTraits<kStreamFp8, 0>::HC};
+    case MOE_FP8_E4M3_NK: return {StreamTraits<kStreamFp8Nk, 0>::KCH, StreamTraits<kStreamFp8Nk, 0>::HC};
+    default: return {StreamTraits<kStreamW4, 32>::KCH, StreamTraits<kStreamW4, 32>::HC};
   }
 }
 

@@ -29,6 +29,11 @@ namespace moe {
 
 constexpr int kFewMaxPlanes = 16;
 constexpr int kFewMaxR = 512;  // expanded rows: 32 tokens, 16 experts each
+// Most rows of one expert that a pass over its weights multiplies; an expert with
+// more rows (the shared one above 16 tokens) is listed twice and streamed twice.
+// Accumulators for 32 rows would leave room for one consumer team only, which
+// costs every expert more than the few long ones gain.
+constexpr int kFewGroup = 16;
 // Up to this many bytes of router planes every CTA reads them all (152 x 64 KB
 // from L2 take about as long as one more barrier).
 constexpr int kFewPlaneBytes = 65536;
@@ -67,12 +72,14 @@ __device__ __forceinline__ float few_act(float g, float u, int act) {
   return 0.5f * g * (1.0f + tanhf(c * (g + 0.044715f * g * g * g))) * u;
 }
 
-// One pass over weights: the shared expert's strips, then the chosen experts',
-// every strip C chunks (stages) long; this CTA's run of the chunks.  Index 0 of
+// One pass over weights: the shared expert's strips, then the chosen experts'
+// (entry by entry), every strip C chunks (stages) long; this CTA's run of the
+// chunks.  Index 0 of
 // S, C, K, width: the shared expert, 1: the routed ones.
 struct FewPass {
   Split sp;
-  long long lo, hi, shared;  // shared: chunks of the shared expert
+  long long lo, hi, shared;  // shared: chunks of the shared expert (all its entries)
+  int shared_entries;
   int S[2], C[2];            // strips of an expert, chunks of a strip
   int K[2], width[2];        // the reduction, the output columns (of gate and up each)
 };
@@ -80,7 +87,7 @@ template <int KIND, int GRP, int NT>
 struct FewSmem {
   using Tr = StreamTraits<KIND, GRP>;
   // Two consumer teams where the accumulators leave room (at most 96 registers a thread)
-  static constexpr int kTeams = KIND == kStreamFp8 ? (NT == 1 ? 2 : 1) : (NT <= 2 ? 2 : 1);
+  static constexpr int kTeams = KIND == kStreamFp8 && NT == 2 ? 1 : 2;
   static constexpr int kCons = 32 * kStreamWarps * kTeams;  // consumer threads
   static constexpr int kFeeders = 2;                        // feeder warps
   static constexpr int kBlock = kCons + 32 + 32 * kFeeders + 32;  // + producer, feeders, finisher: 12 or 20 warps
@@ -90,23 +97,24 @@ struct FewSmem {
   static constexpr int kSlot = stream_slot(kRows);
   static constexpr int kRP = 2 * Tr::HC + 4;  // floats per row of red
   // the router's partial sums take kPlanes planes of red
-  static constexpr int kPlanes = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+  static constexpr int kPlanes = NT == 1 ? 4 : 2;
   static constexpr int kRedBytes = 8 * NT * 4 * (kRP > 68 * kPlanes ? kRP : 68 * kPlanes);
+  static constexpr int kRedBufs = kRedBytes > 20000 ? 1 : 2;
   struct Ctrl {
     StreamRing ring;
     int na;
-    int last;               // of an arrival count
     FewPass pass[2];        // gate/up, down
     int cnt[512];           // rows of an expert
     int ids[kFewMaxR];      // expert of an expanded row
     float w[kFewMaxR];      // its weight
-    uint16_t aexp[512];     // active experts, ascending
-    uint16_t aoff[513];     // first sorted position of an active expert
-    uint16_t amap[512];     // expert -> its index among the active
+    // the chosen experts in ascending order, one entry for each group of 16 rows
+    uint16_t aexp[512];     // expert of an entry
+    uint16_t aoff[513];     // its first sorted position
+    uint16_t amap[512];     // expert -> its first entry
     uint16_t srow[kFewMaxR + kStreamMaxRows];  // token of a row (routed in sorted order, then shared)
     uint16_t pos[kFewMaxR];   // sorted position of an expanded row
   };
-  static constexpr int kOther = 2 * kRedBytes + static_cast<int>(sizeof(Ctrl)) + 16;
+  static constexpr int kOther = kRedBufs * kRedBytes + static_cast<int>(sizeof(Ctrl)) + 16;
   static constexpr int NST = stream_stages(kSlot, kOther);
   static constexpr int kBytes = 1024 + NST * kSlot + kOther;
   static_assert(NST >= 4 && NST % kFeeders == 0, "ring sizes");
@@ -126,14 +134,15 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
     f.S[r] = (f.width[r] + per - 1) / per;
     f.C[r] = (f.K[r] + Tr::KCH - 1) / Tr::KCH;
   }
-  f.shared = p.Is > 0 ? static_cast<long long>(f.S[0]) * f.C[0] : 0;
+  f.shared_entries = p.Is > 0 ? (p.T + kFewGroup - 1) / kFewGroup : 0;
+  f.shared = static_cast<long long>(f.shared_entries) * f.S[0] * f.C[0];
   f.sp = make_split(f.shared + static_cast<long long>(na) * f.S[1] * f.C[1], G);
   f.lo = split_lo(f.sp, b);
   f.hi = split_lo(f.sp, b + 1);
   return f;
 }
-// A chunk's place: shared (r 0) or routed (r 1) expert, active expert, strip,
-// chunk of the strip.
+// A chunk's place: shared (r 0) or routed (r 1) expert, entry, strip, chunk of
+// the strip.
 struct FewAt {
   int r, a, s, kc;
   __device__ __forceinline__ FewAt(const FewPass& f, long long q) {
@@ -155,8 +164,10 @@ struct FewAt {
     kc = 0;
     if (++s == f.S[r]) {
       s = 0;
-      if (r) ++a;
-      r = 1;
+      if (++a == f.shared_entries && !r) {
+        r = 1;
+        a = 0;
+      }
     }
   }
   __device__ __forceinline__ void next(const FewPass& f) {
@@ -172,13 +183,13 @@ struct Few {
   static constexpr int CT = Sm::kCons;
 
   static __device__ __forceinline__ void bar() { bar_consumers<CT>(); }
-  // An expert's rows: the first one's place in the row arrays (routed rows in
+  // An entry's rows: the first one's place in the row arrays (routed rows in
   // sorted order, then the shared expert's), and how many.
   static __device__ __forceinline__ int row_first(const FewParams& p, const Ctrl* ctl, const FewAt& at) {
-    return at.r ? ctl->aoff[at.a] : p.T * p.k;
+    return at.r ? ctl->aoff[at.a] : p.T * p.k + at.a * kFewGroup;
   }
   static __device__ __forceinline__ int row_count(const FewParams& p, const Ctrl* ctl, const FewAt& at) {
-    return at.r ? ctl->aoff[at.a + 1] - ctl->aoff[at.a] : p.T;
+    return at.r ? ctl->aoff[at.a + 1] - ctl->aoff[at.a] : min(kFewGroup, p.T - at.a * kFewGroup);
   }
 
   // Grid barrier i, by the consumers.  One CTA clears the arrivals of `clear`,
@@ -220,11 +231,11 @@ struct Few {
       const int e = at.r ? ctl->aexp[at.a] : 0;
       mbar_arrive_expect_tx(full, kStageBytes);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint8_t* d = dst + h * kHalfBytes;
+      for (int h = 0; h < Tr::BOXES; ++h) {
+        uint8_t* d = dst + h * (kStageBytes / Tr::BOXES);
         if (Tr::KN) {
-          if (DOWN) tma_load_3d(d, m, full, at.s * 2 * Tr::HC + h * Tr::HC, at.kc * Tr::KCH, e, policy);
-          else tma_load_4d(d, m, full, at.s * Tr::HC, h, at.kc * Tr::KCH, e, policy);
+          if (DOWN) tma_load_3d(d, m, full, at.s * 2 * Tr::HC + h * Tr::QC, at.kc * Tr::KCH, e, policy);
+          else tma_load_4d(d, m, full, at.s * Tr::HC + (h & 1) * Tr::QC, h >> 1, at.kc * Tr::KCH, e, policy);
         } else {
           if (DOWN) tma_load_3d(d, m, full, at.kc * 128, at.s * 128 + h * 64, e, policy);
           else tma_load_4d(d, m, full, at.kc * 128, at.s * 64, h, e, policy);
@@ -242,15 +253,18 @@ struct Few {
   static __device__ __forceinline__ void prefetch_shared(const FewParams& p, const CUtensorMap* m, int b, int G,
                                                          int most) {
     FewPass f = few_pass<KIND, GRP>(p, DOWN, 0, G, b);
+    f.sp = make_split(static_cast<long long>(f.S[0]) * f.C[0], G);
+    f.lo = split_lo(f.sp, b);
+    f.hi = split_lo(f.sp, b + 1);
     if (f.lo >= f.hi) return;
     FewAt at(f, f.lo);
 #pragma unroll 1
     for (int left = min(most, static_cast<int>(f.hi - f.lo)); left > 0; --left) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < Tr::BOXES; ++h) {
         if (Tr::KN) {
-          if (DOWN) tma_prefetch_l2_3d(m, at.s * 2 * Tr::HC + h * Tr::HC, at.kc * Tr::KCH, 0);
-          else tma_prefetch_l2_4d(m, at.s * Tr::HC, h, at.kc * Tr::KCH, 0);
+          if (DOWN) tma_prefetch_l2_3d(m, at.s * 2 * Tr::HC + h * Tr::QC, at.kc * Tr::KCH, 0);
+          else tma_prefetch_l2_4d(m, at.s * Tr::HC + (h & 1) * Tr::QC, h >> 1, at.kc * Tr::KCH, 0);
         } else {
           if (DOWN) tma_prefetch_l2_3d(m, at.kc * 128, at.s * 128 + h * 64, 0);
           else tma_prefetch_l2_4d(m, at.kc * 128, at.s * 64, h, 0);
@@ -455,9 +469,9 @@ struct Few {
       last = __shfl_sync(0xffffffffu, last, 0);
     } else {
       bar();
-      if (i0 == 0) ctl->last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+      if (i0 == 0) ctl->ring.last[1] = atomicAdd(p.cnt + c0, 1) == c1 - c0;
       bar();
-      last = ctl->last;
+      last = *reinterpret_cast<volatile int*>(&ctl->ring.last[1]);
     }
     if (!last) return;
     __threadfence();
@@ -501,7 +515,7 @@ struct Few {
       finish_strip<DOWN, 32>(p, f, ctl, red0 + rpos.at * (Sm::kRedBytes / 4), at, end, f.hi - left - end, b, lane);
       __syncwarp();
       mbar_arrive(&ctl->ring.red_empty[rpos.at]);
-      rpos.next(2);
+      rpos.next(Sm::kRedBufs);
       at.next_strip(f);
     }
   }
@@ -592,7 +606,7 @@ struct Few {
       if (left > 0) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->ring.red_full[rpos.at]);
-        rpos.next(2);
+        rpos.next(Sm::kRedBufs);
         at.next_strip(f);
       } else {  // the run's last strip: by all consumers, which have nothing else to do
         bar();
@@ -669,7 +683,7 @@ struct Few {
     for (int i = 0; i < per; ++i) {
       const int e = lane * per + i, n = e < p.E ? ctl->cnt[e] : 0;
       rows += n;
-      act += n > 0;
+      act += (n + kFewGroup - 1) / kFewGroup;
     }
     int ir = rows, ia = act;
 #pragma unroll
@@ -688,13 +702,13 @@ struct Few {
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
       const int e = lane * per + i, n = e < p.E ? ctl->cnt[e] : 0;
-      if (n > 0) {
+      if (n > 0) ctl->amap[e] = static_cast<uint16_t>(ao);
+      for (int i0 = 0; i0 < n; i0 += kFewGroup) {
         ctl->aexp[ao] = static_cast<uint16_t>(e);
-        ctl->aoff[ao] = static_cast<uint16_t>(ro);
-        ctl->amap[e] = static_cast<uint16_t>(ao);
-        ro += n;
+        ctl->aoff[ao] = static_cast<uint16_t>(ro + i0);
         ++ao;
       }
+      ro += n;
     }
     __syncwarp();
 #pragma unroll 1
@@ -706,9 +720,9 @@ struct Few {
     if (lane < p.T) ctl->srow[R + lane] = static_cast<uint16_t>(lane);
   }
 
-  // The router's planes.  A unit is 64 experts x one slice of D; its k16 steps
+  // The router's planes of tokens t0 .. t0 + 8 NT - 1.  A unit is 64 experts x one slice of D; its k16 steps
   // go round the CTA's warps, two at a time.
-  static __device__ __forceinline__ void router(const FewParams& p, float* red, int b, int G) {
+  static __device__ __forceinline__ void router(const FewParams& p, float* red, int b, int G, int t0) {
     constexpr int NW = CT / 32, PL = Sm::kPlanes, PW = 8 * NT * 68;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, c = lane & 3;
     const int SE = (p.E + 63) / 64, steps = (p.D + 15) / 16;
@@ -754,7 +768,7 @@ struct Few {
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const int t = nt * 8 + g, k = k0 + 2 * c;
+            const int t = t0 + nt * 8 + g, k = k0 + 2 * c;
             x[h][nt][0] = x[h][nt][1] = 0u;
             if (t < p.T) {
               const __nv_bfloat16* src = p.x + static_cast<size_t>(t) * p.D + k;
@@ -796,12 +810,12 @@ struct Few {
         bar();
       }
 #pragma unroll 1
-      for (int i = tid; i < p.T * 64; i += CT) {
+      for (int i = tid; i < min(8 * NT, p.T - t0) * 64; i += CT) {
         const int t = i >> 6, e = se * 64 + (i & 63);
         float v = red[t * 68 + (i & 63)];
 #pragma unroll
         for (int q = 1; q < PL; ++q) v += red[q * PW + t * 68 + (i & 63)];
-        if (e < p.E) p.planes[(static_cast<size_t>(pl) * p.T + t) * p.E + e] = v;
+        if (e < p.E) p.planes[(static_cast<size_t>(pl) * p.T + t0 + t) * p.E + e] = v;
       }
       bar();
     }
@@ -867,7 +881,7 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* red = reinterpret_cast<float*>(ring + Sm::NST * Sm::kSlot);
-  Ctrl* ctl = reinterpret_cast<Ctrl*>(ring + Sm::NST * Sm::kSlot + 2 * Sm::kRedBytes);
+  Ctrl* ctl = reinterpret_cast<Ctrl*>(ring + Sm::NST * Sm::kSlot + Sm::kRedBufs * Sm::kRedBytes);
   StreamRing* sr = &ctl->ring;
   const int tid = threadIdx.x, b = blockIdx.x, G = gridDim.x, lane = tid & 31;
   const int R = p.T * p.k;
@@ -922,7 +936,8 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   if (Tr::F16)
     for (int r = b * CT + tid; r < R + p.T; r += G * CT) p.hmax[r] = 0;
   // phase 0
-  F::router(p, red, b, G);
+#pragma unroll 1
+  for (int t0 = 0; t0 < p.T; t0 += 8 * NT) F::router(p, red, b, G, t0);
   F::stage_x(p, red, b, G);
   F::grid_sync(p, sr, 0, 3);
 
@@ -986,12 +1001,15 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
       float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int j = l; j < terms; j += 8) {
         const bool rt = j < p.k;
-        const int e = rt ? ctl->ids[t * p.k + j] : 0, a = rt ? ctl->amap[e] : 0;
-        const int r = rt ? ctl->pos[t * p.k + j] : R + t, sl = rt ? r - ctl->aoff[a] : t;
+        // the row, its entry, its place among the entry's rows
+        const int e = rt ? ctl->ids[t * p.k + j] : 0;
+        const int r = rt ? ctl->pos[t * p.k + j] : R + t;
+        const int at = rt ? r - ctl->aoff[ctl->amap[e]] : t;  // among the expert's rows
+        const int a = (rt ? ctl->amap[e] : 0) + at / kFewGroup, sl = at % kFewGroup;
         float w = rt ? ctl->w[t * p.k + j] : 1.0f;
         if constexpr (Tr::F16) w *= F::exp2_int(-F::row_exp(__ldcg(p.hmax + r)));
         const int C = dn.C[rt];
-        const long long q0 = rt ? dn.shared + (static_cast<long long>(a) * dn.S[1] + s) * C : static_cast<long long>(s) * C;
+        const long long q0 = (rt ? dn.shared : 0) + (static_cast<long long>(a) * dn.S[rt] + s) * C;
         float4 y = __ldcg(reinterpret_cast<const float4*>(p.prim + static_cast<size_t>(r) * p.W +
                                                           static_cast<size_t>(s) * 2 * Tr::HC + col));
         const int c0 = split_cta(dn.sp, q0), c1 = split_cta(dn.sp, q0 + C - 1);
@@ -1043,16 +1061,16 @@ bool few_maps(const void* W13, const void* W2, int G, int D, int I, CUtensorMap&
     const uint64_t eb = KIND == kStreamBf16 ? 2 : 1;
     const auto dt = KIND == kStreamBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const uint64_t d13[4] = {n, 2, d, g}, t13[3] = {n * eb, 2 * n * eb, d * 2 * n * eb};
-    const uint32_t b13[4] = {Tr::HC, 1, 64, 1};
+    const uint32_t b13[4] = {Tr::QC, 1, Tr::BOX_ROWS, 1};
     const uint64_t d2[3] = {d, n, g}, t2[2] = {d * eb, n * d * eb};
-    const uint32_t b2[3] = {Tr::HC, 64, 1};
+    const uint32_t b2[3] = {Tr::QC, Tr::BOX_ROWS, 1};
     return encode_tmap(&m13, W13, 4, d13, t13, b13, dt) && encode_tmap(&m2, W2, 3, d2, t2, b2, dt);
   }
   const uint64_t kb = KIND == kStreamFp8Nk ? d : d / 2, nb = KIND == kStreamFp8Nk ? n : n / 2;
   const uint64_t d13[4] = {kb, n, 2, g}, t13[3] = {kb, n * kb, 2 * n * kb};
-  const uint32_t b13[4] = {128, 64, 1, 1};
+  const uint32_t b13[4] = {128, Tr::BOX_ROWS, 1, 1};
   const uint64_t d2[3] = {nb, d, g}, t2[2] = {nb, d * nb};
-  const uint32_t b2[3] = {128, 64, 1};
+  const uint32_t b2[3] = {128, Tr::BOX_ROWS, 1};
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return encode_tmap(&m13, W13, 4, d13, t13, b13, u8) && encode_tmap(&m2, W2, 3, d2, t2, b2, u8);
 }
@@ -1096,8 +1114,7 @@ cudaError_t launch_few_nt(const FewArgs& a, cudaStream_t s) {
 template <int KIND, int GRP>
 cudaError_t launch_few_kind(const FewArgs& a, cudaStream_t s) {
   if (a.p.T <= 8) return launch_few_nt<KIND, GRP, 1>(a, s);
-  if (a.p.T <= 16) return launch_few_nt<KIND, GRP, 2>(a, s);
-  return launch_few_nt<KIND, GRP, 4>(a, s);
+  return launch_few_nt<KIND, GRP, 2>(a, s);
 }
 
 cudaError_t launch_few_bf16(const FewArgs& a, cudaStream_t s);

@@ -40,10 +40,78 @@ __device__ __forceinline__ void store_y(__nv_bfloat16* y, size_t at, float v) {
   y[at] = __float2bfloat16_rn(v);
 }
 
-// Strips of 128 output features x stages of 256 k, divided into equal runs
-// over the CTAs.  A strip inside one CTA's run is written at once; one that
-// several CTAs share gets its parts added, in the order of k, by the CTA that
-// finishes last (an arrival count per CTA that begins a shared strip).
+// One strip's sums (or this CTA's part of them) to y by THREADS threads: the
+// finisher warp, or all consumers.  A strip inside one CTA's run is written at
+// once; one that several CTAs share gets its parts added, in the order of k, by
+// the CTA that arrives last (a count for each CTA that begins a shared strip).
+template <int THREADS, typename TY>
+__device__ __noinline__ void lin_finish(const LinParams& p, const Split& sp, const float* sums, int RP, int s, int kc,
+                                        int end, int C, int b, int i0, int* flag) {
+  TY* y = static_cast<TY*>(p.y);
+  const int n0 = s * kLinStrip, items = p.M * kLinStrip;
+  if (end == C && kc == 0) {
+#pragma unroll 4
+    for (int i = i0; i < items; i += THREADS) {
+      const int row = i / kLinStrip, col = i % kLinStrip;
+      if (n0 + col < p.N) store_y(y, static_cast<size_t>(row) * p.N + n0 + col, sums[row * RP + col]);
+    }
+    return;
+  }
+  float* mine = p.part + (static_cast<size_t>(b) * 2 + (kc ? 0 : 1)) * items;
+#pragma unroll 4
+  for (int i = i0; i < items; i += THREADS) mine[i] = sums[i / kLinStrip * RP + i % kLinStrip];
+  const long long q0 = static_cast<long long>(s) * C;
+  const int c0 = split_cta(sp, q0), c1 = split_cta(sp, q0 + C - 1);
+  int last = 0;
+  __threadfence();
+  if (THREADS == 32) __syncwarp();
+  else bar_consumers<THREADS>();
+  if (i0 == 0) {
+    last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+    if (last) p.cnt[c0] = 0;
+    *flag = last;
+  }
+  if (THREADS == 32) {
+    last = __shfl_sync(0xffffffffu, last, 0);
+  } else {
+    bar_consumers<THREADS>();
+    last = *reinterpret_cast<volatile int*>(flag);
+  }
+  if (!last) return;
+  __threadfence();
+  const float* head = p.part + (static_cast<size_t>(c0) * 2 + 1) * items;
+  const float* rest = p.part + static_cast<size_t>(c0 + 1) * 2 * items;
+  constexpr int U = 4;
+#pragma unroll 1
+  for (int i = i0; i < items; i += U * THREADS) {
+    float v[U], w[U], x[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int o = i + j * THREADS;
+      v[j] = w[j] = x[j] = 0.0f;
+      if (o < items) {
+        v[j] = __ldcg(head + o);
+        w[j] = __ldcg(rest + o);
+        if (c1 > c0 + 1) x[j] = __ldcg(rest + 2 * items + o);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) v[j] = v[j] + w[j] + x[j];
+#pragma unroll 1
+    for (int cta = c0 + 3; cta <= c1; ++cta)
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (i + j * THREADS < items) v[j] += __ldcg(rest + static_cast<size_t>(cta - c0 - 1) * 2 * items + i + j * THREADS);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int o = i + j * THREADS, n = n0 + o % kLinStrip;
+      if (o < items && n < p.N) store_y(y, static_cast<size_t>(o / kLinStrip) * p.N + n, v[j]);
+    }
+  }
+}
+
+// Strips of 128 output features x stages of 256 k, divided into equal runs over
+// the CTAs.
 template <int GRP, int NT, bool ZERO, typename TY>
 __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     linear_w4_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ LinParams p) {
@@ -65,50 +133,17 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
   pdl_launch_dependents();
   int s = static_cast<int>(lo / C), kc = static_cast<int>(lo % C);
 
-  if (tid >= CT + 32 + 32 * Sm::kFeeders) {  // finisher: a strip's sums to y
-    TY* y = static_cast<TY*>(p.y);
+  if (tid >= CT + 32 + 32 * Sm::kFeeders) {  // finisher: every strip but the run's last
     RingPos rpos;
-    bool begun_earlier = kc != 0;
+    int left = static_cast<int>(hi - lo);
 #pragma unroll 1
-    for (int left = static_cast<int>(hi - lo); left > 0; kc = 0, ++s, begun_earlier = false) {
-      const int chunks = min(C - kc, left), end = kc + chunks, n0 = s * kLinStrip;
+    for (; left > 0; kc = 0, ++s) {
+      const int chunks = min(C - kc, left);
       left -= chunks;
-      const float* sums = red + rpos.at * (Sm::kRedBytes / 4);
+      if (left == 0) break;
       if (!mbar_wait(&sr->red_full[rpos.at], rpos.phase, &sr->abort)) sr->give_up(p.err);
       __syncwarp();
-      if (end == C && !begun_earlier) {  // the whole strip is this CTA's
-#pragma unroll 4
-        for (int i = lane; i < p.M * kLinStrip; i += 32) {
-          const int row = i / kLinStrip, col = i % kLinStrip;
-          if (n0 + col < p.N) store_y(y, static_cast<size_t>(row) * p.N + n0 + col, sums[row * RP + col]);
-        }
-      } else {
-        float* mine = p.part + (static_cast<size_t>(b) * 2 + (begun_earlier ? 0 : 1)) * p.M * kLinStrip;
-#pragma unroll 4
-        for (int i = lane; i < p.M * kLinStrip; i += 32) mine[i] = sums[i / kLinStrip * RP + i % kLinStrip];
-        const long long q0 = static_cast<long long>(s) * C;
-        const int c0 = split_cta(sp, q0), c1 = split_cta(sp, q0 + C - 1);
-        __threadfence();
-        __syncwarp();
-        int last = 0;
-        if (lane == 0) {
-          last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
-          if (last) p.cnt[c0] = 0;
-        }
-        if (__shfl_sync(0xffffffffu, last, 0)) {
-          __threadfence();
-#pragma unroll 4
-          for (int i = lane; i < p.M * kLinStrip; i += 32) {
-            const int row = i / kLinStrip, n = n0 + i % kLinStrip;
-            if (n >= p.N) continue;
-            float v = __ldcg(p.part + (static_cast<size_t>(c0) * 2 + 1) * p.M * kLinStrip + i);
-#pragma unroll 4
-            for (int cta = c0 + 1; cta <= c1; ++cta)
-              v += __ldcg(p.part + static_cast<size_t>(cta) * 2 * p.M * kLinStrip + i);
-            store_y(y, static_cast<size_t>(row) * p.N + n, v);
-          }
-        }
-      }
+      lin_finish<32, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, kc + chunks, C, b, lane, &sr->last[0]);
       __syncwarp();
       mbar_arrive(&sr->red_empty[rpos.at]);
       rpos.next(2);
@@ -226,9 +261,14 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
       if (!mbar_wait(&sr->red_empty[rpos.at], rpos.phase ^ 1u, &sr->abort)) sr->give_up(p.err);
       __syncwarp();
     });
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sr->red_full[rpos.at]);
-    rpos.next(2);
+    if (left > 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sr->red_full[rpos.at]);
+      rpos.next(2);
+    } else {
+      bar_consumers<CT>();
+      lin_finish<CT, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, end, C, b, tid, &sr->last[1]);
+    }
   }
   if (sr->aborted()) drain_grace();
 }

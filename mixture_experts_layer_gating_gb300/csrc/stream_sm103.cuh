@@ -23,11 +23,12 @@
 // two that puts the row's largest element in [2^14, 2^15).  One conversion
 // makes two e4m3 values fp16, and an fp16 row needs no second term for h.
 //
-// A stage is two boxes ("halves") of 64 rows x 128 bytes, 128-byte swizzled:
-//   [.., K, N] weights (bf16, e4m3): 64 consecutive k, 64 or 128 columns a half;
-//     warp w multiplies k 16 (w / 2) .. + 15 of half w % 2, so the four warps of
-//     a half hold partial sums of the same columns;
-//   [.., N, K] weights (e4m3, 4-bit): 64 output rows a half, 128 or 256
+// A stage is 16 KB of 128-byte rows, 128-byte swizzled:
+//   [.., K, N] weights (bf16, e4m3): four boxes ("quarters") of 32 consecutive k
+//     x 64 or 128 columns; warp w multiplies k 16 (w / 4) .. + 15 of quarter w % 4.
+//     Neighbouring quarters are 256 bytes (gate, up) or 512 bytes (down) of a row:
+//     with 128-byte pieces the same layer read HBM at 4.6 TB/s, not 6;
+//   [.., N, K] weights (e4m3, 4-bit): two boxes of 64 output rows x 128 or 256
 //     consecutive k; warp w owns rows 32 (w / 2) .. + 31 of the 128 and one half
 //     of the k (two 16-row tiles share the token rows that it loads).
 // The k order inside an mma is free as long as both operands use the same:
@@ -47,10 +48,9 @@
 namespace moe {
 
 constexpr int kStageBytes = 16384;
-constexpr int kHalfBytes = 8192;
 constexpr int kStreamWarps = 8;     // consumer warps of a team
 constexpr int kStreamMaxCtas = 160; // most CTAs of a launch
-constexpr int kStreamMaxRows = 32;  // most token rows
+constexpr int kStreamMaxRows = 32;  // most token rows of a call
 constexpr int kMaxStages = 12;      // of the ring
 
 enum StreamKind : int { kStreamBf16 = 0, kStreamFp8 = 1, kStreamFp8Nk = 2, kStreamW4 = 3 };
@@ -58,10 +58,12 @@ enum StreamKind : int { kStreamBf16 = 0, kStreamFp8 = 1, kStreamFp8Nk = 2, kStre
 template <int KIND, int GRP>
 struct StreamTraits {
   static constexpr bool KN = KIND == kStreamBf16 || KIND == kStreamFp8;
-  static constexpr int KCH = KN ? 64 : (KIND == kStreamFp8Nk ? 128 : 256);  // k of a stage
-  static constexpr int HC = KIND == kStreamFp8 ? 128 : 64;  // output columns of a half
-  static constexpr int MT = KN ? HC / 16 : 2;               // 16-column mma tiles of a warp
-  static constexpr int KW = KN ? 4 : 2;  // warps of a team that hold sums of the same columns
+  static constexpr int KCH = KN ? 32 : (KIND == kStreamFp8Nk ? 128 : 256);  // k of a stage
+  static constexpr int BOXES = KN ? 4 : 2;
+  static constexpr int BOX_ROWS = KN ? 32 : 64;
+  static constexpr int QC = KIND == kStreamFp8 ? 128 : 64;  // output columns of a box
+  static constexpr int HC = QC * BOXES / 2;                 // of half the boxes (gate or up)
+  static constexpr int MT = KN ? QC / 16 : 2;               // 16-column mma tiles of a warp
   // bytes between token rows in shared memory: the padding makes a quarter-
   // (KN: half-) warp's loads of several rows fall on different banks
   static constexpr int PITCH = KCH * 2 + (KN ? 32 : 64);
@@ -169,6 +171,7 @@ struct StreamRing {
   // the two buffers of finished sums that the consumers hand to the finisher
   uint64_t red_full[2], red_empty[2];
   int abort;
+  int last[2];  // whether an arrival was the last (finisher's, consumers')
   __device__ void init(int consumer_warps) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&red_full[i], consumer_warps);
@@ -255,17 +258,17 @@ __host__ __device__ __forceinline__ int split_cta(const Split& s, long long q) {
 }
 
 // ------------------------------------------------------------ multiply a stage
-// [.., K, N] weights: the warp's k16 of its half times NTU tiles of 8 tokens.
+// [.., K, N] weights: the warp's k16 of its quarter times NTU tiles of 8 tokens.
 // acc[nt][mt] holds columns (2 KIND-dependent widths) as kn_col() says.
 template <int KIND, int NT, bool HILO>
 __device__ __forceinline__ void stage_mma_kn(uint32_t stage, uint32_t bbuf, uint32_t lo_off, int warp,
                                              int lane, int ntu,
                                              float (&acc)[NT][StreamTraits<KIND, 0>::MT][4]) {
   using Tr = StreamTraits<KIND, 0>;
-  const int g = lane >> 2, c = lane & 3, half = warp & 1, kw = warp >> 1;
+  const int g = lane >> 2, c = lane & 3, kw = warp >> 2;
   // rows 2c, 2c+1, 2c+8, 2c+9 of the k16: eight lanes of a load phase (two g,
   // four c) then touch eight different 16-byte columns of the swizzled box
-  const uint32_t base = stage + half * kHalfBytes + (kw * 16 + 2 * c) * 128;
+  const uint32_t base = stage + (warp & 3) * (kStageBytes / 4) + (kw * 16 + 2 * c) * 128;
   const uint32_t x0 = static_cast<uint32_t>(g ^ (2 * c)) << 4;
   const uint32_t x1 = static_cast<uint32_t>(g ^ (2 * c + 1)) << 4;
   const uint4 w0 = lds128(base + x0), w1 = lds128(base + 128 + x1);
@@ -305,7 +308,7 @@ __device__ __forceinline__ void stage_mma_kn(uint32_t stage, uint32_t bbuf, uint
       }
   }
 }
-// column (inside the half) of acc[..][mt][0..1]; [2..3] hold the next one
+// column (inside the box) of acc[..][mt][0..1]; [2..3] hold the next one
 template <int KIND>
 __device__ __forceinline__ int kn_col(int lane, int mt) {
   return (KIND == kStreamBf16 ? 8 : 16) * (lane >> 2) + 2 * mt;
@@ -490,7 +493,7 @@ __device__ __forceinline__ void stage_mma_w4(uint32_t stage, uint32_t rows, int 
   }
 }
 
-// A team's sums into red[row][columns] (RP floats a row): the KW warps of a team
+// A team's sums into red[row][columns] (RP floats a row): the two warps of a team
 // that hold sums of the same columns, and the teams, add theirs one after
 // another, in a fixed order.  `before_first` runs before anything is written.
 template <int KIND, int GRP, int NT, int TEAMS, int RP, typename WAIT>
@@ -498,10 +501,10 @@ __device__ __forceinline__ void add_sums(float* red, int team, int warp, int lan
                                          const float (&acc)[NT][StreamTraits<KIND, GRP>::MT][4], WAIT before_first) {
   using Tr = StreamTraits<KIND, GRP>;
   const int g = lane >> 2, c = lane & 3;
-  const int mine = team * Tr::KW + (Tr::KN ? warp >> 1 : warp & 1);
+  const int mine = team * 2 + (Tr::KN ? warp >> 2 : warp & 1);
   if (mine == 0) before_first();
 #pragma unroll 1
-  for (int r = 0; r < Tr::KW * TEAMS; ++r) {
+  for (int r = 0; r < 2 * TEAMS; ++r) {
     if (r > 0) bar_consumers<32 * kStreamWarps * TEAMS>();
     if (mine == r) {
 #pragma unroll
@@ -509,7 +512,7 @@ __device__ __forceinline__ void add_sums(float* red, int team, int warp, int lan
         if (nt < ntu) {
 #pragma unroll
           for (int mt = 0; mt < Tr::MT; ++mt) {
-            const int col = Tr::KN ? (warp & 1) * Tr::HC + kn_col<KIND>(lane, mt)
+            const int col = Tr::KN ? (warp & 3) * Tr::QC + kn_col<KIND>(lane, mt)
                                    : (warp >> 1) * 32 + mt * 16 + nk_row<KIND, GRP>(g);
             constexpr int step = Tr::KN ? 1 : 8;  // column of v[2..3] after that of v[0..1]
             float* at = red + (nt * 8 + 2 * c) * RP + col;
