@@ -164,7 +164,7 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
 
 size_t moe_linear_w4_workspace_size(int32_t M, int32_t K, int32_t N) {
   if (M < 0 || M > kStreamMaxRows || K < 32 || K % 32 || N < 1) return 0;
-  return sizeof(ControlBlock) + up256(kStreamMaxCtas * 4) + linear_w4_part_bytes(std::max(M, 1));
+  return sizeof(ControlBlock) + linear_w4_scratch(std::max(M, 1), K).total;
 }
 
 int moe_linear_w4(int32_t M, int32_t K, int32_t N, int32_t group, const void* x, const void* Wq,
@@ -177,13 +177,10 @@ int moe_linear_w4(int32_t M, int32_t K, int32_t N, int32_t group, const void* x,
   for (const void* q : {x, Wq, scales, static_cast<const void*>(y)})
     if (!q || !al16(q)) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  uint8_t* base = static_cast<uint8_t*>(ws);
-  int32_t* cnt = reinterpret_cast<int32_t*>(base + sizeof(ControlBlock));
-  float* part = reinterpret_cast<float*>(base + sizeof(ControlBlock) + up256(kStreamMaxCtas * 4));
   const cudaError_t e =
       launch_linear_w4(M, K, N, group, x, Wq, scales, static_cast<const uint8_t*>(zeros), y,
-                       y_dtype == MOE_F32, &reinterpret_cast<ControlBlock*>(ws)->err, cnt, part,
-                       static_cast<cudaStream_t>(stream));
+                       y_dtype == MOE_F32, &reinterpret_cast<ControlBlock*>(ws)->err,
+                       static_cast<uint8_t*>(ws) + sizeof(ControlBlock), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

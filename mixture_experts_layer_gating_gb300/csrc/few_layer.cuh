@@ -77,8 +77,11 @@ __device__ __forceinline__ float few_act(float g, float u, int act) {
 // chunks.  Index 0 of
 // S, C, K, width: the shared expert, 1: the routed ones.
 struct FewPass {
+  // A chunk counts w[r] units in the split: rows beyond eight make a shared
+  // expert's chunk slower than HBM (two tiles to multiply, more rows to feed).
   Split sp;
-  long long lo, hi, shared;  // shared: chunks of the shared expert (all its entries)
+  int w[2];
+  long long lo, hi, shared;  // chunks; shared: of the shared expert (all its entries)
   int shared_entries;
   int S[2], C[2];            // strips of an expert, chunks of a strip
   int K[2], width[2];        // the reduction, the output columns (of gate and up each)
@@ -121,6 +124,16 @@ struct FewSmem {
   static_assert(kBytes <= kStreamSmemMax, "shared memory");
 };
 
+// The first chunk that starts at unit u or later; the unit at which chunk q starts.
+__device__ __forceinline__ long long few_chunk(const FewPass& f, long long u) {
+  const long long su = f.shared * f.w[0];
+  return u < su ? static_cast<long long>(div_u64(u + f.w[0] - 1, f.w[0]))
+                : f.shared + static_cast<long long>(div_u64(u - su + f.w[1] - 1, f.w[1]));
+}
+__device__ __forceinline__ long long few_unit(const FewPass& f, long long q) {
+  return q < f.shared ? q * f.w[0] : f.shared * f.w[0] + (q - f.shared) * f.w[1];
+}
+__device__ __forceinline__ int few_cta(const FewPass& f, long long q) { return split_cta(f.sp, few_unit(f, q)); }
 template <int KIND, int GRP>
 __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int na, int G, int b) {
   using Tr = StreamTraits<KIND, GRP>;
@@ -136,9 +149,18 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
   }
   f.shared_entries = p.Is > 0 ? (p.T + kFewGroup - 1) / kFewGroup : 0;
   f.shared = static_cast<long long>(f.shared_entries) * f.S[0] * f.C[0];
-  f.sp = make_split(f.shared + static_cast<long long>(na) * f.S[1] * f.C[1], G);
-  f.lo = split_lo(f.sp, b);
-  f.hi = split_lo(f.sp, b + 1);
+  f.w[0] = f.w[1] = 1;
+  if (p.T > 8 && f.shared > 0) {
+    // measured on the CTAs that stream the shared expert: 1.1 times a routed chunk's
+    // time, 1.3 to 1.5 in the down pass of 4-bit weights
+    f.w[0] = KIND == kStreamW4 && down ? 3 : 9;
+    f.w[1] = KIND == kStreamW4 && down ? 2 : 8;
+  }
+  // (at least w[0] units, so at least one chunk, for every CTA that has a part)
+  f.sp.N = f.shared * f.w[0] + static_cast<long long>(na) * f.S[1] * f.C[1] * f.w[1];
+  f.sp.Gp = static_cast<int>(min(static_cast<long long>(G), f.sp.N / f.w[0]));
+  f.lo = few_chunk(f, split_lo(f.sp, b));
+  f.hi = few_chunk(f, split_lo(f.sp, b + 1));
   return f;
 }
 // A chunk's place: shared (r 0) or routed (r 1) expert, entry, strip, chunk of
@@ -253,9 +275,9 @@ struct Few {
   static __device__ __forceinline__ void prefetch_shared(const FewParams& p, const CUtensorMap* m, int b, int G,
                                                          int most) {
     FewPass f = few_pass<KIND, GRP>(p, DOWN, 0, G, b);
-    f.sp = make_split(static_cast<long long>(f.S[0]) * f.C[0], G);
-    f.lo = split_lo(f.sp, b);
-    f.hi = split_lo(f.sp, b + 1);
+    const Split sp = make_split(static_cast<long long>(f.S[0]) * f.C[0], G);
+    f.lo = split_lo(sp, b);
+    f.hi = split_lo(sp, b + 1);
     if (f.lo >= f.hi) return;
     FewAt at(f, f.lo);
 #pragma unroll 1
@@ -460,7 +482,7 @@ struct Few {
       *reinterpret_cast<float4*>(dst + row * pitch + col) = *reinterpret_cast<const float4*>(red + row * RP + col);
     }
     if (DOWN) return;
-    const int c0 = split_cta(f.sp, q0), c1 = split_cta(f.sp, q0 + f.C[at.r] - 1);
+    const int c0 = few_cta(f, q0), c1 = few_cta(f, q0 + f.C[at.r] - 1);
     int last = 0;
     __threadfence();
     if (THREADS == 32) {
@@ -573,6 +595,9 @@ struct Few {
         sbase = static_cast<const __nv_bfloat16*>(DOWN ? (at.r ? p.s2 : p.s2s) : (at.r ? p.s13 : p.s13s));
         groups = f.K[at.r] / GRP;
         srow = l < f.width[at.r] ? ((e * (DOWN ? 1 : 2) + half) * f.width[at.r] + l) * groups : -1;
+        // the next strip's first ones into L2 (the strips of an expert follow one another)
+        if (left > chunks && at.s + 1 < f.S[at.r] && (warp & 1) == 0 && l + (DOWN ? 128 : 64) < f.width[at.r])
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(sbase + srow + static_cast<long long>(DOWN ? 128 : 64) * groups));
         scales(sc0, at.kc + team);
         scales(sc1, at.kc + team + Sm::kTeams);
       }
@@ -987,59 +1012,68 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   asm volatile("bar.sync 6, %0;" ::"n"(CT + 32) : "memory");  // the finisher is through
   F::grid_sync(p, sr, 3, 2);
 
-  // phase 4: the weighted sum of a token's rows.  Four columns a group of eight
+  // phase 4: the weighted sum of a token's rows.  Eight columns a group of eight
   // lanes; lane l takes experts l, l + 8 and the shared expert as number k, and
   // the lanes' sums are added in a fixed tree.
   {
-    const int per = p.D / 4, l = lane & 7, items = p.T * per;
+    const int per = p.D / 8, l = lane & 7, items = p.T * per;
     const int terms = p.k + (shared ? 1 : 0);
+#pragma unroll 1
     for (int i0 = (b * CT + tid) >> 3; i0 - (lane >> 3) < items; i0 += (G * CT) >> 3) {
       const bool in = i0 < items;
       const int i = in ? i0 : items - 1;
-      const int t = i / per, d0 = (i - t * per) * 4;
+      const int t = i / per, d0 = (i - t * per) * 8;
       const int s = d0 / (2 * Tr::HC), col = d0 % (2 * Tr::HC);
-      float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float o[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o[q] = 0.0f;
       for (int j = l; j < terms; j += 8) {
         const bool rt = j < p.k;
-        // the row, its entry, its place among the entry's rows
+        // the row, its place among the expert's rows, its entry and place there
         const int e = rt ? ctl->ids[t * p.k + j] : 0;
         const int r = rt ? ctl->pos[t * p.k + j] : R + t;
-        const int at = rt ? r - ctl->aoff[ctl->amap[e]] : t;  // among the expert's rows
-        const int a = (rt ? ctl->amap[e] : 0) + at / kFewGroup, sl = at % kFewGroup;
+        const float4* src = reinterpret_cast<const float4*>(p.prim + static_cast<size_t>(r) * p.W +
+                                                            static_cast<size_t>(s) * 2 * Tr::HC + col);
+        const float4 y0 = __ldcg(src), y1 = __ldcg(src + 1);
         float w = rt ? ctl->w[t * p.k + j] : 1.0f;
         if constexpr (Tr::F16) w *= F::exp2_int(-F::row_exp(__ldcg(p.hmax + r)));
+        float4 c0v = make_float4(1.0f, 1.0f, 1.0f, 1.0f), c1v = c0v;
+        if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
+          const float4* sc = reinterpret_cast<const float4*>(
+              static_cast<const float*>(rt ? p.s2 : p.s2s) + (rt ? static_cast<size_t>(e) * p.D : 0) + d0);
+          c0v = __ldg(sc);
+          c1v = __ldg(sc + 1);
+        }
+        float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        const int at = rt ? r - ctl->aoff[ctl->amap[e]] : t;
+        const int a = (rt ? ctl->amap[e] : 0) + at / kFewGroup, sl = at % kFewGroup;
         const int C = dn.C[rt];
         const long long q0 = (rt ? dn.shared : 0) + (static_cast<long long>(a) * dn.S[rt] + s) * C;
-        float4 y = __ldcg(reinterpret_cast<const float4*>(p.prim + static_cast<size_t>(r) * p.W +
-                                                          static_cast<size_t>(s) * 2 * Tr::HC + col));
-        const int c0 = split_cta(dn.sp, q0), c1 = split_cta(dn.sp, q0 + C - 1);
+        const int c0 = few_cta(dn, q0), c1 = few_cta(dn, q0 + C - 1);
+#pragma unroll 1
         for (int cta = c0 + 1; cta <= c1; ++cta) {
-          const float4 m = __ldcg(reinterpret_cast<const float4*>(
-              p.extra + (static_cast<size_t>(cta) * p.T + sl) * 2 * Tr::HC + col));
-          y.x += m.x; y.y += m.y; y.z += m.z; y.w += m.w;
+          const float4* x = reinterpret_cast<const float4*>(
+              p.extra + (static_cast<size_t>(cta) * p.T + sl) * 2 * Tr::HC + col);
+          const float4 m = __ldcg(x), n = __ldcg(x + 1);
+          y[0] += m.x; y[1] += m.y; y[2] += m.z; y[3] += m.w;
+          y[4] += n.x; y[5] += n.y; y[6] += n.z; y[7] += n.w;
         }
-        if constexpr (KIND == kStreamFp8 || KIND == kStreamFp8Nk) {
-          const float4 sc = __ldg(reinterpret_cast<const float4*>(
-              static_cast<const float*>(rt ? p.s2 : p.s2s) + (rt ? static_cast<size_t>(e) * p.D : 0) + d0));
-          y.x *= sc.x; y.y *= sc.y; y.z *= sc.z; y.w *= sc.w;
-        }
-        o[0] = fmaf(w, y.x, o[0]);
-        o[1] = fmaf(w, y.y, o[1]);
-        o[2] = fmaf(w, y.z, o[2]);
-        o[3] = fmaf(w, y.w, o[3]);
+        const float cs[8] = {c0v.x, c0v.y, c0v.z, c0v.w, c1v.x, c1v.y, c1v.z, c1v.w};
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] = fmaf(w, y[q] * cs[q], o[q]);
       }
 #pragma unroll
       for (int m = 1; m < 8; m <<= 1)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] += __shfl_xor_sync(0xffffffffu, o[q], m);
+        for (int q = 0; q < 8; ++q) o[q] += __shfl_xor_sync(0xffffffffu, o[q], m);
       if (in && l == 0) {
         union {
-          uint2 v;
-          __nv_bfloat16 h[4];
+          uint4 v;
+          __nv_bfloat16 h[8];
         } w;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w.h[q] = __float2bfloat16_rn(o[q]);
-        *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(t) * p.D + d0) = w.v;
+        for (int q = 0; q < 8; ++q) w.h[q] = __float2bfloat16_rn(o[q]);
+        *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(t) * p.D + d0) = w.v;
       }
     }
   }

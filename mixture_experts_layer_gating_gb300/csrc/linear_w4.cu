@@ -16,7 +16,9 @@ struct LinParams {
   int32_t* err;
   int32_t* cnt;   // [ctas] arrivals, zero between launches
   float* part;    // [ctas][2][M][128]: a CTA's part of a strip begun earlier, of one it leaves unfinished
-  int M, K, N;
+  // more than eight rows: x put in the weights' k order by a launch of its own
+  __nv_bfloat16* xp;  // [M][Kp], Kp whole stages
+  int M, K, N, Kp;
 };
 
 template <int GRP, int NT>
@@ -38,6 +40,24 @@ struct LinSmem {
 __device__ __forceinline__ void store_y(float* y, size_t at, float v) { y[at] = v; }
 __device__ __forceinline__ void store_y(__nv_bfloat16* y, size_t at, float v) {
   y[at] = __float2bfloat16_rn(v);
+}
+
+// x (more than eight rows) in the weights' k order, padded with zeros: eight inputs
+// a thread.
+template <int GRP>
+__global__ void __launch_bounds__(256) linear_w4_order_kernel(const __grid_constant__ LinParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int k0 = (blockIdx.x * 256 + threadIdx.x) * 8, row = blockIdx.y;
+  if (k0 >= p.Kp) return;
+  uint4 x = make_uint4(0, 0, 0, 0);
+  if (k0 < p.K) x = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row) * p.K + k0));
+  uint4 v;
+  v.x = __byte_perm(x.x, x.z, 0x5410);
+  v.y = __byte_perm(x.x, x.z, 0x7632);
+  v.z = __byte_perm(x.y, x.w, 0x5410);
+  v.w = __byte_perm(x.y, x.w, 0x7632);
+  *reinterpret_cast<uint4*>(p.xp + static_cast<size_t>(row) * p.Kp + perm_k<kStreamW4, GRP>(k0)) = v;
 }
 
 // One strip's sums (or this CTA's part of them) to y by THREADS threads: the
@@ -150,46 +170,66 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     }
     return;
   }
-  if (tid >= CT + 32) {  // feeders: x rows of every kFeeders-th stage, in the k order of the weights
-    // (always the same slots: a wait cannot mistake a fill for the one before); 32
-    // pieces of 8 inputs a row, one a lane
-    constexpr int J = GRP / 32;
-    const int pc = lane;
-    const uint32_t pdst = (((pc / (4 * J)) * J + pc % J) * 4 + (pc % (4 * J)) / J) * 16;
-    int turn = (tid - CT - 32) >> 5;
+  if (tid >= CT + 32) {  // feeders: x rows of every kFeeders-th stage, always the same slots: a
+    // wait cannot mistake a fill for the one before
+    int left = static_cast<int>(hi - lo);
+    const int first = (tid - CT - 32) >> 5;  // of the run's stages
     RingPos pos;
-    for (int left = static_cast<int>(hi - lo); left > 0; --left) {
-      if (turn == 0) {
+    pos.skip(first, Sm::NST);
+    kc = (kc + first) % C;
+    left -= first;
+    if constexpr (NT == 1) {
+      // up to eight rows: 32 pieces of 8 inputs a row, one a lane, put in order on the
+      // way; the next stage's are loaded before this one's slot is waited for
+      const uint32_t pdst = perm_k<kStreamW4, GRP>(lane * 8) * 2;
+      uint4 x[8];
+      auto load = [&](int kc_) {
+        const int k0 = kc_ * 256 + lane * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (i < p.M && k0 < p.K) x[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(i) * p.K + k0));
+        }
+      };
+      if (left > 0) load(kc);
+#pragma unroll 1
+      for (; left > 0; left -= Sm::kFeeders) {
         if (!mbar_wait(&sr->empty[pos.at], pos.phase ^ 1u, &sr->abort)) {
           sr->give_up(p.err);
           break;
         }
         uint8_t* dst = ring + pos.at * Sm::kSlot + kStageBytes + pdst;
-        const int k0 = kc * 256 + pc * 8;
-#pragma unroll 1
-        for (int r0 = 0; r0 < p.M; r0 += 8) {
-          uint4 x[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (r0 + i < p.M && k0 < p.K)
-              x[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(r0 + i) * p.K + k0));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4 v;
-            v.x = __byte_perm(x[i].x, x[i].z, 0x5410);
-            v.y = __byte_perm(x[i].x, x[i].z, 0x7632);
-            v.z = __byte_perm(x[i].y, x[i].w, 0x5410);
-            v.w = __byte_perm(x[i].y, x[i].w, 0x7632);
-            *reinterpret_cast<uint4*>(dst + (r0 + i) * Tr::PITCH) = v;
-          }
+        for (int i = 0; i < 8; ++i) {
+          if (i >= p.M) break;
+          uint4 v;
+          v.x = __byte_perm(x[i].x, x[i].z, 0x5410);
+          v.y = __byte_perm(x[i].x, x[i].z, 0x7632);
+          v.z = __byte_perm(x[i].y, x[i].w, 0x5410);
+          v.w = __byte_perm(x[i].y, x[i].w, 0x7632);
+          *reinterpret_cast<uint4*>(dst + i * Tr::PITCH) = v;
         }
         mbar_arrive(&sr->full[pos.at]);
+        pos.skip(Sm::kFeeders, Sm::NST);
+        kc = (kc + Sm::kFeeders) % C;
+        if (left > Sm::kFeeders) load(kc);
       }
-      turn = turn == 0 ? Sm::kFeeders - 1 : turn - 1;
-      pos.next(Sm::NST);
-      kc = kc + 1 == C ? 0 : kc + 1;
+    } else {
+#pragma unroll 1
+      for (; left > 0; left -= Sm::kFeeders) {
+        if (!mbar_wait(&sr->empty[pos.at], pos.phase ^ 1u, &sr->abort)) {
+          sr->give_up(p.err);
+          break;
+        }
+        const uint32_t dst = smem_u32(ring) + pos.at * Sm::kSlot + kStageBytes + lane * 16;
+        const __nv_bfloat16* src = p.xp + kc * 256 + lane * 8;
+#pragma unroll 4
+        for (int row = 0; row < p.M; ++row) cp_async_16(dst + row * Tr::PITCH, src + static_cast<size_t>(row) * p.Kp, 16);
+        cp_async_mbar_arrive_noinc(&sr->full[pos.at]);
+        pos.skip(Sm::kFeeders, Sm::NST);
+        kc = (kc + Sm::kFeeders) % C;
+      }
+      cp_async_wait_all();
     }
     return;
   }
@@ -238,6 +278,9 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     const int n = s * kLinStrip + (warp >> 1) * 32 + (c >> 1) * 16 + r + (c & 1) * 8;
     const long long srow = n < p.N ? static_cast<long long>(n) * groups : -1;
     const int qh = (warp & 1) * (128 / GRP);
+    // and the next strip's first ones into L2
+    if (left > chunks && n + kLinStrip < p.N && (warp & 1) == 0)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sc + srow + static_cast<long long>(kLinStrip) * groups));
     W4Scales<GRP> sc0, sc1, sc2;
     w4_load_scales<GRP>(sc0, p.sc, p.zp, srow, groups, (kc + team) * (256 / GRP) + qh);
     w4_load_scales<GRP>(sc1, p.sc, p.zp, srow, groups, (kc + team + Sm::kTeams) * (256 / GRP) + qh);
@@ -301,6 +344,9 @@ cudaError_t launch_lin_types(const CUtensorMap& m, const LinParams& p, bool f32,
 template <int GRP>
 cudaError_t launch_lin_rows(const CUtensorMap& m, const LinParams& p, bool f32, int grid, cudaStream_t s) {
   if (p.M <= 8) return launch_lin_types<GRP, 1>(m, p, f32, grid, s);
+  const cudaError_t e =
+      launch_kernel(linear_w4_order_kernel<GRP>, dim3((p.Kp + 2047) / 2048, p.M), dim3(256), 0, s, p);
+  if (e != cudaSuccess) return e;
   if (p.M <= 16) return launch_lin_types<GRP, 2>(m, p, f32, grid, s);
   return launch_lin_types<GRP, 4>(m, p, f32, grid, s);
 }
@@ -410,13 +456,25 @@ cudaError_t launch_dequantize(const uint8_t* q, const __nv_bfloat16* sc, const u
 
 }  // namespace
 
-size_t linear_w4_part_bytes(int M) {
-  return static_cast<size_t>(kStreamMaxCtas) * 2 * M * kLinStrip * 4;
+// A product's scratch: arrival counts, partial sums, ordered rows.
+LinearW4Scratch linear_w4_scratch(int M, int K) {
+  const size_t Kp = (static_cast<size_t>(K) + 255) / 256 * 256;
+  LinearW4Scratch l{};
+  size_t cur = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = cur;
+    cur = (cur + bytes + 255) / 256 * 256;
+    return o;
+  };
+  l.cnt = take(kStreamMaxCtas * 4);
+  l.part = take(static_cast<size_t>(kStreamMaxCtas) * 2 * M * kLinStrip * 4);
+  l.xp = take(M > 8 ? static_cast<size_t>(M) * Kp * 2 : 0);
+  l.total = cur;
+  return l;
 }
 
 cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, const void* wq, const void* sc,
-                             const uint8_t* zp, void* y, bool y_f32, int32_t* err, int32_t* cnt, float* part,
-                             cudaStream_t s) {
+                             const uint8_t* zp, void* y, bool y_f32, int32_t* err, uint8_t* scratch, cudaStream_t s) {
   CUtensorMap m;
   const uint64_t dims[2] = {static_cast<uint64_t>(K) / 2, static_cast<uint64_t>(N)};
   const uint64_t strides[1] = {static_cast<uint64_t>(K) / 2};
@@ -428,11 +486,14 @@ cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, cons
   p.zp = zp;
   p.y = y;
   p.err = err;
-  p.cnt = cnt;
-  p.part = part;
+  const LinearW4Scratch l = linear_w4_scratch(M, K);
+  p.cnt = reinterpret_cast<int32_t*>(scratch + l.cnt);
+  p.part = reinterpret_cast<float*>(scratch + l.part);
+  p.xp = reinterpret_cast<__nv_bfloat16*>(scratch + l.xp);
   p.M = M;
   p.K = K;
   p.N = N;
+  p.Kp = (K + 255) / 256 * 256;
   const long long chunks = (static_cast<long long>(N) + kLinStrip - 1) / kLinStrip * ((K + 255) / 256);
   int grid = device_sm_count();
   if (grid > kStreamMaxCtas) grid = kStreamMaxCtas;

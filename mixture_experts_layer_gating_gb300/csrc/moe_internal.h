@@ -87,10 +87,12 @@ bool few_supported(const moe_config_t* c);
 size_t few_workspace_bytes(const moe_config_t* c);
 
 // ---------------------------------------------------------------- linear_w4.cu
-size_t linear_w4_part_bytes(int M); // room for the partial sums
+struct LinearW4Scratch {
+  size_t cnt, part, xp, total;
+};
+LinearW4Scratch linear_w4_scratch(int M, int K);  // offsets; the counts (cnt) are zero between launches
 cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, const void* wq, const void* sc,
-                             const uint8_t* zp, void* y, bool y_f32, int32_t* err, int32_t* cnt, float* part,
-                             cudaStream_t s);
+                             const uint8_t* zp, void* y, bool y_f32, int32_t* err, uint8_t* scratch, cudaStream_t s);
 cudaError_t launch_quantize_w4(const void* W, bool f32, long long G, int K, int N, int group, void* q,
                                void* sc, cudaStream_t s);
 cudaError_t launch_dequantize_w4(const void* q, const void* sc, const uint8_t* zp, long long G, int K, int N,

@@ -237,7 +237,7 @@ __device__ __forceinline__ void split_bf16(float v, __nv_bfloat16& hi, __nv_bflo
 }
 
 // ------------------------------------------------------------ work of a CTA
-// N equal chunks over min(G, N) CTAs: CTA b takes [N b / Gp, N (b + 1) / Gp).
+// N units over Gp CTAs: CTA b takes [N b / Gp, N (b + 1) / Gp).
 struct Split {
   long long N;
   int Gp;
@@ -245,16 +245,18 @@ struct Split {
 __host__ __device__ __forceinline__ Split make_split(long long N, int G) {
   return Split{N, static_cast<int>(N < G ? N : G)};
 }
+// (64-bit divisions cost about 100 instructions: only where they are needed)
+__host__ __device__ __forceinline__ unsigned long long div_u64(unsigned long long a, unsigned long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 __host__ __device__ __forceinline__ long long split_lo(const Split& s, int b) {
   if (s.N == 0) return 0;
-  return b >= s.Gp ? s.N : s.N * b / s.Gp;
+  return b >= s.Gp ? s.N : static_cast<long long>(div_u64(s.N * b, s.Gp));
 }
-// the CTA of chunk q
-__host__ __device__ __forceinline__ int split_cta(const Split& s, long long q) {
-  const unsigned long long v = static_cast<unsigned long long>(q + 1) * s.Gp - 1;
-  if ((v >> 32) == 0 && (s.N >> 32) == 0)
-    return static_cast<int>(static_cast<uint32_t>(v) / static_cast<uint32_t>(s.N));
-  return static_cast<int>(v / static_cast<unsigned long long>(s.N));
+// the CTA of unit u
+__host__ __device__ __forceinline__ int split_cta(const Split& s, long long u) {
+  return static_cast<int>(div_u64(static_cast<unsigned long long>(u + 1) * s.Gp - 1, s.N));
 }
 
 // ------------------------------------------------------------ multiply a stage
