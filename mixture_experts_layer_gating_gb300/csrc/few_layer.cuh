@@ -126,11 +126,13 @@ struct FewSmem {
 
 // The first chunk that starts at unit u or later; the unit at which chunk q starts.
 __device__ __forceinline__ long long few_chunk(const FewPass& f, long long u) {
+  if (f.w[0] == 1) return u;
   const long long su = f.shared * f.w[0];
   return u < su ? static_cast<long long>(div_u64(u + f.w[0] - 1, f.w[0]))
                 : f.shared + static_cast<long long>(div_u64(u - su + f.w[1] - 1, f.w[1]));
 }
 __device__ __forceinline__ long long few_unit(const FewPass& f, long long q) {
+  if (f.w[0] == 1) return q;
   return q < f.shared ? q * f.w[0] : f.shared * f.w[0] + (q - f.shared) * f.w[1];
 }
 __device__ __forceinline__ int few_cta(const FewPass& f, long long q) { return split_cta(f.sp, few_unit(f, q)); }
@@ -158,7 +160,7 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
   }
   // (at least w[0] units, so at least one chunk, for every CTA that has a part)
   f.sp.N = f.shared * f.w[0] + static_cast<long long>(na) * f.S[1] * f.C[1] * f.w[1];
-  f.sp.Gp = static_cast<int>(min(static_cast<long long>(G), f.sp.N / f.w[0]));
+  f.sp.Gp = f.sp.N >= static_cast<long long>(G) * f.w[0] ? G : static_cast<int>(f.sp.N) / f.w[0];
   f.lo = few_chunk(f, split_lo(f.sp, b));
   f.hi = few_chunk(f, split_lo(f.sp, b + 1));
   return f;
@@ -519,8 +521,16 @@ struct Few {
     });
   }
 
-  // The finisher's part of a pass: every strip's sums as the consumers hand them
-  // over, but for the run's last, which the consumers finish themselves.
+  // Who finishes a strip: all consumers the run's last one, when they have nothing
+  // else to do, and shared ones of more than two rows, whose parts one warp would
+  // add for tens of microseconds; the finisher warp the others.
+  static __device__ __forceinline__ bool by_consumers(const FewParams& p, const FewPass& f, const Ctrl* ctl,
+                                                      const FewAt& at, int chunks, int left) {
+    return left == 0 || (chunks != f.C[at.r] && row_count(p, ctl, at) > 2);
+  }
+
+  // The finisher's part of a pass: the sums of the strips that the consumers hand
+  // over.
   template <bool DOWN>
   static __device__ __forceinline__ void finish(const FewParams& p, const FewPass& f, Ctrl* ctl, const float* red0,
                                                 RingPos& rpos, int b, int lane) {
@@ -531,7 +541,11 @@ struct Few {
     for (;;) {
       const int chunks = min(f.C[at.r] - at.kc, left), end = at.kc + chunks;
       left -= chunks;
-      if (left == 0) break;
+      if (by_consumers(p, f, ctl, at, chunks, left)) {
+        if (left == 0) break;
+        at.next_strip(f);
+        continue;
+      }
       if (!mbar_wait(&ctl->ring.red_full[rpos.at], rpos.phase, &ctl->ring.abort)) ctl->ring.give_up(p.err);
       __syncwarp();
       finish_strip<DOWN, 32>(p, f, ctl, red0 + rpos.at * (Sm::kRedBytes / 4), at, end, f.hi - left - end, b, lane);
@@ -564,15 +578,31 @@ struct Few {
     FewAt at(f, f.lo);
     int left = static_cast<int>(f.hi - f.lo);
 
-    // 4-bit weights: the lane's row of group scales
-    [[maybe_unused]] W4Scales<GRP == 0 ? 128 : GRP> sc0, sc1, sc2;
+    // 4-bit weights: the lane's row of group scales; a strip's first ones are loaded
+    // while the strip before it is summed up
+    [[maybe_unused]] W4Scales<GRP == 0 ? 128 : GRP, false> sc0, sc1;
     [[maybe_unused]] const __nv_bfloat16* sbase = nullptr;
     [[maybe_unused]] long long srow = 0;
     [[maybe_unused]] int groups = 0;
     auto scales = [&](auto& dst, int kc) {
       if constexpr (KIND == kStreamW4)
-        w4_load_scales<GRP>(dst, sbase, nullptr, srow, groups, kc * (256 / GRP) + (warp & 1) * (128 / GRP));
+        w4_load_scales<GRP, false>(dst, sbase, nullptr, srow, groups, kc * (256 / GRP) + (warp & 1) * (128 / GRP));
     };
+    auto first_scales = [&](const FewAt& x) {
+      if constexpr (KIND == kStreamW4) {
+        // the lane's row: tile c / 2, row g or g + 8; rows 64 on of a gate/up stage are up rows
+        const int half = DOWN ? 0 : warp >> 2;
+        const int l = x.s * (DOWN ? 128 : 64) + ((warp >> 1) & (DOWN ? 3 : 1)) * 32 + (c >> 1) * 16 +
+                      nk_row<KIND, GRP>(g) + (c & 1) * 8;
+        const long long e = x.r ? ctl->aexp[x.a] : 0;
+        sbase = static_cast<const __nv_bfloat16*>(DOWN ? (x.r ? p.s2 : p.s2s) : (x.r ? p.s13 : p.s13s));
+        groups = f.K[x.r] / GRP;
+        srow = l < f.width[x.r] ? ((e * (DOWN ? 1 : 2) + half) * f.width[x.r] + l) * groups : -1;
+        scales(sc0, x.kc + team);
+        scales(sc1, x.kc + team + Sm::kTeams);
+      }
+    };
+    first_scales(at);
 
     float acc[NT][Tr::MT][4];
     while (left > 0) {  // a strip, or this CTA's part of it
@@ -586,58 +616,62 @@ struct Few {
       const int chunks = min(f.C[at.r] - at.kc, left), end = at.kc + chunks;
       RingPos pos = ring_pos;
       if (team) pos.next(Sm::NST);
-      if constexpr (KIND == kStreamW4) {
-        // the lane's row: tile c / 2, row g or g + 8; rows 64 on of a gate/up stage are up rows
-        const int half = DOWN ? 0 : warp >> 2;
-        const int l = at.s * (DOWN ? 128 : 64) + ((warp >> 1) & (DOWN ? 3 : 1)) * 32 + (c >> 1) * 16 +
-                      nk_row<KIND, GRP>(g) + (c & 1) * 8;
-        const long long e = at.r ? ctl->aexp[at.a] : 0;
-        sbase = static_cast<const __nv_bfloat16*>(DOWN ? (at.r ? p.s2 : p.s2s) : (at.r ? p.s13 : p.s13s));
-        groups = f.K[at.r] / GRP;
-        srow = l < f.width[at.r] ? ((e * (DOWN ? 1 : 2) + half) * f.width[at.r] + l) * groups : -1;
-        // the next strip's first ones into L2 (the strips of an expert follow one another)
-        if (left > chunks && at.s + 1 < f.S[at.r] && (warp & 1) == 0 && l + (DOWN ? 128 : 64) < f.width[at.r])
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(sbase + srow + static_cast<long long>(DOWN ? 128 : 64) * groups));
-        scales(sc0, at.kc + team);
-        scales(sc1, at.kc + team + Sm::kTeams);
-      }
-#pragma unroll 1
-      for (int kc = at.kc + team; kc < end; kc += Sm::kTeams) {
-        if constexpr (KIND == kStreamW4) scales(sc2, kc + 2 * Sm::kTeams);
+      auto step = [&](auto& sc, int kc) {
         if (!mbar_wait(&ctl->ring.full[pos.at], pos.phase, &ctl->ring.abort)) ctl->ring.give_up(p.err);
         __syncwarp();
         const uint32_t st = ring + pos.at * Sm::kSlot, rows = st + kStageBytes;
-        if constexpr (Tr::KN) stage_mma_kn<KIND, NT, DOWN && Sm::kHilo>(st, rows, kLo, warp, lane, ntu, acc);
-        else if constexpr (KIND == kStreamFp8Nk)
-          stage_mma_fp8nk<NT>(st, rows, warp, lane, ntu, acc);
-        else {
-          stage_mma_w4<GRP, NT, false, true>(st, rows, warp, lane, ntu, sc0, acc);
-          sc0 = sc1;
-          sc1 = sc2;
+        // (most experts of a batch of 16 have at most eight rows: the code for one tile of
+        // tokens takes three quarters of the time)
+        auto& one = reinterpret_cast<float(&)[1][Tr::MT][4]>(acc[0]);
+        if constexpr (Tr::KN) {
+          if (NT == 1 || ntu == 1) stage_mma_kn<KIND, 1, DOWN && Sm::kHilo>(st, rows, kLo, warp, lane, 1, one);
+          else stage_mma_kn<KIND, NT, DOWN && Sm::kHilo>(st, rows, kLo, warp, lane, NT, acc);
+        } else if constexpr (KIND == kStreamFp8Nk) {
+          if (NT == 1 || ntu == 1) stage_mma_fp8nk<1>(st, rows, warp, lane, 1, one);
+          else stage_mma_fp8nk<NT>(st, rows, warp, lane, NT, acc);
+        } else {
+          if (NT == 1 || ntu == 1) stage_mma_w4<GRP, 1, 1, 2, false, true>(st, rows, warp, lane, 1, sc, one);
+          else stage_mma_w4<GRP, NT, NT, 1, false, true>(st, rows, warp, lane, NT, sc, acc);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->ring.empty[pos.at]);
         pos.skip(Sm::kTeams, Sm::NST);
+        scales(sc, kc + 2 * Sm::kTeams);
+      };
+#pragma unroll 1
+      for (int kc = at.kc + team; kc < end; kc += Sm::kTeams) {
+        step(sc0, kc);
+        if constexpr (KIND == kStreamW4) {
+          // two by two, each with scales of its own: moving them on from one step to the
+          // next would wait for the loads
+          if ((kc += Sm::kTeams) >= end) break;
+          step(sc1, kc);
+        }
       }
       ring_pos.skip(chunks % Sm::NST, Sm::NST);
       ring_pos.phase ^= (chunks / Sm::NST) & 1;
       left -= chunks;
+      if (KIND == kStreamW4 && left > 0) {
+        FewAt x = at;
+        x.next_strip(f);
+        first_scales(x);
+      }
       // the sums over this CTA's chunks of the strip, to the finisher
       add_sums<KIND, GRP, NT, Sm::kTeams, Sm::kRP>(
           red0 + rpos.at * (Sm::kRedBytes / 4), team, warp, lane, ntu, acc, [&]() {
             if (!mbar_wait(&ctl->ring.red_empty[rpos.at], rpos.phase ^ 1u, &ctl->ring.abort)) ctl->ring.give_up(p.err);
             __syncwarp();
           });
-      if (left > 0) {
+      if (by_consumers(p, f, ctl, at, chunks, left)) {
+        bar();
+        finish_strip<DOWN, CT>(p, f, ctl, red0 + rpos.at * (Sm::kRedBytes / 4), at, end, f.hi - left - end, b, tid);
+        bar();
+      } else {
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->ring.red_full[rpos.at]);
         rpos.next(Sm::kRedBufs);
-        at.next_strip(f);
-      } else {  // the run's last strip: by all consumers, which have nothing else to do
-        bar();
-        finish_strip<DOWN, CT>(p, f, ctl, red0 + rpos.at * (Sm::kRedBytes / 4), at, end, f.hi - end, b, tid);
-        bar();
       }
+      at.next_strip(f);
     }
   }
 

@@ -16,7 +16,7 @@ struct LinParams {
   int32_t* err;
   int32_t* cnt;   // [ctas] arrivals, zero between launches
   float* part;    // [ctas][2][M][128]: a CTA's part of a strip begun earlier, of one it leaves unfinished
-  // more than eight rows: x put in the weights' k order by a launch of its own
+  // more than 16 rows: x put in the weights' k order by a launch of its own
   __nv_bfloat16* xp;  // [M][Kp], Kp whole stages
   int M, K, N, Kp;
 };
@@ -31,7 +31,8 @@ struct LinSmem {
   static constexpr int kSlot = stream_slot(8 * NT * Tr::PITCH);
   static constexpr int kRP = 128 + 4;
   static constexpr int kRedBytes = 8 * NT * kRP * 4;
-  static constexpr int kOther = 2 * kRedBytes + static_cast<int>(sizeof(StreamRing)) + 16;
+  static constexpr int kRedBufs = NT <= 2 ? 2 : 1;
+  static constexpr int kOther = kRedBufs * kRedBytes + static_cast<int>(sizeof(StreamRing)) + 16;
   static constexpr int NST = stream_stages(kSlot, kOther);
   static constexpr int kBytes = 1024 + NST * kSlot + kOther;
   static_assert(NST >= 4 && NST % kFeeders == 0 && kBytes <= kStreamSmemMax, "shared memory");
@@ -42,7 +43,7 @@ __device__ __forceinline__ void store_y(__nv_bfloat16* y, size_t at, float v) {
   y[at] = __float2bfloat16_rn(v);
 }
 
-// x (more than eight rows) in the weights' k order, padded with zeros: eight inputs
+// x (more than 16 rows) in the weights' k order, padded with zeros: eight inputs
 // a thread.
 template <int GRP>
 __global__ void __launch_bounds__(256) linear_w4_order_kernel(const __grid_constant__ LinParams p) {
@@ -58,6 +59,14 @@ __global__ void __launch_bounds__(256) linear_w4_order_kernel(const __grid_const
   v.z = __byte_perm(x.y, x.w, 0x5410);
   v.w = __byte_perm(x.y, x.w, 0x7632);
   *reinterpret_cast<uint4*>(p.xp + static_cast<size_t>(row) * p.Kp + perm_k<kStreamW4, GRP>(k0)) = v;
+}
+
+// Who finishes a strip: all consumers the run's last one, when they have nothing
+// else to do, shared ones of more than two rows and any of more than eight (one
+// warp takes 12 us for 32 rows, longer than the strip streams); the finisher warp
+// the others.
+__device__ __forceinline__ bool lin_by_consumers(int M, int C, int chunks, int left) {
+  return left == 0 || M > 8 || (M > 2 && chunks != C);
 }
 
 // One strip's sums (or this CTA's part of them) to y by THREADS threads: the
@@ -141,7 +150,7 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* red = reinterpret_cast<float*>(ring + Sm::NST * Sm::kSlot);
-  StreamRing* sr = reinterpret_cast<StreamRing*>(ring + Sm::NST * Sm::kSlot + 2 * Sm::kRedBytes);
+  StreamRing* sr = reinterpret_cast<StreamRing*>(ring + Sm::NST * Sm::kSlot + Sm::kRedBufs * Sm::kRedBytes);
   const int tid = threadIdx.x, b = blockIdx.x, lane = tid & 31;
   const int C = (p.K + 255) / 256, S = (p.N + kLinStrip - 1) / kLinStrip;
   const Split sp = make_split(static_cast<long long>(S) * C, gridDim.x);
@@ -153,20 +162,20 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
   pdl_launch_dependents();
   int s = static_cast<int>(lo / C), kc = static_cast<int>(lo % C);
 
-  if (tid >= CT + 32 + 32 * Sm::kFeeders) {  // finisher: every strip but the run's last
+  if (tid >= CT + 32 + 32 * Sm::kFeeders) {  // finisher: the strips that the consumers leave to it
     RingPos rpos;
     int left = static_cast<int>(hi - lo);
 #pragma unroll 1
     for (; left > 0; kc = 0, ++s) {
       const int chunks = min(C - kc, left);
       left -= chunks;
-      if (left == 0) break;
+      if (lin_by_consumers(p.M, C, chunks, left)) continue;
       if (!mbar_wait(&sr->red_full[rpos.at], rpos.phase, &sr->abort)) sr->give_up(p.err);
       __syncwarp();
       lin_finish<32, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, kc + chunks, C, b, lane, &sr->last[0]);
       __syncwarp();
       mbar_arrive(&sr->red_empty[rpos.at]);
-      rpos.next(2);
+      rpos.next(Sm::kRedBufs);
     }
     return;
   }
@@ -178,15 +187,15 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     pos.skip(first, Sm::NST);
     kc = (kc + first) % C;
     left -= first;
-    if constexpr (NT == 1) {
-      // up to eight rows: 32 pieces of 8 inputs a row, one a lane, put in order on the
+    if constexpr (NT <= 2) {
+      // up to 16 rows: 32 pieces of 8 inputs a row, one a lane, put in order on the
       // way; the next stage's are loaded before this one's slot is waited for
       const uint32_t pdst = perm_k<kStreamW4, GRP>(lane * 8) * 2;
-      uint4 x[8];
+      uint4 x[8 * NT];
       auto load = [&](int kc_) {
         const int k0 = kc_ * 256 + lane * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8 * NT; ++i) {
           x[i] = make_uint4(0, 0, 0, 0);
           if (i < p.M && k0 < p.K) x[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(i) * p.K + k0));
         }
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
         }
         uint8_t* dst = ring + pos.at * Sm::kSlot + kStageBytes + pdst;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8 * NT; ++i) {
           if (i >= p.M) break;
           uint4 v;
           v.x = __byte_perm(x[i].x, x[i].z, 0x5410);
@@ -262,6 +271,18 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
   const int r = nk_row<kStreamW4, GRP>(g), groups = p.K / GRP;
   const int ntu = (p.M + 7) >> 3;
   RingPos ring_pos, rpos;
+  // the lane's row of group scales, loaded two of the team's chunks ahead, a strip's
+  // first ones while the strip before it is summed up
+  const int qh = (warp & 1) * (128 / GRP);
+  W4Scales<GRP, ZERO> sc0, sc1;
+  long long srow = -1;
+  auto first_scales = [&](int s_, int kc_) {
+    const int n = s_ * kLinStrip + (warp >> 1) * 32 + (c >> 1) * 16 + r + (c & 1) * 8;
+    srow = n < p.N ? static_cast<long long>(n) * groups : -1;
+    w4_load_scales<GRP, ZERO>(sc0, p.sc, p.zp, srow, groups, (kc_ + team) * (256 / GRP) + qh);
+    w4_load_scales<GRP, ZERO>(sc1, p.sc, p.zp, srow, groups, (kc_ + team + Sm::kTeams) * (256 / GRP) + qh);
+  };
+  if (lo < hi) first_scales(s, kc);
   float acc[NT][2][4];
 #pragma unroll 1
   for (int left = static_cast<int>(hi - lo); left > 0; kc = 0, ++s) {  // a strip, or this CTA's part of it
@@ -274,43 +295,40 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     const int chunks = min(C - kc, left), end = kc + chunks;
     RingPos pos = ring_pos;
     if (team) pos.next(Sm::NST);
-    // the lane's row of group scales, loaded two of the team's chunks ahead
-    const int n = s * kLinStrip + (warp >> 1) * 32 + (c >> 1) * 16 + r + (c & 1) * 8;
-    const long long srow = n < p.N ? static_cast<long long>(n) * groups : -1;
-    const int qh = (warp & 1) * (128 / GRP);
-    // and the next strip's first ones into L2
-    if (left > chunks && n + kLinStrip < p.N && (warp & 1) == 0)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sc + srow + static_cast<long long>(kLinStrip) * groups));
-    W4Scales<GRP> sc0, sc1, sc2;
-    w4_load_scales<GRP>(sc0, p.sc, p.zp, srow, groups, (kc + team) * (256 / GRP) + qh);
-    w4_load_scales<GRP>(sc1, p.sc, p.zp, srow, groups, (kc + team + Sm::kTeams) * (256 / GRP) + qh);
-#pragma unroll 1
-    for (int q = kc + team; q < end; q += Sm::kTeams) {
-      w4_load_scales<GRP>(sc2, p.sc, p.zp, srow, groups, (q + 2 * Sm::kTeams) * (256 / GRP) + qh);
+    auto step = [&](W4Scales<GRP, ZERO>& sc, int q) {
       if (!mbar_wait(&sr->full[pos.at], pos.phase, &sr->abort)) sr->give_up(p.err);
       __syncwarp();
       const uint32_t st = ring_a + pos.at * Sm::kSlot;
-      stage_mma_w4<GRP, NT, ZERO, false>(st, st + kStageBytes, warp, lane, ntu, sc0, acc);
+      stage_mma_w4<GRP, NT, NT, NT == 2 ? 1 : 2, ZERO, false>(st, st + kStageBytes, warp, lane, ntu, sc, acc);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sr->empty[pos.at]);
       pos.skip(Sm::kTeams, Sm::NST);
-      sc0 = sc1;
-      sc1 = sc2;
+      w4_load_scales<GRP, ZERO>(sc, p.sc, p.zp, srow, groups, (q + 2 * Sm::kTeams) * (256 / GRP) + qh);
+    };
+    // two by two, each with scales of its own: moving them on from one step to the
+    // next would wait for the loads
+#pragma unroll 1
+    for (int q = kc + team; q < end; q += Sm::kTeams) {
+      step(sc0, q);
+      if ((q += Sm::kTeams) >= end) break;
+      step(sc1, q);
     }
     ring_pos.skip(chunks % Sm::NST, Sm::NST);
     ring_pos.phase ^= (chunks / Sm::NST) & 1;
     left -= chunks;
+    if (left > 0) first_scales(s + 1, 0);
     add_sums<kStreamW4, GRP, NT, Sm::kTeams, RP>(red + rpos.at * (Sm::kRedBytes / 4), team, warp, lane, ntu, acc, [&]() {
       if (!mbar_wait(&sr->red_empty[rpos.at], rpos.phase ^ 1u, &sr->abort)) sr->give_up(p.err);
       __syncwarp();
     });
-    if (left > 0) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sr->red_full[rpos.at]);
-      rpos.next(2);
-    } else {
+    if (lin_by_consumers(p.M, C, chunks, left)) {
       bar_consumers<CT>();
       lin_finish<CT, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, end, C, b, tid, &sr->last[1]);
+      bar_consumers<CT>();
+    } else {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sr->red_full[rpos.at]);
+      rpos.next(Sm::kRedBufs);
     }
   }
   if (sr->aborted()) drain_grace();
@@ -344,10 +362,10 @@ cudaError_t launch_lin_types(const CUtensorMap& m, const LinParams& p, bool f32,
 template <int GRP>
 cudaError_t launch_lin_rows(const CUtensorMap& m, const LinParams& p, bool f32, int grid, cudaStream_t s) {
   if (p.M <= 8) return launch_lin_types<GRP, 1>(m, p, f32, grid, s);
+  if (p.M <= 16) return launch_lin_types<GRP, 2>(m, p, f32, grid, s);
   const cudaError_t e =
       launch_kernel(linear_w4_order_kernel<GRP>, dim3((p.Kp + 2047) / 2048, p.M), dim3(256), 0, s, p);
   if (e != cudaSuccess) return e;
-  if (p.M <= 16) return launch_lin_types<GRP, 2>(m, p, f32, grid, s);
   return launch_lin_types<GRP, 4>(m, p, f32, grid, s);
 }
 
@@ -468,7 +486,7 @@ LinearW4Scratch linear_w4_scratch(int M, int K) {
   };
   l.cnt = take(kStreamMaxCtas * 4);
   l.part = take(static_cast<size_t>(kStreamMaxCtas) * 2 * M * kLinStrip * 4);
-  l.xp = take(M > 8 ? static_cast<size_t>(M) * Kp * 2 : 0);
+  l.xp = take(M > 16 ? static_cast<size_t>(M) * Kp * 2 : 0);
   l.total = cur;
   return l;
 }

@@ -119,6 +119,24 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B.
+template <bool F16>
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // The two e4m3 values in the low (HI false) or high half of a word as fp16.
 template <bool HI>
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
@@ -386,112 +404,121 @@ __device__ __forceinline__ void stage_mma_fp8nk(uint32_t stage, uint32_t rows, i
         for (int i = 0; i < 4; ++i) acc[nt][mt][i] += t[nt][mt][i];
 }
 
-// Group scales (bf16 bits, zero point in the upper half) of a warp's 32 rows and
-// half of the k of one 256-k stage: lane c of a quad holds those of mma row g
-// (even c) or g + 8 (odd c) of tile c / 2, a slot for each group.
-template <int GRP>
+// Group scales (bf16 bits) and zero points of a warp's 32 rows and half of the k of
+// one 256-k stage: lane c of a quad holds those of mma row g (even c) or g + 8 (odd
+// c) of tile c / 2, a slot for each group.  As they were loaded: a conversion here
+// would wait for the loads.
+template <int GRP, bool ZERO>
 struct W4Scales {
   static constexpr int kSlots = 128 / GRP;
-  uint32_t v[kSlots];
+  uint32_t v[kSlots], z[ZERO ? kSlots : 1];
 };
 // `at`: index of the lane's row's first group (-1: a row outside the matrix),
 // groups = groups of a row; q0 = the first group.
-template <int GRP>
-__device__ __forceinline__ void w4_load_scales(W4Scales<GRP>& s, const __nv_bfloat16* sc, const uint8_t* zp,
+template <int GRP, bool ZERO>
+__device__ __forceinline__ void w4_load_scales(W4Scales<GRP, ZERO>& s, const __nv_bfloat16* sc, const uint8_t* zp,
                                                long long at, int groups, int q0) {
 #pragma unroll
-  for (int i = 0; i < W4Scales<GRP>::kSlots; ++i) {
-    uint32_t w = 8u << 16;
+  for (int i = 0; i < W4Scales<GRP, ZERO>::kSlots; ++i) {
+    s.v[i] = 0;
+    if (ZERO) s.z[i] = 0;
     if (at >= 0 && q0 + i < groups) {
-      w = __ldg(reinterpret_cast<const unsigned short*>(sc) + at + q0 + i) |
-          (zp ? static_cast<uint32_t>(__ldg(zp + at + q0 + i) & 15u) << 16 : 8u << 16);
+      s.v[i] = __ldg(reinterpret_cast<const unsigned short*>(sc) + at + q0 + i);
+      if (ZERO) s.z[i] = __ldg(zp + at + q0 + i);
     }
-    s.v[i] = w;
   }
 }
 
-// (Groups beyond the end of a row have scale 0 and zero token rows.)
-template <int GRP, int NT, bool ZERO, bool F16>
+// 4-bit weights: 32 rows x 128 k of the stage.  NI tiles of eight tokens share the
+// converted codes and MI tiles of 16 rows the loads of the tokens; the rest is done
+// again, which saves registers.  (Groups beyond the end of a row have scale 0 and
+// zero token rows.)
+template <int GRP, int NT, int NI, int MI, bool ZERO, bool F16>
 __device__ __forceinline__ void stage_mma_w4(uint32_t stage, uint32_t rows, int warp, int lane, int ntu,
-                                             const W4Scales<GRP>& sc, float (&acc)[NT][2][4]) {
+                                             const W4Scales<GRP, ZERO>& sc, float (&acc)[NT][2][4]) {
   static_assert(!(ZERO && F16), "zero points come with bf16 operands");
   using Tr = StreamTraits<kStreamW4, GRP>;
   constexpr int J = GRP / 32, QB = 128 / GRP;
-  constexpr int CH = NT == 1 ? 2 : 1;  // for few rows: two chains of multiplies a tile
   const int g = lane >> 2, c = lane & 3, kh = warp & 1;
   const int r = nk_row<kStreamW4, GRP>(g);
   const uint32_t base = stage + ((warp >> 1) * 32 + r) * 128;
   const uint32_t ba = rows + g * Tr::PITCH + kh * 256 + c * 16;
   const int from = lane & ~3;
 #pragma unroll
-  for (int q = 0; q < QB; ++q) {
-    uint32_t w[2][2][J];  // [tile][row g, g + 8][word]
-    const int qq = kh * QB + q;
+  for (int m0 = 0; m0 < 2; m0 += MI) {
+    uint32_t w[MI][2][4];  // [tile][row g, g + 8][word of eight codes]
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int m = 0; m < MI; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t at = base + mt * 2048 + h * 1024;
+        const uint32_t at = base + (m0 + m) * 2048 + h * 1024;
         if constexpr (GRP == 128) {
-          const uint4 u = lds128(at + (static_cast<uint32_t>((4 * qq + c) ^ (r & 7)) << 4));
-          w[mt][h][0] = u.x; w[mt][h][1] = u.y; w[mt][h][2] = u.z; w[mt][h][3] = u.w;
+          const uint4 u = lds128(at + (static_cast<uint32_t>((4 * kh + c) ^ (r & 7)) << 4));
+          w[m][h][0] = u.x; w[m][h][1] = u.y; w[m][h][2] = u.z; w[m][h][3] = u.w;
         } else if constexpr (GRP == 64) {
-          const uint2 u = lds64(at + (static_cast<uint32_t>((2 * qq + (c >> 1)) ^ (r & 7)) << 4) + (c & 1) * 8);
-          w[mt][h][0] = u.x; w[mt][h][1] = u.y;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint2 u = lds64(at + (static_cast<uint32_t>((4 * kh + 2 * q + (c >> 1)) ^ (r & 7)) << 4) + (c & 1) * 8);
+            w[m][h][2 * q] = u.x; w[m][h][2 * q + 1] = u.y;
+          }
         } else {
-          w[mt][h][0] = lds32(at + (static_cast<uint32_t>(qq ^ (r & 7)) << 4) + c * 4);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[m][h][q] = lds32(at + (static_cast<uint32_t>((4 * kh + q) ^ (r & 7)) << 4) + c * 4);
         }
       }
-    float f[2][2];
-    uint32_t z[2][2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int n0 = 0; n0 < NT; n0 += NI) {
+      if (n0 >= ntu) break;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t v = __shfl_sync(0xffffffffu, sc.v[q], from | (2 * mt + h));
-        f[mt][h] = __uint_as_float(v << 16);
-        z[mt][h] = ZERO ? 0x43004300u | (v >> 16) | (v & 0xffff0000u) : 0x43084308u;  // 128 + zero point
-      }
-    float part[NT][2][CH][4];
+      for (int q = 0; q < QB; ++q) {
+        float f[MI][2];
+        uint32_t z[MI][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int m = 0; m < MI; ++m)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int h = 0; h < CH; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) part[nt][mt][h][i] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      uint32_t a[2][4], b[2][4];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        w4_pairs<F16>(w[mt][0][j], z[mt][0], a[mt]);
-        w4_pairs<F16>(w[mt][1][j], z[mt][1], b[mt]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (nt < ntu) {
-          const uint4 x = lds128(ba + nt * 8 * Tr::PITCH + (q * J + j) * 64);
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            mma_16816<F16>(part[nt][mt][0], a[mt][0], b[mt][0], a[mt][1], b[mt][1], x.x, x.y);
-            mma_16816<F16>(part[nt][mt][CH - 1], a[mt][2], b[mt][2], a[mt][3], b[mt][3], x.z, x.w);
+          for (int h = 0; h < 2; ++h) {
+            f[m][h] = __uint_as_float(__shfl_sync(0xffffffffu, sc.v[q], from | (2 * (m0 + m) + h)) << 16);
+            z[m][h] = 0x43084308u;  // 128 + zero point
+            if (ZERO) {
+              const uint32_t v = __shfl_sync(0xffffffffu, sc.z[q], from | (2 * (m0 + m) + h)) & 15u;
+              z[m][h] = 0x43004300u | v | (v << 16);
+            }
           }
+        float part[NI][MI][4];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          uint32_t a[MI][4], b[MI][4];
+#pragma unroll
+          for (int m = 0; m < MI; ++m) {
+            w4_pairs<F16>(w[m][0][q * J + j], z[m][0], a[m]);
+            w4_pairs<F16>(w[m][1][q * J + j], z[m][1], b[m]);
+          }
+#pragma unroll
+          for (int n = 0; n < NI; ++n)
+            if (n0 + n < ntu) {
+              const uint4 x = lds128(ba + (n0 + n) * 8 * Tr::PITCH + (q * J + j) * 64);
+#pragma unroll
+              for (int m = 0; m < MI; ++m) {
+                if (j == 0) mma_16816_first<F16>(part[n][m], a[m][0], b[m][0], a[m][1], b[m][1], x.x, x.y);
+                else mma_16816<F16>(part[n][m], a[m][0], b[m][0], a[m][1], b[m][1], x.x, x.y);
+              }
+#pragma unroll
+              for (int m = 0; m < MI; ++m)
+                mma_16816<F16>(part[n][m], a[m][2], b[m][2], a[m][3], b[m][3], x.z, x.w);
+            }
         }
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+          if (n0 + n < ntu) {
+#pragma unroll
+            for (int m = 0; m < MI; ++m)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[n0 + n][m0 + m][e] = fmaf(f[m][e >> 1], part[n][m][e], acc[n0 + n][m0 + m][e]);
+          }
+      }
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      if (nt < ntu) {
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = part[nt][mt][0][i];
-            if (CH == 2) v += part[nt][mt][CH - 1][i];
-            acc[nt][mt][i] = fmaf(f[mt][i >> 1], v, acc[nt][mt][i]);
-          }
-      }
   }
 }
 
