@@ -148,11 +148,20 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's (device) -> cudaStream_t of its current stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        global _raw_stream
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            # an integer straight away where this torch has it: building a Stream
+            # object takes microseconds
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -268,9 +277,16 @@ def moe_linear_w4_workspace_size(M: int, K: int, N: int) -> int:
     return int(load_library().moe_linear_w4_workspace_size(M, K, N))
 
 
+_FLOAT_DTYPES = {}
+
+
 def _float_dtype(t) -> int:
     """moe_dtype_t of a tensor's dtype (-1: none, which the library refuses)."""
-    return {"torch.float32": MOE_F32, "torch.bfloat16": MOE_BF16}.get(str(t.dtype), -1)
+    if not _FLOAT_DTYPES:
+        import torch
+
+        _FLOAT_DTYPES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16})
+    return _FLOAT_DTYPES.get(t.dtype, -1)
 
 
 def moe_linear_w4(M: int, K: int, N: int, group: int, x, Wq, scales, zeros, y, ws, stream=None) -> None:

@@ -160,7 +160,10 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
   }
   // (at least w[0] units, so at least one chunk, for every CTA that has a part)
   f.sp.N = f.shared * f.w[0] + static_cast<long long>(na) * f.S[1] * f.C[1] * f.w[1];
-  f.sp.Gp = f.sp.N >= static_cast<long long>(G) * f.w[0] ? G : static_cast<int>(f.sp.N) / f.w[0];
+  // Small layers: a CTA takes four chunks at least, or a whole short strip.  A strip
+  // that CTAs share costs its last one about 4 us, as much as ten chunks take.
+  const int least = f.w[0] * max(4, min(8, f.C[1]));
+  f.sp.Gp = f.sp.N >= static_cast<long long>(G) * least ? G : max(1, static_cast<int>(f.sp.N) / least);
   f.lo = few_chunk(f, split_lo(f.sp, b));
   f.hi = few_chunk(f, split_lo(f.sp, b + 1));
   return f;
@@ -486,19 +489,17 @@ struct Few {
     if (DOWN) return;
     const int c0 = few_cta(f, q0), c1 = few_cta(f, q0 + f.C[at.r] - 1);
     int last = 0;
-    __threadfence();
     if (THREADS == 32) {
       __syncwarp();
-      if (i0 == 0) last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+      if (i0 == 0) last = arrive_acq_rel(p.cnt + c0) == c1 - c0;
       last = __shfl_sync(0xffffffffu, last, 0);
     } else {
       bar();
-      if (i0 == 0) ctl->ring.last[1] = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+      if (i0 == 0) ctl->ring.last[1] = arrive_acq_rel(p.cnt + c0) == c1 - c0;
       bar();
       last = *reinterpret_cast<volatile int*>(&ctl->ring.last[1]);
     }
     if (!last) return;
-    __threadfence();
     const size_t step = static_cast<size_t>(2) * p.T * 2 * Tr::HC;  // from a CTA's parts to the next one's
     const float* head = part_at(p, c0, 1);
     const float* rest = part_at(p, c0 + 1, 0);
@@ -723,6 +724,25 @@ struct Few {
   // one warp; ctl->cnt is zero on entry.
   static __device__ __forceinline__ void build_lists(const FewParams& p, Ctrl* ctl, int lane) {
     const int R = p.T * p.k;
+    if (p.T == 1) {  // k different experts, a row each
+      const int e = lane < R ? ctl->ids[lane] : 0x7fffffff;
+      int at = 0;
+#pragma unroll 1
+      for (int j = 0; j < R; ++j) at += __shfl_sync(0xffffffffu, e, j) < e;
+      if (lane < R) {
+        ctl->aexp[at] = static_cast<uint16_t>(e);
+        ctl->amap[e] = static_cast<uint16_t>(at);
+        ctl->aoff[at] = static_cast<uint16_t>(at);
+        ctl->pos[lane] = static_cast<uint16_t>(at);
+        ctl->srow[lane] = 0;
+      }
+      if (lane == 0) {
+        ctl->na = R;
+        ctl->aoff[R] = static_cast<uint16_t>(R);
+        ctl->srow[R] = 0;  // the shared expert's row
+      }
+      return;
+    }
     // a row's rank among the rows of its expert, 32 rows at a time
 #pragma unroll 1
     for (int r0 = 0; r0 < R; r0 += 32) {
@@ -992,6 +1012,8 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   // (every named barrier but the consumers' own is used once: a role without
   // work of its own may be at its next one before the others reach the last)
   if (tid == 0) p.cnt[b] = 0;
+  // one token: k entries, whatever the routing
+  if (p.T == 1 && tid >= 32 && tid < 34) ctl->pass[tid - 32] = few_pass<KIND, GRP>(p, tid == 33, p.k, G, b);
   if (Tr::F16)
     for (int r = b * CT + tid; r < R + p.T; r += G * CT) p.hmax[r] = 0;
   // phase 0
@@ -1023,7 +1045,7 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   if (tid < 32) {
     F::build_lists(p, ctl, lane);
     __syncwarp();
-    if (lane < 2) ctl->pass[lane] = few_pass<KIND, GRP>(p, lane == 1, ctl->na, G, b);
+    if (p.T > 1 && lane < 2) ctl->pass[lane] = few_pass<KIND, GRP>(p, lane == 1, ctl->na, G, b);
   }
   F::bar();
   asm volatile("bar.arrive 4, %0;" ::"n"(CT + 32 * Sm::kFeeders + 32) : "memory");
@@ -1053,7 +1075,9 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
     const int per = p.D / 8, l = lane & 7, items = p.T * per;
     const int terms = p.k + (shared ? 1 : 0);
 #pragma unroll 1
-    for (int i0 = (b * CT + tid) >> 3; i0 - (lane >> 3) < items; i0 += (G * CT) >> 3) {
+    // (item groups of a warp's four are dealt to the CTAs in turn)
+    for (int w0 = (tid >> 5) * G + b; w0 * 4 < items; w0 += G * (CT / 32)) {
+      const int i0 = w0 * 4 + (lane >> 3);
       const bool in = i0 < items;
       const int i = in ? i0 : items - 1;
       const int t = i / per, d0 = (i - t * per) * 8;

@@ -92,11 +92,10 @@ __device__ __noinline__ void lin_finish(const LinParams& p, const Split& sp, con
   const long long q0 = static_cast<long long>(s) * C;
   const int c0 = split_cta(sp, q0), c1 = split_cta(sp, q0 + C - 1);
   int last = 0;
-  __threadfence();
   if (THREADS == 32) __syncwarp();
   else bar_consumers<THREADS>();
   if (i0 == 0) {
-    last = atomicAdd(p.cnt + c0, 1) == c1 - c0;
+    last = arrive_acq_rel(p.cnt + c0) == c1 - c0;
     if (last) p.cnt[c0] = 0;
     *flag = last;
   }
@@ -107,7 +106,6 @@ __device__ __noinline__ void lin_finish(const LinParams& p, const Split& sp, con
     last = *reinterpret_cast<volatile int*>(flag);
   }
   if (!last) return;
-  __threadfence();
   const float* head = p.part + (static_cast<size_t>(c0) * 2 + 1) * items;
   const float* rest = p.part + static_cast<size_t>(c0 + 1) * 2 * items;
   constexpr int U = 4;

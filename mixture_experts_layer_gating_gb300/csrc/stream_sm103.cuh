@@ -212,6 +212,14 @@ struct StreamRing {
   }
 };
 
+// Adds 1 to an arrival count (release: what this thread saw written, its own CTA's
+// earlier writes before a barrier among them; acquire: what the others wrote).
+__device__ __forceinline__ int arrive_acq_rel(int32_t* p) {
+  int v;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // Position in a ring of n slots.
 struct RingPos {
   int at = 0;
