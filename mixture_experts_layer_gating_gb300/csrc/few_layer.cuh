@@ -107,7 +107,7 @@ struct FewSmem {
     StreamRing ring;
     int na;
     FewPass pass[2];        // gate/up, down
-    int cnt[512];           // rows of an expert
+    int cnt[512];           // rows of an expert (many rows); expert and rank of a sorted row (few)
     int ids[kFewMaxR];      // expert of an expanded row
     float w[kFewMaxR];      // its weight
     // the chosen experts in ascending order, one entry for each group of 16 rows
@@ -153,10 +153,9 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
   f.shared = static_cast<long long>(f.shared_entries) * f.S[0] * f.C[0];
   f.w[0] = f.w[1] = 1;
   if (p.T > 8 && f.shared > 0) {
-    // measured on the CTAs that stream the shared expert: 1.1 times a routed chunk's
-    // time, 1.3 to 1.5 in the down pass of 4-bit weights
-    f.w[0] = KIND == kStreamW4 && down ? 3 : 9;
-    f.w[1] = KIND == kStreamW4 && down ? 2 : 8;
+    // measured on the CTAs that stream the shared expert of 16 tokens
+    f.w[0] = KIND == kStreamW4 || down ? 9 : 1;
+    f.w[1] = KIND == kStreamW4 || down ? 8 : 1;
   }
   // (at least w[0] units, so at least one chunk, for every CTA that has a part)
   f.sp.N = f.shared * f.w[0] + static_cast<long long>(na) * f.S[1] * f.C[1] * f.w[1];
@@ -311,84 +310,115 @@ struct Few {
   }
   static __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
 
-  // The token rows of the run's chunks that this feeder warp takes (every
-  // kFeeders-th, always the same slots: a wait cannot mistake a fill for the one
-  // before).  n rows x KCH inputs, 8 inputs a lane.
+  // The token rows of the run's chunks that this feeder warp takes: those of every
+  // second slot (always the same slots, so that a wait cannot mistake a fill for the
+  // one before).  n rows x KCH inputs, 8 inputs a lane.
   template <bool DOWN>
   static __device__ __forceinline__ bool feed(const FewParams& p, const FewPass& f, Ctrl* ctl, uint8_t* ring,
-                                              RingPos& pos, int& turn, int lane) {
+                                              RingPos& ring_pos, int me, int lane) {
     constexpr int P = Tr::KCH / 8;  // pieces of a row
+    static_assert(Sm::kFeeders == 2 && Sm::NST % 2 == 0, "slots of a feeder");
     if (f.lo >= f.hi) return true;
-    FewAt at(f, f.lo);
+    const int total = static_cast<int>(f.hi - f.lo), skip = (ring_pos.at + me) & 1;
+    RingPos pos = ring_pos;
+    if (skip) pos.next(Sm::NST);
+    ring_pos.skip(total % Sm::NST, Sm::NST);
+    ring_pos.phase ^= (total / Sm::NST) & 1;
+    if (skip >= total) return true;
+    FewAt at(f, f.lo + skip);
+    if constexpr (DOWN && !Sm::kHilo) {
+      // fp32 h to scaled fp16, in the weights' k order; the first pieces of the
+      // feeder's next chunk are loaded before it waits for that chunk's slot
+      constexpr int U = P == 4 ? 2 : 4;  // pieces in flight
+      float4 a[U], b[U];
+      uint32_t mx[U];
+      auto load = [&](const FewAt& x, int first, int n, int i0) {
+        const int k_end = f.K[x.r] - x.kc * Tr::KCH;  // inputs of this chunk (zeros beyond)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + 32 * u, pc = i % P, row = i / P;
+          a[u] = b[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          mx[u] = 0;
+          if (i < n * P && pc * 8 < k_end) {
+            const int r = first + row;
+            const float4* src = reinterpret_cast<const float4*>(
+                static_cast<const float*>(p.hp) + static_cast<size_t>(r) * p.Ip + x.kc * Tr::KCH + pc * 8);
+            a[u] = src[0];  // (through L1: every strip takes the same rows)
+            b[u] = src[1];
+            mx[u] = p.hmax[r];
+          }
+        }
+      };
+      auto store = [&](uint8_t* rows, int n, int i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + 32 * u, pc = i % P, row = i / P;
+          if (i < n * P) {
+            const float sc = exp2_int(row_exp(mx[u]));
+            const float v[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
+            uint8_t* d = rows + row * Tr::PITCH;
+            auto pair = [&](int j0, int j1) {
+              const __half2 h = __floats2half2_rn(v[j0] * sc, v[j1] * sc);
+              return *reinterpret_cast<const uint32_t*>(&h);
+            };
+            const int at8 = perm_k<KIND, GRP>(pc * 8) * 2;
+            if constexpr (Tr::KN) {  // pairs go to every other word
+#pragma unroll
+              for (int j = 0; j < 8; j += 2) *reinterpret_cast<uint32_t*>(d + at8 + j * 4) = pair(j, j + 1);
+            } else if constexpr (KIND == kStreamW4) {
+              *reinterpret_cast<uint4*>(d + at8) = make_uint4(pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7));
+            } else {
+              // (pieces of 16 inputs: the second one lies 64 bytes on)
+              *reinterpret_cast<uint4*>(d + at8) = make_uint4(pair(0, 1), pair(2, 3), pair(4, 5), pair(6, 7));
+            }
+          }
+        }
+      };
+      int first = row_first(p, ctl, at), n = row_count(p, ctl, at);
+      load(at, first, n, lane);
 #pragma unroll 1
-    for (int left = static_cast<int>(f.hi - f.lo); left > 0; --left) {
-      if (turn == 0) {
+      for (int left = total - skip; left > 0; left -= 2) {
         if (!mbar_wait(&ctl->ring.empty[pos.at], pos.phase ^ 1u, &ctl->ring.abort)) return false;
-        const int first = row_first(p, ctl, at), n = row_count(p, ctl, at);
         uint8_t* rows = ring + pos.at * Sm::kSlot + kStageBytes;
-        if (DOWN && !Sm::kHilo) {
-          // fp32 h to scaled fp16, in the weights' k order
-          const int k_end = f.K[at.r] - at.kc * Tr::KCH;  // inputs of this chunk (zeros beyond)
-          constexpr int U = 4;                      // pieces in flight
-          for (int i0 = lane; i0 < n * P; i0 += 32 * U) {
-            float4 a[U], b[U];
-            uint32_t mx[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int i = i0 + 32 * u, pc = i % P, row = i / P;
-              a[u] = b[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              mx[u] = 0;
-              if (i < n * P && pc * 8 < k_end) {
-                const int r = first + row;
-                const float4* src = reinterpret_cast<const float4*>(
-                    static_cast<const float*>(p.hp) + static_cast<size_t>(r) * p.Ip + at.kc * Tr::KCH + pc * 8);
-                a[u] = src[0];  // (through L1: every strip takes the same rows)
-                b[u] = src[1];
-                mx[u] = p.hmax[r];
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int i = i0 + 32 * u, pc = i % P, row = i / P;
-              if (i < n * P) {
-                const float sc = exp2_int(row_exp(mx[u]));
-                const float v[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
-                uint8_t* d = rows + row * Tr::PITCH;
-                auto pair = [&](int j0, int j1) {
-                  const __half2 h = __floats2half2_rn(v[j0] * sc, v[j1] * sc);
-                  return *reinterpret_cast<const uint32_t*>(&h);
-                };
-                const int at8 = perm_k<KIND, GRP>(pc * 8) * 2;
-                if constexpr (Tr::KN) {  // pairs go to every other word
-#pragma unroll
-                  for (int j = 0; j < 8; j += 2) *reinterpret_cast<uint32_t*>(d + at8 + j * 4) = pair(j, j + 1);
-                } else if constexpr (KIND == kStreamW4) {
-                  *reinterpret_cast<uint4*>(d + at8) = make_uint4(pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7));
-                } else {
-                  *reinterpret_cast<uint4*>(d + at8) = make_uint4(pair(0, 1), pair(2, 3), pair(4, 5), pair(6, 7));
-                }
-              }
-            }
-          }
-          mbar_arrive(&ctl->ring.full[pos.at]);
-        } else {
-          const uint32_t dst = smem_u32(rows);
-          const size_t plane = static_cast<size_t>(p.T * p.k + p.T) * p.Ip;
-          for (int i = lane; i < n * P; i += 32) {
-            const int pc = i % P, row = i / P;
-            const int src = DOWN ? first + row : ctl->srow[first + row];
-            const uint16_t* g = (DOWN ? static_cast<const uint16_t*>(p.hp) : p.xp) +
-                                static_cast<size_t>(src) * (DOWN ? p.Ip : p.Dp) + at.kc * Tr::KCH + pc * 8;
-            const uint32_t d = dst + row * Tr::PITCH + pc * 16;
-            cp_async_16(d, g, 16);
-            if (DOWN) cp_async_16(d + 8 * NT * Tr::PITCH, g + plane, 16);
-          }
-          cp_async_mbar_arrive_noinc(&ctl->ring.full[pos.at]);
+        store(rows, n, lane);
+#pragma unroll 1
+        for (int i0 = lane + 32 * U; i0 - lane < n * P; i0 += 32 * U) {
+          load(at, first, n, i0);
+          store(rows, n, i0);
+        }
+        mbar_arrive(&ctl->ring.full[pos.at]);
+        pos.skip(2, Sm::NST);
+        if (left > 2) {
+          at.next(f);
+          at.next(f);
+          first = row_first(p, ctl, at);
+          n = row_count(p, ctl, at);
+          load(at, first, n, lane);
         }
       }
-      turn = turn == 0 ? Sm::kFeeders - 1 : turn - 1;
-      pos.next(Sm::NST);
-      at.next(f);
+    } else {
+#pragma unroll 1
+      for (int left = total - skip; left > 0; left -= 2) {
+        if (!mbar_wait(&ctl->ring.empty[pos.at], pos.phase ^ 1u, &ctl->ring.abort)) return false;
+        const int first = row_first(p, ctl, at), n = row_count(p, ctl, at);
+        const uint32_t dst = smem_u32(ring) + pos.at * Sm::kSlot + kStageBytes;
+        const size_t plane = static_cast<size_t>(p.T * p.k + p.T) * p.Ip;
+        for (int i = lane; i < n * P; i += 32) {
+          const int pc = i % P, row = i / P;
+          const int src = DOWN ? first + row : ctl->srow[first + row];
+          const uint16_t* g = (DOWN ? static_cast<const uint16_t*>(p.hp) : p.xp) +
+                              static_cast<size_t>(src) * (DOWN ? p.Ip : p.Dp) + at.kc * Tr::KCH + pc * 8;
+          const uint32_t d = dst + row * Tr::PITCH + pc * 16;
+          cp_async_16(d, g, 16);
+          if (DOWN) cp_async_16(d + 8 * NT * Tr::PITCH, g + plane, 16);
+        }
+        cp_async_mbar_arrive_noinc(&ctl->ring.full[pos.at]);
+        pos.skip(2, Sm::NST);
+        if (left > 2) {
+          at.next(f);
+          at.next(f);
+        }
+      }
     }
     return true;
   }
@@ -720,29 +750,54 @@ struct Few {
     warp_topk_softmax<EPL>(v, lane, p.E, p.k, p.renorm, nullptr, keep, ids, w, p.err);
   }
 
-  // The chosen experts in ascending order and their rows in ascending order, by
-  // one warp; ctl->cnt is zero on entry.
+  // The chosen experts in ascending order and their rows in ascending order.  Few
+  // rows (at most 160): every row counts the rows that come before it.
+  static constexpr int kPairRows = 160;
+  static __device__ __forceinline__ void build_lists_pairs(const FewParams& p, Ctrl* ctl, int tid) {
+    const int R = p.T * p.k;
+    if (tid < kPairRows) {  // (whole warps)
+      const int e = tid < R ? ctl->ids[tid] : 0x7fffffff;
+      int before = 0, same = 0;
+#pragma unroll 4
+      for (int r = 0; r < R; ++r) {
+        const int o = ctl->ids[r];
+        before += o < e;
+        same += o == e && r < tid;
+      }
+      if (tid < R) {
+        const int at = before + same;
+        ctl->pos[tid] = static_cast<uint16_t>(at);
+        ctl->srow[at] = static_cast<uint16_t>(tid / p.k);
+        ctl->cnt[at] = e | (same << 16);  // expert and rank of the sorted row
+      }
+    }
+    if (tid < p.T) ctl->srow[R + tid] = static_cast<uint16_t>(tid);
+    bar();
+    if (tid < 32) {  // an entry begins at every 16th row of an expert
+      int entries = 0;
+#pragma unroll 1
+      for (int r0 = 0; r0 < R; r0 += 32) {
+        const int at = r0 + tid, v = at < R ? ctl->cnt[at] : 1 << 16;
+        const bool head = at < R && ((v >> 16) & (kFewGroup - 1)) == 0;
+        const unsigned m = __ballot_sync(0xffffffffu, head);
+        const int a = entries + __popc(m & ((1u << tid) - 1u));
+        if (head) {
+          ctl->aexp[a] = static_cast<uint16_t>(v & 0xffff);
+          ctl->aoff[a] = static_cast<uint16_t>(at);
+          if ((v >> 16) == 0) ctl->amap[v & 0xffff] = static_cast<uint16_t>(a);
+        }
+        entries += __popc(m);
+      }
+      if (tid == 0) {
+        ctl->na = entries;
+        ctl->aoff[entries] = static_cast<uint16_t>(R);
+      }
+    }
+  }
+
+  // The same for many rows, by one warp; ctl->cnt is zero on entry.
   static __device__ __forceinline__ void build_lists(const FewParams& p, Ctrl* ctl, int lane) {
     const int R = p.T * p.k;
-    if (p.T == 1) {  // k different experts, a row each
-      const int e = lane < R ? ctl->ids[lane] : 0x7fffffff;
-      int at = 0;
-#pragma unroll 1
-      for (int j = 0; j < R; ++j) at += __shfl_sync(0xffffffffu, e, j) < e;
-      if (lane < R) {
-        ctl->aexp[at] = static_cast<uint16_t>(e);
-        ctl->amap[e] = static_cast<uint16_t>(at);
-        ctl->aoff[at] = static_cast<uint16_t>(at);
-        ctl->pos[lane] = static_cast<uint16_t>(at);
-        ctl->srow[lane] = 0;
-      }
-      if (lane == 0) {
-        ctl->na = R;
-        ctl->aoff[R] = static_cast<uint16_t>(R);
-        ctl->srow[R] = 0;  // the shared expert's row
-      }
-      return;
-    }
     // a row's rank among the rows of its expert, 32 rows at a time
 #pragma unroll 1
     for (int r0 = 0; r0 < R; r0 += 32) {
@@ -980,11 +1035,11 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   }
   if (tid >= CT + 32) {  // -------------------------------------------- feeders
     RingPos pos;
-    int turn = (tid - CT - 32) >> 5;
+    const int me = (tid - CT - 32) >> 5;
     asm volatile("bar.sync 4, %0;" ::"n"(CT + 32 * Sm::kFeeders + 32) : "memory");  // x rows and expert lists are there
-    bool ok = F::template feed<false>(p, ctl->pass[0], ctl, ring, pos, turn, lane);
+    bool ok = F::template feed<false>(p, ctl->pass[0], ctl, ring, pos, me, lane);
     asm volatile("bar.sync 3, %0;" ::"n"(CT + 32 * Sm::kFeeders) : "memory");  // h rows are there
-    if (ok) ok = F::template feed<true>(p, ctl->pass[1], ctl, ring, pos, turn, lane);
+    if (ok) ok = F::template feed<true>(p, ctl->pass[1], ctl, ring, pos, me, lane);
     if (!ok) sr->give_up(p.err);
     cp_async_wait_all();
     return;
@@ -1023,7 +1078,8 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   F::grid_sync(p, sr, 0, 3);
 
   // phase 1
-  for (int e = tid; e < p.E; e += CT) ctl->cnt[e] = 0;
+  if (R > F::kPairRows)
+    for (int e = tid; e < p.E; e += CT) ctl->cnt[e] = 0;
   if (p.nplanes * p.T * p.E * 4 <= kFewPlaneBytes) {
     F::topk(p, 0, 1, b == 0, ctl->ids, ctl->w, red);
     if (b == 0)
@@ -1042,8 +1098,9 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
     }
     F::bar();
   }
+  if (R <= F::kPairRows) F::build_lists_pairs(p, ctl, tid);
   if (tid < 32) {
-    F::build_lists(p, ctl, lane);
+    if (R > F::kPairRows) F::build_lists(p, ctl, lane);
     __syncwarp();
     if (p.T > 1 && lane < 2) ctl->pass[lane] = few_pass<KIND, GRP>(p, lane == 1, ctl->na, G, b);
   }
