@@ -77,7 +77,7 @@ __device__ __forceinline__ float few_act(float g, float u, int act) {
 // chunks.  Index 0 of
 // S, C, K, width: the shared expert, 1: the routed ones.
 struct FewPass {
-  // A chunk counts w[r] units in the split: rows beyond eight make a shared
+  // A chunk counts w[r] units in the split: more than eight rows make a shared
   // expert's chunk slower than HBM (two tiles to multiply, more rows to feed).
   Split sp;
   int w[2];
@@ -153,9 +153,12 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
   f.shared = static_cast<long long>(f.shared_entries) * f.S[0] * f.C[0];
   f.w[0] = f.w[1] = 1;
   if (p.T > 8 && f.shared > 0) {
-    // measured on the CTAs that stream the shared expert of 16 tokens
-    f.w[0] = KIND == kStreamW4 || down ? 9 : 1;
-    f.w[1] = KIND == kStreamW4 || down ? 8 : 1;
+    // The down rows of 4-bit and e4m3 [N, K] weights are many to a stage.  16 tokens,
+    // shared expert 1% to 6% of the bytes, against equal weights: 4-bit 16 to 32 tokens
+    // 153 -> 144 and 185 -> 172 us; e4m3 [K, N] 856 -> 799; e4m3 [N, K] 1013 -> 813.
+    constexpr bool nk8 = KIND == kStreamFp8Nk;
+    if (KIND == kStreamW4) f.w[0] = 4, f.w[1] = 3;
+    else if (down) f.w[0] = nk8 ? 9 : 3, f.w[1] = nk8 ? 4 : 2;
   }
   // (at least w[0] units, so at least one chunk, for every CTA that has a part)
   f.sp.N = f.shared * f.w[0] + static_cast<long long>(na) * f.S[1] * f.C[1] * f.w[1];
@@ -329,7 +332,7 @@ struct Few {
     if constexpr (DOWN && !Sm::kHilo) {
       // fp32 h to scaled fp16, in the weights' k order; the first pieces of the
       // feeder's next chunk are loaded before it waits for that chunk's slot
-      constexpr int U = P == 4 ? 2 : 4;  // pieces in flight
+      constexpr int U = P == 4 ? 2 : 4;  // pieces in flight (eight spill: slower)
       float4 a[U], b[U];
       uint32_t mx[U];
       auto load = [&](const FewAt& x, int first, int n, int i0) {
