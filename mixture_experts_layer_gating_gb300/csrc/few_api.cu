@@ -164,7 +164,7 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
 
 size_t moe_linear_w4_workspace_size(int32_t M, int32_t K, int32_t N) {
   if (M < 0 || M > kStreamMaxRows || K < 32 || K % 32 || N < 1) return 0;
-  return sizeof(ControlBlock) + linear_w4_scratch(std::max(M, 1), K).total;
+  return sizeof(ControlBlock) + linear_w4_scratch(std::max(M, 1), K, N).total;
 }
 
 int moe_linear_w4(int32_t M, int32_t K, int32_t N, int32_t group, const void* x, const void* Wq,

@@ -1,140 +1,34 @@
-// y = x W^T for at most 32 rows of x and 4-bit weights with group scales
-// (moe_linear_w4), and the weights' way into and out of the 4-bit form.
-#include "stream_sm103.cuh"
+// y = x W^T for a few rows of x and 4-bit weights with group scales (moe_linear_w4;
+// linear_w4_wide.cu has it for more), and the weights' way into and out of the 4-bit form.
+#include "linear_w4.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kLinStrip = 128;  // output features of a strip (one stage's rows)
-
-struct LinParams {
-  const __nv_bfloat16* x;
-  const __nv_bfloat16* sc;
-  const uint8_t* zp;
-  void* y;
-  int32_t* err;
-  int32_t* cnt;   // [ctas] arrivals, zero between launches
-  float* part;    // [ctas][2][M][128]: a CTA's part of a strip begun earlier, of one it leaves unfinished
-  // more than 16 rows: x put in the weights' k order by a launch of its own
-  __nv_bfloat16* xp;  // [M][Kp], Kp whole stages
-  int M, K, N, Kp;
-};
-
 template <int GRP, int NT>
 struct LinSmem {
   using Tr = StreamTraits<kStreamW4, GRP>;
-  static constexpr int kTeams = NT <= 2 ? 2 : 1;
+  static constexpr int kTeams = 2;
   static constexpr int kCons = 32 * kStreamWarps * kTeams;
   static constexpr int kFeeders = 2;  // feeder warps
   static constexpr int kBlock = kCons + 32 + 32 * kFeeders + 32;  // + producer, feeders, finisher
   static constexpr int kSlot = stream_slot(8 * NT * Tr::PITCH);
   static constexpr int kRP = 128 + 4;
   static constexpr int kRedBytes = 8 * NT * kRP * 4;
-  static constexpr int kRedBufs = NT <= 2 ? 2 : 1;
+  static constexpr int kRedBufs = 2;
   static constexpr int kOther = kRedBufs * kRedBytes + static_cast<int>(sizeof(StreamRing)) + 16;
   static constexpr int NST = stream_stages(kSlot, kOther);
   static constexpr int kBytes = 1024 + NST * kSlot + kOther;
   static_assert(NST >= 4 && NST % kFeeders == 0 && kBytes <= kStreamSmemMax, "shared memory");
 };
 
-__device__ __forceinline__ void store_y(float* y, size_t at, float v) { y[at] = v; }
-__device__ __forceinline__ void store_y(__nv_bfloat16* y, size_t at, float v) {
-  y[at] = __float2bfloat16_rn(v);
-}
-
-// x (more than 16 rows) in the weights' k order, padded with zeros: eight inputs
-// a thread.
-template <int GRP>
-__global__ void __launch_bounds__(256) linear_w4_order_kernel(const __grid_constant__ LinParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int k0 = (blockIdx.x * 256 + threadIdx.x) * 8, row = blockIdx.y;
-  if (k0 >= p.Kp) return;
-  uint4 x = make_uint4(0, 0, 0, 0);
-  if (k0 < p.K) x = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row) * p.K + k0));
-  uint4 v;
-  v.x = __byte_perm(x.x, x.z, 0x5410);
-  v.y = __byte_perm(x.x, x.z, 0x7632);
-  v.z = __byte_perm(x.y, x.w, 0x5410);
-  v.w = __byte_perm(x.y, x.w, 0x7632);
-  *reinterpret_cast<uint4*>(p.xp + static_cast<size_t>(row) * p.Kp + perm_k<kStreamW4, GRP>(k0)) = v;
-}
-
 // Who finishes a strip: all consumers the run's last one, when they have nothing
 // else to do, shared ones of more than two rows and any of more than eight (one
-// warp takes 12 us for 32 rows, longer than the strip streams); the finisher warp
-// the others.
+// warp takes about 0.4 us a row, 16 rows longer than a short strip streams); the
+// finisher warp the others.
 __device__ __forceinline__ bool lin_by_consumers(int M, int C, int chunks, int left) {
   return left == 0 || M > 8 || (M > 2 && chunks != C);
-}
-
-// One strip's sums (or this CTA's part of them) to y by THREADS threads: the
-// finisher warp, or all consumers.  A strip inside one CTA's run is written at
-// once; one that several CTAs share gets its parts added, in the order of k, by
-// the CTA that arrives last (a count for each CTA that begins a shared strip).
-template <int THREADS, typename TY>
-__device__ __noinline__ void lin_finish(const LinParams& p, const Split& sp, const float* sums, int RP, int s, int kc,
-                                        int end, int C, int b, int i0, int* flag) {
-  TY* y = static_cast<TY*>(p.y);
-  const int n0 = s * kLinStrip, items = p.M * kLinStrip;
-  if (end == C && kc == 0) {
-#pragma unroll 4
-    for (int i = i0; i < items; i += THREADS) {
-      const int row = i / kLinStrip, col = i % kLinStrip;
-      if (n0 + col < p.N) store_y(y, static_cast<size_t>(row) * p.N + n0 + col, sums[row * RP + col]);
-    }
-    return;
-  }
-  float* mine = p.part + (static_cast<size_t>(b) * 2 + (kc ? 0 : 1)) * items;
-#pragma unroll 4
-  for (int i = i0; i < items; i += THREADS) mine[i] = sums[i / kLinStrip * RP + i % kLinStrip];
-  const long long q0 = static_cast<long long>(s) * C;
-  const int c0 = split_cta(sp, q0), c1 = split_cta(sp, q0 + C - 1);
-  int last = 0;
-  if (THREADS == 32) __syncwarp();
-  else bar_consumers<THREADS>();
-  if (i0 == 0) {
-    last = arrive_acq_rel(p.cnt + c0) == c1 - c0;
-    if (last) p.cnt[c0] = 0;
-    *flag = last;
-  }
-  if (THREADS == 32) {
-    last = __shfl_sync(0xffffffffu, last, 0);
-  } else {
-    bar_consumers<THREADS>();
-    last = *reinterpret_cast<volatile int*>(flag);
-  }
-  if (!last) return;
-  const float* head = p.part + (static_cast<size_t>(c0) * 2 + 1) * items;
-  const float* rest = p.part + static_cast<size_t>(c0 + 1) * 2 * items;
-  constexpr int U = 4;
-#pragma unroll 1
-  for (int i = i0; i < items; i += U * THREADS) {
-    float v[U], w[U], x[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int o = i + j * THREADS;
-      v[j] = w[j] = x[j] = 0.0f;
-      if (o < items) {
-        v[j] = __ldcg(head + o);
-        w[j] = __ldcg(rest + o);
-        if (c1 > c0 + 1) x[j] = __ldcg(rest + 2 * items + o);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j) v[j] = v[j] + w[j] + x[j];
-#pragma unroll 1
-    for (int cta = c0 + 3; cta <= c1; ++cta)
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        if (i + j * THREADS < items) v[j] += __ldcg(rest + static_cast<size_t>(cta - c0 - 1) * 2 * items + i + j * THREADS);
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int o = i + j * THREADS, n = n0 + o % kLinStrip;
-      if (o < items && n < p.N) store_y(y, static_cast<size_t>(o / kLinStrip) * p.N + n, v[j]);
-    }
-  }
 }
 
 // Strips of 128 output features x stages of 256 k, divided into equal runs over
@@ -170,7 +64,7 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
       if (lin_by_consumers(p.M, C, chunks, left)) continue;
       if (!mbar_wait(&sr->red_full[rpos.at], rpos.phase, &sr->abort)) sr->give_up(p.err);
       __syncwarp();
-      lin_finish<32, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, kc + chunks, C, b, lane, &sr->last[0]);
+      lin_finish<32, kLinStrip, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, kc + chunks, C, b, lane, &sr->last[0]);
       __syncwarp();
       mbar_arrive(&sr->red_empty[rpos.at]);
       rpos.next(Sm::kRedBufs);
@@ -185,58 +79,39 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     pos.skip(first, Sm::NST);
     kc = (kc + first) % C;
     left -= first;
-    if constexpr (NT <= 2) {
-      // up to 16 rows: 32 pieces of 8 inputs a row, one a lane, put in order on the
-      // way; the next stage's are loaded before this one's slot is waited for
-      const uint32_t pdst = perm_k<kStreamW4, GRP>(lane * 8) * 2;
-      uint4 x[8 * NT];
-      auto load = [&](int kc_) {
-        const int k0 = kc_ * 256 + lane * 8;
+    // 32 pieces of 8 inputs a row, one a lane, put in order on the way; the next stage's are loaded before this one's slot is waited for
+    const uint32_t pdst = perm_k<kStreamW4, GRP>(lane * 8) * 2;
+    uint4 x[8 * NT];
+    auto load = [&](int kc_) {
+      const int k0 = kc_ * 256 + lane * 8;
 #pragma unroll
-        for (int i = 0; i < 8 * NT; ++i) {
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (i < p.M && k0 < p.K) x[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(i) * p.K + k0));
-        }
-      };
-      if (left > 0) load(kc);
+      for (int i = 0; i < 8 * NT; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (i < p.M && k0 < p.K) x[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(i) * p.K + k0));
+      }
+    };
+    if (left > 0) load(kc);
 #pragma unroll 1
-      for (; left > 0; left -= Sm::kFeeders) {
-        if (!mbar_wait(&sr->empty[pos.at], pos.phase ^ 1u, &sr->abort)) {
-          sr->give_up(p.err);
-          break;
-        }
-        uint8_t* dst = ring + pos.at * Sm::kSlot + kStageBytes + pdst;
+    for (; left > 0; left -= Sm::kFeeders) {
+      if (!mbar_wait(&sr->empty[pos.at], pos.phase ^ 1u, &sr->abort)) {
+        sr->give_up(p.err);
+        break;
+      }
+      uint8_t* dst = ring + pos.at * Sm::kSlot + kStageBytes + pdst;
 #pragma unroll
-        for (int i = 0; i < 8 * NT; ++i) {
-          if (i >= p.M) break;
-          uint4 v;
-          v.x = __byte_perm(x[i].x, x[i].z, 0x5410);
-          v.y = __byte_perm(x[i].x, x[i].z, 0x7632);
-          v.z = __byte_perm(x[i].y, x[i].w, 0x5410);
-          v.w = __byte_perm(x[i].y, x[i].w, 0x7632);
-          *reinterpret_cast<uint4*>(dst + i * Tr::PITCH) = v;
-        }
-        mbar_arrive(&sr->full[pos.at]);
-        pos.skip(Sm::kFeeders, Sm::NST);
-        kc = (kc + Sm::kFeeders) % C;
-        if (left > Sm::kFeeders) load(kc);
+      for (int i = 0; i < 8 * NT; ++i) {
+        if (i >= p.M) break;
+        uint4 v;
+        v.x = __byte_perm(x[i].x, x[i].z, 0x5410);
+        v.y = __byte_perm(x[i].x, x[i].z, 0x7632);
+        v.z = __byte_perm(x[i].y, x[i].w, 0x5410);
+        v.w = __byte_perm(x[i].y, x[i].w, 0x7632);
+        *reinterpret_cast<uint4*>(dst + i * Tr::PITCH) = v;
       }
-    } else {
-#pragma unroll 1
-      for (; left > 0; left -= Sm::kFeeders) {
-        if (!mbar_wait(&sr->empty[pos.at], pos.phase ^ 1u, &sr->abort)) {
-          sr->give_up(p.err);
-          break;
-        }
-        const uint32_t dst = smem_u32(ring) + pos.at * Sm::kSlot + kStageBytes + lane * 16;
-        const __nv_bfloat16* src = p.xp + kc * 256 + lane * 8;
-#pragma unroll 4
-        for (int row = 0; row < p.M; ++row) cp_async_16(dst + row * Tr::PITCH, src + static_cast<size_t>(row) * p.Kp, 16);
-        cp_async_mbar_arrive_noinc(&sr->full[pos.at]);
-        pos.skip(Sm::kFeeders, Sm::NST);
-        kc = (kc + Sm::kFeeders) % C;
-      }
-      cp_async_wait_all();
+      mbar_arrive(&sr->full[pos.at]);
+      pos.skip(Sm::kFeeders, Sm::NST);
+      kc = (kc + Sm::kFeeders) % C;
+      if (left > Sm::kFeeders) load(kc);
     }
     return;
   }
@@ -321,7 +196,7 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     });
     if (lin_by_consumers(p.M, C, chunks, left)) {
       bar_consumers<CT>();
-      lin_finish<CT, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, end, C, b, tid, &sr->last[1]);
+      lin_finish<CT, kLinStrip, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, end, C, b, tid, &sr->last[1]);
       bar_consumers<CT>();
     } else {
       __syncwarp();
@@ -360,11 +235,7 @@ cudaError_t launch_lin_types(const CUtensorMap& m, const LinParams& p, bool f32,
 template <int GRP>
 cudaError_t launch_lin_rows(const CUtensorMap& m, const LinParams& p, bool f32, int grid, cudaStream_t s) {
   if (p.M <= 8) return launch_lin_types<GRP, 1>(m, p, f32, grid, s);
-  if (p.M <= 16) return launch_lin_types<GRP, 2>(m, p, f32, grid, s);
-  const cudaError_t e =
-      launch_kernel(linear_w4_order_kernel<GRP>, dim3((p.Kp + 2047) / 2048, p.M), dim3(256), 0, s, p);
-  if (e != cudaSuccess) return e;
-  return launch_lin_types<GRP, 4>(m, p, f32, grid, s);
+  return launch_lin_types<GRP, 2>(m, p, f32, grid, s);
 }
 
 // ------------------------------------------------------------ 4-bit weights
@@ -473,7 +344,8 @@ cudaError_t launch_dequantize(const uint8_t* q, const __nv_bfloat16* sc, const u
 }  // namespace
 
 // A product's scratch: arrival counts, partial sums, ordered rows.
-LinearW4Scratch linear_w4_scratch(int M, int K) {
+LinearW4Scratch linear_w4_scratch(int M, int K, int N) {
+  const bool wide = linear_w4_wide(M, K, N);
   const size_t Kp = (static_cast<size_t>(K) + 255) / 256 * 256;
   LinearW4Scratch l{};
   size_t cur = 0;
@@ -483,8 +355,8 @@ LinearW4Scratch linear_w4_scratch(int M, int K) {
     return o;
   };
   l.cnt = take(kStreamMaxCtas * 4);
-  l.part = take(static_cast<size_t>(kStreamMaxCtas) * 2 * M * kLinStrip * 4);
-  l.xp = take(M > 16 ? static_cast<size_t>(M) * Kp * 2 : 0);
+  l.part = take(static_cast<size_t>(kStreamMaxCtas) * 2 * M * (wide ? kWideStrip : kLinStrip) * 4);
+  l.xp = take(wide ? static_cast<size_t>(M) * Kp * 2 : 0);
   l.total = cur;
   return l;
 }
@@ -494,7 +366,8 @@ cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, cons
   CUtensorMap m;
   const uint64_t dims[2] = {static_cast<uint64_t>(K) / 2, static_cast<uint64_t>(N)};
   const uint64_t strides[1] = {static_cast<uint64_t>(K) / 2};
-  const uint32_t box[2] = {128, kLinStrip};
+  const bool wide = linear_w4_wide(M, K, N);
+  const uint32_t box[2] = {128, static_cast<uint32_t>(wide ? kWideStrip : kLinStrip)};
   if (!encode_tmap(&m, wq, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8)) return cudaErrorInvalidValue;
   LinParams p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
@@ -502,7 +375,7 @@ cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, cons
   p.zp = zp;
   p.y = y;
   p.err = err;
-  const LinearW4Scratch l = linear_w4_scratch(M, K);
+  const LinearW4Scratch l = linear_w4_scratch(M, K, N);
   p.cnt = reinterpret_cast<int32_t*>(scratch + l.cnt);
   p.part = reinterpret_cast<float*>(scratch + l.part);
   p.xp = reinterpret_cast<__nv_bfloat16*>(scratch + l.xp);
@@ -510,6 +383,7 @@ cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, cons
   p.K = K;
   p.N = N;
   p.Kp = (K + 255) / 256 * 256;
+  if (wide) return launch_linear_w4_wide(group, m, p, y_f32, s);
   const long long chunks = (static_cast<long long>(N) + kLinStrip - 1) / kLinStrip * ((K + 255) / 256);
   int grid = device_sm_count();
   if (grid > kStreamMaxCtas) grid = kStreamMaxCtas;

@@ -86,11 +86,11 @@ inline int w4_group(int dt) {
 bool few_supported(const moe_config_t* c);
 size_t few_workspace_bytes(const moe_config_t* c);
 
-// ---------------------------------------------------------------- linear_w4.cu
+// ------------------------------------------ linear_w4.cu, linear_w4_wide.cu
 struct LinearW4Scratch {
   size_t cnt, part, xp, total;
 };
-LinearW4Scratch linear_w4_scratch(int M, int K);  // offsets; the counts (cnt) are zero between launches
+LinearW4Scratch linear_w4_scratch(int M, int K, int N);  // offsets; the counts (cnt) are zero between launches
 cudaError_t launch_linear_w4(int M, int K, int N, int group, const void* x, const void* wq, const void* sc,
                              const uint8_t* zp, void* y, bool y_f32, int32_t* err, uint8_t* scratch, cudaStream_t s);
 cudaError_t launch_quantize_w4(const void* W, bool f32, long long G, int K, int N, int group, void* q,

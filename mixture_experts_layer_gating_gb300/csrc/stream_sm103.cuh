@@ -190,14 +190,15 @@ struct StreamRing {
   uint64_t red_full[2], red_empty[2];
   int abort;
   int last[2];  // whether an arrival was the last (finisher's, consumers')
-  __device__ void init(int consumer_warps) {
+  // arrivals that make a stage full (a feeder's lanes beside the producer) and empty
+  __device__ void init(int consumer_warps, int filled = 1 + 32, int emptied = kStreamWarps) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&red_full[i], consumer_warps);
       mbar_init(&red_empty[i], 32);
     }
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&full[i], 1 + 32);
-      mbar_init(&empty[i], kStreamWarps);
+      mbar_init(&full[i], filled);
+      mbar_init(&empty[i], emptied);
     }
     abort = 0;
     fence_mbarrier_init();

@@ -413,3 +413,60 @@ def test_quantize_nonfinite_group_is_nan():
     want[:32, 2] = True
     want[32:, 5] = True
     assert torch.equal(bad, want)
+
+
+def _check_some_columns(M, K, N, g, zeros, dt, offset=0):
+    """A large product against 64 bits at 300 of its columns, both ends among them."""
+    q, s, z = _w4(N, K, g, zeros, seed=M + N)
+    if zeros and offset:  # zero points need no alignment
+        raw = torch.empty(z.numel() + offset, dtype=torch.uint8, device="cuda")
+        raw[offset:].copy_(z.reshape(-1))
+        z = raw[offset:].view_as(z)
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    ws = _linear_ws(M, K, N)
+    y = torch.full((M, N), float("nan"), dtype=dt, device="cuda")
+    moe.moe_linear_w4(M, K, N, g, x, q, s, z, y, ws)
+    gen = torch.Generator().manual_seed(3)
+    cols = torch.cat([torch.arange(20), torch.arange(N - 20, N), torch.randint(0, N, (260,), generator=gen)])
+    at = cols.cuda()
+    want, tol = ref.linear(x.cpu(), q[at].cpu(), s[at].cpu(), None if z is None else z[at].cpu(), dt)
+    worst = ((y[:, at].double().cpu() - want).abs() / tol).max().item()
+    assert worst <= 1.0, f"{worst} times the allowed error"
+    assert torch.isfinite(y).all() and moe.moe_read_device_status(ws) == 0
+    again = torch.empty_like(y)
+    moe.moe_linear_w4(M, K, N, g, x, q, s, z, again, ws)
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("g", [32, 64, 128])
+@pytest.mark.parametrize("M,K,N,zeros,dt", [
+    (9, 8192, 8200, True, torch.bfloat16),      # 9 to 16 rows, weights of many stages
+    (16, 384, 131071, False, torch.float32),
+    (32, 256, 117001, True, torch.float32),     # strips of one stage
+    (17, 2816, 40000, False, torch.bfloat16),   # groups of a row no multiple of eight
+    (31, 640, 70002, True, torch.bfloat16),
+])
+def test_linear_many_strips(M, K, N, g, zeros, dt):
+    _check_some_columns(M, K, N, g, zeros, dt)
+
+
+@pytest.mark.parametrize("M,N", [(3, 300), (11, 700), (20, 700)])
+def test_linear_unaligned_zero_points(M, N):
+    for offset in (1, 2, 4):
+        _check_some_columns(M, 2048, N, 64, True, torch.float32, offset)
+
+
+def test_linear_nonfinite_rows_stay_alone_with_many_rows():
+    M, K, N, g = 29, 1024, 600, 32
+    q, s, z = _w4(N, K, g, True)
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    ws = _linear_ws(M, K, N)
+    y = torch.empty(M, N, device="cuda")
+    moe.moe_linear_w4(M, K, N, g, x, q, s, z, y, ws)
+    x[3, 5] = float("nan")
+    x[28, 1000] = float("-inf")
+    y2 = torch.empty_like(y)
+    moe.moe_linear_w4(M, K, N, g, x, q, s, z, y2, ws)
+    rows = [m for m in range(M) if m not in (3, 28)]
+    assert torch.equal(y[rows], y2[rows])
+    assert torch.isnan(y2[3]).all() and not torch.isfinite(y2[28]).any()
