@@ -155,9 +155,10 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
   if (p.T > 8 && f.shared > 0) {
     // The down rows of 4-bit and e4m3 [N, K] weights are many to a stage.  16 tokens,
     // shared expert 1% to 6% of the bytes, against equal weights: 4-bit 16 to 32 tokens
-    // 153 -> 144 and 185 -> 172 us; e4m3 [K, N] 856 -> 799; e4m3 [N, K] 1013 -> 813.
+    // 153 -> 144 and 185 -> 172 us (2:1 since a team takes a short strip alone: 135 ->
+    // 124); e4m3 [K, N] 856 -> 799; e4m3 [N, K] 1013 -> 813.
     constexpr bool nk8 = KIND == kStreamFp8Nk;
-    if (KIND == kStreamW4) f.w[0] = 4, f.w[1] = 3;
+    if (KIND == kStreamW4) f.w[0] = down ? 2 : 4, f.w[1] = down ? 1 : 3;
     else if (down) f.w[0] = nk8 ? 9 : 3, f.w[1] = nk8 ? 4 : 2;
   }
   // (at least w[0] units, so at least one chunk, for every CTA that has a part)
@@ -555,7 +556,14 @@ struct Few {
     });
   }
 
-  // Who finishes a strip: all consumers the run's last one, when they have nothing
+  // Short strips of 4-bit down products: a strip for each team, so that neither waits
+  // for the other at its end (of three stages one team would have two, the other one).
+  // Both teams' strips are in the ring at a time.
+  static __device__ __forceinline__ bool solo(bool down, const FewPass& f, const FewAt& at) {
+    return KIND == kStreamW4 && Sm::kTeams == 2 && Sm::kRedBufs == 2 && down && 2 * f.C[at.r] <= Sm::NST;
+  }
+
+  // Who finishes a strip: all consumers (of a solo strip: its team) the run's last one, when they have nothing
   // else to do, and shared ones of more than two rows, whose parts one warp would
   // add for tens of microseconds; the finisher warp the others.
   static __device__ __forceinline__ bool by_consumers(const FewParams& p, const FewPass& f, const Ctrl* ctl,
@@ -567,25 +575,31 @@ struct Few {
   // over.
   template <bool DOWN>
   static __device__ __forceinline__ void finish(const FewParams& p, const FewPass& f, Ctrl* ctl, const float* red0,
-                                                RingPos& rpos, int b, int lane) {
+                                                RedPos& rpos, int b, int lane) {
     if (f.lo >= f.hi) return;
     FewAt at(f, f.lo);
-    int left = static_cast<int>(f.hi - f.lo);
+    int left = static_cast<int>(f.hi - f.lo), turn = 0;
 #pragma unroll 1
     for (;;) {
       const int chunks = min(f.C[at.r] - at.kc, left), end = at.kc + chunks;
       left -= chunks;
+      int buf = rpos.at;
+      if (solo(DOWN, f, at)) {
+        buf = turn;
+        turn ^= 1;
+      }
       if (by_consumers(p, f, ctl, at, chunks, left)) {
         if (left == 0) break;
         at.next_strip(f);
         continue;
       }
-      if (!mbar_wait(&ctl->ring.red_full[rpos.at], rpos.phase, &ctl->ring.abort)) ctl->ring.give_up(p.err);
+      if (!mbar_wait(&ctl->ring.red_full[buf], rpos.phase(buf), &ctl->ring.abort)) ctl->ring.give_up(p.err);
       __syncwarp();
-      finish_strip<DOWN, 32>(p, f, ctl, red0 + rpos.at * (Sm::kRedBytes / 4), at, end, f.hi - left - end, b, lane);
+      finish_strip<DOWN, 32>(p, f, ctl, red0 + buf * (Sm::kRedBytes / 4), at, end, f.hi - left - end, b, lane);
       __syncwarp();
-      mbar_arrive(&ctl->ring.red_empty[rpos.at]);
-      rpos.next(Sm::kRedBufs);
+      mbar_arrive(&ctl->ring.red_empty[buf]);
+      rpos.handed(buf);
+      rpos.at = (buf + 1) % Sm::kRedBufs;
       at.next_strip(f);
     }
   }
@@ -603,14 +617,14 @@ struct Few {
 
   template <bool DOWN>
   static __device__ __forceinline__ void consume(const FewParams& p, const FewPass& f, Ctrl* ctl, uint32_t ring,
-                                                 float* red0, RingPos& ring_pos, RingPos& rpos, int b) {
+                                                 float* red0, RingPos& ring_pos, RedPos& rpos, int b) {
     if (f.lo >= f.hi) return;
     const int tid = threadIdx.x, team = Sm::kTeams == 1 ? 0 : tid / (32 * kStreamWarps);
     const int warp = (tid >> 5) % kStreamWarps, lane = tid & 31;
     [[maybe_unused]] const int g = lane >> 2, c = lane & 3;
     constexpr uint32_t kLo = 8 * NT * Tr::PITCH;
     FewAt at(f, f.lo);
-    int left = static_cast<int>(f.hi - f.lo);
+    int left = static_cast<int>(f.hi - f.lo), turn = 0;  // turn: the team of the next solo strip
 
     // 4-bit weights: the lane's row of group scales; a strip's first ones are loaded
     // while the strip before it is summed up
@@ -632,78 +646,119 @@ struct Few {
         sbase = static_cast<const __nv_bfloat16*>(DOWN ? (x.r ? p.s2 : p.s2s) : (x.r ? p.s13 : p.s13s));
         groups = f.K[x.r] / GRP;
         srow = l < f.width[x.r] ? ((e * (DOWN ? 1 : 2) + half) * f.width[x.r] + l) * groups : -1;
-        scales(sc0, x.kc + team);
-        scales(sc1, x.kc + team + Sm::kTeams);
+        const bool alone = solo(DOWN, f, x);
+        scales(sc0, x.kc + (alone ? 0 : team));
+        scales(sc1, x.kc + (alone ? 1 : team + Sm::kTeams));
       }
     };
-    first_scales(at);
+    if (solo(DOWN, f, at) && team == 1) {
+      const int skip = f.C[at.r] - at.kc;
+      FewAt x = at;
+      x.next_strip(f);
+      if (left > skip) first_scales(x);
+    } else {
+      first_scales(at);
+    }
 
     float acc[NT][Tr::MT][4];
     while (left > 0) {  // a strip, or this CTA's part of it
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < Tr::MT; ++j)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[i][j][t] = 0.0f;
-      const int ntu = (row_count(p, ctl, at) + 7) >> 3;
+      const bool alone = solo(DOWN, f, at);
+      const bool mine = !alone || turn == team;
+      const int stride = alone ? 1 : Sm::kTeams, buf = alone ? turn : rpos.at;
       const int chunks = min(f.C[at.r] - at.kc, left), end = at.kc + chunks;
       RingPos pos = ring_pos;
-      if (team) pos.next(Sm::NST);
-      auto step = [&](auto& sc, int kc) {
-        if (!mbar_wait(&ctl->ring.full[pos.at], pos.phase, &ctl->ring.abort)) ctl->ring.give_up(p.err);
-        __syncwarp();
-        const uint32_t st = ring + pos.at * Sm::kSlot, rows = st + kStageBytes;
-        // (most experts of a batch of 16 have at most eight rows: the code for one tile of
-        // tokens takes three quarters of the time)
-        auto& one = reinterpret_cast<float(&)[1][Tr::MT][4]>(acc[0]);
-        if constexpr (Tr::KN) {
-          if (NT == 1 || ntu == 1) stage_mma_kn<KIND, 1, DOWN && Sm::kHilo>(st, rows, kLo, warp, lane, 1, one);
-          else stage_mma_kn<KIND, NT, DOWN && Sm::kHilo>(st, rows, kLo, warp, lane, NT, acc);
-        } else if constexpr (KIND == kStreamFp8Nk) {
-          if (NT == 1 || ntu == 1) stage_mma_fp8nk<1>(st, rows, warp, lane, 1, one);
-          else stage_mma_fp8nk<NT>(st, rows, warp, lane, NT, acc);
-        } else {
-          if (NT == 1 || ntu == 1) stage_mma_w4<GRP, 1, 1, 2, false, true>(st, rows, warp, lane, 1, sc, one);
-          else stage_mma_w4<GRP, NT, NT, 1, false, true>(st, rows, warp, lane, NT, sc, acc);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->ring.empty[pos.at]);
-        pos.skip(Sm::kTeams, Sm::NST);
-        scales(sc, kc + 2 * Sm::kTeams);
-      };
-#pragma unroll 1
-      for (int kc = at.kc + team; kc < end; kc += Sm::kTeams) {
-        step(sc0, kc);
-        if constexpr (KIND == kStreamW4) {
-          // two by two, each with scales of its own: moving them on from one step to the
-          // next would wait for the loads
-          if ((kc += Sm::kTeams) >= end) break;
-          step(sc1, kc);
-        }
-      }
       ring_pos.skip(chunks % Sm::NST, Sm::NST);
       ring_pos.phase ^= (chunks / Sm::NST) & 1;
       left -= chunks;
-      if (KIND == kStreamW4 && left > 0) {
-        FewAt x = at;
-        x.next_strip(f);
-        first_scales(x);
-      }
-      // the sums over this CTA's chunks of the strip, to the finisher
-      add_sums<KIND, GRP, NT, Sm::kTeams, Sm::kRP>(
-          red0 + rpos.at * (Sm::kRedBytes / 4), team, warp, lane, ntu, acc, [&]() {
-            if (!mbar_wait(&ctl->ring.red_empty[rpos.at], rpos.phase ^ 1u, &ctl->ring.abort)) ctl->ring.give_up(p.err);
+      turn ^= alone;
+      const bool by_all = by_consumers(p, f, ctl, at, chunks, left);
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < Tr::MT; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[i][j][t] = 0.0f;
+        const int ntu = (row_count(p, ctl, at) + 7) >> 3;
+        if (!alone && team) pos.next(Sm::NST);
+        auto step = [&](auto& sc, int kc) {
+          if (!mbar_wait(&ctl->ring.full[pos.at], pos.phase, &ctl->ring.abort)) ctl->ring.give_up(p.err);
+          __syncwarp();
+          const uint32_t st = ring + pos.at * Sm::kSlot, rows = st + kStageBytes;
+          // (most experts of a batch of 16 have at most eight rows: the code for one tile of
+          // tokens takes three quarters of the time)
+          auto& one = reinterpret_cast<float(&)[1][Tr::MT][4]>(acc[0]);
+          if constexpr (Tr::KN) {
+            if (NT == 1 || ntu == 1) stage_mma_kn<KIND, 1, DOWN && Sm::kHilo>(st, rows, kLo, warp, lane, 1, one);
+            else stage_mma_kn<KIND, NT, DOWN && Sm::kHilo>(st, rows, kLo, warp, lane, NT, acc);
+          } else if constexpr (KIND == kStreamFp8Nk) {
+            if (NT == 1 || ntu == 1) stage_mma_fp8nk<1>(st, rows, warp, lane, 1, one);
+            else stage_mma_fp8nk<NT>(st, rows, warp, lane, NT, acc);
+          } else {
+            if (NT == 1 || ntu == 1) stage_mma_w4<GRP, 1, 1, 2, false, true>(st, rows, warp, lane, 1, sc, one);
+            else stage_mma_w4<GRP, NT, NT, 1, false, true>(st, rows, warp, lane, NT, sc, acc);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->ring.empty[pos.at]);
+          pos.skip(stride, Sm::NST);
+          scales(sc, kc + 2 * stride);
+        };
+#pragma unroll 1
+        for (int kc = at.kc + (alone ? 0 : team); kc < end; kc += stride) {
+          step(sc0, kc);
+          if constexpr (KIND == kStreamW4) {
+            // two by two, each with scales of its own: moving them on from one step to the
+            // next would wait for the loads
+            if ((kc += stride) >= end) break;
+            step(sc1, kc);
+          }
+        }
+        if (KIND == kStreamW4 && left > 0) {  // of the team's next strip
+          FewAt x = at;
+          x.next_strip(f);
+          if (solo(DOWN, f, x) && turn != team) {
+            const int skip = f.C[x.r];
+            x.next_strip(f);
+            if (left > skip) first_scales(x);
+          } else {
+            first_scales(x);
+          }
+        }
+        // the sums over this CTA's chunks of the strip, to the finisher
+        float* red = red0 + buf * (Sm::kRedBytes / 4);
+        auto before_first = [&]() {
+          if (!mbar_wait(&ctl->ring.red_empty[buf], rpos.phase(buf) ^ 1u, &ctl->ring.abort)) ctl->ring.give_up(p.err);
+          __syncwarp();
+        };
+        if constexpr (KIND == kStreamW4 && DOWN && Sm::kTeams == 2) {
+          if (alone) {
+            auto sync = [&]() { named_bar_sync(8 + team, 32 * kStreamWarps); };
+            add_sums<KIND, GRP, NT, 1, Sm::kRP>(red, 0, warp, lane, ntu, acc, before_first, sync);
+            if (by_all) {
+              sync();
+              finish_strip<DOWN, 32 * kStreamWarps>(p, f, ctl, red, at, end, f.hi - left - end, b, tid & (32 * kStreamWarps - 1));
+              sync();
+            } else {
+              __syncwarp();
+              if (lane < 2) mbar_arrive(&ctl->ring.red_full[buf]);  // (for the other team's warp too)
+            }
+          }
+        }
+        if (!alone) {
+          add_sums<KIND, GRP, NT, Sm::kTeams, Sm::kRP>(red, team, warp, lane, ntu, acc, before_first, [] { bar(); });
+          if (by_all) {
+            bar();
+            finish_strip<DOWN, CT>(p, f, ctl, red, at, end, f.hi - left - end, b, tid);
+            bar();
+          } else {
             __syncwarp();
-          });
-      if (by_consumers(p, f, ctl, at, chunks, left)) {
-        bar();
-        finish_strip<DOWN, CT>(p, f, ctl, red0 + rpos.at * (Sm::kRedBytes / 4), at, end, f.hi - left - end, b, tid);
-        bar();
-      } else {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->ring.red_full[rpos.at]);
-        rpos.next(Sm::kRedBufs);
+            if (lane == 0) mbar_arrive(&ctl->ring.red_full[buf]);
+          }
+        }
+      }
+      if (!by_all) {
+        rpos.handed(buf);
+        rpos.at = (buf + 1) % Sm::kRedBufs;
       }
       at.next_strip(f);
     }
@@ -857,16 +912,16 @@ struct Few {
     if (lane < p.T) ctl->srow[R + lane] = static_cast<uint16_t>(lane);
   }
 
-  // The router's planes of tokens t0 .. t0 + 8 NT - 1.  A unit is 64 experts x one slice of D; its k16 steps
-  // go round the CTA's warps, two at a time.
-  static __device__ __forceinline__ void router(const FewParams& p, float* red, int b, int G, int t0) {
+  // The router's planes.  A unit is 64 experts x one slice of D x 8 NT tokens; its k16
+  // steps go round the CTA's warps, two at a time.
+  static __device__ __forceinline__ void router(const FewParams& p, float* red, int b, int G) {
     constexpr int NW = CT / 32, PL = Sm::kPlanes, PW = 8 * NT * 68;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, c = lane & 3;
     const int SE = (p.E + 63) / 64, steps = (p.D + 15) / 16;
     const bool vec = (p.E & 7) == 0;
 #pragma unroll 1
-    for (int u = b; u < SE * p.nplanes; u += G) {
-      const int se = u % SE, pl = u / SE;
+    for (int u = b; u < SE * p.nplanes * ((p.T + 8 * NT - 1) / (8 * NT)); u += G) {
+      const int se = u % SE, pl = u / SE % p.nplanes, t0 = u / (SE * p.nplanes) * 8 * NT;
       const int s0 = steps * pl / p.nplanes, s1 = steps * (pl + 1) / p.nplanes;
       float acc[NT][4][4];
 #pragma unroll
@@ -1028,7 +1083,7 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   __syncthreads();
 
   if (tid >= CT + 32 + 32 * Sm::kFeeders) {  // ------------------------ finisher
-    RingPos rpos;
+    RedPos rpos;
     asm volatile("bar.sync 4, %0;" ::"n"(CT + 32 * Sm::kFeeders + 32) : "memory");  // the expert lists are built
     F::template finish<false>(p, ctl->pass[0], ctl, red, rpos, b, lane);
     asm volatile("bar.arrive 5, %0;" ::"n"(CT + 32) : "memory");  // h is written
@@ -1075,8 +1130,7 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   if (Tr::F16)
     for (int r = b * CT + tid; r < R + p.T; r += G * CT) p.hmax[r] = 0;
   // phase 0
-#pragma unroll 1
-  for (int t0 = 0; t0 < p.T; t0 += 8 * NT) F::router(p, red, b, G, t0);
+  F::router(p, red, b, G);
   F::stage_x(p, red, b, G);
   F::grid_sync(p, sr, 0, 3);
 
@@ -1111,7 +1165,8 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   asm volatile("bar.arrive 4, %0;" ::"n"(CT + 32 * Sm::kFeeders + 32) : "memory");
   asm volatile("bar.arrive 2, %0;" ::"n"(CT + 32) : "memory");
 
-  RingPos pos, rpos;
+  RingPos pos;
+  RedPos rpos;
   const uint32_t ring_a = smem_u32(ring);
   // phase 2: gate/up
   F::template consume<false>(p, ctl->pass[0], ctl, ring_a, red, pos, rpos, b);

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(LinSmem<GRP, NT>::kBlock, 1)
     add_sums<kStreamW4, GRP, NT, Sm::kTeams, RP>(red + rpos.at * (Sm::kRedBytes / 4), team, warp, lane, ntu, acc, [&]() {
       if (!mbar_wait(&sr->red_empty[rpos.at], rpos.phase ^ 1u, &sr->abort)) sr->give_up(p.err);
       __syncwarp();
-    });
+    }, [] { bar_consumers<CT>(); });
     if (lin_by_consumers(p.M, C, chunks, left)) {
       bar_consumers<CT>();
       lin_finish<CT, kLinStrip, TY>(p, sp, red + rpos.at * (Sm::kRedBytes / 4), RP, s, kc, end, C, b, tid, &sr->last[1]);

@@ -240,6 +240,14 @@ struct RingPos {
   }
 };
 
+// Which of the two buffers the next strip's sums go to, and each one's phase.
+struct RedPos {
+  int at = 0;
+  uint32_t bits = 0;
+  __device__ __forceinline__ uint32_t phase(int buf) const { return (bits >> buf) & 1u; }
+  __device__ __forceinline__ void handed(int buf) { bits ^= 1u << buf; }
+};
+
 // After an abort, by the producer: copies still in flight land before the CTA
 // exits.  `pos` is the slot after the last one filled.
 __device__ __forceinline__ void drain_ring(StreamRing* r, RingPos pos, int n) {
@@ -533,17 +541,19 @@ __device__ __forceinline__ void stage_mma_w4(uint32_t stage, uint32_t rows, int 
 
 // A team's sums into red[row][columns] (RP floats a row): the two warps of a team
 // that hold sums of the same columns, and the teams, add theirs one after
-// another, in a fixed order.  `before_first` runs before anything is written.
-template <int KIND, int GRP, int NT, int TEAMS, int RP, typename WAIT>
+// another, in a fixed order, with a `sync` of all of them between two.
+// `before_first` runs before anything is written.
+template <int KIND, int GRP, int NT, int TEAMS, int RP, typename WAIT, typename SYNC>
 __device__ __forceinline__ void add_sums(float* red, int team, int warp, int lane, int ntu,
-                                         const float (&acc)[NT][StreamTraits<KIND, GRP>::MT][4], WAIT before_first) {
+                                         const float (&acc)[NT][StreamTraits<KIND, GRP>::MT][4], WAIT before_first,
+                                         SYNC sync) {
   using Tr = StreamTraits<KIND, GRP>;
   const int g = lane >> 2, c = lane & 3;
   const int mine = team * 2 + (Tr::KN ? warp >> 2 : warp & 1);
   if (mine == 0) before_first();
 #pragma unroll 1
   for (int r = 0; r < 2 * TEAMS; ++r) {
-    if (r > 0) bar_consumers<32 * kStreamWarps * TEAMS>();
+    if (r > 0) sync();
     if (mine == r) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
