@@ -34,6 +34,8 @@ constexpr int kFewMaxR = 512;  // expanded rows: 32 tokens, 16 experts each
 // Accumulators for 32 rows would leave room for one consumer team only, which
 // costs every expert more than the few long ones gain.
 constexpr int kFewGroup = 16;
+// Stages of a short strip (of 4-bit down products; see solo()).
+constexpr int kFewShort = 3;
 // Up to this many bytes of router planes every CTA reads them all (152 x 64 KB
 // from L2 take about as long as one more barrier).
 constexpr int kFewPlaneBytes = 65536;
@@ -121,6 +123,7 @@ struct FewSmem {
   static constexpr int NST = stream_stages(kSlot, kOther);
   static constexpr int kBytes = 1024 + NST * kSlot + kOther;
   static_assert(NST >= 4 && NST % kFeeders == 0, "ring sizes");
+  static_assert(KIND != kStreamW4 || (kTeams == 2 && kRedBufs == 2 && NST >= 2 * kFewShort), "short strips");
   static_assert(kBytes <= kStreamSmemMax, "shared memory");
 };
 
@@ -158,7 +161,8 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
     // 153 -> 144 and 185 -> 172 us (2:1 since a team takes a short strip alone: 135 ->
     // 124); e4m3 [K, N] 856 -> 799; e4m3 [N, K] 1013 -> 813.
     constexpr bool nk8 = KIND == kStreamFp8Nk;
-    if (KIND == kStreamW4) f.w[0] = down ? 2 : 4, f.w[1] = down ? 1 : 3;
+    if (KIND == kStreamW4 && down && f.C[1] <= kFewShort) f.w[0] = 2;
+    else if (KIND == kStreamW4) f.w[0] = 4, f.w[1] = 3;
     else if (down) f.w[0] = nk8 ? 9 : 3, f.w[1] = nk8 ? 4 : 2;
   }
   // (at least w[0] units, so at least one chunk, for every CTA that has a part)
@@ -558,9 +562,9 @@ struct Few {
 
   // Short strips of 4-bit down products: a strip for each team, so that neither waits
   // for the other at its end (of three stages one team would have two, the other one).
-  // Both teams' strips are in the ring at a time.
+  // Both teams' strips are in the ring at a time.  19 tokens: 135 us, not 145.
   static __device__ __forceinline__ bool solo(bool down, const FewPass& f, const FewAt& at) {
-    return KIND == kStreamW4 && Sm::kTeams == 2 && Sm::kRedBufs == 2 && down && 2 * f.C[at.r] <= Sm::NST;
+    return KIND == kStreamW4 && down && f.C[at.r] <= kFewShort;
   }
 
   // Who finishes a strip: all consumers (of a solo strip: its team) the run's last one, when they have nothing
@@ -730,7 +734,7 @@ struct Few {
           if (!mbar_wait(&ctl->ring.red_empty[buf], rpos.phase(buf) ^ 1u, &ctl->ring.abort)) ctl->ring.give_up(p.err);
           __syncwarp();
         };
-        if constexpr (KIND == kStreamW4 && DOWN && Sm::kTeams == 2) {
+        if constexpr (KIND == kStreamW4 && DOWN) {
           if (alone) {
             auto sync = [&]() { named_bar_sync(8 + team, 32 * kStreamWarps); };
             add_sums<KIND, GRP, NT, 1, Sm::kRP>(red, 0, warp, lane, ntu, acc, before_first, sync);
