@@ -470,3 +470,23 @@ def test_linear_nonfinite_rows_stay_alone_with_many_rows():
     rows = [m for m in range(M) if m not in (3, 28)]
     assert torch.equal(y[rows], y2[rows])
     assert torch.isnan(y2[3]).all() and not torch.isfinite(y2[28]).any()
+
+
+@pytest.mark.parametrize("w", ["w4_g32", "w4_g64"])
+@pytest.mark.parametrize("T,D,E,k,I,Is", [
+    (19, 4096, 64, 8, 704, 2112),   # long strips of the shared expert, then short ones
+    (20, 4096, 32, 4, 1536, 320),   # short ones first
+    (3, 8192, 16, 2, 2048, 64),
+    (32, 6144, 48, 3, 256, 704),    # both short, of one and of three stages
+    (1, 8192, 8, 8, 576, 0),
+])
+def test_layer_strips_of_two_lengths(w, T, D, E, k, I, Is):
+    cfg = moe.make_config(T, D, E, k, I, Is, w_dtype=w)
+    d = _inputs(w, T, D, E, k, I, Is, seed=I)
+    ws = moe.alloc_workspace(cfg)
+    out = _call(cfg, d, ws)
+    for _ in range(10):
+        again = _call(cfg, d, ws)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    assert moe.moe_read_device_status(ws) == 0
+    _check(cfg, d, w, ws, out, "swiglu", True, where="cuda")
