@@ -33,7 +33,8 @@
  *   bytes, which makes D, I and I_shared multiples of 8 (16 for fp8 weights).
  * - The control block has to be zero when a workspace is first used (zero-fill
  *   it once); the calls leave it ready for the next.  A workspace serves one
- *   call at a time: calls that may overlap on the GPU need one each.
+ *   call at a time: calls that may overlap on the GPU need one each.  What
+ *   moe_linear_w4 uses as a workspace serves its own calls only.
  * - Dtypes: act_dtype applies to x, W_g, the permuted rows and out.  w_dtype
  *   applies to W13, W2 and the shared expert's weights.  Supported pairs:
  *   (F32, F32), (BF16, BF16), (BF16, FP8_E4M3), (BF16, FP8_E4M3_NK),
@@ -271,12 +272,16 @@ int moe_layer(const moe_config_t* cfg, const void* x, const void* Wg, const floa
  *   FP8_E4M3_NK and W4_*.  s13 / s2 / s13s / s2s: fp32 per column for e4m3
  *   weights, bf16 per row and group for 4-bit weights, NULL for bf16.
  *   Other types and T > 32 return MOE_ERR_UNSUPPORTED.
- *   Arithmetic: weights and x enter the products exactly, in bf16 (4-bit codes
- *   minus 8 and e4m3 values are exact there), with fp32 sums; e4m3 scales
- *   multiply the finished sums, group scales the fp32 sums of their group.  h is
- *   carried as two bf16 terms (16 significant bits); the weighted sum over a
- *   token's experts (j ascending, the shared expert last) is fp32, rounded once
- *   to bf16.  The same inputs give the same bits on every call.
+ *   Arithmetic: bf16 weights are multiplied in bf16, x as it is and h as two bf16
+ *   terms (16 significant bits).  e4m3 weights and 4-bit codes minus 8 are
+ *   multiplied as fp16 (exact there) by rows of x and h in fp16, each row times a
+ *   power of two that puts its largest element in [2^14, 2^15): x keeps its bits
+ *   but where an element is less than 2^-31 of the row's largest (it then errs by
+ *   at most 2^-39 of that one), h is rounded to 11 significant bits (same floor).
+ *   (Rows whose largest element is below 2^-86 keep fewer bits.)  All sums are fp32; e4m3 scales multiply the finished sums, group
+ *   scales the fp32 sums of their group.  The weighted sum over a token's experts
+ *   is fp32 in a fixed order (a tree over j mod 8, the shared expert as j = k),
+ *   rounded once to bf16.  The same inputs give the same bits on every call.
  *   Logits, ids and weights are left in the workspace (MOE_WS_LOGITS,
  *   MOE_WS_TOPK_IDS, MOE_WS_TOPK_W), no other intermediate is.
  *   The kernel is launched cooperatively, one CTA on every SM: it starts when
@@ -295,7 +300,8 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
  * logits of a decode step).  No page has this operator by itself; the Qwen3-MoE
  * page's 4-bit weights are its source.
  *   M       rows of x, 0..32 (more: MOE_ERR_UNSUPPORTED).
- *   K, N    inputs, a multiple of `group`; outputs, any N >= 1.
+ *   K, N    inputs, a multiple of `group`, at most 65535 groups; outputs, any N
+ *           from 1 to 2^31 - 512.
  *   group   32, 64 or 128.
  *   x       [M, K] bf16.
  *   Wq      [N, K/2] bytes as MOE_W4_* describes.
@@ -304,10 +310,14 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
  *   y       [M, N] bf16 or fp32 (y_dtype MOE_BF16 / MOE_F32), one rounding.
  *   ws      moe_linear_w4_workspace_size(M, K, N) bytes, 256-byte aligned,
  *           zero-filled once (all of it); its control block takes the device
- *           error word.  A larger workspace serves too.  After
- *           MOE_DEV_WAIT_TIMEOUT, zero-fill it before the next call.
- *   x, Wq, scales and y 16-byte aligned.  Sums are fp32; the same inputs give
- *   the same bits on every call. */
+ *           error word.  Calls of other sizes may follow in it when it is large
+ *           enough for each, other functions' calls may not: it holds counts that
+ *           are zero between calls.  After MOE_DEV_WAIT_TIMEOUT, zero-fill it
+ *           before the next call.
+ *   x, Wq, scales and y 16-byte aligned, zeros not.  x and code - zero are
+ *   multiplied in bf16, exactly; a group's sum is fp32, its scale multiplies that,
+ *   and the groups are added in fp32.  The same inputs give the same bits on every
+ *   call (of one M, K and N: which kernel runs depends on them). */
 size_t moe_linear_w4_workspace_size(int32_t M, int32_t K, int32_t N);
 int moe_linear_w4(int32_t M, int32_t K, int32_t N, int32_t group, const void* x, const void* Wq,
                   const void* scales, const void* zeros, void* y, int32_t y_dtype, void* ws,

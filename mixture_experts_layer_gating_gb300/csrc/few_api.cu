@@ -70,9 +70,10 @@ FewLayout few_layout(const moe_config_t* c) {
   return L;
 }
 
+constexpr int kW4MaxN = 0x7ffffe00;  // whole strips of columns stay below 2^31
 bool w4_args_ok(int64_t G, int K, int N, int group) {
   return G >= 1 && G <= 65535 && (group == 32 || group == 64 || group == 128) && K >= group &&
-         K % group == 0 && K / group <= 65535 && N >= 1;
+         K % group == 0 && K / group <= 65535 && N >= 1 && N <= kW4MaxN;
 }
 
 }  // namespace
@@ -163,7 +164,7 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
 }
 
 size_t moe_linear_w4_workspace_size(int32_t M, int32_t K, int32_t N) {
-  if (M < 0 || M > kStreamMaxRows || K < 32 || K % 32 || N < 1) return 0;
+  if (M < 0 || M > kStreamMaxRows || K < 32 || K % 32 || N < 1 || N > kW4MaxN) return 0;
   return sizeof(ControlBlock) + linear_w4_scratch(std::max(M, 1), K, N).total;
 }
 

@@ -531,6 +531,7 @@ struct Few {
       __syncwarp();
       if (i0 == 0) last = arrive_acq_rel(p.cnt + c0) == c1 - c0;
       last = __shfl_sync(0xffffffffu, last, 0);
+      __syncwarp();  // what lane 0 acquired
     } else {
       bar();
       if (i0 == 0) ctl->ring.last[1] = arrive_acq_rel(p.cnt + c0) == c1 - c0;

@@ -91,6 +91,7 @@ __device__ __noinline__ void lin_finish(const LinParams& p, const Split& sp, flo
   }
   if (THREADS == 32) {
     last = __shfl_sync(0xffffffffu, last, 0);
+    __syncwarp();  // what lane 0 acquired
   } else {
     bar_consumers<THREADS>();
     last = *reinterpret_cast<volatile int*>(flag);

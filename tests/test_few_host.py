@@ -87,6 +87,9 @@ def test_linear_refusals(lib):
     assert _linear(lib, K=0) == -1
     assert _linear(lib, K=96) == -1          # not whole groups
     assert _linear(lib, N=0) == -1
+    assert _linear(lib, N=2 ** 31 - 511) == -1
+    assert moe.moe_linear_w4_workspace_size(32, 256, 2 ** 31 - 511) == 0
+    assert 0 < moe.moe_linear_w4_workspace_size(32, 256, 2 ** 31 - 512) < 1 << 30
     for g in (0, 16, 48, 256, -32):
         assert _linear(lib, g=g) == -1
     for name in "xqsy":
