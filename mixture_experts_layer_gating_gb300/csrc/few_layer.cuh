@@ -10,16 +10,29 @@
 //   2  gate/up products: the chosen experts' (and the shared expert's) weight
 //      stages, one equal run of them per CTA, so that every SM streams the same
 //      number of bytes whatever the routing.  At the end of a strip of columns
-//      h = act(gate) * up, as a bf16 pair (hi, lo) in the k order of the down
-//      weights; of a strip that several CTAs share, the one that finishes last
-//      adds the partial sums (in the order of k) and does that
+//      h = act(gate) * up: for bf16 weights as a bf16 pair (hi, lo) in the k order
+//      of the down weights, else in fp32 with each row's largest |h|, by which the
+//      down pass's feeders bring it to fp16; of a strip that several CTAs share, the
+//      one that finishes last adds the partial sums (in the order of k) and does that
 //   -- barrier 2
 //   3  down products, divided up the same way, into fp32 rows and the partial
 //      sums of shared strips
 //   -- barrier 3
 //   4  out = sum_j w_j y_j + shared, one rounding
 // The producer runs ahead of the barriers: the weights of the next phase are on
-// their way while a barrier is waited for (up to 192 KB per SM).
+// their way while a barrier is waited for (up to 192 KB per SM), and the shared
+// expert's are brought into L2 while the routing is found out.
+//
+// Figures (D, E, k, I, shared I; floor: the weights' bytes at 6.8 TB/s):
+//   bf16, 8 tokens, 2816, 128, 8, 704, 2112        140 us, floor 100
+//   e4m3 [N, K], 1 token, 8192, 256, 8, 2048, 2048  92, floor 67
+//   e4m3 [K, N], 16 tokens, the same               800, floor 764 (6.4 TB/s)
+//   4-bit, 19 tokens, 2816, 128, 8, 704, 2112      124, floor 43
+//   4-bit, 1 token, 2048, 128, 8, 768               26, floor 3
+// What bounds it: HBM where a CTA has many stages and a stage's products take less
+// than its bytes (697 cycles: e4m3 218 to 383, bf16 145 to 304, 4-bit 552 for eight
+// rows and 724 for sixteen); else the chain of routing (7 us at one token), three
+// barriers (1 us each), the hand-over of shared strips (3 us) and the last sum (2).
 #pragma once
 
 #include "stream_sm103.cuh"

@@ -1,7 +1,7 @@
-// Building blocks of the kernels for a few tokens (few_layer.cuh,
-// linear_w4.cu): weights streamed once from HBM through a ring of 16 KB
+// Building blocks of the kernels for a few tokens (few_layer.cuh, linear_w4.cu,
+// linear_w4_wide.cu): weights streamed once from HBM through a ring of 16 KB
 // shared-memory stages that one thread fills with TMA box loads, multiplied by
-// at most 32 token rows with mma.sync (m16n8k16, the weights as the 16-row
+// at most 16 token rows with mma.sync (m16n8k16, the weights as the 16-row
 // operand and the tokens as the 8 columns).
 //
 // Why mma.sync and not tcgen05: at a few tokens every weight is used for a
@@ -9,7 +9,8 @@
 // HBM, ~24 bytes a cycle, feeds one m16n8k16 every 20 to 40 cycles), while a
 // tcgen05 operand has to lie in shared memory in its final type: 8- and 4-bit
 // weights would be expanded to bf16 there, written and read once more.  With
-// mma.sync they are expanded in the registers that the multiply reads.
+// mma.sync they are expanded in the registers that the multiply reads.  (From 17
+// rows on, mma.sync is the limit; linear_w4_wide.cu expands into tensor memory.)
 //
 // Roles of a CTA: consumer warps in one or two teams of eight (two teams take
 // the stages in turn and add their sums at the end of a strip: twice the time
