@@ -490,3 +490,34 @@ def test_layer_strips_of_two_lengths(w, T, D, E, k, I, Is):
     assert torch.equal(out.view(torch.int16), again.view(torch.int16))
     assert moe.moe_read_device_status(ws) == 0
     _check(cfg, d, w, ws, out, "swiglu", True, where="cuda")
+
+
+def test_calls_on_several_streams_at_once():
+    """Products of many and of few rows and whole layers side by side, each stream
+    with a workspace of its own; a workspace goes from stream to stream in order."""
+    jobs = []
+    for M, K, N, g in ((32, 2048, 20000, 64), (20, 4096, 9000, 32), (3, 2048, 9000, 128)):
+        q, s, z = _w4(N, K, g, True, seed=M)
+        x = torch.randn(M, K, device="cuda").bfloat16()
+        y = torch.empty(M, N, device="cuda")
+        args = (M, K, N, g, x, q, s, z, y, _linear_ws(M, K, N))
+        moe.moe_linear_w4(*args)
+        jobs.append((lambda st, a=args: moe.moe_linear_w4(*a, stream=st), y, y.clone()))
+    cfg = moe.make_config(12, 1024, 16, 4, 768, 256, w_dtype="w4_g64")
+    d = _inputs("w4_g64", 12, 1024, 16, 4, 768, 256, seed=5)
+    ws, out = moe.alloc_workspace(cfg), torch.empty(12, 1024, dtype=torch.bfloat16, device="cuda")
+    _call(cfg, d, ws, out)
+    jobs.append((lambda st: _call(cfg, d, ws, out, st), out, out.clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for turn in range(4):
+        for _, y, _ in jobs:
+            y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for i, (run, _, _) in enumerate(jobs):
+                run(streams[(i + turn) % len(streams)])
+        torch.cuda.synchronize()
+        for _, y, want in jobs:
+            assert torch.equal(y, want)
+    assert moe.moe_read_device_status(ws) == 0
