@@ -13,11 +13,11 @@
 // expanded into shared memory.  A group's sums come back to the thread of the
 // weight row, which multiplies them by the group's scale and adds in fp32.
 //
-// 32 rows x 4096 x 131072 (HBM floor 53 us): groups of 128 74 us (4.8 TB/s; mma.sync
-// 170), of 64 77, of 32 95; with zero points 79, 92, 110.  What bounds it: the
-// conversions, eleven half-rate instructions for eight codes, take 704 of the 1100
-// cycles of a unit on every scheduler, and on the two that have an issuer the rest
-// goes to it and the adders.
+// 32 rows x 4096 x 131072 (HBM floor 42 us): groups of 128 74 us (3.9 TB/s; mma.sync
+// 170), of 64 76, of 32 94; with zero points 79, 86, 108.  What bounds it: eleven
+// half-rate instructions for eight codes, in two converter warps a scheduler, which
+// take 700 of the 1100 cycles of a unit and share the scheduler with others (adders,
+// on two schedulers an issuer) in the rest: ALU pipe 49 %, issue 53 % (8192 x 32768).
 //
 // A stage is 256 weight rows x 256 k (32 KB) and the rows' 256 k (16 KB: read
 // once for 256 weight rows, or they would cost as many bytes from L2 as the
@@ -86,12 +86,17 @@ struct WideScales {
   uint32_t v[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* sc, int N, int groups, int n, int q0) {
     v[0] = v[1] = v[2] = v[3] = 0;
-    if (n >= N) return;
     const size_t at = static_cast<size_t>(n) * groups + q0;
-    if ((groups & 7) == 0) {
-      const uint4 t = __ldg(reinterpret_cast<const uint4*>(sc + at));
-      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    } else {
+    const bool wide = (groups & 7) == 0;
+    // (predicated, not in a branch, whose end would wait for it; for the zeros, which the
+    // converters load, that gains nothing: 86 us either way in groups of 64, 83 for 79 in
+    // groups of 128)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3])
+        : "l"(sc + at), "r"(static_cast<uint32_t>(wide && n < N)));
+    if (!wide && n < N) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (q0 + i < groups)
@@ -118,7 +123,11 @@ struct WideZeros {
         if (q0 + i < groups) v[i >> 2] |= static_cast<uint32_t>(__ldg(zp + at + i)) << (8 * (i & 3));
     }
   }
-  __device__ __forceinline__ uint32_t get(int i) const { return ((i & 4 ? v[1] : v[0]) >> (8 * (i & 3))) & 15u; }
+  // From zero i on (two in one word), zero by zero as the pair of bf16 128 + zero.
+  __device__ __forceinline__ uint32_t from(int i) const { return (i & 4 ? v[1] : v[0]) >> (8 * (i & 3)); }
+  static __device__ __forceinline__ uint32_t pair(uint32_t w, int h) {
+    return __byte_perm(w, 0x43434343u, h ? 0x4141 : 0x4040) & 0xff0fff0fu;
+  }
 };
 
 template <int GRP, bool ZERO, typename TY>
@@ -128,7 +137,7 @@ __global__ void __launch_bounds__(kWideBlock, 1)
   constexpr int UNIT = GRP == 32 ? 64 : 128;   // k of a unit
   // Buffers of weights (both halves': UNIT columns) and sets of sums (both halves': 64
   // columns a sum) fill the 512 columns.  Groups of 64 in units of 64 k, four and four
-  // of them: 87 us, not 77 (4096 x 131072, 32 rows).
+  // of them: 87 us, not 77, when it was tried (4096 x 131072, 32 rows).
   constexpr int NA = GRP == 128 ? 3 : GRP == 64 ? 2 : 4, ND = 2;
   constexpr int UPC = 256 / UNIT;             // units of a stage
   constexpr int SUMS = UNIT / GRP;            // groups, and sums, of a unit: 1 or 2
@@ -286,6 +295,7 @@ __global__ void __launch_bounds__(kWideBlock, 1)
 #pragma unroll 1
         for (int u = 0; u < UPC; ++u) {
           const uint32_t to = tmem + lanes + wpos.at * UNIT + half * (UNIT / 2);
+          const uint32_t zeros = ZERO ? cur.from((q % PER) * (256 / GRP) + u * SUMS) : 0u;
           uint4 w[UNIT / 32];  // 32 codes: 16 bytes of the swizzled row
 #pragma unroll
           for (int j = 0; j < UNIT / 32; ++j) w[j] = lds128(codes + (((u * (UNIT / 32) + j) ^ (row & 7)) << 4));
@@ -295,8 +305,7 @@ __global__ void __launch_bounds__(kWideBlock, 1)
           tc_fence_after_sync();
 #pragma unroll
           for (int j = 0; j < UNIT / 32; ++j) {
-            const uint32_t z = ZERO ? cur.get((q % PER) * (256 / GRP) + (u * UNIT + j * 32) / GRP) : 8u;
-            const uint32_t zero2 = 0x43004300u | z * 0x10001u;  // 128 + zero, twice
+            const uint32_t zero2 = ZERO ? WideZeros::pair(zeros, j * 32 / GRP) : 0x43084308u;
             uint32_t v[16];
             w4_pairs<false>(w[j].x, zero2, reinterpret_cast<uint32_t(&)[4]>(v[0]));
             w4_pairs<false>(w[j].y, zero2, reinterpret_cast<uint32_t(&)[4]>(v[4]));
