@@ -577,8 +577,25 @@ struct Few {
   // Short strips of 4-bit down products: a strip for each team, so that neither waits
   // for the other at its end (of three stages one team would have two, the other one).
   // Both teams' strips are in the ring at a time.  19 tokens: 135 us, not 145.
+  //
+  // A wait for a slot's fill n by parity takes fill n - 2's completion for its own while
+  // fill n - 1 is under way.  Strips of both teams meet at barriers, so that a team knows
+  // the other's stages to have landed, and inside a strip a slot (their number is even)
+  // stays with one team; one team's stages of solo strips say nothing about the other's,
+  // and copies land in any order.  So where a slot's last fill was the other team's
+  // (unseen()), a team first waits for that one to be emptied, as the producer did: the
+  // barrier's phase n - 1 cannot be mistaken, since phase n needs this warp's own arrival,
+  // and phase n - 2 is over because the team has seen a stage at most 2 kFewShort <= NST
+  // before this one.  (A wait at each stage would cost 19 tokens 2 us more.)
   static __device__ __forceinline__ bool solo(bool down, const FewPass& f, const FewAt& at) {
     return KIND == kStreamW4 && down && f.C[at.r] <= kFewShort;
+  }
+  // Which stages of a solo strip of C (a bit each) lie in slots that the other team filled
+  // last: NST stages back is an odd number of strips back.
+  static __host__ __device__ constexpr int unseen(int C) {
+    int m = 0;
+    for (int j = 0; j < C; ++j) m |= (((Sm::NST - j + C - 1) / C) & 1) << j;
+    return m;
   }
 
   // Who finishes a strip: all consumers (of a solo strip: its team) the run's last one, when they have nothing
@@ -678,6 +695,8 @@ struct Few {
       first_scales(at);
     }
 
+    // routed strips behind solo ones of the shared expert: any slot may be unseen
+    [[maybe_unused]] const bool behind = solo(DOWN, f, at) && at.r == 0;
     float acc[NT][Tr::MT][4];
     while (left > 0) {  // a strip, or this CTA's part of it
       const bool alone = solo(DOWN, f, at);
@@ -699,7 +718,23 @@ struct Few {
             for (int t = 0; t < 4; ++t) acc[i][j][t] = 0.0f;
         const int ntu = (row_count(p, ctl, at) + 7) >> 3;
         if (!alone && team) pos.next(Sm::NST);
+        if constexpr (KIND == kStreamW4 && DOWN) {
+          constexpr int m1 = unseen(1), m2 = unseen(2), m3 = unseen(3);
+          static_assert(kFewShort == 3 && Sm::NST >= 2 * kFewShort, "solo strips");
+          if (alone && !(behind && at.r)) {
+            const int C = f.C[at.r];
+            const uint32_t mine = ((1u << chunks) - 1u) << at.kc, other = (C == 1 ? m1 : C == 2 ? m2 : m3) & mine;
+            if (other) {  // the last of them: the other team emptied the ones before it earlier
+              RingPos w = pos;
+              w.skip(31 - __clz(other) - at.kc, Sm::NST);
+              if (!mbar_wait(&ctl->ring.empty[w.at], w.phase ^ 1u, &ctl->ring.abort)) ctl->ring.give_up(p.err);
+            }
+          }
+        }
         auto step = [&](auto& sc, int kc) {
+          if (KIND == kStreamW4 && DOWN && behind && at.r &&
+              !mbar_wait(&ctl->ring.empty[pos.at], pos.phase ^ 1u, &ctl->ring.abort))
+            ctl->ring.give_up(p.err);
           if (!mbar_wait(&ctl->ring.full[pos.at], pos.phase, &ctl->ring.abort)) ctl->ring.give_up(p.err);
           __syncwarp();
           const uint32_t st = ring + pos.at * Sm::kSlot, rows = st + kStageBytes;
