@@ -1201,12 +1201,23 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
     F::topk(p, b, G, true, p.ids, p.topw, red);
     F::grid_sync(p, sr, 1, -1);
     for (int r = tid; r < R; r += CT) {
-      const int e = __ldcg(p.ids + r);
-      const bool bad = static_cast<unsigned>(e) >= static_cast<unsigned>(p.E);  // only after a wait that gave up
-      ctl->ids[r] = bad ? 0 : e;
+      ctl->ids[r] = __ldcg(p.ids + r);
       ctl->w[r] = __ldcg(p.topw + r);
     }
     F::bar();
+    // After a wait that gave up, or with arrivals left over from one, these may be any
+    // numbers; the lists, and the room for an entry's rows, need k experts a token.
+    bool bad = false;
+    for (int r = tid; r < R; r += CT) {
+      const int e = ctl->ids[r];
+      bad |= static_cast<unsigned>(e) >= static_cast<unsigned>(p.E);
+      for (int o = r - r % p.k; o < r; ++o) bad |= ctl->ids[o] == e;
+    }
+    if (bar_consumers_or<CT>(bad)) {
+      for (int r = tid; r < R; r += CT) ctl->ids[r] = r % p.k;
+      if (tid == 0) sr->give_up(p.err);
+      F::bar();
+    }
   }
   if (R <= F::kPairRows) F::build_lists_pairs(p, ctl, tid);
   if (tid < 32) {

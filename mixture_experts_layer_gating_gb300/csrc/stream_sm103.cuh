@@ -182,6 +182,21 @@ __device__ __forceinline__ void bar_consumers() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
+// The same barrier; whether any thread's v is true.
+template <int THREADS>
+__device__ __forceinline__ bool bar_consumers_or(bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(v)), "n"(THREADS)
+      : "memory");
+  return any != 0;
+}
+
 // The ring's barriers: a stage is full once its weights' bytes and the arrivals
 // of the feeder warp that wrote its rows are there, empty once every warp of
 // the team that took it is through.

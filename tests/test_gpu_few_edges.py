@@ -1,0 +1,43 @@
+"""moe_layer_few and moe_linear_w4 on the GPU where something has gone wrong
+before or around them."""
+import pytest
+import torch
+
+import mixture_experts_layer_gating_gb300 as moe
+from tests._lib import ensure_library
+from tests.test_gpu_few import _call, _check, _inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    return ensure_library()
+
+
+@pytest.mark.parametrize("w", ["bf16", "w4_g64"])
+@pytest.mark.parametrize("left_over", ["one short", "many"])
+def test_layer_survives_a_barrier_that_gives_up(w, left_over):
+    """Arrivals left over at the barrier before the chosen experts are read (which
+    moe.h says to clear): CTAs go on with whatever the workspace holds, or wait until
+    they give up (2 s).  The status says so, nothing outside the workspace is
+    written, and a cleared workspace serves the next call."""
+    T, D, E, k, I = 5, 2048, 512, 10, 128
+    cfg = moe.make_config(T, D, E, k, I, w_dtype=w)
+    d = _inputs(w, T, D, E, k, I, 0, seed=2)
+    n, guard = moe.moe_workspace_size(cfg), 1 << 20
+    room = torch.zeros(n + guard, dtype=torch.uint8, device="cuda")
+    room[n:] = 0xA5
+    ws = room[:n]
+    want = _call(cfg, d, ws).clone()
+    assert moe.moe_read_device_status(ws) == 0
+    moe.workspace_view(ws, cfg, "topk_ids", (T, k), torch.int32).fill_(3)  # one expert, ten times a token
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws[:256].view(torch.int32)[32 + 8] = sms - 1 if left_over == "one short" else 1 << 20
+    _call(cfg, d, ws)
+    assert moe.moe_read_device_status(ws) & moe.MOE_DEV_WAIT_TIMEOUT
+    assert (room[n:] == 0xA5).all()
+    ws[:256].zero_()
+    out = _call(cfg, d, ws)
+    assert torch.equal(out, want) and moe.moe_read_device_status(ws) == 0
+    _check(cfg, d, w, ws, out, "swiglu", True)
