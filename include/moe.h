@@ -139,9 +139,14 @@ typedef struct {
   int32_t renormalize; /* 1: gate weights renormalised over the k chosen experts */
 } moe_config_t;
 
-/* Bytes of workspace that every call below accepts for this configuration
- * (moe_layer needs all of it; the stage calls use the control block and
- * their own scratch).  Returns 0 for an invalid configuration. */
+/* Bytes of workspace that every call below accepts for this configuration.
+ * The last region, at T <= 32, is moe_layer_few's scratch, and only that call
+ * asks for it: moe_layer and the stage calls accept what comes before (of
+ * which moe_layer needs all; the stage calls use the control block and their
+ * own scratch).  So a workspace that holds moe_layer's largest batch holds its
+ * smaller ones, while moe_layer_few's few tokens can ask for more than a larger
+ * batch of moe_layer: for both, take the maximum over the configurations.
+ * Returns 0 for an invalid configuration. */
 size_t moe_workspace_size(const moe_config_t* cfg);
 
 /* Router projection and gating_top_k_softmax.

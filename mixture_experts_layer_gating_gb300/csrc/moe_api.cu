@@ -240,9 +240,7 @@ Layout make_layout(const moe_config_t* c) {
     L.hs16 = take(T * Is * 2);
     L.hs_inv = take(T * 4);
   }
-  // moe_layer_few's scratch is the last region
-  if (const size_t few = few_workspace_bytes(c)) take(few);
-  L.total = cur;
+  L.total = cur;  // without moe_layer_few's scratch, which follows
   return L;
 }
 
@@ -591,7 +589,7 @@ extern "C" {
 
 size_t moe_workspace_size(const moe_config_t* cfg) {
   if (!cfg_valid(cfg)) return 0;
-  return make_layout(cfg).total;
+  return make_layout(cfg).total + few_workspace_bytes(cfg);
 }
 
 size_t moe_workspace_offset(const moe_config_t* cfg, int which) {

@@ -41,3 +41,23 @@ def test_layer_survives_a_barrier_that_gives_up(w, left_over):
     out = _call(cfg, d, ws)
     assert torch.equal(out, want) and moe.moe_read_device_status(ws) == 0
     _check(cfg, d, w, ws, out, "swiglu", True)
+
+
+def test_moe_layer_for_few_tokens_in_a_larger_batch_s_workspace():
+    """moe_layer for 16 tokens in a workspace for 64, which moe_layer_few's scratch
+    does not fit into."""
+    D, E, k, I = 2048, 128, 8, 768
+    cfg = moe.make_config(16, D, E, k, I)
+    n, guard = moe.moe_workspace_size(moe.make_config(64, D, E, k, I)), 1 << 16
+    assert n < moe.moe_workspace_size(cfg)
+    room = torch.zeros(n + guard, dtype=torch.uint8, device="cuda")
+    room[n:] = 0xA5
+    d = _inputs("bf16", 16, D, E, k, I, 0, seed=6)
+    out = torch.full((16, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    args = [d[i] for i in ("x", "Wg", "bias", "W13", "s13", "W2", "s2", "W13s", "s13s", "W2s", "s2s")]
+    moe.moe_layer(cfg, *args, out, room[:n])
+    assert moe.moe_read_device_status(room) == 0
+    _check(cfg, d, "bf16", room[:n], out, "swiglu", True, where="cuda")
+    assert (room[n:] == 0xA5).all()
+    with pytest.raises(moe.MoEError):
+        _call(cfg, d, room[:n], out)
