@@ -328,9 +328,17 @@ def dequantize_w4(Wq, scales, zeros=None, stream=None):
     """bf16 weights [.., K, N] of the 4-bit ones, written by moe_dequantize_w4."""
     import torch
 
-    if Wq.dim() not in (2, 3) or Wq.dim() != scales.dim():
-        raise ValueError("dequantize_w4 takes [N, K/2] or [G, N, K/2] codes and scales like them")
+    if Wq.dim() not in (2, 3) or Wq.dim() != scales.dim() or Wq.shape[:-1] != scales.shape[:-1]:
+        raise ValueError("dequantize_w4 takes [N, K/2] or [G, N, K/2] codes and scales [.., N, K/group] of as many rows")
+    if Wq.dtype != torch.uint8 or scales.dtype != torch.bfloat16:
+        raise ValueError("dequantize_w4 takes uint8 codes and bf16 scales")
     lead, N, K = tuple(Wq.shape[:-2]), Wq.shape[-2], 2 * Wq.shape[-1]
+    if not K or K not in [scales.shape[-1] * g for g in (32, 64, 128)]:
+        raise ValueError("dequantize_w4: groups of 32, 64 or 128 inputs")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+        raise ValueError("dequantize_w4: zero points are uint8, one for each scale")
+    if any(t is not None and t.device != Wq.device for t in (scales, zeros)):
+        raise ValueError("dequantize_w4: codes, scales and zero points on one device")
     W = torch.empty((*lead, K, N), dtype=torch.bfloat16, device=Wq.device)
     moe_dequantize_w4(Wq, scales, zeros, lead[0] if lead else 1, K, N, K // scales.shape[-1], W, stream)
     return W

@@ -1,0 +1,46 @@
+"""Refusals of the Python helpers of the 4-bit forms: what would be read out of
+range, or as another type, is refused before any pointer is taken (the tensors here
+are on the CPU, which is the last thing refused)."""
+import pytest
+import torch
+
+import mixture_experts_layer_gating_gb300 as moe
+from tests._lib import ensure_library
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    return ensure_library()
+
+
+def _w4(*lead, N=8, K=128, g=64):
+    return torch.zeros(*lead, N, K // 2, dtype=torch.uint8), torch.zeros(*lead, N, K // g, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("lead", [(), (3,)])
+def test_dequantize_compares_codes_scales_and_zeros(lead):
+    q, s = _w4(*lead)
+    z = torch.zeros(s.shape, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA device"):  # right, but not on a GPU
+        moe.dequantize_w4(q, s, z)
+    fewer = s[..., :4, :].contiguous()
+    for bad in (fewer, s.float(), s[..., :1].expand(*lead, 8, 16).contiguous(), s[..., :0]):
+        with pytest.raises(ValueError, match="dequantize_w4"):
+            moe.dequantize_w4(q, bad)
+    for bad in (z[..., :4, :].contiguous(), z[..., :1].contiguous(), z.int(), s):
+        with pytest.raises(ValueError, match="dequantize_w4"):
+            moe.dequantize_w4(q, s, bad)
+    with pytest.raises(ValueError, match="dequantize_w4"):
+        moe.dequantize_w4(q.int(), s)
+
+
+def test_dequantize_compares_the_leading_size():
+    q, _ = _w4(3)
+    _, s = _w4(2)
+    with pytest.raises(ValueError, match="dequantize_w4"):
+        moe.dequantize_w4(q, s)
+
+
+def test_dequantize_refuses_empty_rows():
+    with pytest.raises(ValueError, match="dequantize_w4"):
+        moe.dequantize_w4(torch.zeros(8, 0, dtype=torch.uint8), torch.zeros(8, 0, dtype=torch.bfloat16))
