@@ -148,27 +148,31 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_raw_stream = None  # torch's (device) -> cudaStream_t of its current stream
+def _first_stream() -> int:
+    """Finds torch's way to the current stream, once."""
+    global _current_stream
+    import torch
+
+    # an integer straight away where this torch has it: building a Stream object
+    # takes microseconds
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _current_stream()
+
+
+_current_stream = _first_stream
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        global _raw_stream
-        import torch
-
-        if _raw_stream is None:
-            # an integer straight away where this torch has it: building a Stream
-            # object takes microseconds
-            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-                lambda device: torch.cuda.current_stream(device).cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _ws(ws):
-    return _ptr(ws), (ws.numel() * ws.element_size() if hasattr(ws, "numel") else 0)
+    return _ptr(ws), getattr(ws, "nbytes", 0)
 
 
 def _check(fn: str, st: int):
@@ -292,9 +296,20 @@ def _float_dtype(t) -> int:
 def moe_linear_w4(M: int, K: int, N: int, group: int, x, Wq, scales, zeros, y, ws, stream=None) -> None:
     """y [M, N] (bf16 or fp32) = x [M, K] times 4-bit weights [N, K/2] with
     scales (and zero points, or None) [N, K/group]."""
+    y_dtype, nk = _float_dtype(y), N * K
+    try:  # (in one expression: a small product takes little longer than its call)
+        fits = (group < 1 or x.nbytes >= 2 * M * K and 2 * Wq.nbytes >= nk and group * scales.nbytes >= 2 * nk
+                and y.nbytes >= (4 if y_dtype == MOE_F32 else 2) * M * N
+                and _FLOAT_DTYPES.get(x.dtype) == MOE_BF16 == _FLOAT_DTYPES.get(scales.dtype)
+                and (zeros is None or group * zeros.nbytes >= nk and zeros.itemsize == 1))
+    except AttributeError:  # addresses, or None, which the library refuses
+        fits = True
+    if not fits:
+        raise ValueError("moe_linear_w4 takes bf16 x [M, K], codes [N, K/2], bf16 scales [N, K/group], zero points "
+                         "of one byte and y [M, N]")
     wp, wb = _ws(ws)
     _check("moe_linear_w4", load_library().moe_linear_w4(
-        M, K, N, group, _ptr(x), _ptr(Wq), _ptr(scales), _ptr(zeros), _ptr(y), _float_dtype(y), wp, wb,
+        M, K, N, group, _ptr(x), _ptr(Wq), _ptr(scales), _ptr(zeros), _ptr(y), y_dtype, wp, wb,
         _stream(stream)))
 
 

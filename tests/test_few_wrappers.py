@@ -44,3 +44,25 @@ def test_dequantize_compares_the_leading_size():
 def test_dequantize_refuses_empty_rows():
     with pytest.raises(ValueError, match="dequantize_w4"):
         moe.dequantize_w4(torch.zeros(8, 0, dtype=torch.uint8), torch.zeros(8, 0, dtype=torch.bfloat16))
+
+
+def test_linear_compares_its_tensors_with_its_sizes():
+    M, K, N, g = 3, 128, 8, 64
+    q, s = _w4(N=N, K=K, g=g)
+    good = dict(x=torch.zeros(M, K, dtype=torch.bfloat16), Wq=q, scales=s,
+                zeros=torch.zeros(s.shape, dtype=torch.uint8), y=torch.zeros(M, N))
+    ws = torch.zeros(moe.moe_linear_w4_workspace_size(M, K, N), dtype=torch.uint8)
+
+    def call(**other):
+        a = dict(good, **other)
+        moe.moe_linear_w4(M, K, N, g, a["x"], a["Wq"], a["scales"], a["zeros"], a["y"], ws)
+
+    for a in ({}, {"zeros": None}, {"y": torch.zeros(M, N, dtype=torch.bfloat16)}, {"x": torch.zeros(M + 1, K).bfloat16()}):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(**a)
+    for name, t in good.items():
+        with pytest.raises(ValueError, match="moe_linear_w4 takes"):
+            call(**{name: t[:-1].contiguous()})
+    for name in ("x", "scales", "zeros"):  # of other types
+        with pytest.raises(ValueError, match="moe_linear_w4 takes"):
+            call(**{name: good[name].float()})
