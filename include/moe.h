@@ -304,7 +304,7 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
  * for the projections around the layer (a dense or shared projection, the
  * logits of a decode step).  No page has this operator by itself; the Qwen3-MoE
  * page's 4-bit weights are its source.
- *   M       rows of x, 0..32 (more: MOE_ERR_UNSUPPORTED).
+ *   M       rows of x, 0..32 (more: MOE_ERR_UNSUPPORTED; 0: nothing is done, x and y may be NULL).
  *   K, N    inputs, a multiple of `group`, at most 65535 groups; outputs, any N
  *           from 1 to 2^31 - 512.
  *   group   32, 64 or 128.

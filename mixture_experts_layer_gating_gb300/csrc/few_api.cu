@@ -175,9 +175,9 @@ int moe_linear_w4(int32_t M, int32_t K, int32_t N, int32_t group, const void* x,
   if (M > kStreamMaxRows || (y_dtype != MOE_BF16 && y_dtype != MOE_F32)) return MOE_ERR_UNSUPPORTED;
   const size_t need = moe_linear_w4_workspace_size(M, K, N);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (M == 0) return MOE_OK;  // (an empty x or y may have no address)
   for (const void* q : {x, Wq, scales, static_cast<const void*>(y)})
     if (!q || !al16(q)) return MOE_ERR_INVALID_ARG;
-  if (M == 0) return MOE_OK;
   const cudaError_t e =
       launch_linear_w4(M, K, N, group, x, Wq, scales, static_cast<const uint8_t*>(zeros), y,
                        y_dtype == MOE_F32, &reinterpret_cast<ControlBlock*>(ws)->err,

@@ -66,3 +66,11 @@ def test_linear_compares_its_tensors_with_its_sizes():
     for name in ("x", "scales", "zeros"):  # of other types
         with pytest.raises(ValueError, match="moe_linear_w4 takes"):
             call(**{name: good[name].float()})
+
+
+def test_linear_of_no_rows_takes_empty_tensors(lib):
+    """An empty tensor has no address."""
+    P = 1 << 20
+    assert lib.moe_linear_w4(0, 128, 8, 64, None, P, P, None, None, moe.MOE_BF16, P, 1 << 30, None) == 0
+    assert lib.moe_linear_w4(0, 128, 8, 64, None, P, P, None, None, moe.MOE_BF16, P, 0, None) == -5
+    assert lib.moe_linear_w4(0, 100, 8, 64, None, P, P, None, None, moe.MOE_BF16, P, 1 << 30, None) == -1

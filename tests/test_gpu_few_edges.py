@@ -61,3 +61,12 @@ def test_moe_layer_for_few_tokens_in_a_larger_batch_s_workspace():
     assert (room[n:] == 0xA5).all()
     with pytest.raises(moe.MoEError):
         _call(cfg, d, room[:n], out)
+
+
+def test_linear_of_no_rows():
+    x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(8, 64, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(8, 2, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(moe.moe_linear_w4_workspace_size(0, 128, 8), dtype=torch.uint8, device="cuda")
+    moe.moe_linear_w4(0, 128, 8, 64, x, q, s, None, torch.empty(0, 8, device="cuda"), ws)
+    assert moe.moe_read_device_status(ws) == 0
