@@ -92,8 +92,8 @@ __device__ __forceinline__ float few_act(float g, float u, int act) {
 // chunks.  Index 0 of
 // S, C, K, width: the shared expert, 1: the routed ones.
 struct FewPass {
-  // A chunk counts w[r] units in the split: more than eight rows make a shared
-  // expert's chunk slower than HBM (two tiles to multiply, more rows to feed).
+  // A chunk counts w[r] units in the split: of e4m3 and 4-bit weights, more than eight
+  // rows make a chunk slower than HBM (two tiles to multiply, more rows to feed).
   Split sp;
   int w[2];
   long long lo, hi, shared;  // chunks; shared: of the shared expert (all its entries)
@@ -168,11 +168,19 @@ __device__ __forceinline__ FewPass few_pass(const FewParams& p, bool down, int n
   f.shared_entries = p.Is > 0 ? (p.T + kFewGroup - 1) / kFewGroup : 0;
   f.shared = static_cast<long long>(f.shared_entries) * f.S[0] * f.C[0];
   f.w[0] = f.w[1] = 1;
-  if (p.T > 8 && f.shared > 0) {
-    // The down rows of 4-bit and e4m3 [N, K] weights are many to a stage.  16 tokens,
-    // shared expert 1% to 6% of the bytes, against equal weights: 4-bit 16 to 32 tokens
-    // 153 -> 144 and 185 -> 172 us (2:1 since a team takes a short strip alone: 135 ->
-    // 124); e4m3 [K, N] 856 -> 799; e4m3 [N, K] 1013 -> 813.
+  if (KIND != kStreamBf16 && p.T > 8 && f.shared > 0 && p.T * p.k <= 5 * na) {
+    // The shared expert's entries have more than eight rows, two tiles to multiply, the
+    // routed ones mostly one while they have few rows on average.  Weighed against equal
+    // parts, in us (32 tokens, 4096, I 2048 or 1024, shared 2048, by rows a routed entry):
+    //                       1.6 (64 experts, T 16)   4 (16 experts)   8 (8)        16 (4)
+    //   4-bit, groups of 64     139 : 160             122 : 135        96 : 93      88 : 84
+    //   e4m3 [N, K]             117 : 140             109 : 123        92 : 85      83 : 75
+    //   e4m3 [K, N]             135 : 137             104 : 104        81 : 78      78 : 75
+    //   bf16 (3:2)              183 : 183             152 : 152       107 : 102     85 : 83
+    // (12 tokens, 4 experts, 6 rows an entry: 61.4 : 60.7, 52.0 : 52.0, 61.2 : 60.0, 65.2 :
+    // 64.1).  17 tokens, whose second shared entry has one row, 128 experts, 2816: 118 : 154,
+    // 120 : 142, 157 : 156.  2:1 since a team takes a short strip alone (135 -> 124 us at 19
+    // tokens).
     constexpr bool nk8 = KIND == kStreamFp8Nk;
     if (KIND == kStreamW4 && down && f.C[1] <= kFewShort) f.w[0] = 2;
     else if (KIND == kStreamW4) f.w[0] = 4, f.w[1] = 3;
