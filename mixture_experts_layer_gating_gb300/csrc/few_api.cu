@@ -34,8 +34,8 @@ bool few_dtype(const moe_config_t* c) {
 }
 
 int few_planes(const moe_config_t* c) {
-  // at least two k16 steps per warp of a unit, at most one unit per CTA of a
-  // 152-SM device
+  // at least two k16 steps per warp of a unit, at most one unit per CTA of a GB300's
+  // 152 (a constant: the workspace's size must not depend on the current device)
   const int steps = ceil_div(c->D, 16), se = ceil_div(c->E, 64);
   return std::max(1, std::min({kFewMaxPlanes, steps / 16, 152 / se}));
 }
@@ -80,10 +80,9 @@ bool w4_args_ok(int64_t G, int K, int N, int group) {
 
 namespace moe {
 
-bool few_supported(const moe_config_t* c) {
-  return few_dtype(c) && c->T >= 1 && c->T <= kStreamMaxRows;
+size_t few_workspace_bytes(const moe_config_t* c) {
+  return few_dtype(c) && c->T >= 1 && c->T <= kStreamMaxRows ? few_layout(c).total : 0;
 }
-size_t few_workspace_bytes(const moe_config_t* c) { return few_supported(c) ? few_layout(c).total : 0; }
 
 }  // namespace moe
 

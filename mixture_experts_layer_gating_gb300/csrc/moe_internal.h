@@ -81,9 +81,8 @@ inline int w4_group(int dt) {
 }
 
 // ---------------------------------------------------------------- few_api.cu
-// Whether moe_layer_few takes the configuration, and the scratch it needs at
-// the end of the workspace (0: not taken).
-bool few_supported(const moe_config_t* c);
+// The scratch that moe_layer_few needs at the end of the workspace (0: it does
+// not take the configuration).
 size_t few_workspace_bytes(const moe_config_t* c);
 
 // ------------------------------------------ linear_w4.cu, linear_w4_wide.cu
