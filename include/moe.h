@@ -268,8 +268,15 @@ int moe_layer(const moe_config_t* cfg, const void* x, const void* Wg, const floa
               void* ws, size_t ws_bytes, void* stream);
 
 /* The whole layer for a few tokens (1 <= T <= 32) as one kernel launch: the
- * decode step of a small batch, where moe_layer's launches cost more than the
- * weights take to read.  Pages: "用SGLang-JAX在TPU上优化Ling-2.6-1T" §4 (decode
+ * decode step of a small batch.  When to take it rather than moe_layer, measured
+ * with weights read from HBM (1 to 32 tokens, five layers in bf16, one in both
+ * e4m3 layouts): it is faster for FP8_E4M3 weights at every T (90 us against 178 at
+ * one token of a Ling-style layer, 1239 against 2079 at 32), for FP8_E4M3_NK up to
+ * 16 tokens (90 : 126, 799 : 813; 32: 1280 : 1234), for bf16 up to 8 tokens (34 : 41
+ * at one token of a Qwen3-style layer, 94 : 107 at 8) and mostly beyond (176 : 183 at
+ * 32).  moe_layer is faster where bf16 layers have many small experts and a wide
+ * shared one (Gemma-style: 138 : 140 at 8 tokens, 205 : 198 at 16, 264 : 246 at 32).
+ * 4-bit weights have no other call.  Pages: "用SGLang-JAX在TPU上优化Ling-2.6-1T" §4 (decode
  * near the weight-read bound); "CANN/cann-recipes-infer：Qwen3-MoE优化" (the
  * single-batch decode it is measured on, and its 4-bit weights).
  *   Arguments, layouts and results as moe_layer, with any E in 1..512 (W_g's
@@ -283,8 +290,9 @@ int moe_layer(const moe_config_t* cfg, const void* x, const void* Wg, const floa
  *   power of two that puts its largest element in [2^14, 2^15): x keeps its bits
  *   but where an element is less than 2^-31 of the row's largest (it then errs by
  *   at most 2^-39 of that one), h is rounded to 11 significant bits (same floor).
- *   (Rows whose largest element is below 2^-86 keep fewer bits.)  All sums are fp32; e4m3 scales multiply the finished sums, group
- *   scales the fp32 sums of their group.  The weighted sum over a token's experts
+ *   (Rows whose largest element is below 2^-86 keep fewer bits.)  All sums are
+ *   fp32; e4m3 scales multiply the finished sums, group scales the fp32 sums of their
+ *   group.  The weighted sum over a token's experts
  *   is fp32 in a fixed order (a tree over j mod 8, the shared expert as j = k),
  *   rounded once to bf16.  The same inputs give the same bits on every call.
  *   Logits, ids and weights are left in the workspace (MOE_WS_LOGITS,

@@ -20,15 +20,18 @@
 //   -- barrier 3
 //   4  out = sum_j w_j y_j + shared, one rounding
 // The producer runs ahead of the barriers: the weights of the next phase are on
-// their way while a barrier is waited for (up to 192 KB per SM), and the shared
+// their way while a barrier is waited for (160 KB per SM for bf16 and e4m3 weights, 128
+// for e4m3 [N, K] and bf16 with more than eight tokens, 128 and 96 for 4-bit ones), and the shared
 // expert's are brought into L2 while the routing is found out.
 //
 // Figures (D, E, k, I, shared I; floor: the weights' bytes at 6.8 TB/s):
-//   bf16, 8 tokens, 2816, 128, 8, 704, 2112        140 us, floor 100
-//   e4m3 [N, K], 1 token, 8192, 256, 8, 2048, 2048  92, floor 67
-//   e4m3 [K, N], 16 tokens, the same               800, floor 764 (6.4 TB/s)
-//   4-bit, 19 tokens, 2816, 128, 8, 704, 2112      124, floor 43
-//   4-bit, 1 token, 2048, 128, 8, 768               26, floor 3
+//   bf16, 1 token, 2048, 128, 8, 768                35 us, floor 11
+//   bf16, 8 tokens, 2816, 128, 8, 704, 2112        133 to 142, floor 100
+//   e4m3, 1 token, 8192, 256, 8, 2048, 2048         92 ([N, K]), 90 ([K, N]), floor 67
+//   e4m3, 16 tokens, the same                      800 ([N, K]), 783 to 830 ([K, N]), floor 764
+//   4-bit, 19 tokens, 2816, 128, 8, 704, 2112      124 to 130, floor 43
+//   4-bit, 1 token, 2048, 128, 8, 768               27, floor 3
+// (a range: GPUs differ)
 // What bounds it: HBM where a CTA has many stages and a stage's products take less
 // than its bytes (697 cycles: e4m3 218 to 383, bf16 145 to 304, 4-bit 552 for eight
 // rows and 724 for sixteen); else the chain of routing (7 us at one token), three

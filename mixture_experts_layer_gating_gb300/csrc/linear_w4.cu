@@ -10,8 +10,10 @@
 // runs over the CTAs, so that every SM streams as many bytes whatever N; the parts
 // of a strip that several CTAs share are added by the one that arrives last.
 //
-// 8192 x 8192, one row 16.3 us (35 MB; HBM floor 5.2), four 18.7, eight 19.1; 2048 x
-// 2048, one row 5.8; 13 rows x 2816 x 4224 12.6.  What bounds it: a CTA has 13 stages
+// In a graph, weights from HBM: 8192 x 8192, groups of 128, one row 15.0 us (35 MB; HBM
+// floor 5.2; with zero points 16.5), four 17.3, eight 17.5, sixteen 20.0; 2048 x 2048, one
+// row 6.1 (a call from Python after another: 6.6, of which the host takes 5.8); 13 rows x
+// 2816 x 4224, groups of 32, 12.8.  What bounds it: a CTA has 13 stages
 // at 8192 x 8192, each 645 cycles of conversions and products (HBM brings one in 697),
 // after the launch and the first bytes (4 us) and before the shared strips' sums (3).
 #include "linear_w4.cuh"

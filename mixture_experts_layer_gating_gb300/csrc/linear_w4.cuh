@@ -102,8 +102,9 @@ __device__ __noinline__ void lin_finish(const LinParams& p, const Split& sp, flo
   const int items4 = items / 4;
   const float4* head = reinterpret_cast<const float4*>(p.part) + (static_cast<size_t>(c0) * 2 + 1) * items4;
   const float4* rest = reinterpret_cast<const float4*>(p.part) + static_cast<size_t>(c0 + 1) * 2 * items4;
-  // (one row of 2048 x 2048: 5.8 us; with four and two as for the wide strips 6.8, with
-  // one and eight at 13 rows 14.2 for 12.6: the code is run once and waits for itself)
+  // (one row of 2048 x 2048 in a graph: 5.8 us, with four and two as for the wide strips
+  // 6.8; 13 rows of 2816 x 4224: 12.6, with one and eight 14.2: the code is run once and
+  // waits for itself)
   constexpr int U = STRIP > kLinStrip ? 4 : 1, V = STRIP > kLinStrip ? 2 : 4;
 #pragma unroll 1
   for (int i = i0; i < items4; i += U * THREADS) {

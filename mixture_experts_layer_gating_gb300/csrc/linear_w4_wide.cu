@@ -13,8 +13,8 @@
 // expanded into shared memory.  A group's sums come back to the thread of the
 // weight row, which multiplies them by the group's scale and adds in fp32.
 //
-// 32 rows x 4096 x 131072 (HBM floor 42 us): groups of 128 74 us (3.9 TB/s; mma.sync
-// 170), of 64 76, of 32 94; with zero points 79, 86, 108.  What bounds it: eleven
+// 32 rows x 4096 x 131072, fp32 out (HBM floor 42 to 47 us): groups of 128 74 us (mma.sync
+// 170), of 64 77, of 32 95; with zero points 80, 88, 108.  What bounds it: eleven
 // half-rate instructions for eight codes, in two converter warps a scheduler, which
 // take 700 of the 1100 cycles of a unit and share the scheduler with others (adders,
 // on two schedulers an issuer) in the rest: ALU pipe 49 %, issue 53 % (8192 x 32768).

@@ -151,7 +151,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
 // (bf16) above a code makes the number 1024 + code or 128 + code; the
 // differences are whole numbers, exact.  In fp16 a code four bits higher up is
 // 1024 + 16 code, and a fused multiply-add by 1/16 brings it down; bf16 has too
-// few bits for that and shifts.
+// few bits for that and shifts.  (Published for weights of 8 and 4 bits by Kim, Henry,
+// Fahim and Hassan Awadalla, "Who Says Elephants Can't Run: Bringing Large Scale MoE
+// Models into Cloud Scale Production", 2022.)
 template <bool F16>
 __device__ __forceinline__ void w4_pairs(uint32_t word, uint32_t zero2, uint32_t (&v)[4]) {
   if constexpr (F16) {
@@ -288,7 +290,8 @@ __device__ __forceinline__ void split_bf16(float v, __nv_bfloat16& hi, __nv_bflo
 }
 
 // ------------------------------------------------------------ work of a CTA
-// N units over Gp CTAs: CTA b takes [N b / Gp, N (b + 1) / Gp).
+// N units over Gp CTAs: CTA b takes [N b / Gp, N (b + 1) / Gp).  (Equal runs that cut a
+// tile's sum between CTAs: Osama, Merrill, Cecka, Garland and Owens, PPoPP 2023.)
 struct Split {
   long long N;
   int Gp;
