@@ -349,6 +349,110 @@ int moe_quantize_w4(const void* W, int32_t w_dtype, int64_t G, int32_t K, int32_
 int moe_dequantize_w4(const void* Wq, const void* scales, const void* zeros, int64_t G, int32_t K,
                       int32_t N, int32_t group, void* W, void* stream);
 
+/* How moe_route_gated and moe_block choose experts.  With logits l [E] of a token
+ * (x W_g + logit_bias, fp32) and its scores p, all in fp32:
+ *   p       softmax over the E experts, or sigmoid of each logit (score).
+ *   c       p + select_bias: takes part in the choice, not in the weights.
+ *   groups  the experts in n_group runs of E / n_group; a group's value is the
+ *           largest c in it, or the sum of the two largest (group_score); the
+ *           topk_group largest groups stay, the others' experts cannot be chosen.
+ *   ids     the k largest c, descending.
+ *   w       p of the chosen (cfg->renormalize: divided by their sum), times scale.
+ * Ties, of groups and of experts, go to the lower index.  Without select_bias the
+ * order of experts (and of groups by their largest) is taken from the logits, which
+ * order as p does and differ where p no longer does.  Renormalised weights of a
+ * softmax are the softmax over the chosen logits; of sigmoids below e^-60 the same
+ * (their ratios there, kept from underflow).  A non-finite logit (or c) counts as
+ * -infinity: p is 0, the expert is chosen last and not part of a group's sum,
+ * MOE_DEV_NONFINITE_LOGIT is set; a token that has only such experts to choose gets
+ * weights scale / k. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2_SUM = 1 } moe_group_score_t;
+typedef struct {
+  int32_t score;       /* moe_score_t */
+  int32_t n_group;     /* 1..32, divides E; 1: no groups */
+  int32_t topk_group;  /* 1..n_group, topk_group * E / n_group >= k */
+  int32_t group_score; /* moe_group_score_t */
+  float scale;         /* factor of the weights, finite */
+} moe_gate_t;
+
+/* moe_route with the choice above.  Arguments as there (x NULL: `logits` is the
+ * input), and
+ *   gate         not NULL.
+ *   select_bias  [E] fp32 or NULL. */
+int moe_route_gated(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const void* Wg,
+                    const float* logit_bias, const float* select_bias, float* logits,
+                    int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, void* stream);
+
+/* The residual's addition and the root-mean-square norm of rows of D values, and the
+ * normed rows in 8 bits:
+ *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight
+ * in fp32 (a row whose squares leave fp32's range is scaled by a power of two first).
+ * Pages: "CANN/cann-recipes-infer：Qwen3-MoE优化", section "融合RMSNorm + Cast" (the
+ * norm writes the forms that its readers take); "用SGLang-JAX在TPU上优化
+ * Ling-2.6-1T" §5 "激活量化" (8-bit rows with dynamic scales).
+ *   rows, D   rows >= 0; D a multiple of 8, 8..32768 (more: MOE_ERR_UNSUPPORTED).
+ *   dtype     MOE_BF16 or MOE_F32: x, residual, weight, sum_out and y.
+ *   x         [rows, D].
+ *   residual  [rows, D] or NULL: nothing is added.
+ *   weight    [D].
+ *   eps       finite, >= 0.
+ *   sum_out   [rows, D] out or NULL: s, rounded once.  May be x or residual itself.
+ *   y         [rows, D] out or NULL, rounded once.  May be x or residual itself.
+ *   q         [rows, D] e4m3 out or NULL; y or q is needed.
+ *   q_group   values to a scale: 0 (the whole row), 32, 64 or 128 (dividing D).
+ *   q_scales  [rows, D / q_group] fp32 out ([rows] for q_group 0), with q.
+ * A scale is max |y| / 448 of its values (1 where all are zero, at least 2^-126, NaN where one
+ * is an infinity or NaN), q = e4m3(y / scale) from y before any other rounding, nearest
+ * even.  All pointers 16-byte aligned; outputs overlap nothing but as said.  NULL tensors
+ * are taken when rows is 0.  No workspace. */
+int moe_add_rms_norm(int32_t rows, int32_t D, int32_t dtype, const void* x, const void* residual,
+                     const void* weight, float eps, void* sum_out, void* y, void* q, int32_t q_group,
+                     float* q_scales, void* stream);
+
+/* The low-rank adapter of each row's own request, beside a projection that all rows
+ * share (moe_linear_w4's, or any):
+ *   y[t, n] = base[t, n] + scales[a] * sum_j (sum_k x[t, k] A[a, j, k]) B[a, n, j],  a = ids[t]
+ *   T         rows, >= 0.
+ *   K, N, r   inputs and outputs, multiples of 8 to 2^24; rank, a multiple of 8 to 256 (more:
+ *             MOE_ERR_UNSUPPORTED).  Adapters of smaller ranks are padded with zeros.
+ *   n         adapters, 1..16384 (more: MOE_ERR_UNSUPPORTED).
+ *   x         [T, K] bf16.
+ *   ids       [T] int32 in any order; a row whose id is not in [0, n) has no adapter:
+ *             its y is its base.
+ *   A, B      [n, r, K] and [n, N, r] bf16.
+ *   scales    [n] fp32, or NULL: 1.
+ *   base      [T, N] of y's type, y itself (in place), or NULL: 0.
+ *   y         [T, N] bf16 or fp32 (y_dtype), one rounding.
+ *   ws        moe_lora_workspace_size(T, K, N, r, n) bytes (0: sizes not taken),
+ *             256-byte aligned, need not be zero; holds nothing between calls.
+ * x A^T is summed in fp32 and multiplied by B as two bf16 terms (16 significant bits),
+ * as three (24) where y is fp32; its sums are fp32.  The same inputs give the same bits
+ * on every call of the same sizes.  Pointers but ids and scales 16-byte aligned, those 4. */
+size_t moe_lora_workspace_size(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n);
+int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* x,
+             const int32_t* ids, const void* A, const void* B, const float* scales, const void* base,
+             void* y, int32_t y_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* A pre-norm residual MoE block: moe_add_rms_norm, then moe_layer with moe_route_gated's
+ * choice, on one stream:
+ *   sum_out = x + residual,  y = norm(sum_out) * norm_weight,  out = layer(y)
+ *   gate        NULL: moe_layer's choice (softmax top-k), select_bias NULL then.
+ *   norm_weight [D] act_dtype, or NULL: no norm, the layer takes x (residual, sum_out
+ *               and y NULL, eps 0).
+ *   y           [T, D] act_dtype out: the normed rows, which the router projects.  May
+ *               not overlap anything else.
+ *   x, residual, sum_out, eps as in moe_add_rms_norm; the other arguments, the weight
+ *   types, the workspace and the errors as in moe_layer (4-bit weights:
+ *   MOE_ERR_UNSUPPORTED).
+ * FP8_E4M3_NK_A8 layers take their 8-bit rows from the norm (rounded once, from fp32),
+ * instead of from y: one launch and one reading of y less. */
+int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const void* residual,
+              const void* norm_weight, float eps, const void* Wg, const float* logit_bias,
+              const float* select_bias, const void* W13, const float* s13, const void* W2,
+              const float* s2, const void* W13s, const float* s13s, const void* W2s, const float* s2s,
+              void* sum_out, void* y, void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Device byte offsets inside `ws` where moe_layer keeps its intermediates,
  * for inspection (logits, ids, weights, counts, offsets, sorted_rows, dest,
  * x_perm, h, y_perm, h_s, s).  `which` is one of the MOE_WS_* indices;

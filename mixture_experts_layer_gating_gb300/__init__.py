@@ -20,6 +20,8 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "moe.h")
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_NK, MOE_FP8_E4M3_NK_A8 = 0, 1, 2, 3, 4
 MOE_W4_G32, MOE_W4_G64, MOE_W4_G128 = 5, 6, 7
 MOE_ACT_SWIGLU, MOE_ACT_GEGLU_TANH = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2_SUM = 0, 1
 MOE_OK = 0
 MOE_DEV_BAD_EXPERT_ID = 0x1
 MOE_DEV_BAD_OFFSETS = 0x2
@@ -34,6 +36,8 @@ _DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3,
            "w4_g32": MOE_W4_G32, "w4_g64": MOE_W4_G64, "w4_g128": MOE_W4_G128}
 MOE_FEW_MAX_TOKENS = 32  # most tokens of moe_layer_few, most rows of moe_linear_w4
 _ACTS = {"swiglu": MOE_ACT_SWIGLU, "geglu_tanh": MOE_ACT_GEGLU_TANH}
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2_sum": MOE_GROUP_TOP2_SUM}
 
 
 class MoEConfig(ctypes.Structure):
@@ -41,6 +45,13 @@ class MoEConfig(ctypes.Structure):
 
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("T", "D", "E", "k", "I", "I_shared", "act", "act_dtype", "w_dtype", "renormalize")]
+
+
+class MoEGate(ctypes.Structure):
+    """Mirror of moe_gate_t."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_group", "topk_group", "group_score")] + [
+        ("scale", ctypes.c_float)]
 
 
 class MoEError(RuntimeError):
@@ -75,6 +86,14 @@ _SIGS = {
                                        ctypes.c_int32, _P, _P, _P]),
     "moe_dequantize_w4": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                          ctypes.c_int32, _P, _P]),
+    "moe_route_gated": (ctypes.c_int, [ctypes.POINTER(MoEConfig), ctypes.POINTER(MoEGate)] + [_P] * 7 +
+                        [_P, ctypes.c_size_t, _P]),
+    "moe_add_rms_norm": (ctypes.c_int, [ctypes.c_int32] * 3 + [_P] * 3 + [ctypes.c_float] + [_P] * 3 +
+                         [ctypes.c_int32, _P, _P]),
+    "moe_lora_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 5),
+    "moe_lora": (ctypes.c_int, [ctypes.c_int32] * 5 + [_P] * 7 + [ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "moe_block": (ctypes.c_int, [ctypes.POINTER(MoEConfig), ctypes.POINTER(MoEGate)] + [_P] * 3 + [ctypes.c_float] +
+                  [_P] * 14 + [_P, ctypes.c_size_t, _P]),
 }
 MOE_OPT_PAIR_TILES = 1
 MOE_OPT_GATHER_A = 2
@@ -134,6 +153,12 @@ def config_from_shape(shape, fp8_layout: str = "kn") -> MoEConfig:
         w = "fp8_e4m3_nk_a8"
     return make_config(shape.T, shape.D, shape.E, shape.k, shape.I, shape.I_shared, shape.act,
                        shape.act_dtype, w, shape.renormalize)
+
+
+def make_gate(score: str = "sigmoid", n_group: int = 1, topk_group: int = 1, group_score: str = "top2_sum",
+              scale: float = 1.0) -> MoEGate:
+    """How moe_route_gated and moe_block choose experts (moe_gate_t)."""
+    return MoEGate(_SCORES[score], n_group, topk_group, _GROUP_SCORES[group_score], scale)
 
 
 def _ptr(t) -> Optional[int]:
@@ -357,6 +382,79 @@ def dequantize_w4(Wq, scales, zeros=None, stream=None):
     W = torch.empty((*lead, K, N), dtype=torch.bfloat16, device=Wq.device)
     moe_dequantize_w4(Wq, scales, zeros, lead[0] if lead else 1, K, N, K // scales.shape[-1], W, stream)
     return W
+
+
+def _gate(gate):
+    return None if gate is None else ctypes.byref(gate)
+
+
+def moe_route_gated(cfg, gate, x, Wg, logit_bias, select_bias, logits, topk_ids, topk_w, ws, stream=None):
+    """moe_route with softmax or sigmoid scores, a bias for the choice, groups and a factor (make_gate)."""
+    wp, wb = _ws(ws)
+    _check("moe_route_gated", load_library().moe_route_gated(
+        ctypes.byref(cfg), _gate(gate), _ptr(x), _ptr(Wg), _ptr(logit_bias), _ptr(select_bias), _ptr(logits),
+        _ptr(topk_ids), _ptr(topk_w), wp, wb, _stream(stream)))
+
+
+def moe_block(cfg, gate, x, residual, norm_weight, eps, Wg, logit_bias, select_bias, W13, s13, W2, s2, W13s, s13s,
+              W2s, s2s, sum_out, y, out, ws, stream=None):
+    """moe_add_rms_norm (norm_weight None: no norm), then moe_layer with the gate's choice (None: softmax top-k)."""
+    wp, wb = _ws(ws)
+    _check("moe_block", load_library().moe_block(
+        ctypes.byref(cfg), _gate(gate), _ptr(x), _ptr(residual), _ptr(norm_weight), eps, _ptr(Wg), _ptr(logit_bias),
+        _ptr(select_bias), _ptr(W13), _ptr(s13), _ptr(W2), _ptr(s2), _ptr(W13s), _ptr(s13s), _ptr(W2s), _ptr(s2s),
+        _ptr(sum_out), _ptr(y), _ptr(out), wp, wb, _stream(stream)))
+
+
+def moe_add_rms_norm(rows: int, D: int, x, residual, weight, eps: float, sum_out, y, q=None, q_scales=None,
+                     q_group: int = 0, stream=None) -> None:
+    """sum_out = x + residual and its root-mean-square norm times weight, as y (x's type) and / or as e4m3 rows q
+    with a scale per row (q_group 0) or per q_group values; None for what is not there or not wanted."""
+    dt = _float_dtype(x)
+    try:  # (in one expression: a small batch takes little longer than its call)
+        n, t = rows * D, x.dtype
+        nb = n * x.itemsize
+        fits = (x.nbytes >= nb and weight.nbytes >= D * x.itemsize and weight.dtype == t
+                and (residual is None or residual.nbytes >= nb and residual.dtype == t)
+                and (sum_out is None or sum_out.nbytes >= nb and sum_out.dtype == t)
+                and (y is None or y.nbytes >= nb and y.dtype == t)
+                and (q is None or q.itemsize == 1 and q.nbytes >= n)
+                and (q_scales is None or q_scales.nbytes >= 4 * rows * (D // q_group if q_group > 0 else 1)
+                     and q_scales.itemsize == 4 and q_scales.is_floating_point()))
+    except AttributeError:
+        fits = False
+    if not fits:
+        raise ValueError("moe_add_rms_norm takes x, residual, sum_out and y [rows, D] and weight [D] of one type, "
+                         "one-byte q [rows, D] and fp32 scales [rows, D / q_group]")
+    _check("moe_add_rms_norm", load_library().moe_add_rms_norm(
+        rows, D, dt, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(sum_out), _ptr(y), _ptr(q), q_group,
+        _ptr(q_scales), _stream(stream)))
+
+
+def moe_lora_workspace_size(T: int, K: int, N: int, r: int, n: int) -> int:
+    return int(load_library().moe_lora_workspace_size(T, K, N, r, n))
+
+
+def moe_lora(T: int, K: int, N: int, r: int, n: int, x, ids, A, B, scales, base, y, ws, stream=None) -> None:
+    """y [T, N] (bf16 or fp32) = base (None: 0; y: in place) + scales[a] x A[a]^T B[a]^T with a = ids[t] of each row
+    (outside [0, n): no adapter); x [T, K], A [n, r, K] and B [n, N, r] bf16, scales [n] fp32 or None."""
+    y_dtype = _float_dtype(y)
+    try:
+        fits = (x.nbytes >= 2 * T * K and A.nbytes >= 2 * n * r * K and B.nbytes >= 2 * n * N * r
+                and _float_dtype(x) == _float_dtype(A) == _float_dtype(B) == MOE_BF16
+                and ids.nbytes >= 4 * T and ids.itemsize == 4 and not ids.is_floating_point()
+                and y.nbytes >= (4 if y_dtype == MOE_F32 else 2) * T * N
+                and (scales is None or scales.nbytes >= 4 * n and _float_dtype(scales) == MOE_F32)
+                and (base is None or base.dtype == y.dtype and base.nbytes >= y.itemsize * T * N))
+    except AttributeError:
+        fits = False
+    if not fits:
+        raise ValueError("moe_lora takes bf16 x [T, K], A [n, r, K] and B [n, N, r], int32 ids [T], fp32 scales [n], "
+                         "y [T, N] and a base of y's type")
+    wp, wb = _ws(ws)
+    _check("moe_lora", load_library().moe_lora(
+        T, K, N, r, n, _ptr(x), _ptr(ids), _ptr(A), _ptr(B), _ptr(scales), _ptr(base), _ptr(y), y_dtype, wp, wb,
+        _stream(stream)))
 
 
 def moe_pack_weights_nk(W, G: int, K: int, N: int, W_nk, stream=None) -> None:

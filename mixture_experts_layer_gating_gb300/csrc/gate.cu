@@ -1,0 +1,70 @@
+// Routing by scores, bias and groups from router logits (moe_route_gated): one warp per
+// token (gate_warp.cuh).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "gate_warp.cuh"
+
+namespace moe {
+namespace {
+
+// v = the nsplit partial planes [nsplit, T, E] of the token's logits, added in order.
+template <int EPL>
+__device__ __forceinline__ void load_logits(const float* __restrict__ planes, int nsplit, size_t plane, int lane,
+                                            int E, bool vec, float (&v)[EPL]) {
+  const int e0 = lane * EPL;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) v[i] = 0.0f;
+  for (int s = 0; s < nsplit; ++s) {
+    const float* row = planes + s * plane;
+    float p[EPL];
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += 4) {
+        const float4 f = e0 + i < E ? *reinterpret_cast<const float4*>(row + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        p[i] = f.x;
+        p[i + 1] = f.y;
+        p[i + 2] = f.z;
+        p[i + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) p[i] = e0 + i < E ? row[e0 + i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = s ? v[i] + p[i] : p[i];
+  }
+}
+
+template <int EPL>
+__global__ void __launch_bounds__(256)
+    gate_kernel(const float* __restrict__ planes, int nsplit, const float* __restrict__ logit_bias,
+                const float* __restrict__ select_bias, float* logits, int T, bool vec, const GateParams g,
+                int32_t* __restrict__ ids, float* __restrict__ w, int32_t* err) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long t = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (t >= T) return;
+  float v[EPL];
+  load_logits<EPL>(planes + t * g.E, nsplit, static_cast<size_t>(T) * g.E, lane, g.E, vec, v);
+  warp_gate_topk<EPL>(v, lane, g, logit_bias, select_bias, (nsplit > 1 || logit_bias) ? logits + t * g.E : nullptr,
+                      ids + t * g.k, w + t * g.k, err);
+}
+
+}  // namespace
+
+cudaError_t launch_gate(const float* planes, int nsplit, const float* logit_bias, const float* select_bias,
+                        float* logits, int T, const GateParams& g, int32_t* ids, float* w, int32_t* err,
+                        cudaStream_t s) {
+  if (T <= 0) return cudaSuccess;
+  const int wpb = 8, blocks = (T + wpb - 1) / wpb;
+  const bool vec = g.E % 4 == 0 && !(reinterpret_cast<uintptr_t>(planes) & 15);
+  auto kern = g.E <= 128 ? gate_kernel<4> : g.E <= 256 ? gate_kernel<8> : gate_kernel<16>;
+  const cudaError_t e = launch_kernel(kern, dim3(blocks), dim3(wpb * 32), 0, s, planes, nsplit, logit_bias, select_bias,
+                                      logits, T, vec, g, ids, w, err);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace moe

@@ -2,6 +2,7 @@
 // layout and the order of kernel launches on the caller's stream.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -316,9 +317,11 @@ bool chunk_sort_on(const moe_config_t* c) {
 // the configuration does not split).
 // `chunk_hist`: where the fused router also writes its per-CTA expert
 // histograms (moe_layer with chunk_sort_on; null otherwise).
+// `gate`: the choice by scores, bias and groups; null: softmax top-k.
 int do_route(const moe_config_t* c, const void* x, const void* Wg, const float* bias,
              float* logits, int32_t* ids, float* w, float* partials, int32_t* err,
-             cudaStream_t s, int32_t* chunk_hist = nullptr) {
+             cudaStream_t s, int32_t* chunk_hist = nullptr, const GateParams* gate = nullptr,
+             const float* select_bias = nullptr) {
   cudaError_t e = cudaSuccess;
   const float* src = logits;
   int nsplit = 1;
@@ -334,7 +337,7 @@ int do_route(const moe_config_t* c, const void* x, const void* Wg, const float* 
       if (fused_router_on(c, nsplit)) {
         // projection and top-k in one launch
         return cuda_status(launch_router_topk(x, Wg, bias, c->T, c->D, c->E, c->k, c->renormalize,
-                                              logits, ids, w, err, s, chunk_hist));
+                                              logits, ids, w, err, s, chunk_hist, gate, select_bias));
       }
       if (router_small_ok(c->T, c->E, c->D, nsplit)) {
         // a few tokens: a matrix-vector product per token on the CUDA cores,
@@ -363,6 +366,8 @@ int do_route(const moe_config_t* c, const void* x, const void* Wg, const float* 
     bias = nullptr;
   }
   trace_mark(s);
+  if (gate)
+    return cuda_status(launch_gate(src, nsplit, bias, select_bias, logits, c->T, *gate, ids, w, err, s));
   return cuda_status(launch_topk_softmax(src, nsplit, bias, logits, c->T, c->E, c->k,
                                          c->renormalize, ids, w, err, s));
 }
@@ -578,9 +583,200 @@ int do_grouped_ffn(const moe_config_t* c, const void* x_perm, const float* xp_sc
   return st;
 }
 
+// The choice of experts that a moe_gate_t asks for, as the kernels take it; false: not a
+// choice of cfg's k experts.
+bool gate_params(const moe_config_t* c, const moe_gate_t* g, GateParams& p) {
+  if (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) return false;
+  if (g->group_score != MOE_GROUP_MAX && g->group_score != MOE_GROUP_TOP2_SUM) return false;
+  if (g->n_group < 1 || g->n_group > 32 || c->E % g->n_group) return false;
+  if (g->topk_group < 1 || g->topk_group > g->n_group || g->topk_group * (c->E / g->n_group) < c->k) return false;
+  if (!std::isfinite(g->scale)) return false;
+  p = GateParams{c->E, c->k, g->n_group, g->topk_group, g->score == MOE_SCORE_SIGMOID,
+                 g->group_score == MOE_GROUP_TOP2_SUM, c->renormalize != 0, g->scale};
+  return true;
+}
+
+int route(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const void* Wg, const float* logit_bias,
+          const float* select_bias, float* logits, int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes,
+          void* stream) {
+  const int st = common_checks(cfg, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  GateParams gp{};
+  if (gate && !gate_params(cfg, gate, gp)) return MOE_ERR_INVALID_ARG;
+  if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+  if (x && (!Wg || !aligned16(x) || !aligned16(Wg))) return MOE_ERR_INVALID_ARG;
+  if (!x && logit_bias) return MOE_ERR_INVALID_ARG;
+  if (cfg->act_dtype == MOE_BF16 && x && (cfg->E % 8)) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  const Layout L = make_layout(cfg);
+  float* partials = L.router_partials ? reinterpret_cast<float*>(ws_at(ws, L.router_partials)) : nullptr;
+  return do_route(cfg, x, Wg, logit_bias, logits, topk_ids, topk_w, partials, err_word(ws),
+                  static_cast<cudaStream_t>(stream), nullptr, gate ? &gp : nullptr, select_bias);
+}
+
 bool fp8_scales_ok(const moe_config_t* c, const float* s13, const float* s2) {
   const bool fp8 = is_fp8(c);
   return fp8 ? (s13 && s2) : (!s13 && !s2);
+}
+
+// The arguments of moe_layer, and of moe_block for the layer.
+int layer_checks(const moe_config_t* cfg, const void* x, const void* Wg, const void* W13, const float* s13,
+                 const void* W2, const float* s2, const void* W13s, const float* s13s, const void* W2s,
+                 const float* s2s, const void* out, void* ws, size_t ws_bytes) {
+  const int st = common_checks(cfg, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (w4_group(cfg->w_dtype)) return MOE_ERR_UNSUPPORTED;  // moe_layer_few
+  if (!x || !Wg || !W13 || !W2 || !out) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {x, Wg, W13, W2, out})
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (!fp8_scales_ok(cfg, s13, s2)) return MOE_ERR_INVALID_ARG;
+  const bool shared = cfg->I_shared > 0;
+  if (shared) {
+    if (!W13s || !W2s || !aligned16(W13s) || !aligned16(W2s)) return MOE_ERR_INVALID_ARG;
+    if (!fp8_scales_ok(cfg, s13s, s2s)) return MOE_ERR_INVALID_ARG;
+  }
+  if (cfg->act_dtype == MOE_BF16 && (cfg->E % 8)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// The layer, its arguments checked and T > 0.  gate, select_bias: as do_route has them;
+// rows_ready: x's rows in 8 bits and their scales (W8A8) are in the workspace already.
+int run_layer(const moe_config_t* cfg, const void* x, const void* Wg, const float* logit_bias,
+              const GateParams* gate, const float* select_bias, bool rows_ready, const void* W13,
+              const float* s13, const void* W2, const float* s2, const void* W13s, const float* s13s,
+              const void* W2s, const float* s2s, void* out, void* ws, cudaStream_t s) {
+  const bool shared = cfg->I_shared > 0;
+  int st = MOE_OK;
+  const Layout L = make_layout(cfg);
+  int32_t* err = err_word(ws);
+  float* logits = reinterpret_cast<float*>(ws_at(ws, L.off[MOE_WS_LOGITS]));
+  int32_t* ids = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_TOPK_IDS]));
+  float* w = reinterpret_cast<float*>(ws_at(ws, L.off[MOE_WS_TOPK_W]));
+  int32_t* counts = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_COUNTS]));
+  int32_t* offsets = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_OFFSETS]));
+  int32_t* sorted_rows = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_SORTED_ROWS]));
+  int32_t* dest = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_DEST]));
+  int32_t* seg = reinterpret_cast<int32_t*>(ws_at(ws, L.seg_scratch));
+  void* x_perm = ws_at(ws, L.off[MOE_WS_X_PERM]);
+  void* h = ws_at(ws, L.off[MOE_WS_H]);
+  void* y_perm = ws_at(ws, L.off[MOE_WS_Y_PERM]);
+  void* h_s = ws_at(ws, L.off[MOE_WS_H_SHARED]);
+  void* s_out = ws_at(ws, L.off[MOE_WS_S]);
+
+  const bool traced = !gate && !rows_ready && g_trace_events && g_trace_n >= moe_layer_launch_count(cfg) + 1;
+  g_trace_next = traced ? 0 : -1;
+  const bool fp8 = is_fp8(cfg);
+  // Fused combine (MOE_OPT_FUSED_COMBINE): the routed down pass adds each row
+  // times its routing weight into [T, D] fp32 sums (the y_perm region), zeroed
+  // here first, and the last kernel rounds sums + shared row; no y_perm rows.
+  const bool fused = fused_combine_on(cfg);
+  if (fused && cudaMemsetAsync(y_perm, 0, static_cast<size_t>(cfg->T) * cfg->D * 4, s) != cudaSuccess)
+    return (g_trace_next = -1, MOE_ERR_CUDA);
+  if (zero_tile_counters(ws, cfg, s) != cudaSuccess) return (g_trace_next = -1, MOE_ERR_CUDA);
+  const void* x_rows = x;  // what the gather and the shared expert read
+  float* tok_inv = nullptr;
+  float* row_inv = nullptr;
+  if (fp8) {
+    // fp8 weights: x once to fp16 rows (or two-term e4m3 rows) with exact
+    // power-of-two scales; the gather carries the inverse scale per row
+    void* x16 = ws_at(ws, L.x16);
+    tok_inv = reinterpret_cast<float*>(ws_at(ws, L.tok_inv));
+    row_inv = reinterpret_cast<float*>(ws_at(ws, L.row_inv));
+    if (!rows_ready) {
+      trace_mark(s);
+      if (rows_to_fp8_layer_form(cfg, x, cfg->T, cfg->D, x16, tok_inv, s) != cudaSuccess)
+        return (g_trace_next = -1, MOE_ERR_CUDA);
+    }
+    x_rows = x16;
+  }
+  // The shared expert as the last group of the routed GEMMs
+  // (MOE_OPT_SHARED_IN_GEMM), or on the side stream (not while tracing: the
+  // trace events time kernels one after another on the caller's stream).
+  const bool in_gemm = shared && shared_in_gemm_on(cfg);
+  cudaStream_t side = nullptr;
+  // MOE_OPT_SHARED_STREAM 1: the side stream forks here, once x is ready;
+  // 2: after init_routing, so that the shared expert's GEMMs (which hold most
+  // of every SM's shared memory) start once the routing kernels (which need
+  // some too) are done, and run beside the permutation kernel (which needs none)
+  const bool want_side = shared && g_shared_stream && !traced && !in_gemm;
+  auto fork_shared = [&]() -> int {
+    side = side_fork(s);
+    if (!side) return MOE_OK;  // no side stream: the shared expert runs on s below
+    int32_t* ctr = tile_counters(ws);
+    const int r = do_ffn(cfg, x_rows, tok_inv, cfg->T, nullptr, 1, W13s, s13s, W2s, s2s,
+                         cfg->I_shared, h_s, s_out, fp8 ? ws_at(ws, L.hs16) : nullptr,
+                         fp8 ? reinterpret_cast<float*>(ws_at(ws, L.hs_inv)) : nullptr, err, side,
+                         nullptr, 0, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr,
+                         ctr ? ctr + 2 : nullptr, g_shared_ctas);
+    if (r != MOE_OK) {
+      side_join(side, s);
+      side = nullptr;
+    }
+    return r;
+  };
+  if (want_side && g_shared_stream == 1) {
+    st = fork_shared();
+    if (st != MOE_OK) return (g_trace_next = -1, st);
+  }
+  // after the fork every early return first joins the side stream back
+  auto fail = [&](int code) {
+    if (side) side_join(side, s);
+    g_trace_next = -1;
+    return code;
+  };
+  float* partials = L.router_partials ? reinterpret_cast<float*>(ws_at(ws, L.router_partials)) : nullptr;
+  int32_t* chunk_hist =
+      chunk_sort_on(cfg) ? reinterpret_cast<int32_t*>(ws_at(ws, L.chunk_hist)) : nullptr;
+  st = do_route(cfg, x, Wg, logit_bias, logits, ids, w, partials, err, s, chunk_hist, gate, select_bias);
+  if (st != MOE_OK) return fail(st);
+  // The routed gate/up pass reads its rows from a permuted copy of x (the
+  // gather kernel streams at HBM speed), or gathers them from x itself
+  // (gather_mode): bf16 prefill layers by default with the GEMM's cp.async
+  // gather warps (x stays in L2; no permuted copy is written or read), on
+  // request with TMA tile::gather4 loads (slower on GB300: 32 four-row
+  // requests per 16 KB A tile).
+  const bool gather = gather_mode(cfg) != 0;
+  const bool late_fork = want_side && g_shared_stream == 2;
+  if (late_fork && !gather && !small_route(static_cast<long long>(cfg->T) * cfg->k, cfg->E)) {
+    // init_routing, the fork, then the permutation beside the shared GEMMs
+    st = do_permute(cfg, ids, nullptr, counts, offsets, sorted_rows, dest, nullptr, seg, err, s,
+                    layer_row_bytes(cfg), nullptr, nullptr, 0, chunk_hist);
+    if (st != MOE_OK) return fail(st);
+    st = fork_shared();
+    if (st != MOE_OK) return fail(st);
+    st = do_permute_rows(cfg, x_rows, sorted_rows, dest, offsets, x_perm, err, s, layer_row_bytes(cfg),
+                         tok_inv, row_inv, 0);
+  } else {
+    st = do_permute(cfg, ids, gather ? nullptr : x_rows, counts, offsets, sorted_rows, dest,
+                    gather ? nullptr : x_perm, seg, err, s, layer_row_bytes(cfg), tok_inv, row_inv,
+                    in_gemm ? cfg->T : 0, chunk_hist);
+    if (st == MOE_OK && late_fork) st = fork_shared();
+  }
+  if (st != MOE_OK) return fail(st);
+  st = do_grouped_ffn(cfg, gather ? x_rows : x_perm, gather ? tok_inv : row_inv, offsets, W13, s13,
+                      W2, s2, h, y_perm, (shared && !side) ? x_rows : nullptr, tok_inv, W13s, s13s,
+                      W2s, s2s, h_s, s_out, ws, err, s, gather ? sorted_rows : nullptr,
+                      fused ? sorted_rows : nullptr, fused ? w : nullptr, in_gemm);
+  if (st != MOE_OK) return fail(st);
+  if (side && !side_join(side, s)) return (g_trace_next = -1, MOE_ERR_CUDA);
+  trace_mark(s);
+  // the shared expert's output rows: s_out, or rows R .. R+T-1 of y_perm when it
+  // ran inside the routed GEMMs (the fused combine has added those already)
+  const void* s_rows =
+      !shared ? nullptr
+              : in_gemm ? static_cast<const void*>(static_cast<const uint8_t*>(y_perm) +
+                                                   static_cast<size_t>(cfg->T) * cfg->k * cfg->D *
+                                                       (fp8 ? 2 : 4))
+                        : s_out;
+  if (fused)
+    st = cuda_status(launch_combine_round(static_cast<const float*>(y_perm), in_gemm ? nullptr : s_rows,
+                                          fp8, cfg->T, cfg->D, out, s));
+  else
+    st = cuda_status(launch_finalize(cfg->act_dtype, y_perm, dest, w, s_rows, out, cfg->T, cfg->k,
+                                     cfg->D, cfg->T * cfg->k, err, s, fp8));
+  trace_mark(s);
+  g_trace_next = -1;
+  return st;
 }
 
 }  // namespace
@@ -603,17 +799,14 @@ size_t moe_workspace_offset(const moe_config_t* cfg, int which) {
 int moe_route(const moe_config_t* cfg, const void* x, const void* Wg, const float* logit_bias,
               float* logits, int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes,
               void* stream) {
-  int st = common_checks(cfg, ws, ws_bytes);
-  if (st != MOE_OK) return st;
-  if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
-  if (x && (!Wg || !aligned16(x) || !aligned16(Wg))) return MOE_ERR_INVALID_ARG;
-  if (!x && logit_bias) return MOE_ERR_INVALID_ARG;
-  if (cfg->act_dtype == MOE_BF16 && x && (cfg->E % 8)) return MOE_ERR_INVALID_ARG;
-  if (cfg->T == 0) return MOE_OK;
-  const Layout L = make_layout(cfg);
-  float* partials = L.router_partials ? reinterpret_cast<float*>(ws_at(ws, L.router_partials)) : nullptr;
-  return do_route(cfg, x, Wg, logit_bias, logits, topk_ids, topk_w, partials, err_word(ws),
-                  static_cast<cudaStream_t>(stream));
+  return route(cfg, nullptr, x, Wg, logit_bias, nullptr, logits, topk_ids, topk_w, ws, ws_bytes, stream);
+}
+
+int moe_route_gated(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const void* Wg,
+                    const float* logit_bias, const float* select_bias, float* logits,
+                    int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+  if (!gate) return MOE_ERR_INVALID_ARG;
+  return route(cfg, gate, x, Wg, logit_bias, select_bias, logits, topk_ids, topk_w, ws, ws_bytes, stream);
 }
 
 int moe_permute(const moe_config_t* cfg, const int32_t* topk_ids, const void* x, int32_t* counts,
@@ -693,149 +886,41 @@ int moe_layer(const moe_config_t* cfg, const void* x, const void* Wg, const floa
               const void* W13, const float* s13, const void* W2, const float* s2,
               const void* W13s, const float* s13s, const void* W2s, const float* s2s, void* out,
               void* ws, size_t ws_bytes, void* stream) {
-  int st = common_checks(cfg, ws, ws_bytes);
-  if (st != MOE_OK) return st;
-  if (w4_group(cfg->w_dtype)) return MOE_ERR_UNSUPPORTED;  // moe_layer_few
-  if (!x || !Wg || !W13 || !W2 || !out) return MOE_ERR_INVALID_ARG;
-  for (const void* p : {x, Wg, W13, W2, static_cast<const void*>(out)})
-    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
-  if (!fp8_scales_ok(cfg, s13, s2)) return MOE_ERR_INVALID_ARG;
-  const bool shared = cfg->I_shared > 0;
-  if (shared) {
-    if (!W13s || !W2s || !aligned16(W13s) || !aligned16(W2s)) return MOE_ERR_INVALID_ARG;
-    if (!fp8_scales_ok(cfg, s13s, s2s)) return MOE_ERR_INVALID_ARG;
-  }
-  if (cfg->act_dtype == MOE_BF16 && (cfg->E % 8)) return MOE_ERR_INVALID_ARG;
-  if (cfg->T == 0) return MOE_OK;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Layout L = make_layout(cfg);
-  int32_t* err = err_word(ws);
-  float* logits = reinterpret_cast<float*>(ws_at(ws, L.off[MOE_WS_LOGITS]));
-  int32_t* ids = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_TOPK_IDS]));
-  float* w = reinterpret_cast<float*>(ws_at(ws, L.off[MOE_WS_TOPK_W]));
-  int32_t* counts = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_COUNTS]));
-  int32_t* offsets = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_OFFSETS]));
-  int32_t* sorted_rows = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_SORTED_ROWS]));
-  int32_t* dest = reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_DEST]));
-  int32_t* seg = reinterpret_cast<int32_t*>(ws_at(ws, L.seg_scratch));
-  void* x_perm = ws_at(ws, L.off[MOE_WS_X_PERM]);
-  void* h = ws_at(ws, L.off[MOE_WS_H]);
-  void* y_perm = ws_at(ws, L.off[MOE_WS_Y_PERM]);
-  void* h_s = ws_at(ws, L.off[MOE_WS_H_SHARED]);
-  void* s_out = ws_at(ws, L.off[MOE_WS_S]);
+  const int st = layer_checks(cfg, x, Wg, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, ws_bytes);
+  if (st != MOE_OK || cfg->T == 0) return st;
+  return run_layer(cfg, x, Wg, logit_bias, nullptr, nullptr, false, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws,
+                   static_cast<cudaStream_t>(stream));
+}
 
-  const bool traced = g_trace_events && g_trace_n >= moe_layer_launch_count(cfg) + 1;
-  g_trace_next = traced ? 0 : -1;
-  const bool fp8 = is_fp8(cfg);
-  // Fused combine (MOE_OPT_FUSED_COMBINE): the routed down pass adds each row
-  // times its routing weight into [T, D] fp32 sums (the y_perm region), zeroed
-  // here first, and the last kernel rounds sums + shared row; no y_perm rows.
-  const bool fused = fused_combine_on(cfg);
-  if (fused && cudaMemsetAsync(y_perm, 0, static_cast<size_t>(cfg->T) * cfg->D * 4, s) != cudaSuccess)
-    return (g_trace_next = -1, MOE_ERR_CUDA);
-  if (zero_tile_counters(ws, cfg, s) != cudaSuccess) return (g_trace_next = -1, MOE_ERR_CUDA);
-  const void* x_rows = x;  // what the gather and the shared expert read
-  float* tok_inv = nullptr;
-  float* row_inv = nullptr;
-  if (fp8) {
-    // fp8 weights: x once to fp16 rows (or two-term e4m3 rows) with exact
-    // power-of-two scales; the gather carries the inverse scale per row
-    void* x16 = ws_at(ws, L.x16);
-    tok_inv = reinterpret_cast<float*>(ws_at(ws, L.tok_inv));
-    row_inv = reinterpret_cast<float*>(ws_at(ws, L.row_inv));
-    trace_mark(s);
-    if (rows_to_fp8_layer_form(cfg, x, cfg->T, cfg->D, x16, tok_inv, s) != cudaSuccess)
-      return (g_trace_next = -1, MOE_ERR_CUDA);
-    x_rows = x16;
+int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const void* residual,
+              const void* norm_weight, float eps, const void* Wg, const float* logit_bias,
+              const float* select_bias, const void* W13, const float* s13, const void* W2,
+              const float* s2, const void* W13s, const float* s13s, const void* W2s, const float* s2s,
+              void* sum_out, void* y, void* out, void* ws, size_t ws_bytes, void* stream) {
+  int st = layer_checks(cfg, x, Wg, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  GateParams gp{};
+  if (gate ? !gate_params(cfg, gate, gp) : select_bias != nullptr) return MOE_ERR_INVALID_ARG;
+  const GateParams* g = gate ? &gp : nullptr;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!norm_weight) {
+    if (residual || sum_out || y || eps != 0.0f) return MOE_ERR_INVALID_ARG;
+    if (cfg->T == 0) return MOE_OK;
+    return run_layer(cfg, x, Wg, logit_bias, g, select_bias, false, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, s);
   }
-  // The shared expert as the last group of the routed GEMMs
-  // (MOE_OPT_SHARED_IN_GEMM), or on the side stream (not while tracing: the
-  // trace events time kernels one after another on the caller's stream).
-  const bool in_gemm = shared && shared_in_gemm_on(cfg);
-  cudaStream_t side = nullptr;
-  // MOE_OPT_SHARED_STREAM 1: the side stream forks here, once x is ready;
-  // 2: after init_routing, so that the shared expert's GEMMs (which hold most
-  // of every SM's shared memory) start once the routing kernels (which need
-  // some too) are done, and run beside the permutation kernel (which needs none)
-  const bool want_side = shared && g_shared_stream && !traced && !in_gemm;
-  auto fork_shared = [&]() -> int {
-    side = side_fork(s);
-    if (!side) return MOE_OK;  // no side stream: the shared expert runs on s below
-    int32_t* ctr = tile_counters(ws);
-    const int r = do_ffn(cfg, x_rows, tok_inv, cfg->T, nullptr, 1, W13s, s13s, W2s, s2s,
-                         cfg->I_shared, h_s, s_out, fp8 ? ws_at(ws, L.hs16) : nullptr,
-                         fp8 ? reinterpret_cast<float*>(ws_at(ws, L.hs_inv)) : nullptr, err, side,
-                         nullptr, 0, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr,
-                         ctr ? ctr + 2 : nullptr, g_shared_ctas);
-    if (r != MOE_OK) {
-      side_join(side, s);
-      side = nullptr;
-    }
-    return r;
-  };
-  if (want_side && g_shared_stream == 1) {
-    st = fork_shared();
-    if (st != MOE_OK) return (g_trace_next = -1, st);
-  }
-  // after the fork every early return first joins the side stream back
-  auto fail = [&](int code) {
-    if (side) side_join(side, s);
-    g_trace_next = -1;
-    return code;
-  };
-  float* partials = L.router_partials ? reinterpret_cast<float*>(ws_at(ws, L.router_partials)) : nullptr;
-  int32_t* chunk_hist =
-      chunk_sort_on(cfg) ? reinterpret_cast<int32_t*>(ws_at(ws, L.chunk_hist)) : nullptr;
-  st = do_route(cfg, x, Wg, logit_bias, logits, ids, w, partials, err, s, chunk_hist);
-  if (st != MOE_OK) return fail(st);
-  // The routed gate/up pass reads its rows from a permuted copy of x (the
-  // gather kernel streams at HBM speed), or gathers them from x itself
-  // (gather_mode): bf16 prefill layers by default with the GEMM's cp.async
-  // gather warps (x stays in L2; no permuted copy is written or read), on
-  // request with TMA tile::gather4 loads (slower on GB300: 32 four-row
-  // requests per 16 KB A tile).
-  const bool gather = gather_mode(cfg) != 0;
-  const bool late_fork = want_side && g_shared_stream == 2;
-  if (late_fork && !gather && !small_route(static_cast<long long>(cfg->T) * cfg->k, cfg->E)) {
-    // init_routing, the fork, then the permutation beside the shared GEMMs
-    st = do_permute(cfg, ids, nullptr, counts, offsets, sorted_rows, dest, nullptr, seg, err, s,
-                    layer_row_bytes(cfg), nullptr, nullptr, 0, chunk_hist);
-    if (st != MOE_OK) return fail(st);
-    st = fork_shared();
-    if (st != MOE_OK) return fail(st);
-    st = do_permute_rows(cfg, x_rows, sorted_rows, dest, offsets, x_perm, err, s, layer_row_bytes(cfg),
-                         tok_inv, row_inv, 0);
-  } else {
-    st = do_permute(cfg, ids, gather ? nullptr : x_rows, counts, offsets, sorted_rows, dest,
-                    gather ? nullptr : x_perm, seg, err, s, layer_row_bytes(cfg), tok_inv, row_inv,
-                    in_gemm ? cfg->T : 0, chunk_hist);
-    if (st == MOE_OK && late_fork) st = fork_shared();
-  }
-  if (st != MOE_OK) return fail(st);
-  st = do_grouped_ffn(cfg, gather ? x_rows : x_perm, gather ? tok_inv : row_inv, offsets, W13, s13,
-                      W2, s2, h, y_perm, (shared && !side) ? x_rows : nullptr, tok_inv, W13s, s13s,
-                      W2s, s2s, h_s, s_out, ws, err, s, gather ? sorted_rows : nullptr,
-                      fused ? sorted_rows : nullptr, fused ? w : nullptr, in_gemm);
-  if (st != MOE_OK) return fail(st);
-  if (side && !side_join(side, s)) return (g_trace_next = -1, MOE_ERR_CUDA);
-  trace_mark(s);
-  // the shared expert's output rows: s_out, or rows R .. R+T-1 of y_perm when it
-  // ran inside the routed GEMMs (the fused combine has added those already)
-  const void* s_rows =
-      !shared ? nullptr
-              : in_gemm ? static_cast<const void*>(static_cast<const uint8_t*>(y_perm) +
-                                                   static_cast<size_t>(cfg->T) * cfg->k * cfg->D *
-                                                       (fp8 ? 2 : 4))
-                        : s_out;
-  if (fused)
-    st = cuda_status(launch_combine_round(static_cast<const float*>(y_perm), in_gemm ? nullptr : s_rows,
-                                          fp8, cfg->T, cfg->D, out, s));
-  else
-    st = cuda_status(launch_finalize(cfg->act_dtype, y_perm, dest, w, s_rows, out, cfg->T, cfg->k,
-                                     cfg->D, cfg->T * cfg->k, err, s, fp8));
-  trace_mark(s);
-  g_trace_next = -1;
-  return st;
+  if (!y || !(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {residual, norm_weight, static_cast<const void*>(sum_out), static_cast<const void*>(y)})
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (cfg->D > kNormMaxD) return MOE_ERR_UNSUPPORTED;
+  if (cfg->T == 0) return MOE_OK;
+  const Layout L = make_layout(cfg);
+  // W8A8 layers: the norm writes the 8-bit rows and their scales where the layer takes them
+  const bool a8 = is_a8(cfg);
+  if (launch_add_rms_norm(cfg->T, cfg->D, cfg->act_dtype == MOE_F32, x, residual, norm_weight, eps, sum_out, y,
+                          a8 ? ws_at(ws, L.x16) : nullptr, 0,
+                          a8 ? reinterpret_cast<float*>(ws_at(ws, L.tok_inv)) : nullptr, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return run_layer(cfg, y, Wg, logit_bias, g, select_bias, a8, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, s);
 }
 
 int moe_pack_weights_nk(const void* W, int64_t G, int32_t K, int32_t N, void* W_nk, void* stream) {

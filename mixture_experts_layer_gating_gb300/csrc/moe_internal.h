@@ -100,6 +100,19 @@ cudaError_t launch_dequantize_w4(const void* q, const void* sc, const uint8_t* z
 inline size_t act_bytes(int dt) { return dt == MOE_F32 ? 4 : 2; }
 inline size_t w_bytes(int dt) { return dt == MOE_F32 ? 4 : (dt == MOE_BF16 ? 2 : 1); }
 
+// --------------------------------------------------------------------- norm.cu
+constexpr int kNormMaxD = 32768;
+cudaError_t launch_add_rms_norm(int rows, int D, bool f32, const void* x, const void* residual, const void* weight,
+                                float eps, void* sum_out, void* y, void* q, int group, float* scales,
+                                cudaStream_t s);
+
+// --------------------------------------------------------------------- lora.cu
+constexpr int kLoraMaxRank = 256, kLoraMaxAdapters = 16384, kLoraMaxWidth = 1 << 24;
+size_t lora_workspace_bytes(int T, int K, int N, int r, int n);
+cudaError_t launch_lora(int T, int K, int N, int r, int n, const void* x, const int32_t* ids, const void* A,
+                        const void* B, const float* scales, const void* base, void* y, bool y_f32, uint8_t* ws,
+                        cudaStream_t s);
+
 // ---------------------------------------------------------------- routing.cu
 // Expanded rows per init_routing segment: 512, raised for large R so that
 // there are at most 128 segments (each scatter block reads all segments'
@@ -130,6 +143,19 @@ cudaError_t launch_topk_softmax(const float* partials, int nsplit, const float* 
                                 int T, int E, int k, int renorm, int32_t* ids, float* w,
                                 int32_t* err, cudaStream_t s);
 
+// --------------------------------------------------------------------- gate.cu
+// moe_gate_t with the sizes it is applied to, as the kernels take it.
+struct GateParams {
+  int E, k, n_group, topk_group;
+  bool sigmoid, top2, renorm;
+  float scale;
+};
+// The choice by scores, bias and groups; planes, logit_bias and logits as
+// launch_topk_softmax has them.
+cudaError_t launch_gate(const float* planes, int nsplit, const float* logit_bias, const float* select_bias,
+                        float* logits, int T, const GateParams& g, int32_t* ids, float* w, int32_t* err,
+                        cudaStream_t s);
+
 // Router projection fused with the top-k softmax (router_sm103.cu), bf16 x
 // and W_g: logits (+ bias) written, then ids / w.  router_topk_ok says which
 // shapes it takes (64 <= E <= 512, E and D multiples of 8, k <= 32);
@@ -142,11 +168,13 @@ void router_topk_split(int T, int E, int D, int& ck, int& nh);
 // Its CTAs, in launch order, and the expanded rows of each one's tokens
 // (128 / (ck nh) tokens times k): CTA b's rows are [b chunk_rows, (b + 1)
 // chunk_rows).  With chunk_hist (16-byte aligned, nchunks x E int32) the
-// kernel also writes each CTA's expert histogram of those rows there.
+// kernel also writes each CTA's expert histogram of those rows there.  With
+// gate the experts are chosen as launch_gate does (bias is then logit_bias).
 void router_topk_chunks(int T, int E, int D, int k, int& nchunks, int& chunk_rows);
 cudaError_t launch_router_topk(const void* x, const void* Wg, const float* bias, int T, int D,
                                int E, int k, int renorm, float* logits, int32_t* ids, float* w,
-                               int32_t* err, cudaStream_t s, int32_t* chunk_hist = nullptr);
+                               int32_t* err, cudaStream_t s, int32_t* chunk_hist = nullptr,
+                               const GateParams* gate = nullptr, const float* select_bias = nullptr);
 // init_routing from those histograms: a CTA per few chunks, no cluster (E <= 512,
 // E % 4 == 0, chunk_rows <= 8192).  Same results as the other init_routing
 // kernels when the histograms count the ids.

@@ -33,7 +33,9 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "gate_warp.cuh"
 #include "moe_internal.h"
 #include "sm103_ptx.cuh"
 #include "topk_warp.cuh"
@@ -91,12 +93,17 @@ struct RtParams {
   // tokens (the tokens [b * 128 / C, (b + 1) * 128 / C), C CTAs per cluster)
   int32_t* chunk_hist;
 };
+struct RtGatedParams : RtParams {
+  GateParams gate;
+  const float* select_bias;
+};
 
-// NB: experts per CTA (the MMA N); EPL: logits per lane in the top-k warp.
-template <int NB, int EPL>
+// NB: experts per CTA (the MMA N); EPL: logits per lane in the top-k warp;
+// GATED: the choice of experts is warp_gate_topk's.
+template <int NB, int EPL, bool GATED>
 __global__ void __launch_bounds__(RT_THREADS, 1)
-    router_topk_kernel(const __grid_constant__ CUtensorMap tmap_x,
-                       const __grid_constant__ CUtensorMap tmap_wg, const RtParams p) {
+    router_topk_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_wg,
+                       const std::conditional_t<GATED, RtGatedParams, RtParams> p) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int STAGES = RtCfg<NB>::kStages;
@@ -275,7 +282,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     float v[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      const int e = lane + 32 * j;
+      const int e = GATED ? lane * EPL + j : lane + 32 * j;
       float s = 0.0f;
       if (e < p.E) {
         s = red[static_cast<size_t>(i) * ld + e];
@@ -283,10 +290,14 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       }
       v[j] = s;
     }
-    const int id = warp_topk_softmax<EPL>(v, lane, p.E, p.k, p.renorm, p.bias,
-                                          p.logits + static_cast<size_t>(t) * p.E,
-                                          p.ids + static_cast<size_t>(t) * p.k,
-                                          p.w + static_cast<size_t>(t) * p.k, p.err);
+    float* logits_row = p.logits + static_cast<size_t>(t) * p.E;
+    int32_t* ids_row = p.ids + static_cast<size_t>(t) * p.k;
+    float* w_row = p.w + static_cast<size_t>(t) * p.k;
+    int id;
+    if constexpr (GATED)
+      id = warp_gate_topk<EPL>(v, lane, p.gate, p.bias, p.select_bias, logits_row, ids_row, w_row, p.err);
+    else
+      id = warp_topk_softmax<EPL>(v, lane, p.E, p.k, p.renorm, p.bias, logits_row, ids_row, w_row, p.err);
     if (id >= 0) atomicAdd(&hist[id], 1);
   }
   if (p.chunk_hist) {
@@ -296,10 +307,10 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   }
 }
 
-template <int NB, int EPL>
-cudaError_t launch_rt(const CUtensorMap& tx, const CUtensorMap& tw, const RtParams& p, int tiles,
+template <int NB, int EPL, typename Params>
+cudaError_t launch_rt(const CUtensorMap& tx, const CUtensorMap& tw, const Params& p, int tiles,
                       cudaStream_t s) {
-  auto kern = router_topk_kernel<NB, EPL>;
+  auto kern = router_topk_kernel<NB, EPL, std::is_same_v<Params, RtGatedParams>>;
   constexpr size_t smem = rt_smem_bytes();
   static bool done[64] = {false};
   int dev = 0;
@@ -328,6 +339,16 @@ cudaError_t launch_rt(const CUtensorMap& tx, const CUtensorMap& tw, const RtPara
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tx, tw, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <typename Params>
+cudaError_t launch_rt_sizes(const CUtensorMap& tx, const CUtensorMap& tw, const Params& p, int tiles,
+                            cudaStream_t s) {
+  const int per_cta = p.E / p.nh;  // experts of one CTA
+  if (p.nh == 2) return launch_rt<256, 16>(tx, tw, p, tiles, s);
+  if (per_cta <= 64) return launch_rt<64, 2>(tx, tw, p, tiles, s);
+  if (per_cta <= 128) return launch_rt<128, 4>(tx, tw, p, tiles, s);
+  return launch_rt<256, 8>(tx, tw, p, tiles, s);
 }
 
 }  // namespace
@@ -368,11 +389,12 @@ void router_topk_chunks(int T, int E, int D, int k, int& nchunks, int& chunk_row
 
 cudaError_t launch_router_topk(const void* x, const void* Wg, const float* bias, int T, int D,
                                int E, int k, int renorm, float* logits, int32_t* ids, float* w,
-                               int32_t* err, cudaStream_t s, int32_t* chunk_hist) {
+                               int32_t* err, cudaStream_t s, int32_t* chunk_hist,
+                               const GateParams* gate, const float* select_bias) {
   if (!router_topk_ok(T, E, D, k) || !x || !Wg || !logits || !ids || !w ||
       (reinterpret_cast<uintptr_t>(chunk_hist) & 15))
     return cudaErrorInvalidValue;
-  RtParams p;
+  RtGatedParams p;
   p.T = T;
   p.D = D;
   p.E = E;
@@ -403,11 +425,10 @@ cudaError_t launch_router_topk(const void* x, const void* Wg, const float* bias,
       return cudaErrorInvalidValue;
   }
   const int tiles = (T + RT_BM - 1) / RT_BM;
-  const int per_cta = E / p.nh;  // experts of one CTA
-  if (p.nh == 2) return launch_rt<256, 16>(tx, tw, p, tiles, s);
-  if (per_cta <= 64) return launch_rt<64, 2>(tx, tw, p, tiles, s);
-  if (per_cta <= 128) return launch_rt<128, 4>(tx, tw, p, tiles, s);
-  return launch_rt<256, 8>(tx, tw, p, tiles, s);
+  if (!gate) return launch_rt_sizes<RtParams>(tx, tw, p, tiles, s);
+  p.gate = *gate;
+  p.select_bias = select_bias;
+  return launch_rt_sizes(tx, tw, p, tiles, s);
 }
 
 }  // namespace moe

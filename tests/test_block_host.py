@@ -1,0 +1,170 @@
+"""Host-side checks of moe_add_rms_norm, moe_route_gated, moe_lora and moe_block:
+everything refused here is refused before any CUDA call."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import mixture_experts_layer_gating_gb300 as moe
+from tests import _block_ref as ref
+from tests._lib import ensure_library
+
+P = 1 << 20  # a fake, aligned device address: validation fails before any use
+INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -5
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ensure_library()
+
+
+# ------------------------------------------------------------------- norm
+def _norm(lib, rows=4, D=256, dt=moe.MOE_BF16, x=P, res=P, w=P, eps=1e-6, sum_out=P, y=P, q=P, group=0, s=P):
+    return lib.moe_add_rms_norm(rows, D, dt, x, res, w, eps, sum_out, y, q, group, s, None)
+
+
+def test_norm_refusals(lib):
+    assert _norm(lib, rows=0) == 0
+    assert _norm(lib, rows=0, x=None, res=None, w=None, sum_out=None, y=None, q=None, s=None) == 0
+    for bad in ({"rows": -1}, {"D": 0}, {"D": 252}, {"eps": -1e-6}, {"eps": math.inf}, {"eps": math.nan}, {"group": 16},
+                {"group": 256}, {"D": 264, "group": 32}, {"x": None}, {"w": None}, {"y": None, "q": None, "s": None},
+                {"s": None}, {"q": None}, {"x": P + 8}, {"res": P + 2}, {"w": P + 4}, {"sum_out": P + 8}, {"y": P + 8},
+                {"q": P + 4}, {"s": P + 4}):
+        assert _norm(lib, **bad) == INVALID, bad
+    for bad in ({"dt": moe.MOE_FP8_E4M3}, {"dt": -1}, {"D": 32776}):
+        assert _norm(lib, **bad) == UNSUPPORTED, bad
+
+
+def test_norm_wrapper_compares_its_tensors():
+    T, D = 3, 256
+    x = torch.zeros(T, D, dtype=torch.bfloat16)
+    good = dict(x=x, residual=x, weight=x[0], sum_out=x, y=x, q=torch.zeros(T, D, dtype=torch.uint8),
+                q_scales=torch.zeros(T, D // 64))
+
+    def call(**other):
+        a = dict(good, **other)
+        moe.moe_add_rms_norm(T, D, a["x"], a["residual"], a["weight"], 1e-6, a["sum_out"], a["y"], a["q"], a["q_scales"], 64)
+
+    ensure_library()
+    for a in ({}, {"residual": None}, {"sum_out": None}, {"y": None}, {"q": torch.zeros(T, D).to(torch.float8_e4m3fn)}):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(**a)
+    for name, t in good.items():
+        with pytest.raises(ValueError, match="moe_add_rms_norm takes"):
+            call(**{name: t[:-1].contiguous()})
+        with pytest.raises(ValueError, match="moe_add_rms_norm takes"):
+            call(**{name: t.double()})
+
+
+# ------------------------------------------------------------------- gate
+def _cfg(T=4, E=64, k=4, **kw):
+    return moe.make_config(T, 256, E, k, 128, **kw)
+
+
+def _route(lib, cfg, gate, x=P, Wg=P, lb=None, sb=P, logits=P, ids=P, w=P, ws=P, n=None):
+    return lib.moe_route_gated(ctypes.byref(cfg), None if gate is None else ctypes.byref(gate), x, Wg, lb, sb, logits, ids,
+                               w, ws, moe.moe_workspace_size(cfg) if n is None else n, None)
+
+
+BAD_GATES = [dict(n_group=0), dict(n_group=3), dict(n_group=64), dict(n_group=4, topk_group=0), dict(n_group=4, topk_group=5),
+             dict(n_group=32, topk_group=1), dict(scale=math.inf), dict(scale=math.nan)]
+
+
+def test_gate_refusals(lib):
+    assert _route(lib, _cfg(T=0), moe.make_gate()) == 0
+    assert _route(lib, _cfg(), None) == INVALID
+    for bad in BAD_GATES:
+        assert _route(lib, _cfg(), moe.make_gate(**bad)) == INVALID, bad
+    for field in ("score", "group_score"):
+        for v in (-1, 2):
+            g = moe.make_gate()
+            setattr(g, field, v)
+            assert _route(lib, _cfg(), g) == INVALID
+    g = moe.make_gate(n_group=8, topk_group=2)
+    for bad in ({"Wg": None}, {"x": P + 8}, {"Wg": P + 8}, {"x": None, "lb": P}, {"logits": None}, {"ids": None}, {"w": None}):
+        assert _route(lib, _cfg(), g, **bad) == INVALID, bad
+    assert _route(lib, _cfg(E=60), moe.make_gate(n_group=4, topk_group=1)) == INVALID  # rows of W_g
+    assert _route(lib, _cfg(), g, ws=None) == WORKSPACE
+    assert _route(lib, _cfg(), g, n=1000) == WORKSPACE
+    with pytest.raises(KeyError):
+        moe.make_gate("tanh")
+
+
+# ------------------------------------------------------------------- lora
+def _lora(lib, T=4, K=256, N=64, r=16, n=3, x=P, ids=P, A=P, B=P, s=P, base=P, y=P, dt=moe.MOE_BF16, ws=P, size=1 << 40):
+    return lib.moe_lora(T, K, N, r, n, x, ids, A, B, s, base, y, dt, ws, size, None)
+
+
+def test_lora_refusals(lib):
+    assert _lora(lib, T=0) == 0
+    assert _lora(lib, T=0, x=None, ids=None, y=None, base=None) == 0
+    for bad in ({"T": -1}, {"K": 0}, {"K": 252}, {"N": 12}, {"N": -8}, {"r": 0}, {"r": 12}, {"n": 0}, {"K": (1 << 24) + 8},
+                {"N": (1 << 24) + 8}, {"x": None}, {"ids": None}, {"A": None}, {"B": None}, {"y": None}, {"x": P + 8},
+                {"A": P + 2}, {"B": P + 8}, {"y": P + 8}, {"base": P + 8}, {"ids": P + 2}, {"s": P + 1}):
+        assert _lora(lib, **bad) == INVALID, bad
+    for bad in ({"r": 264}, {"n": 16385}, {"dt": moe.MOE_FP8_E4M3}, {"dt": -1}):
+        assert _lora(lib, **bad) == UNSUPPORTED, bad
+    need = moe.moe_lora_workspace_size(4, 256, 64, 16, 3)
+    assert need > 0
+    for bad in ({"ws": None}, {"ws": P + 16}, {"size": need - 1}):
+        assert _lora(lib, **bad) == WORKSPACE, bad
+    for bad in ((-1, 256, 64, 16, 3), (4, 250, 64, 16, 3), (4, 256, 64, 264, 3), (4, 256, 64, 16, 0)):
+        assert moe.moe_lora_workspace_size(*bad) == 0
+
+
+def test_lora_wrapper_compares_its_tensors(lib):
+    T, K, N, r, n = 3, 64, 24, 8, 2
+    good = dict(x=torch.zeros(T, K).bfloat16(), ids=torch.zeros(T, dtype=torch.int32), A=torch.zeros(n, r, K).bfloat16(),
+                B=torch.zeros(n, N, r).bfloat16(), scales=torch.zeros(n), base=torch.zeros(T, N), y=torch.zeros(T, N))
+    ws = torch.zeros(moe.moe_lora_workspace_size(T, K, N, r, n), dtype=torch.uint8)
+
+    def call(**other):
+        a = dict(good, **other)
+        moe.moe_lora(T, K, N, r, n, a["x"], a["ids"], a["A"], a["B"], a["scales"], a["base"], a["y"], ws)
+
+    for a in ({}, {"scales": None}, {"base": None}, {"y": good["y"].bfloat16(), "base": good["y"].bfloat16()}):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(**a)
+    for name, t in good.items():
+        with pytest.raises(ValueError, match="moe_lora takes"):
+            call(**{name: t[:-1].contiguous()})
+        with pytest.raises((ValueError, moe.MoEError)):
+            call(**{name: t.double()})
+    with pytest.raises(ValueError, match="moe_lora takes"):
+        call(y=good["y"].bfloat16())  # a base of another type
+
+
+# ------------------------------------------------------------------ block
+def _block(lib, cfg, gate=None, x=P, res=None, nw=P, eps=1e-6, sb=None, W13=P, s13=None, sum_out=None, y=P, out=P, ws=P, n=None):
+    return lib.moe_block(ctypes.byref(cfg), None if gate is None else ctypes.byref(gate), x, res, nw, eps, P, None, sb, W13, s13,
+                         P, s13, None, None, None, None, sum_out, y, out, ws, moe.moe_workspace_size(cfg) if n is None else n, None)
+
+
+def test_block_refusals(lib):
+    assert _block(lib, _cfg(T=0)) == 0
+    assert _block(lib, _cfg(T=0), nw=None, y=None, eps=0.0) == 0
+    for bad in ({"x": None}, {"x": P + 8}, {"W13": None}, {"out": None}, {"s13": P}, {"y": None}, {"y": P + 8}, {"nw": P + 8},
+                {"res": P + 8}, {"sum_out": P + 8}, {"eps": -1.0}, {"eps": math.nan}, {"sb": P},
+                {"nw": None}, {"nw": None, "y": None}, {"nw": None, "y": None, "eps": 0.0, "res": P},
+                {"nw": None, "y": None, "eps": 0.0, "sum_out": P}):
+        assert _block(lib, _cfg(), **bad) == INVALID, bad
+    for bad in BAD_GATES:
+        assert _block(lib, _cfg(), moe.make_gate(**bad)) == INVALID, bad
+    assert _block(lib, _cfg(w_dtype="w4_g64"), s13=P) == UNSUPPORTED
+    assert _block(lib, moe.make_config(4, 32776, 64, 4, 128)) == UNSUPPORTED
+    assert _block(lib, _cfg(), n=1000) == WORKSPACE
+
+
+# -------------------------------------------------------------- reference
+def test_gate_reference_on_hand_written_rows():
+    l = torch.tensor([[0.0, 2.0, 2.0, -1.0, 3.0, float("nan"), 1.0, 1.0]])
+    ids, w, _ = ref.gate(l, None, 3, renorm=False)
+    assert ids.tolist() == [[4, 1, 2]] and abs(w[0, 0] - 1 / (1 + math.exp(-3))) < 1e-15
+    # groups of two: sums of sigmoids (.5 + .88), (.88 + .27), (.95), (.73 + .73)
+    ids, _, _ = ref.gate(l, None, 2, n_group=4, topk_group=2)
+    assert ids.tolist() == [[1, 6]]
+    ids, _, _ = ref.gate(l, None, 2, n_group=4, topk_group=2, group_score="max")
+    assert ids.tolist() == [[4, 1]]
+    ids, w, _ = ref.gate(l, torch.tensor([9.0, 0, 0, 0, 0, 9.0, 0, 0]), 2, score="softmax", scale=2.0)
+    assert ids.tolist() == [[0, 4]] and abs(w[0].sum() - 2.0) < 1e-12 and abs(w[0, 1] / w[0, 0] - math.exp(3)) < 1e-9
