@@ -18,6 +18,8 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxTprLog2 = 9, kMaxWarps = 1 << (kMaxTprLog2 - 5);  // threads to a row, 2^5 .. 2^9
+constexpr int kSms = 152;
 
 struct NormParams {
   const void *x, *residual, *weight;
@@ -25,7 +27,7 @@ struct NormParams {
   uint8_t* q;
   float* scales;
   int rows, D, group;  // group: values to a scale, 0 = the row
-  int tpr_log2;        // threads to a row, 2^5 .. 2^10
+  int tpr_log2;        // threads to a row
   float eps;
 };
 
@@ -75,99 +77,124 @@ struct Vec8<float> {
   }
 };
 
-// Sum (or largest) over the threads of a row, the same bits on each; NaN stays NaN.
-template <bool MAX>
-__device__ __forceinline__ float combine(float a, float b) {
-  if (!MAX) return a + b;
-  return a > b || a != a ? a : b;  // (b NaN: the comparison is false)
-}
-template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* red, int warps) {
+// Sum over the threads of a row, or the largest of unsigned numbers, the same on each.
+// Magnitudes are compared as the unsigned bits of |f|, which order as they do and put NaN
+// above infinity.
+__device__ __forceinline__ float join(float a, float b) { return a + b; }
+__device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) { return max(a, b); }
+template <typename V>
+__device__ __forceinline__ V row_reduce(V v, V* red, int warps) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = combine<MAX>(v, __shfl_xor_sync(kFull, v, o));
+  for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(kFull, v, o));
   if (warps == 1) return v;
-  const int warp = threadIdx.x >> 5, first = warp & ~(warps - 1);
-  __syncthreads();  // the last reading of red
-  if ((threadIdx.x & 31) == 0) red[warp] = v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = red[first];
-  for (int w = 1; w < warps; ++w) v = combine<MAX>(v, red[first + w]);
-  return v;
+  v = lane < warps ? red[lane] : V(0);
+#pragma unroll
+  for (int o = kMaxWarps / 2; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(kFull, v, o));
+  return __shfl_sync(kFull, v, 0);
 }
+__device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
-__device__ __forceinline__ float e4m3_scale(float largest) {
-  if (largest == 0.0f) return 1.0f;
+__device__ __forceinline__ float e4m3_scale(uint32_t largest) {
+  if (largest == 0u) return 1.0f;
   // (an infinity or NaN gives NaN, so that the group's products are NaN)
-  return isfinite(largest) ? fmaxf(__fdiv_rn(largest, 448.0f), FLT_MIN) : __int_as_float(0x7fffffff);
+  return largest < 0x7f800000u ? fmaxf(__fdiv_rn(__uint_as_float(largest), 448.0f), FLT_MIN)
+                               : __uint_as_float(0x7fffffffu);
+}
+__device__ __forceinline__ uint2 e4m3_codes(const float (&f)[8], float scale) {
+  const float inv = 1.0f / scale;
+  uint32_t u[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    u[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv),
+                                                                __NV_SATFINITE, __NV_E4M3))
+                 << (16 * (i & 1));
+  return make_uint2(u[0], u[1]);
 }
 
-// VPT vectors of 8 values a thread.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) {
+enum QMode { kNoQ, kRowQ, kGroupQ };
+
+// VPT vectors of 8 values a thread.  Each block takes rows in turn (a row of one warp: a
+// block takes eight).  Where registers allow, it has the next row's loads under way while it
+// reduces and stores this one's, and keeps its part of the weight.
+template <typename T, int VPT, bool ADD, QMode Q>
+__global__ void __launch_bounds__(32 * kMaxWarps) add_rms_norm_kernel(const NormParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float red[32];
+  // two of each, taken in turn: one barrier a reduction (the next use of the same is
+  // behind the other's barrier)
+  __shared__ float red[2][kMaxWarps];
+  __shared__ uint32_t redm[2][kMaxWarps];
   const int tpr = 1 << p.tpr_log2, rpb = blockDim.x >> p.tpr_log2;
   const int li = threadIdx.x & (tpr - 1), warps = tpr >> 5;
   const int nvec = p.D / 8;
-  // (rows of several warps have a block of their own, whose threads all run the same
-  // iterations and branches on the row: row_reduce's barriers)
-  for (long long r0 = static_cast<long long>(blockIdx.x) * rpb; r0 < p.rows;
-       r0 += static_cast<long long>(gridDim.x) * rpb) {
-    const long long r = r0 + (threadIdx.x >> p.tpr_log2);
-    const bool valid = r < p.rows;
-    const long long base = r * nvec;
-    float f[VPT][8];
-    {
-      Vec8<T> a[VPT], b[VPT];
+  const float rD = 1.0f / static_cast<float>(p.D);
+  constexpr bool kAhead = VPT <= 4, kKeep = VPT * sizeof(T) <= 8;
+  Vec8<T> a[VPT], b[VPT], w[VPT];
+  auto load = [&](long long r) {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int v = li + tpr * j;
-        if (valid && v < nvec) {
-          a[j].load(p.x, base + v);
-          if (p.residual) b[j].load(p.residual, base + v);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        if (valid && li + tpr * j < nvec) {
-          a[j].get(f[j]);
-          if (p.residual) {
-            float g[8];
-            b[j].get(g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[j][i] += g[i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[j][i] = 0.0f;
-        }
+    for (int j = 0; j < VPT; ++j) {
+      const int v = li + tpr * j;
+      if (r < p.rows && v < nvec) {
+        a[j].load(p.x, r * nvec + v);
+        if (ADD) b[j].load(p.residual, r * nvec + v);
       }
     }
+  };
+  long long r = static_cast<long long>(blockIdx.x) * rpb + (threadIdx.x >> p.tpr_log2);
+  const long long step = static_cast<long long>(gridDim.x) * rpb;
+  load(r);
+  if (kKeep) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (li + tpr * j < nvec) w[j].load_kept(p.weight, li + tpr * j);
+  }
+  // (rows of several warps have a block of their own, whose threads all run the same
+  // iterations and branches on the row: row_reduce's barriers)
+  for (int buf = 0; r < p.rows; r += step, buf ^= 1) {
+    const long long base = r * nvec;
+    float f[VPT][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (li + tpr * j < nvec) {
+        a[j].get(f[j]);
+        if (ADD) {
+          float g[8];
+          b[j].get(g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[j][i] += g[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[j][i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i], f[j][i], ss);
+    }
+    if (kAhead) load(r + step);
     if (p.sum_out) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-        if (valid && li + tpr * j < nvec) Vec8<T>::store(p.sum_out, base + li + tpr * j, f[j]);
+        if (li + tpr * j < nvec) Vec8<T>::store(p.sum_out, base + li + tpr * j, f[j]);
     }
-    float ss = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i], f[j][i], ss);
-    ss = row_reduce<false>(ss, red, warps);
-    float rstd = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
+    ss = row_reduce(ss, red[buf], warps);
+    float rstd = rsqrtf(fmaf(ss, rD, p.eps));
     // squares that leave fp32's range (above; or below, where eps does not cover them): the
     // row times the power of two that brings its largest value to [1, 2), or, below, as far
     // as eps times its square stays in range
     if (!(ss <= 1e37f) || (ss < 1e-27f && p.eps < 1e-25f)) {
-      float m = 0.0f;
+      uint32_t m = 0u;
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = combine<true>(m, fabsf(f[j][i]));
-      m = row_reduce<true>(m, red, warps);
-      if (m > 0.0f && isfinite(m)) {
-        const int e = max(ilogbf(m), p.eps > 0.0f ? -44 : -200);
+        for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[j][i]));
+      if (warps > 1) __syncthreads();
+      m = row_reduce(m, redm[buf], warps);
+      if (m > 0u && m < 0x7f800000u) {
+        const int e = max(ilogbf(__uint_as_float(m)), p.eps > 0.0f ? -44 : -200);
         ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
@@ -176,78 +203,91 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
             f[j][i] = ldexpf(f[j][i], -e);
             ss = fmaf(f[j][i], f[j][i], ss);
           }
-        ss = row_reduce<false>(ss, red, warps);
-        rstd = rsqrtf(ss / static_cast<float>(p.D) + ldexpf(p.eps, -2 * e));
+        ss = row_reduce(ss, red[buf], warps);
+        rstd = rsqrtf(fmaf(ss, rD, ldexpf(p.eps, -2 * e)));
       }
+      if (warps > 1) __syncthreads();
     }
-    float most = 0.0f;
+    uint32_t most[VPT];
+    uint32_t all = 0u;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int v = li + tpr * j;
-      if (v < nvec) {
-        Vec8<T> w;
-        w.load_kept(p.weight, v);
+      most[j] = 0u;
+      if (li + tpr * j < nvec) {
         float g[8];
-        w.get(g);
+        if (!kKeep) w[j].load_kept(p.weight, li + tpr * j);
+        w[j].get(g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           f[j][i] = f[j][i] * rstd * g[i];
-          most = combine<true>(most, fabsf(f[j][i]));
+          if (Q != kNoQ) most[j] = max(most[j], magnitude(f[j][i]));
         }
-        if (valid && p.y) Vec8<T>::store(p.y, base + v, f[j]);
+        if (p.y) Vec8<T>::store(p.y, base + li + tpr * j, f[j]);
+      }
+      all = max(all, most[j]);
+    }
+    if (Q == kRowQ) {
+      const float s = e4m3_scale(row_reduce(all, redm[buf], warps));
+      if (li == 0) p.scales[r] = s;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (li + tpr * j < nvec) reinterpret_cast<uint2*>(p.q)[base + li + tpr * j] = e4m3_codes(f[j], s);
+    }
+    if (Q == kGroupQ) {
+      // group / 8 neighbouring threads hold a group (D is a multiple of it, so they hold it
+      // whole or not at all)
+      const int lanes = p.group / 8;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        uint32_t m = most[j];
+        for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+        const int v = li + tpr * j;
+        if (v < nvec) {
+          const float s = e4m3_scale(m);
+          if (v % lanes == 0) p.scales[r * (nvec / lanes) + v / lanes] = s;
+          reinterpret_cast<uint2*>(p.q)[base + v] = e4m3_codes(f[j], s);
+        }
       }
     }
-    if (!p.q) continue;
-    if (!p.group) {
-      const float s = e4m3_scale(row_reduce<true>(most, red, warps));
-      if (valid && li == 0) p.scales[r] = s;
-      most = s;
-    }
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = li + tpr * j;
-      float s = most;
-      if (p.group) {
-        // group / 8 neighbouring threads hold a group (D is a multiple of it, so they
-        // hold it whole or not at all)
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = combine<true>(s, fabsf(f[j][i]));
-        for (int o = 1; o < p.group / 8; o <<= 1) s = combine<true>(s, __shfl_xor_sync(kFull, s, o));
-        s = e4m3_scale(s);
-        if (valid && v < nvec && v % (p.group / 8) == 0)
-          p.scales[r * (p.D / p.group) + v / (p.group / 8)] = s;
-      }
-      if (valid && v < nvec) {
-        const float inv = 1.0f / s;
-        uint32_t u[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          u[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
-                           make_float2(f[j][2 * i] * inv, f[j][2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3))
-                       << (16 * (i & 1));
-        reinterpret_cast<uint2*>(p.q)[base + v] = make_uint2(u[0], u[1]);
-      }
-    }
+    if (!kAhead) load(r + step);
   }
 }
 
-template <typename T, int VPT>
-cudaError_t launch_vpt(const NormParams& p, cudaStream_t s) {
+template <typename T, int VPT, bool ADD>
+cudaError_t launch_q(const NormParams& p, cudaStream_t s) {
+  auto kern = !p.q ? add_rms_norm_kernel<T, VPT, ADD, kNoQ>
+                   : p.group ? add_rms_norm_kernel<T, VPT, ADD, kGroupQ> : add_rms_norm_kernel<T, VPT, ADD, kRowQ>;
   const int tpr = 1 << p.tpr_log2, block = tpr == 32 ? 256 : tpr, rpb = block / tpr;
   const long long want = (static_cast<long long>(p.rows) + rpb - 1) / rpb;
-  const int grid = static_cast<int>(std::min<long long>(want, 2048ll / block * device_sm_count()));
-  const cudaError_t e = launch_kernel(add_rms_norm_kernel<T, VPT>, dim3(grid), dim3(block), 0, s, p);
+  // (as many as 512 threads an SM: what their registers allow)
+  const int grid = static_cast<int>(std::min<long long>(want, 512ll / block * device_sm_count()));
+  const cudaError_t e = launch_kernel(kern, dim3(grid), dim3(block), 0, s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <typename T, int VPT>
+cudaError_t launch_vpt(const NormParams& p, cudaStream_t s) {
+  return p.residual ? launch_q<T, VPT, true>(p, s) : launch_q<T, VPT, false>(p, s);
 }
 
 template <typename T>
 cudaError_t launch_type(NormParams& p, cudaStream_t s) {
   const int nvec = p.D / 8;
-  int tl = 5;
-  while ((4 << tl) < nvec) ++tl;
-  p.tpr_log2 = tl;
-  return launch_vpt<T, 4>(p, s);
+  auto threads = [&](int vpt) {
+    int tl = 5;
+    while ((vpt << tl) < nvec) ++tl;
+    return tl;
+  };
+  // few rows: every thread has one vector, for the shortest chain
+  if (p.rows <= 2 * kSms && threads(1) <= kMaxTprLog2) {
+    p.tpr_log2 = threads(1);
+    return launch_vpt<T, 1>(p, s);
+  }
+  if (threads(4) <= kMaxTprLog2) {
+    p.tpr_log2 = threads(4);
+    return launch_vpt<T, 4>(p, s);
+  }
+  p.tpr_log2 = threads(8);
+  return launch_vpt<T, 8>(p, s);
 }
 
 }  // namespace
