@@ -361,7 +361,7 @@ int moe_dequantize_w4(const void* Wq, const void* scales, const void* zeros, int
  * Ties, of groups and of experts, go to the lower index.  Without select_bias the
  * order of experts (and of groups by their largest) is taken from the logits, which
  * order as p does and differ where p no longer does.  Renormalised weights of a
- * softmax are the softmax over the chosen logits; of sigmoids below e^-60 the same
+ * softmax are the softmax over the chosen logits; of sigmoids below e^-57 the same
  * (their ratios there, kept from underflow).  A non-finite logit (or c) counts as
  * -infinity: p is 0, the expert is chosen last and not part of a group's sum,
  * MOE_DEV_NONFINITE_LOGIT is set; a token that has only such experts to choose gets

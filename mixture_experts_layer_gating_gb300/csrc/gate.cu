@@ -37,20 +37,24 @@ __device__ __forceinline__ void load_logits(const float* __restrict__ planes, in
   }
 }
 
-template <int EPL>
-__global__ void __launch_bounds__(256)
+constexpr int kGateWarps = 8;
+
+template <int EPL, bool WHOLE>
+__global__ void __launch_bounds__(kGateWarps * 32)
     gate_kernel(const float* __restrict__ planes, int nsplit, const float* __restrict__ logit_bias,
                 const float* __restrict__ select_bias, float* logits, int T, bool vec, const GateParams g,
                 int32_t* __restrict__ ids, float* __restrict__ w, int32_t* err) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long t = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  __shared__ __align__(16) uint32_t scratch[kGateWarps][32 * EPL];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long t = static_cast<long long>(blockIdx.x) * kGateWarps + warp;
   if (t >= T) return;
   float v[EPL];
   load_logits<EPL>(planes + t * g.E, nsplit, static_cast<size_t>(T) * g.E, lane, g.E, vec, v);
-  warp_gate_topk<EPL>(v, lane, g, logit_bias, select_bias, (nsplit > 1 || logit_bias) ? logits + t * g.E : nullptr,
-                      ids + t * g.k, w + t * g.k, err);
+  warp_gate_topk<EPL, WHOLE>(v, lane, g, logit_bias, select_bias,
+                             (nsplit > 1 || logit_bias) ? logits + t * g.E : nullptr, ids + t * g.k, w + t * g.k,
+                             scratch[warp], err);
 }
 
 }  // namespace
@@ -59,11 +63,13 @@ cudaError_t launch_gate(const float* planes, int nsplit, const float* logit_bias
                         float* logits, int T, const GateParams& g, int32_t* ids, float* w, int32_t* err,
                         cudaStream_t s) {
   if (T <= 0) return cudaSuccess;
-  const int wpb = 8, blocks = (T + wpb - 1) / wpb;
+  const int blocks = (T + kGateWarps - 1) / kGateWarps;
   const bool vec = g.E % 4 == 0 && !(reinterpret_cast<uintptr_t>(planes) & 15);
-  auto kern = g.E <= 128 ? gate_kernel<4> : g.E <= 256 ? gate_kernel<8> : gate_kernel<16>;
-  const cudaError_t e = launch_kernel(kern, dim3(blocks), dim3(wpb * 32), 0, s, planes, nsplit, logit_bias, select_bias,
-                                      logits, T, vec, g, ids, w, err);
+  auto kern = g.E <= 128   ? (g.E % 4 ? gate_kernel<4, false> : gate_kernel<4, true>)
+              : g.E <= 256 ? (g.E % 8 ? gate_kernel<8, false> : gate_kernel<8, true>)
+                           : (g.E % 16 ? gate_kernel<16, false> : gate_kernel<16, true>);
+  const cudaError_t e = launch_kernel(kern, dim3(blocks), dim3(kGateWarps * 32), 0, s, planes, nsplit, logit_bias,
+                                      select_bias, logits, T, vec, g, ids, w, err);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -21,51 +21,89 @@ __device__ __forceinline__ float ordered_value(uint32_t k) {
 __device__ __forceinline__ float gate_sigmoid(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
 
 // (a, b) becomes the two largest of a >= b and c >= d.
-__device__ __forceinline__ void merge_top2(float& a, float& b, float c, float d) {
-  b = fmaxf(fminf(a, c), fmaxf(b, d));
-  a = fmaxf(a, c);
+__device__ __forceinline__ void merge_top2(uint32_t& a, uint32_t& b, uint32_t c, uint32_t d) {
+  b = max(min(a, c), max(b, d));
+  a = max(a, c);
+}
+
+// Descending (Batcher's odd-even merge sort: 19 exchanges for 8, 63 for 16).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&s)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t x = s[i + j], y = s[i + j + q];
+            s[i + j] = max(x, y);
+            s[i + j + q] = min(x, y);
+          }
+}
+
+template <int EPL>
+__device__ __forceinline__ void put_lane(uint32_t* to, const uint32_t (&s)[EPL]) {
+  if constexpr (EPL == 2) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(s[0], s[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; i += 4) *reinterpret_cast<uint4*>(to + i) = make_uint4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+  }
 }
 
 // Lane l holds the token's projected logits of experts l EPL .. l EPL + EPL - 1 in v
 // (E <= 32 EPL; entries past E are ignored), so that among lanes and within one the lower
 // index comes first.  Writes the final logits to logits_row (when given), ids_row and
-// w_row [k]; returns ids_row[lane] on lanes below k <= 32, -1 on the others.
+// w_row [k]; returns ids_row[lane] on lanes below k <= 16, -1 on the others.
+//   WHOLE    E is a multiple of EPL: a lane has all its entries or none.
+//   scratch  32 EPL words of the warp's own in shared memory, 16-byte aligned.
 //
-// A group's value is found by lanes that hold whole parts of one group (the group's size a
-// multiple of EPL, a power of two lanes: shuffles among them), else group after group.
-template <int EPL>
+// Bound by instructions, most of them on the half-rate integer pipe, so each lane sorts
+// its keys once and the k rounds look at one head a lane: a warp maximum, the first lane
+// that has it, and that lane's next key from shared memory.  Which entry of the lane a
+// chosen key is, is found once at the end, by k lanes at a time.  A group's value comes from
+// the sorted keys of the lanes that hold it (the group's size a multiple of EPL, a power of
+// two lanes), else group after group.
+template <int EPL, bool WHOLE>
 __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const GateParams& g,
                                               const float* __restrict__ logit_bias,
                                               const float* __restrict__ select_bias, float* logits_row,
                                               int32_t* __restrict__ ids_row, float* __restrict__ w_row,
-                                              int32_t* err) {
+                                              uint32_t* scratch, int32_t* err) {
   constexpr unsigned kFull = 0xffffffffu;
   const int e0 = lane * EPL, E = g.E, k = g.k;
+  auto has = [&](int i) { return WHOLE ? e0 < E : e0 + i < E; };
+  uint32_t* mine = scratch + e0;
   bool bad = false;
+  {
+    uint32_t most = 0u;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    float x = -INFINITY;
-    if (e0 + i < E) {
-      x = v[i];
-      if (logit_bias) x += logit_bias[e0 + i];
-      if (logits_row) logits_row[e0 + i] = x;
-      if (!isfinite(x)) {
-        bad = true;
-        x = -INFINITY;
-      }
+    for (int i = 0; i < EPL; ++i) {
+      if (!has(i)) v[i] = -INFINITY;
+      if (logit_bias && has(i)) v[i] += logit_bias[e0 + i];
+      if (logits_row && has(i)) logits_row[e0 + i] = v[i];
+      if (has(i)) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
     }
-    v[i] = x;
+    if (most >= 0x7f800000u) {
+      bad = true;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (!isfinite(v[i])) v[i] = -INFINITY;
+    }
   }
+  const bool grouped = g.topk_group < g.n_group;
   // softmax over all experts: its largest logit and the inverse of its sum, where the
   // scores themselves are needed (renormalised weights need only those chosen)
-  const bool by_score = select_bias || (g.n_group > 1 && g.top2);
+  const bool scores = select_bias || (grouped && g.top2) || !g.renorm;
   float m = 0.0f, rz = 1.0f;
-  if (!g.sigmoid && (by_score || !g.renorm)) {
+  if (!g.sigmoid && scores) {
     m = v[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    m = ordered_value(__reduce_max_sync(kFull, ordered_key(m)));
     if (m == -INFINITY) m = 0.0f;
     float z = 0.0f;
 #pragma unroll
@@ -75,127 +113,165 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     rz = z > 0.0f ? 1.0f / z : 0.0f;
   }
   auto score = [&](float x) { return g.sigmoid ? gate_sigmoid(x) : expf(x - m) * rz; };
-  float c[EPL];  // what is compared: the biased score, or the logit
+  // keys of what is compared, the biased score or the logit; 0: not to be chosen (below
+  // every value's key, -infinity's too)
+  uint32_t key[EPL];
+  if (select_bias) {
+    float c[EPL];
+    uint32_t most = 0u;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    c[i] = v[i];
-    if (select_bias && e0 + i < E && v[i] != -INFINITY) {
-      c[i] = score(v[i]) + select_bias[e0 + i];
-      if (!isfinite(c[i])) {
-        bad = true;
-        c[i] = -INFINITY;
+    for (int i = 0; i < EPL; ++i) {
+      c[i] = has(i) ? score(v[i]) + select_bias[e0 + i] : 0.0f;
+      most = max(most, __float_as_uint(c[i]) & 0x7fffffffu);
+    }
+    if (bad || most >= 0x7f800000u) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        bad |= !isfinite(c[i]);
+        if (!isfinite(c[i]) || v[i] == -INFINITY) c[i] = -INFINITY;
       }
     }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = has(i) ? ordered_key(c[i]) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = has(i) ? ordered_key(v[i]) : 0u;
   }
   if (__any_sync(kFull, bad) && lane == 0) atomicOr(err, MOE_DEV_NONFINITE_LOGIT);
 
-  uint32_t key[EPL];  // 0: not to be chosen (below every value's key, -infinity's too)
+  // a group's value as a key, of the keys a >= b of its two largest
+  auto group_key = [&](uint32_t ka, uint32_t kb) {
+    const float a = ordered_value(ka), b = ordered_value(kb);
+    if (!g.top2 || a == -INFINITY) return ka;
+    const bool two = kb != 0u && b != -INFINITY;
+    if (select_bias) return ordered_key(two ? a + b : a);
+    return ordered_key(score(a) + (two ? score(b) : 0.0f));
+  };
+  const int size = grouped ? E / g.n_group : E, lanes = size / EPL;
+  const bool by_lanes = size % EPL == 0 && (lanes & (lanes - 1)) == 0;
+  if (grouped && !by_lanes) {
+    uint32_t gk = 0u;  // lane j: group j
+    for (int j = 0; j < g.n_group; ++j) {
+      uint32_t a = 0u, b = 0u;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) key[i] = e0 + i < E ? ordered_key(c[i]) : 0u;
-
-  if (g.topk_group < g.n_group) {
-    const int size = E / g.n_group, lanes = size / EPL;
-    // (of the two largest, b <= a; -infinity: not there)
-    auto value = [&](float a, float b) {
-      if (!g.top2 || a == -INFINITY) return a;
-      if (select_bias) return b == -INFINITY ? a : a + b;
-      return score(a) + score(b);
-    };
-    if (size % EPL == 0 && (lanes & (lanes - 1)) == 0) {
-      float a = c[0], b = -INFINITY;
+      for (int i = 0; i < EPL; ++i)
+        if (e0 + i >= j * size && e0 + i < (j + 1) * size) merge_top2(a, b, key[i], 0u);
 #pragma unroll
-      for (int i = 1; i < EPL; ++i) merge_top2(a, b, c[i], -INFINITY);
-      for (int o = 1; o < lanes; o <<= 1)
+      for (int o = 16; o > 0; o >>= 1)
         merge_top2(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
-      uint32_t gk = e0 < E ? ordered_key(value(a, b)) : 0u;
-      bool kept = false;
-      for (int j = 0; j < g.topk_group; ++j) {
-        const uint32_t best = __reduce_max_sync(kFull, gk);
-        const int first = __ffs(__ballot_sync(kFull, gk == best)) - 1;
-        if (e0 < E && lane / lanes == first / lanes) {
-          kept = true;
-          gk = 0u;
-        }
-      }
-      if (!kept) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = 0u;
-      }
-    } else {
-      uint32_t gk = 0u;  // lane j: group j
-      for (int j = 0; j < g.n_group; ++j) {
-        float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (e0 + i >= j * size && e0 + i < (j + 1) * size) merge_top2(a, b, c[i], -INFINITY);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          merge_top2(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
-        const uint32_t kj = ordered_key(value(a, b));
-        if (lane == j) gk = kj;
-      }
-      uint32_t kept = 0u;
-      for (int j = 0; j < g.topk_group; ++j) {
-        const uint32_t best = __reduce_max_sync(kFull, gk);
-        const int first = __ffs(__ballot_sync(kFull, gk == best)) - 1;
-        kept |= 1u << first;
-        if (lane == first) gk = 0u;
-      }
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (e0 + i < E && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
+      const uint32_t kj = group_key(a, b);
+      if (lane == j) gk = kj;
     }
+    uint32_t kept = 0u;
+    for (int j = 0; j < g.topk_group; ++j) {
+      const uint32_t best = __reduce_max_sync(kFull, gk);
+      const int first = __ffs(__ballot_sync(kFull, gk == best)) - 1;
+      kept |= 1u << first;
+      if (lane == first) gk = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (has(i) && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
+  }
+  uint32_t s[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) s[i] = key[i];
+  sort_keys(s);
+  uint32_t head = s[0];
+  if (grouped && by_lanes) {
+    uint32_t a = s[0], b = s[1];
+    for (int o = 1; o < lanes; o <<= 1)
+      merge_top2(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
+    uint32_t gk = e0 < E ? group_key(a, b) : 0u;
+    const int shift = 31 - __clz(lanes);
+    bool kept = false;
+    for (int j = 0; j < g.topk_group; ++j) {
+      const uint32_t best = __reduce_max_sync(kFull, gk);
+      const int first = __ffs(__ballot_sync(kFull, gk == best)) - 1;
+      if (e0 < E && lane >> shift == first >> shift) {
+        kept = true;
+        gk = 0u;
+      }
+    }
+    if (!kept) head = 0u;  // (its other keys are then never looked at)
   }
 
-  // k rounds: the largest key of the warp, the first lane that has it, its first entry
-  float my_x = -INFINITY;  // logit of lane j's choice
-  int my_e = 0;
+  __syncwarp();
+  put_lane(mine, s);
+  int at = 0, my_from = 0;
+  uint32_t my_key = 0u;
   for (int j = 0; j < k; ++j) {
-    uint32_t bk = key[0];
-    int bi = 0;
-    float bx = v[0];
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) {
-      if (key[i] > bk) {
-        bk = key[i];
-        bi = i;
-        bx = v[i];
-      }
-    }
-    const uint32_t best = __reduce_max_sync(kFull, bk);
-    const int from = __ffs(__ballot_sync(kFull, bk == best)) - 1;
-    const float x = __shfl_sync(kFull, bx, from);
-    const int e = from * EPL + __shfl_sync(kFull, bi, from);
-    if (lane == from) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == bi) key[i] = 0u;
-    }
+    const uint32_t best = __reduce_max_sync(kFull, head);
+    const int from = __ffs(__ballot_sync(kFull, head == best)) - 1;
+    if (lane == from) head = ++at < EPL ? mine[at] : 0u;
     if (lane == j) {
-      my_x = x;
-      my_e = e;
+      my_key = best;
+      my_from = from;
     }
   }
-  float top = my_x;  // largest chosen logit (lanes past k hold -infinity)
+  // the entry of lane my_from: the first with this key, or, where the lane gave the same key
+  // in the rounds just before (equal keys are chosen one after another), the one after those
+  __syncwarp();
+  put_lane(mine, key);
+  __syncwarp();
+  const uint32_t* theirs = scratch + my_from * EPL;
+  const uint32_t up_key = __shfl_up_sync(kFull, my_key, 1);
+  const int up_from = __shfl_up_sync(kFull, my_from, 1);
+  const uint32_t again = __ballot_sync(kFull, lane > 0 && lane < k && my_key == up_key && my_from == up_from);
+  int idx = 0;
+  if (again == 0u) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  float w;
-  if (top == -INFINITY) {
-    w = 1.0f / static_cast<float>(k);
-  } else if (g.renorm) {
-    // (e^l is sigmoid(l) in fp32 below -60, and more: it does not run out there)
-    const float p = g.sigmoid && top > -60.0f ? gate_sigmoid(my_x) : expf(my_x - top);
-    float z = lane < k ? p : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-    w = p / z;
+    for (int i = EPL - 1; i > 0; --i)
+      if (theirs[i] == my_key) idx = i;
+    if (theirs[0] == my_key) idx = 0;
   } else {
+    int skip = lane - (31 - __clz(~again & ((2u << lane) - 1u)));
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (theirs[i] == my_key && skip-- == 0) idx = i;
+  }
+  float my_x = ordered_value(my_key);  // logit of lane j's choice
+  if (select_bias) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = __float_as_uint(v[i]);
+    put_lane(mine, key);
+    __syncwarp();
+    my_x = __uint_as_float(theirs[idx]);
+  }
+  if (lane >= k) my_x = -INFINITY;
+
+  float w;
+  if (!g.renorm && __shfl_sync(kFull, my_x, 0) != -INFINITY) {
     w = score(my_x);
+  } else {
+    // (a softmax's first choice, where its scores were not needed, is its largest logit)
+    const float first = __shfl_sync(kFull, my_x, 0);
+    float p = g.sigmoid || scores ? score(my_x) : expf(my_x - (first == -INFINITY ? 0.0f : first));
+    if (lane >= k) p = 0.0f;
+    float z = p;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+    if (__shfl_sync(kFull, z, 0) > 1e-25f) {
+      w = __fdividef(p, z);
+    } else {
+      // scores that run out of range: of a softmax, those beside its largest; sigmoids, which
+      // are e^l there.  Their ratios are the exponentials of differences
+      float top = my_x;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      p = lane >= k ? 0.0f : top == -INFINITY ? 1.0f : expf(my_x - top);
+      z = p;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+      w = __fdividef(p, z);
+    }
   }
   if (lane >= k) return -1;
-  ids_row[lane] = my_e;
+  const int e = my_from * EPL + idx;
+  ids_row[lane] = e;
   w_row[lane] = w * g.scale;
-  return my_e;
+  return e;
 }
 
 }  // namespace moe

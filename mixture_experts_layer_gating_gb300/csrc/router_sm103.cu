@@ -64,8 +64,12 @@ struct RtCfg {
   // partial rows of the cluster's tile at their finishing CTA: 128 / nh rows
   // of nh * NB + 4 floats (the padding spreads a warp's 16-byte row stores
   // over all banks); nh = 2 only with NB = 256
-  static_assert(RT_BM * (NB + 4) * 4 <= RT_RING_BYTES, "partial rows fit the ring");
-  static_assert((RT_BM / 2) * (2 * 256 + 4) * 4 <= RT_RING_BYTES, "partial rows fit the ring");
+  static constexpr int kRedBytes = RT_BM * (NB + 4) * 4;  // (nh = 2: a little less)
+  static_assert(kRedBytes <= RT_RING_BYTES, "partial rows fit the ring");
+  static_assert((RT_BM / 2) * (2 * 256 + 4) * 4 <= RT_BM * (256 + 4) * 4, "partial rows fit the ring");
+  // behind them, the gated choice's scratch of each warp (nh = 2: 512 experts)
+  static_assert(kRedBytes % 16 == 0 && kRedBytes + RT_WARPS * (NB == 256 ? 512 : NB) * 4 <= RT_RING_BYTES,
+                "the scratch of the choice fits behind the partial rows");
 };
 
 struct RtCtrl {
@@ -295,7 +299,10 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     float* w_row = p.w + static_cast<size_t>(t) * p.k;
     int id;
     if constexpr (GATED)
-      id = warp_gate_topk<EPL>(v, lane, p.gate, p.bias, p.select_bias, logits_row, ids_row, w_row, p.err);
+      // (E is a multiple of 8)
+      id = warp_gate_topk<EPL, (EPL <= 8)>(v, lane, p.gate, p.bias, p.select_bias, logits_row, ids_row, w_row,
+                                           reinterpret_cast<uint32_t*>(base + RtCfg<NB>::kRedBytes) + warp * 32 * EPL,
+                                           p.err);
     else
       id = warp_topk_softmax<EPL>(v, lane, p.E, p.k, p.renorm, p.bias, logits_row, ids_row, w_row, p.err);
     if (id >= 0) atomicAdd(&hist[id], 1);
