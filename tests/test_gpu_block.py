@@ -324,7 +324,9 @@ def _check_lora(d, dt, base=True, scales=True, in_place=False):
     (1, 8, 8, 8, 1, "one"), (1, 2048, 2048, 16, 8, "one"), (2, 264, 40, 24, 2, "mixed"), (17, 1000, 1032, 8, 1, "one"),
     (33, 512, 264, 64, 3, "mixed"), (61, 1024, 520, 64, 40, "mixed"), (64, 256, 512, 128, 64, "mixed"), (64, 256, 256, 72, 2, "none"),
     (65, 256, 264, 16, 1, "one"), (100, 328, 776, 40, 90, "mixed"), (129, 512, 256, 32, 2, "runs"), (300, 256, 1544, 256, 5, "mixed"),
-    (1000, 512, 320, 64, 4, "runs"), (1025, 136, 128, 24, 1, "none"), (2000, 256, 264, 16, 1500, "mixed"), (513, 64, 64, 200, 16, "mixed")])
+    (1000, 512, 320, 64, 4, "runs"), (1025, 136, 128, 24, 1, "none"), (2000, 256, 264, 16, 1500, "mixed"), (513, 64, 64, 200, 16, "mixed"),
+    (700, 520, 1288, 96, 6, "mixed"), (400, 264, 136, 128, 2, "runs"), (5000, 1000, 1000, 40, 3, "mixed"), (260, 136, 2056, 16, 2, "mixed"),
+    (3000, 4104, 72, 8, 7, "runs"), (90, 72, 8, 256, 1, "one")])
 def test_lora(T, K, N, r, n, how, dt):
     d = _lora_inputs(T, K, N, r, n, dt, T + K + N + r, how)
     y = _check_lora(d, dt)
