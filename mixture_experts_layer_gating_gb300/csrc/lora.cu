@@ -8,11 +8,11 @@
 // the tiles.  Then two launches: lora_shrink, v = x A^T as fp32 planes over slices of K, and
 // lora_expand, which adds the planes in order and multiplies by B.
 //
-// Both products are mma.sync on operands that go from global memory straight to the
-// registers that multiply them: A and B are row after row of the reduction dimension, as
-// are x and v, and since a sum may take its terms in any order, a thread's four-byte pieces
-// of a 32-wide step are taken from the 16 bytes that it loads.  At ranks of 8 to 256 the
-// products are a small part of the time that x, y and the adapters' bytes need.
+// A few rows to an adapter: both products are mma.sync on operands that go from global
+// memory straight to the registers that multiply them: A and B are row after row of the
+// reduction dimension, as are x and v, and since a sum may take its terms in any order, a
+// thread's four-byte pieces of a 32-wide step are taken from the 16 bytes that it loads.  The
+// adapters' bytes are the bound.  Many rows: tcgen05 (below), x and y are.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,10 +45,11 @@ struct LoraParams {
   int32_t* order;
   LoraTile* tiles;
   int32_t* ntiles;
+  int32_t* err;
   int T, K, N, r, n;
-  int splits;  // of K
+  int splits;  // of K (and planes, where the slices are not added at once)
   int slices;  // of r
-  int chunk;   // columns of y a CTA takes, a multiple of 256
+  int chunk;   // columns of y a CTA takes, a multiple of 64 (few rows: of 256)
 };
 
 // ------------------------------------------------------------------- plan
@@ -64,22 +65,32 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const LoraParams p, int
   for (int i = tid; i < nb; i += 1024) bins[i] = 0;
   __syncthreads();
   auto bin = [&](int id) { return static_cast<unsigned>(id) < static_cast<unsigned>(p.n) ? id : p.n; };
-  // position of row t in its adapter's bin (t past the last: none).  A request's rows lie
-  // together: one atomic for a warp whose rows have one adapter.
-  auto take = [&](int t) {
-    const bool in = t < p.T;
-    const int b = in ? bin(p.ids[t]) : -1, b0 = __shfl_sync(0xffffffffu, b, 0);
-    const unsigned mask = __ballot_sync(0xffffffffu, in);
+  // position of a row in its adapter's bin b (-1: no row).  A request's rows lie together: one
+  // atomic for a warp whose rows have one adapter.
+  auto take = [&](int b) {
+    const unsigned mask = __ballot_sync(0xffffffffu, b >= 0);
+    const int b0 = __shfl_sync(0xffffffffu, b, 0);
     int at = 0;
-    if (__all_sync(0xffffffffu, b == b0 || !in)) {
-      if (lane == 0 && in) at = atomicAdd(&bins[b], __popc(mask));
+    if (__all_sync(0xffffffffu, b == b0 || b < 0)) {
+      if (lane == 0 && b >= 0) at = atomicAdd(&bins[b], __popc(mask));
       at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1u));
-    } else if (in) {
+    } else if (b >= 0) {
       at = atomicAdd(&bins[b], 1);
     }
     return at;
   };
-  for (int t = tid; t - tid < p.T; t += 1024) take(t);
+  // the bins of the rows t, t + 1024, ..: eight loads under way at a time
+  auto bins_of = [&](long long t, int (&b)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = t + 1024 * i < p.T ? bin(p.ids[t + 1024 * i]) : -1;
+  };
+  for (long long t = tid; t - tid < p.T; t += 8192) {
+    int b[8];
+    bins_of(t, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t - tid + 1024 * i < p.T) take(b[i]);
+  }
   __syncthreads();
   // exclusive sums of rows and of tiles over the adapters, a run of them a thread
   const int per = (nb + 1023) / 1024, b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
@@ -113,9 +124,15 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const LoraParams p, int
   }
   if (tid == 1023) *p.ntiles = tile;
   __syncthreads();
-  for (int t = tid; t - tid < p.T; t += 1024) {
-    const int at = take(t);
-    if (t < p.T) p.order[at] = t;
+  for (long long t = tid; t - tid < p.T; t += 8192) {
+    int b[8];
+    bins_of(t, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t - tid + 1024 * i < p.T) {
+        const int at = take(b[i]);
+        if (b[i] >= 0) p.order[at] = static_cast<int>(t) + 1024 * i;
+      }
   }
 }
 
@@ -430,277 +447,393 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_expand_kernel(const L
 }
 
 // --------------------------------------------------------- many rows to a tile
-// Rings of shared-memory stages filled by cp.async, each stage's rows cut into 16-byte
-// pieces.  Two neighbouring rows are read by a quarter of a warp at the same piece of
-// each, so where they would meet in the banks odd rows keep their pieces in another order.
+// Tiles of 128 rows on the tensor cores (tcgen05): the rows of a tile, which may lie
+// anywhere, come by 16-byte cp.async into the operands' swizzled layout, through rings of
+// stages that eight warps fill and one of their lanes multiplies from.
+//
+// Both kernels take their tensor memory before they let the next launch begin (shrink) or
+// wait for the one before (expand): a CTA that waits for a launch never keeps one of that
+// launch from its tensor memory.
+constexpr int kWideRows = 128, kWideThreads = 256, kWideStages = 4, kMaxCluster = 8;
+struct WideCtl {
+  uint64_t mma[kWideStages];  // a stage's products are done
+  uint64_t all;
+  uint32_t tmem;
+  int abort;
+};
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+__device__ __forceinline__ void wide_begin(WideCtl* ctl, uint32_t cols) {
+  if (threadIdx.x < 32) {
+    tmem_alloc(&ctl->tmem, cols);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWideStages; ++i) mbar_init(&ctl->mma[i], 1);
+    mbar_init(&ctl->all, 1);
+    ctl->abort = 0;
+    fence_mbarrier_init();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+}
+__device__ __forceinline__ void wide_end(uint32_t tmem, uint32_t cols) {
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (threadIdx.x < 32) tmem_dealloc(tmem, cols);
+}
+// A wait that gives up lets the others go, and is reported; every thread stays in its loop.
+__device__ __forceinline__ void wide_wait(WideCtl* ctl, uint64_t* bar, uint32_t parity, int32_t* err) {
+  if (mbar_wait(bar, parity, &ctl->abort)) return;
+  ctl->abort = 1;
+  atomicOr(err, MOE_DEV_WAIT_TIMEOUT);
+}
+// 1024-byte aligned start of the dynamic shared memory
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  const uint32_t a = smem_u32(p);
+  return p + (((a + 1023u) & ~1023u) - a);
 }
 
-// Shrink.  A CTA: a tile of at most BM rows, a slice of 8 NT RW columns of v and a slice of
-// K.  Its four warps hold 32 rows x 8 NT columns each (RW of them beside one another).
-constexpr int kShrinkStages = 4, kShrinkThreads = 128;
-template <int BM, int NT>
-struct ShrinkTile {
-  static constexpr int RW = 4 * 32 / BM, COLS = 8 * NT * RW;
-  static constexpr int kStage = (BM + COLS) * 128;  // 64 of K a stage
-  static constexpr int kSmem = kShrinkStages * kStage;
+inline __host__ __device__ int pow2_cols(int n) {
+  int c = 32;
+  while (c < n) c *= 2;
+  return c;
+}
+
+// Shrink.  A cluster: a tile; its CTAs: slices of K, 64 of it a stage; v [128, r] in tensor
+// memory.  At the end the slices' sums are added in their order through distributed shared
+// memory, a part of the rows by each CTA.
+struct ShrinkGeom {
+  int rn;  // r, a multiple of 16
+  __host__ __device__ explicit ShrinkGeom(int r) : rn((r + 15) / 16 * 16) {}
+  __host__ __device__ uint32_t stage() const { return (kWideRows + rn) * 128; }
+  __host__ __device__ uint32_t cols() const { return pow2_cols(rn); }
+  // (the sums, rows of rn + 4 floats, fit the ring: 512 (rn + 4) <= 512 (128 + rn))
+  size_t smem() const { return 1024 + kWideStages * stage(); }
 };
-template <int BM, int NT>
-__global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_wide_kernel(const LoraParams p) {
+__global__ void __launch_bounds__(kWideThreads, 2) lora_shrink_wide_kernel(const LoraParams p) {
+  __shared__ WideCtl ctl;
+  __shared__ int rows[kWideRows];
+  extern __shared__ uint8_t raw[];
+  const ShrinkGeom geom(p.r);
+  wide_begin(&ctl, geom.cols());
+  const uint32_t tmem = ctl.tmem;
   pdl_wait();
   pdl_launch_dependents();
-  using Tile = ShrinkTile<BM, NT>;
-  __shared__ int rows[BM];
-  extern __shared__ __align__(128) uint8_t ring[];
-  if (blockIdx.x >= *p.ntiles) return;
-  const LoraTile tile = p.tiles[blockIdx.x];
-  if (tile.adapter < 0) return;
-  for (int i = threadIdx.x; i < BM; i += kShrinkThreads) rows[i] = i < tile.count ? p.order[tile.first + i] : -1;
+  const bool there = static_cast<int>(blockIdx.x) < *p.ntiles;
+  const LoraTile tile = there ? p.tiles[blockIdx.x] : LoraTile{-1, 0, 0};
+  if (tile.adapter < 0) {  // (the whole cluster)
+    wide_end(tmem, geom.cols());
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < kWideRows) rows[tid] = tid < tile.count ? p.order[tile.first + tid] : -1;
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const int slice = blockIdx.y % p.slices, split = blockIdx.y / p.slices;
-  const int j0 = slice * Tile::COLS;
-  const int steps = (p.K + 63) / 64, s0 = static_cast<long long>(steps) * split / p.splits,
-            s1 = static_cast<long long>(steps) * (split + 1) / p.splits;
-  // this thread's piece of 16 bytes, of rows t0, t0 + 16, ...
-  const int piece = threadIdx.x & 7, t0 = threadIdx.x >> 3;
-  const uint32_t base = smem_u32(ring), put = t0 * 128 + ((piece ^ (4 * (t0 & 1))) << 4);
-  const __nv_bfloat16* A = p.A + (static_cast<size_t>(tile.adapter) * p.r + j0) * p.K;
-  int xrow[BM / 16];
+  uint8_t* ring = align1024(raw);
+  const uint32_t base = smem_u32(ring), stage_bytes = geom.stage();
+  const int steps = (p.K + 63) / 64;
+  const int s0 = static_cast<long long>(steps) * blockIdx.y / p.splits,
+            s1 = static_cast<long long>(steps) * (blockIdx.y + 1) / p.splits;
+  // this thread's piece of 16 bytes, of rows t0, t0 + 32, ... (which agree mod 8)
+  constexpr int kStep = kWideThreads / 8, kRowsEach = kWideRows / kStep;
+  const int piece = tid & 7, t0 = tid >> 3;
+  const uint32_t put = base + t0 * 128 + ((piece ^ (t0 & 7)) << 4);
+  const __nv_bfloat16* xp[kRowsEach];
+  uint32_t xbytes[kRowsEach];
 #pragma unroll
-  for (int i = 0; i < BM / 16; ++i) xrow[i] = rows[t0 + 16 * i];
-  auto load = [&](int s) {
-    if (s < s1) {
-      const uint32_t to = base + static_cast<uint32_t>((s - s0) % kShrinkStages) * Tile::kStage + put;
-      const int k = 64 * s + 8 * piece;
-      const bool in = k < p.K;
+  for (int i = 0; i < kRowsEach; ++i) {
+    const int row = rows[t0 + kStep * i];
+    xp[i] = p.x + static_cast<size_t>(max(row, 0)) * p.K + 64 * s0 + 8 * piece;
+    xbytes[i] = row >= 0 ? 16u : 0u;
+  }
+  const size_t apitch = static_cast<size_t>(kStep) * p.K;
+  const __nv_bfloat16* ap = p.A + (static_cast<size_t>(tile.adapter) * p.r + t0) * p.K + 64 * s0 + 8 * piece;
+  int k = 64 * s0 + 8 * piece, left = s1 - s0;  // of the next stage to be filled; those left
+  uint32_t slot = 0;
+  auto load = [&]() {
+    if (left > 0) {
+      const uint32_t to = put + slot * stage_bytes;
+      const bool in = k < p.K;  // (past it nothing is read: K is a multiple of a piece)
 #pragma unroll
-      for (int i = 0; i < BM / 16; ++i) {
-        const bool on = in && xrow[i] >= 0;
-        cp_async_16(to + i * 2048, on ? p.x + static_cast<size_t>(xrow[i]) * p.K + k : p.x, on ? 16u : 0u);
+      for (int i = 0; i < kRowsEach; ++i) {
+        cp_async_16(to + i * kStep * 128, in ? xp[i] : p.x, in ? xbytes[i] : 0u);
+        xp[i] += 64;
       }
-#pragma unroll
-      for (int i = 0; i < (Tile::COLS + 15) / 16; ++i) {
-        const int j = t0 + 16 * i;
-        const bool on = in && j0 + j < p.r;
-        cp_async_16(to + BM * 128 + i * 2048, on ? A + static_cast<size_t>(j) * p.K + k : p.x, on ? 16u : 0u);
+      const __nv_bfloat16* a = ap;
+      for (int j = t0; j < geom.rn; j += kStep, a += apitch) {
+        const bool on = in && j < p.r;
+        cp_async_16(to + (kWideRows + j - t0) * 128, on ? a : p.x, on ? 16u : 0u);
       }
+      ap += 64;
+      k += 64;
+      --left;
+      slot = slot + 1 == kWideStages ? 0 : slot + 1;
     }
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kShrinkStages - 1; ++i) load(s0 + i);
-  const int m0 = warp / Tile::RW * 32, c0 = warp % Tile::RW * 8 * NT;
-  const uint32_t xat = base + (m0 + g) * 128, aat = base + (BM + c0 + g) * 128;
-  float acc[2][NT][4] = {};
-  for (int s = s0; s < s1; ++s) {
-    cp_wait<kShrinkStages - 2>();
-    __syncthreads();  // the stage is there, and every warp is done with the one filled next
-    load(s + kShrinkStages - 1);
-    const uint32_t stage = static_cast<uint32_t>((s - s0) % kShrinkStages) * Tile::kStage;
+  for (int i = 0; i < kWideStages - 1; ++i) load();
+  const uint32_t idesc = make_idesc_bf16_f32(kWideRows, geom.rn, 0, 0);
+  for (int i = 0; i < s1 - s0; ++i) {
+    cp_wait<kWideStages - 2>();
+    fence_proxy_async_smem();
+    __syncthreads();  // the stage is there
+    if (tid == 0) {
+      tc_fence_after_sync();
+      const uint32_t at = base + static_cast<uint32_t>(i % kWideStages) * stage_bytes;
+      const uint64_t xd = make_smem_desc_sw128(at, 16, 1024), ad = make_smem_desc_sw128(at + kWideRows * 128, 16, 1024);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t at = stage + (((4 * h + tig) ^ (4 * (g & 1))) << 4);
-      uint4 xa[2][2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        xa[m][0] = lds16(xat + at + m * 2048);
-        xa[m][1] = lds16(xat + at + m * 2048 + 1024);
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const uint4 col = lds16(aat + at + j * 1024);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) step32(acc[m][j], xa[m][0], xa[m][1], col);
-      }
+      for (int q = 0; q < 4; ++q)
+        tc_mma_f16(tmem, smem_desc_advance(xd, 32 * q), smem_desc_advance(ad, 32 * q), idesc, (i | q) != 0);
+      tc_commit(&ctl.mma[i % kWideStages]);
+      if (i + 1 == s1 - s0) tc_commit(&ctl.all);
     }
+    // the stage that is filled next was multiplied from one step before
+    if (i > 0) wide_wait(&ctl, &ctl.mma[(i - 1) % kWideStages], ((i - 1) / kWideStages) & 1, p.err);
+    load();
   }
-  float* plane = p.planes + static_cast<size_t>(split) * p.T * p.r;
+  wide_wait(&ctl, &ctl.all, 0, p.err);
+  __syncwarp();
+  tc_fence_after_sync();
+  const int mine = 32 * (warp & 3) + lane;  // this thread's row; every second 32 of its columns
+  const bool alone = p.splits == 1;
+  float* part = reinterpret_cast<float*>(ring);
+  float* to = alone ? p.planes + static_cast<size_t>(max(rows[mine], 0)) * p.r : part + mine * (geom.rn + 4);
+  const int upto = !alone ? geom.rn : rows[mine] >= 0 ? p.r : 0;
+  for (int c = 32 * (warp >> 2); c < geom.rn; c += 64) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
+    tc_wait_ld();
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = rows[m0 + 16 * m + 8 * h + g];
-      if (row < 0) continue;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (j0 + c0 + 8 * j < p.r)
-          *reinterpret_cast<float2*>(plane + static_cast<size_t>(row) * p.r + j0 + c0 + 8 * j + 2 * tig) =
-              make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+    for (int j = 0; j < 32; j += 4)
+      if (c + j < upto) *reinterpret_cast<uint4*>(to + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  }
+  if (!alone) {
+    __syncwarp();
+    cluster_sync();
+    const int each = (kWideRows + p.splits - 1) / p.splits, first = each * blockIdx.y, quads = p.r / 4;
+    for (int o = tid; o < each * quads; o += kWideThreads) {
+      const int t = first + o / quads, c = 4 * (o % quads);
+      if (t >= kWideRows || rows[t] < 0) continue;
+      const float* at = part + t * (geom.rn + 4) + c;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int z = 0; z < p.splits; ++z) {
+        const float4 w = ld_cluster_v4(mapa_shared(at, z));
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
+      }
+      *reinterpret_cast<float4*>(p.planes + static_cast<size_t>(rows[t]) * p.r + c) = v;
     }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves before its sums are read
+  }
+  wide_end(tmem, geom.cols());
 }
 
-// Expand.  A CTA: a tile and `chunk` columns of y in blocks of 128 bytes of a row of y (ranks
-// past 64: 64 columns), whose rows of B and whose base come through the ring.  Eight warps of
-// 16 rows each, or, for ranks past 64, two beside one another on each 16 rows.  v's terms stay in
-// registers up to rank 64, past it in shared memory.
-constexpr int kExpandThreads = 256;
-template <typename Ty, bool HIGH>
-struct ExpandTile {
+// Expand.  A CTA: a tile and `chunk` columns of y in blocks of 128 bytes of a row of y.  v's
+// bf16 terms lie in tensor memory as the operand that stays; a stage holds the block's rows
+// of B and the tile's base; a block's products go to one of two sums in tensor memory and
+// are finished while the next block's are made: sums and base are added in place of the base
+// in shared memory, and go from there to y by pieces of 64 bytes of a row.  A warp brings,
+// adds and stores the same half of the columns of the same 32 rows, so that only B's stages
+// are shared between warps.
+template <typename Ty>
+struct ExpandGeom {
   static constexpr int TERMS = sizeof(Ty) == 2 ? 2 : 3;
-  static constexpr int BM = HIGH ? 64 : 128;
-  static constexpr int COLS = HIGH ? 64 : 128 / sizeof(Ty);
-  static constexpr int kStages = !HIGH ? 4 : sizeof(Ty) == 2 ? 3 : 2;  // (rank 256: 184 KB and 192 KB)
-  static constexpr int kRow = COLS * sizeof(Ty);  // bytes of a row of the base
-  static size_t smem(int rp) {
-    return static_cast<size_t>(kStages) * (COLS * rp * 2 + BM * kRow) + (HIGH ? TERMS * BM * rp * 2 : 0);
-  }
+  static constexpr int COLS = 128 / sizeof(Ty);
+  int atoms;  // of 64 of the rank
+  int ksteps; // of 16 of the rank
+  int kcols;  // tensor-memory columns of a term, whole stores of 16
+  __host__ __device__ explicit ExpandGeom(int r) : atoms((r + 63) / 64), ksteps((r + 15) / 16), kcols((r + 31) / 32 * 16) {}
+  __host__ __device__ uint32_t stage() const { return (atoms * COLS + kWideRows) * 128; }
+  __host__ __device__ uint32_t sums() const { return TERMS * kcols; }
+  __host__ __device__ uint32_t cols() const { return pow2_cols(TERMS * kcols + 2 * COLS); }
+  size_t smem() const { return 1024 + kWideStages * stage(); }
 };
-template <typename Ty, bool HIGH>
-__global__ void __launch_bounds__(kExpandThreads, HIGH ? 1 : 2) lora_expand_wide_kernel(const LoraParams p) {
-  using Tile = ExpandTile<Ty, HIGH>;
-  constexpr int TERMS = Tile::TERMS, BM = Tile::BM, COLS = Tile::COLS, STAGES = Tile::kStages;
-  constexpr int W = sizeof(Ty) / 2;  // 16-byte words of eight values
-  __shared__ int rows[BM];
-  extern __shared__ __align__(128) uint8_t ring[];
-  const bool there = blockIdx.x < *p.ntiles;
+template <typename Ty>
+__global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const LoraParams p) {
+  using Geom = ExpandGeom<Ty>;
+  constexpr int TERMS = Geom::TERMS, COLS = Geom::COLS, V = 16 / sizeof(Ty);
+  __shared__ WideCtl ctl;
+  __shared__ int rows[kWideRows];
+  extern __shared__ uint8_t raw[];
+  const Geom geom(p.r);
+  wide_begin(&ctl, geom.cols());
+  const uint32_t tmem = ctl.tmem;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool there = static_cast<int>(blockIdx.x) < *p.ntiles;
   const LoraTile tile = there ? p.tiles[blockIdx.x] : LoraTile{-1, 0, 0};
-  for (int i = threadIdx.x; i < BM; i += kExpandThreads) rows[i] = i < tile.count ? p.order[tile.first + i] : -1;
+  if (tid < kWideRows) rows[tid] = tid < tile.count ? p.order[tile.first + tid] : -1;
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const bool work = there && tile.adapter >= 0;
   const int c0 = blockIdx.y * p.chunk, c1 = min(p.N, c0 + p.chunk);
   const Ty* base = static_cast<const Ty*>(p.base);
   Ty* y = static_cast<Ty*>(p.y);
-  const int rp = (p.r + 31) / 32 * 32, pieces = rp / 8;
-  const int swz = rp & 32 ? 0 : 4;  // rows of an odd number of 64 bytes do not meet in the banks
-  const uint32_t stage_bytes = COLS * rp * 2 + BM * Tile::kRow, smem = smem_u32(ring);
-  const uint32_t terms_at = smem + STAGES * stage_bytes;
-  const __nv_bfloat16* B = p.B + static_cast<size_t>(max(tile.adapter, 0)) * p.N * p.r;
   const int blocks = (c1 - c0 + COLS - 1) / COLS;
-  auto load = [&](int b) {
-    if (b < blocks) {
-      const uint32_t to = smem + static_cast<uint32_t>(b % STAGES) * stage_bytes;
-      const int n0 = c0 + b * COLS;
-      for (int i = threadIdx.x; i < COLS * pieces; i += kExpandThreads) {
-        const int n = i / pieces, c = i % pieces;
-        const bool on = n0 + n < p.N && 8 * c < p.r;
-        cp_async_16(to + n * rp * 2 + ((c ^ (swz * (n & 1))) << 4), on ? B + static_cast<size_t>(n0 + n) * p.r + 8 * c : p.B,
-                    on ? 16u : 0u);
-      }
-      if (base) {
-        constexpr int PR = Tile::kRow / 16;
+  uint8_t* ring = align1024(raw);
+  const uint32_t ring_at = smem_u32(ring), stage_bytes = geom.stage(), base_at = geom.atoms * COLS * 128;
+  // B's pieces of 16 bytes: eight threads to a row, kStep rows at a time
+  constexpr int kStep = kWideThreads / 8;
+  const int bpiece = tid & 7, t0 = tid >> 3;
+  const uint32_t bput = ring_at + t0 * 128 + ((bpiece ^ (t0 & 7)) << 4);
+  const __nv_bfloat16* bp =
+      p.B + (static_cast<size_t>(max(tile.adapter, 0)) * p.N + c0 + t0) * p.r + 8 * bpiece;
+  // the base's and y's: four lanes to half a row, eight rows at a time (rows 4 apart to a
+  // quarter of the warp: no two of its pieces meet in the banks)
+  const int quarter = warp & 3, half = warp >> 2, piece = 4 * half + (lane & 3);
+  const int wrow = ((lane >> 2) & 1) * 4 + (lane >> 3);
+  const uint32_t wput = (32 * quarter + wrow) * 128 + ((piece ^ (wrow & 7)) << 4);  // + 1024 i
+  size_t off[4];
+  uint32_t ybytes[4];
 #pragma unroll
-        for (int u = 0; u < BM * PR / kExpandThreads; ++u) {
-          const int i = threadIdx.x + u * kExpandThreads, t = i / PR, c = i % PR, n = n0 + c * 16 / static_cast<int>(sizeof(Ty));
-          const int row = rows[t];
-          const bool on = row >= 0 && n < p.N;
-          cp_async_16(to + COLS * rp * 2 + t * Tile::kRow + ((c ^ ((W == 1 ? 4 : 1) * (t & 1))) << 4),
-                      on ? base + static_cast<size_t>(row) * p.N + n : base, on ? 16u : 0u);
+  for (int i = 0; i < 4; ++i) {
+    const int row = rows[32 * quarter + wrow + 8 * i];
+    off[i] = static_cast<size_t>(max(row, 0)) * p.N + c0 + V * piece;
+    ybytes[i] = row >= 0 ? 16u : 0u;
+  }
+  int n_load = 0, left = blocks;  // columns of the next block to be brought, from c0; blocks left
+  uint32_t slot = 0;
+  auto load = [&]() {
+    if (left > 0) {
+      const uint32_t at = slot * stage_bytes;
+      for (int a = 0; a < geom.atoms; ++a)
+#pragma unroll
+        for (int i = 0; i < COLS / kStep; ++i) {
+          const bool on = c0 + n_load + t0 + kStep * i < p.N && 64 * a + 8 * bpiece < p.r;
+          cp_async_16(bput + at + (a * COLS + kStep * i) * 128, on ? bp + static_cast<size_t>(kStep * i) * p.r + 64 * a : p.B,
+                      on ? 16u : 0u);
         }
+      bp += static_cast<size_t>(COLS) * p.r;
+      if (base) {
+        const bool in = c0 + n_load + V * piece < p.N;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          cp_async_16(ring_at + at + base_at + wput + 1024 * i, in ? base + off[i] + n_load : base, in ? ybytes[i] : 0u);
       }
+      n_load += COLS;
+      --left;
+      slot = slot + 1 == kWideStages ? 0 : slot + 1;
     }
     cp_commit();
   };
-  if (there && tile.adapter >= 0) {  // nothing of these comes from the launch before (the planes do)
+  if (work) {  // nothing of these comes from the launch before (the planes do)
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) load(i);
+    for (int i = 0; i < kWideStages; ++i) load();
   }
   pdl_wait();
   pdl_launch_dependents();
-  if (!there) return;
-  if (tile.adapter < 0) {
-    copy_rows(base, y, rows, tile.count, p.N, c0, c1);
+  if (!work) {
+    if (there) copy_rows(base, y, rows, tile.count, p.N, c0, c1);
+    wide_end(tmem, geom.cols());
     return;
   }
-  const float scale = p.scales ? p.scales[tile.adapter] : 1.0f;
-  const int mw = warp % (BM / 16), nw = warp / (BM / 16);
-  const int row[2] = {rows[16 * mw + g], rows[16 * mw + 8 + g]};
-  uint4 va[HIGH ? 1 : 2][2][TERMS];  // [32 of the rank][row half]
-  if constexpr (HIGH) {
-    for (int i = threadIdx.x; i < BM * pieces; i += kExpandThreads) {
-      const int t = i / pieces, c = i % pieces;
-      float f[8] = {};
-      if (rows[t] >= 0 && 8 * c < p.r) {
-        sum_planes(p, rows[t], 8 * c, f);
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+  {
+    // a row of v by two threads, 32 of the rank (16 columns) at a time
+    const int row = rows[32 * quarter + lane];
+    const float scale = p.scales ? p.scales[tile.adapter] : 1.0f;
+    for (int j = 32 * half; j < 2 * geom.kcols; j += 64) {
+      float f[4][8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] *= scale;
+      for (int q = 0; q < 4; ++q) {
+        const bool on = row >= 0 && j + 8 * q < p.r;
+        const float4* at = reinterpret_cast<const float4*>(p.planes + static_cast<size_t>(max(row, 0)) * p.r + j + 8 * q);
+        const float4 a = on ? at[0] : make_float4(0.f, 0.f, 0.f, 0.f), b = on ? at[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+        f[q][0] = a.x, f[q][1] = a.y, f[q][2] = a.z, f[q][3] = a.w, f[q][4] = b.x, f[q][5] = b.y, f[q][6] = b.z, f[q][7] = b.w;
       }
-      uint4 term[TERMS];
-      split_terms<TERMS>(f, term);
+      uint32_t t[TERMS][16];
 #pragma unroll
-      for (int z = 0; z < TERMS; ++z)
-        *reinterpret_cast<uint4*>(ring + STAGES * stage_bytes + ((z * BM + t) * pieces + (c ^ (swz * (t & 1)))) * 16) = term[z];
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[q][i] *= scale;
+        uint4 u[TERMS];
+        split_terms<TERMS>(f[q], u);
+#pragma unroll
+        for (int z = 0; z < TERMS; ++z) {
+          t[z][4 * q] = u[z].x;
+          t[z][4 * q + 1] = u[z].y;
+          t[z][4 * q + 2] = u[z].z;
+          t[z][4 * q + 3] = u[z].w;
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < TERMS; ++z) tmem_st_32x32b_x16(lanes + z * geom.kcols + j / 2, t[z]);
     }
-  } else {
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float f[8] = {};
-        if (row[h] >= 0 && 32 * u + 8 * tig < p.r) {
-          sum_planes(p, row[h], 32 * u + 8 * tig, f);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) f[q] *= scale;
-        }
-        split_terms<TERMS>(f, va[u][h]);
-      }
+    tc_wait_st();
   }
-  const int nb = 8 * (g >> 1) + (g & 1);
-  constexpr int NBLK = HIGH ? 1 : COLS / 32;  // 32-wide blocks a warp takes of a stage
-  for (int b = 0; b < blocks; ++b) {
-    cp_wait<STAGES - 2>();
-    __syncthreads();  // the stage (and v's terms) are there, and every warp is done with the one filled next
-    load(b + STAGES - 1);
-    const uint32_t stage = smem + static_cast<uint32_t>(b % STAGES) * stage_bytes;
-#pragma unroll
-    for (int q = 0; q < NBLK; ++q) {
-      const int w0 = 32 * (HIGH ? nw : q);  // first column of the warp's block in the stage
-      const uint32_t bat = stage + (w0 + nb) * rp * 2;
-      float acc[4][4] = {};
-      auto multiply = [&](int r0, const uint4 (&lo)[TERMS], const uint4 (&hi)[TERMS]) {
-        const uint32_t c = ((r0 / 8 + tig) ^ (swz * (g & 1))) << 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 col = lds16(bat + 2 * j * rp * 2 + c);
-#pragma unroll
-          for (int z = 0; z < TERMS; ++z) step32(acc[j], lo[z], hi[z], col);
-        }
-      };
-      if constexpr (HIGH) {
-        for (int r0 = 0; r0 < rp; r0 += 32) {
-          uint4 lo[TERMS], hi[TERMS];
-          const uint32_t c = ((r0 / 8 + tig) ^ (swz * (g & 1))) << 4;
-#pragma unroll
-          for (int z = 0; z < TERMS; ++z) {
-            lo[z] = lds16(terms_at + (z * BM + 16 * mw + g) * rp * 2 + c);
-            hi[z] = lds16(terms_at + (z * BM + 16 * mw + 8 + g) * rp * 2 + c);
-          }
-          multiply(r0, lo, hi);
-        }
-      } else {
-        multiply(0, va[0][0], va[0][1]);
-        if (rp > 32) multiply(32, va[1][0], va[1][1]);
-      }
-      const int n = c0 + b * COLS + w0 + 8 * tig;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (row[h] < 0 || n >= c1) continue;
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[2 * j] = acc[j][2 * h];
-          f[2 * j + 1] = acc[j][2 * h + 1];
-        }
-        uint4 w[W];
-        if (base) {
-          const int t = 16 * mw + 8 * h + g;
-#pragma unroll
-          for (int i = 0; i < W; ++i)
-            w[i] = lds16(stage + COLS * rp * 2 + t * Tile::kRow +
-                         (((W * (w0 / 8 + tig) + i) ^ ((W == 1 ? 4 : 1) * (t & 1))) << 4));
-        }
-        put8(y + static_cast<size_t>(row[h]) * p.N + n, f, base != nullptr, w);
+  const uint32_t idesc = make_idesc_bf16_f32(kWideRows, COLS, 0, 0);
+  for (int b = 0; b <= blocks; ++b) {
+    if (b < blocks) {
+      cp_wait<kWideStages - 2>();
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      __syncthreads();  // the stage (and, at first, v) is there, the sums' former block is finished
+      if (warp == 0) {
+        tc_fence_after_sync();
+        const uint32_t from = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t bd = make_smem_desc_sw128(ring_at + static_cast<uint32_t>(b % kWideStages) * stage_bytes, 16, 1024);
+        const uint32_t to = from + geom.sums() + (b & 1) * COLS;
+        for (int z = 0; z < TERMS; ++z)
+          for (int k = 0; k < geom.ksteps; ++k)
+            tc_mma_f16_ts_elect(to, from + z * geom.kcols + 8 * k,
+                                smem_desc_advance(bd, (k >> 2) * COLS * 128 + (k & 3) * 32), idesc, (z | k) != 0);
+        tc_commit_elect(&ctl.mma[b % kWideStages]);
+        __syncwarp();
       }
     }
+    if (b == 0) continue;
+    const int f = b - 1;  // the block that is finished now
+    wide_wait(&ctl, &ctl.mma[f % kWideStages], (f / kWideStages) & 1, p.err);
+    __syncwarp();
+    tc_fence_after_sync();
+    uint8_t* tile_at = ring + static_cast<size_t>(f % kWideStages) * stage_bytes + base_at;
+    uint8_t* mine = tile_at + (32 * quarter + lane) * 128;
+    constexpr int MINE = COLS / 2;  // columns
+    uint32_t v[MINE];
+    if constexpr (MINE == 32)
+      tmem_ld_32x32b_x32(lanes + geom.sums() + (f & 1) * COLS + MINE * half, v);
+    else
+      tmem_ld_32x32b_x16(lanes + geom.sums() + (f & 1) * COLS + MINE * half, v);
+    uint4 w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = base ? *reinterpret_cast<const uint4*>(mine + (((4 * half + q) ^ (lane & 7)) << 4)) : make_uint4(0u, 0u, 0u, 0u);
+    tc_wait_ld();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t u[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(Ty) == 2) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(
+              __uint_as_float(v[8 * q + 2 * i]) + __uint_as_float(u[i] << 16),
+              __uint_as_float(v[8 * q + 2 * i + 1]) + __uint_as_float(u[i] & 0xffff0000u));
+          u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          u[i] = __float_as_uint(__uint_as_float(v[4 * q + i]) + __uint_as_float(u[i]));
+        }
+      }
+      *reinterpret_cast<uint4*>(mine + (((4 * half + q) ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __syncwarp();
+    const int n = f * COLS;
+    const bool in = c0 + n + V * piece < c1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 out = *reinterpret_cast<const uint4*>(tile_at + wput + 1024 * i);
+      if (in && ybytes[i]) *reinterpret_cast<uint4*>(y + off[i] + n) = out;
+    }
+    __syncwarp();  // (the warp's part of the stage is filled again)
+    load();
   }
+  wide_end(tmem, geom.cols());
 }
 
 constexpr int kSms = 152;  // a constant: results must not depend on the device
@@ -709,24 +842,23 @@ constexpr int kSms = 152;  // a constant: results must not depend on the device
 // kernels for many rows to a tile (at least 32 rows an adapter on average).
 struct LoraPlan {
   bool scan, wide;
-  int tile_rows, tiles, slice_cols, slices, splits, chunk;
+  int tile_rows, tiles, slices, splits, chunk;
 };
 LoraPlan lora_plan(int T, int K, int N, int r, int n) {
   LoraPlan q{};
   q.scan = T <= kLoraScanRows;
   q.wide = !q.scan && T >= 32ll * n;
-  q.tile_rows = !q.wide ? 16 : r <= 64 ? 128 : 64;
+  q.tile_rows = q.wide ? kWideRows : 16;
   q.tiles = q.scan ? T : static_cast<int>(std::min<long long>(T, (T + q.tile_rows - 1ll) / q.tile_rows + n));
   // tiles with an adapter, about
   const long long tiles = std::max(1, q.scan ? std::min(T, n) : q.wide ? (T + q.tile_rows - 1) / q.tile_rows + n / 2 : q.tiles);
-  q.slice_cols = q.wide ? (r <= 16 ? 16 : r <= 32 ? 32 : 64) : kRankSlice;
-  q.slices = (r + q.slice_cols - 1) / q.slice_cols;
+  q.slices = q.wide ? 1 : (r + kRankSlice - 1) / kRankSlice;
   // two CTAs an SM; a step at least for each warp of a split, or four stages
   const int most = q.wide ? (K + 255) / 256 : (K + 32 * kLoraWarps - 1) / (32 * kLoraWarps);
   q.splits = static_cast<int>(std::max(1ll, std::min<long long>(2 * kSms / (tiles * q.slices), most)));
-  // wide: two CTAs an SM, of four blocks at least; else four CTAs an SM, a block of 32 columns at
-  // least for each warp
-  const int unit = q.wide ? 256 : 32 * kLoraWarps, units = (N + unit - 1) / unit;
+  if (q.wide) q.splits = std::min(q.splits, kMaxCluster);
+  // wide: two CTAs an SM; else four, a block of 32 columns at least for each warp
+  const int unit = q.wide ? 64 : 32 * kLoraWarps, units = (N + unit - 1) / unit;
   const int chunks = static_cast<int>(std::max(1ll, std::min<long long>((q.wide ? 2 : 4) * kSms / tiles, units)));
   q.chunk = (units + chunks - 1) / chunks * unit;
   return q;
@@ -737,19 +869,19 @@ struct LoraLayout {
 };
 LoraLayout lora_layout(const LoraPlan& q, int T, int r) {
   LoraLayout L{};
-  size_t cur = 0;
+  size_t cur = sizeof(ControlBlock);
   auto take = [&](size_t bytes) {
     const size_t o = cur;
     cur = (cur + bytes + 255) / 256 * 256;
     return o;
   };
-  L.planes = take(static_cast<size_t>(q.splits) * T * r * 4);
+  L.planes = take(static_cast<size_t>(q.wide ? 1 : q.splits) * T * r * 4);
   if (!q.scan) {
     L.order = take(static_cast<size_t>(T) * 4);
     L.tiles = take(static_cast<size_t>(q.tiles) * sizeof(LoraTile));
     L.ntiles = take(4);
   }
-  L.total = std::max<size_t>(cur, 256);
+  L.total = cur;
   return L;
 }
 
@@ -772,31 +904,31 @@ cudaError_t products(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStr
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int BM, int NT>
-cudaError_t shrink_wide(const LoraParams& p, const LoraPlan& q, cudaStream_t s) {
-  constexpr size_t smem = ShrinkTile<BM, NT>::kSmem;
-  const cudaError_t e = allow_smem(lora_shrink_wide_kernel<BM, NT>, smem);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(lora_shrink_wide_kernel<BM, NT>, dim3(q.tiles, p.splits * p.slices), dim3(kShrinkThreads), smem, s, p);
-}
-template <typename Ty, bool HIGH>
-cudaError_t expand_wide(const LoraParams& p, const LoraPlan& q, cudaStream_t s) {
-  const size_t smem = ExpandTile<Ty, HIGH>::smem((p.r + 31) / 32 * 32);
-  const cudaError_t e = allow_smem(lora_expand_wide_kernel<Ty, HIGH>, smem);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(lora_expand_wide_kernel<Ty, HIGH>, dim3(q.tiles, (p.N + p.chunk - 1) / p.chunk), dim3(kExpandThreads),
-                       smem, s, p);
-}
 cudaError_t products_wide(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStream_t s) {
-  cudaError_t e = p.r > 64    ? shrink_wide<64, 4>(p, q, s)
-                  : p.r > 32  ? shrink_wide<128, 8>(p, q, s)
-                  : p.r > 16  ? shrink_wide<128, 4>(p, q, s)
-                              : shrink_wide<128, 2>(p, q, s);
+  const size_t shrink = ShrinkGeom(p.r).smem();
+  cudaError_t e = allow_smem(lora_shrink_wide_kernel, shrink);
   if (e != cudaSuccess) return e;
-  if (p.r > 64)
-    e = y_f32 ? expand_wide<float, true>(p, q, s) : expand_wide<__nv_bfloat16, true>(p, q, s);
-  else
-    e = y_f32 ? expand_wide<float, false>(p, q, s) : expand_wide<__nv_bfloat16, false>(p, q, s);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = p.splits;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = g_pdl ? 1 : 0;
+  cfg.gridDim = dim3(q.tiles, p.splits);
+  cfg.blockDim = dim3(kWideThreads);
+  cfg.dynamicSmemBytes = shrink;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, lora_shrink_wide_kernel, p);
+  if (e != cudaSuccess) return e;
+  auto kern = y_f32 ? lora_expand_wide_kernel<float> : lora_expand_wide_kernel<__nv_bfloat16>;
+  const size_t expand = y_f32 ? ExpandGeom<float>(p.r).smem() : ExpandGeom<__nv_bfloat16>(p.r).smem();
+  e = allow_smem(kern, expand);
+  if (e == cudaSuccess)
+    e = launch_kernel(kern, dim3(q.tiles, (p.N + p.chunk - 1) / p.chunk), dim3(kWideThreads), expand, s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -822,6 +954,7 @@ cudaError_t launch_lora(int T, int K, int N, int r, int n, const void* x, const 
   p.order = reinterpret_cast<int32_t*>(ws + L.order);
   p.tiles = reinterpret_cast<LoraTile*>(ws + L.tiles);
   p.ntiles = reinterpret_cast<int32_t*>(ws + L.ntiles);
+  p.err = &reinterpret_cast<ControlBlock*>(ws)->err;
   p.T = T;
   p.K = K;
   p.N = N;
