@@ -406,29 +406,49 @@ def moe_block(cfg, gate, x, residual, norm_weight, eps, Wg, logit_bias, select_b
         _ptr(sum_out), _ptr(y), _ptr(out), wp, wb, _stream(stream)))
 
 
+def _on_current_device(t) -> int:
+    """Index of t's device, where the kernels are launched (the current one)."""
+    import torch
+
+    device = t.get_device()
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError("tensor arguments must live on the current CUDA device")
+    return device
+
+
+def _address(t, device: int) -> int:
+    """t's address; t is contiguous and lives on that device."""
+    if t.get_device() != device:
+        raise ValueError("tensor arguments must live on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return t.data_ptr()
+
+
 def moe_add_rms_norm(rows: int, D: int, x, residual, weight, eps: float, sum_out, y, q=None, q_scales=None,
                      q_group: int = 0, stream=None) -> None:
     """sum_out = x + residual and its root-mean-square norm times weight, as y (x's type) and / or as e4m3 rows q
     with a scale per row (q_group 0) or per q_group values; None for what is not there or not wanted."""
-    dt = _float_dtype(x)
-    try:  # (in one expression: a small batch takes little longer than its call)
-        n, t = rows * D, x.dtype
-        nb = n * x.itemsize
-        fits = (x.nbytes >= nb and weight.nbytes >= D * x.itemsize and weight.dtype == t
-                and (residual is None or residual.nbytes >= nb and residual.dtype == t)
-                and (sum_out is None or sum_out.nbytes >= nb and sum_out.dtype == t)
-                and (y is None or y.nbytes >= nb and y.dtype == t)
-                and (q is None or q.itemsize == 1 and q.nbytes >= n)
-                and (q_scales is None or q_scales.nbytes >= 4 * rows * (D // q_group if q_group > 0 else 1)
-                     and q_scales.itemsize == 4 and q_scales.is_floating_point()))
-    except AttributeError:
-        fits = False
-    if not fits:
-        raise ValueError("moe_add_rms_norm takes x, residual, sum_out and y [rows, D] and weight [D] of one type, "
-                         "one-byte q [rows, D] and fp32 scales [rows, D / q_group]")
-    _check("moe_add_rms_norm", load_library().moe_add_rms_norm(
-        rows, D, dt, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(sum_out), _ptr(y), _ptr(q), q_group,
-        _ptr(q_scales), _stream(stream)))
+    # (a small batch takes little longer than its call: no loops, each attribute looked up once)
+    t, dt = x.dtype, _float_dtype(x)
+    nb = rows * D * (4 if dt == MOE_F32 else 2)
+    if (dt < 0 or x.nbytes < nb or weight.dtype is not t or rows > 0 and weight.numel() < D
+            or residual is not None and (residual.dtype is not t or residual.nbytes < nb)
+            or sum_out is not None and (sum_out.dtype is not t or sum_out.nbytes < nb)
+            or y is not None and (y.dtype is not t or y.nbytes < nb)
+            or q is not None and (q.itemsize != 1 or q.nbytes < rows * D)
+            or q_scales is not None and (_float_dtype(q_scales) != MOE_F32
+                                         or q_scales.numel() < rows * (D // q_group if q_group > 0 else 1))):
+        raise ValueError("moe_add_rms_norm takes x, residual, sum_out and y [rows, D] and weight [D] of one type (bf16 "
+                         "or fp32), one-byte q [rows, D] and fp32 scales [rows, D / q_group]")
+    device = _on_current_device(x)
+    st = load_library().moe_add_rms_norm(
+        rows, D, dt, _address(x, device), None if residual is None else _address(residual, device),
+        _address(weight, device), eps, None if sum_out is None else _address(sum_out, device),
+        None if y is None else _address(y, device), None if q is None else _address(q, device), q_group,
+        None if q_scales is None else _address(q_scales, device), _stream(stream))
+    if st:
+        _check("moe_add_rms_norm", st)
 
 
 def moe_lora_workspace_size(T: int, K: int, N: int, r: int, n: int) -> int:
@@ -438,23 +458,24 @@ def moe_lora_workspace_size(T: int, K: int, N: int, r: int, n: int) -> int:
 def moe_lora(T: int, K: int, N: int, r: int, n: int, x, ids, A, B, scales, base, y, ws, stream=None) -> None:
     """y [T, N] (bf16 or fp32) = base (None: 0; y: in place) + scales[a] x A[a]^T B[a]^T with a = ids[t] of each row
     (outside [0, n): no adapter); x [T, K], A [n, r, K] and B [n, N, r] bf16, scales [n] fp32 or None."""
-    y_dtype = _float_dtype(y)
-    try:
-        fits = (x.nbytes >= 2 * T * K and A.nbytes >= 2 * n * r * K and B.nbytes >= 2 * n * N * r
-                and _float_dtype(x) == _float_dtype(A) == _float_dtype(B) == MOE_BF16
-                and ids.nbytes >= 4 * T and ids.itemsize == 4 and not ids.is_floating_point()
-                and y.nbytes >= (4 if y_dtype == MOE_F32 else 2) * T * N
-                and (scales is None or scales.nbytes >= 4 * n and _float_dtype(scales) == MOE_F32)
-                and (base is None or base.dtype == y.dtype and base.nbytes >= y.itemsize * T * N))
-    except AttributeError:
-        fits = False
-    if not fits:
+    t, y_dtype, yt = x.dtype, _float_dtype(y), y.dtype
+    yb = T * N * (4 if y_dtype == MOE_F32 else 2)
+    if (_float_dtype(x) != MOE_BF16 or A.dtype is not t or B.dtype is not t or x.nbytes < 2 * T * K
+            or A.nbytes < 2 * n * r * K or B.nbytes < 2 * n * N * r or y_dtype < 0 or y.nbytes < yb
+            or ids.itemsize != 4 or ids.nbytes < 4 * T or ids.is_floating_point()
+            or scales is not None and (_float_dtype(scales) != MOE_F32 or scales.nbytes < 4 * n)
+            or base is not None and base is not y and (base.dtype is not yt or base.nbytes < yb)):
         raise ValueError("moe_lora takes bf16 x [T, K], A [n, r, K] and B [n, N, r], int32 ids [T], fp32 scales [n], "
                          "y [T, N] and a base of y's type")
-    wp, wb = _ws(ws)
-    _check("moe_lora", load_library().moe_lora(
-        T, K, N, r, n, _ptr(x), _ptr(ids), _ptr(A), _ptr(B), _ptr(scales), _ptr(base), _ptr(y), y_dtype, wp, wb,
-        _stream(stream)))
+    device = _on_current_device(x)
+    to = _address(y, device)
+    st = load_library().moe_lora(
+        T, K, N, r, n, _address(x, device), _address(ids, device), _address(A, device), _address(B, device),
+        None if scales is None else _address(scales, device),
+        None if base is None else to if base is y else _address(base, device), to, y_dtype, _address(ws, device),
+        ws.nbytes, _stream(stream))
+    if st:
+        _check("moe_lora", st)
 
 
 def moe_pack_weights_nk(W, G: int, K: int, N: int, W_nk, stream=None) -> None:

@@ -9,37 +9,28 @@
 namespace moe {
 namespace {
 
-// v = the nsplit partial planes [nsplit, T, E] of the token's logits, added in order.
+// v += a plane's row of logits (EPL neighbouring experts of this lane).
 template <int EPL>
-__device__ __forceinline__ void load_logits(const float* __restrict__ planes, int nsplit, size_t plane, int lane,
-                                            int E, bool vec, float (&v)[EPL]) {
+__device__ __forceinline__ void add_logits(const float* __restrict__ row, int lane, int E, bool vec, float (&v)[EPL]) {
   const int e0 = lane * EPL;
+  if (vec) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) v[i] = 0.0f;
-  for (int s = 0; s < nsplit; ++s) {
-    const float* row = planes + s * plane;
-    float p[EPL];
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < EPL; i += 4) {
-        const float4 f = e0 + i < E ? *reinterpret_cast<const float4*>(row + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        p[i] = f.x;
-        p[i + 1] = f.y;
-        p[i + 2] = f.z;
-        p[i + 3] = f.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) p[i] = e0 + i < E ? row[e0 + i] : 0.0f;
+    for (int i = 0; i < EPL; i += 4) {
+      const float4 f = e0 + i < E ? *reinterpret_cast<const float4*>(row + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[i] += f.x;
+      v[i + 1] += f.y;
+      v[i + 2] += f.z;
+      v[i + 3] += f.w;
     }
+  } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) v[i] = s ? v[i] + p[i] : p[i];
+    for (int i = 0; i < EPL; ++i) v[i] += e0 + i < E ? row[e0 + i] : 0.0f;
   }
 }
 
 constexpr int kGateWarps = 8;
 
-template <int EPL, bool WHOLE>
+template <int EPL, bool WHOLE, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kGateWarps * 32)
     gate_kernel(const float* __restrict__ planes, int nsplit, const float* __restrict__ logit_bias,
                 const float* __restrict__ select_bias, float* logits, int T, bool vec, const GateParams g,
@@ -50,11 +41,19 @@ __global__ void __launch_bounds__(kGateWarps * 32)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long t = static_cast<long long>(blockIdx.x) * kGateWarps + warp;
   if (t >= T) return;
-  float v[EPL];
-  load_logits<EPL>(planes + t * g.E, nsplit, static_cast<size_t>(T) * g.E, lane, g.E, vec, v);
-  warp_gate_topk<EPL, WHOLE>(v, lane, g, logit_bias, select_bias,
-                             (nsplit > 1 || logit_bias) ? logits + t * g.E : nullptr, ids + t * g.k, w + t * g.k,
-                             scratch[warp], err);
+  float v[EPL] = {};
+  const size_t at = static_cast<size_t>(t) * g.E;
+  add_logits<EPL>(planes + at, lane, g.E, vec, v);
+  for (int s = 1; s < nsplit; ++s) add_logits<EPL>(planes + s * (static_cast<size_t>(T) * g.E) + at, lane, g.E, vec, v);
+  warp_gate_topk<EPL, WHOLE, SIGMOID, BIAS>(v, lane, g, logit_bias, select_bias,
+                                            (nsplit > 1 || logit_bias) ? logits + at : nullptr, ids + t * g.k,
+                                            w + t * g.k, scratch[warp], err);
+}
+
+template <int EPL, bool WHOLE>
+auto gate_kernel_of(bool sigmoid, bool bias) {
+  return sigmoid ? (bias ? gate_kernel<EPL, WHOLE, true, true> : gate_kernel<EPL, WHOLE, true, false>)
+                 : (bias ? gate_kernel<EPL, WHOLE, false, true> : gate_kernel<EPL, WHOLE, false, false>);
 }
 
 }  // namespace
@@ -65,9 +64,10 @@ cudaError_t launch_gate(const float* planes, int nsplit, const float* logit_bias
   if (T <= 0) return cudaSuccess;
   const int blocks = (T + kGateWarps - 1) / kGateWarps;
   const bool vec = g.E % 4 == 0 && !(reinterpret_cast<uintptr_t>(planes) & 15);
-  auto kern = g.E <= 128   ? (g.E % 4 ? gate_kernel<4, false> : gate_kernel<4, true>)
-              : g.E <= 256 ? (g.E % 8 ? gate_kernel<8, false> : gate_kernel<8, true>)
-                           : (g.E % 16 ? gate_kernel<16, false> : gate_kernel<16, true>);
+  const bool sg = g.sigmoid, sb = select_bias != nullptr;
+  auto kern = g.E <= 128   ? (g.E % 4 ? gate_kernel_of<4, false>(sg, sb) : gate_kernel_of<4, true>(sg, sb))
+              : g.E <= 256 ? (g.E % 8 ? gate_kernel_of<8, false>(sg, sb) : gate_kernel_of<8, true>(sg, sb))
+                           : (g.E % 16 ? gate_kernel_of<16, false>(sg, sb) : gate_kernel_of<16, true>(sg, sb));
   const cudaError_t e = launch_kernel(kern, dim3(blocks), dim3(kGateWarps * 32), 0, s, planes, nsplit, logit_bias,
                                       select_bias, logits, T, vec, g, ids, w, err);
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -18,7 +18,11 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
 __device__ __forceinline__ float ordered_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
-__device__ __forceinline__ float gate_sigmoid(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+__device__ __forceinline__ float gate_sigmoid(float x) {
+  float r;  // (of 1 to infinity)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-x)));
+  return r;
+}
 
 // (a, b) becomes the two largest of a >= b and c >= d.
 __device__ __forceinline__ void merge_top2(uint32_t& a, uint32_t& b, uint32_t c, uint32_t d) {
@@ -59,6 +63,7 @@ __device__ __forceinline__ void put_lane(uint32_t* to, const uint32_t (&s)[EPL])
 // index comes first.  Writes the final logits to logits_row (when given), ids_row and
 // w_row [k]; returns ids_row[lane] on lanes below k <= 16, -1 on the others.
 //   WHOLE    E is a multiple of EPL: a lane has all its entries or none.
+//   SIGMOID, BIAS  as g.sigmoid and select_bias say (no branch an entry on them).
 //   scratch  32 EPL words of the warp's own in shared memory, 16-byte aligned.
 //
 // Bound by instructions, most of them on the half-rate integer pipe, so each lane sorts
@@ -67,27 +72,29 @@ __device__ __forceinline__ void put_lane(uint32_t* to, const uint32_t (&s)[EPL])
 // chosen key is, is found once at the end, by k lanes at a time.  A group's value comes from
 // the sorted keys of the lanes that hold it (the group's size a multiple of EPL, a power of
 // two lanes), else group after group.
-template <int EPL, bool WHOLE>
+template <int EPL, bool WHOLE, bool SIGMOID, bool BIAS>
 __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const GateParams& g,
                                               const float* __restrict__ logit_bias,
                                               const float* __restrict__ select_bias, float* logits_row,
                                               int32_t* __restrict__ ids_row, float* __restrict__ w_row,
                                               uint32_t* scratch, int32_t* err) {
+  const bool bias_vec = !(reinterpret_cast<uintptr_t>(select_bias) & 15);
   constexpr unsigned kFull = 0xffffffffu;
   const int e0 = lane * EPL, E = g.E, k = g.k;
   auto has = [&](int i) { return WHOLE ? e0 < E : e0 + i < E; };
   uint32_t* mine = scratch + e0;
   bool bad = false;
   {
-    uint32_t most = 0u;
+    float zero = 0.0f;  // NaN once an entry is not finite
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      if (!has(i)) v[i] = -INFINITY;
+      if (!has(i)) v[i] = 0.0f;
       if (logit_bias && has(i)) v[i] += logit_bias[e0 + i];
       if (logits_row && has(i)) logits_row[e0 + i] = v[i];
-      if (has(i)) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+      zero = fmaf(v[i], 0.0f, zero);
+      if (!has(i)) v[i] = -INFINITY;
     }
-    if (most >= 0x7f800000u) {
+    if (!(zero == 0.0f)) {
       bad = true;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
@@ -97,9 +104,9 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
   const bool grouped = g.topk_group < g.n_group;
   // softmax over all experts: its largest logit and the inverse of its sum, where the
   // scores themselves are needed (renormalised weights need only those chosen)
-  const bool scores = select_bias || (grouped && g.top2) || !g.renorm;
+  const bool scores = BIAS || (grouped && g.top2) || !g.renorm;
   float m = 0.0f, rz = 1.0f;
-  if (!g.sigmoid && scores) {
+  if (!SIGMOID && scores) {
     m = v[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
@@ -112,19 +119,28 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
     rz = z > 0.0f ? 1.0f / z : 0.0f;
   }
-  auto score = [&](float x) { return g.sigmoid ? gate_sigmoid(x) : expf(x - m) * rz; };
+  auto score = [&](float x) { return SIGMOID ? gate_sigmoid(x) : expf(x - m) * rz; };
   // keys of what is compared, the biased score or the logit; 0: not to be chosen (below
   // every value's key, -infinity's too)
   uint32_t key[EPL];
-  if (select_bias) {
-    float c[EPL];
-    uint32_t most = 0u;
+  if (BIAS) {
+    float c[EPL], zero = 0.0f;
+    if (WHOLE && EPL % 4 == 0 && bias_vec) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += 4) {
+        const float4 f = e0 < E ? *reinterpret_cast<const float4*>(select_bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        c[i] = f.x, c[i + 1] = f.y, c[i + 2] = f.z, c[i + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = has(i) ? select_bias[e0 + i] : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      c[i] = has(i) ? score(v[i]) + select_bias[e0 + i] : 0.0f;
-      most = max(most, __float_as_uint(c[i]) & 0x7fffffffu);
+      c[i] += score(v[i]);
+      zero = fmaf(c[i], 0.0f, zero);
     }
-    if (bad || most >= 0x7f800000u) {
+    if (bad || !(zero == 0.0f)) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         bad |= !isfinite(c[i]);
@@ -144,7 +160,7 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     const float a = ordered_value(ka), b = ordered_value(kb);
     if (!g.top2 || a == -INFINITY) return ka;
     const bool two = kb != 0u && b != -INFINITY;
-    if (select_bias) return ordered_key(two ? a + b : a);
+    if (BIAS) return ordered_key(two ? a + b : a);
     return ordered_key(score(a) + (two ? score(b) : 0.0f));
   };
   const int size = grouped ? E / g.n_group : E, lanes = size / EPL;
@@ -231,7 +247,7 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
       if (theirs[i] == my_key && skip-- == 0) idx = i;
   }
   float my_x = ordered_value(my_key);  // logit of lane j's choice
-  if (select_bias) {
+  if (BIAS) {
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = __float_as_uint(v[i]);
@@ -247,7 +263,7 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
   } else {
     // (a softmax's first choice, where its scores were not needed, is its largest logit)
     const float first = __shfl_sync(kFull, my_x, 0);
-    float p = g.sigmoid || scores ? score(my_x) : expf(my_x - (first == -INFINITY ? 0.0f : first));
+    float p = SIGMOID || scores ? score(my_x) : expf(my_x - (first == -INFINITY ? 0.0f : first));
     if (lane >= k) p = 0.0f;
     float z = p;
 #pragma unroll

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "moe_internal.h"
 #include "sm103_ptx.cuh"
@@ -885,11 +886,16 @@ LoraLayout lora_layout(const LoraPlan& q, int T, int r) {
   return L;
 }
 
-// More shared memory than a launch gets unasked.
-template <typename Kernel>
-cudaError_t allow_smem(Kernel* kern, size_t bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+// Once a kernel and device: all the shared memory that any of its launches takes.
+template <auto KERNEL>
+cudaError_t allow_smem(size_t most) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return e;
 }
 
 template <bool SCAN>
@@ -904,9 +910,15 @@ cudaError_t products(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStr
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <typename Ty>
+cudaError_t expand_wide(const LoraParams& p, dim3 grid, cudaStream_t s) {
+  const cudaError_t e = allow_smem<lora_expand_wide_kernel<Ty>>(ExpandGeom<Ty>(kLoraMaxRank).smem());
+  if (e != cudaSuccess) return e;
+  return launch_kernel(lora_expand_wide_kernel<Ty>, grid, dim3(kWideThreads), ExpandGeom<Ty>(p.r).smem(), s, p);
+}
 cudaError_t products_wide(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStream_t s) {
   const size_t shrink = ShrinkGeom(p.r).smem();
-  cudaError_t e = allow_smem(lora_shrink_wide_kernel, shrink);
+  cudaError_t e = allow_smem<lora_shrink_wide_kernel>(ShrinkGeom(kLoraMaxRank).smem());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -924,11 +936,8 @@ cudaError_t products_wide(const LoraParams& p, const LoraPlan& q, bool y_f32, cu
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, lora_shrink_wide_kernel, p);
   if (e != cudaSuccess) return e;
-  auto kern = y_f32 ? lora_expand_wide_kernel<float> : lora_expand_wide_kernel<__nv_bfloat16>;
-  const size_t expand = y_f32 ? ExpandGeom<float>(p.r).smem() : ExpandGeom<__nv_bfloat16>(p.r).smem();
-  e = allow_smem(kern, expand);
-  if (e == cudaSuccess)
-    e = launch_kernel(kern, dim3(q.tiles, (p.N + p.chunk - 1) / p.chunk), dim3(kWideThreads), expand, s, p);
+  const dim3 grid(q.tiles, (p.N + p.chunk - 1) / p.chunk);
+  e = y_f32 ? expand_wide<float>(p, grid, s) : expand_wide<__nv_bfloat16>(p, grid, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -965,7 +974,7 @@ cudaError_t launch_lora(int T, int K, int N, int r, int n, const void* x, const 
   p.chunk = q.chunk;
   if (q.scan) return products<true>(p, q, y_f32, s);
   const size_t smem = static_cast<size_t>(n + 1) * 4;
-  cudaError_t e = allow_smem(lora_plan_kernel, smem);
+  cudaError_t e = allow_smem<lora_plan_kernel>(static_cast<size_t>(kLoraMaxAdapters + 1) * 4);
   if (e == cudaSuccess) e = launch_kernel(lora_plan_kernel, dim3(1), dim3(1024), smem, s, p, q.tile_rows);
   if (e != cudaSuccess) return e;
   return q.wide ? products_wide(p, q, y_f32, s) : products<false>(p, q, y_f32, s);

@@ -298,13 +298,20 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     int32_t* ids_row = p.ids + static_cast<size_t>(t) * p.k;
     float* w_row = p.w + static_cast<size_t>(t) * p.k;
     int id;
-    if constexpr (GATED)
+    if constexpr (GATED) {
       // (E is a multiple of 8)
-      id = warp_gate_topk<EPL, (EPL <= 8)>(v, lane, p.gate, p.bias, p.select_bias, logits_row, ids_row, w_row,
-                                           reinterpret_cast<uint32_t*>(base + RtCfg<NB>::kRedBytes) + warp * 32 * EPL,
-                                           p.err);
-    else
+      auto choose = [&](auto sigmoid, auto bias) {
+        return warp_gate_topk<EPL, (EPL <= 8), decltype(sigmoid)::value, decltype(bias)::value>(
+            v, lane, p.gate, p.bias, p.select_bias, logits_row, ids_row, w_row,
+            reinterpret_cast<uint32_t*>(base + RtCfg<NB>::kRedBytes) + warp * 32 * EPL, p.err);
+      };
+      using Yes = std::true_type;
+      using No = std::false_type;
+      id = p.gate.sigmoid ? (p.select_bias ? choose(Yes(), Yes()) : choose(Yes(), No()))
+                          : (p.select_bias ? choose(No(), Yes()) : choose(No(), No()));
+    } else {
       id = warp_topk_softmax<EPL>(v, lane, p.E, p.k, p.renorm, p.bias, logits_row, ids_row, w_row, p.err);
+    }
     if (id >= 0) atomicAdd(&hist[id], 1);
   }
   if (p.chunk_hist) {
