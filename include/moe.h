@@ -454,6 +454,15 @@ int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, co
               const float* s2, const void* W13s, const float* s13s, const void* W2s, const float* s2s,
               void* sum_out, void* y, void* out, void* ws, size_t ws_bytes, void* stream);
 
+/* One of the calls above with its arguments in a block of 8-byte words, in their
+ * order: integers and addresses (0: NULL) as they are, eps as a double.  For bindings
+ * that take longer for a call the more arguments it has; same results and errors,
+ * MOE_ERR_INVALID_ARG for another call or NULL words. */
+#define MOE_CALL_ADD_RMS_NORM 0
+#define MOE_CALL_ROUTE_GATED 1
+#define MOE_CALL_LORA 2
+int moe_call(int32_t call, const void* words);
+
 /* Device byte offsets inside `ws` where moe_layer keeps its intermediates,
  * for inspection (logits, ids, weights, counts, offsets, sorted_rows, dest,
  * x_perm, h, y_perm, h_s, s).  `which` is one of the MOE_WS_* indices;

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Optional
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -94,7 +95,11 @@ _SIGS = {
     "moe_lora": (ctypes.c_int, [ctypes.c_int32] * 5 + [_P] * 7 + [ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "moe_block": (ctypes.c_int, [ctypes.POINTER(MoEConfig), ctypes.POINTER(MoEGate)] + [_P] * 3 + [ctypes.c_float] +
                   [_P] * 14 + [_P, ctypes.c_size_t, _P]),
+    "moe_call": (ctypes.c_int, [ctypes.c_int32, ctypes.c_char_p]),
 }
+# moe_call's calls and the words of their arguments
+_NORM, _ROUTE_GATED, _LORA = 0, 1, 2
+_NORM_WORDS, _ROUTE_GATED_WORDS, _LORA_WORDS = (struct.Struct(f).pack for f in ("=6qd6q", "=12q", "=16q"))
 MOE_OPT_PAIR_TILES = 1
 MOE_OPT_GATHER_A = 2
 MOE_OPT_DECODE_KERNEL = 3
@@ -194,6 +199,38 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _first_launch(t, stream):
+    """Finds torch's way to the current device and its stream, once."""
+    global _launch
+    import torch
+
+    device_of, raw = torch._C._cuda_getDevice, getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+    def launch(t, stream):
+        device = t.get_device()
+        if device < 0 or device != device_of():
+            raise ValueError("tensor arguments must live on the current CUDA device")
+        return device, raw(device) if stream is None and raw else _stream(stream) or 0
+
+    _launch = launch
+    return launch(t, stream)
+
+
+# (device, stream) of a call on tensor t: the current device, on which the kernels are launched, is t's
+_launch = _first_launch
+
+
+def _address(t, device: int):
+    """t's address (None: 0); t is contiguous and lives on that device."""
+    if t is None:
+        return 0
+    if t.get_device() != device:
+        raise ValueError("tensor arguments must live on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return t.data_ptr()
 
 
 def _ws(ws):
@@ -384,45 +421,46 @@ def dequantize_w4(Wq, scales, zeros=None, stream=None):
     return W
 
 
-def _gate(gate):
-    return None if gate is None else ctypes.byref(gate)
+def _f32(t, n: int) -> bool:
+    """t is None or n fp32 values."""
+    return t is None or t.nbytes >= 4 * n and _FLOAT_DTYPES.get(t.dtype) == MOE_F32
 
 
 def moe_route_gated(cfg, gate, x, Wg, logit_bias, select_bias, logits, topk_ids, topk_w, ws, stream=None):
     """moe_route with softmax or sigmoid scores, a bias for the choice, groups and a factor (make_gate)."""
-    wp, wb = _ws(ws)
-    _check("moe_route_gated", load_library().moe_route_gated(
-        ctypes.byref(cfg), _gate(gate), _ptr(x), _ptr(Wg), _ptr(logit_bias), _ptr(select_bias), _ptr(logits),
-        _ptr(topk_ids), _ptr(topk_w), wp, wb, _stream(stream)))
+    T, E, n = cfg.T, cfg.E, cfg.T * cfg.k
+    dt = _float_dtype(logits)
+    if (dt != MOE_F32 or logits.nbytes < 4 * T * E or not _f32(topk_w, n) or topk_ids.nbytes < 4 * n
+            or topk_ids.itemsize != 4 or topk_ids.is_floating_point() or not _f32(logit_bias, E)
+            or not _f32(select_bias, E)
+            or x is not None and (_float_dtype(x) != cfg.act_dtype or x.numel() < T * cfg.D or Wg.dtype is not x.dtype
+                                  or Wg.numel() < cfg.D * E)):
+        raise ValueError("moe_route_gated takes fp32 logits [T, E], weights [T, k] and biases [E], int32 ids [T, k], "
+                         "and x [T, D] and Wg [D, E] of act_dtype")
+    device, s = _launch(logits, stream)
+    st = load_library().moe_call(_ROUTE_GATED, _ROUTE_GATED_WORDS(
+        ctypes.addressof(cfg), 0 if gate is None else ctypes.addressof(gate), _address(x, device), _address(Wg, device),
+        _address(logit_bias, device), _address(select_bias, device), _address(logits, device), _address(topk_ids, device),
+        _address(topk_w, device), _address(ws, device), ws.nbytes, s))
+    if st:
+        _check("moe_route_gated", st)
 
 
 def moe_block(cfg, gate, x, residual, norm_weight, eps, Wg, logit_bias, select_bias, W13, s13, W2, s2, W13s, s13s,
               W2s, s2s, sum_out, y, out, ws, stream=None):
     """moe_add_rms_norm (norm_weight None: no norm), then moe_layer with the gate's choice (None: softmax top-k)."""
-    wp, wb = _ws(ws)
+    dt, n = x.dtype, cfg.T * cfg.D
+    if (_float_dtype(x) != cfg.act_dtype or any(t is not None and (t.dtype is not dt or t.numel() < m) for t, m in
+                                                ((x, n), (residual, n), (sum_out, n), (y, n), (out, n),
+                                                 (norm_weight, cfg.D), (Wg, cfg.D * cfg.E)))
+            or not _f32(logit_bias, cfg.E) or not _f32(select_bias, cfg.E)):
+        raise ValueError("moe_block takes x, residual, sum_out, y and out [T, D], norm_weight [D] and Wg [D, E] of "
+                         "act_dtype and fp32 biases [E]")
+    device, s = _launch(x, stream)
+    a = [_address(t, device) for t in (x, residual, norm_weight, Wg, logit_bias, select_bias, W13, s13, W2, s2, W13s, s13s,
+                                       W2s, s2s, sum_out, y, out, ws)]
     _check("moe_block", load_library().moe_block(
-        ctypes.byref(cfg), _gate(gate), _ptr(x), _ptr(residual), _ptr(norm_weight), eps, _ptr(Wg), _ptr(logit_bias),
-        _ptr(select_bias), _ptr(W13), _ptr(s13), _ptr(W2), _ptr(s2), _ptr(W13s), _ptr(s13s), _ptr(W2s), _ptr(s2s),
-        _ptr(sum_out), _ptr(y), _ptr(out), wp, wb, _stream(stream)))
-
-
-def _on_current_device(t) -> int:
-    """Index of t's device, where the kernels are launched (the current one)."""
-    import torch
-
-    device = t.get_device()
-    if device < 0 or device != torch.cuda.current_device():
-        raise ValueError("tensor arguments must live on the current CUDA device")
-    return device
-
-
-def _address(t, device: int) -> int:
-    """t's address; t is contiguous and lives on that device."""
-    if t.get_device() != device:
-        raise ValueError("tensor arguments must live on the current CUDA device")
-    if not t.is_contiguous():
-        raise ValueError("tensor arguments must be contiguous")
-    return t.data_ptr()
+        ctypes.byref(cfg), None if gate is None else ctypes.byref(gate), *a[:3], eps, *a[3:], ws.nbytes, s))
 
 
 def moe_add_rms_norm(rows: int, D: int, x, residual, weight, eps: float, sum_out, y, q=None, q_scales=None,
@@ -441,12 +479,10 @@ def moe_add_rms_norm(rows: int, D: int, x, residual, weight, eps: float, sum_out
                                          or q_scales.numel() < rows * (D // q_group if q_group > 0 else 1))):
         raise ValueError("moe_add_rms_norm takes x, residual, sum_out and y [rows, D] and weight [D] of one type (bf16 "
                          "or fp32), one-byte q [rows, D] and fp32 scales [rows, D / q_group]")
-    device = _on_current_device(x)
-    st = load_library().moe_add_rms_norm(
-        rows, D, dt, _address(x, device), None if residual is None else _address(residual, device),
-        _address(weight, device), eps, None if sum_out is None else _address(sum_out, device),
-        None if y is None else _address(y, device), None if q is None else _address(q, device), q_group,
-        None if q_scales is None else _address(q_scales, device), _stream(stream))
+    device, s = _launch(x, stream)
+    st = load_library().moe_call(_NORM, _NORM_WORDS(
+        rows, D, dt, _address(x, device), _address(residual, device), _address(weight, device), eps,
+        _address(sum_out, device), _address(y, device), _address(q, device), q_group, _address(q_scales, device), s))
     if st:
         _check("moe_add_rms_norm", st)
 
@@ -467,13 +503,12 @@ def moe_lora(T: int, K: int, N: int, r: int, n: int, x, ids, A, B, scales, base,
             or base is not None and base is not y and (base.dtype is not yt or base.nbytes < yb)):
         raise ValueError("moe_lora takes bf16 x [T, K], A [n, r, K] and B [n, N, r], int32 ids [T], fp32 scales [n], "
                          "y [T, N] and a base of y's type")
-    device = _on_current_device(x)
+    device, s = _launch(x, stream)
     to = _address(y, device)
-    st = load_library().moe_lora(
+    st = load_library().moe_call(_LORA, _LORA_WORDS(
         T, K, N, r, n, _address(x, device), _address(ids, device), _address(A, device), _address(B, device),
-        None if scales is None else _address(scales, device),
-        None if base is None else to if base is y else _address(base, device), to, y_dtype, _address(ws, device),
-        ws.nbytes, _stream(stream))
+        _address(scales, device), to if base is y else _address(base, device), to, y_dtype, _address(ws, device),
+        ws.nbytes, s))
     if st:
         _check("moe_lora", st)
 

@@ -1,9 +1,10 @@
 // C ABI of the operators around the experts that need no configuration (include/moe.h):
-// moe_add_rms_norm, moe_lora.
+// moe_add_rms_norm, moe_lora; and moe_call.
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "moe_internal.h"
 
@@ -61,6 +62,59 @@ int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* 
   const cudaError_t e = launch_lora(T, K, N, r, n, x, ids, A, B, scales, base, y, y_dtype == MOE_F32,
                                     static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_call(int32_t call, const void* words) {
+  if (!words) return MOE_ERR_INVALID_ARG;
+  const char* at = static_cast<const char*>(words);
+  auto word = [&]() {
+    int64_t v;
+    std::memcpy(&v, at, sizeof(v));
+    at += sizeof(v);
+    return v;
+  };
+  auto i32 = [&]() { return static_cast<int32_t>(word()); };
+  auto ptr = [&]() { return reinterpret_cast<void*>(word()); };
+  switch (call) {
+    case MOE_CALL_ADD_RMS_NORM: {
+      const int32_t rows = i32(), D = i32(), dtype = i32();
+      const void *x = ptr(), *residual = ptr(), *weight = ptr();
+      double eps;
+      std::memcpy(&eps, at, sizeof(eps));
+      at += sizeof(eps);
+      void *sum_out = ptr(), *y = ptr(), *q = ptr();
+      const int32_t group = i32();
+      float* scales = static_cast<float*>(ptr());
+      return moe_add_rms_norm(rows, D, dtype, x, residual, weight, static_cast<float>(eps), sum_out, y, q, group,
+                              scales, ptr());
+    }
+    case MOE_CALL_ROUTE_GATED: {
+      const auto* cfg = static_cast<const moe_config_t*>(ptr());
+      const auto* gate = static_cast<const moe_gate_t*>(ptr());
+      const void *x = ptr(), *Wg = ptr();
+      const float *lb = static_cast<const float*>(ptr()), *sb = static_cast<const float*>(ptr());
+      float* logits = static_cast<float*>(ptr());
+      int32_t* ids = static_cast<int32_t*>(ptr());
+      float* w = static_cast<float*>(ptr());
+      void* ws = ptr();
+      const size_t bytes = static_cast<size_t>(word());
+      return moe_route_gated(cfg, gate, x, Wg, lb, sb, logits, ids, w, ws, bytes, ptr());
+    }
+    case MOE_CALL_LORA: {
+      const int32_t T = i32(), K = i32(), N = i32(), r = i32(), n = i32();
+      const void* x = ptr();
+      const int32_t* ids = static_cast<const int32_t*>(ptr());
+      const void *A = ptr(), *B = ptr();
+      const float* scales = static_cast<const float*>(ptr());
+      const void* base = ptr();
+      void* y = ptr();
+      const int32_t y_dtype = i32();
+      void* ws = ptr();
+      const size_t bytes = static_cast<size_t>(word());
+      return moe_lora(T, K, N, r, n, x, ids, A, B, scales, base, y, y_dtype, ws, bytes, ptr());
+    }
+    default: return MOE_ERR_INVALID_ARG;
+  }
 }
 
 }  // extern "C"

@@ -91,6 +91,26 @@ def test_gate_refusals(lib):
         moe.make_gate("tanh")
 
 
+def test_gate_wrapper_compares_its_tensors(lib):
+    T, E, k, D = 3, 64, 4, 256
+    cfg = _cfg(T=T)
+    good = dict(x=torch.zeros(T, D).bfloat16(), Wg=torch.zeros(D, E).bfloat16(), lb=torch.zeros(E), sb=torch.zeros(E),
+                logits=torch.zeros(T, E), ids=torch.zeros(T, k, dtype=torch.int32), w=torch.zeros(T, k))
+    ws = torch.zeros(moe.moe_workspace_size(cfg), dtype=torch.uint8)
+
+    def call(**other):
+        a = dict(good, **other)
+        moe.moe_route_gated(cfg, moe.make_gate(), a["x"], a["Wg"], a["lb"], a["sb"], a["logits"], a["ids"], a["w"], ws)
+
+    for a in ({}, {"x": None, "Wg": None, "lb": None}, {"sb": None}):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(**a)
+    for name, t in good.items():
+        for bad in (t[:-1].contiguous(), t.double()):
+            with pytest.raises(ValueError, match="moe_route_gated takes"):
+                call(**{name: bad})
+
+
 # ------------------------------------------------------------------- lora
 def _lora(lib, T=4, K=256, N=64, r=16, n=3, x=P, ids=P, A=P, B=P, s=P, base=P, y=P, dt=moe.MOE_BF16, ws=P, size=1 << 40):
     return lib.moe_lora(T, K, N, r, n, x, ids, A, B, s, base, y, dt, ws, size, None)
@@ -154,6 +174,60 @@ def test_block_refusals(lib):
     assert _block(lib, _cfg(w_dtype="w4_g64"), s13=P) == UNSUPPORTED
     assert _block(lib, moe.make_config(4, 32776, 64, 4, 128)) == UNSUPPORTED
     assert _block(lib, _cfg(), n=1000) == WORKSPACE
+
+
+def test_block_wrapper_compares_its_tensors(lib):
+    T, D, E = 3, 256, 64
+    cfg = _cfg(T=T)
+    x, W = torch.zeros(T, D).bfloat16(), torch.zeros(8).bfloat16()
+    good = dict(x=x, residual=x, nw=x[0], Wg=torch.zeros(D, E).bfloat16(), lb=torch.zeros(E), sb=torch.zeros(E), sum_out=x, y=x, out=x)
+
+    def call(**other):
+        a = dict(good, **other)
+        moe.moe_block(cfg, moe.make_gate(), a["x"], a["residual"], a["nw"], 1e-6, a["Wg"], a["lb"], a["sb"], W, None, W, None, None, None,
+                      None, None, a["sum_out"], a["y"], a["out"], W)
+
+    for a in ({}, {"residual": None, "sum_out": None}, {"sb": None, "lb": None}):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(**a)
+    for name, t in good.items():
+        for bad in (t[:-1].contiguous(), t.double()):
+            with pytest.raises(ValueError, match="moe_block takes"):
+                call(**{name: bad})
+
+
+# ------------------------------------------------------------------- call
+def test_call_gives_the_calls_their_arguments(lib):
+    """The same refusals, one argument wrong at a time, from the words as from the arguments."""
+    need = moe.moe_lora_workspace_size(4, 256, 64, 16, 3)
+    good = [0, 256, 64, 16, 3, P, P, P, P, P, P, P, moe.MOE_BF16, P, need, 0]
+    for i, bad, want in [(0, 0, 0), (0, -1, -1), (1, 12, -1), (2, 4, -1), (3, 264, -2), (4, 0, -1), (12, 9, -2), (13, P + 8, -5), (14, need - 1, -5)]:
+        a = list(good)
+        a[i] = bad
+        if i == 14:
+            a[0] = 4
+        assert lib.moe_call(moe._LORA, moe._LORA_WORDS(*a)) == want == lib.moe_lora(*a)
+    for i in (5, 6, 7, 8, 11):
+        a = [4] + good[1:]
+        a[i] = 0
+        assert lib.moe_call(moe._LORA, moe._LORA_WORDS(*a)) == -1
+    good = [0, 256, moe.MOE_BF16, P, P, P, 1e-6, P, P, P, 0, P, 0]
+    for i, bad, want in [(0, 0, 0), (1, 12, -1), (2, 9, -2), (6, -1.0, -1), (6, math.inf, -1), (10, 16, -1)]:
+        a = list(good)
+        a[i] = bad
+        assert lib.moe_call(moe._NORM, moe._NORM_WORDS(*a)) == want == lib.moe_add_rms_norm(*a)
+    for i in (3, 5, 9, 11):
+        a = [4] + good[1:]
+        a[i] = 0
+        assert lib.moe_call(moe._NORM, moe._NORM_WORDS(*a)) == -1
+    cfg, gate = _cfg(), moe.make_gate()
+    n = moe.moe_workspace_size(cfg)
+    good = [ctypes.addressof(cfg), ctypes.addressof(gate), P, P, 0, P, P, P, P, P, n, 0]
+    for i, bad, want in [(0, 0, -1), (1, 0, -1), (2, P + 8, -1), (3, 0, -1), (6, 0, -1), (7, 0, -1), (8, 0, -1), (9, 0, -5), (10, 100, -5)]:
+        a = list(good)
+        a[i] = bad
+        assert lib.moe_call(moe._ROUTE_GATED, moe._ROUTE_GATED_WORDS(*a)) == want
+    assert lib.moe_call(3, moe._LORA_WORDS(*range(16))) == -1 and lib.moe_call(0, None) == -1
 
 
 # -------------------------------------------------------------- reference
