@@ -31,10 +31,10 @@ constexpr int kLoraWarps = 8;
 constexpr int kRankSlice = 64;  // columns of v that one warp holds sums of
 
 struct LoraTile {
-  int adapter;  // -1: rows without one
-  int first;    // in the sorted rows
+  int adapter;  // kNoAdapter, or kNoTile: past the last tile
   int count;
 };
+constexpr int kNoAdapter = -1, kNoTile = -2;
 
 struct LoraParams {
   const __nv_bfloat16 *x, *A, *B;
@@ -43,103 +43,112 @@ struct LoraParams {
   const void* base;
   void* y;
   float* planes;  // [splits, T, r]
-  int32_t* order;
+  int32_t* order;  // rows of each tile (tile_rows places of a tile; -1: none)
   LoraTile* tiles;
-  int32_t* ntiles;
   int32_t* err;
   int T, K, N, r, n;
+  int tile_rows, max_tiles;
   int splits;  // of K (and planes, where the slices are not added at once)
   int slices;  // of r
   int chunk;   // columns of y a CTA takes, a multiple of 64 (few rows: of 256)
 };
 
 // ------------------------------------------------------------------- plan
-// One CTA: rows counted by adapter, adapters' starts, tiles of at most 16 MT rows, rows
-// scattered (in any order inside an adapter: what a row gets does not depend on the rows
-// beside it).
-__global__ void __launch_bounds__(1024) lora_plan_kernel(const LoraParams p, int tile_rows) {
+// One CTA: rows counted by adapter, each adapter's first tile, rows to their tiles (in any
+// order inside an adapter: what a row gets does not depend on the rows beside it).  Up to
+// kPlanRows rows a thread keeps its rows' adapters and ranks; more rows are counted twice.
+constexpr int kPlanThreads = 1024, kPlanEach = 8, kPlanRows = kPlanThreads * kPlanEach;
+__global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  extern __shared__ int32_t bins[];  // n + 1 counts, then next free positions
-  __shared__ int2 warp_sum[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = p.n + 1;
-  for (int i = tid; i < nb; i += 1024) bins[i] = 0;
-  __syncthreads();
-  auto bin = [&](int id) { return static_cast<unsigned>(id) < static_cast<unsigned>(p.n) ? id : p.n; };
-  // position of a row in its adapter's bin b (-1: no row).  A request's rows lie together: one
-  // atomic for a warp whose rows have one adapter.
-  auto take = [&](int b) {
-    const unsigned mask = __ballot_sync(0xffffffffu, b >= 0);
-    const int b0 = __shfl_sync(0xffffffffu, b, 0);
-    int at = 0;
-    if (__all_sync(0xffffffffu, b == b0 || b < 0)) {
-      if (lane == 0 && b >= 0) at = atomicAdd(&bins[b], __popc(mask));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1u));
-    } else if (b >= 0) {
-      at = atomicAdd(&bins[b], 1);
+  extern __shared__ int32_t bins[];  // n + 1 counts, then first (next free) places in order
+  __shared__ int warp_sum[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = p.n + 1, R = p.tile_rows;
+  for (int i = tid; i < nb; i += kPlanThreads) bins[i] = 0;
+  // the bins of kPlanRows rows (-1: no row), all loads under way at a time
+  int b[kPlanEach], at[kPlanEach];
+  auto load = [&](long long t0) {
+#pragma unroll
+    for (int i = 0; i < kPlanEach; ++i) {
+      const long long t = t0 + tid + kPlanThreads * i;
+      b[i] = -1;
+      if (t < p.T) {
+        const int id = p.ids[t];
+        b[i] = static_cast<unsigned>(id) < static_cast<unsigned>(p.n) ? id : p.n;
+      }
     }
-    return at;
   };
-  // the bins of the rows t, t + 1024, ..: eight loads under way at a time
-  auto bins_of = [&](long long t, int (&b)[8]) {
+  // at[i]: place of a row in its bin.  A request's rows lie together: one atomic for a warp
+  // whose rows have one adapter.
+  auto take = [&](long long t0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = t + 1024 * i < p.T ? bin(p.ids[t + 1024 * i]) : -1;
+    for (int i = 0; i < kPlanEach; ++i) {
+      if (t0 + kPlanThreads * i >= p.T) break;
+      const unsigned mask = __ballot_sync(0xffffffffu, b[i] >= 0);
+      const int first = __shfl_sync(0xffffffffu, b[i], 0);
+      if (__all_sync(0xffffffffu, b[i] == first || b[i] < 0)) {
+        int a = 0;
+        if (lane == 0 && first >= 0) a = atomicAdd(&bins[first], __popc(mask));
+        at[i] = __shfl_sync(0xffffffffu, a, 0) + __popc(mask & ((1u << lane) - 1u));
+      } else if (b[i] >= 0) {
+        at[i] = atomicAdd(&bins[b[i]], 1);
+      }
+    }
   };
-  for (long long t = tid; t - tid < p.T; t += 8192) {
-    int b[8];
-    bins_of(t, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (t - tid + 1024 * i < p.T) take(b[i]);
+  load(0);
+  __syncthreads();
+  take(0);
+  for (long long t = kPlanRows; t < p.T; t += kPlanRows) {
+    load(t);
+    take(t);
   }
   __syncthreads();
-  // exclusive sums of rows and of tiles over the adapters, a run of them a thread
-  const int per = (nb + 1023) / 1024, b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
-  int rows = 0, tiles = 0;
-  for (int b = b0; b < b1; ++b) {
-    rows += bins[b];
-    tiles += (bins[b] + tile_rows - 1) / tile_rows;
-  }
-  int2 inc = make_int2(rows, tiles);
+  // exclusive sums of the adapters' tiles, a run of adapters a thread
+  const int per = (nb + kPlanThreads - 1) / kPlanThreads, b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
+  int tiles = 0;
+  for (int i = b0; i < b1; ++i) tiles += (bins[i] + R - 1) / R;
+  int inc = tiles;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, inc.x, o), c = __shfl_up_sync(0xffffffffu, inc.y, o);
-    if (lane >= o) {
-      inc.x += a;
-      inc.y += c;
-    }
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
   }
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  int row = inc.x - rows, tile = inc.y - tiles;
-  for (int w = 0; w < warp; ++w) {
-    row += warp_sum[w].x;
-    tile += warp_sum[w].y;
-  }
-  for (int b = b0; b < b1; ++b) {
-    const int c = bins[b];
-    for (int i = 0; i < c; i += tile_rows)
-      p.tiles[tile++] = LoraTile{b < p.n ? b : -1, row + i, min(tile_rows, c - i)};
-    bins[b] = row;
-    row += c;
-  }
-  if (tid == 1023) *p.ntiles = tile;
-  __syncthreads();
-  for (long long t = tid; t - tid < p.T; t += 8192) {
-    int b[8];
-    bins_of(t, b);
+  int before = warp_sum[lane], all = before;
+  if (lane >= warp) before = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (t - tid + 1024 * i < p.T) {
-        const int at = take(b[i]);
-        if (b[i] >= 0) p.order[at] = static_cast<int>(t) + 1024 * i;
-      }
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  int tile = before + inc - tiles;
+  for (int i = b0; i < b1; ++i) {
+    const int c = bins[i];
+    bins[i] = tile * R;
+    for (int r = 0; r < c; r += R, ++tile) p.tiles[tile] = LoraTile{i < p.n ? i : kNoAdapter, min(R, c - r)};
+  }
+  for (int i = all + tid; i < p.max_tiles; i += kPlanThreads) p.tiles[i] = LoraTile{kNoTile, 0};
+  for (int i = tid; i < all * (R / 4); i += kPlanThreads) reinterpret_cast<int4*>(p.order)[i] = make_int4(-1, -1, -1, -1);
+  __syncthreads();
+  if (p.T <= kPlanRows) {
+#pragma unroll
+    for (int i = 0; i < kPlanEach; ++i)
+      if (b[i] >= 0) p.order[bins[b[i]] + at[i]] = tid + kPlanThreads * i;
+    return;
+  }
+  for (long long t = 0; t < p.T; t += kPlanRows) {
+    load(t);
+    take(t);
+#pragma unroll
+    for (int i = 0; i < kPlanEach; ++i)
+      if (b[i] >= 0) p.order[at[i]] = static_cast<int>(t) + tid + kPlanThreads * i;
   }
 }
 
 // --------------------------------------------------------------- tile rows
-// The CTA's tile: its rows' numbers in `rows` (at most max_rows of them), its adapter;
-// false when it has none.  Without a plan (SCAN) the tile is all rows with row b's adapter.
+// The CTA's tile: its rows' numbers in `rows`, its adapter; false when it has none.  Without a
+// plan (SCAN) the tile is all rows with row b's adapter.
 template <bool SCAN>
 __device__ __forceinline__ bool lora_tile(const LoraParams& p, int b, int* rows, int* count_slot, int& adapter,
                                           int& count) {
@@ -167,15 +176,15 @@ __device__ __forceinline__ bool lora_tile(const LoraParams& p, int b, int* rows,
     adapter = count_slot[1];
     return count > 0;
   }
-  if (b >= *p.ntiles) return false;
   const LoraTile t = p.tiles[b];
   adapter = t.adapter;
   count = t.count;
-  if (static_cast<int>(threadIdx.x) < t.count) rows[threadIdx.x] = p.order[t.first + threadIdx.x];
+  if (threadIdx.x < 16) rows[threadIdx.x] = p.order[16 * static_cast<size_t>(b) + threadIdx.x];
   __syncthreads();
-  return true;
+  return adapter != kNoTile;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ uint4 ldg16(const __nv_bfloat16* p, bool ok) {
   return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
 }
@@ -368,17 +377,27 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_expand_kernel(const L
     load_cols(col[0], n0, r0);
     load_cols(col[1], n0, r0 + 32);
   };
-  const bool work = tile && adapter >= 0;
+  if (!tile) return;  // (at once, to make room; a tile there is)
   const int n_first = c0 + 32 * warp;
-  if (work) load_step(n_first, 0);
+  if (adapter >= 0) {
+    load_step(n_first, 0);
+    // the base, and the second block's rows of B, as far as L2
+    if (base) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (8 * h + g < count && n_first + 8 * tig < c1) prefetch_l2(base + static_cast<size_t>(rows[8 * h + g]) * p.N + n_first + 8 * tig);
+    }
+    const int n = n_first + 32 * kLoraWarps + lane;
+    if (n < c1)
+      for (int k = 0; k < p.r; k += 64) prefetch_l2(B + static_cast<size_t>(n) * p.r + k);
+  }
+  const float scale = p.scales && adapter >= 0 ? p.scales[adapter] : 1.0f;
   pdl_wait();
   pdl_launch_dependents();
-  if (!tile) return;
-  if (!work) {
+  if (adapter < 0) {
     copy_rows(base, y, rows, count, p.N, c0, c1);
     return;
   }
-  const float scale = p.scales ? p.scales[adapter] : 1.0f;
   constexpr int W = sizeof(Ty) / 2;  // 16-byte words of eight values
   for (int m0 = 0; m0 < count; m0 += 16) {
     if (m0) {
@@ -526,14 +545,13 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_shrink_wide_kernel(const
   const uint32_t tmem = ctl.tmem;
   pdl_wait();
   pdl_launch_dependents();
-  const bool there = static_cast<int>(blockIdx.x) < *p.ntiles;
-  const LoraTile tile = there ? p.tiles[blockIdx.x] : LoraTile{-1, 0, 0};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const LoraTile tile = p.tiles[blockIdx.x];
+  if (tid < kWideRows) rows[tid] = p.order[static_cast<size_t>(blockIdx.x) * kWideRows + tid];  // (of no tile: not read)
   if (tile.adapter < 0) {  // (the whole cluster)
     wide_end(tmem, geom.cols());
     return;
   }
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid < kWideRows) rows[tid] = tid < tile.count ? p.order[tile.first + tid] : -1;
   __syncthreads();
   uint8_t* ring = align1024(raw);
   const uint32_t base = smem_u32(ring), stage_bytes = geom.stage();
@@ -666,31 +684,31 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
   __shared__ int rows[kWideRows];
   extern __shared__ uint8_t raw[];
   const Geom geom(p.r);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const LoraTile tile = p.tiles[blockIdx.x];
+  if (tid < kWideRows) rows[tid] = p.order[static_cast<size_t>(blockIdx.x) * kWideRows + tid];
+  if (tile.adapter == kNoTile) return;  // (at once, to make room; a tile there is)
+  const float scale = p.scales && tile.adapter >= 0 ? p.scales[tile.adapter] : 1.0f;
   wide_begin(&ctl, geom.cols());
   const uint32_t tmem = ctl.tmem;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool there = static_cast<int>(blockIdx.x) < *p.ntiles;
-  const LoraTile tile = there ? p.tiles[blockIdx.x] : LoraTile{-1, 0, 0};
-  if (tid < kWideRows) rows[tid] = tid < tile.count ? p.order[tile.first + tid] : -1;
-  __syncthreads();
-  const bool work = there && tile.adapter >= 0;
-  const int c0 = blockIdx.y * p.chunk, c1 = min(p.N, c0 + p.chunk);
+  const int c0 = blockIdx.y * p.chunk, c1 = min(p.N, c0 + p.chunk), blocks = (c1 - c0 + COLS - 1) / COLS;
   const Ty* base = static_cast<const Ty*>(p.base);
   Ty* y = static_cast<Ty*>(p.y);
-  const int blocks = (c1 - c0 + COLS - 1) / COLS;
   uint8_t* ring = align1024(raw);
   const uint32_t ring_at = smem_u32(ring), stage_bytes = geom.stage(), base_at = geom.atoms * COLS * 128;
   // B's pieces of 16 bytes: eight threads to a row, kStep rows at a time
   constexpr int kStep = kWideThreads / 8;
   const int bpiece = tid & 7, t0 = tid >> 3;
   const uint32_t bput = ring_at + t0 * 128 + ((bpiece ^ (t0 & 7)) << 4);
-  const __nv_bfloat16* bp =
-      p.B + (static_cast<size_t>(max(tile.adapter, 0)) * p.N + c0 + t0) * p.r + 8 * bpiece;
   // the base's and y's: four lanes to half a row, eight rows at a time (rows 4 apart to a
   // quarter of the warp: no two of its pieces meet in the banks)
   const int quarter = warp & 3, half = warp >> 2, piece = 4 * half + (lane & 3);
   const int wrow = ((lane >> 2) & 1) * 4 + (lane >> 3);
   const uint32_t wput = (32 * quarter + wrow) * 128 + ((piece ^ (wrow & 7)) << 4);  // + 1024 i
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+  const uint32_t idesc = make_idesc_bf16_f32(kWideRows, COLS, 0, 0);
+  const __nv_bfloat16* bp =
+      p.B + (static_cast<size_t>(max(tile.adapter, 0)) * p.N + c0 + t0) * p.r + 8 * bpiece;
   size_t off[4];
   uint32_t ybytes[4];
 #pragma unroll
@@ -724,22 +742,20 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
     }
     cp_commit();
   };
-  if (work) {  // nothing of these comes from the launch before (the planes do)
+  if (tile.adapter >= 0) {  // nothing of these comes from the launch before (the planes do)
 #pragma unroll
     for (int i = 0; i < kWideStages; ++i) load();
   }
   pdl_wait();
   pdl_launch_dependents();
-  if (!work) {
-    if (there) copy_rows(base, y, rows, tile.count, p.N, c0, c1);
+  if (tile.adapter < 0) {
+    copy_rows(base, y, rows, tile.count, p.N, c0, c1);
     wide_end(tmem, geom.cols());
     return;
   }
-  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
   {
     // a row of v by two threads, 32 of the rank (16 columns) at a time
     const int row = rows[32 * quarter + lane];
-    const float scale = p.scales ? p.scales[tile.adapter] : 1.0f;
     for (int j = 32 * half; j < 2 * geom.kcols; j += 64) {
       float f[4][8];
 #pragma unroll
@@ -769,7 +785,6 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
     }
     tc_wait_st();
   }
-  const uint32_t idesc = make_idesc_bf16_f32(kWideRows, COLS, 0, 0);
   for (int b = 0; b <= blocks; ++b) {
     if (b < blocks) {
       cp_wait<kWideStages - 2>();
@@ -858,7 +873,8 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n) {
   const int most = q.wide ? (K + 255) / 256 : (K + 32 * kLoraWarps - 1) / (32 * kLoraWarps);
   q.splits = static_cast<int>(std::max(1ll, std::min<long long>(2 * kSms / (tiles * q.slices), most)));
   if (q.wide) q.splits = std::min(q.splits, kMaxCluster);
-  // wide: two CTAs an SM; else four, a block of 32 columns at least for each warp
+  // wide: as many CTAs as have room at a time; else four an SM, a block of 32 columns at least
+  // for each warp
   const int unit = q.wide ? 64 : 32 * kLoraWarps, units = (N + unit - 1) / unit;
   const int chunks = static_cast<int>(std::max(1ll, std::min<long long>((q.wide ? 2 : 4) * kSms / tiles, units)));
   q.chunk = (units + chunks - 1) / chunks * unit;
@@ -866,7 +882,7 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n) {
 }
 
 struct LoraLayout {
-  size_t planes, order, tiles, ntiles, total;
+  size_t planes, order, tiles, total;
 };
 LoraLayout lora_layout(const LoraPlan& q, int T, int r) {
   LoraLayout L{};
@@ -878,9 +894,8 @@ LoraLayout lora_layout(const LoraPlan& q, int T, int r) {
   };
   L.planes = take(static_cast<size_t>(q.wide ? 1 : q.splits) * T * r * 4);
   if (!q.scan) {
-    L.order = take(static_cast<size_t>(T) * 4);
+    L.order = take(static_cast<size_t>(q.tiles) * q.tile_rows * 4);
     L.tiles = take(static_cast<size_t>(q.tiles) * sizeof(LoraTile));
-    L.ntiles = take(4);
   }
   L.total = cur;
   return L;
@@ -911,10 +926,12 @@ cudaError_t products(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStr
 }
 
 template <typename Ty>
-cudaError_t expand_wide(const LoraParams& p, dim3 grid, cudaStream_t s) {
+cudaError_t expand_wide(const LoraParams& p, cudaStream_t s) {
+  const ExpandGeom<Ty> geom(p.r);
   const cudaError_t e = allow_smem<lora_expand_wide_kernel<Ty>>(ExpandGeom<Ty>(kLoraMaxRank).smem());
   if (e != cudaSuccess) return e;
-  return launch_kernel(lora_expand_wide_kernel<Ty>, grid, dim3(kWideThreads), ExpandGeom<Ty>(p.r).smem(), s, p);
+  const dim3 grid(p.max_tiles, (p.N + p.chunk - 1) / p.chunk);
+  return launch_kernel(lora_expand_wide_kernel<Ty>, grid, dim3(kWideThreads), geom.smem(), s, p);
 }
 cudaError_t products_wide(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStream_t s) {
   const size_t shrink = ShrinkGeom(p.r).smem();
@@ -936,8 +953,7 @@ cudaError_t products_wide(const LoraParams& p, const LoraPlan& q, bool y_f32, cu
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, lora_shrink_wide_kernel, p);
   if (e != cudaSuccess) return e;
-  const dim3 grid(q.tiles, (p.N + p.chunk - 1) / p.chunk);
-  e = y_f32 ? expand_wide<float>(p, grid, s) : expand_wide<__nv_bfloat16>(p, grid, s);
+  e = y_f32 ? expand_wide<float>(p, s) : expand_wide<__nv_bfloat16>(p, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -962,20 +978,21 @@ cudaError_t launch_lora(int T, int K, int N, int r, int n, const void* x, const 
   p.planes = reinterpret_cast<float*>(ws + L.planes);
   p.order = reinterpret_cast<int32_t*>(ws + L.order);
   p.tiles = reinterpret_cast<LoraTile*>(ws + L.tiles);
-  p.ntiles = reinterpret_cast<int32_t*>(ws + L.ntiles);
   p.err = &reinterpret_cast<ControlBlock*>(ws)->err;
   p.T = T;
   p.K = K;
   p.N = N;
   p.r = r;
   p.n = n;
+  p.tile_rows = q.tile_rows;
+  p.max_tiles = q.tiles;
   p.splits = q.splits;
   p.slices = q.slices;
   p.chunk = q.chunk;
   if (q.scan) return products<true>(p, q, y_f32, s);
   const size_t smem = static_cast<size_t>(n + 1) * 4;
   cudaError_t e = allow_smem<lora_plan_kernel>(static_cast<size_t>(kLoraMaxAdapters + 1) * 4);
-  if (e == cudaSuccess) e = launch_kernel(lora_plan_kernel, dim3(1), dim3(1024), smem, s, p, q.tile_rows);
+  if (e == cudaSuccess) e = launch_kernel(lora_plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, p);
   if (e != cudaSuccess) return e;
   return q.wide ? products_wide(p, q, y_f32, s) : products<false>(p, q, y_f32, s);
 }
