@@ -350,7 +350,8 @@ int moe_dequantize_w4(const void* Wq, const void* scales, const void* zeros, int
                       int32_t N, int32_t group, void* W, void* stream);
 
 /* How moe_route_gated and moe_block choose experts.  With logits l [E] of a token
- * (x W_g + logit_bias, fp32) and its scores p, all in fp32:
+ * (x W_g + logit_bias, fp32) and its scores p, all in fp32 (what is compared to 2^-22
+ * and 2^-23 of |l| relative, the weights as expf has them):
  *   p       softmax over the E experts, or sigmoid of each logit (score).
  *   c       p + select_bias: takes part in the choice, not in the weights.
  *   groups  the experts in n_group runs of E / n_group; a group's value is the

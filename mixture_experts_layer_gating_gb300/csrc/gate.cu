@@ -9,22 +9,25 @@
 namespace moe {
 namespace {
 
-// v += a plane's row of logits (EPL neighbouring experts of this lane).
-template <int EPL>
-__device__ __forceinline__ void add_logits(const float* __restrict__ row, int lane, int E, bool vec, float (&v)[EPL]) {
+// v = or (ADD) += a plane's row of logits (EPL neighbouring experts of this lane; 0 past E).
+template <int EPL, bool ADD>
+__device__ __forceinline__ void load_logits(const float* __restrict__ row, int lane, int E, bool vec, float (&v)[EPL]) {
   const int e0 = lane * EPL;
   if (vec) {
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
       const float4 f = e0 + i < E ? *reinterpret_cast<const float4*>(row + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      v[i] += f.x;
-      v[i + 1] += f.y;
-      v[i + 2] += f.z;
-      v[i + 3] += f.w;
+      v[i] = ADD ? v[i] + f.x : f.x;
+      v[i + 1] = ADD ? v[i + 1] + f.y : f.y;
+      v[i + 2] = ADD ? v[i + 2] + f.z : f.z;
+      v[i + 3] = ADD ? v[i + 3] + f.w : f.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) v[i] += e0 + i < E ? row[e0 + i] : 0.0f;
+    for (int i = 0; i < EPL; ++i) {
+      const float f = e0 + i < E ? row[e0 + i] : 0.0f;
+      v[i] = ADD ? v[i] + f : f;
+    }
   }
 }
 
@@ -37,14 +40,15 @@ __global__ void __launch_bounds__(kGateWarps * 32)
                 int32_t* __restrict__ ids, float* __restrict__ w, int32_t* err) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ __align__(16) uint32_t scratch[kGateWarps][32 * EPL];
+  __shared__ __align__(16) uint32_t scratch[kGateWarps][gate_scratch(EPL)];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long t = static_cast<long long>(blockIdx.x) * kGateWarps + warp;
   if (t >= T) return;
-  float v[EPL] = {};
+  float v[EPL];
   const size_t at = static_cast<size_t>(t) * g.E;
-  add_logits<EPL>(planes + at, lane, g.E, vec, v);
-  for (int s = 1; s < nsplit; ++s) add_logits<EPL>(planes + s * (static_cast<size_t>(T) * g.E) + at, lane, g.E, vec, v);
+  load_logits<EPL, false>(planes + at, lane, g.E, vec, v);
+  for (int s = 1; s < nsplit; ++s)
+    load_logits<EPL, true>(planes + s * (static_cast<size_t>(T) * g.E) + at, lane, g.E, vec, v);
   warp_gate_topk<EPL, WHOLE, SIGMOID, BIAS>(v, lane, g, logit_bias, select_bias,
                                             (nsplit > 1 || logit_bias) ? logits + at : nullptr, ids + t * g.k,
                                             w + t * g.k, scratch[warp], err);

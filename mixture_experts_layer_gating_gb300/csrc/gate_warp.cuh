@@ -10,17 +10,25 @@
 
 namespace moe {
 
-// A float's bits in an order that unsigned integers compare (-0 as +0).
+// A float's bits in an order that unsigned integers compare (-0 below +0).
 __device__ __forceinline__ uint32_t ordered_key(float x) {
-  const uint32_t u = __float_as_uint(x + 0.0f);
+  const uint32_t u = __float_as_uint(x);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float ordered_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
+// e^x by the hardware's 2^x: off by 2^-22 and 2^-23 |x| of the value at most (of a sigmoid by
+// half an ulp of 1), for what is compared; weights take expf.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+template <bool FAST>
 __device__ __forceinline__ float gate_sigmoid(float x) {
   float r;  // (of 1 to infinity)
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-x)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + (FAST ? fast_exp(-x) : expf(-x))));
   return r;
 }
 
@@ -58,13 +66,16 @@ __device__ __forceinline__ void put_lane(uint32_t* to, const uint32_t (&s)[EPL])
   }
 }
 
+// (a lane's keys and a 0 behind them, rows of 16 bytes)
+__host__ __device__ constexpr int gate_scratch(int epl) { return 32 * ((epl + 4) / 4 * 4); }
+
 // Lane l holds the token's projected logits of experts l EPL .. l EPL + EPL - 1 in v
-// (E <= 32 EPL; entries past E are ignored), so that among lanes and within one the lower
-// index comes first.  Writes the final logits to logits_row (when given), ids_row and
+// (E <= 32 EPL; entries past E are ignored, but are numbers), so that among lanes and within
+// one the lower index comes first.  Writes the final logits to logits_row (when given), ids_row and
 // w_row [k]; returns ids_row[lane] on lanes below k <= 16, -1 on the others.
 //   WHOLE    E is a multiple of EPL: a lane has all its entries or none.
 //   SIGMOID, BIAS  as g.sigmoid and select_bias say (no branch an entry on them).
-//   scratch  32 EPL words of the warp's own in shared memory, 16-byte aligned.
+//   scratch  gate_scratch(EPL) words of the warp's own in shared memory, 16-byte aligned.
 //
 // Bound by instructions, most of them on the half-rate integer pipe, so each lane sorts
 // its keys once and the k rounds look at one head a lane: a warp maximum, the first lane
@@ -81,16 +92,25 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
   const bool bias_vec = !(reinterpret_cast<uintptr_t>(select_bias) & 15);
   constexpr unsigned kFull = 0xffffffffu;
   const int e0 = lane * EPL, E = g.E, k = g.k;
-  auto has = [&](int i) { return WHOLE ? e0 < E : e0 + i < E; };
-  uint32_t* mine = scratch + e0;
+  const bool here = e0 < E;
+  auto has = [&](int i) { return WHOLE || e0 + i < E; };  // (of a lane that is here)
+  constexpr int kRow = gate_scratch(EPL) / 32;
+  uint32_t* mine = scratch + lane * kRow;
   bool bad = false;
   {
     float zero = 0.0f;  // NaN once an entry is not finite
+    if (logit_bias && here) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (has(i)) v[i] += logit_bias[e0 + i];
+    }
+    if (logits_row && here) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (has(i)) logits_row[e0 + i] = v[i];
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      if (!has(i)) v[i] = 0.0f;
-      if (logit_bias && has(i)) v[i] += logit_bias[e0 + i];
-      if (logits_row && has(i)) logits_row[e0 + i] = v[i];
       zero = fmaf(v[i], 0.0f, zero);
       if (!has(i)) v[i] = -INFINITY;
     }
@@ -110,16 +130,18 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     m = v[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
-    m = ordered_value(__reduce_max_sync(kFull, ordered_key(m)));
+    m = ordered_value(__reduce_max_sync(kFull, here ? ordered_key(m) : 0x007fffffu));  // (-infinity's)
     if (m == -INFINITY) m = 0.0f;
     float z = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) z += expf(v[i] - m);
+    if (!here) z = 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
     rz = z > 0.0f ? 1.0f / z : 0.0f;
   }
-  auto score = [&](float x) { return SIGMOID ? gate_sigmoid(x) : expf(x - m) * rz; };
+  auto score = [&](float x) { return SIGMOID ? gate_sigmoid<false>(x) : expf(x - m) * rz; };
+  auto compared = [&](float x) { return SIGMOID ? gate_sigmoid<true>(x) : fast_exp(x - m) * rz; };
   // keys of what is compared, the biased score or the logit; 0: not to be chosen (below
   // every value's key, -infinity's too)
   uint32_t key[EPL];
@@ -128,16 +150,16 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     if (WHOLE && EPL % 4 == 0 && bias_vec) {
 #pragma unroll
       for (int i = 0; i < EPL; i += 4) {
-        const float4 f = e0 < E ? *reinterpret_cast<const float4*>(select_bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 f = here ? *reinterpret_cast<const float4*>(select_bias + e0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
         c[i] = f.x, c[i + 1] = f.y, c[i + 2] = f.z, c[i + 3] = f.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) c[i] = has(i) ? select_bias[e0 + i] : 0.0f;
+      for (int i = 0; i < EPL; ++i) c[i] = here && has(i) ? select_bias[e0 + i] : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      c[i] += score(v[i]);
+      c[i] += compared(v[i]);
       zero = fmaf(c[i], 0.0f, zero);
     }
     if (bad || !(zero == 0.0f)) {
@@ -151,7 +173,7 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     for (int i = 0; i < EPL; ++i) key[i] = has(i) ? ordered_key(c[i]) : 0u;
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = has(i) ? ordered_key(v[i]) : 0u;
+    for (int i = 0; i < EPL; ++i) key[i] = has(i) ? ordered_key(v[i] + 0.0f) : 0u;  // (-0 as +0)
   }
   if (__any_sync(kFull, bad) && lane == 0) atomicOr(err, MOE_DEV_NONFINITE_LOGIT);
 
@@ -161,7 +183,7 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     if (!g.top2 || a == -INFINITY) return ka;
     const bool two = kb != 0u && b != -INFINITY;
     if (BIAS) return ordered_key(two ? a + b : a);
-    return ordered_key(score(a) + (two ? score(b) : 0.0f));
+    return ordered_key(compared(a) + (two ? compared(b) : 0.0f));
   };
   const int size = grouped ? E / g.n_group : E, lanes = size / EPL;
   const bool by_lanes = size % EPL == 0 && (lanes & (lanes - 1)) == 0;
@@ -187,24 +209,24 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (has(i) && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
+      if (here && has(i) && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
   }
   uint32_t s[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) s[i] = key[i];
   sort_keys(s);
-  uint32_t head = s[0];
+  uint32_t head = here ? s[0] : 0u;
   if (grouped && by_lanes) {
     uint32_t a = s[0], b = s[1];
     for (int o = 1; o < lanes; o <<= 1)
       merge_top2(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
-    uint32_t gk = e0 < E ? group_key(a, b) : 0u;
+    uint32_t gk = here ? group_key(a, b) : 0u;
     const int shift = 31 - __clz(lanes);
     bool kept = false;
     for (int j = 0; j < g.topk_group; ++j) {
       const uint32_t best = __reduce_max_sync(kFull, gk);
       const int first = __ffs(__ballot_sync(kFull, gk == best)) - 1;
-      if (e0 < E && lane >> shift == first >> shift) {
+      if (here && lane >> shift == first >> shift) {
         kept = true;
         gk = 0u;
       }
@@ -214,12 +236,14 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
 
   __syncwarp();
   put_lane(mine, s);
-  int at = 0, my_from = 0;
+  mine[EPL] = 0u;
+  int my_from = 0;
+  const uint32_t* next = mine;
   uint32_t my_key = 0u;
   for (int j = 0; j < k; ++j) {
     const uint32_t best = __reduce_max_sync(kFull, head);
     const int from = __ffs(__ballot_sync(kFull, head == best)) - 1;
-    if (lane == from) head = ++at < EPL ? mine[at] : 0u;
+    if (lane == from) head = *++next;
     if (lane == j) {
       my_key = best;
       my_from = from;
@@ -230,7 +254,7 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
   __syncwarp();
   put_lane(mine, key);
   __syncwarp();
-  const uint32_t* theirs = scratch + my_from * EPL;
+  const uint32_t* theirs = scratch + my_from * kRow;
   const uint32_t up_key = __shfl_up_sync(kFull, my_key, 1);
   const int up_from = __shfl_up_sync(kFull, my_from, 1);
   const uint32_t again = __ballot_sync(kFull, lane > 0 && lane < k && my_key == up_key && my_from == up_from);

@@ -68,7 +68,7 @@ struct RtCfg {
   static_assert(kRedBytes <= RT_RING_BYTES, "partial rows fit the ring");
   static_assert((RT_BM / 2) * (2 * 256 + 4) * 4 <= RT_BM * (256 + 4) * 4, "partial rows fit the ring");
   // behind them, the gated choice's scratch of each warp (nh = 2: 512 experts)
-  static_assert(kRedBytes % 16 == 0 && kRedBytes + RT_WARPS * (NB == 256 ? 512 : NB) * 4 <= RT_RING_BYTES,
+  static_assert(kRedBytes % 16 == 0 && kRedBytes + RT_WARPS * gate_scratch(NB == 256 ? 16 : NB / 32) * 4 <= RT_RING_BYTES,
                 "the scratch of the choice fits behind the partial rows");
 };
 
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       auto choose = [&](auto sigmoid, auto bias) {
         return warp_gate_topk<EPL, (EPL <= 8), decltype(sigmoid)::value, decltype(bias)::value>(
             v, lane, p.gate, p.bias, p.select_bias, logits_row, ids_row, w_row,
-            reinterpret_cast<uint32_t*>(base + RtCfg<NB>::kRedBytes) + warp * 32 * EPL, p.err);
+            reinterpret_cast<uint32_t*>(base + RtCfg<NB>::kRedBytes) + warp * gate_scratch(EPL), p.err);
       };
       using Yes = std::true_type;
       using No = std::false_type;
