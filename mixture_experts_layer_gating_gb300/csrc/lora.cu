@@ -596,10 +596,13 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_shrink_wide_kernel(const
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kWideStages - 1; ++i) load();
+  for (int i = 0; i < kWideStages; ++i) load();
   const uint32_t idesc = make_idesc_bf16_f32(kWideRows, geom.rn, 0, 0);
   for (int i = 0; i < s1 - s0; ++i) {
-    cp_wait<kWideStages - 2>();
+    if (i == 0)
+      cp_wait<kWideStages - 1>();
+    else
+      cp_wait<kWideStages - 2>();
     fence_proxy_async_smem();
     __syncthreads();  // the stage is there
     if (tid == 0) {
@@ -613,8 +616,10 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_shrink_wide_kernel(const
       if (i + 1 == s1 - s0) tc_commit(&ctl.all);
     }
     // the stage that is filled next was multiplied from one step before
-    if (i > 0) wide_wait(&ctl, &ctl.mma[(i - 1) % kWideStages], ((i - 1) / kWideStages) & 1, p.err);
-    load();
+    if (i > 0) {
+      wide_wait(&ctl, &ctl.mma[(i - 1) % kWideStages], ((i - 1) / kWideStages) & 1, p.err);
+      load();
+    }
   }
   wide_wait(&ctl, &ctl.all, 0, p.err);
   __syncwarp();
@@ -866,17 +871,24 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n) {
   q.wide = !q.scan && T >= 32ll * n;
   q.tile_rows = q.wide ? kWideRows : 16;
   q.tiles = q.scan ? T : static_cast<int>(std::min<long long>(T, (T + q.tile_rows - 1ll) / q.tile_rows + n));
-  // tiles with an adapter, about
-  const long long tiles = std::max(1, q.scan ? std::min(T, n) : q.wide ? (T + q.tile_rows - 1) / q.tile_rows + n / 2 : q.tiles);
+  // adapters that some row has, about, and tiles
+  const long long used = std::min<long long>(T, static_cast<long long>(n) * T / (T + n / 2));
+  const long long tiles =
+      std::max(1ll, q.scan ? used : q.wide ? (T + q.tile_rows - 1) / q.tile_rows + n / 2 : used + T / 32);
   q.slices = q.wide ? 1 : (r + kRankSlice - 1) / kRankSlice;
-  // two CTAs an SM; a step at least for each warp of a split, or four stages
-  const int most = q.wide ? (K + 255) / 256 : (K + 32 * kLoraWarps - 1) / (32 * kLoraWarps);
-  q.splits = static_cast<int>(std::max(1ll, std::min<long long>(2 * kSms / (tiles * q.slices), most)));
-  if (q.wide) q.splits = std::min(q.splits, kMaxCluster);
-  // wide: as many CTAs as have room at a time; else four an SM, a block of 32 columns at least
-  // for each warp
+  // slices of K: as many CTAs as have room at a time (two an SM)
+  const long long room = std::max(1ll, 2ll * kSms / (tiles * q.slices));
+  if (q.wide) {  // of four stages at least
+    q.splits = static_cast<int>(std::min<long long>({room, (K + 255) / 256, kMaxCluster}));
+  } else {  // and no more than what its warps load at once need (two steps each)
+    const int steps = (K + 31) / 32, once = 2 * kLoraWarps;
+    const long long most = std::min<long long>(room, (steps + kLoraWarps - 1) / kLoraWarps);
+    const long long rounds = ((steps + most - 1) / most + once - 1) / once;
+    q.splits = static_cast<int>((steps + rounds * once - 1) / (rounds * once));
+  }
+  // y's columns: as many CTAs as have room, a block of 32 columns at least for each warp
   const int unit = q.wide ? 64 : 32 * kLoraWarps, units = (N + unit - 1) / unit;
-  const int chunks = static_cast<int>(std::max(1ll, std::min<long long>((q.wide ? 2 : 4) * kSms / tiles, units)));
+  const int chunks = static_cast<int>(std::min<long long>(std::max(1ll, 2ll * kSms / tiles), units));
   q.chunk = (units + chunks - 1) / chunks * unit;
   return q;
 }
