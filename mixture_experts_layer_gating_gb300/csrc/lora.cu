@@ -665,9 +665,9 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_shrink_wide_kernel(const
 // bf16 terms lie in tensor memory as the operand that stays; a stage holds the block's rows
 // of B and the tile's base; a block's products go to one of two sums in tensor memory and
 // are finished while the next block's are made: sums and base are added in place of the base
-// in shared memory, and go from there to y by pieces of 64 bytes of a row.  A warp brings,
-// adds and stores the same half of the columns of the same 32 rows, so that only B's stages
-// are shared between warps.
+// in shared memory, and go from there to y by whole rows of 128 bytes.  Two warps have 32 rows
+// of a tile to themselves: each brings and stores 16 of them and adds half of the columns of
+// all, so that they wait for one another once a block, and for the others for B alone.
 template <typename Ty>
 struct ExpandGeom {
   static constexpr int TERMS = sizeof(Ty) == 2 ? 2 : 3;
@@ -705,11 +705,10 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
   constexpr int kStep = kWideThreads / 8;
   const int bpiece = tid & 7, t0 = tid >> 3;
   const uint32_t bput = ring_at + t0 * 128 + ((bpiece ^ (t0 & 7)) << 4);
-  // the base's and y's: four lanes to half a row, eight rows at a time (rows 4 apart to a
-  // quarter of the warp: no two of its pieces meet in the banks)
-  const int quarter = warp & 3, half = warp >> 2, piece = 4 * half + (lane & 3);
-  const int wrow = ((lane >> 2) & 1) * 4 + (lane >> 3);
-  const uint32_t wput = (32 * quarter + wrow) * 128 + ((piece ^ (wrow & 7)) << 4);  // + 1024 i
+  // the base's and y's: eight lanes to a row, four rows at a time of the warp's sixteen
+  const int quarter = warp & 3, half = warp >> 2, piece = lane & 7;
+  const int wrow = 32 * quarter + 16 * half + (lane >> 3);  // + 4 i
+  auto place = [&](int i) { return (wrow + 4 * i) * 128 + ((piece ^ (lane >> 3) ^ (4 * (i & 1))) << 4); };
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
   const uint32_t idesc = make_idesc_bf16_f32(kWideRows, COLS, 0, 0);
   const __nv_bfloat16* bp =
@@ -718,7 +717,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
   uint32_t ybytes[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = rows[32 * quarter + wrow + 8 * i];
+    const int row = rows[wrow + 4 * i];
     off[i] = static_cast<size_t>(max(row, 0)) * p.N + c0 + V * piece;
     ybytes[i] = row >= 0 ? 16u : 0u;
   }
@@ -739,7 +738,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
         const bool in = c0 + n_load + V * piece < p.N;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          cp_async_16(ring_at + at + base_at + wput + 1024 * i, in ? base + off[i] + n_load : base, in ? ybytes[i] : 0u);
+          cp_async_16(ring_at + at + base_at + place(i), in ? base + off[i] + n_load : base, in ? ybytes[i] : 0u);
       }
       n_load += COLS;
       --left;
@@ -843,15 +842,15 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
       }
       *reinterpret_cast<uint4*>(mine + (((4 * half + q) ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    __syncwarp();
+    named_bar_sync(1 + quarter, 64);  // the other half of the columns
     const int n = f * COLS;
     const bool in = c0 + n + V * piece < c1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 out = *reinterpret_cast<const uint4*>(tile_at + wput + 1024 * i);
+      const uint4 out = *reinterpret_cast<const uint4*>(tile_at + place(i));
       if (in && ybytes[i]) *reinterpret_cast<uint4*>(y + off[i] + n) = out;
     }
-    __syncwarp();  // (the warp's part of the stage is filled again)
+    __syncwarp();  // (the warp's rows of the stage are filled again)
     load();
   }
   wide_end(tmem, geom.cols());
