@@ -77,7 +77,7 @@
  *   4 significant bits of each activation); the bf16-activation layouts
  *   above are the configured arithmetic.
  * - W4_G32 / W4_G64 / W4_G128: 4-bit weights with group scales, taken by
- *   moe_layer_few (moe_layer and moe_grouped_ffn return
+ *   moe_layer_few and moe_block (moe_layer and moe_grouped_ffn return
  *   MOE_ERR_UNSUPPORTED; moe_dequantize_w4 gives them bf16 weights).  A matrix
  *   with N outputs and K inputs is [N, K/2] bytes: byte j of a row holds the
  *   codes 0..15 of inputs 2j (low nibble) and 2j + 1 (high nibble); with a
@@ -436,23 +436,28 @@ int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* 
              const int32_t* ids, const void* A, const void* B, const float* scales, const void* base,
              void* y, int32_t y_dtype, void* ws, size_t ws_bytes, void* stream);
 
-/* A pre-norm residual MoE block: moe_add_rms_norm, then moe_layer with moe_route_gated's
- * choice, on one stream:
+/* A pre-norm residual MoE block: moe_add_rms_norm, then moe_layer or moe_layer_few with
+ * moe_route_gated's choice, on one stream:
  *   sum_out = x + residual,  y = norm(sum_out) * norm_weight,  out = layer(y)
  *   gate        NULL: moe_layer's choice (softmax top-k), select_bias NULL then.
  *   norm_weight [D] act_dtype, or NULL: no norm, the layer takes x (residual, sum_out
  *               and y NULL, eps 0).
  *   y           [T, D] act_dtype out: the normed rows, which the router projects.  May
  *               not overlap anything else.
- *   x, residual, sum_out, eps as in moe_add_rms_norm; the other arguments, the weight
- *   types, the workspace and the errors as in moe_layer (4-bit weights:
- *   MOE_ERR_UNSUPPORTED).
+ *   s13, s2, s13s, s2s  fp32 per column (e4m3 weights), bf16 per row and group (4-bit
+ *               weights, as moe_layer_few has them), or NULL.
+ *   ws          moe_workspace_size(cfg) bytes.
+ *   x, residual, sum_out, eps as in moe_add_rms_norm; the other arguments and the errors
+ *   as in moe_layer (E a multiple of 8 for bf16 activations).
+ * moe_layer_few's kernel takes 4-bit weights (T <= 32, else MOE_ERR_UNSUPPORTED),
+ * FP8_E4M3 up to 32 tokens, FP8_E4M3_NK up to 16 and BF16 up to 8, and leaves in the
+ * workspace what it does; with a gate it is given the choice of the launches before it.
  * FP8_E4M3_NK_A8 layers take their 8-bit rows from the norm (rounded once, from fp32),
  * instead of from y: one launch and one reading of y less. */
 int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const void* residual,
               const void* norm_weight, float eps, const void* Wg, const float* logit_bias,
-              const float* select_bias, const void* W13, const float* s13, const void* W2,
-              const float* s2, const void* W13s, const float* s13s, const void* W2s, const float* s2s,
+              const float* select_bias, const void* W13, const void* s13, const void* W2,
+              const void* s2, const void* W13s, const void* s13s, const void* W2s, const void* s2s,
               void* sum_out, void* y, void* out, void* ws, size_t ws_bytes, void* stream);
 
 /* One of the calls above with its arguments in a block of 8-byte words, in their

@@ -84,30 +84,11 @@ size_t few_workspace_bytes(const moe_config_t* c) {
   return few_dtype(c) && c->T >= 1 && c->T <= kStreamMaxRows ? few_layout(c).total : 0;
 }
 
-}  // namespace moe
-
-extern "C" {
-
-int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const float* logit_bias,
-                  const void* W13, const void* s13, const void* W2, const void* s2, const void* W13s,
-                  const void* s13s, const void* W2s, const void* s2s, void* out, void* ws,
-                  size_t ws_bytes, void* stream) {
-  if (!cfg_valid(cfg)) return MOE_ERR_INVALID_ARG;
-  if (!few_dtype(cfg) || cfg->T > kStreamMaxRows) return MOE_ERR_UNSUPPORTED;
-  const size_t need = moe_workspace_size(cfg);
-  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need) return MOE_ERR_WORKSPACE;
-  for (const void* q : {x, Wg, W13, W2, static_cast<const void*>(out)})
-    if (!q || !al16(q)) return MOE_ERR_INVALID_ARG;
-  const bool scaled = cfg->w_dtype != MOE_BF16, shared = cfg->I_shared > 0;
-  if (scaled != (s13 != nullptr) || scaled != (s2 != nullptr)) return MOE_ERR_INVALID_ARG;
-  for (const void* q : {s13, s2, shared ? s13s : nullptr, shared ? s2s : nullptr})
-    if (!al16(q)) return MOE_ERR_INVALID_ARG;
-  if (shared) {
-    if (!W13s || !W2s || !al16(W13s) || !al16(W2s)) return MOE_ERR_INVALID_ARG;
-    if (scaled != (s13s != nullptr) || scaled != (s2s != nullptr)) return MOE_ERR_INVALID_ARG;
-  }
-  if (cfg->T == 0) return MOE_OK;
+int run_few(const moe_config_t* cfg, const void* x, const void* Wg, const float* logit_bias, const void* W13,
+            const void* s13, const void* W2, const void* s2, const void* W13s, const void* s13s, const void* W2s,
+            const void* s2s, void* out, void* ws, cudaStream_t s) {
   const FewLayout L = few_layout(cfg);
+  const size_t need = moe_workspace_size(cfg);
   uint8_t* base = static_cast<uint8_t*>(ws);
   uint8_t* few = base + (need - L.total);  // the last region of the workspace
   FewArgs a{};
@@ -151,7 +132,6 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
   a.W2 = W2;
   a.W13s = W13s;
   a.W2s = W2s;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (cfg->w_dtype) {
     case MOE_BF16: e = launch_few_bf16(a, s); break;
@@ -160,6 +140,33 @@ int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const 
     default: e = launch_few_w4(w4_group(cfg->w_dtype), a, s); break;
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace moe
+
+extern "C" {
+
+int moe_layer_few(const moe_config_t* cfg, const void* x, const void* Wg, const float* logit_bias,
+                  const void* W13, const void* s13, const void* W2, const void* s2, const void* W13s,
+                  const void* s13s, const void* W2s, const void* s2s, void* out, void* ws,
+                  size_t ws_bytes, void* stream) {
+  if (!cfg_valid(cfg)) return MOE_ERR_INVALID_ARG;
+  if (!few_dtype(cfg) || cfg->T > kStreamMaxRows) return MOE_ERR_UNSUPPORTED;
+  const size_t need = moe_workspace_size(cfg);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  for (const void* q : {x, Wg, W13, W2, static_cast<const void*>(out)})
+    if (!q || !al16(q)) return MOE_ERR_INVALID_ARG;
+  const bool scaled = cfg->w_dtype != MOE_BF16, shared = cfg->I_shared > 0;
+  if (scaled != (s13 != nullptr) || scaled != (s2 != nullptr)) return MOE_ERR_INVALID_ARG;
+  for (const void* q : {s13, s2, shared ? s13s : nullptr, shared ? s2s : nullptr})
+    if (!al16(q)) return MOE_ERR_INVALID_ARG;
+  if (shared) {
+    if (!W13s || !W2s || !al16(W13s) || !al16(W2s)) return MOE_ERR_INVALID_ARG;
+    if (scaled != (s13s != nullptr) || scaled != (s2s != nullptr)) return MOE_ERR_INVALID_ARG;
+  }
+  if (cfg->T == 0) return MOE_OK;
+  return run_few(cfg, x, Wg, logit_bias, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws,
+                 static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_linear_w4_workspace_size(int32_t M, int32_t K, int32_t N) {

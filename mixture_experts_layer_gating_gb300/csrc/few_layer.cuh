@@ -58,7 +58,7 @@ constexpr int kFewPlaneBytes = 65536;
 
 struct FewParams {
   const __nv_bfloat16* x;
-  const __nv_bfloat16* Wg;
+  const __nv_bfloat16* Wg;  // null: ids and topw are given
   const float* bias;
   const void *s13, *s2, *s13s, *s2s;  // fp32 per column (e4m3) or bf16 per group (4-bit)
   __nv_bfloat16* out;
@@ -1193,15 +1193,16 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
   if (p.T == 1 && tid >= 32 && tid < 34) ctl->pass[tid - 32] = few_pass<KIND, GRP>(p, tid == 33, p.k, G, b);
   if (Tr::F16)
     for (int r = b * CT + tid; r < R + p.T; r += G * CT) p.hmax[r] = 0;
-  // phase 0
-  F::router(p, red, b, G);
+  // phase 0 (no router weights: the experts are chosen already, in ids and topw)
+  const bool given = p.Wg == nullptr;
+  if (!given) F::router(p, red, b, G);
   F::stage_x(p, red, b, G);
   F::grid_sync(p, sr, 0, 3);
 
   // phase 1
   if (R > F::kPairRows)
     for (int e = tid; e < p.E; e += CT) ctl->cnt[e] = 0;
-  if (p.nplanes * p.T * p.E * 4 <= kFewPlaneBytes) {
+  if (!given && p.nplanes * p.T * p.E * 4 <= kFewPlaneBytes) {
     F::topk(p, 0, 1, b == 0, ctl->ids, ctl->w, red);
     if (b == 0)
       for (int r = tid; r < R; r += CT) {
@@ -1209,8 +1210,10 @@ __global__ void __launch_bounds__(FewSmem<KIND, GRP, NT>::kBlock, 1)
         p.topw[r] = ctl->w[r];
       }
   } else {
-    F::topk(p, b, G, true, p.ids, p.topw, red);
-    F::grid_sync(p, sr, 1, -1);
+    if (!given) {
+      F::topk(p, b, G, true, p.ids, p.topw, red);
+      F::grid_sync(p, sr, 1, -1);
+    }
     for (int r = tid; r < R; r += CT) {
       ctl->ids[r] = __ldcg(p.ids + r);
       ctl->w[r] = __ldcg(p.topw + r);

@@ -614,29 +614,35 @@ int route(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const 
                   static_cast<cudaStream_t>(stream), nullptr, gate ? &gp : nullptr, select_bias);
 }
 
-bool fp8_scales_ok(const moe_config_t* c, const float* s13, const float* s2) {
-  const bool fp8 = is_fp8(c);
-  return fp8 ? (s13 && s2) : (!s13 && !s2);
+bool scales_ok(const moe_config_t* c, const void* s13, const void* s2) {
+  return is_fp8(c) || w4_group(c->w_dtype) ? (s13 && s2) : (!s13 && !s2);
 }
 
-// The arguments of moe_layer, and of moe_block for the layer.
-int layer_checks(const moe_config_t* cfg, const void* x, const void* Wg, const void* W13, const float* s13,
-                 const void* W2, const float* s2, const void* W13s, const float* s13s, const void* W2s,
-                 const float* s2s, const void* out, void* ws, size_t ws_bytes) {
-  const int st = common_checks(cfg, ws, ws_bytes);
-  if (st != MOE_OK) return st;
-  if (w4_group(cfg->w_dtype)) return MOE_ERR_UNSUPPORTED;  // moe_layer_few
+// The arguments of moe_layer, and of moe_block for the layer (scales of either type).
+int layer_args(const moe_config_t* cfg, const void* x, const void* Wg, const void* W13, const void* s13,
+               const void* W2, const void* s2, const void* W13s, const void* s13s, const void* W2s,
+               const void* s2s, const void* out) {
   if (!x || !Wg || !W13 || !W2 || !out) return MOE_ERR_INVALID_ARG;
   for (const void* p : {x, Wg, W13, W2, out})
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
-  if (!fp8_scales_ok(cfg, s13, s2)) return MOE_ERR_INVALID_ARG;
+  if (!scales_ok(cfg, s13, s2)) return MOE_ERR_INVALID_ARG;
   const bool shared = cfg->I_shared > 0;
   if (shared) {
     if (!W13s || !W2s || !aligned16(W13s) || !aligned16(W2s)) return MOE_ERR_INVALID_ARG;
-    if (!fp8_scales_ok(cfg, s13s, s2s)) return MOE_ERR_INVALID_ARG;
+    if (!scales_ok(cfg, s13s, s2s)) return MOE_ERR_INVALID_ARG;
   }
   if (cfg->act_dtype == MOE_BF16 && (cfg->E % 8)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
+}
+
+// moe_block takes moe_layer_few's kernel: 4-bit weights, and where it measured faster.
+bool few_preferred(const moe_config_t* c) {
+  if (c->act_dtype != MOE_BF16) return false;
+  const int most = w4_group(c->w_dtype) || c->w_dtype == MOE_FP8_E4M3 ? kFewTokens
+                   : c->w_dtype == MOE_FP8_E4M3_NK                    ? 16
+                   : c->w_dtype == MOE_BF16                           ? 8
+                                                                      : 0;
+  return c->T <= most;
 }
 
 // The layer, its arguments checked and T > 0.  gate, select_bias: as do_route has them;
@@ -834,13 +840,13 @@ int moe_grouped_ffn(const moe_config_t* cfg, const void* x_perm, const int32_t* 
   if (!x_perm || !offsets || !W13 || !W2 || !h || !y_perm) return MOE_ERR_INVALID_ARG;
   for (const void* p : {x_perm, W13, W2, static_cast<const void*>(h), static_cast<const void*>(y_perm)})
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
-  if (!fp8_scales_ok(cfg, s13, s2)) return MOE_ERR_INVALID_ARG;
+  if (!scales_ok(cfg, s13, s2)) return MOE_ERR_INVALID_ARG;
   const bool shared = x && cfg->I_shared > 0;
   if (shared) {
     if (!W13s || !W2s || !h_s || !s_out) return MOE_ERR_INVALID_ARG;
     for (const void* p : {x, W13s, W2s, static_cast<const void*>(h_s), static_cast<const void*>(s_out)})
       if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
-    if (!fp8_scales_ok(cfg, s13s, s2s)) return MOE_ERR_INVALID_ARG;
+    if (!scales_ok(cfg, s13s, s2s)) return MOE_ERR_INVALID_ARG;
   }
   if (cfg->T == 0) return MOE_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -886,7 +892,10 @@ int moe_layer(const moe_config_t* cfg, const void* x, const void* Wg, const floa
               const void* W13, const float* s13, const void* W2, const float* s2,
               const void* W13s, const float* s13s, const void* W2s, const float* s2s, void* out,
               void* ws, size_t ws_bytes, void* stream) {
-  const int st = layer_checks(cfg, x, Wg, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, ws_bytes);
+  int st = common_checks(cfg, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (w4_group(cfg->w_dtype)) return MOE_ERR_UNSUPPORTED;  // moe_layer_few
+  st = layer_args(cfg, x, Wg, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out);
   if (st != MOE_OK || cfg->T == 0) return st;
   return run_layer(cfg, x, Wg, logit_bias, nullptr, nullptr, false, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws,
                    static_cast<cudaStream_t>(stream));
@@ -894,33 +903,55 @@ int moe_layer(const moe_config_t* cfg, const void* x, const void* Wg, const floa
 
 int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const void* residual,
               const void* norm_weight, float eps, const void* Wg, const float* logit_bias,
-              const float* select_bias, const void* W13, const float* s13, const void* W2,
-              const float* s2, const void* W13s, const float* s13s, const void* W2s, const float* s2s,
+              const float* select_bias, const void* W13, const void* s13, const void* W2,
+              const void* s2, const void* W13s, const void* s13s, const void* W2s, const void* s2s,
               void* sum_out, void* y, void* out, void* ws, size_t ws_bytes, void* stream) {
-  int st = layer_checks(cfg, x, Wg, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, ws_bytes);
+  int st = common_checks(cfg, ws, ws_bytes);
   if (st != MOE_OK) return st;
+  const bool few = few_preferred(cfg);
+  if (w4_group(cfg->w_dtype) && !few) return MOE_ERR_UNSUPPORTED;
+  if (ws_bytes < moe_workspace_size(cfg)) return MOE_ERR_WORKSPACE;
+  st = layer_args(cfg, x, Wg, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out);
+  if (st != MOE_OK) return st;
+  if (few)
+    for (const void* p : {s13, s2, s13s, s2s})
+      if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
   GateParams gp{};
   if (gate ? !gate_params(cfg, gate, gp) : select_bias != nullptr) return MOE_ERR_INVALID_ARG;
   const GateParams* g = gate ? &gp : nullptr;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!norm_weight) {
-    if (residual || sum_out || y || eps != 0.0f) return MOE_ERR_INVALID_ARG;
-    if (cfg->T == 0) return MOE_OK;
-    return run_layer(cfg, x, Wg, logit_bias, g, select_bias, false, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, s);
+  if (norm_weight) {
+    if (!y || !(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+    for (const void* p : {residual, norm_weight, static_cast<const void*>(sum_out), static_cast<const void*>(y)})
+      if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if (cfg->D > kNormMaxD) return MOE_ERR_UNSUPPORTED;
+  } else if (residual || sum_out || y || eps != 0.0f) {
+    return MOE_ERR_INVALID_ARG;
   }
-  if (!y || !(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
-  for (const void* p : {residual, norm_weight, static_cast<const void*>(sum_out), static_cast<const void*>(y)})
-    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
-  if (cfg->D > kNormMaxD) return MOE_ERR_UNSUPPORTED;
   if (cfg->T == 0) return MOE_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Layout L = make_layout(cfg);
   // W8A8 layers: the norm writes the 8-bit rows and their scales where the layer takes them
-  const bool a8 = is_a8(cfg);
-  if (launch_add_rms_norm(cfg->T, cfg->D, cfg->act_dtype == MOE_F32, x, residual, norm_weight, eps, sum_out, y,
-                          a8 ? ws_at(ws, L.x16) : nullptr, 0,
-                          a8 ? reinterpret_cast<float*>(ws_at(ws, L.tok_inv)) : nullptr, s) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  return run_layer(cfg, y, Wg, logit_bias, g, select_bias, a8, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, s);
+  const bool rows = norm_weight && is_a8(cfg);
+  if (norm_weight) {
+    if (launch_add_rms_norm(cfg->T, cfg->D, cfg->act_dtype == MOE_F32, x, residual, norm_weight, eps, sum_out, y,
+                            rows ? ws_at(ws, L.x16) : nullptr, 0,
+                            rows ? reinterpret_cast<float*>(ws_at(ws, L.tok_inv)) : nullptr, s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    x = y;
+  }
+  if (!few)
+    return run_layer(cfg, x, Wg, logit_bias, g, select_bias, rows, W13, static_cast<const float*>(s13), W2,
+                     static_cast<const float*>(s2), W13s, static_cast<const float*>(s13s), W2s,
+                     static_cast<const float*>(s2s), out, ws, s);
+  if (g) {
+    st = do_route(cfg, x, Wg, logit_bias, reinterpret_cast<float*>(ws_at(ws, L.off[MOE_WS_LOGITS])),
+                  reinterpret_cast<int32_t*>(ws_at(ws, L.off[MOE_WS_TOPK_IDS])),
+                  reinterpret_cast<float*>(ws_at(ws, L.off[MOE_WS_TOPK_W])),
+                  L.router_partials ? reinterpret_cast<float*>(ws_at(ws, L.router_partials)) : nullptr, err_word(ws), s,
+                  nullptr, g, select_bias);
+    if (st != MOE_OK) return st;
+  }
+  return run_few(cfg, x, g ? nullptr : Wg, logit_bias, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out, ws, s);
 }
 
 int moe_pack_weights_nk(const void* W, int64_t G, int32_t K, int32_t N, void* W_nk, void* stream) {

@@ -81,9 +81,15 @@ inline int w4_group(int dt) {
 }
 
 // ---------------------------------------------------------------- few_api.cu
+constexpr int kFewTokens = 32;  // most tokens of moe_layer_few
 // The scratch that moe_layer_few needs at the end of the workspace (0: it does
 // not take the configuration).
 size_t few_workspace_bytes(const moe_config_t* c);
+// moe_layer_few, its arguments checked and T > 0.  Wg null: the experts are chosen already, in
+// the workspace's MOE_WS_TOPK_IDS and MOE_WS_TOPK_W.
+int run_few(const moe_config_t* cfg, const void* x, const void* Wg, const float* logit_bias, const void* W13,
+            const void* s13, const void* W2, const void* s2, const void* W13s, const void* s13s, const void* W2s,
+            const void* s2s, void* out, void* ws, cudaStream_t s);
 
 // ------------------------------------------ linear_w4.cu, linear_w4_wide.cu
 struct LinearW4Scratch {

@@ -171,7 +171,13 @@ def test_block_refusals(lib):
         assert _block(lib, _cfg(), **bad) == INVALID, bad
     for bad in BAD_GATES:
         assert _block(lib, _cfg(), moe.make_gate(**bad)) == INVALID, bad
-    assert _block(lib, _cfg(w_dtype="w4_g64"), s13=P) == UNSUPPORTED
+    w4 = dict(w_dtype="w4_g64")
+    assert _block(lib, _cfg(T=33, **w4), s13=P) == UNSUPPORTED  # 4-bit weights: a few tokens
+    assert _block(lib, _cfg(T=0, **w4), s13=P) == 0
+    for c in (w4, dict(w_dtype="fp8_e4m3")):
+        assert _block(lib, _cfg(T=4, **c)) == INVALID  # no scales
+        assert _block(lib, _cfg(T=4, **c), s13=P + 8) == INVALID
+    assert _block(lib, _cfg(T=4), n=moe.moe_workspace_size(_cfg(T=4)) - 1) == WORKSPACE
     assert _block(lib, moe.make_config(4, 32776, 64, 4, 128)) == UNSUPPORTED
     assert _block(lib, _cfg(), n=1000) == WORKSPACE
 

@@ -7,6 +7,7 @@ import torch
 
 import mixture_experts_layer_gating_gb300 as moe
 from tests import _block_ref as ref
+from tests import _few_ref as few
 from tests._lib import ensure_library
 
 pytestmark = pytest.mark.gpu
@@ -485,6 +486,62 @@ def test_block_without_norm_and_gate_is_moe_layer(w):
     _, _, out = _block(cfg, None, d, ws, norm=False, sb=False)
     want = torch.empty_like(out)
     moe.moe_layer(cfg, d["x"], d["Wg"], d["lb"], d["W13"], d["s13"], d["W2"], d["s2"], d["W13s"], d["s13s"], d["W2s"], d["s2s"], want, ws)
+    assert torch.equal(out, want)
+
+
+def _few_expected(d, kind, y, ids, w, act):
+    """(out, allowed error) of a few-token layer for rows y, the chosen experts and their weights."""
+    x = y.double().cpu()
+    out, err = torch.zeros_like(x), torch.zeros_like(x)
+    cpu = {m: None if v is None else v.cpu() for m, v in d.items()}
+    k = ids.shape[1]
+    for e in ids.unique().tolist():
+        t, j = (ids == e).nonzero(as_tuple=True)
+        one = lambda s: None if s is None else s[e]  # noqa: E731
+        f, ef = few._ffn(x[t], few.dense(cpu["W13"][e], one(cpu["s13"]), kind), few.dense(cpu["W2"][e], one(cpu["s2"]), kind), act,
+                         kind != "bf16")
+        out.index_put_((t,), w[t, j, None] * f, accumulate=True)
+        err.index_put_((t,), w[t, j, None] * (ef + (k + 2) * few.U32 * f.abs()), accumulate=True)
+    if cpu["W13s"] is not None:
+        f, ef = few._ffn(x, few.dense(cpu["W13s"], cpu["s13s"], kind), few.dense(cpu["W2s"], cpu["s2s"], kind), act, kind != "bf16")
+        out, err = out + f, err + ef + 2 * few.U32 * (f.abs() + out.abs())
+    return out, err + few.BF16 * (out.abs() + err)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_nk", "w4_g32", "w4_g64", "w4_g128"])
+@pytest.mark.parametrize("T,k,Is", [(1, 4, 128), (8, 6, 0), (13, 3, 256), (32, 4, 128)])
+def test_block_of_a_few_tokens(kind, T, k, Is):
+    """4-bit weights with the choice by scores, and the other types where moe_layer_few's kernel
+    takes them: that kernel's output for the choice that moe_route_gated makes of the normed rows;
+    without a gate, moe_layer_few's bits."""
+    D, E, I = 512, 64, 256
+    if T > {"bf16": 8, "fp8_e4m3_nk": 16}.get(kind, 32):
+        pytest.skip("moe_layer's kernels")
+    w4 = kind.startswith("w4")
+    d = _block_inputs("bf16" if kind == "bf16" or w4 else "fp8_e4m3" if kind == "fp8_e4m3" else "nk", T, D, E, k, I, Is, seed=T)
+    if w4:
+        for i, (m, s) in enumerate((("W13", "s13"), ("W2", "s2"), ("W13s", "s13s"), ("W2s", "s2s"))):
+            if d[m] is not None:
+                lead, width = ((E,), I) if i < 2 else ((), Is)
+                W, _ = _weights("bf16", lead, *((D, 2 * width) if "13" in m else (width, D)), _gen(T + i))
+                d[m], d[s] = moe.quantize_w4(W, int(kind[4:]))
+    cfg = moe.make_config(T, D, E, k, I, Is, w_dtype=kind)
+    gate = moe.make_gate(n_group=8, topk_group=4, scale=2.5)
+    ws = moe.alloc_workspace(cfg)
+    sum_out, y, out = _block(cfg, gate, d, ws)
+    assert moe.moe_read_device_status(ws) == 0
+    ids = moe.workspace_view(ws, cfg, "topk_ids", (T, k), torch.int32).clone()
+    w = moe.workspace_view(ws, cfg, "topk_w", (T, k), F32).clone()
+    ws2 = moe.alloc_workspace(cfg)
+    logits, ids2, w2 = torch.empty((T, E), device="cuda"), torch.empty_like(ids), torch.empty_like(w)
+    moe.moe_route_gated(cfg, gate, y, d["Wg"], d["lb"], d["sb"], logits, ids2, w2, ws2)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    want, allowed = _few_expected(d, kind, y, ids.long().cpu(), w.double().cpu(), "swiglu")
+    _within(out.cpu(), want, allowed)
+    assert torch.equal(out, _block(cfg, gate, d, ws)[2])
+    _, y, out = _block(cfg, None, d, ws, sb=False)
+    want = torch.empty_like(out)
+    moe.moe_layer_few(cfg, y, d["Wg"], d["lb"], d["W13"], d["s13"], d["W2"], d["s2"], d["W13s"], d["s13s"], d["W2s"], d["s2s"], want, ws2)
     assert torch.equal(out, want)
 
 
