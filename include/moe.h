@@ -405,7 +405,8 @@ int moe_route_gated(const moe_config_t* cfg, const moe_gate_t* gate, const void*
  *   q_scales  [rows, D / q_group] fp32 out ([rows] for q_group 0), with q.
  * A scale is max |y| / 448 of its values (1 where all are zero, at least 2^-126, NaN where one
  * is an infinity or NaN), q = e4m3(y / scale) from y before any other rounding, nearest
- * even.  All pointers 16-byte aligned; outputs overlap nothing but as said.  NULL tensors
+ * even.  All pointers 16-byte aligned; outputs overlap nothing but as said (sum_out and y
+ * are two buffers).  NULL tensors
  * are taken when rows is 0.  No workspace. */
 int moe_add_rms_norm(int32_t rows, int32_t D, int32_t dtype, const void* x, const void* residual,
                      const void* weight, float eps, void* sum_out, void* y, void* q, int32_t q_group,
@@ -414,7 +415,7 @@ int moe_add_rms_norm(int32_t rows, int32_t D, int32_t dtype, const void* x, cons
 /* The low-rank adapter of each row's own request, beside a projection that all rows
  * share (moe_linear_w4's, or any):
  *   y[t, n] = base[t, n] + scales[a] * sum_j (sum_k x[t, k] A[a, j, k]) B[a, n, j],  a = ids[t]
- *   T         rows, >= 0.
+ *   T         rows, 0..2^30.
  *   K, N, r   inputs and outputs, multiples of 8 to 2^24; rank, a multiple of 8 to 256 (more:
  *             MOE_ERR_UNSUPPORTED).  Adapters of smaller ranks are padded with zeros.
  *   n         adapters, 1..16384 (more: MOE_ERR_UNSUPPORTED).
@@ -450,8 +451,9 @@ int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* 
  *   x, residual, sum_out, eps as in moe_add_rms_norm; the other arguments and the errors
  *   as in moe_layer (E a multiple of 8 for bf16 activations).
  * moe_layer_few's kernel takes 4-bit weights (T <= 32, else MOE_ERR_UNSUPPORTED),
- * FP8_E4M3 up to 32 tokens, FP8_E4M3_NK up to 16 and BF16 up to 8, and leaves in the
- * workspace what it does; with a gate it is given the choice of the launches before it.
+ * FP8_E4M3 up to 32 tokens, FP8_E4M3_NK up to 16 and BF16 up to 8 (with a gate 4), and
+ * leaves in the workspace what it does; with a gate it is given the choice of the
+ * launches before it.
  * FP8_E4M3_NK_A8 layers take their 8-bit rows from the norm (rounded once, from fp32),
  * instead of from y: one launch and one reading of y less. */
 int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, const void* residual,

@@ -18,7 +18,7 @@ inline bool width_ok(int v) { return v >= 8 && v % 8 == 0 && v <= kLoraMaxWidth;
 
 // MOE_OK, or why sizes are not taken
 int lora_sizes(int T, int K, int N, int r, int n) {
-  if (T < 0 || !width_ok(K) || !width_ok(N) || r < 8 || r % 8 || n < 1) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || T > (1 << 30) || !width_ok(K) || !width_ok(N) || r < 8 || r % 8 || n < 1) return MOE_ERR_INVALID_ARG;
   return r > kLoraMaxRank || n > kLoraMaxAdapters ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
@@ -34,7 +34,7 @@ int moe_add_rms_norm(int32_t rows, int32_t D, int32_t dtype, const void* x, cons
   if (q_group && D % q_group) return MOE_ERR_INVALID_ARG;
   if ((dtype != MOE_BF16 && dtype != MOE_F32) || D > kNormMaxD) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;  // (empty tensors may have no address)
-  if (!x || !weight || (!y && !q) || (q != nullptr) != (q_scales != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!x || !weight || (!y && !q) || (y && sum_out == y) || (q != nullptr) != (q_scales != nullptr)) return MOE_ERR_INVALID_ARG;
   for (const void* p : {x, residual, weight, static_cast<const void*>(sum_out), static_cast<const void*>(y),
                         static_cast<const void*>(q), static_cast<const void*>(q_scales)})
     if (!al16(p)) return MOE_ERR_INVALID_ARG;

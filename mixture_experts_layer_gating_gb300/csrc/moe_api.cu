@@ -635,12 +635,16 @@ int layer_args(const moe_config_t* cfg, const void* x, const void* Wg, const voi
   return MOE_OK;
 }
 
-// moe_block takes moe_layer_few's kernel: 4-bit weights, and where it measured faster.
-bool few_preferred(const moe_config_t* c) {
+// moe_block takes moe_layer_few's kernel: 4-bit weights, and where it measured faster (us, with
+// a gate, and so the routing by launches of its own, against moe_layer's kernels, 4 and 8 tokens:
+// 2048, 128 experts, top-8, 768, bf16 70 : 80, 96 : 103; 2816, 128, top-8, 704, shared 2112, bf16
+// 98 : 102, 152 : 142; 4096, 256, top-8, 1024, shared 1024, e4m3 98 : 165, 151 : 238, and at 32
+// tokens 371 : 570; the same [N, K] 89 : 115, 156 : 173, at 16 218 : 241, at 17 248 : 246).
+bool few_preferred(const moe_config_t* c, bool gated) {
   if (c->act_dtype != MOE_BF16) return false;
   const int most = w4_group(c->w_dtype) || c->w_dtype == MOE_FP8_E4M3 ? kFewTokens
                    : c->w_dtype == MOE_FP8_E4M3_NK                    ? 16
-                   : c->w_dtype == MOE_BF16                           ? 8
+                   : c->w_dtype == MOE_BF16                           ? (gated ? 4 : 8)
                                                                       : 0;
   return c->T <= most;
 }
@@ -908,7 +912,7 @@ int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, co
               void* sum_out, void* y, void* out, void* ws, size_t ws_bytes, void* stream) {
   int st = common_checks(cfg, ws, ws_bytes);
   if (st != MOE_OK) return st;
-  const bool few = few_preferred(cfg);
+  const bool few = few_preferred(cfg, gate != nullptr);
   if (w4_group(cfg->w_dtype) && !few) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < moe_workspace_size(cfg)) return MOE_ERR_WORKSPACE;
   st = layer_args(cfg, x, Wg, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out);
@@ -920,7 +924,8 @@ int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, co
   if (gate ? !gate_params(cfg, gate, gp) : select_bias != nullptr) return MOE_ERR_INVALID_ARG;
   const GateParams* g = gate ? &gp : nullptr;
   if (norm_weight) {
-    if (!y || !(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+    if (!y || y == x || y == residual || y == sum_out || !(eps >= 0.0f) || !std::isfinite(eps))
+      return MOE_ERR_INVALID_ARG;
     for (const void* p : {residual, norm_weight, static_cast<const void*>(sum_out), static_cast<const void*>(y)})
       if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
     if (cfg->D > kNormMaxD) return MOE_ERR_UNSUPPORTED;

@@ -20,7 +20,10 @@ def lib():
 
 
 # ------------------------------------------------------------------- norm
-def _norm(lib, rows=4, D=256, dt=moe.MOE_BF16, x=P, res=P, w=P, eps=1e-6, sum_out=P, y=P, q=P, group=0, s=P):
+Q = 1 << 21  # another
+
+
+def _norm(lib, rows=4, D=256, dt=moe.MOE_BF16, x=P, res=P, w=P, eps=1e-6, sum_out=P, y=Q, q=P, group=0, s=P):
     return lib.moe_add_rms_norm(rows, D, dt, x, res, w, eps, sum_out, y, q, group, s, None)
 
 
@@ -29,7 +32,7 @@ def test_norm_refusals(lib):
     assert _norm(lib, rows=0, x=None, res=None, w=None, sum_out=None, y=None, q=None, s=None) == 0
     for bad in ({"rows": -1}, {"D": 0}, {"D": 252}, {"eps": -1e-6}, {"eps": math.inf}, {"eps": math.nan}, {"group": 16},
                 {"group": 256}, {"D": 264, "group": 32}, {"x": None}, {"w": None}, {"y": None, "q": None, "s": None},
-                {"s": None}, {"q": None}, {"x": P + 8}, {"res": P + 2}, {"w": P + 4}, {"sum_out": P + 8}, {"y": P + 8},
+                {"s": None}, {"q": None}, {"y": P}, {"x": P + 8}, {"res": P + 2}, {"w": P + 4}, {"sum_out": P + 8}, {"y": P + 8},
                 {"q": P + 4}, {"s": P + 4}):
         assert _norm(lib, **bad) == INVALID, bad
     for bad in ({"dt": moe.MOE_FP8_E4M3}, {"dt": -1}, {"D": 32776}):
@@ -119,7 +122,7 @@ def _lora(lib, T=4, K=256, N=64, r=16, n=3, x=P, ids=P, A=P, B=P, s=P, base=P, y
 def test_lora_refusals(lib):
     assert _lora(lib, T=0) == 0
     assert _lora(lib, T=0, x=None, ids=None, y=None, base=None) == 0
-    for bad in ({"T": -1}, {"K": 0}, {"K": 252}, {"N": 12}, {"N": -8}, {"r": 0}, {"r": 12}, {"n": 0}, {"K": (1 << 24) + 8},
+    for bad in ({"T": -1}, {"T": (1 << 30) + 1}, {"K": 0}, {"K": 252}, {"N": 12}, {"N": -8}, {"r": 0}, {"r": 12}, {"n": 0}, {"K": (1 << 24) + 8},
                 {"N": (1 << 24) + 8}, {"x": None}, {"ids": None}, {"A": None}, {"B": None}, {"y": None}, {"x": P + 8},
                 {"A": P + 2}, {"B": P + 8}, {"y": P + 8}, {"base": P + 8}, {"ids": P + 2}, {"s": P + 1}):
         assert _lora(lib, **bad) == INVALID, bad
@@ -156,7 +159,7 @@ def test_lora_wrapper_compares_its_tensors(lib):
 
 
 # ------------------------------------------------------------------ block
-def _block(lib, cfg, gate=None, x=P, res=None, nw=P, eps=1e-6, sb=None, W13=P, s13=None, sum_out=None, y=P, out=P, ws=P, n=None):
+def _block(lib, cfg, gate=None, x=P, res=None, nw=P, eps=1e-6, sb=None, W13=P, s13=None, sum_out=None, y=Q, out=P, ws=P, n=None):
     return lib.moe_block(ctypes.byref(cfg), None if gate is None else ctypes.byref(gate), x, res, nw, eps, P, None, sb, W13, s13,
                          P, s13, None, None, None, None, sum_out, y, out, ws, moe.moe_workspace_size(cfg) if n is None else n, None)
 
@@ -164,7 +167,7 @@ def _block(lib, cfg, gate=None, x=P, res=None, nw=P, eps=1e-6, sb=None, W13=P, s
 def test_block_refusals(lib):
     assert _block(lib, _cfg(T=0)) == 0
     assert _block(lib, _cfg(T=0), nw=None, y=None, eps=0.0) == 0
-    for bad in ({"x": None}, {"x": P + 8}, {"W13": None}, {"out": None}, {"s13": P}, {"y": None}, {"y": P + 8}, {"nw": P + 8},
+    for bad in ({"x": None}, {"x": P + 8}, {"W13": None}, {"out": None}, {"s13": P}, {"y": None}, {"y": P}, {"y": P + 8}, {"res": Q}, {"sum_out": Q}, {"nw": P + 8},
                 {"res": P + 8}, {"sum_out": P + 8}, {"eps": -1.0}, {"eps": math.nan}, {"sb": P},
                 {"nw": None}, {"nw": None, "y": None}, {"nw": None, "y": None, "eps": 0.0, "res": P},
                 {"nw": None, "y": None, "eps": 0.0, "sum_out": P}):
@@ -217,7 +220,7 @@ def test_call_gives_the_calls_their_arguments(lib):
         a = [4] + good[1:]
         a[i] = 0
         assert lib.moe_call(moe._LORA, moe._LORA_WORDS(*a)) == -1
-    good = [0, 256, moe.MOE_BF16, P, P, P, 1e-6, P, P, P, 0, P, 0]
+    good = [0, 256, moe.MOE_BF16, P, P, P, 1e-6, P, Q, P, 0, P, 0]
     for i, bad, want in [(0, 0, 0), (1, 12, -1), (2, 9, -2), (6, -1.0, -1), (6, math.inf, -1), (10, 16, -1)]:
         a = list(good)
         a[i] = bad
