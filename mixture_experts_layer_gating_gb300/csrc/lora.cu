@@ -196,9 +196,9 @@ __device__ __forceinline__ void step32(float (&d)[4], const uint4& lo, const uin
 
 // ---------------------------------------------------- shrink, a few rows to a tile
 // planes[split][t][j] = sum over the split's k of x[t, k] A[a, j, k].  A CTA: a tile, a slice
-// of at most 64 columns, a slice of K, whose 32-wide steps its warps take in turn, two at a
-// time so that both steps' loads are under way; their sums are added in the order of the
-// warps.
+// of at most 64 columns, a slice of K, whose 32-wide steps its warps take in turn, two
+// neighbours at a time (128 bytes of a row, all under way); their sums are added in the order
+// of the warps.
 template <int NT, bool SCAN>
 __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_shrink_kernel(const LoraParams p) {
   pdl_wait();
@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_shrink_kernel(const L
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const int slice = blockIdx.y % p.slices, split = blockIdx.y / p.slices;
   const int j0 = slice * kRankSlice;
-  const int steps = (p.K + 31) / 32, s0 = static_cast<long long>(steps) * split / p.splits,
-            s1 = static_cast<long long>(steps) * (split + 1) / p.splits;
+  const int pairs = (p.K + 63) / 64, q0 = static_cast<long long>(pairs) * split / p.splits,
+            q1 = static_cast<long long>(pairs) * (split + 1) / p.splits;
   const __nv_bfloat16* A = p.A + (static_cast<size_t>(adapter) * p.r + j0) * p.K;
   float* plane = p.planes + static_cast<size_t>(split) * p.T * p.r;
   for (int m0 = 0; m0 < count; m0 += 16) {
@@ -220,12 +220,12 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_shrink_kernel(const L
     const __nv_bfloat16* x0 = p.x + static_cast<size_t>(on0 ? rows[m0 + g] : 0) * p.K;
     const __nv_bfloat16* x1 = p.x + static_cast<size_t>(on1 ? rows[m0 + 8 + g] : 0) * p.K;
     float acc[NT][4] = {};
-    for (int s = s0 + warp; s < s1; s += 2 * kLoraWarps) {
+    for (int q = q0 + warp; q < q1; q += kLoraWarps) {
       uint4 lo[2], hi[2], col[2][NT];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int k = 32 * (s + u * kLoraWarps) + 8 * tig;
-        const bool in = k < p.K && (u == 0 || s + kLoraWarps < s1);
+        const int k = 64 * q + 32 * u + 8 * tig;
+        const bool in = k < p.K;
         lo[u] = ldg16(x0 + k, in && on0);
         hi[u] = ldg16(x1 + k, in && on1);
 #pragma unroll
@@ -883,10 +883,10 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n) {
   if (q.wide) {  // of four stages at least
     q.splits = static_cast<int>(std::min<long long>({room, (K + 255) / 256, kMaxCluster}));
   } else {  // and no more than what its warps load at once need (two steps each)
-    const int steps = (K + 31) / 32, once = 2 * kLoraWarps;
-    const long long most = std::min<long long>(room, (steps + kLoraWarps - 1) / kLoraWarps);
-    const long long rounds = ((steps + most - 1) / most + once - 1) / once;
-    q.splits = static_cast<int>((steps + rounds * once - 1) / (rounds * once));
+    const int pairs = (K + 63) / 64;
+    const long long most = std::min<long long>(room, (pairs + kLoraWarps - 1) / kLoraWarps);
+    const long long rounds = ((pairs + most - 1) / most + kLoraWarps - 1) / kLoraWarps;
+    q.splits = static_cast<int>((pairs + rounds * kLoraWarps - 1) / (rounds * kLoraWarps));
   }
   // y's columns: as many CTAs as have room, a block of 32 columns at least for each warp
   const int unit = q.wide ? 64 : 32 * kLoraWarps, units = (N + unit - 1) / unit;
