@@ -104,7 +104,8 @@ __device__ __forceinline__ float e4m3_scale(uint32_t largest) {
                                : __uint_as_float(0x7fffffffu);
 }
 __device__ __forceinline__ uint2 e4m3_codes(const float (&f)[8], float scale) {
-  const float inv = 1.0f / scale;
+  float inv;  // (to an ulp: far below a step of e4m3; scale is normal, or NaN)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
   uint32_t u[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
