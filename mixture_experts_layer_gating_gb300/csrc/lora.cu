@@ -199,59 +199,71 @@ __device__ __forceinline__ void step32(float (&d)[4], const uint4& lo, const uin
 // of at most 64 columns, a slice of K, whose 32-wide steps its warps take in turn, two
 // neighbours at a time (128 bytes of a row, all under way); their sums are added in the order
 // of the warps.
+template <int NT>
+using ShrinkRed = float[kLoraWarps][32][4 * NT + 1];
+// out(i, c, sum) for rows m0 + i, i < 16, of the tile and columns j0 + c, c < 8 NT, over pairs of
+// steps [q0, q1); every output by one thread, behind a barrier.
+template <int NT, typename Out>
+__device__ __forceinline__ void shrink_rows(const LoraParams& p, const __nv_bfloat16* A, int j0, const int* rows,
+                                            int count, int m0, int q0, int q1, ShrinkRed<NT>& red, const Out& out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const bool on0 = m0 + g < count, on1 = m0 + 8 + g < count;
+  const __nv_bfloat16* x0 = p.x + static_cast<size_t>(on0 ? rows[m0 + g] : 0) * p.K;
+  const __nv_bfloat16* x1 = p.x + static_cast<size_t>(on1 ? rows[m0 + 8 + g] : 0) * p.K;
+  float acc[NT][4] = {};
+  constexpr int P = NT == 2 ? 2 : 1;  // pairs whose loads are under way at a time (what registers allow)
+  for (int q = q0 + warp; q < q1; q += P * kLoraWarps) {
+    uint4 lo[2 * P], hi[2 * P], col[2 * P][NT];
+#pragma unroll
+    for (int u = 0; u < 2 * P; ++u) {
+      const int at = q + u / 2 * kLoraWarps, k = 64 * at + 32 * (u % 2) + 8 * tig;
+      const bool in = k < p.K && at < q1;
+      lo[u] = ldg16(x0 + k, in && on0);
+      hi[u] = ldg16(x1 + k, in && on1);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        col[u][j] = ldg16(A + static_cast<size_t>(8 * j + g) * p.K + k, in && j0 + 8 * j < p.r);
+    }
+#pragma unroll
+    for (int u = 0; u < 2 * P; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) step32(acc[j], lo[u], hi[u], col[u][j]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[warp][lane][4 * j + i] = acc[j][i];
+  __syncthreads();
+  for (int o = threadIdx.x; o < 16 * 8 * NT; o += kLoraWarps * 32) {
+    const int i = o / (8 * NT), c = o % (8 * NT);  // row and column of the 16 x 8 NT tile
+    const int l = 4 * (i & 7) + ((c & 7) >> 1), e = 4 * (c >> 3) + 2 * (i >> 3) + (c & 1);
+    float v = red[0][l][e];
+#pragma unroll
+    for (int w = 1; w < kLoraWarps; ++w) v += red[w][l][e];
+    out(i, c, v);
+  }
+}
+
 template <int NT, bool SCAN>
 __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_shrink_kernel(const LoraParams p) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ int rows[SCAN ? kLoraScanRows : 16];
   __shared__ int slot[2];
-  __shared__ float red[kLoraWarps][32][4 * NT + 1];
+  __shared__ ShrinkRed<NT> red;
   int adapter, count;
   if (!lora_tile<SCAN>(p, blockIdx.x, rows, slot, adapter, count) || adapter < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const int slice = blockIdx.y % p.slices, split = blockIdx.y / p.slices;
   const int j0 = slice * kRankSlice;
   const int pairs = (p.K + 63) / 64, q0 = static_cast<long long>(pairs) * split / p.splits,
             q1 = static_cast<long long>(pairs) * (split + 1) / p.splits;
   const __nv_bfloat16* A = p.A + (static_cast<size_t>(adapter) * p.r + j0) * p.K;
   float* plane = p.planes + static_cast<size_t>(split) * p.T * p.r;
-  for (int m0 = 0; m0 < count; m0 += 16) {
-    const bool on0 = m0 + g < count, on1 = m0 + 8 + g < count;
-    const __nv_bfloat16* x0 = p.x + static_cast<size_t>(on0 ? rows[m0 + g] : 0) * p.K;
-    const __nv_bfloat16* x1 = p.x + static_cast<size_t>(on1 ? rows[m0 + 8 + g] : 0) * p.K;
-    float acc[NT][4] = {};
-    for (int q = q0 + warp; q < q1; q += kLoraWarps) {
-      uint4 lo[2], hi[2], col[2][NT];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int k = 64 * q + 32 * u + 8 * tig;
-        const bool in = k < p.K;
-        lo[u] = ldg16(x0 + k, in && on0);
-        hi[u] = ldg16(x1 + k, in && on1);
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          col[u][j] = ldg16(A + static_cast<size_t>(8 * j + g) * p.K + k, in && j0 + 8 * j < p.r);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) step32(acc[j], lo[u], hi[u], col[u][j]);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[warp][lane][4 * j + i] = acc[j][i];
-    __syncthreads();
-    for (int o = threadIdx.x; o < 16 * 8 * NT; o += kLoraWarps * 32) {
-      const int i = o / (8 * NT), c = o % (8 * NT);  // row and column of the 16 x 8 NT tile
-      const int l = 4 * (i & 7) + ((c & 7) >> 1), e = 4 * (c >> 3) + 2 * (i >> 3) + (c & 1);
-      float v = red[0][l][e];
-#pragma unroll
-      for (int w = 1; w < kLoraWarps; ++w) v += red[w][l][e];
+  for (int m0 = 0; m0 < count; m0 += 16)
+    shrink_rows<NT>(p, A, j0, rows, count, m0, q0, q1, red, [&](int i, int c, float v) {
       if (m0 + i < count && j0 + c < p.r) plane[static_cast<size_t>(rows[m0 + i]) * p.r + j0 + c] = v;
-    }
-  }
+    });
 }
 
 // y = base + f for 8 neighbouring values; b: the base's, as loaded (not read where !has).
@@ -349,8 +361,15 @@ __device__ __forceinline__ void split_terms(float (&f)[8], uint4 (&t)[TERMS]) {
 // so that a thread's four of them hold eight neighbouring columns of y.  The first block's
 // part of B is loaded before the planes are waited for: of what this launch reads only they
 // come from the one before it, which itself began after all that went before.
-template <int TERMS, bool SCAN, typename Ty>
+//
+// NT > 0: there is no launch before; every CTA makes v itself (ranks up to 8 NT), which takes
+// less than a launch and a hand-over where A is small.
+template <int TERMS, bool SCAN, typename Ty, int NT = 0>
 __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_expand_kernel(const LoraParams p) {
+  if (NT > 0) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   __shared__ int rows[SCAN ? kLoraScanRows : 16];
   __shared__ int slot[2];
   extern __shared__ __align__(16) __nv_bfloat16 vs[];  // [TERMS][16][ld]
@@ -380,42 +399,59 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_expand_kernel(const L
   if (!tile) return;  // (at once, to make room; a tile there is)
   const int n_first = c0 + 32 * warp;
   if (adapter >= 0) {
-    load_step(n_first, 0);
-    // the base, and the second block's rows of B, as far as L2
+    if (NT == 0) load_step(n_first, 0);
+    // the base, and the second block's (without v: the first one's too) rows of B, as far as L2
     if (base) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (8 * h + g < count && n_first + 8 * tig < c1) prefetch_l2(base + static_cast<size_t>(rows[8 * h + g]) * p.N + n_first + 8 * tig);
     }
-    const int n = n_first + 32 * kLoraWarps + lane;
-    if (n < c1)
+    for (int n = n_first + lane + (NT > 0 ? 0 : 32 * kLoraWarps); n < min(c1, n_first + 32 * kLoraWarps + 32);
+         n += 32 * kLoraWarps)
       for (int k = 0; k < p.r; k += 64) prefetch_l2(B + static_cast<size_t>(n) * p.r + k);
   }
   const float scale = p.scales && adapter >= 0 ? p.scales[adapter] : 1.0f;
-  pdl_wait();
-  pdl_launch_dependents();
+  if (NT == 0) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   if (adapter < 0) {
     copy_rows(base, y, rows, count, p.N, c0, c1);
     return;
   }
   constexpr int W = sizeof(Ty) / 2;  // 16-byte words of eight values
   for (int m0 = 0; m0 < count; m0 += 16) {
-    if (m0) {
-      __syncthreads();
+    if (m0) __syncthreads();
+    if constexpr (NT > 0) {
+      __shared__ ShrinkRed<NT> red;
+      auto put = [&](int i, int c, float v) {
+        v *= scale;
+#pragma unroll
+        for (int z = 0; z < TERMS; ++z) {
+          const __nv_bfloat16 h = __float2bfloat16_rn(v);
+          vs[(z * 16 + i) * ld + c] = h;
+          const float f = __bfloat162float(h);
+          v = isfinite(f) ? v - f : 0.0f;  // (as split_terms)
+        }
+      };
+      for (int o = threadIdx.x; o < 16 * (rp - 8 * NT); o += kLoraWarps * 32) put(o % 16, 8 * NT + o / 16, 0.0f);
+      shrink_rows<NT>(p, p.A + static_cast<size_t>(adapter) * p.r * p.K, 0, rows, count, m0, 0, (p.K + 63) / 64, red, put);
       load_step(n_first, 0);
-    }
-    for (int o = threadIdx.x; o < 2 * rp; o += kLoraWarps * 32) {
-      const int i = o / (rp / 8), j = o % (rp / 8) * 8;
-      float f[8] = {};
-      if (m0 + i < count && j < p.r) {
-        sum_planes(p, rows[m0 + i], j, f);
+    } else {
+      if (m0) load_step(n_first, 0);
+      for (int o = threadIdx.x; o < 2 * rp; o += kLoraWarps * 32) {
+        const int i = o / (rp / 8), j = o % (rp / 8) * 8;
+        float f[8] = {};
+        if (m0 + i < count && j < p.r) {
+          sum_planes(p, rows[m0 + i], j, f);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] *= scale;
+          for (int q = 0; q < 8; ++q) f[q] *= scale;
+        }
+        uint4 t[TERMS];
+        split_terms<TERMS>(f, t);
+#pragma unroll
+        for (int z = 0; z < TERMS; ++z) *reinterpret_cast<uint4*>(vs + (z * 16 + i) * ld + j) = t[z];
       }
-      uint4 t[TERMS];
-      split_terms<TERMS>(f, t);
-#pragma unroll
-      for (int z = 0; z < TERMS; ++z) *reinterpret_cast<uint4*>(vs + (z * 16 + i) * ld + j) = t[z];
     }
     __syncthreads();
     for (int n0 = n_first; n0 < c1; n0 += 32 * kLoraWarps) {
@@ -858,10 +894,10 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
 
 constexpr int kSms = 152;  // a constant: results must not depend on the device
 
-// How T rows of n adapters are taken: `scan`, tiles found by the CTAs themselves; `wide`, the
-// kernels for many rows to a tile.
+// How T rows of n adapters are taken: `scan`, tiles found by the CTAs themselves; `at_once`,
+// these in one launch; `wide`, the kernels for many rows to a tile.
 struct LoraPlan {
-  bool scan, wide;
+  bool scan, at_once, wide;
   int tile_rows, tiles, slices, splits, chunk;
 };
 LoraPlan lora_plan(int T, int K, int N, int r, int n) {
@@ -873,6 +909,10 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n) {
   q.wide = T >= 1024 && T >= (T >= 2048 ? 32ll : 64ll) * n;
   q.tile_rows = q.wide ? kWideRows : 16;
   q.tiles = q.scan ? T : static_cast<int>(std::min<long long>(T, (T + q.tile_rows - 1ll) / q.tile_rows + n));
+  // one launch instead of two: as long on the GPU (us of two : of one, 1, 16, 32, 64 rows with
+  // adapters of their own: 2048 x 2048, rank 16 4.7 : 4.9, 5.4 : 5.1, 5.8 : 6.1, 7.1 : 7.1; 4096 x
+  // 4096, rank 16 5.1 : 6.1, 6.1 : 7.7, 7.2 : 8.7, 8.2 : 9.7), and 1.5 less of the caller's time
+  q.at_once = T <= 32 && r <= 32 && static_cast<long long>(r) * K <= 32768;
   // adapters that some row has, about, and tiles
   const long long used = std::min<long long>(T, static_cast<long long>(n) * T / (T + n / 2));
   const long long tiles =
@@ -906,7 +946,7 @@ LoraLayout lora_layout(const LoraPlan& q, int T, int r) {
     cur = (cur + bytes + 255) / 256 * 256;
     return o;
   };
-  L.planes = take(static_cast<size_t>(q.wide ? 1 : q.splits) * T * r * 4);
+  if (!q.at_once) L.planes = take(static_cast<size_t>(q.wide ? 1 : q.splits) * T * r * 4);
   if (!q.scan) {
     L.order = take(static_cast<size_t>(q.tiles) * q.tile_rows * 4);
     L.tiles = take(static_cast<size_t>(q.tiles) * sizeof(LoraTile));
@@ -927,6 +967,9 @@ cudaError_t allow_smem(size_t most) {
   return e;
 }
 
+size_t expand_smem(const LoraParams& p, bool y_f32) {
+  return static_cast<size_t>(y_f32 ? 3 : 2) * 16 * ((p.r + 31) / 32 * 32 + 8) * 2;
+}
 template <bool SCAN>
 cudaError_t products(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStream_t s) {
   const dim3 block(kLoraWarps * 32), grid(q.tiles, p.splits * p.slices), egrid(q.tiles, (p.N + p.chunk - 1) / p.chunk);
@@ -934,8 +977,15 @@ cudaError_t products(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStr
   cudaError_t e = launch_kernel(shrink, grid, block, 0, s, p);
   if (e != cudaSuccess) return e;
   auto expand = y_f32 ? lora_expand_kernel<3, SCAN, float> : lora_expand_kernel<2, SCAN, __nv_bfloat16>;
-  const size_t smem = static_cast<size_t>(y_f32 ? 3 : 2) * 16 * ((p.r + 31) / 32 * 32 + 8) * 2;
-  e = launch_kernel(expand, egrid, block, smem, s, p);
+  e = launch_kernel(expand, egrid, block, expand_smem(p, y_f32), s, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+// Both products in one launch (few rows, small adapters).
+template <int NT>
+cudaError_t products_at_once(const LoraParams& p, const LoraPlan& q, bool y_f32, cudaStream_t s) {
+  auto kern = y_f32 ? lora_expand_kernel<3, true, float, NT> : lora_expand_kernel<2, true, __nv_bfloat16, NT>;
+  const cudaError_t e = launch_kernel(kern, dim3(q.tiles, (p.N + p.chunk - 1) / p.chunk), dim3(kLoraWarps * 32),
+                                      expand_smem(p, y_f32), s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1003,6 +1053,7 @@ cudaError_t launch_lora(int T, int K, int N, int r, int n, const void* x, const 
   p.splits = q.splits;
   p.slices = q.slices;
   p.chunk = q.chunk;
+  if (q.at_once) return r <= 16 ? products_at_once<2>(p, q, y_f32, s) : products_at_once<4>(p, q, y_f32, s);
   if (q.scan) return products<true>(p, q, y_f32, s);
   const size_t smem = static_cast<size_t>(n + 1) * 4;
   cudaError_t e = allow_smem<lora_plan_kernel>(static_cast<size_t>(kLoraMaxAdapters + 1) * 4);

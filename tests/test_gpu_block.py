@@ -322,7 +322,8 @@ def _check_lora(d, dt, base=True, scales=True, in_place=False):
 
 @pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("T,K,N,r,n,how", [
-    (1, 8, 8, 8, 1, "one"), (1, 2048, 2048, 16, 8, "one"), (2, 264, 40, 24, 2, "mixed"), (17, 1000, 1032, 8, 1, "one"),
+    (1, 8, 8, 8, 1, "one"), (1, 2048, 2048, 16, 8, "one"), (1, 2056, 520, 16, 3, "mixed"), (5, 1000, 520, 32, 4, "mixed"),
+    (32, 1024, 264, 24, 2, "mixed"), (31, 4096, 1032, 8, 31, "mixed"), (33, 256, 264, 16, 4, "mixed"), (30, 512, 40, 16, 3, "none"), (2, 264, 40, 24, 2, "mixed"), (17, 1000, 1032, 8, 1, "one"),
     (33, 512, 264, 64, 3, "mixed"), (61, 1024, 520, 64, 40, "mixed"), (64, 256, 512, 128, 64, "mixed"), (64, 256, 256, 72, 2, "none"),
     (65, 256, 264, 16, 1, "one"), (100, 328, 776, 40, 90, "mixed"), (129, 512, 256, 32, 2, "runs"), (300, 256, 1544, 256, 5, "mixed"),
     (1000, 512, 320, 64, 4, "runs"), (1025, 136, 128, 24, 1, "none"), (2000, 256, 264, 16, 1500, "mixed"), (513, 64, 64, 200, 16, "mixed"),
@@ -423,6 +424,8 @@ def test_lora_offsets_that_pass_32_bits():
     y = _lora(d, torch.empty_like(d["base"]), d["base"])
     y64, allowed = ref.lora(d["x"][rows], d["ids"][rows], d["A"], d["B"], d["scales"], d["base"][rows], BF16)
     _within(y[rows], y64, allowed)
+    few = dict(d, x=d["x"][rows].contiguous(), ids=d["ids"][rows].contiguous(), base=d["base"][rows].contiguous())
+    _within(_lora(few, torch.empty_like(few["base"]), few["base"]), y64, allowed)  # the few-row kernels
     d["ids"][rows] = -1
     bare = d["ids"] == -1
     y[rows] = 0
