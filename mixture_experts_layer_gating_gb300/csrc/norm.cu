@@ -4,7 +4,12 @@
 //   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight
 //
 // Bound by memory: every row is read once and held in registers, a group of threads to a
-// row, from the sum of squares to the stores.
+// row, from the sum of squares to the stores.  Measured (one GB300, inputs rotated so that
+// they come from HBM; share of what a copy reaches): 16384 x 8192 bf16 with residual, sum, y
+// and e4m3 rows 195 us (6.2 TB/s, 0.91), 8192 x 4096 the same 51 us (0.87), 4096 x 2048 fp32
+// 13.6 us (0.73: launch and first bytes are 3 of them), one row of 2048 2.3 us.  Four vectors
+// of 8 values a thread and 16 warps an SM: with two vectors and more warps 206 us, 67 us, 15.1
+// us; with the row read again for the norm it would move a third more.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
