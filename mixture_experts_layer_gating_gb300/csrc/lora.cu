@@ -923,7 +923,7 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n) {
   // 4096, rank 16 5.1 : 6.1, 6.1 : 7.7, 7.2 : 8.7, 8.2 : 9.7), and 1.5 less of the caller's time
   q.at_once = T <= 32 && r <= 32 && static_cast<long long>(r) * K <= 32768;
   // adapters that some row has, about, and tiles
-  const long long used = std::min<long long>(T, static_cast<long long>(n) * T / (T + n / 2));
+  const long long used = std::min<long long>(T, static_cast<long long>(n) * T / std::max(1, T + n / 2));
   const long long tiles =
       std::max(1ll, q.scan ? used : q.wide ? (T + q.tile_rows - 1) / q.tile_rows + n / 2 : used + T / 32);
   q.slices = q.wide ? 1 : (r + kRankSlice - 1) / kRankSlice;

@@ -120,7 +120,10 @@ def _lora(lib, T=4, K=256, N=64, r=16, n=3, x=P, ids=P, A=P, B=P, s=P, base=P, y
 
 
 def test_lora_refusals(lib):
-    assert _lora(lib, T=0) == 0
+    for n in (1, 2, 16384):
+        assert _lora(lib, T=0, n=n) == 0
+        for T in (0, 1, 64, 65, 1 << 30):
+            assert moe.moe_lora_workspace_size(T, 1 << 24, 8, 256, n) > 0
     assert _lora(lib, T=0, x=None, ids=None, y=None, base=None) == 0
     for bad in ({"T": -1}, {"T": (1 << 30) + 1}, {"K": 0}, {"K": 252}, {"N": 12}, {"N": -8}, {"r": 0}, {"r": 12}, {"n": 0}, {"K": (1 << 24) + 8},
                 {"N": (1 << 24) + 8}, {"x": None}, {"ids": None}, {"A": None}, {"B": None}, {"y": None}, {"x": P + 8},
