@@ -425,7 +425,8 @@ int moe_add_rms_norm(int32_t rows, int32_t D, int32_t dtype, const void* x, cons
  *   A, B      [n, r, K] and [n, N, r] bf16.
  *   scales    [n] fp32, or NULL: 1.
  *   base      [T, N] of y's type, y itself (in place), or NULL: 0.
- *   y         [T, N] bf16 or fp32 (y_dtype), one rounding.
+ *   y         [T, N] bf16 or fp32 (y_dtype), one rounding.  Overlaps nothing else (y == x:
+ *             MOE_ERR_INVALID_ARG).
  *   ws        moe_lora_workspace_size(T, K, N, r, n) bytes (0: sizes not taken),
  *             256-byte aligned; holds nothing between calls but the control block
  *             (its first 256 bytes, zero-filled once), which takes the device error word.

@@ -58,7 +58,7 @@ int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* 
   if (T == 0) return MOE_OK;  // (empty tensors may have no address)
   for (const void* p : {x, A, B, static_cast<const void*>(y)})
     if (!p || !al16(p)) return MOE_ERR_INVALID_ARG;
-  if (!ids || !al4(ids) || !al4(scales) || !al16(base)) return MOE_ERR_INVALID_ARG;
+  if (!ids || !al4(ids) || !al4(scales) || !al16(base) || y == x) return MOE_ERR_INVALID_ARG;
   const cudaError_t e = launch_lora(T, K, N, r, n, x, ids, A, B, scales, base, y, y_dtype == MOE_F32,
                                     static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

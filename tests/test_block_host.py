@@ -139,6 +139,14 @@ def test_lora_refusals(lib):
         assert moe.moe_lora_workspace_size(*bad) == 0
 
 
+def test_lora_does_not_write_its_input(lib):
+    assert _lora(lib, K=64, N=64, x=P, y=P, base=P) == INVALID  # rows would be read after they are written
+    assert _lora(lib, T=0, K=64, N=64, x=P, y=P, base=P) == 0
+    for bad in ({"x": None}, {"ids": None}, {"A": None}, {"B": None}, {"y": None}, {"x": P + 8}, {"A": P + 2}, {"B": P + 8},
+                {"y": Q + 8}, {"base": P + 8}, {"ids": P + 2}, {"s": P + 1}):  # refused with a y of its own too
+        assert _lora(lib, **{"y": Q, **bad}) == INVALID, bad
+
+
 def test_lora_wrapper_compares_its_tensors(lib):
     T, K, N, r, n = 3, 64, 24, 8, 2
     good = dict(x=torch.zeros(T, K).bfloat16(), ids=torch.zeros(T, dtype=torch.int32), A=torch.zeros(n, r, K).bfloat16(),
