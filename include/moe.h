@@ -466,7 +466,7 @@ int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, co
 /* One of the calls above with its arguments in a block of 8-byte words, in their
  * order: integers and addresses (0: NULL) as they are, eps as a double.  For bindings
  * that take longer for a call the more arguments it has; same results and errors,
- * MOE_ERR_INVALID_ARG for another call or NULL words. */
+ * MOE_ERR_INVALID_ARG for another call, NULL words or an int32 argument of more bits. */
 #define MOE_CALL_ADD_RMS_NORM 0
 #define MOE_CALL_ROUTE_GATED 1
 #define MOE_CALL_LORA 2

@@ -73,7 +73,12 @@ int moe_call(int32_t call, const void* words) {
     at += sizeof(v);
     return v;
   };
-  auto i32 = [&]() { return static_cast<int32_t>(word()); };
+  bool fits = true;  // no integer of more than 32 bits
+  auto i32 = [&]() {
+    const int64_t v = word();
+    fits = fits && v == static_cast<int32_t>(v);
+    return static_cast<int32_t>(v);
+  };
   auto ptr = [&]() { return reinterpret_cast<void*>(word()); };
   switch (call) {
     case MOE_CALL_ADD_RMS_NORM: {
@@ -85,6 +90,7 @@ int moe_call(int32_t call, const void* words) {
       void *sum_out = ptr(), *y = ptr(), *q = ptr();
       const int32_t group = i32();
       float* scales = static_cast<float*>(ptr());
+      if (!fits) return MOE_ERR_INVALID_ARG;
       return moe_add_rms_norm(rows, D, dtype, x, residual, weight, static_cast<float>(eps), sum_out, y, q, group,
                               scales, ptr());
     }
@@ -111,6 +117,7 @@ int moe_call(int32_t call, const void* words) {
       const int32_t y_dtype = i32();
       void* ws = ptr();
       const size_t bytes = static_cast<size_t>(word());
+      if (!fits) return MOE_ERR_INVALID_ARG;
       return moe_lora(T, K, N, r, n, x, ids, A, B, scales, base, y, y_dtype, ws, bytes, ptr());
     }
     default: return MOE_ERR_INVALID_ARG;

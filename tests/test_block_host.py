@@ -250,6 +250,19 @@ def test_call_gives_the_calls_their_arguments(lib):
     assert lib.moe_call(3, moe._LORA_WORDS(*range(16))) == -1 and lib.moe_call(0, None) == -1
 
 
+def test_call_takes_no_integer_of_more_than_32_bits(lib):
+    lora = [0, 256, 64, 16, 3, P, P, P, P, P, P, Q, moe.MOE_BF16, P, 1 << 40, 0]
+    norm = [0, 256, moe.MOE_BF16, P, P, P, 1e-6, P, Q, P, 0, P, 0]
+    for call, words, good, places in ((moe._LORA, moe._LORA_WORDS, lora, (0, 1, 2, 3, 4, 12)),
+                                      (moe._NORM, moe._NORM_WORDS, norm, (0, 1, 2, 10))):
+        assert lib.moe_call(call, words(*good)) == 0
+        for i in places:
+            for add in (1 << 32, -1 << 32, 1 << 40):
+                a = list(good)
+                a[i] += add
+                assert lib.moe_call(call, words(*a)) == INVALID, (call, i)
+
+
 # -------------------------------------------------------------- reference
 def test_gate_reference_on_hand_written_rows():
     l = torch.tensor([[0.0, 2.0, 2.0, -1.0, 3.0, float("nan"), 1.0, 1.0]])
