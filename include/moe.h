@@ -446,6 +446,7 @@ int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* 
  *               and y NULL, eps 0).
  *   y           [T, D] act_dtype out: the normed rows, which the router projects.  May
  *               not overlap anything else.
+ *   sum_out     and out are two buffers.
  *   s13, s2, s13s, s2s  fp32 per column (e4m3 weights), bf16 per row and group (4-bit
  *               weights, as moe_layer_few has them), or NULL.
  *   ws          moe_workspace_size(cfg) bytes.

@@ -924,7 +924,8 @@ int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, co
   if (gate ? !gate_params(cfg, gate, gp) : select_bias != nullptr) return MOE_ERR_INVALID_ARG;
   const GateParams* g = gate ? &gp : nullptr;
   if (norm_weight) {
-    if (!y || y == x || y == residual || y == sum_out || !(eps >= 0.0f) || !std::isfinite(eps))
+    if (!y || y == x || y == residual || y == sum_out || y == out || sum_out == out ||
+        !(eps >= 0.0f) || !std::isfinite(eps))
       return MOE_ERR_INVALID_ARG;
     for (const void* p : {residual, norm_weight, static_cast<const void*>(sum_out), static_cast<const void*>(y)})
       if (!aligned16(p)) return MOE_ERR_INVALID_ARG;

@@ -196,6 +196,13 @@ def test_block_refusals(lib):
     assert _block(lib, _cfg(), n=1000) == WORKSPACE
 
 
+def test_block_outputs_are_three_buffers(lib):
+    R = 1 << 22
+    for bad in ({"y": Q, "out": Q}, {"sum_out": R, "out": R}):
+        assert _block(lib, _cfg(), **bad) == INVALID, bad
+    assert _block(lib, _cfg(T=0), y=Q, out=R, sum_out=P) == 0
+
+
 def test_block_wrapper_compares_its_tensors(lib):
     T, D, E = 3, 256, 64
     cfg = _cfg(T=T)
