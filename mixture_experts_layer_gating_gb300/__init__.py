@@ -441,7 +441,7 @@ def moe_route_gated(cfg, gate, x, Wg, logit_bias, select_bias, logits, topk_ids,
     st = load_library().moe_call(_ROUTE_GATED, _ROUTE_GATED_WORDS(
         ctypes.addressof(cfg), 0 if gate is None else ctypes.addressof(gate), _address(x, device), _address(Wg, device),
         _address(logit_bias, device), _address(select_bias, device), _address(logits, device), _address(topk_ids, device),
-        _address(topk_w, device), _address(ws, device), ws.nbytes, s))
+        _address(topk_w, device), _address(ws, device), getattr(ws, "nbytes", 0), s))
     if st:
         _check("moe_route_gated", st)
 
@@ -460,7 +460,7 @@ def moe_block(cfg, gate, x, residual, norm_weight, eps, Wg, logit_bias, select_b
     a = [_address(t, device) for t in (x, residual, norm_weight, Wg, logit_bias, select_bias, W13, s13, W2, s2, W13s, s13s,
                                        W2s, s2s, sum_out, y, out, ws)]
     _check("moe_block", load_library().moe_block(
-        ctypes.byref(cfg), None if gate is None else ctypes.byref(gate), *a[:3], eps, *a[3:], ws.nbytes, s))
+        ctypes.byref(cfg), None if gate is None else ctypes.byref(gate), *a[:3], eps, *a[3:], getattr(ws, "nbytes", 0), s))
 
 
 def moe_add_rms_norm(rows: int, D: int, x, residual, weight, eps: float, sum_out, y, q=None, q_scales=None,
@@ -508,7 +508,7 @@ def moe_lora(T: int, K: int, N: int, r: int, n: int, x, ids, A, B, scales, base,
     st = load_library().moe_call(_LORA, _LORA_WORDS(
         T, K, N, r, n, _address(x, device), _address(ids, device), _address(A, device), _address(B, device),
         _address(scales, device), to if base is y else _address(base, device), to, y_dtype, _address(ws, device),
-        ws.nbytes, s))
+        getattr(ws, "nbytes", 0), s))
     if st:
         _check("moe_lora", st)
 

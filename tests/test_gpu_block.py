@@ -266,6 +266,19 @@ def test_gate_from_rows(T, D, E, k, fused):
         moe.moe_set_option(moe.MOE_OPT_FUSED_ROUTING, old)
 
 
+@pytest.mark.parametrize("T,D,E,k", [(5, 64, 30, 3), (70, 72, 7, 7), (33, 256, 512, 16)])
+def test_gate_from_rows_in_32_bits(T, D, E, k):
+    g = _gen(E)
+    x, Wg, sb = _normal((T, D), 1, g, F32), _normal((D, E), 0.1, g, F32), _normal((E,), 0.2, g, F32)
+    cfg = moe.make_config(T, D, E, k, 8, act_dtype="f32", w_dtype="f32")
+    ws, logits = moe.alloc_workspace(cfg), torch.empty((T, E), device="cuda")
+    ids, w = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+    moe.moe_route_gated(cfg, moe.make_gate(), x, Wg, None, sb, logits, ids, w, ws)
+    _within(logits, x.double() @ Wg.double(), (D + 20) * 2 * ref.U * (x.double().abs() @ Wg.double().abs()))
+    again, w2 = _gate(logits.clone(), sb, k, moe.make_gate())
+    assert torch.equal(ids, again) and torch.equal(w, w2)
+
+
 def test_gate_of_softmax_is_moe_route():
     """Without bias, groups and factor the choice is moe_route's."""
     for T, E, k in ((3, 48, 5), (100, 128, 8), (257, 512, 10)):
@@ -330,7 +343,8 @@ def _check_lora(d, dt, base=True, scales=True, in_place=False):
     (700, 520, 1288, 96, 6, "mixed"), (400, 264, 136, 128, 2, "runs"), (5000, 1000, 1000, 40, 3, "mixed"), (260, 136, 2056, 16, 2, "mixed"),
     (3000, 4104, 72, 8, 7, "runs"), (90, 72, 8, 256, 1, "one"), (1024, 64, 64, 200, 16, "mixed"), (1500, 256, 1544, 256, 5, "mixed"),
     (1100, 520, 1288, 96, 6, "mixed"), (2100, 264, 136, 128, 2, "runs"), (1300, 136, 2056, 16, 2, "mixed"), (1024, 72, 8, 256, 1, "one"),
-    (9000, 200, 104, 16, 30, "mixed"), (2049, 512, 264, 32, 64, "mixed"), (1023, 512, 264, 32, 2, "mixed")])
+    (9000, 200, 104, 16, 30, "mixed"), (1024, 2048, 64, 256, 2, "mixed"), (1030, 4104, 72, 136, 1, "one"), (1100, 1032, 200, 64, 9, "mixed"),
+    (2049, 512, 264, 32, 64, "mixed"), (1023, 512, 264, 32, 2, "mixed")])
 def test_lora(T, K, N, r, n, how, dt):
     d = _lora_inputs(T, K, N, r, n, dt, T + K + N + r, how)
     y = _check_lora(d, dt)
@@ -430,6 +444,25 @@ def test_lora_offsets_that_pass_32_bits():
     bare = d["ids"] == -1
     y[rows] = 0
     assert not bool(y[bare].any())
+
+
+def test_no_workspace_is_refused():
+    """None for ws: the library's error, as the other calls have it, and nothing written."""
+    g = _gen(3)
+    T, K, N, r, n = 3, 64, 24, 8, 2
+    x, A, B = _normal((T, K), 1, g), _normal((n, r, K), 1, g), _normal((n, N, r), 1, g)
+    ids, y = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.full((T, N), 7.0, dtype=BF16, device="cuda")
+    cfg = moe.make_config(T, K, 16, 2, 16)
+    logits, chosen, w = _normal((T, 16), 1, g, F32), torch.full((T, 2), -3, dtype=torch.int32, device="cuda"), torch.empty((T, 2), device="cuda")
+    with pytest.raises(moe.MoEError, match="workspace"):
+        moe.moe_lora(T, K, N, r, n, x, ids, A, B, None, None, y, None)
+    with pytest.raises(moe.MoEError, match="workspace"):
+        moe.moe_route_gated(cfg, moe.make_gate(), None, None, None, None, logits, chosen, w, None)
+    W13, W2, Wg = _normal((16, K, 32), 1, g), _normal((16, 16, K), 1, g), _normal((K, 16), 1, g)
+    out = torch.full_like(x, 7.0)
+    with pytest.raises(moe.MoEError, match="workspace"):
+        moe.moe_block(cfg, None, x, None, None, 0.0, Wg, None, None, W13, None, W2, None, None, None, None, None, None, None, out, None)
+    assert bool((y == 7).all()) and bool((out == 7).all()) and bool((chosen == -3).all())
 
 
 # ------------------------------------------------------------------ block
