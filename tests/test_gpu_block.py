@@ -704,3 +704,67 @@ def test_a_served_step():
     step()
     torch.cuda.synchronize()
     assert torch.equal(logits, got) and not torch.equal(got, want)
+
+
+def _three_calls(T, seed):
+    """Norm, choice and adapters of T rows: inputs of their own, and a function that runs them in given workspaces."""
+    D, E, k, N, r, n = 512, 64, 6, 520, 40, 5
+    g, gate, cfg = _gen(seed), moe.make_gate(n_group=8, topk_group=4), moe.make_config(T, 512, 64, 6, 16)
+    ld, Wg, sb = _lora_inputs(T, D, N, r, n, F32, seed, "mixed"), _normal((D, E), 0.1, g), _normal((E,), 0.2, g, F32)
+    x, res, w = _normal((T, D), 1, g), _normal((T, D), 1, g), _normal((D,), 1, g)
+    out = [torch.zeros((T, D), dtype=BF16, device="cuda"), torch.zeros((T, D), dtype=BF16, device="cuda"), torch.zeros((T, E), device="cuda"),
+           torch.zeros((T, k), dtype=torch.int32, device="cuda"), torch.zeros((T, k), device="cuda"), torch.zeros((T, N), device="cuda")]
+
+    def run(ws, lws):
+        moe.moe_add_rms_norm(T, D, x, res, w, 1e-6, out[0], out[1])
+        moe.moe_route_gated(cfg, gate, out[1], Wg, None, sb, out[2], out[3], out[4], ws)
+        moe.moe_lora(T, D, N, r, n, out[1], ld["ids"], ld["A"], ld["B"], ld["scales"], ld["base"], out[5], lws)
+
+    return run, out, moe.moe_workspace_size(cfg), moe.moe_lora_workspace_size(T, D, N, r, n)
+
+
+def _serial(calls):
+    """What the calls write, one by one, each waited for."""
+    want = []
+    for run, out, a, b in calls:
+        run(torch.zeros(a, dtype=torch.uint8, device="cuda"), torch.zeros(b, dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out])
+        for t in out:
+            t.zero_()
+    return want
+
+
+def test_calls_on_two_streams_at_once():
+    """Each stream with workspaces of its own, the sizes of one beside those of the other."""
+    calls = [_three_calls(T, i) for i, T in enumerate((3000, 7, 64, 1500, 300, 33))]
+    want = _serial(calls)
+    spaces = [(torch.zeros(max(c[2] for c in calls), dtype=torch.uint8, device="cuda"),
+               torch.zeros(max(c[3] for c in calls), dtype=torch.uint8, device="cuda")) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, c in enumerate(calls):
+            with torch.cuda.stream(streams[i % 2]):
+                c[0](*spaces[i % 2])
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(c[1], w))
+
+
+def test_graphs_share_workspaces():
+    """Captured for several batch sizes in the same workspaces, replayed in any order."""
+    calls = [_three_calls(T, i) for i, T in enumerate((1, 16, 65, 2000))]
+    want = _serial(calls)
+    ws = torch.zeros(max(c[2] for c in calls), dtype=torch.uint8, device="cuda")
+    lws = torch.zeros(max(c[3] for c in calls), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c[0](ws, lws)
+    for i in (0, 3, 1, 2, 3, 0, 2, 1, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(c[1], w))
