@@ -18,7 +18,7 @@
 // Measured (one GB300, inputs rotated so that they come from HBM): one row, 2048 x 2048, rank
 // 16 5.0 us; 61 rows of 40 adapters, 4096 x 4096, rank 64 12.4 us (33 MB in 4.9 at a copy's rate;
 // two launches, each three dependent trips to memory); 2000 rows of 4 requests, 2048 x 4224,
-// rank 24, fp32 28 us (11.3); 8192 rows of 12, 8192 x 8192, rank 64 93 us (428 MB in 63).
+// rank 24, fp32 27 us (11.3); 8192 rows of 12, 8192 x 8192, rank 64 93 us (428 MB in 63).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -56,7 +56,7 @@ struct LoraParams {
   int tile_rows, max_tiles;
   int splits;  // of K (and planes, where the slices are not added at once)
   int slices;  // of r
-  int chunk;   // columns of y a CTA takes, a multiple of 64 (few rows: of 256)
+  int chunk;   // columns of y a CTA takes, a multiple of 128 bytes (few rows: of 256 columns)
 };
 
 // ------------------------------------------------------------------- plan
@@ -909,7 +909,7 @@ struct LoraPlan {
   bool scan, at_once, wide;
   int tile_rows, tiles, slices, splits, chunk;
 };
-LoraPlan lora_plan(int T, int K, int N, int r, int n) {
+LoraPlan lora_plan(int T, int K, int N, int r, int n, bool y_f32) {
   LoraPlan q{};
   q.scan = T <= kLoraScanRows;
   // (measured, 4096 x 4096, rank 64, rows in any order, us of few-row : many-row kernels: 1024 rows
@@ -937,8 +937,9 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n) {
     const long long rounds = ((pairs + most - 1) / most + kLoraWarps - 1) / kLoraWarps;
     q.splits = static_cast<int>((pairs + rounds * kLoraWarps - 1) / (rounds * kLoraWarps));
   }
-  // y's columns: as many CTAs as have room, a block of 32 columns at least for each warp
-  const int unit = q.wide ? 64 : 32 * kLoraWarps, units = (N + unit - 1) / unit;
+  // y's columns: as many CTAs as have room, in blocks of 128 bytes, or of 32 columns for each warp
+  // (fp32 in blocks of 64 columns, 320 to a CTA instead of 288: 2000 rows of 4 28.2 us, not 27.4)
+  const int unit = !q.wide ? 32 * kLoraWarps : y_f32 ? 32 : 64, units = (N + unit - 1) / unit;
   const int chunks = static_cast<int>(std::min<long long>(std::max(1ll, 2ll * kSms / tiles), units));
   q.chunk = (units + chunks - 1) / chunks * unit;
   return q;
@@ -1032,13 +1033,15 @@ cudaError_t products_wide(const LoraParams& p, const LoraPlan& q, bool y_f32, cu
 
 }  // namespace
 
-size_t lora_workspace_bytes(int T, int K, int N, int r, int n) { return lora_layout(lora_plan(T, K, N, r, n), T, r).total; }
+size_t lora_workspace_bytes(int T, int K, int N, int r, int n) {
+  return lora_layout(lora_plan(T, K, N, r, n, false), T, r).total;  // (y's type is that of the chunk alone)
+}
 
 cudaError_t launch_lora(int T, int K, int N, int r, int n, const void* x, const int32_t* ids, const void* A,
                         const void* B, const float* scales, const void* base, void* y, bool y_f32, uint8_t* ws,
                         cudaStream_t s) {
   if (T <= 0) return cudaSuccess;
-  const LoraPlan q = lora_plan(T, K, N, r, n);
+  const LoraPlan q = lora_plan(T, K, N, r, n, y_f32);
   const LoraLayout L = lora_layout(q, T, r);
   LoraParams p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
