@@ -3,9 +3,8 @@
 //   y[t] = base[t] + scales[a] (x[t] A_a^T) B_a^T,   a = ids[t]
 //
 // Rows are taken in tiles of one adapter each.  Up to kLoraScanRows rows a CTA finds its
-// tile in the ids by itself (the tile of row t is that of all rows with its adapter, and
-// only the first of them has one); beyond, a launch sorts the rows by adapter and lists
-// the tiles.  Then two launches: lora_shrink, v = x A^T as fp32 planes over slices of K, and
+// tile in the ids by itself (every sixteenth row of an adapter, from its first on, has one: its
+// own and the next fifteen); beyond, a launch sorts the rows by adapter and lists the tiles.  Then two launches: lora_shrink, v = x A^T as fp32 planes over slices of K, and
 // lora_expand, which adds the planes in order and multiplies by B (few rows and small adapters:
 // both in one).
 //
@@ -16,7 +15,7 @@
 // adapters' bytes are the bound.  Many rows: tcgen05 (below), x and y are.
 //
 // Measured (one GB300, inputs rotated so that they come from HBM): one row, 2048 x 2048, rank
-// 16 5.0 us; 61 rows of 40 adapters, 4096 x 4096, rank 64 12.4 us (33 MB in 4.9 at a copy's rate;
+// 16 5.0 us; 61 rows of 40 adapters, 4096 x 4096, rank 64 11.7 us (33 MB in 4.9 at a copy's rate;
 // two launches, each three dependent trips to memory); 2000 rows of 4 requests, 2048 x 4224,
 // rank 24, fp32 27 us (11.3); 8192 rows of 12, 8192 x 8192, rank 64 93 us (428 MB in 63).
 #include <cuda_bf16.h>
@@ -154,7 +153,9 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraParam
 
 // --------------------------------------------------------------- tile rows
 // The CTA's tile: its rows' numbers in `rows`, its adapter; false when it has none.  Without a
-// plan (SCAN) the tile is all rows with row b's adapter.
+// plan (SCAN) the tile is row b and the next fifteen rows with its adapter, where a multiple of
+// sixteen go before it.  (All of an adapter's rows in one CTA, sixteen at a time: 64 rows of one
+// adapter of 8192 x 8192, rank 64 29.3 us, 11.5 with tiles of sixteen.)
 template <bool SCAN>
 __device__ __forceinline__ bool lora_tile(const LoraParams& p, int b, int* rows, int* count_slot, int& adapter,
                                           int& count) {
@@ -168,12 +169,13 @@ __device__ __forceinline__ bool lora_tile(const LoraParams& p, int b, int* rows,
       const int i0 = id(lane), i1 = id(lane + 32);
       const int mine = b < 32 ? __shfl_sync(0xffffffffu, i0, b) : __shfl_sync(0xffffffffu, i1, b - 32);
       const unsigned m0 = __ballot_sync(0xffffffffu, i0 == mine), m1 = __ballot_sync(0xffffffffu, i1 == mine);
-      const int first = m0 ? __ffs(m0) - 1 : 32 + __ffs(m1) - 1;
-      const unsigned below = (1u << lane) - 1u;
-      if (i0 == mine) rows[__popc(m0 & below)] = lane;
-      if (i1 == mine) rows[__popc(m0) + __popc(m1 & below)] = lane + 32;
+      const unsigned below = (1u << lane) - 1u, before_b = (1u << (b & 31)) - 1u;
+      const int from = b < 32 ? __popc(m0 & before_b) : __popc(m0) + __popc(m1 & before_b);
+      const int r0 = __popc(m0 & below) - from, r1 = __popc(m0) + __popc(m1 & below) - from;
+      if (i0 == mine && r0 >= 0 && r0 < 16) rows[r0] = lane;
+      if (i1 == mine && r1 >= 0 && r1 < 16) rows[r1] = lane + 32;
       if (lane == 0) {
-        count_slot[0] = first == b ? __popc(m0) + __popc(m1) : 0;
+        count_slot[0] = from % 16 == 0 ? min(16, __popc(m0) + __popc(m1) - from) : 0;
         count_slot[1] = mine;
       }
     }
@@ -207,15 +209,15 @@ __device__ __forceinline__ void step32(float (&d)[4], const uint4& lo, const uin
 // of the warps.
 template <int NT>
 using ShrinkRed = float[kLoraWarps][32][4 * NT + 1];
-// out(i, c, sum) for rows m0 + i, i < 16, of the tile and columns j0 + c, c < 8 NT, over pairs of
-// steps [q0, q1); every output by one thread, behind a barrier.
+// out(i, c, sum) for rows i < 16 of the tile and columns j0 + c, c < 8 NT, over pairs of steps
+// [q0, q1); every output by one thread, behind a barrier.
 template <int NT, typename Out>
 __device__ __forceinline__ void shrink_rows(const LoraParams& p, const __nv_bfloat16* A, int j0, const int* rows,
-                                            int count, int m0, int q0, int q1, ShrinkRed<NT>& red, const Out& out) {
+                                            int count, int q0, int q1, ShrinkRed<NT>& red, const Out& out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const bool on0 = m0 + g < count, on1 = m0 + 8 + g < count;
-  const __nv_bfloat16* x0 = p.x + static_cast<size_t>(on0 ? rows[m0 + g] : 0) * p.K;
-  const __nv_bfloat16* x1 = p.x + static_cast<size_t>(on1 ? rows[m0 + 8 + g] : 0) * p.K;
+  const bool on0 = g < count, on1 = 8 + g < count;
+  const __nv_bfloat16* x0 = p.x + static_cast<size_t>(on0 ? rows[g] : 0) * p.K;
+  const __nv_bfloat16* x1 = p.x + static_cast<size_t>(on1 ? rows[8 + g] : 0) * p.K;
   float acc[NT][4] = {};
   constexpr int P = NT == 2 ? 2 : 1;  // pairs whose loads are under way at a time (what registers allow)
   for (int q = q0 + warp; q < q1; q += P * kLoraWarps) {
@@ -235,7 +237,6 @@ __device__ __forceinline__ void shrink_rows(const LoraParams& p, const __nv_bflo
 #pragma unroll
       for (int j = 0; j < NT; ++j) step32(acc[j], lo[u], hi[u], col[u][j]);
   }
-  __syncthreads();
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -255,7 +256,7 @@ template <int NT, bool SCAN>
 __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_shrink_kernel(const LoraParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ int rows[SCAN ? kLoraScanRows : 16];
+  __shared__ int rows[16];
   __shared__ int slot[2];
   __shared__ ShrinkRed<NT> red;
   int adapter, count;
@@ -266,10 +267,9 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_shrink_kernel(const L
             q1 = static_cast<long long>(pairs) * (split + 1) / p.splits;
   const __nv_bfloat16* A = p.A + (static_cast<size_t>(adapter) * p.r + j0) * p.K;
   float* plane = p.planes + static_cast<size_t>(split) * p.T * p.r;
-  for (int m0 = 0; m0 < count; m0 += 16)
-    shrink_rows<NT>(p, A, j0, rows, count, m0, q0, q1, red, [&](int i, int c, float v) {
-      if (m0 + i < count && j0 + c < p.r) plane[static_cast<size_t>(rows[m0 + i]) * p.r + j0 + c] = v;
-    });
+  shrink_rows<NT>(p, A, j0, rows, count, q0, q1, red, [&](int i, int c, float v) {
+    if (i < count && j0 + c < p.r) plane[static_cast<size_t>(rows[i]) * p.r + j0 + c] = v;
+  });
 }
 
 // y = base + f for 8 neighbouring values; b: the base's, as loaded (not read where !has).
@@ -316,48 +316,42 @@ __device__ __forceinline__ void copy_rows(const Ty* base, Ty* y, const int* rows
   }
 }
 
-// f[0..7] = v[row][j .. j + 7]: the planes added in their order, four planes' loads at a time.
-__device__ __forceinline__ void sum_planes(const LoraParams& p, int row, int j, float (&f)[8]) {
+// f[0..3] = v[row][j .. j + 3]: the planes added in their order, eight planes' loads at a time.
+__device__ __forceinline__ void sum_planes(const LoraParams& p, int row, int j, float (&f)[4]) {
+  constexpr int P = 8;
   const float* q = p.planes + static_cast<size_t>(row) * p.r + j;
   const size_t plane = static_cast<size_t>(p.T) * p.r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-  for (int s = 0; s < p.splits; s += 4) {
-    float4 a[4][2];
+  for (int i = 0; i < 4; ++i) f[i] = 0.0f;
+  for (int s = 0; s < p.splits; s += P) {
+    float4 a[P];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < P; ++u)
+      if (s + u < p.splits) a[u] = *reinterpret_cast<const float4*>(q + (s + u) * plane);
+#pragma unroll
+    for (int u = 0; u < P; ++u)
       if (s + u < p.splits) {
-        a[u][0] = *reinterpret_cast<const float4*>(q + (s + u) * plane);
-        a[u][1] = *reinterpret_cast<const float4*>(q + (s + u) * plane + 4);
+        f[0] += a[u].x;
+        f[1] += a[u].y;
+        f[2] += a[u].z;
+        f[3] += a[u].w;
       }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (s + u < p.splits)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f[4 * h] += a[u][h].x;
-          f[4 * h + 1] += a[u][h].y;
-          f[4 * h + 2] += a[u][h].z;
-          f[4 * h + 3] += a[u][h].w;
-        }
   }
 }
-// f as TERMS bf16 terms, 8 values to a word of 16 bytes; f keeps what is left.
-template <int TERMS>
-__device__ __forceinline__ void split_terms(float (&f)[8], uint4 (&t)[TERMS]) {
+// f as TERMS bf16 terms, two neighbours to a word; f keeps what is left.
+template <int TERMS, int H>
+__device__ __forceinline__ void split_terms(float (&f)[2 * H], uint32_t (&t)[TERMS][H]) {
 #pragma unroll
   for (int z = 0; z < TERMS; ++z) {
-    uint32_t u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < H; ++j) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-      u[j] = *reinterpret_cast<const uint32_t*>(&h);
+      t[z][j] = *reinterpret_cast<const uint32_t*>(&h);
       const float2 b = __bfloat1622float2(h);
       // (past bf16's range the first term is infinite and the others are 0)
       f[2 * j] = isfinite(b.x) ? f[2 * j] - b.x : 0.0f;
       f[2 * j + 1] = isfinite(b.y) ? f[2 * j + 1] - b.y : 0.0f;
     }
-    t[z] = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
@@ -376,7 +370,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_expand_kernel(const L
     pdl_wait();
     pdl_launch_dependents();
   }
-  __shared__ int rows[SCAN ? kLoraScanRows : 16];
+  __shared__ int rows[16];
   __shared__ int slot[2];
   extern __shared__ __align__(16) __nv_bfloat16 vs[];  // [TERMS][16][ld]
   int adapter, count;
@@ -426,84 +420,80 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_expand_kernel(const L
     return;
   }
   constexpr int W = sizeof(Ty) / 2;  // 16-byte words of eight values
-  for (int m0 = 0; m0 < count; m0 += 16) {
-    if (m0) __syncthreads();
-    if constexpr (NT > 0) {
-      __shared__ ShrinkRed<NT> red;
-      auto put = [&](int i, int c, float v) {
-        v *= scale;
+  if constexpr (NT > 0) {
+    __shared__ ShrinkRed<NT> red;
+    auto put = [&](int i, int c, float v) {
+      v *= scale;
 #pragma unroll
-        for (int z = 0; z < TERMS; ++z) {
-          const __nv_bfloat16 h = __float2bfloat16_rn(v);
-          vs[(z * 16 + i) * ld + c] = h;
-          const float f = __bfloat162float(h);
-          v = isfinite(f) ? v - f : 0.0f;  // (as split_terms)
-        }
-      };
-      for (int o = threadIdx.x; o < 16 * (rp - 8 * NT); o += kLoraWarps * 32) put(o % 16, 8 * NT + o / 16, 0.0f);
-      shrink_rows<NT>(p, p.A + static_cast<size_t>(adapter) * p.r * p.K, 0, rows, count, m0, 0, (p.K + 63) / 64, red, put);
-      load_step(n_first, 0);
-    } else {
-      if (m0) load_step(n_first, 0);
-      for (int o = threadIdx.x; o < 2 * rp; o += kLoraWarps * 32) {
-        const int i = o / (rp / 8), j = o % (rp / 8) * 8;
-        float f[8] = {};
-        if (m0 + i < count && j < p.r) {
-          sum_planes(p, rows[m0 + i], j, f);
+      for (int z = 0; z < TERMS; ++z) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        vs[(z * 16 + i) * ld + c] = h;
+        const float f = __bfloat162float(h);
+        v = isfinite(f) ? v - f : 0.0f;  // (as split_terms)
+      }
+    };
+    for (int o = threadIdx.x; o < 16 * (rp - 8 * NT); o += kLoraWarps * 32) put(o % 16, 8 * NT + o / 16, 0.0f);
+    shrink_rows<NT>(p, p.A + static_cast<size_t>(adapter) * p.r * p.K, 0, rows, count, 0, (p.K + 63) / 64, red, put);
+    load_step(n_first, 0);
+  } else {
+    for (int o = threadIdx.x; o < 4 * rp; o += kLoraWarps * 32) {
+      const int i = o / (rp / 4), j = o % (rp / 4) * 4;
+      float f[4] = {};
+      if (i < count && j < p.r) {
+        sum_planes(p, rows[i], j, f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) f[q] *= scale;
-        }
-        uint4 t[TERMS];
-        split_terms<TERMS>(f, t);
+        for (int q = 0; q < 4; ++q) f[q] *= scale;
+      }
+      uint32_t t[TERMS][2];
+      split_terms<TERMS>(f, t);
 #pragma unroll
-        for (int z = 0; z < TERMS; ++z) *reinterpret_cast<uint4*>(vs + (z * 16 + i) * ld + j) = t[z];
+      for (int z = 0; z < TERMS; ++z) *reinterpret_cast<uint2*>(vs + (z * 16 + i) * ld + j) = make_uint2(t[z][0], t[z][1]);
+    }
+  }
+  __syncthreads();
+  for (int n0 = n_first; n0 < c1; n0 += 32 * kLoraWarps) {
+    const int n = n0 + 8 * tig;
+    uint4 b[2][W];
+    size_t at[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = 8 * h + g;
+      at[h] = static_cast<size_t>(i < count ? rows[i] : 0) * p.N + n;
+      if (base && i < count && n < c1) {
+#pragma unroll
+        for (int q = 0; q < W; ++q) b[h][q] = reinterpret_cast<const uint4*>(base + at[h])[q];
       }
     }
-    __syncthreads();
-    for (int n0 = n_first; n0 < c1; n0 += 32 * kLoraWarps) {
-      const int n = n0 + 8 * tig;
-      uint4 b[2][W];
-      size_t at[2];
+    float acc[4][4] = {};
+    for (int r0 = 0; r0 < rp; r0 += 64) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = m0 + 8 * h + g;
-        at[h] = static_cast<size_t>(i < count ? rows[i] : 0) * p.N + n;
-        if (base && i < count && n < c1) {
+      for (int u = 0; u < 2; ++u) {
+        if (r0 + 32 * u >= rp) break;
 #pragma unroll
-          for (int q = 0; q < W; ++q) b[h][q] = reinterpret_cast<const uint4*>(base + at[h])[q];
+        for (int z = 0; z < TERMS; ++z) {
+          const __nv_bfloat16* a = vs + (z * 16 + g) * ld + r0 + 32 * u + 8 * tig;
+          const uint4 lo = *reinterpret_cast<const uint4*>(a), hi = *reinterpret_cast<const uint4*>(a + 8 * ld);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) step32(acc[j], lo, hi, col[u][j]);
         }
       }
-      float acc[4][4] = {};
-      for (int r0 = 0; r0 < rp; r0 += 64) {
+      // the next step's, under way while this block is finished
+      if (r0 + 64 < rp)
+        load_step(n0, r0 + 64);
+      else if (n0 + 32 * kLoraWarps < c1)
+        load_step(n0 + 32 * kLoraWarps, 0);
+    }
+    if (n >= c1) continue;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (r0 + 32 * u >= rp) break;
+    for (int h = 0; h < 2; ++h) {
+      if (8 * h + g >= count) continue;
+      float f[8];
 #pragma unroll
-          for (int z = 0; z < TERMS; ++z) {
-            const __nv_bfloat16* a = vs + (z * 16 + g) * ld + r0 + 32 * u + 8 * tig;
-            const uint4 lo = *reinterpret_cast<const uint4*>(a), hi = *reinterpret_cast<const uint4*>(a + 8 * ld);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) step32(acc[j], lo, hi, col[u][j]);
-          }
-        }
-        // the next step's, under way while this block is finished
-        if (r0 + 64 < rp)
-          load_step(n0, r0 + 64);
-        else if (n0 + 32 * kLoraWarps < c1)
-          load_step(n0 + 32 * kLoraWarps, 0);
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = acc[j][2 * h];
+        f[2 * j + 1] = acc[j][2 * h + 1];
       }
-      if (n >= c1) continue;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (m0 + 8 * h + g >= count) continue;
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[2 * j] = acc[j][2 * h];
-          f[2 * j + 1] = acc[j][2 * h + 1];
-        }
-        put8(y + at[h], f, base != nullptr, b[h]);
-      }
+      put8(y + at[h], f, base != nullptr, b[h]);
     }
   }
 }
@@ -819,15 +809,12 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_expand_wide_kernel(const
       for (int q = 0; q < 4; ++q) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[q][i] *= scale;
-        uint4 u[TERMS];
+        uint32_t u[TERMS][4];
         split_terms<TERMS>(f[q], u);
 #pragma unroll
-        for (int z = 0; z < TERMS; ++z) {
-          t[z][4 * q] = u[z].x;
-          t[z][4 * q + 1] = u[z].y;
-          t[z][4 * q + 2] = u[z].z;
-          t[z][4 * q + 3] = u[z].w;
-        }
+        for (int z = 0; z < TERMS; ++z)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[z][4 * q + i] = u[z][i];
       }
 #pragma unroll
       for (int z = 0; z < TERMS; ++z) tmem_st_32x32b_x16(lanes + z * geom.kcols + j / 2, t[z]);
@@ -919,13 +906,14 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n, bool y_f32) {
   q.tile_rows = q.wide ? kWideRows : 16;
   q.tiles = q.scan ? T : static_cast<int>(std::min<long long>(T, (T + q.tile_rows - 1ll) / q.tile_rows + n));
   // one launch instead of two: as long on the GPU (us of two : of one, 1, 16, 32, 64 rows with
-  // adapters of their own: 2048 x 2048, rank 16 4.7 : 4.9, 5.4 : 5.1, 5.8 : 6.1, 7.1 : 7.1; 4096 x
-  // 4096, rank 16 5.1 : 6.1, 6.1 : 7.7, 7.2 : 8.7, 8.2 : 9.7), and 1.5 less of the caller's time
+  // adapters of their own: 2048 x 2048, rank 16 5.1 : 4.7, 5.5 : 5.1, 6.1 : 6.1, 7.1 : 7.2; 4096 x
+  // 4096, rank 16 5.1 : 6.1, 6.0 : 7.6, 7.1 : 8.7, 8.2 : 9.7), and 1.5 less of the caller's time
   q.at_once = T <= 32 && r <= 32 && static_cast<long long>(r) * K <= 32768;
   // adapters that some row has, about, and tiles
   const long long used = std::min<long long>(T, static_cast<long long>(n) * T / std::max(1, T + n / 2));
   const long long tiles =
-      std::max(1ll, q.scan ? used : q.wide ? (T + q.tile_rows - 1) / q.tile_rows + n / 2 : used + T / 32);
+      std::max(1ll, q.scan ? used * ((T + 16 * used - 1) / std::max(1ll, 16 * used))
+                           : q.wide ? (T + q.tile_rows - 1) / q.tile_rows + n / 2 : used + T / 32);
   q.slices = q.wide ? 1 : (r + kRankSlice - 1) / kRankSlice;
   // slices of K: as many CTAs as have room at a time (two an SM)
   const long long room = std::max(1ll, 2ll * kSms / (tiles * q.slices));

@@ -344,6 +344,7 @@ def _check_lora(d, dt, base=True, scales=True, in_place=False):
     (3000, 4104, 72, 8, 7, "runs"), (90, 72, 8, 256, 1, "one"), (1024, 64, 64, 200, 16, "mixed"), (1500, 256, 1544, 256, 5, "mixed"),
     (1100, 520, 1288, 96, 6, "mixed"), (2100, 264, 136, 128, 2, "runs"), (1300, 136, 2056, 16, 2, "mixed"), (1024, 72, 8, 256, 1, "one"),
     (9000, 200, 104, 16, 30, "mixed"), (1024, 2048, 64, 256, 2, "mixed"), (1030, 4104, 72, 136, 1, "one"), (1100, 1032, 200, 64, 9, "mixed"),
+    (64, 1000, 520, 24, 1, "one"), (49, 264, 264, 128, 2, "runs"), (64, 2048, 520, 64, 3, "mixed"), (32, 1024, 264, 16, 1, "one"),
     (2049, 512, 264, 32, 64, "mixed"), (1023, 512, 264, 32, 2, "mixed")])
 def test_lora(T, K, N, r, n, how, dt):
     d = _lora_inputs(T, K, N, r, n, dt, T + K + N + r, how)
