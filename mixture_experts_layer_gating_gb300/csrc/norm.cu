@@ -108,16 +108,51 @@ __device__ __forceinline__ float e4m3_scale(uint32_t largest) {
   return largest < 0x7f800000u ? fmaxf(__fdiv_rn(__uint_as_float(largest), 448.0f), FLT_MIN)
                                : __uint_as_float(0x7fffffffu);
 }
-__device__ __forceinline__ uint2 e4m3_codes(const float (&f)[8], float scale) {
-  float inv;  // (to an ulp: far below a step of e4m3; scale is normal, or NaN)
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+// Two fp32 values to a register pair, for the instructions that take both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// e4m3 of the fp32 quotients f / scale, rounded to nearest; inv: 1 / scale, rounded.  The
+// product with the inverse is within two ulps of the quotient, one correction by its remainder
+// brings it within one, and the next, whose remainder is exact, rounds as division does
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990).  Without them a quotient next to the middle of two codes takes the wrong one, 9 of a
+// million; by __fdiv_rn 16384 x 8192 take 209 us, not 192.  Two values at a time, and minus the
+// quotient, which keeps the sign of a zero.
+__device__ __forceinline__ uint2 e4m3_codes(const float (&f)[8], float scale, float inv) {
+  uint64_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+  if (scale < 0x1p-60f) {  // times 2^64, exactly: no remainder is subnormal
+    scale *= 0x1p64f;
+    inv *= 0x1p-64f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], pair(0x1p64f, 0x1p64f));
+  }
+  const uint64_t by = pair(scale, scale), minus = pair(-inv, -inv);
   uint32_t u[2] = {0u, 0u};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    u[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv),
-                                                                __NV_SATFINITE, __NV_E4M3))
-                 << (16 * (i & 1));
-  return make_uint2(u[0], u[1]);
+  for (int i = 0; i < 4; ++i) {
+    uint64_t q = mul2(v[i], minus);
+    q = fma2(fma2(q, by, v[i]), minus, q);
+    q = fma2(fma2(q, by, v[i]), minus, q);
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(q));
+    u[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3)) << (16 * (i & 1));
+  }
+  return make_uint2(u[0] ^ 0x80808080u, u[1] ^ 0x80808080u);
 }
 
 enum QMode { kNoQ, kRowQ, kGroupQ };
@@ -235,23 +270,37 @@ __global__ void __launch_bounds__(32 * kMaxWarps) add_rms_norm_kernel(const Norm
     if (Q == kRowQ) {
       const float s = e4m3_scale(row_reduce(all, redm[buf], warps));
       if (li == 0) p.scales[r] = s;
+      const float inv = __frcp_rn(s);
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-        if (li + tpr * j < nvec) reinterpret_cast<uint2*>(p.q)[base + li + tpr * j] = e4m3_codes(f[j], s);
+        if (li + tpr * j < nvec) reinterpret_cast<uint2*>(p.q)[base + li + tpr * j] = e4m3_codes(f[j], s, inv);
     }
     if (Q == kGroupQ) {
       // group / 8 neighbouring threads hold a group (D is a multiple of it, so they hold it
       // whole or not at all)
       const int lanes = p.group / 8;
+      // scales and their inverses: those of four vectors by a lane each (four neighbours are
+      // of one group)
+      constexpr int C = VPT < 4 ? 1 : 4;
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        uint32_t m = most[j];
-        for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-        const int v = li + tpr * j;
-        if (v < nvec) {
-          const float s = e4m3_scale(m);
-          if (v % lanes == 0) p.scales[r * (nvec / lanes) + v / lanes] = s;
-          reinterpret_cast<uint2*>(p.q)[base + v] = e4m3_codes(f[j], s);
+      for (int j0 = 0; j0 < VPT; j0 += C) {
+        uint32_t mine = 0u;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          uint32_t m = most[j0 + c];
+          for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+          if (C == 1 || (li & 3) == c) mine = m;
+        }
+        const float my_s = e4m3_scale(mine), my_inv = __frcp_rn(my_s);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const float s = C == 1 ? my_s : __shfl_sync(kFull, my_s, c, 4);
+          const float inv = C == 1 ? my_inv : __shfl_sync(kFull, my_inv, c, 4);
+          const int v = li + tpr * (j0 + c);
+          if (v < nvec) {
+            if (v % lanes == 0) p.scales[r * (nvec / lanes) + v / lanes] = s;
+            reinterpret_cast<uint2*>(p.q)[base + v] = e4m3_codes(f[j0 + c], s, inv);
+          }
         }
       }
     }

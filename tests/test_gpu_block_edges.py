@@ -1,0 +1,65 @@
+"""moe_add_rms_norm, moe_route_gated and moe_lora on the GPU, where their inputs
+or sizes are at an end of what they take."""
+import math
+
+import pytest
+import torch
+
+import mixture_experts_layer_gating_gb300 as moe
+from tests import _block_ref as ref
+from tests._lib import ensure_library
+from tests.test_gpu_block import BF16, F32, W_REL, _gate, _gen, _normal, _within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    return ensure_library()
+
+
+# ------------------------------------------------------------------- norm
+def _codes(x, res, w, eps, group):
+    """(y, q, scales) of moe_add_rms_norm; y of fp32 inputs is what q is made of."""
+    T, D = x.shape
+    y, q = torch.empty_like(x), torch.empty((T, D), dtype=torch.uint8, device="cuda")
+    s = torch.empty((T, D // (group or D)), device="cuda")
+    moe.moe_add_rms_norm(T, D, x, res, w, eps, None, y, q, s, group)
+    return y, q, s
+
+
+def _divided(y, s, group):
+    """e4m3 codes of y / scale by fp32 division and torch's conversion, nearest even (on the host)."""
+    v = y.cpu().view(y.shape[0], -1, group or y.shape[1]) / s.cpu()[:, :, None]
+    return v.view_as(y).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+@pytest.mark.parametrize("T,D,group", [(300, 4096, 0), (300, 4096, 32), (1000, 2816, 128), (400, 8192, 64), (700, 8192, 0), (200, 20480, 0), (200, 20480, 128)])
+def test_norm_codes_are_those_of_the_quotients(T, D, group):
+    """q = e4m3(y / scale): no code next to it where the quotient lies near the middle of two."""
+    g = _gen(T + D + group)
+    x, res = _normal((T, D), 1, g), _normal((T, D), 2, g)
+    w = (1 + _normal((D,), 0.2, g, F32)).to(BF16)
+    x[0], res[0, 1::2] = 0, 0  # zeros, of either sign
+    x[0, 3], res[0, 3] = -0.0, -0.0
+    y, q, s = _codes(x.float(), res.float(), w.float(), 1e-6, group)
+    most = y.cpu().abs().view(T, -1, group or D).amax(2)
+    assert torch.equal(s.cpu(), torch.where(most > 0, most / 448, torch.ones_like(most)))
+    assert torch.equal(q.cpu(), _divided(y, s, group))
+    _, q16, s16 = _codes(x, res, w, 1e-6, group)  # the same values in bf16: the same rows
+    assert torch.equal(q16, q) and torch.equal(s16, s)
+
+
+@pytest.mark.parametrize("e", [-124, -119, -110, -80, -64, -62, -60, -40, 60, 100, 120, 125])
+def test_norm_codes_at_the_ends_of_the_range(e):
+    """Scales near the smallest normal number and the largest; the smallest is 2^-126."""
+    T, D = 64, 4096
+    g = _gen(e + 200)
+    x = _normal((T, D), 1, g, F32)
+    w = torch.full((D,), 2.0 ** e, device="cuda")
+    for group in (0, 128):
+        y, q, s = _codes(x, None, w, 0.0, group)
+        assert bool(y.isfinite().all())
+        most = y.cpu().abs().view(T, -1, group or D).amax(2)
+        assert torch.equal(s.cpu(), (most / 448).clamp(min=2.0 ** -126))
+        assert torch.equal(q.cpu(), _divided(y, s, group))
