@@ -165,7 +165,8 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
       c[i] += compared(v[i]);
       zero = fmaf(c[i], 0.0f, zero);
     }
-    if (bad || !(zero == 0.0f)) {
+    // (a lane past E compares no expert's: 0 against a largest logit far below it is infinite)
+    if (here && (bad || !(zero == 0.0f))) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         bad |= !isfinite(c[i]);

@@ -63,3 +63,53 @@ def test_norm_codes_at_the_ends_of_the_range(e):
         most = y.cpu().abs().view(T, -1, group or D).amax(2)
         assert torch.equal(s.cpu(), (most / 448).clamp(min=2.0 ** -126))
         assert torch.equal(q.cpu(), _divided(y, s, group))
+
+
+# ------------------------------------------------------------------- gate
+def _far_logits(E):
+    """Rows whose largest logit is far below 0: finite, the type's lowest value among them."""
+    low = torch.finfo(F32).min
+    rows = torch.full((6, E), -100.0)
+    rows[1, E // 2:] = low
+    rows[2, :] = low
+    rows[3] = -torch.linspace(89, 2000, E)
+    rows[4, 1:] = low
+    rows[5] = -60.0
+    return rows
+
+
+def _softmax_choice(logits, sb, k):
+    """ids and renormalised weights of softmax scores with a bias, in 64 bits."""
+    p = torch.softmax(logits.double(), dim=1)
+    ids = torch.sort(p + sb.double(), dim=1, descending=True, stable=True).indices[:, :k]
+    q = p.gather(1, ids)
+    return ids, q / q.sum(1, keepdim=True)
+
+
+@pytest.mark.parametrize("E", [32, 64, 96, 100, 128, 160, 320, 384, 512])
+def test_gate_finite_logits_far_below_zero_set_no_flag(E):
+    logits, sb = _far_logits(E), (torch.arange(E) % 7).float() * -0.125
+    sb[5:9] = 0.5  # (distinct from the next by far more than a softmax of equal logits)
+    ids, w = _softmax_choice(logits, sb, 4)
+    got, gw = _gate(logits.cuda(), sb.cuda(), 4, moe.make_gate("softmax"), flags=0)
+    for t in (0, 1, 2, 5):  # (equal scores in the others: order and weights hang on the last bits of a softmax)
+        assert got[t].tolist() == ids[t].tolist() == [5, 6, 7, 8]
+        _within(gw[t].cpu(), w[t], w[t] * W_REL)
+    assert bool(gw.isfinite().all()) and bool(((gw.sum(1) - 1).abs() < 1e-6).all())
+
+
+@pytest.mark.parametrize("E", [96, 160, 320, 512])
+@pytest.mark.parametrize("fused", [1, 2])
+@pytest.mark.parametrize("T", [3, 130])
+def test_gate_from_rows_with_logits_far_below_zero_sets_no_flag(E, fused, T):
+    x, Wg = torch.zeros((T, 256), dtype=BF16, device="cuda"), torch.zeros((256, E), dtype=BF16, device="cuda")
+    sb = torch.zeros(E, device="cuda")
+    sb[5:9] = 0.5
+    old = moe.moe_set_option(moe.MOE_OPT_FUSED_ROUTING, fused)
+    try:
+        for far in (-100.0, torch.finfo(F32).min):
+            lb = torch.full((E,), far, device="cuda")
+            got, gw = _gate(torch.empty((T, E), device="cuda"), sb, 4, moe.make_gate("softmax"), x=x, Wg=Wg, lb=lb, flags=0)
+            assert bool((got == torch.tensor([5, 6, 7, 8], device="cuda")).all()) and bool(((gw - 0.25).abs() < 1e-6).all())
+    finally:
+        moe.moe_set_option(moe.MOE_OPT_FUSED_ROUTING, old)
