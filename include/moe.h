@@ -366,7 +366,8 @@ int moe_dequantize_w4(const void* Wq, const void* scales, const void* zeros, int
  * (their ratios there, kept from underflow).  A non-finite logit (or c) counts as
  * -infinity: p is 0, the expert is chosen last and not part of a group's sum,
  * MOE_DEV_NONFINITE_LOGIT is set; a token that has only such experts to choose gets
- * weights scale / k. */
+ * weights scale / k.  (So a select_bias of -infinity takes an expert out.  A softmax's sum
+ * is over all finite logits, those of such experts too.) */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2_SUM = 1 } moe_group_score_t;
 typedef struct {

@@ -169,8 +169,10 @@ __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const G
     if (here && (bad || !(zero == 0.0f))) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        bad |= !isfinite(c[i]);
-        if (!isfinite(c[i]) || v[i] == -INFINITY) c[i] = -INFINITY;
+        const bool out = !isfinite(c[i]);  // (its weight, which is taken from v, is 0 too)
+        bad |= out;
+        if (out) v[i] = -INFINITY;
+        if (v[i] == -INFINITY) c[i] = -INFINITY;
       }
     }
 #pragma unroll

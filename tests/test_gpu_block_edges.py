@@ -113,3 +113,27 @@ def test_gate_from_rows_with_logits_far_below_zero_sets_no_flag(E, fused, T):
             assert bool((got == torch.tensor([5, 6, 7, 8], device="cuda")).all()) and bool(((gw - 0.25).abs() < 1e-6).all())
     finally:
         moe.moe_set_option(moe.MOE_OPT_FUSED_ROUTING, old)
+
+
+@pytest.mark.parametrize("mask", [-math.inf, math.inf, math.nan])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("kw", [dict(), dict(score="softmax"), dict(n_group=8, topk_group=2), dict(score="softmax", n_group=8, topk_group=2, group_score="max")],
+                         ids=["sigmoid", "softmax", "sigmoid-groups", "softmax-groups"])
+def test_gate_experts_masked_by_the_bias_weigh_nothing(kw, renorm, mask):
+    """A bias that is not finite takes its expert out: chosen last, weight 0, whatever its logit;
+    a token that has only such experts to choose gets equal weights."""
+    E, k = 64, 4
+    logits = torch.linspace(-2, 2, E).repeat(3, 1)
+    logits[1] = logits[1].flip(0)
+    logits[2, :30] = -60.0
+    for left in (0, 1, 2, 3, 20):
+        sb = torch.full((E,), mask)
+        sb[7:7 + left] = 0.25
+        out = torch.where(sb.isfinite(), logits, torch.full_like(logits, -math.inf))
+        ids, w, _ = ref.gate(out, torch.where(sb.isfinite(), sb, torch.zeros(E)), k, renorm=renorm, scale=2.0, **kw)
+        if not renorm and left and kw.get("score") == "softmax":  # the softmax is over all finite logits
+            w = 2.0 * torch.softmax(logits.double(), dim=1).gather(1, ids) * sb.isfinite()[ids]
+        got, gw = _gate(logits.cuda(), sb.cuda(), k, moe.make_gate(scale=2.0, **kw), renorm, flags=moe.MOE_DEV_NONFINITE_LOGIT)
+        assert got.tolist() == ids.tolist(), left
+        _within(gw.cpu(), w, w * W_REL)
+        assert bool((gw.cpu()[~sb.isfinite()[ids]] == (0 if left else 2.0 / k)).all())
