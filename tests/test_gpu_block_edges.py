@@ -137,3 +137,23 @@ def test_gate_experts_masked_by_the_bias_weigh_nothing(kw, renorm, mask):
         assert got.tolist() == ids.tolist(), left
         _within(gw.cpu(), w, w * W_REL)
         assert bool((gw.cpu()[~sb.isfinite()[ids]] == (0 if left else 2.0 / k)).all())
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("sigmoid", False)])
+def test_gate_weights_are_quotients(score, renorm):
+    """Weights as expf and division have them: half an ulp (and 2^-20 of one) from the quotient
+    of fp32 numbers, which torch's exp, the same function, gives here, its sum added in pairs 4,
+    2 and 1 lanes apart as the kernel adds it."""
+    T, E, k = 20000, 128, 8
+    logits = _normal((T, E), 3, _gen(11), F32)
+    ids, w = _gate(logits, None, k, moe.make_gate(score), renorm)
+    x = logits.gather(1, ids.long())
+    if score == "sigmoid":
+        p, z = torch.ones_like(x), 1 + torch.exp(-x)
+    else:
+        z = p = torch.exp(x - x[:, :1])
+        for o in (4, 2, 1):
+            z = z[:, :o] + z[:, o:2 * o]
+    want = p.double() / z.double()
+    ulp = 2.0 ** (torch.floor(torch.log2(want)) - 23)
+    _within(w, want, ulp * 0.5 * (1 + 2.0 ** -19))
