@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_expand_kernel(const L
   if constexpr (NT > 0) {
     __shared__ ShrinkRed<NT> red;
     auto put = [&](int i, int c, float v) {
-      v *= scale;
+      v = c < p.r ? v * scale : 0.0f;  // (past the rank: 0 times an infinity of x)
 #pragma unroll
       for (int z = 0; z < TERMS; ++z) {
         const __nv_bfloat16 h = __float2bfloat16_rn(v);

@@ -157,3 +157,25 @@ def test_gate_weights_are_quotients(score, renorm):
     want = p.double() / z.double()
     ulp = 2.0 ** (torch.floor(torch.log2(want)) - 23)
     _within(w, want, ulp * 0.5 * (1 + 2.0 ** -19))
+
+
+# ------------------------------------------------------------------- lora
+@pytest.mark.parametrize("T", [1, 5, 32, 40, 100, 1024])
+@pytest.mark.parametrize("r", [8, 16, 24, 40])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_lora_infinite_rows_stay_infinite(T, r, dt):
+    """An infinity of x times positive A and B is one in y (ranks that a kernel pads bring no
+    0 times infinity), and leaves the other rows alone."""
+    K = N = 64
+    g = _gen(T + r)
+    x = _normal((T, K), 1, g).abs()
+    A, B = _normal((1, r, K), 0.1, g).abs() + 0.01, _normal((1, N, r), 0.1, g).abs() + 0.01
+    ids, base = torch.zeros(T, dtype=torch.int32, device="cuda"), _normal((T, N), 1, g, dt)
+    ws = torch.zeros(moe.moe_lora_workspace_size(T, K, N, r, 1), dtype=torch.uint8, device="cuda")
+    before, y = torch.empty_like(base), torch.empty_like(base)
+    moe.moe_lora(T, K, N, r, 1, x, ids, A, B, None, base, before, ws)
+    x[T // 2, 9] = math.inf
+    moe.moe_lora(T, K, N, r, 1, x, ids, A, B, None, base, y, ws)
+    assert bool((y[T // 2] == math.inf).all())
+    before[T // 2] = math.inf
+    assert torch.equal(y, before)
