@@ -428,9 +428,10 @@ int moe_add_rms_norm(int32_t rows, int32_t D, int32_t dtype, const void* x, cons
  *   base      [T, N] of y's type, y itself (in place), or NULL: 0.
  *   y         [T, N] bf16 or fp32 (y_dtype), one rounding.  Overlaps nothing else (y == x:
  *             MOE_ERR_INVALID_ARG).
- *   ws        moe_lora_workspace_size(T, K, N, r, n) bytes (0: sizes not taken),
- *             256-byte aligned; holds nothing between calls but the control block
- *             (its first 256 bytes, zero-filled once), which takes the device error word.
+ *   ws        moe_lora_workspace_size(T, K, N, r, n) bytes (0: sizes not taken), which hold
+ *             every batch of up to T rows with the same K, N, r and n; 256-byte aligned;
+ *             holds nothing between calls but the control block (its first 256 bytes,
+ *             zero-filled once), which takes the device error word.
  * x A^T is summed in fp32 and multiplied by B as two bf16 terms (16 significant bits),
  * as three (24) where y is fp32; its sums are fp32.  The same inputs give the same bits
  * on every call of the same sizes.  Pointers but ids and scales 16-byte aligned, those 4. */

@@ -53,7 +53,7 @@ int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* 
   const int st = lora_sizes(T, K, N, r, n);
   if (st != MOE_OK) return st;
   if (y_dtype != MOE_BF16 && y_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
-  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < lora_workspace_bytes(T, K, N, r, n))
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < lora_need_bytes(T, K, N, r, n))
     return MOE_ERR_WORKSPACE;
   if (T == 0) return MOE_OK;  // (empty tensors may have no address)
   for (const void* p : {x, A, B, static_cast<const void*>(y)})

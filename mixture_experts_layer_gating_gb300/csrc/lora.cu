@@ -896,13 +896,17 @@ struct LoraPlan {
   bool scan, at_once, wide;
   int tile_rows, tiles, slices, splits, chunk;
 };
+// Rows from which n adapters are taken by the kernels for many rows to a tile: 1024, and 64 an
+// adapter, or 32 from 2048 on.
+// (measured, 4096 x 4096, rank 64, rows in any order, us of few-row : many-row kernels: 1024 rows
+// of 16 adapters 23.7 : 21.7, of 32 27.2 : 32.0; 4096 of 128 107 : 96, of 256 119 : 131; 256 of 4
+// 13.2 : 17.5)
+long long lora_wide_from(int n) { return n < 32 ? std::max(1024ll, 64ll * n) : std::max(2048ll, 32ll * n); }
+
 LoraPlan lora_plan(int T, int K, int N, int r, int n, bool y_f32) {
   LoraPlan q{};
   q.scan = T <= kLoraScanRows;
-  // (measured, 4096 x 4096, rank 64, rows in any order, us of few-row : many-row kernels: 1024 rows
-  // of 16 adapters 23.7 : 21.7, of 32 27.2 : 32.0; 4096 of 128 107 : 96, of 256 119 : 131; 256 of 4
-  // 13.2 : 17.5)
-  q.wide = T >= 1024 && T >= (T >= 2048 ? 32ll : 64ll) * n;
+  q.wide = T >= lora_wide_from(n);
   q.tile_rows = q.wide ? kWideRows : 16;
   q.tiles = q.scan ? T : static_cast<int>(std::min<long long>(T, (T + q.tile_rows - 1ll) / q.tile_rows + n));
   // one launch instead of two: as long on the GPU (us of two : of one, 1, 16, 32, 64 rows with
@@ -1021,8 +1025,23 @@ cudaError_t products_wide(const LoraParams& p, const LoraPlan& q, bool y_f32, cu
 
 }  // namespace
 
-size_t lora_workspace_bytes(int T, int K, int N, int r, int n) {
+size_t lora_need_bytes(int T, int K, int N, int r, int n) {
   return lora_layout(lora_plan(T, K, N, r, n, false), T, r).total;  // (y's type is that of the chunk alone)
+}
+
+// The most that T rows or fewer need.  A batch of the few-row kernels can need more than a
+// larger one: many rows have one plane, few rows one for each slice of K, whose number falls as
+// the tiles become more.  With a plan the tiles grow with T, so from the first T on that has a
+// single slice the need grows too, up to the last T of those kernels.
+size_t lora_workspace_bytes(int T, int K, int N, int r, int n) {
+  const int few = std::min<long long>(T, lora_wide_from(n) - 1);
+  size_t most = std::max(lora_need_bytes(T, K, N, r, n), lora_need_bytes(few, K, N, r, n));
+  for (int t = 1; t < few; ++t) {
+    const LoraPlan q = lora_plan(t, K, N, r, n, false);
+    if (!q.scan && q.splits == 1) break;
+    most = std::max(most, lora_layout(q, t, r).total);
+  }
+  return most;
 }
 
 cudaError_t launch_lora(int T, int K, int N, int r, int n, const void* x, const int32_t* ids, const void* A,

@@ -114,7 +114,8 @@ cudaError_t launch_add_rms_norm(int rows, int D, bool f32, const void* x, const 
 
 // --------------------------------------------------------------------- lora.cu
 constexpr int kLoraMaxRank = 256, kLoraMaxAdapters = 16384, kLoraMaxWidth = 1 << 24;
-size_t lora_workspace_bytes(int T, int K, int N, int r, int n);
+size_t lora_workspace_bytes(int T, int K, int N, int r, int n);  // of all batches of up to T rows
+size_t lora_need_bytes(int T, int K, int N, int r, int n);       // of T rows
 cudaError_t launch_lora(int T, int K, int N, int r, int n, const void* x, const int32_t* ids, const void* A,
                         const void* B, const float* scales, const void* base, void* y, bool y_f32, uint8_t* ws,
                         cudaStream_t s);

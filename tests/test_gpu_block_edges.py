@@ -179,3 +179,19 @@ def test_lora_infinite_rows_stay_infinite(T, r, dt):
     assert bool((y[T // 2] == math.inf).all())
     before[T // 2] = math.inf
     assert torch.equal(y, before)
+
+
+def test_lora_in_the_workspace_of_a_larger_batch():
+    """One workspace, of the size for the most rows, takes every smaller batch."""
+    for K, N, r, n, most in ((1032, 264, 64, 1, 2100), (520, 264, 40, 20, 1400), (264, 136, 128, 70, 2600)):
+        g = _gen(K + n)
+        x, A, B = _normal((most, K), 1, g), _normal((n, r, K), 0.1, g), _normal((n, N, r), 0.1, g)
+        ids, base = torch.randint(-1, n, (most,), device="cuda", generator=g).int(), _normal((most, N), 1, g)
+        size = moe.moe_lora_workspace_size(most, K, N, r, n)
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        for T in (most, 1023, 1024, 700, 300, 65, 64, 33, 1, most):
+            y = torch.empty((T, N), dtype=BF16, device="cuda")
+            moe.moe_lora(T, K, N, r, n, x, ids, A, B, None, base, y, ws)
+            y64, allowed = ref.lora(x[:T], ids[:T], A, B, None, base[:T], BF16)
+            _within(y, y64, allowed)
+        assert moe.moe_read_device_status(ws) == 0
