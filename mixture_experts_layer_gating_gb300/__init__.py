@@ -429,12 +429,11 @@ def _f32(t, n: int) -> bool:
 def moe_route_gated(cfg, gate, x, Wg, logit_bias, select_bias, logits, topk_ids, topk_w, ws, stream=None):
     """moe_route with softmax or sigmoid scores, a bias for the choice, groups and a factor (make_gate)."""
     T, E, n = cfg.T, cfg.E, cfg.T * cfg.k
-    dt = _float_dtype(logits)
-    if (dt != MOE_F32 or logits.nbytes < 4 * T * E or not _f32(topk_w, n) or topk_ids.nbytes < 4 * n
-            or topk_ids.itemsize != 4 or topk_ids.is_floating_point() or not _f32(logit_bias, E)
+    if (logits is None or _float_dtype(logits) != MOE_F32 or logits.nbytes < 4 * T * E or not _f32(topk_w, n)
+            or topk_ids is None or topk_ids.nbytes < 4 * n or topk_ids.itemsize != 4 or topk_ids.is_floating_point() or not _f32(logit_bias, E)
             or not _f32(select_bias, E)
-            or x is not None and (_float_dtype(x) != cfg.act_dtype or x.numel() < T * cfg.D or Wg.dtype is not x.dtype
-                                  or Wg.numel() < cfg.D * E)):
+            or x is not None and (_float_dtype(x) != cfg.act_dtype or x.numel() < T * cfg.D or Wg is None
+                                  or Wg.dtype is not x.dtype or Wg.numel() < cfg.D * E)):
         raise ValueError("moe_route_gated takes fp32 logits [T, E], weights [T, k] and biases [E], int32 ids [T, k], "
                          "and x [T, D] and Wg [D, E] of act_dtype")
     device, s = _launch(logits, stream)
@@ -449,8 +448,8 @@ def moe_route_gated(cfg, gate, x, Wg, logit_bias, select_bias, logits, topk_ids,
 def moe_block(cfg, gate, x, residual, norm_weight, eps, Wg, logit_bias, select_bias, W13, s13, W2, s2, W13s, s13s,
               W2s, s2s, sum_out, y, out, ws, stream=None):
     """moe_add_rms_norm (norm_weight None: no norm), then moe_layer with the gate's choice (None: softmax top-k)."""
-    dt, n = x.dtype, cfg.T * cfg.D
-    if (_float_dtype(x) != cfg.act_dtype or any(t is not None and (t.dtype is not dt or t.numel() < m) for t, m in
+    dt, n = getattr(x, "dtype", None), cfg.T * cfg.D
+    if (x is None or _float_dtype(x) != cfg.act_dtype or any(t is not None and (t.dtype is not dt or t.numel() < m) for t, m in
                                                 ((x, n), (residual, n), (sum_out, n), (y, n), (out, n),
                                                  (norm_weight, cfg.D), (Wg, cfg.D * cfg.E)))
             or not _f32(logit_bias, cfg.E) or not _f32(select_bias, cfg.E)):
@@ -468,9 +467,9 @@ def moe_add_rms_norm(rows: int, D: int, x, residual, weight, eps: float, sum_out
     """sum_out = x + residual and its root-mean-square norm times weight, as y (x's type) and / or as e4m3 rows q
     with a scale per row (q_group 0) or per q_group values; None for what is not there or not wanted."""
     # (a small batch takes little longer than its call: no loops, each attribute looked up once)
-    t, dt = x.dtype, _float_dtype(x)
+    t, dt = (None, -1) if x is None else (x.dtype, _float_dtype(x))
     nb = rows * D * (4 if dt == MOE_F32 else 2)
-    if (dt < 0 or x.nbytes < nb or weight.dtype is not t or rows > 0 and weight.numel() < D
+    if (dt < 0 or x.nbytes < nb or weight is None or weight.dtype is not t or rows > 0 and weight.numel() < D
             or residual is not None and (residual.dtype is not t or residual.nbytes < nb)
             or sum_out is not None and (sum_out.dtype is not t or sum_out.nbytes < nb)
             or y is not None and (y.dtype is not t or y.nbytes < nb)
@@ -494,9 +493,10 @@ def moe_lora_workspace_size(T: int, K: int, N: int, r: int, n: int) -> int:
 def moe_lora(T: int, K: int, N: int, r: int, n: int, x, ids, A, B, scales, base, y, ws, stream=None) -> None:
     """y [T, N] (bf16 or fp32) = base (None: 0; y: in place) + scales[a] x A[a]^T B[a]^T with a = ids[t] of each row
     (outside [0, n): no adapter); x [T, K], A [n, r, K] and B [n, N, r] bf16, scales [n] fp32 or None."""
-    t, y_dtype, yt = x.dtype, _float_dtype(y), y.dtype
+    there = not (x is None or ids is None or A is None or B is None or y is None)
+    t, y_dtype, yt = (x.dtype, _float_dtype(y), y.dtype) if there else (None, -1, None)
     yb = T * N * (4 if y_dtype == MOE_F32 else 2)
-    if (_float_dtype(x) != MOE_BF16 or A.dtype is not t or B.dtype is not t or x.nbytes < 2 * T * K
+    if (not there or _float_dtype(x) != MOE_BF16 or A.dtype is not t or B.dtype is not t or x.nbytes < 2 * T * K
             or A.nbytes < 2 * n * r * K or B.nbytes < 2 * n * N * r or y_dtype < 0 or y.nbytes < yb
             or ids.itemsize != 4 or ids.nbytes < 4 * T or ids.is_floating_point()
             or scales is not None and (_float_dtype(scales) != MOE_F32 or scales.nbytes < 4 * n)

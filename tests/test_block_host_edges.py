@@ -39,3 +39,27 @@ def test_lora_workspace_is_what_some_batch_needs(lib, K, N, r, n):
     for T in (1, 64, 700, 1024, 2300):
         size = moe.moe_lora_workspace_size(T, K, N, r, n)
         assert any(_lora(lib, T=t, K=K, N=N, r=r, n=n, x=None, size=size - 1) == WORKSPACE for t in range(1, T + 1))
+
+
+# --------------------------------------------------------------- wrappers
+def test_wrappers_say_which_tensors_they_take(lib):
+    """A tensor that has to be there and is not: the wrapper's own error."""
+    T, D, E, k, r, n = 3, 256, 64, 4, 8, 2
+    x, W, logits = torch.zeros(T, D).bfloat16(), torch.zeros(D, E).bfloat16(), torch.zeros(T, E)
+    ids, w, ws = torch.zeros(T, k, dtype=torch.int32), torch.zeros(T, k), torch.zeros(1 << 20, dtype=torch.uint8)
+    cfg, gate = moe.make_config(T, D, E, k, 128), moe.make_gate()
+
+    for a in ((x, None, logits, ids), (x, W, None, ids), (x, W, logits, None), (None, None, None, ids)):
+        with pytest.raises(ValueError, match="moe_route_gated takes"):
+            moe.moe_route_gated(cfg, gate, a[0], a[1], None, None, a[2], a[3], w, ws)
+    for a in ((None, x[0]), (x, None)):
+        with pytest.raises(ValueError, match="moe_add_rms_norm takes"):
+            moe.moe_add_rms_norm(T, D, a[0], None, a[1], 1e-6, None, x)
+    good = [x, torch.zeros(T, dtype=torch.int32), torch.zeros(n, r, D).bfloat16(), torch.zeros(n, E, r).bfloat16(), None, None, logits]
+    for i in (0, 1, 2, 3, 6):
+        a = list(good)
+        a[i] = None
+        with pytest.raises(ValueError, match="moe_lora takes"):
+            moe.moe_lora(T, D, E, r, n, *a, ws)
+    with pytest.raises(ValueError, match="moe_block takes"):
+        moe.moe_block(cfg, gate, None, None, x[0], 1e-6, W, None, None, W, None, W, None, None, None, None, None, None, x, x, ws)
