@@ -140,12 +140,13 @@ typedef struct {
 } moe_config_t;
 
 /* Bytes of workspace that every call below accepts for this configuration.
- * The last region, at T <= 32, is moe_layer_few's scratch, and only that call
- * asks for it: moe_layer and the stage calls accept what comes before (of
- * which moe_layer needs all; the stage calls use the control block and their
- * own scratch).  So a workspace that holds moe_layer's largest batch holds its
- * smaller ones, while moe_layer_few's few tokens can ask for more than a larger
- * batch of moe_layer: for both, take the maximum over the configurations.
+ * The last region, at T <= 32, is the scratch of moe_layer_few's kernel, and only
+ * that call, and moe_block where it takes that kernel, ask for it: moe_layer, the
+ * stage calls and other batches of moe_block accept what comes before (of which
+ * moe_layer needs all; the stage calls use the control block and their own
+ * scratch).  So a workspace that holds moe_layer's largest batch holds its smaller
+ * ones, while few tokens of moe_layer_few or moe_block can ask for more than a
+ * larger batch: for these, take the maximum over the configurations.
  * Returns 0 for an invalid configuration. */
 size_t moe_workspace_size(const moe_config_t* cfg);
 
@@ -451,7 +452,8 @@ int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* 
  *   sum_out     and out are two buffers.
  *   s13, s2, s13s, s2s  fp32 per column (e4m3 weights), bf16 per row and group (4-bit
  *               weights, as moe_layer_few has them), or NULL.
- *   ws          moe_workspace_size(cfg) bytes.
+ *   ws          moe_workspace_size(cfg) bytes (as said there, for batches of up to 32
+ *               tokens and larger ones the maximum over both).
  *   x, residual, sum_out, eps as in moe_add_rms_norm; the other arguments and the errors
  *   as in moe_layer (E a multiple of 8 for bf16 activations).
  * moe_layer_few's kernel takes 4-bit weights (T <= 32, else MOE_ERR_UNSUPPORTED),

@@ -914,7 +914,7 @@ int moe_block(const moe_config_t* cfg, const moe_gate_t* gate, const void* x, co
   if (st != MOE_OK) return st;
   const bool few = few_preferred(cfg, gate != nullptr);
   if (w4_group(cfg->w_dtype) && !few) return MOE_ERR_UNSUPPORTED;
-  if (ws_bytes < moe_workspace_size(cfg)) return MOE_ERR_WORKSPACE;
+  if (few && ws_bytes < moe_workspace_size(cfg)) return MOE_ERR_WORKSPACE;  // its scratch
   st = layer_args(cfg, x, Wg, W13, s13, W2, s2, W13s, s13s, W2s, s2s, out);
   if (st != MOE_OK) return st;
   if (few)

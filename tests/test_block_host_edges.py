@@ -1,11 +1,13 @@
 """Host-side checks of moe_lora's workspace and of the Python wrappers of the
 operators around the experts."""
+import ctypes
+
 import pytest
 import torch
 
 import mixture_experts_layer_gating_gb300 as moe
 from tests._lib import ensure_library
-from tests.test_block_host import INVALID, WORKSPACE, _lora
+from tests.test_block_host import INVALID, P, WORKSPACE, _lora
 
 
 @pytest.fixture(scope="module")
@@ -63,3 +65,23 @@ def test_wrappers_say_which_tensors_they_take(lib):
             moe.moe_lora(T, D, E, r, n, *a, ws)
     with pytest.raises(ValueError, match="moe_block takes"):
         moe.moe_block(cfg, gate, None, None, x[0], 1e-6, W, None, None, W, None, W, None, None, None, None, None, None, x, x, ws)
+
+
+# ------------------------------------------------------------------ block
+@pytest.mark.parametrize("gate", [False, True])
+def test_block_asks_for_the_few_token_scratch_only_where_it_uses_it(lib, gate):
+    """A workspace of 64 tokens takes moe_block's batches that run moe_layer's kernels, however
+    few the tokens (the next check, of the null pointers, is what refuses these calls)."""
+    g = ctypes.byref(moe.make_gate()) if gate else None
+    for w, most in (("bf16", 4 if gate else 8), ("fp8_e4m3_nk", 16), ("fp8_e4m3_nk_a8", 0), ("fp8_e4m3", 32), ("w4_g64", 32)):
+        n = moe.moe_workspace_size(moe.make_config(64, 2048, 128, 8, 768, w_dtype=w))
+        for T in (1, 4, 5, 8, 9, 16, 17, 32, 33, 64):
+            cfg = moe.make_config(T, 2048, 128, 8, 768, w_dtype=w)
+            own = moe.moe_workspace_size(cfg)
+            if w[0] == "w" and T > 32:
+                continue  # (not taken)
+            small = T <= most and n < own
+            assert lib.moe_block(ctypes.byref(cfg), g, *[None] * 3, 0.0, *[None] * 14, P, n, None) == (WORKSPACE if small else INVALID), (w, T)
+            assert lib.moe_block(ctypes.byref(cfg), g, *[None] * 3, 0.0, *[None] * 14, P, max(n, own), None) == INVALID
+            if T <= most:
+                assert lib.moe_block(ctypes.byref(cfg), g, *[None] * 3, 0.0, *[None] * 14, P, own - 1, None) == WORKSPACE

@@ -8,7 +8,7 @@ import torch
 import mixture_experts_layer_gating_gb300 as moe
 from tests import _block_ref as ref
 from tests._lib import ensure_library
-from tests.test_gpu_block import BF16, F32, W_REL, _gate, _gen, _normal, _within
+from tests.test_gpu_block import BF16, F32, W_REL, WD, _block, _block_inputs, _gate, _gen, _normal, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -195,3 +195,21 @@ def test_lora_in_the_workspace_of_a_larger_batch():
             y64, allowed = ref.lora(x[:T], ids[:T], A, B, None, base[:T], BF16)
             _within(y, y64, allowed)
         assert moe.moe_read_device_status(ws) == 0
+
+
+# ------------------------------------------------------------------ block
+@pytest.mark.parametrize("w", ["bf16", "nk", "a8"])
+def test_block_in_the_workspace_of_a_larger_batch(w):
+    """Batches that run moe_layer's kernels, in a workspace without the few-token scratch, as in
+    one of their own: the same bits, and nothing written behind it."""
+    D, E, k, I, Is = 512, 64, 4, 128, 128
+    gate = moe.make_gate(n_group=8, topk_group=4, scale=2.5)
+    n = moe.moe_workspace_size(moe.make_config(64, D, E, k, I, Is, **WD[w]))
+    ws = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
+    ws[n:] = 173
+    for T in (64, 17, 24, 32, 40):
+        d = _block_inputs(w, T, D, E, k, I, Is, seed=T)
+        cfg = moe.make_config(T, D, E, k, I, Is, **WD[w])
+        want = _block(cfg, gate, d, moe.alloc_workspace(cfg))
+        assert all(torch.equal(a, b) for a, b in zip(_block(cfg, gate, d, ws[:n]), want))
+    assert moe.moe_read_device_status(ws[:n]) == 0 and bool((ws[n:] == 173).all())
