@@ -352,7 +352,7 @@ int moe_dequantize_w4(const void* Wq, const void* scales, const void* zeros, int
 
 /* How moe_route_gated and moe_block choose experts.  With logits l [E] of a token
  * (x W_g + logit_bias, fp32) and its scores p, all in fp32 (what is compared to 2^-22
- * and 2^-23 of |l| relative, the weights as expf has them):
+ * and 2^-23 of |l| relative, the weights as expf and division have them):
  *   p       softmax over the E experts, or sigmoid of each logit (score).
  *   c       p + select_bias: takes part in the choice, not in the weights.
  *   groups  the experts in n_group runs of E / n_group; a group's value is the
@@ -406,10 +406,10 @@ int moe_route_gated(const moe_config_t* cfg, const moe_gate_t* gate, const void*
  *   q_group   values to a scale: 0 (the whole row), 32, 64 or 128 (dividing D).
  *   q_scales  [rows, D / q_group] fp32 out ([rows] for q_group 0), with q.
  * A scale is max |y| / 448 of its values (1 where all are zero, at least 2^-126, NaN where one
- * is an infinity or NaN), q = e4m3(y / scale) from y before any other rounding, nearest
- * even.  All pointers 16-byte aligned; outputs overlap nothing but as said (sum_out and y
- * are two buffers).  NULL tensors
- * are taken when rows is 0.  No workspace. */
+ * is an infinity or NaN), q = e4m3(y / scale) from y before any other rounding (fp32
+ * division, nearest even).  All pointers 16-byte aligned; outputs overlap nothing but as
+ * said (sum_out and y are two buffers).  NULL tensors are taken when rows is 0.  No
+ * workspace. */
 int moe_add_rms_norm(int32_t rows, int32_t D, int32_t dtype, const void* x, const void* residual,
                      const void* weight, float eps, void* sum_out, void* y, void* q, int32_t q_group,
                      float* q_scales, void* stream);
@@ -434,7 +434,9 @@ int moe_add_rms_norm(int32_t rows, int32_t D, int32_t dtype, const void* x, cons
  *             holds nothing between calls but the control block (its first 256 bytes,
  *             zero-filled once), which takes the device error word.
  * x A^T is summed in fp32 and multiplied by B as two bf16 terms (16 significant bits),
- * as three (24) where y is fp32; its sums are fp32.  The same inputs give the same bits
+ * as three (24) where y is fp32; its sums are fp32.  Infinities of x are the formula's; an
+ * infinite B may give NaN (its product with a term that is 0), and s x A^T beyond bf16's largest
+ * number counts as infinite.  The same inputs give the same bits
  * on every call of the same sizes.  Pointers but ids and scales 16-byte aligned, those 4. */
 size_t moe_lora_workspace_size(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n);
 int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* x,
@@ -443,7 +445,8 @@ int moe_lora(int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* 
 
 /* A pre-norm residual MoE block: moe_add_rms_norm, then moe_layer or moe_layer_few with
  * moe_route_gated's choice, on one stream:
- *   sum_out = x + residual,  y = norm(sum_out) * norm_weight,  out = layer(y)
+ *   sum_out = x + residual,  y = norm(x + residual) * norm_weight,  out = layer(y)
+ * (the sum is normed before it is rounded for sum_out).
  *   gate        NULL: moe_layer's choice (softmax top-k), select_bias NULL then.
  *   norm_weight [D] act_dtype, or NULL: no norm, the layer takes x (residual, sum_out
  *               and y NULL, eps 0).

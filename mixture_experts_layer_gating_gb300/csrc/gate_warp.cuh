@@ -96,10 +96,10 @@ __host__ __device__ constexpr int gate_scratch(int epl) { return 32 * ((epl + 4)
 // that has it, and that lane's next key from shared memory.  Which entry of the lane a
 // chosen key is, is found once at the end, by k lanes at a time.  A group's value comes from
 // the sorted keys of the lanes that hold it (the group's size a multiple of EPL, a power of
-// two lanes), else group after group.  Measured (one GB300): 16384 tokens of 256 experts in 8
-// groups, 4 kept, top-8, sigmoid and bias 13.1 us (646 instructions a token, ALU pipe at 57 %;
-// reading the logits would take 2.6; every round over all keys 28.0), 509 tokens of 512 experts,
-// top-10, softmax and bias 4.9 us, one token 3.5 us.
+// two lanes), else group after group.  Measured (one GB300, from a graph): 16384 tokens of 256
+// experts in 8 groups, 4 kept, top-8, sigmoid and bias 12.3 us (656 instructions a token, which
+// are 8.5 us at one a cycle on each scheduler; reading the logits would take 2.6; every round over
+// all keys 28.0), 509 tokens of 512 experts, top-10, softmax and bias 3.7 us, one token 2.4 us.
 template <int EPL, bool WHOLE, bool SIGMOID, bool BIAS>
 __device__ __forceinline__ int warp_gate_topk(float (&v)[EPL], int lane, const GateParams& g,
                                               const float* __restrict__ logit_bias,

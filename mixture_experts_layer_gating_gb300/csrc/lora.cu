@@ -15,9 +15,9 @@
 // adapters' bytes are the bound.  Many rows: tcgen05 (below), x and y are.
 //
 // Measured (one GB300, inputs rotated so that they come from HBM): one row, 2048 x 2048, rank
-// 16 5.0 us; 61 rows of 40 adapters, 4096 x 4096, rank 64 11.7 us (33 MB in 4.9 at a copy's rate;
+// 16 4.0 us; 61 rows of 40 adapters, 4096 x 4096, rank 64 11.8 us (33 MB in 4.9 at a copy's rate;
 // two launches, each three dependent trips to memory); 2000 rows of 4 requests, 2048 x 4224,
-// rank 24, fp32 27 us (11.3); 8192 rows of 12, 8192 x 8192, rank 64 93 us (428 MB in 63).
+// rank 24, fp32 26.4 us (11.3); 8192 rows of 12, 8192 x 8192, rank 64 91 us (428 MB in 63).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -900,7 +900,11 @@ struct LoraPlan {
 // adapter, or 32 from 2048 on.
 // (measured, 4096 x 4096, rank 64, rows in any order, us of few-row : many-row kernels: 1024 rows
 // of 16 adapters 23.7 : 21.7, of 32 27.2 : 32.0; 4096 of 128 107 : 96, of 256 119 : 131; 256 of 4
-// 13.2 : 17.5)
+// 13.2 : 17.5.  The rule does not look at K, N and r.  What the switch does at other sizes, requests
+// in runs, us of 1023 : 1024 rows: 2048 x 2048 one adapter, rank 16 14.3 : 13.4, rank 256 36 : 30, 16
+// adapters 12.3 : 14.6 and 30 : 39; 8192 x 8192 one adapter 27.9 : 24.3 and 88 : 47, 16 adapters 33 : 27
+// and 106 : 74.  So wide projections and large ranks would gain from a switch at fewer rows, and small
+// ones with many adapters from one at more)
 long long lora_wide_from(int n) { return n < 32 ? std::max(1024ll, 64ll * n) : std::max(2048ll, 32ll * n); }
 
 LoraPlan lora_plan(int T, int K, int N, int r, int n, bool y_f32) {
@@ -909,7 +913,7 @@ LoraPlan lora_plan(int T, int K, int N, int r, int n, bool y_f32) {
   q.wide = T >= lora_wide_from(n);
   q.tile_rows = q.wide ? kWideRows : 16;
   q.tiles = q.scan ? T : static_cast<int>(std::min<long long>(T, (T + q.tile_rows - 1ll) / q.tile_rows + n));
-  // one launch instead of two: as long on the GPU (us of two : of one, 1, 16, 32, 64 rows with
+  // one launch instead of two, where every CTA of 256 columns makes v again: as long on the GPU (us of two : of one, 1, 16, 32, 64 rows with
   // adapters of their own: 2048 x 2048, rank 16 5.1 : 4.7, 5.5 : 5.1, 6.1 : 6.1, 7.1 : 7.2; 4096 x
   // 4096, rank 16 5.1 : 6.1, 6.0 : 7.6, 7.1 : 8.7, 8.2 : 9.7), and 1.5 less of the caller's time
   q.at_once = T <= 32 && r <= 32 && static_cast<long long>(r) * K <= 32768;

@@ -6,10 +6,13 @@
 // Bound by memory: every row is read once and held in registers, a group of threads to a
 // row, from the sum of squares to the stores.  Measured (one GB300, inputs rotated so that
 // they come from HBM; share of what a copy reaches): 16384 x 8192 bf16 with residual, sum, y
-// and e4m3 rows 195 us (6.2 TB/s, 0.91), 8192 x 4096 the same 51 us (0.87), 4096 x 2048 fp32
-// 13.6 us (0.73: launch and first bytes are 3 of them), one row of 2048 2.3 us.  Four vectors
+// and e4m3 rows 193 us (6.3 TB/s, 0.92), 8192 x 4096 the same 51 us (0.86), 4096 x 2048 fp32
+// 13.6 us (0.73: launch and first bytes are 3 of them), one row of 2048 1.5 us.  Four vectors
 // of 8 values a thread and 16 warps an SM: with two vectors and more warps 206 us, 67 us, 15.1
-// us; with the row read again for the norm it would move a third more.
+// us; with the row read again for the norm it would move a third more.  Farther from a copy:
+// 2000 x 4096 with scales of 128 17.2 us (0.62: 608 blocks take 3.3 rows each), and rows of more
+// than 16384 values, whose eight vectors a thread spill registers and leave none for the next
+// row (4096 x 32768 bf16 with row scales 285 us, 0.62; fp32 without 521 us, 0.61).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -24,7 +27,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxTprLog2 = 9, kMaxWarps = 1 << (kMaxTprLog2 - 5);  // threads to a row, 2^5 .. 2^9
-constexpr int kSms = 152;
+constexpr int kSms = 152;  // a constant, for the choice of threads to a row: results must not depend on the device
 
 struct NormParams {
   const void *x, *residual, *weight;
@@ -332,7 +335,7 @@ cudaError_t launch_type(NormParams& p, cudaStream_t s) {
     while ((vpt << tl) < nvec) ++tl;
     return tl;
   };
-  // few rows: every thread has one vector, for the shortest chain
+  // few rows (one or two to an SM): every thread has one vector, for the shortest chain
   if (p.rows <= 2 * kSms && threads(1) <= kMaxTprLog2) {
     p.tpr_log2 = threads(1);
     return launch_vpt<T, 1>(p, s);
