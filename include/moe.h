@@ -123,7 +123,7 @@ typedef enum {
 #define MOE_DEV_BAD_EXPERT_ID 0x1   /* an id outside [0, E) reached routing */
 #define MOE_DEV_BAD_OFFSETS 0x2     /* offsets not monotone or beyond T*k */
 #define MOE_DEV_BAD_DEST 0x4        /* a permuted position outside [0, T*k) */
-#define MOE_DEV_NONFINITE_LOGIT 0x8 /* NaN / Inf router logit (treated as -Inf) */
+#define MOE_DEV_NONFINITE_LOGIT 0x8 /* NaN / Inf router logit or biased score (treated as -Inf) */
 #define MOE_DEV_WAIT_TIMEOUT 0x10   /* a bounded pipeline wait gave up */
 
 typedef struct {
